@@ -423,6 +423,86 @@ int tv_commit_kv(const tv_commit_params* params, const uint16_t* k_nodes,
                  const int32_t* prefix_lens, uint16_t* k_prefix_blocks, uint16_t* v_prefix_blocks,
                  int32_t* new_prefix_lens, int32_t* status, cudaStream_t stream);
 
+/* ========================================================================
+ * Attention of a chunk of new tokens over the paged cache: the prompt (or a
+ * part of it) that fills the cache which tree attention then reads, or one
+ * plain decode token per sequence, in one ragged batch.
+ *
+ * Sequence b has seq_lens[b] cached tokens, of which the last C_b =
+ * token_offsets[b+1] - token_offsets[b] (0 <= C_b <= seq_lens[b]) are the
+ * chunk: their K/V are in the pool already (tv_append_kv).  Token i of the
+ * chunk is row token_offsets[b] + i of q and sits at position
+ * p = seq_lens[b] - C_b + i.  For every query head h, with KV head
+ * floor(h / (Hq/Hkv)):
+ *   out[row][h] = sum_k softmax_k(scale * q.k_k) * v_k   over the keys
+ *   k <= p with  window == 0  or  k > p - window  or  k < sinks:
+ * causal, optionally with a sliding window of `window` tokens (the token
+ * itself included) next to which the first `sinks` tokens stay visible.  Every
+ * row sees at least itself.
+ *   - Pages that no row of the chunk sees are not read: their block-table
+ *     entries may hold anything (a windowed cache frees them).  Cached values
+ *     at positions that no row sees do not matter; a non-finite V at a position
+ *     that some row sees may also reach rows that do not see it (their weight
+ *     of 0 times it is NaN).
+ *   - An empty chunk (C_b = 0) writes nothing.  Rows of out past
+ *     token_offsets[batch] are left as they were.
+ *   - A sequence with a malformed extent (C_b < 0, C_b > seq_lens[b], rows past
+ *     total_tokens, seq_lens[b] > max_len) or a bad block id of a page that it
+ *     sees gets status TV_ERR_BAD_TREE and all-zero rows.
+ * Inputs bf16, accumulation and softmax fp32, output bf16 or fp32; P is rounded
+ * to bf16 for the P V product, so the fp32 output carries that rounding.
+ * Repeated calls agree bit for bit.
+ * ====================================================================== */
+typedef struct {
+  int32_t batch;              /* B >= 1                                        */
+  int32_t num_q_heads;        /* Hq                                            */
+  int32_t num_kv_heads;       /* Hkv; Hq % Hkv == 0, Hq / Hkv <= 256           */
+  int32_t head_dim;           /* D: 64 or 128                                  */
+  int32_t block_size;         /* tokens per page: must be TV_BLOCK_SIZE (16)   */
+  int32_t max_blocks_per_seq; /* row stride of block_table                     */
+  int32_t num_blocks;         /* pages in the pool                             */
+  int32_t total_tokens;       /* rows of q and out, >= token_offsets[batch]
+                                 (host copy); 0: only status is written        */
+  int32_t max_len;            /* upper bound of seq_lens[b]                    */
+  int32_t window;             /* 0: every earlier token, else >= 1             */
+  int32_t sinks;              /* first tokens that stay visible next to a window */
+  int32_t out_dtype;          /* tv_out_dtype of `out`                         */
+  float softmax_scale;        /* 0 => 1/sqrt(D)                                */
+  int64_t q_stride;           /* elements between the rows of q (a slice of a
+                                 fused projection), 0 => Hq*D; rows 16-byte aligned */
+} tv_chunk_params;            /* host struct */
+
+/* Bytes of device workspace for these parameters on the current device (0 if
+ * they are invalid): a ticket counter per CTA (zeroed by every call, on the
+ * stream) and two partial-result slots per CTA, at most 40.5 MB at D = 128 on
+ * 152 SMs.  Contents need no initialisation; calls that overlap on the GPU
+ * (two captured graphs replayed at once among them) need distinct workspaces. */
+size_t tv_chunk_attention_workspace_size(const tv_chunk_params* params);
+
+/* Layouts: q bf16 [total_tokens][Hq][D] (rows q_stride apart); k_pool, v_pool
+ * bf16 [num_blocks][Hkv][16][D]; block_table int32 [batch][max_blocks_per_seq];
+ * seq_lens int32 [batch]; token_offsets int32 [batch+1]; out [total_tokens]
+ * [Hq][D]; status int32 [batch].  All device pointers 16-byte aligned.
+ * TV_ERR_UNSUPPORTED: a head_dim other than 64 and 128, or Hq / Hkv > 256. */
+int tv_chunk_attention(const tv_chunk_params* params, const uint16_t* q, const uint16_t* k_pool,
+                       const uint16_t* v_pool, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* token_offsets, void* out,
+                       int32_t* status, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/* The same over an E4M3 cache (tv_append_kv_fp8), in the formats and the
+ * arithmetic of tv_tree_attention_fp8: q u8 codes [total_tokens][Hq][128] with
+ * q_scale fp32 [total_tokens][Hq] (tv_quantize_rows), pools u8 [num_blocks]
+ * [Hkv][16][128] with scales fp32 [num_blocks][Hkv][16].  Scales are positive;
+ * code x scale of V lies in the fp16 range.  head_dim must be 128
+ * (TV_ERR_UNSUPPORTED otherwise). */
+int tv_chunk_attention_fp8(const tv_chunk_params* params, const uint8_t* q, const float* q_scale,
+                           const uint8_t* k_pool, const float* k_scale, const uint8_t* v_pool,
+                           const float* v_scale, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* token_offsets, void* out,
+                           int32_t* status, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -297,3 +297,33 @@ def retained_set(q_rows, mass: float):
         z32[r] = zs.value
         kept[r] = k.value
     return masks, zf, z32, kept
+
+
+# ------------------------------------------------------------------ chunk attention
+def e4m3_table() -> np.ndarray:
+    """The value of each of the 256 E4M3 codes."""
+    return np.array([e4m3_value(c) for c in range(256)])
+
+
+def chunk_attention(q, k_pool, v_pool, block_table, seq_lens, token_offsets, window: int = 0,
+                    sinks: int = 0, scale: float | None = None, out=None) -> np.ndarray:
+    """fp64 attention of every sequence's last C_b tokens over its pages, on
+    real values: q [total, Hq, D], pools [blocks, Hkv, 16, D].  Row i of
+    sequence b sits at p = seq_lens[b] - C_b + i and sees key k iff k <= p and
+    (window == 0 or k > p - window or k < sinks).  Rows of no sequence keep
+    what `out` holds (zeros by default)."""
+    q, k_pool, v_pool = (np.asarray(x, np.float64) for x in (q, k_pool, v_pool))
+    hq, d = q.shape[1:]
+    g = hq // k_pool.shape[1]
+    out = np.zeros(q.shape) if out is None else out
+    for b, n in enumerate(np.asarray(seq_lens).tolist()):
+        r0, r1 = int(token_offsets[b]), int(token_offsets[b + 1])
+        for i in range(r1 - r0):
+            p = n - (r1 - r0) + i
+            keys = np.array([k for k in range(p + 1) if not window or k > p - window or k < sinks])
+            blk, at = np.asarray(block_table)[b, keys // 16], keys % 16
+            for h in range(hq):
+                s = k_pool[blk, h // g, at] @ q[r0 + i, h] * (scale or d ** -0.5)
+                w = np.exp(s - s.max())
+                out[r0 + i, h] = w @ v_pool[blk, h // g, at] / w.sum()
+    return out

@@ -12,6 +12,8 @@ PyTorch is used for device memory and the current CUDA stream only.
     accept(...)          -> dict of outputs  (tv_accept)
     commit_kv(...)       -> new_prefix_lens, status (tv_commit_kv)
     retained_set(...)    -> mask, z_fixed, z, kept (tv_retained_set)
+    chunk_attention(...) -> out, status      (tv_chunk_attention: prompts and decode tokens)
+    chunk_attention_fp8(...) -> out, status  (tv_chunk_attention_fp8, E4M3 cache)
 """
 from __future__ import annotations
 
@@ -19,6 +21,7 @@ import ctypes as C
 import os
 
 __all__ = ["TVError", "load", "tree_attention", "tree_attention_fp8", "accept", "commit_kv", "retained_set",
+           "chunk_attention", "chunk_attention_fp8", "chunk_params", "chunk_workspace_size",
            "attention_workspace_size", "attention_plan", "attention_params",
            "TV_MAX_NODES", "TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_DEVICE_TIMEOUT", "TV_ERR_NO_PAGE",
            "status_string"]
@@ -40,7 +43,8 @@ EXPORTS = ("tv_status_string", "tv_version", "tv_tree_attention_workspace_size",
            "tv_tree_attention", "tv_accept_workspace_size", "tv_accept", "tv_accept_ex",
            "tv_commit_kv",
            "tv_retained_set", "tv_selftest_wait_timeout", "tv_tree_attention_plan",
-           "tv_tree_attention_no_alloc", "tv_tree_attention_fp8")
+           "tv_tree_attention_no_alloc", "tv_tree_attention_fp8",
+           "tv_chunk_attention_workspace_size", "tv_chunk_attention", "tv_chunk_attention_fp8")
 
 
 class TVError(RuntimeError):
@@ -82,6 +86,15 @@ class CommitParams(C.Structure):
                 ("num_blocks", C.c_int32), ("max_nodes", C.c_int32), ("total_nodes", C.c_int32)]
 
 
+class ChunkParams(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("block_size", C.c_int32),
+                ("max_blocks_per_seq", C.c_int32), ("num_blocks", C.c_int32),
+                ("total_tokens", C.c_int32), ("max_len", C.c_int32), ("window", C.c_int32),
+                ("sinks", C.c_int32), ("out_dtype", C.c_int32), ("softmax_scale", C.c_float),
+                ("q_stride", C.c_int64)]
+
+
 _lib = None
 
 
@@ -121,6 +134,12 @@ def load(path: str | None = None) -> C.CDLL:
     lib.tv_commit_kv.restype = C.c_int
     lib.tv_retained_set.argtypes = [C.POINTER(RetainParams)] + [vp] * 5 + [vp]
     lib.tv_retained_set.restype = C.c_int
+    lib.tv_chunk_attention_workspace_size.argtypes = [C.POINTER(ChunkParams)]
+    lib.tv_chunk_attention_workspace_size.restype = sz
+    lib.tv_chunk_attention.argtypes = [C.POINTER(ChunkParams)] + [vp] * 9 + [sz, vp]
+    lib.tv_chunk_attention.restype = C.c_int
+    lib.tv_chunk_attention_fp8.argtypes = [C.POINTER(ChunkParams)] + [vp] * 12 + [sz, vp]
+    lib.tv_chunk_attention_fp8.restype = C.c_int
     if path is None:
         _lib = lib
     return lib
@@ -410,3 +429,153 @@ def retained_set(draft_probs, mass: float, *, mask=None, z_fixed=None, z=None, k
     if rc != TV_OK:
         raise TVError(rc, "tv_retained_set")
     return mask, z_fixed, z, kept
+
+
+# ---------------------------------------------------------------- chunks of new tokens
+# The calls below take tensors of one CUDA device, which need not be the
+# current one, and run on `stream` or on that device's current stream; buffers
+# that they create belong to that stream.
+
+def _bad(name, what):
+    raise ValueError(f"{name} must be {what}")
+
+
+def _arg(name, t, dtype, shape, dev, strided=0):
+    """Checks one tensor argument (None passes when shape is None): a CUDA
+    tensor of `dev`, of one of the dtypes and of `shape` (None entries match
+    anything), contiguous, or with `strided` = 1 contiguous but for a first
+    stride that is at least a row."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        _bad(name, f"a tensor on {dev}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        _bad(name, f"of type {dtype}, not {t.dtype}")
+    if len(t.shape) != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        _bad(name, f"of shape {tuple('*' if s is None else s for s in shape)}, not {tuple(t.shape)}")
+    if t.is_contiguous():
+        return
+    if not (strided and t[0].is_contiguous() and t.stride(0) >= t[0].numel()):
+        _bad(name, "contiguous" + (" but for the stride between its rows" if strided else ""))
+
+
+def _cuda(name, t):
+    if not getattr(t, "is_cuda", False):
+        _bad(name, "a CUDA tensor")
+    return t.device
+
+
+class _on:
+    """Makes `dev` and the stream of the call current, so that what is
+    allocated belongs to that stream; `.ptr` is the stream's handle."""
+
+    def __init__(self, dev, stream):
+        import torch
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream must be one of {dev}")
+        self._stream = torch.cuda.current_stream(dev) if stream is None else stream
+        self._ctx = torch.cuda.stream(self._stream)
+        self.ptr = C.c_void_p(self._stream.cuda_stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _row_stride(t):
+    """Elements between the rows of a tensor whose rows are contiguous (0: packed)."""
+    return 0 if t.is_contiguous() else t.stride(0)
+
+
+def chunk_params(q, k_pool, block_table, seq_lens, *, max_len: int, window: int = 0, sinks: int = 0,
+                 softmax_scale: float = 0.0, out_dtype: str = "bf16") -> ChunkParams:
+    """The parameters of a chunk_attention or chunk_attention_fp8 call."""
+    if out_dtype not in OUT_DTYPES:
+        _bad("out_dtype", "'bf16' or 'fp32'")
+    total, hq, d = q.shape
+    return ChunkParams(seq_lens.shape[0], hq, k_pool.shape[1], d, k_pool.shape[2],
+                       block_table.shape[1], k_pool.shape[0], total, int(max_len), int(window),
+                       int(sinks), OUT_DTYPES[out_dtype], float(softmax_scale), _row_stride(q))
+
+
+def chunk_workspace_size(params: ChunkParams) -> int:
+    return int(load().tv_chunk_attention_workspace_size(C.byref(params)))
+
+
+def _chunk(q, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens, token_offsets, out,
+           status, workspace, stream, kw):
+    import torch
+    lib = load()
+    fp8 = q_scale is not None
+    dev = _cuda("q", q)
+    elem = torch.uint8 if fp8 else torch.bfloat16
+    _arg("q", q, elem, (None, None, None), dev, strided=1)
+    _arg("k_pool", k_pool, elem, (None, None, TV_BLOCK_SIZE, q.shape[2]), dev)
+    _arg("v_pool", v_pool, elem, k_pool.shape, dev)
+    if fp8:
+        _arg("q_scale", q_scale, torch.float32, q.shape[:2], dev)
+        _arg("k_scale", k_scale, torch.float32, k_pool.shape[:3], dev)
+        _arg("v_scale", v_scale, torch.float32, k_pool.shape[:3], dev)
+    _arg("seq_lens", seq_lens, torch.int32, (None,), dev)
+    batch = seq_lens.shape[0]
+    _arg("block_table", block_table, torch.int32, (batch, None), dev)
+    _arg("token_offsets", token_offsets, torch.int32, (batch + 1,), dev)
+    prm = chunk_params(q, k_pool, block_table, seq_lens, **kw)
+    odt = torch.float32 if prm.out_dtype else torch.bfloat16
+    if out is not None:
+        _arg("out", out, odt, q.shape, dev)
+    if status is not None:
+        _arg("status", status, torch.int32, (batch,), dev)
+    with _on(dev, stream) as on:
+        if out is None:
+            out = torch.empty(q.shape, device=dev, dtype=odt)
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(int(lib.tv_chunk_attention_workspace_size(C.byref(prm))),
+                                    dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            _bad("workspace", f"a contiguous tensor on {dev}")
+        tail = [block_table.data_ptr(), seq_lens.data_ptr(), token_offsets.data_ptr(), out.data_ptr(),
+                status.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), on.ptr]
+        if fp8:
+            rc = lib.tv_chunk_attention_fp8(C.byref(prm), q.data_ptr(), q_scale.data_ptr(), k_pool.data_ptr(),
+                                            k_scale.data_ptr(), v_pool.data_ptr(), v_scale.data_ptr(), *tail)
+        else:
+            rc = lib.tv_chunk_attention(C.byref(prm), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), *tail)
+    if rc != TV_OK:
+        raise TVError(rc, "tv_chunk_attention_fp8" if fp8 else "tv_chunk_attention")
+    return out, status
+
+
+def chunk_attention(q, k_pool, v_pool, block_table, seq_lens, token_offsets, *, max_len: int,
+                    window: int = 0, sinks: int = 0, softmax_scale: float = 0.0, out=None,
+                    status=None, workspace=None, stream=None, out_dtype: str = "bf16"):
+    """tv_chunk_attention: causal attention of the last token_offsets[b+1] -
+    token_offsets[b] of the seq_lens[b] cached tokens of every sequence over
+    that sequence's pages, optionally with a sliding window next to which the
+    first `sinks` tokens stay visible.  q [total, Hq, D] bf16 (rows may be
+    strided: a slice of a fused projection); k/v_pool [num_blocks, Hkv, 16, D]
+    bf16; block_table [B, max_blocks], seq_lens [B], token_offsets [B+1] int32;
+    max_len an upper bound of seq_lens.  Returns (out, status); nothing is
+    synchronised."""
+    return _chunk(q, None, k_pool, None, v_pool, None, block_table, seq_lens, token_offsets, out,
+                  status, workspace, stream,
+                  dict(max_len=max_len, window=window, sinks=sinks, softmax_scale=softmax_scale,
+                       out_dtype=out_dtype))
+
+
+def chunk_attention_fp8(q_codes, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens,
+                        token_offsets, *, max_len: int, window: int = 0, sinks: int = 0,
+                        softmax_scale: float = 0.0, out=None, status=None, workspace=None,
+                        stream=None, out_dtype: str = "bf16"):
+    """tv_chunk_attention_fp8: chunk_attention over an E4M3 cache: codes
+    (uint8) with one fp32 scale per row of 128; q_codes and q_scale come from
+    quantize_rows, the pools from append_kv_fp8.  Returns (out, status);
+    nothing is synchronised."""
+    return _chunk(q_codes, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens,
+                  token_offsets, out, status, workspace, stream,
+                  dict(max_len=max_len, window=window, sinks=sinks, softmax_scale=softmax_scale,
+                       out_dtype=out_dtype))

@@ -1,0 +1,1239 @@
+// chunk_attn_kernel.cu -- attention of a chunk of new tokens over a paged
+// cache on sm_103a (tv_chunk_attention, tv_chunk_attention_fp8).
+//
+// Mathematics.  Token i of sequence b sits at position p = len_b - C_b + i;
+// its K/V are in the cache already.  Row (i, head) is
+//   out = sum_k 2^(s_k - m) v_k / sum_k 2^(s_k - m),  s_k = log2(e) scale q.k_k
+// over the visible keys: k <= p and (no window, or k > p - window, or
+// k < sinks).  A row always sees itself, so the sum is never empty.
+//
+// Rows.  The packed query rows of one (sequence, KV head) are
+// R = token * g + head-in-group, so the query heads of a GQA group share each
+// K/V tile.  A unit is floor(256 / g) consecutive tokens of one (sequence, KV
+// head): up to 256 rows, two 128-row m-tiles.  Its keys are the 128-key tiles
+// that any of its rows sees: the tiles of the sinks, then the tiles from the
+// start of the first row's window to the last row's position.
+//
+// Work.  Persistent grid, one CTA per SM.  The key tiles of all units lie on
+// one line ordered (sequence, unit, KV head, tile), cut into equal contiguous
+// ranges, one per CTA, computed on the device from the lengths.  A single
+// decode token of one sequence and a long prompt are split the same way.  A
+// range boundary inside a unit splits it into pieces: each leaves its
+// unnormalised O and (m, l) in a workspace slot, and the last piece to take a
+// ticket merges all slots in piece order, so results do not depend on timing.
+//
+// One CTA has 320 threads (384 for an E4M3 cache):
+//   warp 8      loads K and V tiles by TMA, one box per 16-token page through
+//               the block table; pages that no row of the unit sees are never
+//               read (an out-of-range page index loads zeros).
+//   warp 9      issues tcgen05.mma for both m-tiles h: S_h = Q_h K^T into
+//               TMEM, O_h += P_h V with P_h from TMEM.  P_h lies over S_h.
+//   warps 0-7   softmax of m-tile 0 and 1, one thread per row.  P is handed
+//               over in halves (64 keys), so that the first four P V steps run
+//               under the exponentials of the second half, and the row sum is
+//               taken after the hand-over, under the MMAs: what stays on the
+//               chain S -> P -> S of an m-tile is the TMEM load, the row max
+//               and the exponentials.
+//   warps 10-11 (E4M3) convert V tiles to fp16 with their row scales.
+// TMEM (512 columns): S_0/P_0 at 0, S_1/P_1 at 128, O_0 at 256, O_1 at 256 + D.
+// Every wait on an mbarrier is bounded; on expiry the CTA reports
+// TV_ERR_DEVICE_TIMEOUT for its sequence, drains its copies and returns.
+//
+// Precision.  S, the softmax and O are fp32.  P is rounded to the 16-bit type
+// of V for the P V product (bf16; fp16 for an E4M3 cache) and the row sum adds
+// the rounded values, so that O / l weights V exactly as the product did.
+#include <climits>
+
+#include "tv_device.cuh"
+#include "tv_launch.h"
+
+namespace tv {
+namespace {
+
+constexpr int BM = 128;               // rows of one m-tile
+constexpr int BN = 128;               // keys per tile
+constexpr int kUnitRows = 2 * BM;
+constexpr int kSoftmaxThreads = 256;  // warps 0-7: two groups of four warps
+constexpr int kTmaWarp = 8;
+constexpr int kMmaWarp = 9;           // issues every MMA; owns the TMEM allocation
+constexpr int kConvWarp = 10;         // E4M3: warps 10-11 convert V tiles to fp16
+constexpr int kConvThreads = 64;
+constexpr int kThreads = 320;
+constexpr int kThreadsF8 = 384;
+// the running max moves only when a tile exceeds it by 2^8: P stays below
+// 2^8 and the row sum below 2^8 x keys, well inside fp32 (and fp16 for P)
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMaxPieces = 16;        // pieces per scheduling round
+constexpr int kSclSlots = 8;          // E4M3: scale slots (tile tau in slot tau % 8)
+
+// Named barriers (0 is __syncthreads): softmax group 0 alone, both groups.
+constexpr int kBarGroup0 = 1;
+constexpr int kBarPair = 2;
+
+// A piece: the key tiles [t0, t1) of one unit that this CTA computes.
+struct Piece {
+  int b, kvh;
+  int tok0;         // first token of the unit (row of q)
+  int pos0;         // its position
+  int lo, hi;       // the unit sees keys < sinks and keys lo .. hi
+  int st, skip;     // tile t < st is key tile t, later ones key tile t + skip
+  int t0, t1;
+  int rows;         // packed rows of the unit (1 .. 256)
+  int slot;         // partial-result slot, -1 when the piece is the whole unit
+  int cnt;          // ticket counter of a split unit
+  int npieces;      // pieces of a split unit
+  int vfirst;       // CTA of the unit's first piece
+  int pad;
+};
+
+// Shared memory of one CTA.  bf16: K and V tiles of 128 keys x D in rings of
+// 2 and 3 (the P V of a tile runs a period after its S, so V waits longer).
+// E4M3 (D = 128): K and raw V tiles of one-byte codes in rings of 3, two
+// converted fp16 V tiles, and 8 slots of per-key scales (K, V).
+template <int D, bool F8>
+struct Layout {
+  static_assert(!F8 || D == 128, "an E4M3 cache needs D = 128");
+  static constexpr int kHalves = D / 64;               // 64-column halves of a 16-bit row
+  static constexpr int kStages = F8 ? 3 : (D == 128 ? 2 : 4);
+  static constexpr int kVStages = F8 ? 3 : (D == 128 ? 3 : 5);
+  static constexpr int kGroupBytes = kHalves * 1024;   // 8 rows of a 16-bit tile
+  static constexpr int kTileBytes = BN * D * 2;
+  static constexpr int kKTileBytes = F8 ? BN * D : kTileBytes;  // a K or raw V tile as loaded
+  static constexpr int kQBytes = F8 ? BM * D : BM * D * 2;
+  static constexpr int kQ = 0;                         // Q_0, Q_1
+  static constexpr int kKRing = kQ + 2 * kQBytes;
+  static constexpr int kVRing = kKRing + kStages * kKTileBytes;
+  static constexpr int kV16 = kVRing + kVStages * kKTileBytes;
+  static constexpr int kV16Bytes = F8 ? 2 * kTileBytes : 0;
+  static constexpr int kScl = kV16 + kV16Bytes;        // F8: [8][2][128] floats
+  static constexpr int kSclBytes = F8 ? kSclSlots * 2 * BN * 4 : 0;
+  static constexpr int kPieces = kScl + kSclBytes;
+  static constexpr int kPiecesBytes = kMaxPieces * static_cast<int>(sizeof(Piece));
+  static constexpr int kBlk = kPieces + kPiecesBytes;  // block ids of the last 8 K tiles
+  static constexpr int kBlkBytes = 8 * 8 * 4;
+  static constexpr int kBar = kBlk + kBlkBytes;
+  // kfull, kempty [S], vfull, vempty [VS], s_full, p_a, p_b, o_done, q_full
+  // [2], drain, v16full, v16empty [2], sfull [8]
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11 + (F8 ? 4 + kSclSlots : 0);
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kMiscBytes = 160;
+  static constexpr int kTotal = kMisc + kMiscBytes;
+  static constexpr int kAlloc = kTotal + 1024;  // slack for 1024-byte alignment
+  // the schedule's scratch (a chunk of 256 sequences) lies over Q, which is
+  // written only after the piece list is built
+  static constexpr int kSeq = kQ;                      // [4][256] ints, then 8 warp sums
+  static constexpr int kTmemCols = 512;
+  static_assert(4 * 256 * 4 + 32 <= 2 * kQBytes, "schedule scratch fits over Q");
+  static_assert(kAlloc <= 232448, "shared memory per CTA");
+};
+
+struct Misc {
+  uint32_t tmem_base;
+  int abort;
+  int npieces;                // pieces of this round
+  int more;                   // another round follows
+  int merge;                  // this CTA merges the current split unit
+  int zero_needed;            // a malformed sequence's rows are zeroed by this CTA
+  int piece_bad[kMaxPieces];  // a block id of the piece was out of range
+};
+static_assert(sizeof(Misc) <= Layout<128, true>::kMiscBytes, "Misc fits its area");
+
+// Partial-result slot: unnormalised O (fp32) as float4 [D/4][rows of the
+// unit], (m, l) per row, a flag.
+template <int D>
+struct Slot {
+  static constexpr size_t kO = 0;
+  static constexpr size_t kMl = static_cast<size_t>(kUnitRows) * D * 4;
+  static constexpr size_t kFlag = kMl + kUnitRows * 8;
+  static constexpr size_t kBytes = kFlag + 256;
+};
+
+// max of three (NaN operands are ignored, as in fmaxf)
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ void named_sync(int id, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+__device__ __forceinline__ void record_status(int32_t* status, int b, int code) {
+  atomicMax(status + b, code);
+}
+
+// Waits for this thread's TMEM loads; the registers they fill are operands, so
+// that nothing that reads them is moved ahead of the wait.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Bits 0 .. n-1 of a 32-bit word (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// ---------------------------------------------------------------- schedule
+struct Unit {
+  int pos0, ntok;
+  int lo, hi, st, skip, T;
+};
+
+// Unit u of a chunk of C tokens that starts at position ctx.  When the whole
+// context is visible to the unit (no window, or a window that reaches the
+// sinks), lo = st = skip = 0.
+__device__ __forceinline__ Unit unit_of(const ChunkArgs& a, int ctx, int C, int u) {
+  Unit x;
+  const int tok = u * a.unit_tokens;
+  x.ntok = min(a.unit_tokens, C - tok);
+  x.pos0 = ctx + tok;
+  x.hi = x.pos0 + x.ntok - 1;
+  x.lo = x.st = x.skip = 0;
+  if (a.window > 0 && x.pos0 - a.window + 1 > a.sinks) {
+    x.lo = x.pos0 - a.window + 1;
+    x.st = (a.sinks + BN - 1) / BN;
+    x.skip = max(0, x.lo / BN - x.st);
+  }
+  x.T = x.hi / BN + 1 - x.skip;
+  return x;
+}
+
+struct SeqInfo {
+  int n0, C, len;
+  int units;        // per KV head; 0 for an empty chunk or a malformed one
+  int bad;          // the extent is malformed
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const ChunkArgs& a, int b) {
+  SeqInfo s;
+  s.n0 = __ldg(a.token_offsets + b);
+  const long long c = static_cast<long long>(__ldg(a.token_offsets + b + 1)) - s.n0;
+  s.len = __ldg(a.seq_lens + b);
+  s.bad = c < 0 || (c > 0 && (s.n0 < 0 || s.n0 + c > a.total_tokens || s.len < c || s.len > a.max_len));
+  s.C = s.bad ? 0 : static_cast<int>(c);
+  s.units = (s.C + a.unit_tokens - 1) / a.unit_tokens;
+  return s;
+}
+
+// Exclusive scan over the 256 softmax threads; *total = the sum.
+__device__ __forceinline__ int scan256(int v, int* scratch, int sid, int* total) {
+  const int lane = sid & 31, w = sid >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scratch[w] = x;
+  named_sync(kBarPair, kSoftmaxThreads);
+  int before = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int s = scratch[k];
+    if (k < w) before += s;
+    all += s;
+  }
+  named_sync(kBarPair, kSoftmaxThreads);  // scratch may be reused
+  *total = all;
+  return before + x - v;
+}
+
+// Range boundaries of V CTAs on a line of W tiles: CTA v takes [start(v),
+// start(v+1)) with start(v) = floor(v W / V), computed as v q + floor(v r / V)
+// with W = q V + r.  floor(v r / V) (v r <= V^2 < 2^24) comes from the fp32
+// product with 1/V, within one of the quotient, and one integer correction.
+struct Line {
+  int V, q, r;
+  float rV;  // 1 / V
+  float VW;  // V / W
+  __device__ __forceinline__ int start(int v) const {
+    const int n = v * r;
+    int k = static_cast<int>(static_cast<float>(n) * rV);
+    if (k * V > n) {
+      --k;
+    } else if ((k + 1) * V <= n) {
+      ++k;
+    }
+    return v * q + k;
+  }
+  // the CTA whose range holds position p (0 <= p < W): the fp32 estimate
+  // p V / W is within two of it; exact integer steps finish it
+  __device__ __forceinline__ int owner(int p) const {
+    int o = min(V - 1, max(0, static_cast<int>(static_cast<float>(p) * VW)));
+#pragma unroll 1
+    for (int k = 0; k < 4 && o > 0 && start(o) > p; ++k) --o;
+#pragma unroll 1
+    for (int k = 0; k < 4 && o + 1 < V && start(o + 1) <= p; ++k) ++o;
+    return o;
+  }
+};
+
+// Builds this CTA's pieces of scheduling round `round` into shared memory
+// (the 256 softmax threads).  `line` is filled in round 0.  Sequences are
+// taken 256 at a time, and the units of such a chunk 256 at a time, one per
+// thread: the tiles of a unit are hkv consecutive runs of T on the line.  In
+// round 0 the rows of malformed sequences are zeroed and their status recorded.
+template <int D, bool F8>
+__device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int sid, Line* line) {
+  using Ly = Layout<D, F8>;
+  Misc* misc = reinterpret_cast<Misc*>(smem + Ly::kMisc);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + Ly::kPieces);
+  int* seq_u = reinterpret_cast<int*>(smem + Ly::kSeq);  // first unit of each sequence
+  int* seq_n0 = seq_u + 256;
+  int* seq_c = seq_n0 + 256;
+  int* seq_ctx = seq_c + 256;
+  int* scratch = seq_ctx + 256;
+
+  int units = 0;      // units of the current chunk of sequences
+  int loaded = -1;    // the chunk in shared memory
+  auto load_chunk = [&](int base) {
+    if (loaded == base) return;
+    const int b = base + sid;
+    SeqInfo s;
+    s.units = s.n0 = s.C = s.len = s.bad = 0;
+    if (b < a.batch) s = seq_info(a, b);
+    if (round == 0 && s.bad && b % gridDim.x == blockIdx.x) {
+      record_status(a.status, b, kBadTree);
+      misc->zero_needed = 1;
+    }
+    seq_u[sid] = scan256(s.units, scratch, sid, &units);
+    seq_n0[sid] = s.n0;
+    seq_c[sid] = s.C;
+    seq_ctx[sid] = s.len - s.C;
+    loaded = base;
+    named_sync(kBarPair, kSoftmaxThreads);
+  };
+  // unit j of the loaded chunk: its sequence (the last whose first unit is
+  // <= j: sequences without units share the next one's) and its extent
+  auto locate = [&](int j, int& i, int& u) {
+    i = 0;
+#pragma unroll
+    for (int step = 128; step > 0; step >>= 1)
+      if (seq_u[i + step] <= j) i += step;
+    u = j - seq_u[i];
+    return unit_of(a, seq_ctx[i], seq_c[i], u);
+  };
+
+  // a chunk with at most 256 units is located once for both passes
+  Unit x;
+  int xi = 0, xu = 0, xbase = -1;
+  if (round == 0) {
+    int W = 0;
+    for (int base = 0; base < a.batch; base += kSoftmaxThreads) {
+      load_chunk(base);
+      for (int ub = 0; ub < units; ub += kSoftmaxThreads) {
+        int T = 0, tot;
+        if (ub + sid < units) {
+          x = locate(ub + sid, xi, xu);
+          T = x.T;
+        }
+        xbase = base + ub;
+        scan256(T, scratch, sid, &tot);
+        W += tot * a.hkv;
+      }
+      if (base + kSoftmaxThreads < a.batch || units > kSoftmaxThreads) xbase = -1;
+      named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
+    }
+    line->V = max(1, min(a.vctas, W / max(1, a.min_tiles)));
+    line->q = W / line->V;
+    line->r = W % line->V;
+    line->rV = 1.0f / static_cast<float>(line->V);
+    line->VW = W > 0 ? static_cast<float>(line->V) / static_cast<float>(W) : 0.0f;
+    if (misc->zero_needed) {
+      // the rows of a malformed sequence that can be addressed get zeros
+      const size_t row_bytes = static_cast<size_t>(a.hq) * D * (a.out_fp32 ? 4 : 2);
+      for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+        if (!seq_info(a, b).bad) continue;
+        const long long n0 = a.token_offsets[b], n1 = a.token_offsets[b + 1];
+        if (n0 < 0 || n1 <= n0 || n1 > a.total_tokens) continue;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
+        for (size_t k = sid; k < (n1 - n0) * row_bytes / 16; k += kSoftmaxThreads) dst[k] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  const int v = static_cast<int>(blockIdx.x);
+  int count = 0;  // pieces of this CTA so far (all rounds)
+  const int s_v = v < line->V ? line->start(v) : 0, e_v = v < line->V ? line->start(v + 1) : 0;
+  int cum = 0;    // line position of the next group of units
+  for (int base = 0; base < a.batch && cum < e_v; base += kSoftmaxThreads) {
+    load_chunk(base);
+    for (int ub = 0; ub < units && cum < e_v; ub += kSoftmaxThreads) {
+      const bool have = ub + sid < units;
+      if (xbase != base + ub && have) x = locate(ub + sid, xi, xu);
+      int tot;
+      const int c0 = cum + scan256(have ? x.T * a.hkv : 0, scratch, sid, &tot);
+      cum += tot;
+      // KV heads [h0, h1) of this unit meet [s_v, e_v)
+      int h0 = 0, h1 = 0;
+      if (have && c0 < e_v && c0 + x.T * a.hkv > s_v) {
+        h0 = max(0, s_v - c0) / x.T;
+        h1 = (min(e_v - c0, x.T * a.hkv) + x.T - 1) / x.T;
+      }
+      int ptot;
+      int k = count + scan256(h1 - h0, scratch, sid, &ptot) - round * kMaxPieces;
+      count += ptot;
+      for (int h = h0; h < h1; ++h, ++k) {
+        if (k < 0 || k >= kMaxPieces) continue;
+        const int u0 = c0 + h * x.T;  // line position of the unit's first tile
+        Piece pc;
+        pc.b = base + xi;
+        pc.kvh = h;
+        pc.tok0 = seq_n0[xi] + xu * a.unit_tokens;
+        pc.pos0 = x.pos0;
+        pc.lo = x.lo;
+        pc.hi = x.hi;
+        pc.st = x.st;
+        pc.skip = x.skip;
+        pc.t0 = max(s_v - u0, 0);
+        pc.t1 = min(e_v - u0, x.T);
+        pc.rows = x.ntok * a.group;
+        pc.slot = pc.cnt = -1;
+        pc.npieces = 1;
+        pc.vfirst = v;
+        pc.pad = 0;
+        if (pc.t0 > 0 || pc.t1 < x.T) {
+          // the first piece (it holds tile 0) uses the CTA's slot 1, every
+          // later piece (it starts the CTA's range) slot 0
+          pc.vfirst = line->owner(u0);
+          pc.npieces = line->owner(u0 + x.T - 1) - pc.vfirst + 1;
+          pc.cnt = pc.vfirst;
+          pc.slot = 2 * v + (pc.t0 > 0 ? 0 : 1);
+        }
+        pieces[k] = pc;
+      }
+    }
+    named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
+  }
+  if (sid == 0) {
+    const int n = count - round * kMaxPieces;
+    misc->npieces = max(0, min(kMaxPieces, n));
+    misc->more = n > kMaxPieces;
+    for (int k = 0; k < kMaxPieces; ++k) misc->piece_bad[k] = 0;
+  }
+}
+
+// ---------------------------------------------------------------- output
+// Writes 32 values of one output row (fp32 or bf16) at column c0.
+template <int D>
+__device__ __forceinline__ void store_row_chunk(const ChunkArgs& a, size_t row, int c0,
+                                                const float (&v)[32]) {
+  if (a.out_fp32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + c0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * D + c0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint4 w;
+      w.x = pack_bf16x2(v[8 * k + 0], v[8 * k + 1]);
+      w.y = pack_bf16x2(v[8 * k + 2], v[8 * k + 3]);
+      w.z = pack_bf16x2(v[8 * k + 4], v[8 * k + 5]);
+      w.w = pack_bf16x2(v[8 * k + 6], v[8 * k + 7]);
+      dst[k] = w;
+    }
+  }
+}
+
+// Merges the pieces of a split unit: O = sum_s 2^(m_s - M) O_s /
+// sum_s 2^(m_s - M) l_s in piece order.  The (row, 4 columns) items of the
+// unit are spread over the nthr participants, rows fastest: a unit of 8 decode
+// rows split 20 ways still has 256 independent items, and a warp's loads are
+// consecutive.
+template <int D>
+__device__ void merge_unit(const ChunkArgs& a, const Piece& pc, int ur, int nthr) {
+  using Sl = Slot<D>;
+  const uint8_t* first = a.slots + static_cast<size_t>(2 * pc.vfirst + 1) * Sl::kBytes;
+  auto base = [&](int s) {
+    return s == 0 ? first : a.slots + static_cast<size_t>(2 * (pc.vfirst + s)) * Sl::kBytes;
+  };
+  int bad = 0;
+#pragma unroll 4
+  for (int s = 0; s < pc.npieces; ++s) bad |= __ldcg(reinterpret_cast<const int*>(base(s) + Sl::kFlag));
+  for (int it = ur; it < pc.rows * (D / 4); it += nthr) {
+    const int row = it % pc.rows, d4 = it / pc.rows;
+    float M = -INFINITY;
+#pragma unroll 4
+    for (int s = 0; s < pc.npieces; ++s)
+      M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row).x);
+    float l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = 0; s < pc.npieces; ++s) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(base(s) + Sl::kO) + it);
+      const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+      l += w * ml.y;
+      acc.x += w * o.x;
+      acc.y += w * o.y;
+      acc.z += w * o.z;
+      acc.w += w * o.w;
+    }
+    const float inv = (l > 0.0f && !bad) ? 1.0f / l : 0.0f;
+    if (bad) acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const size_t out_row = static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group;
+    if (a.out_fp32) {
+      reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D)[d4] =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D)[d4] =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+  }
+}
+
+// status and the ticket counters start at zero.  The attention kernel may
+// start while this one runs (programmatic dependent launch); it waits for its
+// end before it touches either.
+__global__ void chunk_init_kernel(int32_t* status, int batch, int32_t* counters, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < batch; i += blockDim.x) status[i] = kOk;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D, bool F8>
+__global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
+    chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
+  using Ly = Layout<D, F8>;
+  using Sl = Slot<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  constexpr int kStages = Ly::kStages;
+  constexpr int kVStages = Ly::kVStages;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Ly::kBar);
+  uint64_t* kempty = kfull + kStages;
+  uint64_t* vfull = kempty + kStages;
+  uint64_t* vempty = vfull + kVStages;    // F8: the converters have read the raw V
+  uint64_t* s_full = vempty + kVStages;   // [2]: S_h(t) complete (and every MMA before it)
+  uint64_t* p_a = s_full + 2;             // [2]: P_h(t) of keys 0 .. 63 in TMEM (128 arrivals)
+  uint64_t* p_b = p_a + 2;                // [2]: P_h(t) of keys 64 .. 127
+  uint64_t* o_done = p_b + 2;             // [2]: the last P_h V of a piece complete
+  uint64_t* q_full = o_done + 2;          // [2]: Q_h of a piece in shared memory (128 arrivals)
+  uint64_t* drain = q_full + 2;           // every MMA issued so far complete (once per round)
+  uint64_t* v16full = drain + 1;          // F8 [2]: V(t) converted (64 arrivals)
+  uint64_t* v16empty = v16full + 2;       // F8 [2]: the P V of tile t complete
+  uint64_t* sfull = v16empty + 2;         // F8 [8]: the scales of tile t landed (32 arrivals)
+  Misc* misc = reinterpret_cast<Misc*>(smem + Ly::kMisc);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + Ly::kPieces);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  if (tid == 0) {
+    misc->abort = 0;
+    misc->zero_needed = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], F8 ? kConvThreads : 1);
+    }
+    if constexpr (F8) {
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&v16full[k], kConvThreads);
+        mbar_init(&v16empty[k], 1);
+      }
+      for (int k = 0; k < kSclSlots; ++k) mbar_init(&sfull[k], 32);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_full[h], 1);
+      mbar_init(&p_a[h], BM);
+      mbar_init(&p_b[h], BM);
+      mbar_init(&o_done[h], 1);
+      mbar_init(&q_full[h], BM);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&misc->tmem_base, Ly::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // status and counters are zero
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem_base;
+  volatile int* abort_flag = &misc->abort;
+  const int g = a.group;
+  Line line;
+
+  // Progress kept across pieces and rounds (ring slots and barrier phases):
+  // g_tile = K/V tiles of every earlier round; in a role, the tiles and the
+  // pieces of m-tile h so far (MMA: both m-tiles; softmax: its own).
+  int g_tile = 0;
+  int tiles_h0 = 0, tiles_h1 = 0, pieces_h0 = 0, pieces_h1 = 0;
+
+  for (int round = 0;; ++round) {
+    if (warp < kTmaWarp) build_schedule<D, F8>(a, smem, round, tid, &line);
+    __syncthreads();
+    const int npieces = misc->npieces;
+    const bool more = misc->more != 0;
+    if (npieces == 0 || misc->abort) break;
+
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------ TMA producer
+      // Lane 0 arms the slot's barrier, then lane u issues the box of page u
+      // of the tile.  K runs ahead of V: a K slot is free again once the last
+      // S of its tile is done, a V slot once the last P V is.
+      if (round == 0 && lane == 0) {
+        prefetch_tmap(&maps.k_pool);
+        prefetch_tmap(&maps.v_pool);
+      }
+      constexpr int kPages = BN / 16;
+      constexpr int kUnseen = INT_MIN;  // no row of the unit sees the page -> zeros
+      const bool page_lane = lane < kPages;
+      const int pool_pages = a.num_blocks * a.hkv;
+      int* blk_ring = reinterpret_cast<int*>(smem + Ly::kBlk);  // [tile & 7][page]
+      volatile int* piece_bad = misc->piece_bad;
+      auto fetch_block = [&](int p, int t) -> int {
+        if (p >= npieces || !page_lane) return kUnseen;
+        const Piece& pc = pieces[p];
+        const int lp = (t < pc.st ? t : t + pc.skip) * kPages + lane;
+        const int k0 = lp * 16;
+        return k0 <= pc.hi && (k0 < a.sinks || k0 + 15 >= pc.lo)
+                   ? __ldg(a.block_table + static_cast<size_t>(pc.b) * a.max_blocks_per_seq + lp)
+                   : kUnseen;
+      };
+      // issues a tile (global tile tau) of piece p of tensor kv (0 = K, 1 = V)
+      auto issue = [&](int p, int tau, int kv, int blk) {
+        const Piece& pc = pieces[p];
+        const int st = kv ? tau % kVStages : tau % kStages;
+        uint64_t* bar = kv ? &vfull[st] : &kfull[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, Ly::kKTileBytes);
+        __syncwarp();
+        uint8_t* tile = smem + (kv ? Ly::kVRing : Ly::kKRing) + st * Ly::kKTileBytes;
+        const bool good = blk >= 0 && blk < a.num_blocks;
+        if (page_lane) {
+          const int page = good ? blk * a.hkv + pc.kvh : pool_pages;  // out of bounds: zero fill
+          if (!good && blk != kUnseen && kv == 0) {  // malformed block id: zeros, reported
+            piece_bad[p] = 1;
+            record_status(a.status, pc.b, kBadTree);
+          }
+          const CUtensorMap* map = kv ? &maps.v_pool : &maps.k_pool;
+          if constexpr (F8) {
+            tma_load_3d(tile + lane * 2048, map, bar, 0, 0, page);
+          } else {
+            tma_load_5d(tile + lane * 2 * Ly::kGroupBytes, map, bar, 0, 0, 0, 0, page);
+          }
+        }
+        if constexpr (F8) {
+          if (kv == 0) {
+            // the tile's K and V scales into slot tau % 8: lane u the keys
+            // 4u .. 4u+3 (page u / 4); 0 where the page is not read
+            float* sc = reinterpret_cast<float*>(smem + Ly::kScl) + (tau % kSclSlots) * 2 * BN + 4 * lane;
+            const int pblk = __shfl_sync(0xffffffffu, blk, lane >> 2);
+            const bool read = pblk >= 0 && pblk < a.num_blocks;
+            const size_t idx = read ? (static_cast<size_t>(pblk) * a.hkv + pc.kvh) * 16 + (lane & 3) * 4 : 0;
+            cpa16_zfill(sc, a.k_scale + idx, read ? 16 : 0);
+            cpa16_zfill(sc + BN, a.v_scale + idx, read ? 16 : 0);
+            cpa_arrive_noinc(&sfull[tau % kSclSlots]);
+          }
+        }
+      };
+      auto advance = [&](int& p, int& t) {
+        if (++t >= pieces[p].t1) {
+          ++p;
+          if (p < npieces) t = pieces[p].t0;
+        }
+      };
+      int kp = 0, kt = pieces[0].t0, vp = 0, vt = pieces[0].t0;
+      int blk_k = fetch_block(kp, kt);  // the block ids of the next K tile, read ahead
+      int tk = g_tile, tv = g_tile;
+      bool ok = true;
+      unsigned long long t_idle = 0;
+      while (vp < npieces) {
+        bool progressed = false;
+        // V before K: the next P V needs its V tile before the S after it
+        // needs its K tile, and the copies of one warp land in issue order
+        if (tv < tk) {
+          int ready = lane == 0 ? mbar_test_wait(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1) : 0;
+          if (__shfl_sync(0xffffffffu, ready, 0)) {
+            issue(vp, tv, 1, page_lane ? blk_ring[(tv & 7) * 8 + lane] : kUnseen);
+            ++tv;
+            advance(vp, vt);
+            progressed = true;
+          }
+        }
+        if (kp < npieces) {
+          // a K tile only when no V copy could be issued now instead
+          int ready = 0;
+          if (lane == 0) {
+            const bool v_free = tv < tk && mbar_test_wait(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1);
+            ready = !v_free && mbar_test_wait(&kempty[tk % kStages], ((tk / kStages) & 1) ^ 1);
+          }
+          if (__shfl_sync(0xffffffffu, ready, 0)) {
+            if (page_lane) blk_ring[(tk & 7) * 8 + lane] = blk_k;
+            issue(kp, tk, 0, blk_k);
+            ++tk;
+            advance(kp, kt);
+            blk_k = fetch_block(kp, kt);
+            progressed = true;
+          }
+        }
+        int stop = 0;
+        if (!progressed && lane == 0) {
+          // sleep (at most about 200 ns) on the slot likely to free first
+          // instead of polling, which takes issue slots from the softmax
+          const bool k_next = kp < npieces;
+          const bool v_next = tv < tk;
+          if (v_next && (!k_next || tv - kVStages < tk - kStages))
+            mbar_try_wait_ns(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1, 200);
+          else if (k_next)
+            mbar_try_wait_ns(&kempty[tk % kStages], ((tk / kStages) & 1) ^ 1, 200);
+        }
+        if (lane == 0) {
+          if (progressed) {
+            t_idle = 0;
+          } else if (t_idle == 0) {
+            t_idle = global_ns();
+          } else if (global_ns() - t_idle > kWaitLimitNs || misc->abort) {
+            stop = 1;
+          }
+        }
+        if (__shfl_sync(0xffffffffu, stop, 0)) {
+          ok = false;
+          break;
+        }
+      }
+      if constexpr (F8) cpa_wait_all();  // this lane's scale copies have landed
+      if (lane == 0) {
+        if (!ok) {
+          record_status(a.status, pieces[min(vp, npieces - 1)].b, kDeviceTimeout);
+          misc->abort = 1;
+        }
+        // every issued copy has landed before the ring is reused or the CTA
+        // exits (at most a ring of each can still be in flight)
+        for (int t = max(g_tile, tk - kStages); t < tk; ++t)
+          mbar_wait(&kfull[t % kStages], (t / kStages) & 1);
+        for (int t = max(g_tile, tv - kVStages); t < tv; ++t)
+          mbar_wait(&vfull[t % kVStages], (t / kVStages) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        // bf16: both products on kind::f16 in bf16.  E4M3: S on kind::f8f6f4
+        // over the codes, P V on kind::f16 in fp16.
+        constexpr uint32_t idesc_s = F8 ? idesc_e4m3(BM, BN) : idesc_bf16(BM, BN, 0);
+        constexpr uint32_t idesc_o = F8 ? idesc_f16(BM, D, 1) : idesc_bf16(BM, D, 1);
+        // K and Q (K-major): 8-row groups at kGroupBytes (16-bit) or 1024
+        // (8-bit), 64-column halves at +1024.  V (MN-major): 8-key groups at
+        // kGroupBytes, column halves at +1024.
+        constexpr uint32_t kKRow8 = F8 ? 1024 : Ly::kGroupBytes;
+        const uint64_t dk0 = smem_desc(smem_u32(smem + Ly::kKRing), 16, kKRow8);
+        const uint64_t dv0 = smem_desc(smem_u32(smem + (F8 ? Ly::kV16 : Ly::kVRing)), 1024, Ly::kGroupBytes);
+        const uint64_t dq0 = smem_desc(smem_u32(smem + Ly::kQ), 16, kKRow8);
+        auto issue_s = [&](int h, int t) {  // S_h = Q_h K(t)^T into columns 128 h
+          const uint64_t dk = dk0 + static_cast<uint64_t>((t % kStages) * (Ly::kKTileBytes >> 4));
+          const uint64_t dq = dq0 + static_cast<uint64_t>(h * (Ly::kQBytes >> 4));
+          if constexpr (F8) {
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row per MMA
+              mma_f8_ss(tmem + h * BN, dq + kk * 2, dk + kk * 2, idesc_s, kk > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+              mma_bf16_ss(tmem + h * BN, dq + off, dk + off, idesc_s, kk > 0 ? 1u : 0u);
+            }
+          }
+          mma_commit(&s_full[h]);
+        };
+        // O_h (+)= P_h V(t) over keys 64 half .. 64 half + 63
+        auto issue_pv = [&](int h, int t, int half, bool acc) {
+          const uint64_t dv = dv0 + static_cast<uint64_t>((F8 ? (t & 1) : (t % kVStages)) * (Ly::kTileBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < BN / 32; ++k) {
+            const int kk = half * (BN / 32) + k;
+            mma_bf16_ts(tmem + 256 + h * D, tmem + h * BN + kk * 8,
+                        dv + ((kk * 2 * Ly::kGroupBytes) >> 4), idesc_o, (acc || k > 0) ? 1u : 0u);
+          }
+        };
+        bool ok = true;
+        int tau = g_tile;
+        for (int p = 0; p < npieces && ok; ++p) {
+          const int nm = pieces[p].rows > BM ? 2 : 1, T = pieces[p].t1 - pieces[p].t0;
+          // the piece's first S of each m-tile, once its Q is loaded and K has landed
+          for (int h = 0; h < nm && ok; ++h) {
+            ok = mbar_wait(&q_full[h], (h ? pieces_h1 : pieces_h0) & 1, abort_flag);
+            if (ok && h == 0) ok = mbar_wait(&kfull[tau % kStages], (tau / kStages) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(h, tau);
+          }
+          if (!ok) break;
+          mma_commit(&kempty[tau % kStages]);
+          for (int i = 0; i < T && ok; ++i) {
+            const int t = tau + i;
+            for (int h = 0; h < nm; ++h) {
+              const int ph = (h ? tiles_h1 : tiles_h0) & 1;
+              ok = mbar_wait(&p_a[h], ph, abort_flag);
+              if (ok && h == 0) {
+                if constexpr (F8) {
+                  ok = mbar_wait(&v16full[t & 1], (t >> 1) & 1, abort_flag);  // V(t) in fp16
+                } else {
+                  ok = mbar_wait(&vfull[t % kVStages], (t / kVStages) & 1, abort_flag);
+                }
+              }
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(h, t, 0, i > 0);
+              ok = mbar_wait(&p_b[h], ph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(h, t, 1, true);
+              if (i + 1 < T) {
+                if (h == 0) {
+                  ok = mbar_wait(&kfull[(t + 1) % kStages], ((t + 1) / kStages) & 1, abort_flag);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                issue_s(h, t + 1);
+              }
+              if (h) ++tiles_h1; else ++tiles_h0;
+            }
+            if (!ok) break;
+            // the V slot (F8: the converted slot) and the K slot are free
+            if constexpr (F8) {
+              mma_commit(&v16empty[t & 1]);
+            } else {
+              mma_commit(&vempty[t % kVStages]);
+            }
+            if (i + 1 < T) mma_commit(&kempty[(t + 1) % kStages]);
+          }
+          if (!ok) break;
+          mma_commit(&o_done[0]);
+          ++pieces_h0;
+          if (nm == 2) {
+            mma_commit(&o_done[1]);
+            ++pieces_h1;
+          }
+          tau += T;
+        }
+        if (!ok) {
+          record_status(a.status, pieces[0].b, kDeviceTimeout);
+          misc->abort = 1;
+        }
+        // every MMA issued so far completes before the next round or the exit
+        mma_commit(drain);
+        mbar_wait(drain, round & 1);
+      }
+      __syncwarp();
+    } else if (F8 && warp >= kConvWarp) {
+      // ------------------------------------------------------ V conversion (E4M3)
+      // Per tile: each key's row as fp16 of code x V scale (one rounding of
+      // the exact product) into converted slot t % 2, in the MN-major layout
+      // the P V MMA reads.  Keys that no row of the unit sees get zero rows
+      // (their codes may be stale).
+      if constexpr (F8) {
+        const int ct = tid - kConvWarp * 32;  // 0 .. 63
+        const float* scl = reinterpret_cast<const float*>(smem + Ly::kScl);
+        bool ok = true;
+        int tau = g_tile;
+        for (int p = 0; p < npieces; ++p) {
+          const Piece& pc = pieces[p];
+          for (int t = pc.t0; t < pc.t1; ++t, ++tau) {
+            const int vs = tau % kVStages;
+            if (ok) ok = mbar_wait(&vfull[vs], (tau / kVStages) & 1, abort_flag);
+            if (ok) ok = mbar_wait(&sfull[tau % kSclSlots], (tau / kSclSlots) & 1, abort_flag);
+            if (ok && tau >= 2) ok = mbar_wait(&v16empty[tau & 1], ((tau - 2) >> 1) & 1, abort_flag);
+            if (!ok) {
+              misc->abort = 1;
+            } else {
+              const float* sv = scl + (tau % kSclSlots) * 2 * BN + BN;
+              // thread ct: the 16 codes of columns 16c .. 16c+15 (c = ct % 8)
+              // of keys k0 + 8i, k0 = ct / 8, i = 0 .. 15.  Raw: 128 bytes a
+              // key, 16-byte chunk c at chunk c ^ (key % 8); fp16: [8-key
+              // group][64-column half][key][128 B], 16-byte chunk q of a
+              // line at chunk q ^ (key % 8).  key % 8 = k0 for every i.
+              const int k0 = ct >> 3, c = ct & 7;
+              const int key0 = (t < pc.st ? t : t + pc.skip) * BN + k0;
+              const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + k0 * 128 + ((c ^ k0) << 4);
+              uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (c >> 2) * 1024 + k0 * 128;
+              const int q0 = (((2 * c) & 7) ^ k0) << 4, q1 = (((2 * c + 1) & 7) ^ k0) << 4;
+#pragma unroll 1
+              for (int i = 0; i < 16; ++i) {
+                const int key = key0 + 8 * i;
+                uint32_t h[8];
+                if (key <= pc.hi && (key < a.sinks || key >= pc.lo)) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(raw + i * 1024);
+                  const float s1 = sv[k0 + 8 * i];
+                  const float2 s2 = make_float2(s1, s1);
+                  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    // codes -> fp16 (exact) -> fp32, times the scale, -> fp16
+                    uint32_t c01, c23;
+                    e4m3x4_to_f16x2x2(ww[k], c01, c23);
+                    const float2 v01 = mul2(unpack_f16x2(c01), s2);
+                    const float2 v23 = mul2(unpack_f16x2(c23), s2);
+                    h[2 * k] = pack_f16x2(v01.x, v01.y);
+                    h[2 * k + 1] = pack_f16x2(v23.x, v23.y);
+                  }
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) h[k] = 0u;
+                }
+                uint8_t* dst = v16 + i * Ly::kGroupBytes;
+                *reinterpret_cast<uint4*>(dst + q0) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(dst + q1) = make_uint4(h[4], h[5], h[6], h[7]);
+              }
+              fence_proxy_async_smem();  // generic writes, read by the MMA
+            }
+            mbar_arrive(&v16full[tau & 1]);
+            mbar_arrive(&vempty[vs]);
+          }
+        }
+        if (!ok) record_status(a.status, pieces[0].b, kDeviceTimeout);
+      }
+    } else {
+      // ------------------------------------------------------ softmax groups
+      // Warps 4h .. 4h+3 own m-tile h; warp w's rows are its TMEM lane
+      // quarter 32 (w % 4) .. +31.
+      const int h = warp >> 2;
+      const int r = (warp & 3) * 32 + lane;  // row of the m-tile == TMEM lane
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tmem_s = tmem + h * BN + lane_off;
+      const uint32_t tmem_o = tmem + 256 + h * D + lane_off;
+      uint8_t* qh = smem + Ly::kQ + h * Ly::kQBytes;
+      volatile int* piece_bad = misc->piece_bad;
+      int my_tiles = h ? tiles_h1 : tiles_h0;
+      int my_pieces = h ? pieces_h1 : pieces_h0;
+      bool ok = true;
+      int tau = g_tile;  // global index of the piece's first tile
+      for (int p = 0; p < npieces; ++p) {
+        const Piece pc = pieces[p];
+        const int T = pc.t1 - pc.t0;
+        const int nm = pc.rows > BM ? 2 : 1;
+        if (h >= nm) {  // this m-tile has no rows in the unit
+          tau += T;
+          continue;
+        }
+        const int ur = h * BM + r;                 // row of the unit
+        const bool live = ur < pc.rows;
+        const int tok = live ? ur / g : 0;
+        const int pos = pc.pos0 + tok;             // position of this row
+        const size_t q_row = static_cast<size_t>(pc.tok0 + tok);
+        const int head = pc.kvh * g + (live ? ur - tok * g : 0);
+        // Q rows -> shared memory in the 128-byte swizzled K-major layout
+        // (the 16-byte chunk c of row r sits at chunk c ^ (r % 8)); rows past
+        // the unit are zero.  The buffer is free: the previous piece's last
+        // S_h completed before its epilogue.  E4M3: one 128-byte line of
+        // codes a row, and the row's scale folded into the exponent factor
+        // (kept above 0, so that a masked -inf never meets a factor of 0).
+        float cq = a.scale_log2;
+        {
+          constexpr int kRowBytes = F8 ? D : 2 * D;
+          constexpr int kLineBytes = F8 ? 1024 : Ly::kGroupBytes;  // 8 rows
+          uint8_t* dst = qh + (r >> 3) * kLineBytes + (r & 7) * 128;
+          if (live) {
+            const uint8_t* src = static_cast<const uint8_t*>(a.q) + q_row * a.q_stride_bytes +
+                                 static_cast<size_t>(head) * kRowBytes;
+#pragma unroll
+            for (int k = 0; k < kRowBytes / 16; ++k)
+              cpa16(dst + (k >> 3) * 1024 + (((k & 7) ^ (r & 7)) << 4), src + k * 16);
+            if constexpr (F8) cq = fmaxf(a.scale_log2 * __ldg(a.q_scale + q_row * a.hq + head), 1e-37f);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kRowBytes / 16; ++k)
+              *reinterpret_cast<uint4*>(dst + (k >> 3) * 1024 + k % 8 * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        // the next piece's Q row of this thread into L2
+        if (p + 1 < npieces && ur < pieces[p + 1].rows) {
+          const Piece& nx = pieces[p + 1];
+          const uint8_t* q = static_cast<const uint8_t*>(a.q) +
+                             static_cast<size_t>(nx.tok0 + ur / g) * a.q_stride_bytes +
+                             static_cast<size_t>(nx.kvh * g + ur % g) * (F8 ? D : 2 * D);
+#pragma unroll
+          for (int k = 0; k < (F8 ? D : 2 * D); k += 128) prefetch_l2(q + k);
+        }
+        cpa_wait_all();
+        fence_proxy_async_smem();  // generic writes of Q, read by the MMA
+        mbar_arrive(&q_full[h]);
+
+        float m_run = -INFINITY;  // running max (log2 units)
+        float l_run = 0.0f;       // row sum against m_run
+        for (int i = 0; i < T; ++i) {
+          const int t = pc.t0 + i;                                 // tile of the unit
+          const int k0 = (t < pc.st ? t : t + pc.skip) * BN;       // its first key
+          const int gt = tau + i;                                  // global tile (ring slot)
+          if (ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[h], my_tiles & 1, abort_flag));
+            if constexpr (F8) {  // the keys' K scales (landed with the K tile)
+              ok = ok && __all_sync(0xffffffffu, mbar_wait(&sfull[gt % kSclSlots], (gt / kSclSlots) & 1, abort_flag));
+            }
+            if (!ok) misc->abort = 1;
+          }
+          ++my_tiles;
+          if (!ok) {
+            mbar_arrive(&p_a[h]);
+            mbar_arrive(&p_b[h]);
+            continue;
+          }
+          // some row of the unit does not see some key of the tile
+          const bool masked = k0 + BN - 1 > pc.pos0 ||
+                              (a.window > 0 && pc.hi - a.window >= k0 && k0 + BN > a.sinks);
+          // keys that no row of the unit sees: their V rows are cleared
+          // (stale data; P is 0 there but 0 * NaN would poison O).  Group 0
+          // does it, a row per thread, before P_0(t) V(t), the first reader.
+          if constexpr (!F8) {
+            if (h == 0 && (k0 + BN - 1 > pc.hi || (pc.lo > k0 && k0 + BN > a.sinks))) {
+              const int st = gt % kVStages;
+              mbar_wait(&vfull[st], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
+              const int key = k0 + r;
+              if (!(key <= pc.hi && (key < a.sinks || key >= pc.lo))) {
+                uint8_t* row = smem + Ly::kVRing + st * Ly::kTileBytes + (r >> 3) * Ly::kGroupBytes + (r & 7) * 128;
+#pragma unroll
+                for (int k = 0; k < 8 * Ly::kHalves; ++k)
+                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();  // generic writes, read by the MMA
+            }
+          }
+          // the scores, 32 columns at a time: the next load is in flight
+          // while the max of the last 32 is taken.  They stay unscaled; the
+          // softmax scale is folded into the exponent.
+          float x[128];
+          float mx[4];
+          tc_fence_after();
+          tmem_ld32(tmem_s, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
+            if (c < 3) tmem_ld32(tmem_s + 32 * (c + 1), *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c + 32]));
+            float* y = x + 32 * c;
+            if constexpr (F8) {
+              const float* sk = reinterpret_cast<const float*>(smem + Ly::kScl) + (gt % kSclSlots) * 2 * BN + 32 * c;
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 s4 = *reinterpret_cast<const float4*>(sk + k);
+                const float2 a2 = mul2(make_float2(y[k], y[k + 1]), make_float2(s4.x, s4.y));
+                const float2 b2 = mul2(make_float2(y[k + 2], y[k + 3]), make_float2(s4.z, s4.w));
+                y[k] = a2.x;
+                y[k + 1] = a2.y;
+                y[k + 2] = b2.x;
+                y[k + 3] = b2.y;
+              }
+            }
+            if (masked) {
+              const int kc = k0 + 32 * c;
+              uint32_t bits = bits_below(pos + 1 - kc);
+              if (a.window > 0) bits &= ~bits_below(pos + 1 - a.window - kc) | bits_below(a.sinks - kc);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = (bits & (1u << k)) ? y[k] : -INFINITY;
+            }
+            float u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              u[j] = fmax3(y[j], y[j + 4], y[j + 8]);
+              u[j] = fmax3(u[j], y[j + 12], y[j + 16]);
+              u[j] = fmax3(u[j], y[j + 20], y[j + 24]);
+              u[j] = fmaxf(u[j], y[j + 28]);
+            }
+            mx[c] = fmax3(u[0], u[1], fmaxf(u[2], u[3]));
+          }
+          const float smax = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cq;
+          float alpha = 1.0f;
+          bool rescale = false;
+          if (smax != -INFINITY) {
+            if (m_run == -INFINITY) {
+              m_run = smax;
+            } else if (smax > m_run + kRescaleLog2) {
+              alpha = exp2f(m_run - smax);
+              m_run = smax;
+              rescale = true;
+            }
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            // O holds P(..t-1) V against the old max; P_h(t-1) V is complete
+            // (S_h(t), which this thread has seen complete, was issued after it)
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(tmem_o + c0, o);
+              tmem_ld_wait32(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(tmem_o + c0, o);
+            }
+            l_run *= alpha;  // (this tile's sum is added below, against the new max)
+          }
+          // P = 2^(s * scale * log2(e) - m) as 16-bit pairs (column c holds
+          // keys 2c, 2c+1), written over S_h; masked scores are -inf -> 0
+          const float mref = m_run == -INFINITY ? 0.0f : m_run;
+          const float2 sc2 = make_float2(cq, cq);
+          const float2 nm2 = make_float2(-mref, -mref);
+          uint32_t pk[4][16];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 e = fma2(make_float2(x[32 * q4 + 2 * k], x[32 * q4 + 2 * k + 1]), sc2, nm2);
+              const float e0 = ex2_approx(e.x), e1 = ex2_approx(e.y);
+              pk[q4][k] = F8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+            }
+            tmem_st16(tmem_s + 16 * q4, pk[q4]);
+            if (q4 == 1 || q4 == 3) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(q4 == 1 ? &p_a[h] : &p_b[h]);
+            }
+          }
+          // the row sum of the rounded values, under the MMAs
+          float2 lacc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              if constexpr (F8) {
+                acc_f16x2(pk[q4][k], lacc[k & 1]);
+              } else {
+                acc_bf16x2(pk[q4][k], lacc[k & 1]);
+              }
+            }
+          l_run += (lacc[0].x + lacc[1].x) + (lacc[0].y + lacc[1].y);
+        }
+        // -------------------------------------------------- piece epilogue
+        bool done = false;
+        if (ok) {
+          done = __all_sync(0xffffffffu, mbar_wait(&o_done[h], my_pieces & 1, abort_flag));
+          if (!done) {
+            ok = false;
+            misc->abort = 1;
+            record_status(a.status, pc.b, kDeviceTimeout);
+          }
+        }
+        ++my_pieces;
+        const bool bad = piece_bad[p] != 0;
+        tc_fence_after();
+        if (pc.slot < 0) {
+          // the whole unit: normalise and write
+          const float inv_l = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+            if (done) {
+              tmem_ld32(tmem_o + c0, o);
+              tmem_ld_wait32(o);
+            }
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = bad ? 0.0f : __uint_as_float(o[k]) * inv_l;
+            if (live && done) store_row_chunk<D>(a, q_row * a.hq + head, c0, v);
+          }
+        } else {
+          // a piece of a split unit: raw O and (m, l) to its slot, then a
+          // ticket; the last piece to take one merges every slot of the unit
+          const int nthr = nm * BM;
+          const int bar = nm == 2 ? kBarPair : kBarGroup0;
+          uint8_t* sl = a.slots + static_cast<size_t>(pc.slot) * Sl::kBytes;
+          float4* so4 = reinterpret_cast<float4*>(sl + Sl::kO) + ur;
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+            if (done) {
+              tmem_ld32(tmem_o + c0, o);
+              tmem_ld_wait32(o);
+            }
+            if (live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                __stcg(so4 + static_cast<size_t>(c0 / 4 + k) * pc.rows,
+                       make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
+            }
+          }
+          if (live) __stcg(reinterpret_cast<float2*>(sl + Sl::kMl) + ur, make_float2(m_run, l_run));
+          if (ur == 0) __stcg(reinterpret_cast<int*>(sl + Sl::kFlag), (bad || !done) ? 1 : 0);
+          __threadfence();
+          named_sync(bar, nthr);
+          if (ur == 0) misc->merge = atomicAdd(a.counters + pc.cnt, 1) == pc.npieces - 1;
+          named_sync(bar, nthr);
+          if (misc->merge) {
+            __threadfence();
+            merge_unit<D>(a, pc, ur, nthr);
+          }
+          named_sync(bar, nthr);  // misc->merge is rewritten by the next split piece
+        }
+        tc_fence_before();
+        tau += T;
+      }
+      if (h) {
+        tiles_h1 = my_tiles;
+        pieces_h1 = my_pieces;
+      } else {
+        tiles_h0 = my_tiles;
+        pieces_h0 = my_pieces;
+      }
+    }
+    // every role has finished the round's pieces (the TMA copies have
+    // landed, the MMAs are complete)
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    for (int p = 0; p < npieces; ++p) g_tile += pieces[p].t1 - pieces[p].t0;
+    __syncthreads();  // the piece list is rebuilt next round
+    if (!more || misc->abort) break;
+  }
+  if (warp == kMmaWarp) tmem_dealloc(tmem, Ly::kTmemCols);
+}
+
+template <int D, bool F8>
+int launch(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
+  static thread_local int attr_set_device = -1;  // the attribute is set once per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (attr_set_device != dev) {
+    if (cudaFuncSetAttribute(chunk_attn_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<D, F8>::kAlloc) != cudaSuccess)
+      return -1;
+    attr_set_device = dev;
+  }
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.vctas, 1, 1);
+  cfg.blockDim = dim3(F8 ? kThreadsF8 : kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Layout<D, F8>::kAlloc;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D, F8>, a, maps) == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+size_t chunk_slot_bytes(int head_dim) {
+  return head_dim == 64 ? Slot<64>::kBytes : Slot<128>::kBytes;
+}
+
+int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
+  chunk_init_kernel<<<1, 256, 0, stream>>>(a.status, a.batch, a.counters, a.total_tokens > 0 ? a.vctas : 0);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  if (a.total_tokens == 0) return 0;
+  if (a.fp8) return launch<128, true>(a, maps, stream);
+  return a.head_dim == 128 ? launch<128, false>(a, maps, stream) : launch<64, false>(a, maps, stream);
+}
+
+}  // namespace tv

@@ -114,6 +114,64 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The tensor map of a paged pool whose box is one 16-token page of one KV head.
+// E4M3: (128 bytes, 16 rows, pages).  bf16: (64 columns, 8 rows, halves, 2 row
+// groups, pages), landing as [8-row group][64-column half][8 rows][128 B].
+bool encode_pool(CUtensorMap* m, const void* pool, int D, uint64_t pages, bool fp8) {
+  if (fp8) {
+    const cuuint64_t dims[3] = {128, 16, pages};
+    const cuuint64_t str[2] = {128, 2048};
+    const cuuint32_t box[3] = {128, 16, 1};
+    return encode(m, pool, 3, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+  }
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t halves = static_cast<cuuint64_t>(D) / 64;
+  const cuuint64_t dims[5] = {64, 8, halves, 2, pages};
+  const cuuint64_t str[4] = {row, 128, row * 8, row * 16};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(halves), 2, 1};
+  return encode(m, pool, 5, dims, str, box);
+}
+
+struct ChunkPlan {
+  int unit_tokens;  // tokens of a unit
+  int vctas;        // CTAs (ranges of the line of key tiles)
+  size_t workspace; // counters + partial-result slots
+};
+
+// Launch plan of the chunk attention for `sms` SMs: a unit is as many whole
+// tokens as give at most 256 packed rows; the CTAs share the line of key tiles
+// (at most `wmax` by the host hints) in ranges of at least kMinTiles.
+// Workspace: a ticket counter per CTA, then two partial-result slots per CTA.
+bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
+  if (!p || sms < 1) return false;
+  if (p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1) return false;
+  if (p->num_q_heads % p->num_kv_heads || p->num_q_heads / p->num_kv_heads > 256) return false;
+  if (p->head_dim != 64 && p->head_dim != 128) return false;
+  if (p->block_size != TV_BLOCK_SIZE) return false;
+  if (p->total_tokens < 0 || p->num_blocks < 1 || p->max_blocks_per_seq < 1) return false;
+  if (p->max_len < 0 || p->max_len > INT32_MAX - 256) return false;
+  if ((p->max_len + 15) / 16 > p->max_blocks_per_seq) return false;
+  if (p->window < 0 || p->sinks < 0) return false;
+  if (p->out_dtype != TV_OUT_BF16 && p->out_dtype != TV_OUT_FP32) return false;
+  if (static_cast<int64_t>(p->num_blocks) * p->num_kv_heads * 16 >= (1ll << 31)) return false;
+  if (static_cast<int64_t>(p->total_tokens) * p->num_q_heads >= (1ll << 31)) return false;
+  ChunkPlan pl;
+  pl.unit_tokens = 256 / (p->num_q_heads / p->num_kv_heads);
+  const int64_t units = p->total_tokens / pl.unit_tokens + static_cast<int64_t>(std::min(p->batch, p->total_tokens));
+  int64_t tiles = (static_cast<int64_t>(p->max_len) + 127) / 128;
+  if (p->window > 0)  // the sinks' tiles, and the tiles that a unit's windows meet
+    tiles = std::min(tiles, (static_cast<int64_t>(p->sinks) + 127) / 128 +
+                                (static_cast<int64_t>(p->window) + pl.unit_tokens + 253) / 128);
+  const int64_t wmax = units * p->num_kv_heads * std::max<int64_t>(tiles, 1);
+  if (units * p->num_kv_heads >= (1ll << 31) || wmax >= (1ll << 31)) return false;  // counted in 32 bits
+  // at most 4096 CTAs: the range boundaries are fp32 products below 2^24
+  pl.vctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms, wmax / kMinTiles, 4096})));
+  pl.workspace = (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256 +
+                 2 * static_cast<size_t>(pl.vctas) * tv::chunk_slot_bytes(p->head_dim);
+  *out = pl;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -471,4 +529,102 @@ int tv_retained_set(const tv_retain_params* p, const float* draft_probs, uint32_
   a.vocab = p->vocab;
   if (a.threshold < 1) return TV_ERR_INVALID_ARG;
   return tv::launch_retained_set(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+size_t tv_chunk_attention_workspace_size(const tv_chunk_params* p) {
+  ChunkPlan pl;
+  if (!plan_chunk(p, sm_count(), &pl)) return 0;
+  return pl.workspace;
+}
+
+namespace {
+
+// The shared path of tv_chunk_attention and tv_chunk_attention_fp8 (q_scale
+// non-null): checks, tensor maps, arguments and the launch.
+int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q_scale,
+               const void* k_pool, const float* k_scale, const void* v_pool, const float* v_scale,
+               const int32_t* block_table, const int32_t* seq_lens, const int32_t* token_offsets,
+               void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+               cudaStream_t stream) {
+  if (!p) return TV_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
+  if (fp8 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
+  if (p->num_kv_heads > 0 && p->num_q_heads / p->num_kv_heads > 256) return TV_ERR_UNSUPPORTED;
+  ChunkPlan pl;
+  if (!plan_chunk(p, sm_count(), &pl)) return TV_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
+  const int64_t elem = fp8 ? 1 : 2;
+  const int64_t stride = p->q_stride ? p->q_stride : row;
+  if (stride < row || stride > INT64_MAX / 2 || stride * elem % 16) return TV_ERR_INVALID_ARG;
+  const void* ptrs[] = {k_pool, v_pool, block_table, seq_lens, token_offsets, status};
+  for (const void* x : ptrs)
+    if (!x || !aligned16(x)) return TV_ERR_INVALID_ARG;
+  if (p->total_tokens > 0 && (!q || !out)) return TV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return TV_ERR_INVALID_ARG;
+  if (fp8) {
+    if (p->total_tokens > 0 && !q_scale) return TV_ERR_INVALID_ARG;
+    if (!k_scale || !v_scale || !aligned16(q_scale) || !aligned16(k_scale) || !aligned16(v_scale))
+      return TV_ERR_INVALID_ARG;
+  }
+  if (!workspace || workspace_bytes < pl.workspace || !aligned16(workspace))
+    return TV_ERR_WORKSPACE;
+  tv::ChunkMaps maps;
+  const uint64_t pages = static_cast<uint64_t>(p->num_blocks) * p->num_kv_heads;
+  if (!encode_pool(&maps.k_pool, k_pool, p->head_dim, pages, fp8) ||
+      !encode_pool(&maps.v_pool, v_pool, p->head_dim, pages, fp8))
+    return TV_ERR_CUDA;
+  tv::ChunkArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.q = q;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.token_offsets = token_offsets;
+  a.out = out;
+  a.status = status;
+  a.counters = static_cast<int32_t*>(workspace);
+  a.slots = static_cast<uint8_t*>(workspace) + (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256;
+  a.q_stride_bytes = static_cast<size_t>(stride * elem);
+  a.batch = p->batch;
+  a.hq = p->num_q_heads;
+  a.hkv = p->num_kv_heads;
+  a.group = p->num_q_heads / p->num_kv_heads;
+  a.head_dim = p->head_dim;
+  a.max_blocks_per_seq = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  a.max_len = p->max_len;
+  a.total_tokens = p->total_tokens;
+  a.unit_tokens = pl.unit_tokens;
+  a.vctas = pl.vctas;
+  a.min_tiles = kMinTiles;
+  a.window = p->window;
+  a.sinks = p->sinks;
+  a.out_fp32 = p->out_dtype == TV_OUT_FP32 ? 1 : 0;
+  a.fp8 = fp8 ? 1 : 0;
+  const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q_scale = q_scale;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return tv::launch_chunk_attention(a, maps, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // namespace
+
+int tv_chunk_attention(const tv_chunk_params* p, const uint16_t* q, const uint16_t* k_pool,
+                       const uint16_t* v_pool, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* token_offsets, void* out,
+                       int32_t* status, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  return chunk_call(p, false, q, nullptr, k_pool, nullptr, v_pool, nullptr, block_table, seq_lens,
+                    token_offsets, out, status, workspace, workspace_bytes, stream);
+}
+
+int tv_chunk_attention_fp8(const tv_chunk_params* p, const uint8_t* q, const float* q_scale,
+                           const uint8_t* k_pool, const float* k_scale, const uint8_t* v_pool,
+                           const float* v_scale, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* token_offsets, void* out,
+                           int32_t* status, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  return chunk_call(p, true, q, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens,
+                    token_offsets, out, status, workspace, workspace_bytes, stream);
 }

@@ -153,6 +153,12 @@ __device__ __forceinline__ void cpa4_zfill(void* dst, const void* src, uint32_t 
                "r"(src_bytes)
                : "memory");
 }
+// 16-byte cp.async with the same rule (src_bytes 16 or 0).
+__device__ __forceinline__ void cpa16_zfill(void* dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(src_bytes)
+               : "memory");
+}
 // The barrier receives one arrival (counted in its expected arrivals) once
 // every cp.async this thread issued before has landed.
 __device__ __forceinline__ void cpa_arrive_noinc(uint64_t* bar) {

@@ -91,6 +91,38 @@ int launch_tree_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t 
 // Bytes of one partial-result slot: 256 rows of fp32 O, (m, l) per row, a flag.
 size_t attn_slot_bytes(int head_dim);
 
+struct ChunkArgs {
+  const void* q;              // [total_tokens] rows of Hq x D, q_stride_bytes apart
+  const int32_t* block_table; // [batch][max_blocks_per_seq]
+  const int32_t* seq_lens;    // [batch] cached tokens, the chunk's included
+  const int32_t* token_offsets; // [batch+1]
+  void* out;                  // [total_tokens][Hq][D], bf16 or fp32 (out_fp32)
+  int32_t* status;            // [batch]
+  int32_t* counters;          // [vctas] ticket counters of split units (zeroed per call)
+  uint8_t* slots;             // [2 * vctas] partial-result slots of chunk_slot_bytes(D)
+  size_t q_stride_bytes;
+  int32_t batch, hq, hkv, group, head_dim;
+  int32_t max_blocks_per_seq, num_blocks, max_len, total_tokens;
+  int32_t unit_tokens;        // tokens of a unit: floor(256 / group)
+  int32_t vctas;              // CTAs launched
+  int32_t min_tiles;          // fewest key tiles a CTA is given
+  int32_t window, sinks;      // window 0: every earlier key
+  int32_t out_fp32;
+  int32_t fp8;                // E4M3 codes with one fp32 scale per row
+  float scale_log2;           // softmax scale * log2(e)
+  const float* q_scale;       // [total_tokens][Hq]
+  const float* k_scale;       // [num_blocks][Hkv][16]
+  const float* v_scale;
+};
+
+struct ChunkMaps {
+  CUtensorMap k_pool;   // as AttnMaps
+  CUtensorMap v_pool;
+};
+
+int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream);
+size_t chunk_slot_bytes(int head_dim);
+
 struct CommitArgs {
   const uint16_t* k_nodes;    // [total_nodes][Hkv][D]
   const uint16_t* v_nodes;
