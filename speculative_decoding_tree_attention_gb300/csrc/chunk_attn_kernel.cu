@@ -22,7 +22,7 @@
 // unnormalised O and (m, l) in a workspace slot, and the last piece to take a
 // ticket merges all slots in piece order, so results do not depend on timing.
 //
-// One CTA has 320 threads (384 for an E4M3 cache):
+// One CTA has 384 threads:
 //   warp 8      loads K and V tiles by TMA, one box per 16-token page through
 //               the block table; pages that no row of the unit sees are never
 //               read (an out-of-range page index loads zeros).
@@ -58,17 +58,21 @@ constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;           // issues every MMA; owns the TMEM allocation
 constexpr int kConvWarp = 10;         // E4M3: warps 10-11 convert V tiles to fp16
 constexpr int kConvThreads = 64;
-constexpr int kThreads = 320;
-constexpr int kThreadsF8 = 384;
+constexpr int kThreads = 384;         // three warpgroups
+// Registers a thread after the split (launched with 168): the softmax holds a
+// row of 128 scores.  256 x 208 + 128 x 80 = 63488 <= 384 x 168 = 64512.
+constexpr int kSoftmaxRegs = 208;
+constexpr int kOtherRegs = 80;
 // the running max moves only when a tile exceeds it by 2^8: P stays below
 // 2^8 and the row sum below 2^8 x keys, well inside fp32 (and fp16 for P)
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxPieces = 16;        // pieces per scheduling round
 constexpr int kSclSlots = 8;          // E4M3: scale slots (tile tau in slot tau % 8)
 
-// Named barriers (0 is __syncthreads): softmax group 0 alone, both groups.
+// Named barriers (0 is __syncthreads): softmax group 0 alone, both groups, all.
 constexpr int kBarGroup0 = 1;
 constexpr int kBarPair = 2;
+constexpr int kBarCta = 3;            // every thread, from the roles' own loops
 
 // A piece: the key tiles [t0, t1) of one unit that this CTA computes.
 struct Piece {
@@ -174,6 +178,21 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])
                :
+               : "memory");
+}
+
+// 8 consecutive TMEM columns of this thread's lane, loaded (with the wait) and stored.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
@@ -502,8 +521,8 @@ __global__ void chunk_init_kernel(int32_t* status, int batch, int32_t* counters,
 
 // ---------------------------------------------------------------- the kernel
 template <int D, bool F8>
-__global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
-    chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
   using Ly = Layout<D, F8>;
   using Sl = Slot<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -570,7 +589,6 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
   const uint32_t tmem = misc->tmem_base;
   volatile int* abort_flag = &misc->abort;
   const int g = a.group;
-  Line line;
 
   // Progress kept across pieces and rounds (ring slots and barrier phases):
   // g_tile = K/V tiles of every earlier round; in a role, the tiles and the
@@ -578,14 +596,33 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
   int g_tile = 0;
   int tiles_h0 = 0, tiles_h1 = 0, pieces_h0 = 0, pieces_h1 = 0;
 
-  for (int round = 0;; ++round) {
-    if (warp < kTmaWarp) build_schedule<D, F8>(a, smem, round, tid, &line);
-    __syncthreads();
-    const int npieces = misc->npieces;
-    const bool more = misc->more != 0;
-    if (npieces == 0 || misc->abort) break;
+  // Each role runs the scheduling rounds in a loop of its own (its registers
+  // are its own too).  A round: the softmax warps build the piece list, every
+  // role works through it, and all meet again once the round's copies have
+  // landed and its MMAs are complete.
+  auto rounds = [&](auto&& build, auto&& work) {
+    for (int round = 0;; ++round) {
+      build(round);
+      named_sync(kBarCta, kThreads);
+      const int npieces = misc->npieces;
+      const bool more = misc->more != 0;
+      if (npieces == 0) break;
+      work(round, npieces);
+      tc_fence_before();
+      named_sync(kBarCta, kThreads);
+      tc_fence_after();
+      for (int p = 0; p < npieces; ++p) g_tile += pieces[p].t1 - pieces[p].t0;
+      const bool stop = !more || misc->abort;
+      named_sync(kBarCta, kThreads);  // the piece list is rebuilt next round
+      if (stop) break;
+    }
+  };
+  auto nothing = [](int) {};
 
+  if (warp >= kTmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
+      rounds(nothing, [&](int round, int npieces) {
       // ------------------------------------------------------ TMA producer
       // Lane 0 arms the slot's barrier, then lane u issues the box of page u
       // of the tile.  K runs ahead of V: a K slot is free again once the last
@@ -724,7 +761,9 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
           mbar_wait(&vfull[t % kVStages], (t / kVStages) & 1);
       }
       __syncwarp();
+      });
     } else if (warp == kMmaWarp) {
+      rounds(nothing, [&](int round, int npieces) {
       // ------------------------------------------------------ MMA issuer
       if (lane == 0) {
         // bf16: both products on kind::f16 in bf16.  E4M3: S on kind::f8f6f4
@@ -834,7 +873,10 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         mbar_wait(drain, round & 1);
       }
       __syncwarp();
-    } else if (F8 && warp >= kConvWarp) {
+      });
+      tmem_dealloc(tmem, Ly::kTmemCols);
+    } else {
+      rounds(nothing, [&](int, int npieces) {
       // ------------------------------------------------------ V conversion (E4M3)
       // Per tile: each key's row as fp16 of code x V scale (one rounding of
       // the exact product) into converted slot t % 2, in the MN-major layout
@@ -901,7 +943,12 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         }
         if (!ok) record_status(a.status, pieces[0].b, kDeviceTimeout);
       }
-    } else {
+      });
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    Line line;
+    rounds([&](int round) { build_schedule<D, F8>(a, smem, round, tid, &line); }, [&](int, int npieces) {
       // ------------------------------------------------------ softmax groups
       // Warps 4h .. 4h+3 own m-tile h; warp w's rows are its TMEM lane
       // quarter 32 (w % 4) .. +31.
@@ -917,7 +964,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
       bool ok = true;
       int tau = g_tile;  // global index of the piece's first tile
       for (int p = 0; p < npieces; ++p) {
-        const Piece pc = pieces[p];
+        const Piece& pc = pieces[p];
         const int T = pc.t1 - pc.t0;
         const int nm = pc.rows > BM ? 2 : 1;
         if (h >= nm) {  // this m-tile has no rows in the unit
@@ -1063,14 +1110,13 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
           if (__any_sync(0xffffffffu, rescale)) {
             // O holds P(..t-1) V against the old max; P_h(t-1) V is complete
             // (S_h(t), which this thread has seen complete, was issued after it)
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 8) {
+              uint32_t o[8];  // few at a time: the 128 scores are live
+              tmem_ld8(tmem_o + c0, o);
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(tmem_o + c0, o);
-              tmem_ld_wait32(o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st32(tmem_o + c0, o);
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st8(tmem_o + c0, o);
             }
             l_run *= alpha;  // (this tile's sum is added below, against the new max)
           }
@@ -1185,17 +1231,8 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         tiles_h0 = my_tiles;
         pieces_h0 = my_pieces;
       }
-    }
-    // every role has finished the round's pieces (the TMA copies have
-    // landed, the MMAs are complete)
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    for (int p = 0; p < npieces; ++p) g_tile += pieces[p].t1 - pieces[p].t0;
-    __syncthreads();  // the piece list is rebuilt next round
-    if (!more || misc->abort) break;
+    });
   }
-  if (warp == kMmaWarp) tmem_dealloc(tmem, Ly::kTmemCols);
 }
 
 template <int D, bool F8>
@@ -1214,7 +1251,7 @@ int launch(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.vctas, 1, 1);
-  cfg.blockDim = dim3(F8 ? kThreadsF8 : kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Layout<D, F8>::kAlloc;
   cfg.stream = stream;
   cfg.attrs = &attr;
