@@ -22,19 +22,27 @@
 // unnormalised O and (m, l) in a workspace slot, and the last piece to take a
 // ticket merges all slots in piece order, so results do not depend on timing.
 //
-// One CTA has 384 threads:
+// One CTA has 384 threads (512 for an E4M3 cache):
 //   warp 8      loads K and V tiles by TMA, one box per 16-token page through
 //               the block table; pages that no row of the unit sees are never
 //               read (an out-of-range page index loads zeros).
-//   warp 9      issues tcgen05.mma for both m-tiles h: S_h = Q_h K^T into
-//               TMEM, O_h += P_h V with P_h from TMEM.  P_h lies over S_h.
+//   warps 9, 10 issue the tcgen05.mma of m-tile h = 0 and 1: S_h = Q_h K^T
+//               into TMEM, O_h += P_h V with P_h from TMEM.  P_h lies over S_h;
+//               the MMAs of one thread run in order, so S_h(t+1) follows
+//               P_h(t) V.  The two take turns, P_0 V(t), S_0(t+1), P_1 V(t),
+//               S_1(t+1): the softmax of one m-tile runs under the MMAs of the
+//               other.  Two threads, because a wait that is over already still
+//               costs 100 to 200 clocks and a tile has five of them: the thread
+//               whose turn is next has done its own before the turn comes.
+//               (Without turns the two fall into step, both softmaxes and then
+//               both MMAs: period 4540 clocks a tile pair.)
 //   warps 0-7   softmax of m-tile 0 and 1, one thread per row.  P is handed
 //               over in halves (64 keys), so that the first four P V steps run
 //               under the exponentials of the second half, and the row sum is
 //               taken after the hand-over, under the MMAs: what stays on the
 //               chain S -> P -> S of an m-tile is the TMEM load, the row max
 //               and the exponentials.
-//   warps 10-11 (E4M3) convert V tiles to fp16 with their row scales.
+//   warps 12-15 (E4M3) convert V tiles to fp16 with their row scales.
 // TMEM (512 columns): S_0/P_0 at 0, S_1/P_1 at 128, O_0 at 256, O_1 at 256 + D.
 // Every wait on an mbarrier is bounded; on expiry the CTA reports
 // TV_ERR_DEVICE_TIMEOUT for its sequence, drains its copies and returns.
@@ -55,14 +63,19 @@ constexpr int BN = 128;               // keys per tile
 constexpr int kUnitRows = 2 * BM;
 constexpr int kSoftmaxThreads = 256;  // warps 0-7: two groups of four warps
 constexpr int kTmaWarp = 8;
-constexpr int kMmaWarp = 9;           // issues every MMA; owns the TMEM allocation
-constexpr int kConvWarp = 10;         // E4M3: warps 10-11 convert V tiles to fp16
-constexpr int kConvThreads = 64;
-constexpr int kThreads = 384;         // three warpgroups
-// Registers a thread after the split (launched with 168): the softmax holds a
-// row of 128 scores.  256 x 208 + 128 x 80 = 63488 <= 384 x 168 = 64512.
-constexpr int kSoftmaxRegs = 208;
-constexpr int kOtherRegs = 80;
+constexpr int kMmaWarp = 9;           // warps 9, 10 issue the MMAs of m-tile 0, 1
+constexpr int kConvWarp = 12;         // E4M3: warps 12-15 convert V tiles to fp16
+constexpr int kConvThreads = 128;
+// Threads, and registers a thread after the split: the softmax holds a row of
+// 128 scores.  bf16: three warpgroups launched with 168 registers, 256 x 208 +
+// 128 x 80 = 63488 <= 384 x 168.  E4M3: four launched with 128, 256 x 184 +
+// 256 x 72 = 65536 = 512 x 128.
+template <bool F8>
+struct Shares {
+  static constexpr int kThreads = F8 ? 512 : 384;
+  static constexpr int kSoftmaxRegs = F8 ? 184 : 208;
+  static constexpr int kOtherRegs = F8 ? 72 : 80;
+};
 // the running max moves only when a tile exceeds it by 2^8: P stays below
 // 2^8 and the row sum below 2^8 x keys, well inside fp32 (and fp16 for P)
 constexpr float kRescaleLog2 = 8.0f;
@@ -117,8 +130,8 @@ struct Layout {
   static constexpr int kBlkBytes = 8 * 8 * 4;
   static constexpr int kBar = kBlk + kBlkBytes;
   // kfull, kempty [S], vfull, vempty [VS], s_full, p_a, p_b, o_done, q_full
-  // [2], drain, v16full, v16empty [2], sfull [8]
-  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11 + (F8 ? 4 + kSclSlots : 0);
+  // [2], drain [2], turn [2], v16full, v16empty [2], sfull [8]
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 14 + (F8 ? 4 + kSclSlots : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kMiscBytes = 160;
   static constexpr int kTotal = kMisc + kMiscBytes;
@@ -464,48 +477,69 @@ __device__ __forceinline__ void store_row_chunk(const ChunkArgs& a, size_t row, 
 }
 
 // Merges the pieces of a split unit: O = sum_s 2^(m_s - M) O_s /
-// sum_s 2^(m_s - M) l_s in piece order.  The (row, 4 columns) items of the
-// unit are spread over the nthr participants, rows fastest: a unit of 8 decode
-// rows split 20 ways still has 256 independent items, and a warp's loads are
-// consecutive.
+// sum_s 2^(m_s - M) l_s in piece order.  A thread keeps one row and takes every
+// `step`-th group of 4 columns of it, rows fastest across the threads (a
+// warp's loads are consecutive), 8 groups at a time with all their loads in
+// flight: a unit of 256 rows has a thread per row, one of 8 decode rows split
+// 20 ways has 16 threads per row.
 template <int D>
 __device__ void merge_unit(const ChunkArgs& a, const Piece& pc, int ur, int nthr) {
   using Sl = Slot<D>;
+  constexpr int kG = 8;
+  const int step = nthr / pc.rows;
+  const int row = ur % pc.rows, sub = ur / pc.rows;
+  if (sub >= step) return;
   const uint8_t* first = a.slots + static_cast<size_t>(2 * pc.vfirst + 1) * Sl::kBytes;
   auto base = [&](int s) {
     return s == 0 ? first : a.slots + static_cast<size_t>(2 * (pc.vfirst + s)) * Sl::kBytes;
   };
   int bad = 0;
-#pragma unroll 4
-  for (int s = 0; s < pc.npieces; ++s) bad |= __ldcg(reinterpret_cast<const int*>(base(s) + Sl::kFlag));
-  for (int it = ur; it < pc.rows * (D / 4); it += nthr) {
-    const int row = it % pc.rows, d4 = it / pc.rows;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int s = 0; s < pc.npieces; ++s)
-      M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row).x);
+  float M = -INFINITY;
+#pragma unroll 8
+  for (int s = 0; s < pc.npieces; ++s) {
+    bad |= __ldcg(reinterpret_cast<const int*>(base(s) + Sl::kFlag));
+    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row).x);
+  }
+  const size_t out_row = static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group;
+#pragma unroll 1
+  for (int d0 = sub; d0 < D / 4; d0 += kG * step) {
     float l = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+    float4 acc[kG];
+#pragma unroll
+    for (int k = 0; k < kG; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
     for (int s = 0; s < pc.npieces; ++s) {
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(base(s) + Sl::kO) + it);
+      float4 o[kG];
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        const int d4 = d0 + k * step;
+        o[k] = d4 < D / 4 ? __ldcg(reinterpret_cast<const float4*>(base(s) + Sl::kO) + d4 * pc.rows + row)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
       const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
       l += w * ml.y;
-      acc.x += w * o.x;
-      acc.y += w * o.y;
-      acc.z += w * o.z;
-      acc.w += w * o.w;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        acc[k].x += w * o[k].x;
+        acc[k].y += w * o[k].y;
+        acc[k].z += w * o[k].z;
+        acc[k].w += w * o[k].w;
+      }
     }
-    const float inv = (l > 0.0f && !bad) ? 1.0f / l : 0.0f;
-    if (bad) acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const size_t out_row = static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group;
-    if (a.out_fp32) {
-      reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D)[d4] =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    } else {
-      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D)[d4] =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      const int d4 = d0 + k * step;
+      if (d4 >= D / 4) break;
+      const float4 v = bad ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                           : make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+      if (a.out_fp32) {
+        reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D)[d4] = v;
+      } else {
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D)[d4] =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      }
     }
   }
 }
@@ -521,7 +555,7 @@ __global__ void chunk_init_kernel(int32_t* status, int batch, int32_t* counters,
 
 // ---------------------------------------------------------------- the kernel
 template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
   using Ly = Layout<D, F8>;
   using Sl = Slot<D>;
@@ -539,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_b = p_a + 2;                // [2]: P_h(t) of keys 64 .. 127
   uint64_t* o_done = p_b + 2;             // [2]: the last P_h V of a piece complete
   uint64_t* q_full = o_done + 2;          // [2]: Q_h of a piece in shared memory (128 arrivals)
-  uint64_t* drain = q_full + 2;           // every MMA issued so far complete (once per round)
-  uint64_t* v16full = drain + 1;          // F8 [2]: V(t) converted (64 arrivals)
+  uint64_t* drain = q_full + 2;           // [2]: every MMA of m-tile h so far complete (once per round)
+  uint64_t* turn = drain + 2;             // [2]: m-tile h may issue (units with both)
+  uint64_t* v16full = turn + 2;           // F8 [2]: V(t) converted (128 arrivals)
   uint64_t* v16empty = v16full + 2;       // F8 [2]: the P V of tile t complete
   uint64_t* sfull = v16empty + 2;         // F8 [8]: the scales of tile t landed (32 arrivals)
   Misc* misc = reinterpret_cast<Misc*>(smem + Ly::kMisc);
@@ -555,16 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc->zero_needed = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], 2);  // one arrival per m-tile
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], F8 ? kConvThreads : 1);
+      mbar_init(&vempty[s], F8 ? kConvThreads : 2);
     }
     if constexpr (F8) {
       for (int k = 0; k < 2; ++k) {
         mbar_init(&v16full[k], kConvThreads);
-        mbar_init(&v16empty[k], 1);
+        mbar_init(&v16empty[k], 2);
       }
       for (int k = 0; k < kSclSlots; ++k) mbar_init(&sfull[k], 32);
     }
@@ -574,8 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_b[h], BM);
       mbar_init(&o_done[h], 1);
       mbar_init(&q_full[h], BM);
+      mbar_init(&drain[h], 1);
+      mbar_init(&turn[h], 1);
     }
-    mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -591,10 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = a.group;
 
   // Progress kept across pieces and rounds (ring slots and barrier phases):
-  // g_tile = K/V tiles of every earlier round; in a role, the tiles and the
-  // pieces of m-tile h so far (MMA: both m-tiles; softmax: its own).
-  int g_tile = 0;
-  int tiles_h0 = 0, tiles_h1 = 0, pieces_h0 = 0, pieces_h1 = 0;
+  // g_tile = K/V tiles of every earlier round; my_tiles and my_pieces = the
+  // tiles and pieces of this role's m-tile so far (MMA and softmax).
+  int g_tile = 0, my_tiles = 0, my_pieces = 0, my_turns = 0;
 
   // Each role runs the scheduling rounds in a loop of its own (its registers
   // are its own too).  A round: the softmax warps build the piece list, every
@@ -603,24 +638,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto rounds = [&](auto&& build, auto&& work) {
     for (int round = 0;; ++round) {
       build(round);
-      named_sync(kBarCta, kThreads);
+      named_sync(kBarCta, Shares<F8>::kThreads);
       const int npieces = misc->npieces;
       const bool more = misc->more != 0;
       if (npieces == 0) break;
       work(round, npieces);
       tc_fence_before();
-      named_sync(kBarCta, kThreads);
+      named_sync(kBarCta, Shares<F8>::kThreads);
       tc_fence_after();
       for (int p = 0; p < npieces; ++p) g_tile += pieces[p].t1 - pieces[p].t0;
       const bool stop = !more || misc->abort;
-      named_sync(kBarCta, kThreads);  // the piece list is rebuilt next round
+      named_sync(kBarCta, Shares<F8>::kThreads);  // the piece list is rebuilt next round
       if (stop) break;
     }
   };
   auto nothing = [](int) {};
 
   if (warp >= kTmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shares<F8>::kOtherRegs));
     if (warp == kTmaWarp) {
       rounds(nothing, [&](int round, int npieces) {
       // ------------------------------------------------------ TMA producer
@@ -762,10 +797,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       });
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       rounds(nothing, [&](int round, int npieces) {
-      // ------------------------------------------------------ MMA issuer
+      // ------------------------------------------------------ MMA issuer of m-tile h
       if (lane == 0) {
+        const int h = warp - kMmaWarp;
         // bf16: both products on kind::f16 in bf16.  E4M3: S on kind::f8f6f4
         // over the codes, P V on kind::f16 in fp16.
         constexpr uint32_t idesc_s = F8 ? idesc_e4m3(BM, BN) : idesc_bf16(BM, BN, 0);
@@ -776,92 +812,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kKRow8 = F8 ? 1024 : Ly::kGroupBytes;
         const uint64_t dk0 = smem_desc(smem_u32(smem + Ly::kKRing), 16, kKRow8);
         const uint64_t dv0 = smem_desc(smem_u32(smem + (F8 ? Ly::kV16 : Ly::kVRing)), 1024, Ly::kGroupBytes);
-        const uint64_t dq0 = smem_desc(smem_u32(smem + Ly::kQ), 16, kKRow8);
-        auto issue_s = [&](int h, int t) {  // S_h = Q_h K(t)^T into columns 128 h
+        const uint64_t dq = smem_desc(smem_u32(smem + Ly::kQ + h * Ly::kQBytes), 16, kKRow8);
+        const uint32_t tmem_s = tmem + h * BN, tmem_o = tmem + 256 + h * D;
+        uint64_t* vready = F8 ? v16full : vfull;  // V(t) as the P V reads it, and its release
+        uint64_t* vdone = F8 ? v16empty : vempty;
+        constexpr int kVSlots = F8 ? 2 : kVStages;
+        auto k_wait = [&](int t) { return mbar_wait(&kfull[t % kStages], (t / kStages) & 1, abort_flag); };
+        auto v_wait = [&](int t) { return mbar_wait(&vready[t % kVSlots], (t / kVSlots) & 1, abort_flag); };
+        auto issue_s = [&](int t) {  // S_h = Q_h K(t)^T
           const uint64_t dk = dk0 + static_cast<uint64_t>((t % kStages) * (Ly::kKTileBytes >> 4));
-          const uint64_t dq = dq0 + static_cast<uint64_t>(h * (Ly::kQBytes >> 4));
           if constexpr (F8) {
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row per MMA
-              mma_f8_ss(tmem + h * BN, dq + kk * 2, dk + kk * 2, idesc_s, kk > 0 ? 1u : 0u);
+              mma_f8_ss(tmem_s, dq + kk * 2, dk + kk * 2, idesc_s, kk > 0 ? 1u : 0u);
           } else {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-              mma_bf16_ss(tmem + h * BN, dq + off, dk + off, idesc_s, kk > 0 ? 1u : 0u);
+              mma_bf16_ss(tmem_s, dq + off, dk + off, idesc_s, kk > 0 ? 1u : 0u);
             }
           }
           mma_commit(&s_full[h]);
         };
         // O_h (+)= P_h V(t) over keys 64 half .. 64 half + 63
-        auto issue_pv = [&](int h, int t, int half, bool acc) {
-          const uint64_t dv = dv0 + static_cast<uint64_t>((F8 ? (t & 1) : (t % kVStages)) * (Ly::kTileBytes >> 4));
+        auto issue_pv = [&](int t, int half, bool acc) {
+          const uint64_t dv = dv0 + static_cast<uint64_t>((t % kVSlots) * (Ly::kTileBytes >> 4));
 #pragma unroll
           for (int k = 0; k < BN / 32; ++k) {
             const int kk = half * (BN / 32) + k;
-            mma_bf16_ts(tmem + 256 + h * D, tmem + h * BN + kk * 8,
-                        dv + ((kk * 2 * Ly::kGroupBytes) >> 4), idesc_o, (acc || k > 0) ? 1u : 0u);
+            mma_bf16_ts(tmem_o, tmem_s + kk * 8, dv + ((kk * 2 * Ly::kGroupBytes) >> 4), idesc_o,
+                        (acc || k > 0) ? 1u : 0u);
           }
+        };
+        // turns are taken in units with both m-tiles, m-tile 0 first
+        auto turn_wait = [&]() {
+          const int n = my_turns - (h == 0 ? 1 : 0);
+          return n < 0 || mbar_wait(&turn[h], n & 1, abort_flag);
+        };
+        auto turn_pass = [&]() {
+          mbar_arrive(&turn[h ^ 1]);
+          ++my_turns;
         };
         bool ok = true;
         int tau = g_tile;
         for (int p = 0; p < npieces && ok; ++p) {
           const int nm = pieces[p].rows > BM ? 2 : 1, T = pieces[p].t1 - pieces[p].t0;
-          // the piece's first S of each m-tile, once its Q is loaded and K has landed
-          for (int h = 0; h < nm && ok; ++h) {
-            ok = mbar_wait(&q_full[h], (h ? pieces_h1 : pieces_h0) & 1, abort_flag);
-            if (ok && h == 0) ok = mbar_wait(&kfull[tau % kStages], (tau / kStages) & 1, abort_flag);
+          if (h >= nm) {
+            // no rows of this m-tile: its arrivals keep the rings turning
+            for (int t = tau; t < tau + T && ok; ++t) {
+              ok = k_wait(t);
+              if (ok) mbar_arrive(&kempty[t % kStages]);
+              ok = ok && v_wait(t);
+              if (ok) mbar_arrive(&vdone[t % kVSlots]);
+            }
+            tau += T;
+            continue;
+          }
+          // the piece's first S, once its Q is loaded and K has landed
+          ok = mbar_wait(&q_full[h], my_pieces & 1, abort_flag) && k_wait(tau);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(tau);
+          mma_commit(&kempty[tau % kStages]);
+          for (int i = 0; i < T; ++i) {
+            const int t = tau + i;
+            const bool next = i + 1 < T;
+            // everything but the second half of P before the turn
+            ok = v_wait(t) && (!next || k_wait(t + 1)) && mbar_wait(&p_a[h], my_tiles & 1, abort_flag) &&
+                 (nm == 1 || turn_wait());
             if (!ok) break;
             tc_fence_after();
-            issue_s(h, tau);
-          }
-          if (!ok) break;
-          mma_commit(&kempty[tau % kStages]);
-          for (int i = 0; i < T && ok; ++i) {
-            const int t = tau + i;
-            for (int h = 0; h < nm; ++h) {
-              const int ph = (h ? tiles_h1 : tiles_h0) & 1;
-              ok = mbar_wait(&p_a[h], ph, abort_flag);
-              if (ok && h == 0) {
-                if constexpr (F8) {
-                  ok = mbar_wait(&v16full[t & 1], (t >> 1) & 1, abort_flag);  // V(t) in fp16
-                } else {
-                  ok = mbar_wait(&vfull[t % kVStages], (t / kVStages) & 1, abort_flag);
-                }
-              }
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(h, t, 0, i > 0);
-              ok = mbar_wait(&p_b[h], ph, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(h, t, 1, true);
-              if (i + 1 < T) {
-                if (h == 0) {
-                  ok = mbar_wait(&kfull[(t + 1) % kStages], ((t + 1) / kStages) & 1, abort_flag);
-                  if (!ok) break;
-                  tc_fence_after();
-                }
-                issue_s(h, t + 1);
-              }
-              if (h) ++tiles_h1; else ++tiles_h0;
-            }
+            issue_pv(t, 0, i > 0);
+            ok = mbar_wait(&p_b[h], my_tiles & 1, abort_flag);
             if (!ok) break;
-            // the V slot (F8: the converted slot) and the K slot are free
-            if constexpr (F8) {
-              mma_commit(&v16empty[t & 1]);
-            } else {
-              mma_commit(&vempty[t % kVStages]);
-            }
-            if (i + 1 < T) mma_commit(&kempty[(t + 1) % kStages]);
+            tc_fence_after();
+            issue_pv(t, 1, true);
+            if (next) issue_s(t + 1);
+            if (nm == 2) turn_pass();
+            ++my_tiles;
+            mma_commit(&vdone[t % kVSlots]);
+            if (next) mma_commit(&kempty[(t + 1) % kStages]);
           }
           if (!ok) break;
-          mma_commit(&o_done[0]);
-          ++pieces_h0;
-          if (nm == 2) {
-            mma_commit(&o_done[1]);
-            ++pieces_h1;
-          }
+          mma_commit(&o_done[h]);
+          ++my_pieces;
           tau += T;
         }
         if (!ok) {
@@ -869,12 +903,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           misc->abort = 1;
         }
         // every MMA issued so far completes before the next round or the exit
-        mma_commit(drain);
-        mbar_wait(drain, round & 1);
+        mma_commit(&drain[h]);
+        mbar_wait(&drain[h], round & 1);
       }
       __syncwarp();
       });
-      tmem_dealloc(tmem, Ly::kTmemCols);
+      if (warp == kMmaWarp) tmem_dealloc(tmem, Ly::kTmemCols);
     } else {
       rounds(nothing, [&](int, int npieces) {
       // ------------------------------------------------------ V conversion (E4M3)
@@ -882,8 +916,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the exact product) into converted slot t % 2, in the MN-major layout
       // the P V MMA reads.  Keys that no row of the unit sees get zero rows
       // (their codes may be stale).
-      if constexpr (F8) {
-        const int ct = tid - kConvWarp * 32;  // 0 .. 63
+      if (F8 && warp >= kConvWarp) {
+        const int ct = tid - kConvWarp * 32;  // 0 .. 127
         const float* scl = reinterpret_cast<const float*>(smem + Ly::kScl);
         bool ok = true;
         int tau = g_tile;
@@ -899,17 +933,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               const float* sv = scl + (tau % kSclSlots) * 2 * BN + BN;
               // thread ct: the 16 codes of columns 16c .. 16c+15 (c = ct % 8)
-              // of keys k0 + 8i, k0 = ct / 8, i = 0 .. 15.  Raw: 128 bytes a
-              // key, 16-byte chunk c at chunk c ^ (key % 8); fp16: [8-key
-              // group][64-column half][key][128 B], 16-byte chunk q of a
+              // of keys k0 + 8i, k0 = (ct / 8) % 8, i = 8 (ct / 64) .. + 7.  Raw:
+              // 128 bytes a key, 16-byte chunk c at chunk c ^ (key % 8); fp16:
+              // [8-key group][64-column half][key][128 B], 16-byte chunk q of a
               // line at chunk q ^ (key % 8).  key % 8 = k0 for every i.
-              const int k0 = ct >> 3, c = ct & 7;
+              const int k0 = (ct >> 3) & 7, c = ct & 7, i0 = (ct >> 6) * 8;
               const int key0 = (t < pc.st ? t : t + pc.skip) * BN + k0;
               const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + k0 * 128 + ((c ^ k0) << 4);
               uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (c >> 2) * 1024 + k0 * 128;
               const int q0 = (((2 * c) & 7) ^ k0) << 4, q1 = (((2 * c + 1) & 7) ^ k0) << 4;
 #pragma unroll 1
-              for (int i = 0; i < 16; ++i) {
+              for (int i = i0; i < i0 + 8; ++i) {
                 const int key = key0 + 8 * i;
                 uint32_t h[8];
                 if (key <= pc.hi && (key < a.sinks || key >= pc.lo)) {
@@ -946,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       });
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shares<F8>::kSoftmaxRegs));
     Line line;
     rounds([&](int round) { build_schedule<D, F8>(a, smem, round, tid, &line); }, [&](int, int npieces) {
       // ------------------------------------------------------ softmax groups
@@ -959,8 +993,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tmem_o = tmem + 256 + h * D + lane_off;
       uint8_t* qh = smem + Ly::kQ + h * Ly::kQBytes;
       volatile int* piece_bad = misc->piece_bad;
-      int my_tiles = h ? tiles_h1 : tiles_h0;
-      int my_pieces = h ? pieces_h1 : pieces_h0;
       bool ok = true;
       int tau = g_tile;  // global index of the piece's first tile
       for (int p = 0; p < npieces; ++p) {
@@ -1016,10 +1048,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         float m_run = -INFINITY;  // running max (log2 units)
         float l_run = 0.0f;       // row sum against m_run
+        const int t0 = pc.t0, st = pc.st, skip = pc.skip, lo = pc.lo, hi = pc.hi, pos0 = pc.pos0;
         for (int i = 0; i < T; ++i) {
-          const int t = pc.t0 + i;                                 // tile of the unit
-          const int k0 = (t < pc.st ? t : t + pc.skip) * BN;       // its first key
-          const int gt = tau + i;                                  // global tile (ring slot)
+          const int k0 = (t0 + i < st ? t0 + i : t0 + i + skip) * BN;  // first key of the tile
+          const int gt = tau + i;                                      // global tile (ring slot)
+          // some row of the unit does not see some key of the tile
+          const bool masked = k0 + BN - 1 > pos0 || (a.window > 0 && hi - a.window >= k0 && k0 + BN > a.sinks);
+          // keys that no row of the unit sees: their V rows are cleared
+          // (stale data; P is 0 there but 0 * NaN would poison O), a row per
+          // thread, by each group before its own P_h(t) V(t).
+          if constexpr (!F8) {
+            if (ok && (k0 + BN - 1 > hi || (lo > k0 && k0 + BN > a.sinks))) {
+              const int vs = gt % kVStages;
+              mbar_wait(&vfull[vs], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
+              const int key = k0 + r;
+              if (!(key <= hi && (key < a.sinks || key >= lo))) {
+                uint8_t* row = smem + Ly::kVRing + vs * Ly::kTileBytes + (r >> 3) * Ly::kGroupBytes + (r & 7) * 128;
+#pragma unroll
+                for (int k = 0; k < 8 * Ly::kHalves; ++k)
+                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();  // generic writes, read by the MMA
+            }
+          }
           if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[h], my_tiles & 1, abort_flag));
             if constexpr (F8) {  // the keys' K scales (landed with the K tile)
@@ -1033,37 +1084,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&p_b[h]);
             continue;
           }
-          // some row of the unit does not see some key of the tile
-          const bool masked = k0 + BN - 1 > pc.pos0 ||
-                              (a.window > 0 && pc.hi - a.window >= k0 && k0 + BN > a.sinks);
-          // keys that no row of the unit sees: their V rows are cleared
-          // (stale data; P is 0 there but 0 * NaN would poison O).  Group 0
-          // does it, a row per thread, before P_0(t) V(t), the first reader.
-          if constexpr (!F8) {
-            if (h == 0 && (k0 + BN - 1 > pc.hi || (pc.lo > k0 && k0 + BN > a.sinks))) {
-              const int st = gt % kVStages;
-              mbar_wait(&vfull[st], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
-              const int key = k0 + r;
-              if (!(key <= pc.hi && (key < a.sinks || key >= pc.lo))) {
-                uint8_t* row = smem + Ly::kVRing + st * Ly::kTileBytes + (r >> 3) * Ly::kGroupBytes + (r & 7) * 128;
-#pragma unroll
-                for (int k = 0; k < 8 * Ly::kHalves; ++k)
-                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();  // generic writes, read by the MMA
-            }
-          }
-          // the scores, 32 columns at a time: the next load is in flight
-          // while the max of the last 32 is taken.  They stay unscaled; the
-          // softmax scale is folded into the exponent.
+          // the scores stay unscaled; the softmax scale is folded into the exponent
           float x[128];
           float mx[4];
           tc_fence_after();
-          tmem_ld32(tmem_s, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tmem_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
-            if (c < 3) tmem_ld32(tmem_s + 32 * (c + 1), *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c + 32]));
             float* y = x + 32 * c;
             if constexpr (F8) {
               const float* sk = reinterpret_cast<const float*>(smem + Ly::kScl) + (gt % kSclSlots) * 2 * BN + 32 * c;
@@ -1096,22 +1125,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[c] = fmax3(u[0], u[1], fmaxf(u[2], u[3]));
           }
           const float smax = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cq;
-          float alpha = 1.0f;
-          bool rescale = false;
-          if (smax != -INFINITY) {
-            if (m_run == -INFINITY) {
-              m_run = smax;
-            } else if (smax > m_run + kRescaleLog2) {
-              alpha = exp2f(m_run - smax);
-              m_run = smax;
-              rescale = true;
-            }
-          }
-          if (__any_sync(0xffffffffu, rescale)) {
+          const bool up = smax > m_run + kRescaleLog2;  // (the first visible score too)
+          if (__any_sync(0xffffffffu, up)) {
+            const float alpha = up ? exp2f(m_run - smax) : 1.0f;
+            if (up) m_run = smax;
             // O holds P(..t-1) V against the old max; P_h(t-1) V is complete
             // (S_h(t), which this thread has seen complete, was issued after it)
+            // (the piece's first P V overwrites O)
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 8) {
+            for (int c0 = 0; i > 0 && c0 < D; c0 += 8) {
               uint32_t o[8];  // few at a time: the 128 scores are live
               tmem_ld8(tmem_o + c0, o);
 #pragma unroll
@@ -1224,13 +1246,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         tau += T;
       }
-      if (h) {
-        tiles_h1 = my_tiles;
-        pieces_h1 = my_pieces;
-      } else {
-        tiles_h0 = my_tiles;
-        pieces_h0 = my_pieces;
-      }
     });
   }
 }
@@ -1251,7 +1266,7 @@ int launch(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.vctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(Shares<F8>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Layout<D, F8>::kAlloc;
   cfg.stream = stream;
   cfg.attrs = &attr;
