@@ -97,14 +97,12 @@ struct Piece {
   int t0, t1;
   int rows;         // packed rows of the unit (1 .. 256)
   int slot;         // partial-result slot, -1 when the piece is the whole unit
-  int cnt;          // ticket counter of a split unit
   int npieces;      // pieces of a split unit
-  int vfirst;       // CTA of the unit's first piece
-  int pad;
+  int vfirst;       // CTA of the unit's first piece (its ticket counter)
+  int pad[2];
 };
 
-// Shared memory of one CTA.  bf16: K and V tiles of 128 keys x D in rings of
-// 2 and 3 (the P V of a tile runs a period after its S, so V waits longer).
+// Shared memory of one CTA.  bf16: K and V tiles of 128 keys x D in rings.
 // E4M3 (D = 128): K and raw V tiles of one-byte codes in rings of 3, two
 // converted fp16 V tiles, and 8 slots of per-key scales (K, V).
 template <int D, bool F8>
@@ -116,9 +114,10 @@ struct Layout {
   static constexpr int kGroupBytes = kHalves * 1024;   // 8 rows of a 16-bit tile
   static constexpr int kTileBytes = BN * D * 2;
   static constexpr int kKTileBytes = F8 ? BN * D : kTileBytes;  // a K or raw V tile as loaded
-  static constexpr int kQBytes = F8 ? BM * D : BM * D * 2;
-  static constexpr int kQ = 0;                         // Q_0, Q_1
-  static constexpr int kKRing = kQ + 2 * kQBytes;
+  static constexpr int kQLines = F8 ? 1 : kHalves;     // 128-byte lines of a Q row
+  static constexpr int kQLineBytes = kUnitRows * 128;  // Q: [line][256 rows][128 B]
+  static constexpr int kQ = 0;
+  static constexpr int kKRing = kQ + kQLines * kQLineBytes;
   static constexpr int kVRing = kKRing + kStages * kKTileBytes;
   static constexpr int kV16 = kVRing + kVStages * kKTileBytes;
   static constexpr int kV16Bytes = F8 ? 2 * kTileBytes : 0;
@@ -129,8 +128,8 @@ struct Layout {
   static constexpr int kBlk = kPieces + kPiecesBytes;  // block ids of the last 8 K tiles
   static constexpr int kBlkBytes = 8 * 8 * 4;
   static constexpr int kBar = kBlk + kBlkBytes;
-  // kfull, kempty [S], vfull, vempty [VS], s_full, p_a, p_b, o_done, q_full
-  // [2], drain [2], turn [2], v16full, v16empty [2], sfull [8]
+  // kfull, kempty [S], vfull, vempty [VS], s_full, p_a, p_b, o_done, drain,
+  // turn [2], q_full, q_empty, v16full, v16empty [2], sfull [8]
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 14 + (F8 ? 4 + kSclSlots : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kMiscBytes = 160;
@@ -140,7 +139,7 @@ struct Layout {
   // written only after the piece list is built
   static constexpr int kSeq = kQ;                      // [4][256] ints, then 8 warp sums
   static constexpr int kTmemCols = 512;
-  static_assert(4 * 256 * 4 + 32 <= 2 * kQBytes, "schedule scratch fits over Q");
+  static_assert(4 * 256 * 4 + 32 <= kQLines * kQLineBytes, "schedule scratch fits over Q");
   static_assert(kAlloc <= 232448, "shared memory per CTA");
 };
 
@@ -194,19 +193,17 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// 8 consecutive TMEM columns of this thread's lane, loaded (with the wait) and stored.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+// 16 consecutive TMEM columns of this thread's lane, with the wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 
 // Bits 0 .. n-1 of a 32-bit word (none for n <= 0, all for n >= 32).
@@ -257,7 +254,7 @@ __device__ __forceinline__ SeqInfo seq_info(const ChunkArgs& a, int b) {
 }
 
 // Exclusive scan over the 256 softmax threads; *total = the sum.
-__device__ __forceinline__ int scan256(int v, int* scratch, int sid, int* total) {
+__device__ __noinline__ int scan256(int v, int* scratch, int sid, int* total) {
   const int lane = sid & 31, w = sid >> 5;
   int x = v;
 #pragma unroll
@@ -344,106 +341,102 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
     loaded = base;
     named_sync(kBarPair, kSoftmaxThreads);
   };
-  // unit j of the loaded chunk: its sequence (the last whose first unit is
-  // <= j: sequences without units share the next one's) and its extent
-  auto locate = [&](int j, int& i, int& u) {
-    i = 0;
-#pragma unroll
-    for (int step = 128; step > 0; step >>= 1)
-      if (seq_u[i + step] <= j) i += step;
-    u = j - seq_u[i];
-    return unit_of(a, seq_ctx[i], seq_c[i], u);
-  };
-
-  // a chunk with at most 256 units is located once for both passes
+  // Pass 0 (round 0 only) adds the line up, pass 1 emits the pieces.  One copy
+  // of the code serves both: run once, it costs its instructions' way from L2.
+  // A batch with at most 256 units is located once.
+  const int v = static_cast<int>(blockIdx.x);
   Unit x;
-  int xi = 0, xu = 0, xbase = -1;
-  if (round == 0) {
-    int W = 0;
-    for (int base = 0; base < a.batch; base += kSoftmaxThreads) {
+  int xi = 0, xu = 0;
+  bool kept = false;
+  int count = 0;  // pieces of this CTA so far (all rounds)
+#pragma unroll 1
+  for (int pass = round == 0 ? 0 : 1; pass < 2; ++pass) {
+    int s_v = 0, e_v = INT_MAX;
+    if (pass == 1) {
+      s_v = v < line->V ? line->start(v) : 0;
+      e_v = v < line->V ? line->start(v + 1) : 0;
+    }
+    int cum = 0;  // line position of the next group of units
+#pragma unroll 1
+    for (int base = 0; base < a.batch && cum < e_v; base += kSoftmaxThreads) {
       load_chunk(base);
-      for (int ub = 0; ub < units; ub += kSoftmaxThreads) {
-        int T = 0, tot;
-        if (ub + sid < units) {
-          x = locate(ub + sid, xi, xu);
-          T = x.T;
+#pragma unroll 1
+      for (int ub = 0; ub < units && cum < e_v; ub += kSoftmaxThreads) {
+        const bool have = ub + sid < units;
+        if (have && !kept) {
+          // unit j of the chunk: its sequence (the last whose first unit is
+          // <= j: sequences without units share the next one's), its extent
+          const int j = ub + sid;
+          xi = 0;
+#pragma unroll 1
+          for (int step = 128; step > 0; step >>= 1)
+            if (seq_u[xi + step] <= j) xi += step;
+          xu = j - seq_u[xi];
+          x = unit_of(a, seq_ctx[xi], seq_c[xi], xu);
         }
-        xbase = base + ub;
-        scan256(T, scratch, sid, &tot);
-        W += tot * a.hkv;
+        const int len = have ? x.T * a.hkv : 0;
+        int tot;
+        const int c0 = cum + scan256(len, scratch, sid, &tot);
+        cum += tot;
+        if (pass == 0) continue;
+        // KV heads [h0, h1) of this unit meet [s_v, e_v)
+        int h0 = 0, h1 = 0;
+        if (have && c0 < e_v && c0 + len > s_v) {
+          h0 = max(0, s_v - c0) / x.T;
+          h1 = (min(e_v - c0, len) + x.T - 1) / x.T;
+        }
+        int ptot;
+        int k = count + scan256(h1 - h0, scratch, sid, &ptot) - round * kMaxPieces;
+        count += ptot;
+#pragma unroll 1
+        for (int h = h0; h < h1; ++h, ++k) {
+          if (k < 0 || k >= kMaxPieces) continue;
+          const int u0 = c0 + h * x.T;  // line position of the unit's first tile
+          Piece& pc = pieces[k];
+          const int t0 = max(s_v - u0, 0), t1 = min(e_v - u0, x.T);
+          pc.b = base + xi;
+          pc.kvh = h;
+          pc.tok0 = seq_n0[xi] + xu * a.unit_tokens;
+          pc.pos0 = x.pos0;
+          pc.lo = x.lo;
+          pc.hi = x.hi;
+          pc.st = x.st;
+          pc.skip = x.skip;
+          pc.t0 = t0;
+          pc.t1 = t1;
+          pc.rows = x.ntok * a.group;
+          // the first piece of a split unit (it holds tile 0) uses the CTA's
+          // slot 1, every later piece (it starts the CTA's range) slot 0
+          const bool split = t0 > 0 || t1 < x.T;
+          const int vf = split ? line->owner(u0) : v;
+          pc.vfirst = vf;
+          pc.npieces = split ? line->owner(u0 + x.T - 1) - vf + 1 : 1;
+          pc.slot = split ? 2 * v + (t0 > 0 ? 0 : 1) : -1;
+        }
       }
-      if (base + kSoftmaxThreads < a.batch || units > kSoftmaxThreads) xbase = -1;
+      kept = pass == 0 && a.batch <= kSoftmaxThreads && units <= kSoftmaxThreads;
       named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
     }
-    line->V = max(1, min(a.vctas, W / max(1, a.min_tiles)));
-    line->q = W / line->V;
-    line->r = W % line->V;
-    line->rV = 1.0f / static_cast<float>(line->V);
-    line->VW = W > 0 ? static_cast<float>(line->V) / static_cast<float>(W) : 0.0f;
-    if (misc->zero_needed) {
-      // the rows of a malformed sequence that can be addressed get zeros
-      const size_t row_bytes = static_cast<size_t>(a.hq) * D * (a.out_fp32 ? 4 : 2);
-      for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-        if (!seq_info(a, b).bad) continue;
-        const long long n0 = a.token_offsets[b], n1 = a.token_offsets[b + 1];
-        if (n0 < 0 || n1 <= n0 || n1 > a.total_tokens) continue;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
-        for (size_t k = sid; k < (n1 - n0) * row_bytes / 16; k += kSoftmaxThreads) dst[k] = make_uint4(0, 0, 0, 0);
-      }
+    if (pass == 0) {
+      line->V = max(1, min(a.vctas, cum / max(1, a.min_tiles)));
+      line->q = cum / line->V;
+      line->r = cum % line->V;
+      line->rV = 1.0f / static_cast<float>(line->V);
+      line->VW = cum > 0 ? static_cast<float>(line->V) / static_cast<float>(cum) : 0.0f;
     }
   }
-  const int v = static_cast<int>(blockIdx.x);
-  int count = 0;  // pieces of this CTA so far (all rounds)
-  const int s_v = v < line->V ? line->start(v) : 0, e_v = v < line->V ? line->start(v + 1) : 0;
-  int cum = 0;    // line position of the next group of units
-  for (int base = 0; base < a.batch && cum < e_v; base += kSoftmaxThreads) {
-    load_chunk(base);
-    for (int ub = 0; ub < units && cum < e_v; ub += kSoftmaxThreads) {
-      const bool have = ub + sid < units;
-      if (xbase != base + ub && have) x = locate(ub + sid, xi, xu);
-      int tot;
-      const int c0 = cum + scan256(have ? x.T * a.hkv : 0, scratch, sid, &tot);
-      cum += tot;
-      // KV heads [h0, h1) of this unit meet [s_v, e_v)
-      int h0 = 0, h1 = 0;
-      if (have && c0 < e_v && c0 + x.T * a.hkv > s_v) {
-        h0 = max(0, s_v - c0) / x.T;
-        h1 = (min(e_v - c0, x.T * a.hkv) + x.T - 1) / x.T;
-      }
-      int ptot;
-      int k = count + scan256(h1 - h0, scratch, sid, &ptot) - round * kMaxPieces;
-      count += ptot;
-      for (int h = h0; h < h1; ++h, ++k) {
-        if (k < 0 || k >= kMaxPieces) continue;
-        const int u0 = c0 + h * x.T;  // line position of the unit's first tile
-        Piece pc;
-        pc.b = base + xi;
-        pc.kvh = h;
-        pc.tok0 = seq_n0[xi] + xu * a.unit_tokens;
-        pc.pos0 = x.pos0;
-        pc.lo = x.lo;
-        pc.hi = x.hi;
-        pc.st = x.st;
-        pc.skip = x.skip;
-        pc.t0 = max(s_v - u0, 0);
-        pc.t1 = min(e_v - u0, x.T);
-        pc.rows = x.ntok * a.group;
-        pc.slot = pc.cnt = -1;
-        pc.npieces = 1;
-        pc.vfirst = v;
-        pc.pad = 0;
-        if (pc.t0 > 0 || pc.t1 < x.T) {
-          // the first piece (it holds tile 0) uses the CTA's slot 1, every
-          // later piece (it starts the CTA's range) slot 0
-          pc.vfirst = line->owner(u0);
-          pc.npieces = line->owner(u0 + x.T - 1) - pc.vfirst + 1;
-          pc.cnt = pc.vfirst;
-          pc.slot = 2 * v + (pc.t0 > 0 ? 0 : 1);
-        }
-        pieces[k] = pc;
-      }
+  if (round == 0 && misc->zero_needed) {
+    // the rows of a malformed sequence that can be addressed get zeros
+    const size_t row_bytes = static_cast<size_t>(a.hq) * D * (a.out_fp32 ? 4 : 2);
+#pragma unroll 1
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+      if (!seq_info(a, b).bad) continue;
+      const long long n0 = a.token_offsets[b], n1 = a.token_offsets[b + 1];
+      if (n0 < 0 || n1 <= n0 || n1 > a.total_tokens) continue;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
+#pragma unroll 1
+      for (size_t k = sid; k < (n1 - n0) * row_bytes / 16; k += kSoftmaxThreads) dst[k] = make_uint4(0, 0, 0, 0);
     }
-    named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
   }
   if (sid == 0) {
     const int n = count - round * kMaxPieces;
@@ -451,95 +444,198 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
     misc->more = n > kMaxPieces;
     for (int k = 0; k < kMaxPieces; ++k) misc->piece_bad[k] = 0;
   }
+  fence_proxy_async_smem();  // the scratch lies where TMA writes Q
 }
 
 // ---------------------------------------------------------------- output
-// Writes 32 values of one output row (fp32 or bf16) at column c0.
+// Where the lanes of a quad write: lane r of a quad stores 16-byte piece r of
+// 64 bytes of the rows of all four lanes, one row after the other, so that a
+// warp's store covers 64 consecutive bytes of 8 rows.  (A lane storing its own
+// row touches 32 lines a store: about 2 clocks each, 4000 clocks for an m-tile.)
+struct QuadRows {
+  uint8_t* at[4];  // row k of the quad, at byte 16 r; null: not written
+};
 template <int D>
-__device__ __forceinline__ void store_row_chunk(const ChunkArgs& a, size_t row, int c0,
-                                                const float (&v)[32]) {
-  if (a.out_fp32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + c0);
+__device__ __forceinline__ QuadRows quad_rows(const ChunkArgs& a, size_t row, bool live) {
+  const int lane = threadIdx.x & 31;
+  const unsigned long long mine =
+      live ? reinterpret_cast<unsigned long long>(a.out) + row * D * (a.out_fp32 ? 4 : 2) : 0ull;
+  QuadRows q;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  } else {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * D + c0);
+  for (int k = 0; k < 4; ++k) {
+    const unsigned long long p = __shfl_sync(0xffffffffu, mine, (lane & ~3) + k);
+    q.at[k] = p ? reinterpret_cast<uint8_t*>(p) + (lane & 3) * 16 : nullptr;
+  }
+  return q;
+}
+// Stores piece c = w[c] of each lane's row, c = 0 .. 3, at byte `off` of the
+// rows: a 4 x 4 transposition inside the quad (two exchange steps), then a
+// store per row.
+__device__ __forceinline__ void quad_store(const QuadRows& q, int off, uint4 (&w)[4]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint4 w;
-      w.x = pack_bf16x2(v[8 * k + 0], v[8 * k + 1]);
-      w.y = pack_bf16x2(v[8 * k + 2], v[8 * k + 3]);
-      w.z = pack_bf16x2(v[8 * k + 4], v[8 * k + 5]);
-      w.w = pack_bf16x2(v[8 * k + 6], v[8 * k + 7]);
-      dst[k] = w;
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+      uint4& lo = w[i];
+      uint4& hi = w[i | bit];
+      uint4 x = up ? lo : hi;
+      x.x = __shfl_xor_sync(0xffffffffu, x.x, bit);
+      x.y = __shfl_xor_sync(0xffffffffu, x.y, bit);
+      x.z = __shfl_xor_sync(0xffffffffu, x.z, bit);
+      x.w = __shfl_xor_sync(0xffffffffu, x.w, bit);
+      if (up) lo = x; else hi = x;
     }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (q.at[k]) *reinterpret_cast<uint4*>(q.at[k] + off) = w[k];
+}
+// Writes columns c0 .. c0 + 31 of each lane's output row (fp32 or bf16), by
+// the whole warp.
+__device__ __forceinline__ void store_rows32(const ChunkArgs& a, const QuadRows& q, int c0, const float (&v)[32]) {
+  uint4 w[4];
+  if (a.out_fp32) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float* x = v + 16 * half + 4 * c;
+        w[c] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      }
+      quad_store(q, (c0 + 16 * half) * 4, w);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float* x = v + 8 * c;
+      w[c] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    quad_store(q, c0 * 2, w);
   }
 }
 
-// Merges the pieces of a split unit: O = sum_s 2^(m_s - M) O_s /
-// sum_s 2^(m_s - M) l_s in piece order.  A thread keeps one row and takes every
-// `step`-th group of 4 columns of it, rows fastest across the threads (a
-// warp's loads are consecutive), 8 groups at a time with all their loads in
-// flight: a unit of 256 rows has a thread per row, one of 8 decode rows split
-// 20 ways has 16 threads per row.
+// The slots of a split unit's pieces.
 template <int D>
-__device__ void merge_unit(const ChunkArgs& a, const Piece& pc, int ur, int nthr) {
-  using Sl = Slot<D>;
-  constexpr int kG = 8;
-  const int step = nthr / pc.rows;
-  const int row = ur % pc.rows, sub = ur / pc.rows;
-  if (sub >= step) return;
-  const uint8_t* first = a.slots + static_cast<size_t>(2 * pc.vfirst + 1) * Sl::kBytes;
-  auto base = [&](int s) {
-    return s == 0 ? first : a.slots + static_cast<size_t>(2 * (pc.vfirst + s)) * Sl::kBytes;
-  };
-  int bad = 0;
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int s = 0; s < pc.npieces; ++s) {
-    bad |= __ldcg(reinterpret_cast<const int*>(base(s) + Sl::kFlag));
-    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row).x);
+struct Slots {
+  const uint8_t *first, *rest;
+  __device__ __forceinline__ Slots(const ChunkArgs& a, const Piece& pc)
+      : first(a.slots + static_cast<size_t>(2 * pc.vfirst + 1) * Slot<D>::kBytes),
+        rest(a.slots + static_cast<size_t>(2 * pc.vfirst) * Slot<D>::kBytes) {}
+  __device__ __forceinline__ const uint8_t* at(int s) const {
+    return s == 0 ? first : rest + static_cast<size_t>(2 * s) * Slot<D>::kBytes;
   }
-  const size_t out_row = static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group;
-#pragma unroll 1
-  for (int d0 = sub; d0 < D / 4; d0 += kG * step) {
-    float l = 0.0f;
-    float4 acc[kG];
-#pragma unroll
-    for (int k = 0; k < kG; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __device__ __forceinline__ int flag(int s) const {
+    return __ldcg(reinterpret_cast<const int*>(at(s) + Slot<D>::kFlag));
+  }
+  __device__ __forceinline__ float2 ml(int s, int row) const {
+    return __ldcg(reinterpret_cast<const float2*>(at(s) + Slot<D>::kMl) + row);
+  }
+  __device__ __forceinline__ const float4* o(int s, int row) const {
+    return reinterpret_cast<const float4*>(at(s) + Slot<D>::kO) + row;
+  }
+};
+
+// Merges the pieces of a split unit: O = sum_s 2^(m_s - M) O_s /
+// sum_s 2^(m_s - M) l_s in piece order.  Both forms run once or twice in a
+// launch, at its end, and stay rolled: what such code costs besides its loads
+// is its instructions' way from L2.
+//
+// A thread per row (more than half as many rows as threads): piece `own` from
+// TMEM and registers (bit for bit what its slot would hold), the others from
+// their slots, 64 columns of a piece in flight.  Writing and reading its own
+// slot too, 16 columns at a time, took 28000 clocks of a 250-row unit.
+template <int D>
+__device__ void merge_rows(const ChunkArgs& a, const Piece& pc, int ur, int own, float m_own, float l_own,
+                           int bad, uint32_t tmem_o) {
+  const Slots<D> sl(a, pc);
+  const bool live = ur < pc.rows;
+  const int row = min(ur, pc.rows - 1);
+  float M = m_own;
 #pragma unroll 2
-    for (int s = 0; s < pc.npieces; ++s) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(base(s) + Sl::kMl) + row);
-      float4 o[kG];
+  for (int s = 0; s < pc.npieces; ++s) {
+    if (s == own) continue;
+    bad |= sl.flag(s);
+    M = fmaxf(M, sl.ml(s, row).x);
+  }
+  const QuadRows quad =
+      quad_rows<D>(a, static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group, live);
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 64) {
+    float l = 0.0f;
+    float acc[64];
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        const int d4 = d0 + k * step;
-        o[k] = d4 < D / 4 ? __ldcg(reinterpret_cast<const float4*>(base(s) + Sl::kO) + d4 * pc.rows + row)
-                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < 64; ++k) acc[k] = 0.0f;
+#pragma unroll 1
+    for (int s = 0; s < pc.npieces; ++s) {
+      float x[64];
+      float2 ml = make_float2(m_own, l_own);
+      if (s == own) {
+        tmem_ld32(tmem_o + c0, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+        tmem_ld32(tmem_o + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+        tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+        tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      } else {
+        ml = sl.ml(s, row);
+        const float4* o4 = sl.o(s, row) + (c0 / 4) * pc.rows;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) *reinterpret_cast<float4*>(&x[4 * k]) = __ldcg(o4 + k * pc.rows);
       }
       const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
       l += w * ml.y;
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        acc[k].x += w * o[k].x;
-        acc[k].y += w * o[k].y;
-        acc[k].z += w * o[k].z;
-        acc[k].w += w * o[k].w;
-      }
+      for (int k = 0; k < 64; ++k) acc[k] += w * x[k];
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-    for (int k = 0; k < kG; ++k) {
-      const int d4 = d0 + k * step;
-      if (d4 >= D / 4) break;
-      const float4 v = bad ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                           : make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
-      if (a.out_fp32) {
-        reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D)[d4] = v;
-      } else {
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D)[d4] =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      }
+    for (int k = 0; k < 64; ++k) acc[k] = bad ? 0.0f : acc[k] * inv;
+#pragma unroll
+    for (int c = 0; c < 64; c += 32)
+      store_rows32(a, quad, c0 + c, *reinterpret_cast<const float(*)[32]>(&acc[c]));
+  }
+}
+
+// Several threads per row (a few decode rows, split many ways): every piece
+// from its slot, thread `sub` of a row taking groups sub, sub + step, .. of 4
+// columns.
+template <int D>
+__device__ void merge_groups(const ChunkArgs& a, const Piece& pc, int ur, int step) {
+  const Slots<D> sl(a, pc);
+  const int row = ur % pc.rows, sub = ur / pc.rows;
+  if (sub >= step) return;
+  int bad = 0;
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < pc.npieces; ++s) {
+    bad |= sl.flag(s);
+    M = fmaxf(M, sl.ml(s, row).x);
+  }
+  const size_t out_row = static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group;
+#pragma unroll 1
+  for (int d4 = sub; d4 < D / 4; d4 += step) {
+    float l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = 0; s < pc.npieces; ++s) {
+      const float2 ml = sl.ml(s, row);
+      const float4 o = __ldcg(sl.o(s, row) + d4 * pc.rows);
+      const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+      l += w * ml.y;
+      acc.x += w * o.x;
+      acc.y += w * o.y;
+      acc.z += w * o.z;
+      acc.w += w * o.w;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float4 v = bad ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                         : make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (a.out_fp32) {
+      reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D)[d4] = v;
+    } else {
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * D)[d4] =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
   }
 }
@@ -572,10 +668,11 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   uint64_t* p_a = s_full + 2;             // [2]: P_h(t) of keys 0 .. 63 in TMEM (128 arrivals)
   uint64_t* p_b = p_a + 2;                // [2]: P_h(t) of keys 64 .. 127
   uint64_t* o_done = p_b + 2;             // [2]: the last P_h V of a piece complete
-  uint64_t* q_full = o_done + 2;          // [2]: Q_h of a piece in shared memory (128 arrivals)
-  uint64_t* drain = q_full + 2;           // [2]: every MMA of m-tile h so far complete (once per round)
+  uint64_t* drain = o_done + 2;           // [2]: every MMA of m-tile h so far complete (once per round)
   uint64_t* turn = drain + 2;             // [2]: m-tile h may issue (units with both)
-  uint64_t* v16full = turn + 2;           // F8 [2]: V(t) converted (128 arrivals)
+  uint64_t* q_full = turn + 2;            // Q of a piece in shared memory
+  uint64_t* q_empty = q_full + 1;         // the last S of both m-tiles of a piece complete
+  uint64_t* v16full = q_empty + 1;         // F8 [2]: V(t) converted (128 arrivals)
   uint64_t* v16empty = v16full + 2;       // F8 [2]: the P V of tile t complete
   uint64_t* sfull = v16empty + 2;         // F8 [8]: the scales of tile t landed (32 arrivals)
   Misc* misc = reinterpret_cast<Misc*>(smem + Ly::kMisc);
@@ -608,10 +705,11 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       mbar_init(&p_a[h], BM);
       mbar_init(&p_b[h], BM);
       mbar_init(&o_done[h], 1);
-      mbar_init(&q_full[h], BM);
       mbar_init(&drain[h], 1);
       mbar_init(&turn[h], 1);
     }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -627,9 +725,10 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   const int g = a.group;
 
   // Progress kept across pieces and rounds (ring slots and barrier phases):
-  // g_tile = K/V tiles of every earlier round; my_tiles and my_pieces = the
-  // tiles and pieces of this role's m-tile so far (MMA and softmax).
-  int g_tile = 0, my_tiles = 0, my_pieces = 0, my_turns = 0;
+  // g_tile, g_piece = K/V tiles and pieces of every earlier round; my_tiles,
+  // my_pieces and my_turns = the tiles and pieces of this role's m-tile and its
+  // turns so far (MMA and softmax).
+  int g_tile = 0, g_piece = 0, my_tiles = 0, my_pieces = 0, my_turns = 0;
 
   // Each role runs the scheduling rounds in a loop of its own (its registers
   // are its own too).  A round: the softmax warps build the piece list, every
@@ -647,6 +746,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       named_sync(kBarCta, Shares<F8>::kThreads);
       tc_fence_after();
       for (int p = 0; p < npieces; ++p) g_tile += pieces[p].t1 - pieces[p].t0;
+      g_piece += npieces;
       const bool stop = !more || misc->abort;
       named_sync(kBarCta, Shares<F8>::kThreads);  // the piece list is rebuilt next round
       if (stop) break;
@@ -663,6 +763,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       // of the tile.  K runs ahead of V: a K slot is free again once the last
       // S of its tile is done, a V slot once the last P V is.
       if (round == 0 && lane == 0) {
+        prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k_pool);
         prefetch_tmap(&maps.v_pool);
       }
@@ -723,13 +824,33 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           if (p < npieces) t = pieces[p].t0;
         }
       };
+      // Q of piece p (q_tokens tokens of g heads, rows past the unit are other
+      // tokens' or zeros and unused), once the S of piece p - 1 are complete
+      auto issue_q = [&](int p) {
+        if (lane == 0) {
+          const Piece& pc = pieces[p];
+          mbar_arrive_expect_tx(q_full, Ly::kQLines * a.q_tokens * a.group * 128);
+          for (int l = 0; l < Ly::kQLines; ++l)
+            tma_load_3d(smem + Ly::kQ + l * Ly::kQLineBytes, &maps.q, q_full, l * 64, pc.kvh * a.group, pc.tok0);
+        }
+        __syncwarp();
+      };
+      int qp = 0;
       int kp = 0, kt = pieces[0].t0, vp = 0, vt = pieces[0].t0;
       int blk_k = fetch_block(kp, kt);  // the block ids of the next K tile, read ahead
       int tk = g_tile, tv = g_tile;
       bool ok = true;
       unsigned long long t_idle = 0;
-      while (vp < npieces) {
+      while (vp < npieces || qp < npieces) {
         bool progressed = false;
+        if (qp < npieces) {
+          const int n = g_piece + qp;
+          int ready = lane == 0 ? (n == 0 || mbar_test_wait(q_empty, (n - 1) & 1)) : 0;
+          if (__shfl_sync(0xffffffffu, ready, 0)) {
+            issue_q(qp++);
+            progressed = true;
+          }
+        }
         // V before K: the next P V needs its V tile before the S after it
         // needs its K tile, and the copies of one warp land in issue order
         if (tv < tk) {
@@ -767,6 +888,8 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             mbar_try_wait_ns(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1, 200);
           else if (k_next)
             mbar_try_wait_ns(&kempty[tk % kStages], ((tk / kStages) & 1) ^ 1, 200);
+          else if (qp < npieces)
+            mbar_try_wait_ns(q_empty, (g_piece + qp - 1) & 1, 200);
         }
         if (lane == 0) {
           if (progressed) {
@@ -785,7 +908,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       if constexpr (F8) cpa_wait_all();  // this lane's scale copies have landed
       if (lane == 0) {
         if (!ok) {
-          record_status(a.status, pieces[min(vp, npieces - 1)].b, kDeviceTimeout);
+          record_status(a.status, pieces[min(min(vp, qp), npieces - 1)].b, kDeviceTimeout);
           misc->abort = 1;
         }
         // every issued copy has landed before the ring is reused or the CTA
@@ -794,6 +917,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           mbar_wait(&kfull[t % kStages], (t / kStages) & 1);
         for (int t = max(g_tile, tv - kVStages); t < tv; ++t)
           mbar_wait(&vfull[t % kVStages], (t / kVStages) & 1);
+        if (qp > 0) mbar_wait(q_full, (g_piece + qp - 1) & 1);
       }
       __syncwarp();
       });
@@ -806,13 +930,14 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         // over the codes, P V on kind::f16 in fp16.
         constexpr uint32_t idesc_s = F8 ? idesc_e4m3(BM, BN) : idesc_bf16(BM, BN, 0);
         constexpr uint32_t idesc_o = F8 ? idesc_f16(BM, D, 1) : idesc_bf16(BM, D, 1);
-        // K and Q (K-major): 8-row groups at kGroupBytes (16-bit) or 1024
+        // K (K-major): 8-row groups at kGroupBytes (16-bit) or 1024
         // (8-bit), 64-column halves at +1024.  V (MN-major): 8-key groups at
         // kGroupBytes, column halves at +1024.
+        // Q (K-major): 8-row groups at 1024, lines at kQLineBytes.
         constexpr uint32_t kKRow8 = F8 ? 1024 : Ly::kGroupBytes;
         const uint64_t dk0 = smem_desc(smem_u32(smem + Ly::kKRing), 16, kKRow8);
         const uint64_t dv0 = smem_desc(smem_u32(smem + (F8 ? Ly::kV16 : Ly::kVRing)), 1024, Ly::kGroupBytes);
-        const uint64_t dq = smem_desc(smem_u32(smem + Ly::kQ + h * Ly::kQBytes), 16, kKRow8);
+        const uint64_t dq = smem_desc(smem_u32(smem + Ly::kQ + h * BM * 128), 16, 1024);
         const uint32_t tmem_s = tmem + h * BN, tmem_o = tmem + 256 + h * D;
         uint64_t* vready = F8 ? v16full : vfull;  // V(t) as the P V reads it, and its release
         uint64_t* vdone = F8 ? v16empty : vempty;
@@ -828,8 +953,9 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           } else {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-              mma_bf16_ss(tmem_s, dq + off, dk + off, idesc_s, kk > 0 ? 1u : 0u);
+              const uint32_t in = (kk & 3) * 2;  // 32 bytes within the 128-byte line
+              mma_bf16_ss(tmem_s, dq + (kk >> 2) * (Ly::kQLineBytes >> 4) + in, dk + (kk >> 2) * 64 + in,
+                          idesc_s, kk > 0 ? 1u : 0u);
             }
           }
           mma_commit(&s_full[h]);
@@ -859,6 +985,8 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           const int nm = pieces[p].rows > BM ? 2 : 1, T = pieces[p].t1 - pieces[p].t0;
           if (h >= nm) {
             // no rows of this m-tile: its arrivals keep the rings turning
+            ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag);
+            if (ok) mbar_arrive(q_empty);
             for (int t = tau; t < tau + T && ok; ++t) {
               ok = k_wait(t);
               if (ok) mbar_arrive(&kempty[t % kStages]);
@@ -869,11 +997,12 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             continue;
           }
           // the piece's first S, once its Q is loaded and K has landed
-          ok = mbar_wait(&q_full[h], my_pieces & 1, abort_flag) && k_wait(tau);
+          ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag) && k_wait(tau);
           if (!ok) break;
           tc_fence_after();
           issue_s(tau);
           mma_commit(&kempty[tau % kStages]);
+          if (T == 1) mma_commit(q_empty);
           for (int i = 0; i < T; ++i) {
             const int t = tau + i;
             const bool next = i + 1 < T;
@@ -892,6 +1021,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             ++my_tiles;
             mma_commit(&vdone[t % kVSlots]);
             if (next) mma_commit(&kempty[(t + 1) % kStages]);
+            if (i + 2 == T) mma_commit(q_empty);
           }
           if (!ok) break;
           mma_commit(&o_done[h]);
@@ -991,7 +1121,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tmem_s = tmem + h * BN + lane_off;
       const uint32_t tmem_o = tmem + 256 + h * D + lane_off;
-      uint8_t* qh = smem + Ly::kQ + h * Ly::kQBytes;
       volatile int* piece_bad = misc->piece_bad;
       bool ok = true;
       int tau = g_tile;  // global index of the piece's first tile
@@ -1009,42 +1138,11 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         const int pos = pc.pos0 + tok;             // position of this row
         const size_t q_row = static_cast<size_t>(pc.tok0 + tok);
         const int head = pc.kvh * g + (live ? ur - tok * g : 0);
-        // Q rows -> shared memory in the 128-byte swizzled K-major layout
-        // (the 16-byte chunk c of row r sits at chunk c ^ (r % 8)); rows past
-        // the unit are zero.  The buffer is free: the previous piece's last
-        // S_h completed before its epilogue.  E4M3: one 128-byte line of
-        // codes a row, and the row's scale folded into the exponent factor
-        // (kept above 0, so that a masked -inf never meets a factor of 0).
+        // E4M3: the row's scale is folded into the exponent factor (kept above
+        // 0, so that a masked -inf never meets a factor of 0)
         float cq = a.scale_log2;
-        {
-          constexpr int kRowBytes = F8 ? D : 2 * D;
-          constexpr int kLineBytes = F8 ? 1024 : Ly::kGroupBytes;  // 8 rows
-          uint8_t* dst = qh + (r >> 3) * kLineBytes + (r & 7) * 128;
-          if (live) {
-            const uint8_t* src = static_cast<const uint8_t*>(a.q) + q_row * a.q_stride_bytes +
-                                 static_cast<size_t>(head) * kRowBytes;
-#pragma unroll
-            for (int k = 0; k < kRowBytes / 16; ++k)
-              cpa16(dst + (k >> 3) * 1024 + (((k & 7) ^ (r & 7)) << 4), src + k * 16);
-            if constexpr (F8) cq = fmaxf(a.scale_log2 * __ldg(a.q_scale + q_row * a.hq + head), 1e-37f);
-          } else {
-#pragma unroll
-            for (int k = 0; k < kRowBytes / 16; ++k)
-              *reinterpret_cast<uint4*>(dst + (k >> 3) * 1024 + k % 8 * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        // the next piece's Q row of this thread into L2
-        if (p + 1 < npieces && ur < pieces[p + 1].rows) {
-          const Piece& nx = pieces[p + 1];
-          const uint8_t* q = static_cast<const uint8_t*>(a.q) +
-                             static_cast<size_t>(nx.tok0 + ur / g) * a.q_stride_bytes +
-                             static_cast<size_t>(nx.kvh * g + ur % g) * (F8 ? D : 2 * D);
-#pragma unroll
-          for (int k = 0; k < (F8 ? D : 2 * D); k += 128) prefetch_l2(q + k);
-        }
-        cpa_wait_all();
-        fence_proxy_async_smem();  // generic writes of Q, read by the MMA
-        mbar_arrive(&q_full[h]);
+        if constexpr (F8)
+          if (live) cq = fmaxf(a.scale_log2 * __ldg(a.q_scale + q_row * a.hq + head), 1e-37f);
 
         float m_run = -INFINITY;  // running max (log2 units)
         float l_run = 0.0f;       // row sum against m_run
@@ -1111,8 +1209,11 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               const int kc = k0 + 32 * c;
               uint32_t bits = bits_below(pos + 1 - kc);
               if (a.window > 0) bits &= ~bits_below(pos + 1 - a.window - kc) | bits_below(a.sinks - kc);
+              // (the rows of a warp are a few tokens: most of its words are whole)
+              if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = (bits & (1u << k)) ? y[k] : -INFINITY;
+                for (int k = 0; k < 32; ++k) y[k] = (bits & (1u << k)) ? y[k] : -INFINITY;
+              }
             }
             float u[4];
 #pragma unroll
@@ -1125,7 +1226,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             mx[c] = fmax3(u[0], u[1], fmaxf(u[2], u[3]));
           }
           const float smax = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cq;
-          const bool up = smax > m_run + kRescaleLog2;  // (the first visible score too)
+          const bool up = live && smax > m_run + kRescaleLog2;  // (the first visible score too)
           if (__any_sync(0xffffffffu, up)) {
             const float alpha = up ? exp2f(m_run - smax) : 1.0f;
             if (up) m_run = smax;
@@ -1133,12 +1234,12 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             // (S_h(t), which this thread has seen complete, was issued after it)
             // (the piece's first P V overwrites O)
 #pragma unroll 1
-            for (int c0 = 0; i > 0 && c0 < D; c0 += 8) {
-              uint32_t o[8];  // few at a time: the 128 scores are live
-              tmem_ld8(tmem_o + c0, o);
+            for (int c0 = 0; i > 0 && c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem_o + c0, o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st8(tmem_o + c0, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st16(tmem_o + c0, o);
             }
             l_run *= alpha;  // (this tile's sum is added below, against the new max)
           }
@@ -1192,54 +1293,67 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         tc_fence_after();
         if (pc.slot < 0) {
           // the whole unit: normalise and write
+          // (rolled, as everything that runs once a piece: see merge_unit)
           const float inv_l = l_run > 0.0f ? 1.0f / l_run : 0.0f;
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0u;
-            if (done) {
+          if (done) {
+            const QuadRows quad = quad_rows<D>(a, q_row * a.hq + head, live);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
               tmem_ld32(tmem_o + c0, o);
               tmem_ld_wait32(o);
-            }
-            float v[32];
+              float v[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = bad ? 0.0f : __uint_as_float(o[k]) * inv_l;
-            if (live && done) store_row_chunk<D>(a, q_row * a.hq + head, c0, v);
+              for (int k = 0; k < 32; ++k) v[k] = bad ? 0.0f : __uint_as_float(o[k]) * inv_l;
+              store_rows32(a, quad, c0, v);
+            }
           }
         } else {
-          // a piece of a split unit: raw O and (m, l) to its slot, then a
-          // ticket; the last piece to take one merges every slot of the unit
+          // a piece of a split unit.  With a thread per row, a piece that
+          // finds every other one done merges straight from TMEM.  Otherwise
+          // raw O and (m, l) go to its slot and it takes a ticket; the last to
+          // take one merges.
           const int nthr = nm * BM;
           const int bar = nm == 2 ? kBarPair : kBarGroup0;
-          uint8_t* sl = a.slots + static_cast<size_t>(pc.slot) * Sl::kBytes;
-          float4* so4 = reinterpret_cast<float4*>(sl + Sl::kO) + ur;
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0u;
-            if (done) {
-              tmem_ld32(tmem_o + c0, o);
-              tmem_ld_wait32(o);
-            }
-            if (live) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                __stcg(so4 + static_cast<size_t>(c0 / 4 + k) * pc.rows,
-                       make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
-            }
-          }
-          if (live) __stcg(reinterpret_cast<float2*>(sl + Sl::kMl) + ur, make_float2(m_run, l_run));
-          if (ur == 0) __stcg(reinterpret_cast<int*>(sl + Sl::kFlag), (bad || !done) ? 1 : 0);
-          __threadfence();
+          const int step = nthr / pc.rows;
+          const int flag = (bad || !done) ? 1 : 0;
+          int* ticket = a.counters + pc.vfirst;
+          if (ur == 0) misc->merge = step == 1 && *static_cast<volatile int*>(ticket) == pc.npieces - 1;
           named_sync(bar, nthr);
-          if (ur == 0) misc->merge = atomicAdd(a.counters + pc.cnt, 1) == pc.npieces - 1;
-          named_sync(bar, nthr);
-          if (misc->merge) {
+          bool merge = misc->merge;
+          if (!merge) {
+            uint8_t* slot = a.slots + static_cast<size_t>(pc.slot) * Sl::kBytes;
+            float4* so4 = reinterpret_cast<float4*>(slot + Sl::kO) + ur;
+            if (done) {  // (otherwise the flag voids the slot)
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(tmem_o + c0, o);
+                tmem_ld_wait32(o);
+                if (live) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    __stcg(so4 + (c0 / 4 + k) * pc.rows,
+                           make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                       __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
+                }
+              }
+            }
+            if (live) __stcg(reinterpret_cast<float2*>(slot + Sl::kMl) + ur, make_float2(m_run, l_run));
+            if (ur == 0) __stcg(reinterpret_cast<int*>(slot + Sl::kFlag), flag);
             __threadfence();
-            merge_unit<D>(a, pc, ur, nthr);
+            named_sync(bar, nthr);
+            if (ur == 0) misc->merge = atomicAdd(ticket, 1) == pc.npieces - 1;
+            named_sync(bar, nthr);
+            merge = misc->merge;
+          }
+          if (merge) {
+            __threadfence();
+            if (step == 1) {
+              merge_rows<D>(a, pc, ur, static_cast<int>(blockIdx.x) - pc.vfirst, m_run, l_run, flag, tmem_o);
+            } else {
+              merge_groups<D>(a, pc, ur, step);
+            }
           }
           named_sync(bar, nthr);  // misc->merge is rewritten by the next split piece
         }

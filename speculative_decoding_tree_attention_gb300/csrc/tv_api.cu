@@ -555,7 +555,7 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
   const int64_t row = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
   const int64_t elem = fp8 ? 1 : 2;
   const int64_t stride = p->q_stride ? p->q_stride : row;
-  if (stride < row || stride > INT64_MAX / 2 || stride * elem % 16) return TV_ERR_INVALID_ARG;
+  if (stride < row || stride >= (1ll << 38) || stride * elem % 16) return TV_ERR_INVALID_ARG;
   const void* ptrs[] = {k_pool, v_pool, block_table, seq_lens, token_offsets, status};
   for (const void* x : ptrs)
     if (!x || !aligned16(x)) return TV_ERR_INVALID_ARG;
@@ -575,7 +575,18 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
     return TV_ERR_CUDA;
   tv::ChunkArgs a;
   std::memset(&a, 0, sizeof a);
-  a.q = q;
+  a.q_tokens = std::min(pl.unit_tokens, p->total_tokens);
+  if (p->total_tokens > 0) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p->head_dim), static_cast<cuuint64_t>(p->num_q_heads),
+                                static_cast<cuuint64_t>(p->total_tokens)};
+    const cuuint64_t str[2] = {static_cast<cuuint64_t>(p->head_dim * elem), static_cast<cuuint64_t>(stride * elem)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem),
+                               static_cast<cuuint32_t>(p->num_q_heads / p->num_kv_heads),
+                               static_cast<cuuint32_t>(a.q_tokens)};
+    if (!encode(&maps.q, q, 3, dims, str, box,
+                fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
+      return TV_ERR_CUDA;
+  }
   a.block_table = block_table;
   a.seq_lens = seq_lens;
   a.token_offsets = token_offsets;
@@ -583,7 +594,6 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
   a.status = status;
   a.counters = static_cast<int32_t*>(workspace);
   a.slots = static_cast<uint8_t*>(workspace) + (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256;
-  a.q_stride_bytes = static_cast<size_t>(stride * elem);
   a.batch = p->batch;
   a.hq = p->num_q_heads;
   a.hkv = p->num_kv_heads;

@@ -92,7 +92,6 @@ int launch_tree_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t 
 size_t attn_slot_bytes(int head_dim);
 
 struct ChunkArgs {
-  const void* q;              // [total_tokens] rows of Hq x D, q_stride_bytes apart
   const int32_t* block_table; // [batch][max_blocks_per_seq]
   const int32_t* seq_lens;    // [batch] cached tokens, the chunk's included
   const int32_t* token_offsets; // [batch+1]
@@ -100,7 +99,7 @@ struct ChunkArgs {
   int32_t* status;            // [batch]
   int32_t* counters;          // [vctas] ticket counters of split units (zeroed per call)
   uint8_t* slots;             // [2 * vctas] partial-result slots of chunk_slot_bytes(D)
-  size_t q_stride_bytes;
+  int32_t q_tokens;           // tokens of a Q box: min(unit_tokens, total_tokens)
   int32_t batch, hq, hkv, group, head_dim;
   int32_t max_blocks_per_seq, num_blocks, max_len, total_tokens;
   int32_t unit_tokens;        // tokens of a unit: floor(256 / group)
@@ -116,6 +115,7 @@ struct ChunkArgs {
 };
 
 struct ChunkMaps {
+  CUtensorMap q;        // 3D (row, heads, tokens), box = 128 bytes of the g heads of q_tokens tokens
   CUtensorMap k_pool;   // as AttnMaps
   CUtensorMap v_pool;
 };
