@@ -23,9 +23,10 @@
 // ticket merges all slots in piece order, so results do not depend on timing.
 //
 // One CTA has 384 threads (512 for an E4M3 cache):
-//   warp 8      loads K and V tiles by TMA, one box per 16-token page through
-//               the block table; pages that no row of the unit sees are never
-//               read (an out-of-range page index loads zeros).
+//   warps 8, 11 load the K tiles, and the V tiles and Q, by TMA: one box per
+//               16-token page through the block table; pages that no row of
+//               the unit sees are never read (an out-of-range page index loads
+//               zeros).
 //   warps 9, 10 issue the tcgen05.mma of m-tile h = 0 and 1: S_h = Q_h K^T
 //               into TMEM, O_h += P_h V with P_h from TMEM.  P_h lies over S_h;
 //               the MMAs of one thread run in order, so S_h(t+1) follows
@@ -62,7 +63,8 @@ constexpr int BM = 128;               // rows of one m-tile
 constexpr int BN = 128;               // keys per tile
 constexpr int kUnitRows = 2 * BM;
 constexpr int kSoftmaxThreads = 256;  // warps 0-7: two groups of four warps
-constexpr int kTmaWarp = 8;
+constexpr int kKWarp = 8;             // TMA: K tiles
+constexpr int kVWarp = 11;            // TMA: V tiles and Q
 constexpr int kMmaWarp = 9;           // warps 9, 10 issue the MMAs of m-tile 0, 1
 constexpr int kConvWarp = 12;         // E4M3: warps 12-15 convert V tiles to fp16
 constexpr int kConvThreads = 128;
@@ -92,14 +94,16 @@ struct Piece {
   int b, kvh;
   int tok0;         // first token of the unit (row of q)
   int pos0;         // its position
-  int lo, hi;       // the unit sees keys < sinks and keys lo .. hi
-  int st, skip;     // tile t < st is key tile t, later ones key tile t + skip
+  int ntok;         // tokens of the unit
   int t0, t1;
-  int rows;         // packed rows of the unit (1 .. 256)
-  int slot;         // partial-result slot, -1 when the piece is the whole unit
-  int npieces;      // pieces of a split unit
-  int vfirst;       // CTA of the unit's first piece (its ticket counter)
-  int pad[2];
+  int cut;          // pieces of the unit << 16 | CTA of its first piece (its ticket counter)
+  __device__ __forceinline__ int npieces() const { return cut >> 16; }
+  __device__ __forceinline__ int vfirst() const { return cut & 0xffff; }
+  __device__ __forceinline__ int hi() const { return pos0 + ntok - 1; }
+  // partial-result slot of a split unit's piece: the first piece (it holds
+  // tile 0) uses its CTA's slot 1, every later piece (it starts its CTA's
+  // range) slot 0
+  __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (t0 > 0 ? 0 : 1); }
 };
 
 // Shared memory of one CTA.  bf16: K and V tiles of 128 keys x D in rings.
@@ -121,18 +125,19 @@ struct Layout {
   static constexpr int kVRing = kKRing + kStages * kKTileBytes;
   static constexpr int kV16 = kVRing + kVStages * kKTileBytes;
   static constexpr int kV16Bytes = F8 ? 2 * kTileBytes : 0;
-  static constexpr int kScl = kV16 + kV16Bytes;        // F8: [8][2][128] floats
-  static constexpr int kSclBytes = F8 ? kSclSlots * 2 * BN * 4 : 0;
+  static constexpr int kScl = kV16 + kV16Bytes;        // F8: K scales [8][128], V scales [VS][128]
+  static constexpr int kVScl = kScl + (F8 ? kSclSlots * BN * 4 : 0);
+  static constexpr int kSclBytes = F8 ? (kSclSlots + kVStages) * BN * 4 : 0;
   static constexpr int kPieces = kScl + kSclBytes;
   static constexpr int kPiecesBytes = kMaxPieces * static_cast<int>(sizeof(Piece));
-  static constexpr int kBlk = kPieces + kPiecesBytes;  // block ids of the last 8 K tiles
-  static constexpr int kBlkBytes = 8 * 8 * 4;
-  static constexpr int kBar = kBlk + kBlkBytes;
+  static constexpr int kXch = kPieces + kPiecesBytes;  // [128] (m, l) of group 1, narrow pieces
+  static constexpr int kXchBytes = BM * 8;
+  static constexpr int kBar = kXch + kXchBytes;
   // kfull, kempty [S], vfull, vempty [VS], s_full, p_a, p_b, o_done, drain,
   // turn [2], q_full, q_empty, v16full, v16empty [2], sfull [8]
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 14 + (F8 ? 4 + kSclSlots : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kMiscBytes = 160;
+  static constexpr int kMiscBytes = 96;
   static constexpr int kTotal = kMisc + kMiscBytes;
   static constexpr int kAlloc = kTotal + 1024;  // slack for 1024-byte alignment
   // the schedule's scratch (a chunk of 256 sequences) lies over Q, which is
@@ -212,27 +217,36 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 }
 
 // ---------------------------------------------------------------- schedule
-struct Unit {
-  int pos0, ntok;
-  int lo, hi, st, skip, T;
+// The keys that a unit whose first token sits at pos0 sees, besides those past
+// its last token: keys < sinks and keys >= lo.  Tile t < st of the unit is key
+// tile t, later ones key tile t + skip.  When the whole context is visible (no
+// window, or one that reaches the sinks), lo = st = skip = 0.
+struct Extent {
+  int lo, st, skip;
+  __device__ __forceinline__ int key_tile(int t) const { return t < st ? t : t + skip; }
 };
+__device__ __forceinline__ Extent extent_of(const ChunkArgs& a, int pos0) {
+  Extent e;
+  e.lo = e.st = e.skip = 0;
+  if (a.window > 0 && pos0 - a.window + 1 > a.sinks) {
+    e.lo = pos0 - a.window + 1;
+    e.st = (a.sinks + BN - 1) / BN;
+    e.skip = max(0, e.lo / BN - e.st);
+  }
+  return e;
+}
 
-// Unit u of a chunk of C tokens that starts at position ctx.  When the whole
-// context is visible to the unit (no window, or a window that reaches the
-// sinks), lo = st = skip = 0.
+// Unit u of a chunk of C tokens that starts at position ctx: its first
+// position, tokens and key tiles.
+struct Unit {
+  int pos0, ntok, T;
+};
 __device__ __forceinline__ Unit unit_of(const ChunkArgs& a, int ctx, int C, int u) {
   Unit x;
   const int tok = u * a.unit_tokens;
   x.ntok = min(a.unit_tokens, C - tok);
   x.pos0 = ctx + tok;
-  x.hi = x.pos0 + x.ntok - 1;
-  x.lo = x.st = x.skip = 0;
-  if (a.window > 0 && x.pos0 - a.window + 1 > a.sinks) {
-    x.lo = x.pos0 - a.window + 1;
-    x.st = (a.sinks + BN - 1) / BN;
-    x.skip = max(0, x.lo / BN - x.st);
-  }
-  x.T = x.hi / BN + 1 - x.skip;
+  x.T = (x.pos0 + x.ntok - 1) / BN + 1 - extent_of(a, x.pos0).skip;
   return x;
 }
 
@@ -398,20 +412,15 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
           pc.kvh = h;
           pc.tok0 = seq_n0[xi] + xu * a.unit_tokens;
           pc.pos0 = x.pos0;
-          pc.lo = x.lo;
-          pc.hi = x.hi;
-          pc.st = x.st;
-          pc.skip = x.skip;
+          pc.ntok = x.ntok;
           pc.t0 = t0;
           pc.t1 = t1;
-          pc.rows = x.ntok * a.group;
-          // the first piece of a split unit (it holds tile 0) uses the CTA's
-          // slot 1, every later piece (it starts the CTA's range) slot 0
-          const bool split = t0 > 0 || t1 < x.T;
-          const int vf = split ? line->owner(u0) : v;
-          pc.vfirst = vf;
-          pc.npieces = split ? line->owner(u0 + x.T - 1) - vf + 1 : 1;
-          pc.slot = split ? 2 * v + (t0 > 0 ? 0 : 1) : -1;
+          int vf = v, np = 1;
+          if (t0 > 0 || t1 < x.T) {
+            vf = line->owner(u0);
+            np = line->owner(u0 + x.T - 1) - vf + 1;
+          }
+          pc.cut = np << 16 | vf;
         }
       }
       kept = pass == 0 && a.batch <= kSoftmaxThreads && units <= kSoftmaxThreads;
@@ -522,8 +531,8 @@ template <int D>
 struct Slots {
   const uint8_t *first, *rest;
   __device__ __forceinline__ Slots(const ChunkArgs& a, const Piece& pc)
-      : first(a.slots + static_cast<size_t>(2 * pc.vfirst + 1) * Slot<D>::kBytes),
-        rest(a.slots + static_cast<size_t>(2 * pc.vfirst) * Slot<D>::kBytes) {}
+      : first(a.slots + static_cast<size_t>(2 * pc.vfirst() + 1) * Slot<D>::kBytes),
+        rest(a.slots + static_cast<size_t>(2 * pc.vfirst()) * Slot<D>::kBytes) {}
   __device__ __forceinline__ const uint8_t* at(int s) const {
     return s == 0 ? first : rest + static_cast<size_t>(2 * s) * Slot<D>::kBytes;
   }
@@ -538,6 +547,29 @@ struct Slots {
   }
 };
 
+// This thread's row of the piece's O: O_h of its m-tile, or, in a narrow piece
+// whose key tiles the two groups took in turn, w0 O_0 + w1 O_1 against the
+// larger maximum.
+template <int D>
+struct OwnO {
+  uint32_t tmem;  // O_h
+  bool two;
+  float w0, w1;
+  __device__ __forceinline__ void load(int c0, float (&v)[32]) const {
+    uint32_t o[32];
+    tmem_ld32(tmem + c0, o);
+    tmem_ld_wait32(o);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
+    if (two) {
+      tmem_ld32(tmem + D + c0, o);
+      tmem_ld_wait32(o);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = w0 * v[k] + w1 * __uint_as_float(o[k]);
+    }
+  }
+};
+
 // Merges the pieces of a split unit: O = sum_s 2^(m_s - M) O_s /
 // sum_s 2^(m_s - M) l_s in piece order.  Both forms run once or twice in a
 // launch, at its end, and stay rolled: what such code costs besides its loads
@@ -549,13 +581,14 @@ struct Slots {
 // slot too, 16 columns at a time, took 28000 clocks of a 250-row unit.
 template <int D>
 __device__ void merge_rows(const ChunkArgs& a, const Piece& pc, int ur, int own, float m_own, float l_own,
-                           int bad, uint32_t tmem_o) {
+                           int bad, const OwnO<D>& o) {
   const Slots<D> sl(a, pc);
-  const bool live = ur < pc.rows;
-  const int row = min(ur, pc.rows - 1);
+  const int np = pc.npieces(), rows = pc.ntok * a.group;
+  const bool live = ur < rows;
+  const int row = min(ur, rows - 1);
   float M = m_own;
 #pragma unroll 2
-  for (int s = 0; s < pc.npieces; ++s) {
+  for (int s = 0; s < np; ++s) {
     if (s == own) continue;
     bad |= sl.flag(s);
     M = fmaxf(M, sl.ml(s, row).x);
@@ -569,19 +602,17 @@ __device__ void merge_rows(const ChunkArgs& a, const Piece& pc, int ur, int own,
 #pragma unroll
     for (int k = 0; k < 64; ++k) acc[k] = 0.0f;
 #pragma unroll 1
-    for (int s = 0; s < pc.npieces; ++s) {
+    for (int s = 0; s < np; ++s) {
       float x[64];
       float2 ml = make_float2(m_own, l_own);
       if (s == own) {
-        tmem_ld32(tmem_o + c0, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-        tmem_ld32(tmem_o + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-        tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-        tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) o.load(c0 + c, *reinterpret_cast<float(*)[32]>(&x[c]));
       } else {
         ml = sl.ml(s, row);
-        const float4* o4 = sl.o(s, row) + (c0 / 4) * pc.rows;
+        const float4* o4 = sl.o(s, row) + (c0 / 4) * rows;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) *reinterpret_cast<float4*>(&x[4 * k]) = __ldcg(o4 + k * pc.rows);
+        for (int k = 0; k < 16; ++k) *reinterpret_cast<float4*>(&x[4 * k]) = __ldcg(o4 + k * rows);
       }
       const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
       l += w * ml.y;
@@ -603,12 +634,13 @@ __device__ void merge_rows(const ChunkArgs& a, const Piece& pc, int ur, int own,
 template <int D>
 __device__ void merge_groups(const ChunkArgs& a, const Piece& pc, int ur, int step) {
   const Slots<D> sl(a, pc);
-  const int row = ur % pc.rows, sub = ur / pc.rows;
+  const int np = pc.npieces(), rows = pc.ntok * a.group;
+  const int row = ur % rows, sub = ur / rows;
   if (sub >= step) return;
   int bad = 0;
   float M = -INFINITY;
 #pragma unroll 4
-  for (int s = 0; s < pc.npieces; ++s) {
+  for (int s = 0; s < np; ++s) {
     bad |= sl.flag(s);
     M = fmaxf(M, sl.ml(s, row).x);
   }
@@ -618,9 +650,9 @@ __device__ void merge_groups(const ChunkArgs& a, const Piece& pc, int ur, int st
     float l = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int s = 0; s < pc.npieces; ++s) {
+    for (int s = 0; s < np; ++s) {
       const float2 ml = sl.ml(s, row);
-      const float4 o = __ldcg(sl.o(s, row) + d4 * pc.rows);
+      const float4 o = __ldcg(sl.o(s, row) + d4 * rows);
       const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
       l += w * ml.y;
       acc.x += w * o.x;
@@ -690,7 +722,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       mbar_init(&kempty[s], 2);  // one arrival per m-tile
     }
     for (int s = 0; s < kVStages; ++s) {
-      mbar_init(&vfull[s], 1);
+      mbar_init(&vfull[s], F8 ? 33 : 1);  // E4M3: and every lane's scales
       mbar_init(&vempty[s], F8 ? kConvThreads : 2);
     }
     if constexpr (F8) {
@@ -725,10 +757,10 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   const int g = a.group;
 
   // Progress kept across pieces and rounds (ring slots and barrier phases):
-  // g_tile, g_piece = K/V tiles and pieces of every earlier round; my_tiles,
-  // my_pieces and my_turns = the tiles and pieces of this role's m-tile and its
-  // turns so far (MMA and softmax).
-  int g_tile = 0, g_piece = 0, my_tiles = 0, my_pieces = 0, my_turns = 0;
+  // g_tile, g_piece = K/V tiles and pieces of every earlier round; my_tiles =
+  // the tiles of this softmax group so far; tiles0, tiles1 = the tiles of
+  // groups 0 and 1, and my_turns = the turns of this MMA thread.
+  int g_tile = 0, g_piece = 0, my_tiles = 0, tiles0 = 0, tiles1 = 0, my_turns = 0;
 
   // Each role runs the scheduling rounds in a loop of its own (its registers
   // are its own too).  A round: the softmax warps build the piece list, every
@@ -754,170 +786,104 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   };
   auto nothing = [](int) {};
 
-  if (warp >= kTmaWarp) {
+  if (warp >= kKWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shares<F8>::kOtherRegs));
-    if (warp == kTmaWarp) {
-      rounds(nothing, [&](int round, int npieces) {
-      // ------------------------------------------------------ TMA producer
-      // Lane 0 arms the slot's barrier, then lane u issues the box of page u
-      // of the tile.  K runs ahead of V: a K slot is free again once the last
-      // S of its tile is done, a V slot once the last P V is.
-      if (round == 0 && lane == 0) {
-        prefetch_tmap(&maps.q);
-        prefetch_tmap(&maps.k_pool);
-        prefetch_tmap(&maps.v_pool);
-      }
+    if (warp == kKWarp || warp == kVWarp) {
+      rounds(nothing, [&](int, int npieces) {
+      // ------------------------------------------------------ K producer, V and Q producer
+      // A tile: lane 0 arms the slot's barrier, then lane u issues the box of
+      // page u.  A K slot is free again once the last S of its tile is done, a
+      // V slot once the last P V is.  The next tile's block ids are read ahead.
+      // (One warp polling for both took 3300 clocks a tile, more than an E4M3
+      // tile has at the HBM rate.)
       constexpr int kPages = BN / 16;
       constexpr int kUnseen = INT_MIN;  // no row of the unit sees the page -> zeros
-      const bool page_lane = lane < kPages;
-      const int pool_pages = a.num_blocks * a.hkv;
-      int* blk_ring = reinterpret_cast<int*>(smem + Ly::kBlk);  // [tile & 7][page]
+      const bool is_v = warp == kVWarp;
+      const int stages = is_v ? kVStages : kStages;
+      uint64_t* full = is_v ? vfull : kfull;
+      uint64_t* empty = is_v ? vempty : kempty;
+      uint8_t* ring = smem + (is_v ? Ly::kVRing : Ly::kKRing);
+      const CUtensorMap* map = is_v ? &maps.v_pool : &maps.k_pool;
+      const float* scales = is_v ? a.v_scale : a.k_scale;
+      float* scl_ring = reinterpret_cast<float*>(smem + (is_v ? Ly::kVScl : Ly::kScl));
       volatile int* piece_bad = misc->piece_bad;
-      auto fetch_block = [&](int p, int t) -> int {
-        if (p >= npieces || !page_lane) return kUnseen;
+      bool ok = true;
+      int tau = g_tile;
+      int st = g_tile % stages, ph = (g_tile / stages) & 1;  // ring slot and phase of tile tau
+      int p = 0;
+      for (; p < npieces && ok; ++p) {
         const Piece& pc = pieces[p];
-        const int lp = (t < pc.st ? t : t + pc.skip) * kPages + lane;
-        const int k0 = lp * 16;
-        return k0 <= pc.hi && (k0 < a.sinks || k0 + 15 >= pc.lo)
-                   ? __ldg(a.block_table + static_cast<size_t>(pc.b) * a.max_blocks_per_seq + lp)
-                   : kUnseen;
-      };
-      // issues a tile (global tile tau) of piece p of tensor kv (0 = K, 1 = V)
-      auto issue = [&](int p, int tau, int kv, int blk) {
-        const Piece& pc = pieces[p];
-        const int st = kv ? tau % kVStages : tau % kStages;
-        uint64_t* bar = kv ? &vfull[st] : &kfull[st];
-        if (lane == 0) mbar_arrive_expect_tx(bar, Ly::kKTileBytes);
-        __syncwarp();
-        uint8_t* tile = smem + (kv ? Ly::kVRing : Ly::kKRing) + st * Ly::kKTileBytes;
-        const bool good = blk >= 0 && blk < a.num_blocks;
-        if (page_lane) {
-          const int page = good ? blk * a.hkv + pc.kvh : pool_pages;  // out of bounds: zero fill
-          if (!good && blk != kUnseen && kv == 0) {  // malformed block id: zeros, reported
+        const Extent ext = extent_of(a, pc.pos0);
+        const int t1 = pc.t1, hi = pc.hi(), kvh = pc.kvh;
+        const int32_t* table = a.block_table + static_cast<size_t>(pc.b) * a.max_blocks_per_seq;
+        auto fetch_block = [&](int t) -> int {
+          const int lp = ext.key_tile(t) * kPages + lane;
+          const int k0 = lp * 16;
+          return lane < kPages && t < t1 && k0 <= hi && (k0 < a.sinks || k0 + 15 >= ext.lo) ? __ldg(table + lp) : kUnseen;
+        };
+        int blk = fetch_block(pc.t0);
+        if (is_v) {
+          // Q (q_tokens tokens of g heads, rows past the unit are other tokens'
+          // or zeros and unused), once the S of the piece before are complete
+          const int n = g_piece + p;
+          ok = n == 0 || __all_sync(0xffffffffu, mbar_wait(q_empty, (n - 1) & 1, abort_flag));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full, Ly::kQLines * a.q_tokens * g * 128);
+            for (int l = 0; l < Ly::kQLines; ++l)
+              tma_load_3d(smem + Ly::kQ + l * Ly::kQLineBytes, &maps.q, q_full, l * 64, kvh * g, pc.tok0);
+          }
+          __syncwarp();
+        }
+        for (int t = pc.t0; t < t1; ++t) {
+          const int page_id = blk;
+          const bool good = page_id >= 0 && page_id < a.num_blocks;
+          const int page = good ? page_id * a.hkv + kvh : a.num_blocks * a.hkv;  // out of bounds: zero fill
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, abort_flag));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], Ly::kKTileBytes);
+          __syncwarp();
+          if (lane < kPages) {
+            uint8_t* dst = ring + st * Ly::kKTileBytes + lane * (Ly::kKTileBytes / kPages);
+            if constexpr (F8) {
+              tma_load_3d(dst, map, &full[st], 0, 0, page);
+            } else {
+              tma_load_5d(dst, map, &full[st], 0, 0, 0, 0, page);
+            }
+          }
+          blk = fetch_block(t + 1);
+          if constexpr (F8) {
+            // the tile's scales: lane u the keys 4u .. 4u+3 (page u / 4); 0
+            // where the page is not read.  K: slot tau % 8 with a barrier of its
+            // own (the softmax reads them later than the MMA the tile); V: with
+            // the tile.
+            const int from = __shfl_sync(0xffffffffu, good ? page : -1, lane >> 2);
+            const size_t idx = from >= 0 ? static_cast<size_t>(from) * 16 + (lane & 3) * 4 : 0;
+            cpa16_zfill(scl_ring + (is_v ? st : tau % kSclSlots) * BN + 4 * lane, scales + idx, from >= 0 ? 16 : 0);
+            cpa_arrive_noinc(is_v ? &vfull[st] : &sfull[tau % kSclSlots]);
+          }
+          if (!is_v && !good && page_id != kUnseen) {  // malformed block id: zeros, reported
             piece_bad[p] = 1;
             record_status(a.status, pc.b, kBadTree);
           }
-          const CUtensorMap* map = kv ? &maps.v_pool : &maps.k_pool;
-          if constexpr (F8) {
-            tma_load_3d(tile + lane * 2048, map, bar, 0, 0, page);
-          } else {
-            tma_load_5d(tile + lane * 2 * Ly::kGroupBytes, map, bar, 0, 0, 0, 0, page);
+          ++tau;
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1;
           }
         }
-        if constexpr (F8) {
-          if (kv == 0) {
-            // the tile's K and V scales into slot tau % 8: lane u the keys
-            // 4u .. 4u+3 (page u / 4); 0 where the page is not read
-            float* sc = reinterpret_cast<float*>(smem + Ly::kScl) + (tau % kSclSlots) * 2 * BN + 4 * lane;
-            const int pblk = __shfl_sync(0xffffffffu, blk, lane >> 2);
-            const bool read = pblk >= 0 && pblk < a.num_blocks;
-            const size_t idx = read ? (static_cast<size_t>(pblk) * a.hkv + pc.kvh) * 16 + (lane & 3) * 4 : 0;
-            cpa16_zfill(sc, a.k_scale + idx, read ? 16 : 0);
-            cpa16_zfill(sc + BN, a.v_scale + idx, read ? 16 : 0);
-            cpa_arrive_noinc(&sfull[tau % kSclSlots]);
-          }
-        }
-      };
-      auto advance = [&](int& p, int& t) {
-        if (++t >= pieces[p].t1) {
-          ++p;
-          if (p < npieces) t = pieces[p].t0;
-        }
-      };
-      // Q of piece p (q_tokens tokens of g heads, rows past the unit are other
-      // tokens' or zeros and unused), once the S of piece p - 1 are complete
-      auto issue_q = [&](int p) {
-        if (lane == 0) {
-          const Piece& pc = pieces[p];
-          mbar_arrive_expect_tx(q_full, Ly::kQLines * a.q_tokens * a.group * 128);
-          for (int l = 0; l < Ly::kQLines; ++l)
-            tma_load_3d(smem + Ly::kQ + l * Ly::kQLineBytes, &maps.q, q_full, l * 64, pc.kvh * a.group, pc.tok0);
-        }
-        __syncwarp();
-      };
-      int qp = 0;
-      int kp = 0, kt = pieces[0].t0, vp = 0, vt = pieces[0].t0;
-      int blk_k = fetch_block(kp, kt);  // the block ids of the next K tile, read ahead
-      int tk = g_tile, tv = g_tile;
-      bool ok = true;
-      unsigned long long t_idle = 0;
-      while (vp < npieces || qp < npieces) {
-        bool progressed = false;
-        if (qp < npieces) {
-          const int n = g_piece + qp;
-          int ready = lane == 0 ? (n == 0 || mbar_test_wait(q_empty, (n - 1) & 1)) : 0;
-          if (__shfl_sync(0xffffffffu, ready, 0)) {
-            issue_q(qp++);
-            progressed = true;
-          }
-        }
-        // V before K: the next P V needs its V tile before the S after it
-        // needs its K tile, and the copies of one warp land in issue order
-        if (tv < tk) {
-          int ready = lane == 0 ? mbar_test_wait(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1) : 0;
-          if (__shfl_sync(0xffffffffu, ready, 0)) {
-            issue(vp, tv, 1, page_lane ? blk_ring[(tv & 7) * 8 + lane] : kUnseen);
-            ++tv;
-            advance(vp, vt);
-            progressed = true;
-          }
-        }
-        if (kp < npieces) {
-          // a K tile only when no V copy could be issued now instead
-          int ready = 0;
-          if (lane == 0) {
-            const bool v_free = tv < tk && mbar_test_wait(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1);
-            ready = !v_free && mbar_test_wait(&kempty[tk % kStages], ((tk / kStages) & 1) ^ 1);
-          }
-          if (__shfl_sync(0xffffffffu, ready, 0)) {
-            if (page_lane) blk_ring[(tk & 7) * 8 + lane] = blk_k;
-            issue(kp, tk, 0, blk_k);
-            ++tk;
-            advance(kp, kt);
-            blk_k = fetch_block(kp, kt);
-            progressed = true;
-          }
-        }
-        int stop = 0;
-        if (!progressed && lane == 0) {
-          // sleep (at most about 200 ns) on the slot likely to free first
-          // instead of polling, which takes issue slots from the softmax
-          const bool k_next = kp < npieces;
-          const bool v_next = tv < tk;
-          if (v_next && (!k_next || tv - kVStages < tk - kStages))
-            mbar_try_wait_ns(&vempty[tv % kVStages], ((tv / kVStages) & 1) ^ 1, 200);
-          else if (k_next)
-            mbar_try_wait_ns(&kempty[tk % kStages], ((tk / kStages) & 1) ^ 1, 200);
-          else if (qp < npieces)
-            mbar_try_wait_ns(q_empty, (g_piece + qp - 1) & 1, 200);
-        }
-        if (lane == 0) {
-          if (progressed) {
-            t_idle = 0;
-          } else if (t_idle == 0) {
-            t_idle = global_ns();
-          } else if (global_ns() - t_idle > kWaitLimitNs || misc->abort) {
-            stop = 1;
-          }
-        }
-        if (__shfl_sync(0xffffffffu, stop, 0)) {
-          ok = false;
-          break;
-        }
+      }
+      if (!ok) {
+        misc->abort = 1;
+        if (lane == 0) record_status(a.status, pieces[min(p, npieces - 1)].b, kDeviceTimeout);
       }
       if constexpr (F8) cpa_wait_all();  // this lane's scale copies have landed
       if (lane == 0) {
-        if (!ok) {
-          record_status(a.status, pieces[min(min(vp, qp), npieces - 1)].b, kDeviceTimeout);
-          misc->abort = 1;
-        }
         // every issued copy has landed before the ring is reused or the CTA
-        // exits (at most a ring of each can still be in flight)
-        for (int t = max(g_tile, tk - kStages); t < tk; ++t)
-          mbar_wait(&kfull[t % kStages], (t / kStages) & 1);
-        for (int t = max(g_tile, tv - kVStages); t < tv; ++t)
-          mbar_wait(&vfull[t % kVStages], (t / kVStages) & 1);
-        if (qp > 0) mbar_wait(q_full, (g_piece + qp - 1) & 1);
+        // exits (at most a ring of them can still be in flight)
+        for (int t = max(g_tile, tau - stages); t < tau; ++t)
+          mbar_wait(&full[t % stages], (t / stages) & 1);
+        if (is_v && ok) mbar_wait(q_full, (g_piece + npieces - 1) & 1);
       }
       __syncwarp();
       });
@@ -937,15 +903,16 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         constexpr uint32_t kKRow8 = F8 ? 1024 : Ly::kGroupBytes;
         const uint64_t dk0 = smem_desc(smem_u32(smem + Ly::kKRing), 16, kKRow8);
         const uint64_t dv0 = smem_desc(smem_u32(smem + (F8 ? Ly::kV16 : Ly::kVRing)), 1024, Ly::kGroupBytes);
-        const uint64_t dq = smem_desc(smem_u32(smem + Ly::kQ + h * BM * 128), 16, 1024);
-        const uint32_t tmem_s = tmem + h * BN, tmem_o = tmem + 256 + h * D;
+        const uint64_t dq0 = smem_desc(smem_u32(smem + Ly::kQ), 16, 1024);
         uint64_t* vready = F8 ? v16full : vfull;  // V(t) as the P V reads it, and its release
         uint64_t* vdone = F8 ? v16empty : vempty;
         constexpr int kVSlots = F8 ? 2 : kVStages;
         auto k_wait = [&](int t) { return mbar_wait(&kfull[t % kStages], (t / kStages) & 1, abort_flag); };
         auto v_wait = [&](int t) { return mbar_wait(&vready[t % kVSlots], (t / kVSlots) & 1, abort_flag); };
-        auto issue_s = [&](int t) {  // S_h = Q_h K(t)^T
+        auto issue_s = [&](int x, int m, int t) {  // S_x = Q_m K(t)^T
           const uint64_t dk = dk0 + static_cast<uint64_t>((t % kStages) * (Ly::kKTileBytes >> 4));
+          const uint64_t dq = dq0 + static_cast<uint64_t>(m * (BM * 128 >> 4));
+          const uint32_t tmem_s = tmem + x * BN;
           if constexpr (F8) {
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row per MMA
@@ -958,19 +925,19 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
                           idesc_s, kk > 0 ? 1u : 0u);
             }
           }
-          mma_commit(&s_full[h]);
+          mma_commit(&s_full[x]);
         };
-        // O_h (+)= P_h V(t) over keys 64 half .. 64 half + 63
-        auto issue_pv = [&](int t, int half, bool acc) {
+        // O_x (+)= P_x V(t) over keys 64 half .. 64 half + 63
+        auto issue_pv = [&](int x, int t, int half, bool acc) {
           const uint64_t dv = dv0 + static_cast<uint64_t>((t % kVSlots) * (Ly::kTileBytes >> 4));
 #pragma unroll
           for (int k = 0; k < BN / 32; ++k) {
             const int kk = half * (BN / 32) + k;
-            mma_bf16_ts(tmem_o, tmem_s + kk * 8, dv + ((kk * 2 * Ly::kGroupBytes) >> 4), idesc_o,
-                        (acc || k > 0) ? 1u : 0u);
+            mma_bf16_ts(tmem + 256 + x * D, tmem + x * BN + kk * 8, dv + ((kk * 2 * Ly::kGroupBytes) >> 4),
+                        idesc_o, (acc || k > 0) ? 1u : 0u);
           }
         };
-        // turns are taken in units with both m-tiles, m-tile 0 first
+        // turns are taken in wide pieces, m-tile 0 first
         auto turn_wait = [&]() {
           const int n = my_turns - (h == 0 ? 1 : 0);
           return n < 0 || mbar_wait(&turn[h], n & 1, abort_flag);
@@ -979,53 +946,66 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           mbar_arrive(&turn[h ^ 1]);
           ++my_turns;
         };
+        auto count = [&](int T, bool narrow) {
+          tiles0 += narrow ? (T + 1) / 2 : T;
+          tiles1 += narrow ? T / 2 : T;
+        };
         bool ok = true;
         int tau = g_tile;
         for (int p = 0; p < npieces && ok; ++p) {
-          const int nm = pieces[p].rows > BM ? 2 : 1, T = pieces[p].t1 - pieces[p].t0;
-          if (h >= nm) {
-            // no rows of this m-tile: its arrivals keep the rings turning
-            ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag);
-            if (ok) mbar_arrive(q_empty);
+          const int T = pieces[p].t1 - pieces[p].t0;
+          const bool narrow = pieces[p].ntok * g <= BM;
+          ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag);
+          if (!ok) break;
+          if (narrow && h == 1) {
+            // warp 9 issues for both groups: these arrivals keep the rings turning
+            mbar_arrive(q_empty);
             for (int t = tau; t < tau + T && ok; ++t) {
               ok = k_wait(t);
               if (ok) mbar_arrive(&kempty[t % kStages]);
               ok = ok && v_wait(t);
               if (ok) mbar_arrive(&vdone[t % kVSlots]);
             }
+            count(T, true);
             tau += T;
             continue;
           }
-          // the piece's first S, once its Q is loaded and K has landed
-          ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag) && k_wait(tau);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(tau);
-          mma_commit(&kempty[tau % kStages]);
-          if (T == 1) mma_commit(q_empty);
-          for (int i = 0; i < T; ++i) {
-            const int t = tau + i;
-            const bool next = i + 1 < T;
+          // tile i goes to S_x, P_x and O_x: x = h, or in a narrow piece the
+          // tile's parity; the S of a tile is issued `ahead` tiles before its P V
+          const int ahead = narrow ? 2 : 1;
+          const int m = narrow ? 0 : h;
+          for (int i = 0; i < min(ahead, T) && ok; ++i) {
+            ok = k_wait(tau + i);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(narrow ? i : h, m, tau + i);
+            mma_commit(&kempty[(tau + i) % kStages]);
+          }
+          if (ok && T <= ahead) mma_commit(q_empty);
+          for (int i = 0; i < T && ok; ++i) {
+            const int t = tau + i, x = narrow ? i & 1 : h;
+            const bool next = i + ahead < T;
+            const int ph = ((x ? tiles1 : tiles0) + (narrow ? i >> 1 : i)) & 1;
             // everything but the second half of P before the turn
-            ok = v_wait(t) && (!next || k_wait(t + 1)) && mbar_wait(&p_a[h], my_tiles & 1, abort_flag) &&
-                 (nm == 1 || turn_wait());
+            ok = v_wait(t) && (!next || k_wait(t + ahead)) && mbar_wait(&p_a[x], ph, abort_flag) &&
+                 (narrow || turn_wait());
             if (!ok) break;
             tc_fence_after();
-            issue_pv(t, 0, i > 0);
-            ok = mbar_wait(&p_b[h], my_tiles & 1, abort_flag);
+            issue_pv(x, t, 0, i >= ahead);
+            ok = mbar_wait(&p_b[x], ph, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(t, 1, true);
-            if (next) issue_s(t + 1);
-            if (nm == 2) turn_pass();
-            ++my_tiles;
+            issue_pv(x, t, 1, true);
+            if (next) issue_s(x, m, t + ahead);
+            if (!narrow) turn_pass();
             mma_commit(&vdone[t % kVSlots]);
-            if (next) mma_commit(&kempty[(t + 1) % kStages]);
-            if (i + 2 == T) mma_commit(q_empty);
+            if (next) mma_commit(&kempty[(t + ahead) % kStages]);
+            if (i + 1 + ahead == T) mma_commit(q_empty);
           }
           if (!ok) break;
           mma_commit(&o_done[h]);
-          ++my_pieces;
+          if (narrow) mma_commit(&o_done[1]);
+          count(T, narrow);
           tau += T;
         }
         if (!ok) {
@@ -1048,27 +1028,28 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       // (their codes may be stale).
       if (F8 && warp >= kConvWarp) {
         const int ct = tid - kConvWarp * 32;  // 0 .. 127
-        const float* scl = reinterpret_cast<const float*>(smem + Ly::kScl);
+        const float* scl = reinterpret_cast<const float*>(smem + Ly::kVScl);
         bool ok = true;
         int tau = g_tile;
         for (int p = 0; p < npieces; ++p) {
           const Piece& pc = pieces[p];
+          const Extent ext = extent_of(a, pc.pos0);
+          const int hi = pc.hi();
           for (int t = pc.t0; t < pc.t1; ++t, ++tau) {
             const int vs = tau % kVStages;
             if (ok) ok = mbar_wait(&vfull[vs], (tau / kVStages) & 1, abort_flag);
-            if (ok) ok = mbar_wait(&sfull[tau % kSclSlots], (tau / kSclSlots) & 1, abort_flag);
             if (ok && tau >= 2) ok = mbar_wait(&v16empty[tau & 1], ((tau - 2) >> 1) & 1, abort_flag);
             if (!ok) {
               misc->abort = 1;
             } else {
-              const float* sv = scl + (tau % kSclSlots) * 2 * BN + BN;
+              const float* sv = scl + vs * BN;
               // thread ct: the 16 codes of columns 16c .. 16c+15 (c = ct % 8)
               // of keys k0 + 8i, k0 = (ct / 8) % 8, i = 8 (ct / 64) .. + 7.  Raw:
               // 128 bytes a key, 16-byte chunk c at chunk c ^ (key % 8); fp16:
               // [8-key group][64-column half][key][128 B], 16-byte chunk q of a
               // line at chunk q ^ (key % 8).  key % 8 = k0 for every i.
               const int k0 = (ct >> 3) & 7, c = ct & 7, i0 = (ct >> 6) * 8;
-              const int key0 = (t < pc.st ? t : t + pc.skip) * BN + k0;
+              const int key0 = ext.key_tile(t) * BN + k0;
               const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + k0 * 128 + ((c ^ k0) << 4);
               uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (c >> 2) * 1024 + k0 * 128;
               const int q0 = (((2 * c) & 7) ^ k0) << 4, q1 = (((2 * c + 1) & 7) ^ k0) << 4;
@@ -1076,7 +1057,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               for (int i = i0; i < i0 + 8; ++i) {
                 const int key = key0 + 8 * i;
                 uint32_t h[8];
-                if (key <= pc.hi && (key < a.sinks || key >= pc.lo)) {
+                if (key <= hi && (key < a.sinks || key >= ext.lo)) {
                   const uint4 w = *reinterpret_cast<const uint4*>(raw + i * 1024);
                   const float s1 = sv[k0 + 8 * i];
                   const float2 s2 = make_float2(s1, s1);
@@ -1127,13 +1108,12 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       for (int p = 0; p < npieces; ++p) {
         const Piece& pc = pieces[p];
         const int T = pc.t1 - pc.t0;
-        const int nm = pc.rows > BM ? 2 : 1;
-        if (h >= nm) {  // this m-tile has no rows in the unit
-          tau += T;
-          continue;
-        }
-        const int ur = h * BM + r;                 // row of the unit
-        const bool live = ur < pc.rows;
+        const int rows = pc.ntok * g;
+        // a narrow piece has one m-tile: group h takes every second key tile of
+        // its rows, from tile h on, and group 0 joins the two results
+        const bool narrow = rows <= BM;
+        const int ur = narrow ? r : h * BM + r;    // row of the unit
+        const bool live = ur < rows;
         const int tok = live ? ur / g : 0;
         const int pos = pc.pos0 + tok;             // position of this row
         const size_t q_row = static_cast<size_t>(pc.tok0 + tok);
@@ -1146,10 +1126,12 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
 
         float m_run = -INFINITY;  // running max (log2 units)
         float l_run = 0.0f;       // row sum against m_run
-        const int t0 = pc.t0, st = pc.st, skip = pc.skip, lo = pc.lo, hi = pc.hi, pos0 = pc.pos0;
-        for (int i = 0; i < T; ++i) {
-          const int k0 = (t0 + i < st ? t0 + i : t0 + i + skip) * BN;  // first key of the tile
-          const int gt = tau + i;                                      // global tile (ring slot)
+        const Extent ext = extent_of(a, pc.pos0);
+        const int t0 = pc.t0, lo = ext.lo, hi = pc.hi(), pos0 = pc.pos0;
+        const int first = narrow ? h : 0, every = narrow ? 2 : 1;
+        for (int i = first; i < T; i += every) {
+          const int k0 = ext.key_tile(t0 + i) * BN;  // first key of the tile
+          const int gt = tau + i;                    // global tile (ring slot)
           // some row of the unit does not see some key of the tile
           const bool masked = k0 + BN - 1 > pos0 || (a.window > 0 && hi - a.window >= k0 && k0 + BN > a.sinks);
           // keys that no row of the unit sees: their V rows are cleared
@@ -1193,7 +1175,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
             float* y = x + 32 * c;
             if constexpr (F8) {
-              const float* sk = reinterpret_cast<const float*>(smem + Ly::kScl) + (gt % kSclSlots) * 2 * BN + 32 * c;
+              const float* sk = reinterpret_cast<const float*>(smem + Ly::kScl) + (gt % kSclSlots) * BN + 32 * c;
 #pragma unroll
               for (int k = 0; k < 32; k += 4) {
                 const float4 s4 = *reinterpret_cast<const float4*>(sk + k);
@@ -1234,7 +1216,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             // (S_h(t), which this thread has seen complete, was issued after it)
             // (the piece's first P V overwrites O)
 #pragma unroll 1
-            for (int c0 = 0; i > 0 && c0 < D; c0 += 16) {
+            for (int c0 = 0; i > first && c0 < D; c0 += 16) {
               uint32_t o[16];
               tmem_ld16(tmem_o + c0, o);
 #pragma unroll
@@ -1281,30 +1263,47 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         // -------------------------------------------------- piece epilogue
         bool done = false;
         if (ok) {
-          done = __all_sync(0xffffffffu, mbar_wait(&o_done[h], my_pieces & 1, abort_flag));
+          done = mbar_wait(&o_done[h], (g_piece + p) & 1, abort_flag);
+          if (narrow && h == 0) done = done && mbar_wait(&o_done[1], (g_piece + p) & 1, abort_flag);
+          done = __all_sync(0xffffffffu, done);
           if (!done) {
             ok = false;
             misc->abort = 1;
             record_status(a.status, pc.b, kDeviceTimeout);
           }
         }
-        ++my_pieces;
         const bool bad = piece_bad[p] != 0;
         tc_fence_after();
-        if (pc.slot < 0) {
+        OwnO<D> own_o = {tmem_o, false, 1.0f, 0.0f};
+        if (narrow) {
+          // join: weights against the larger maximum, as in a merge
+          float2* xch = reinterpret_cast<float2*>(smem + Ly::kXch);
+          if (h == 1) xch[r] = make_float2(m_run, l_run);
+          named_sync(kBarPair, kSoftmaxThreads);
+          if (h == 0 && T > 1) {
+            const float2 other = xch[r];
+            const float M = fmaxf(m_run, other.x);
+            own_o.two = true;
+            own_o.w0 = m_run == -INFINITY ? 0.0f : exp2f(m_run - M);
+            own_o.w1 = other.x == -INFINITY ? 0.0f : exp2f(other.x - M);
+            l_run = own_o.w0 * l_run + own_o.w1 * other.y;
+            m_run = M;
+          }
+        }
+        if (narrow && h == 1) {
+          // (group 0 writes)
+        } else if (pc.npieces() == 1) {
           // the whole unit: normalise and write
-          // (rolled, as everything that runs once a piece: see merge_unit)
+          // (rolled, as everything that runs once a piece: see merge_rows)
           const float inv_l = l_run > 0.0f ? 1.0f / l_run : 0.0f;
           if (done) {
             const QuadRows quad = quad_rows<D>(a, q_row * a.hq + head, live);
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(tmem_o + c0, o);
-              tmem_ld_wait32(o);
               float v[32];
+              own_o.load(c0, v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = bad ? 0.0f : __uint_as_float(o[k]) * inv_l;
+              for (int k = 0; k < 32; ++k) v[k] = bad ? 0.0f : v[k] * inv_l;
               store_rows32(a, quad, c0, v);
             }
           }
@@ -1313,29 +1312,26 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           // finds every other one done merges straight from TMEM.  Otherwise
           // raw O and (m, l) go to its slot and it takes a ticket; the last to
           // take one merges.
-          const int nthr = nm * BM;
-          const int bar = nm == 2 ? kBarPair : kBarGroup0;
-          const int step = nthr / pc.rows;
+          const int nthr = narrow ? BM : kSoftmaxThreads;
+          const int bar = narrow ? kBarGroup0 : kBarPair;
+          const int step = nthr / rows;
           const int flag = (bad || !done) ? 1 : 0;
-          int* ticket = a.counters + pc.vfirst;
-          if (ur == 0) misc->merge = step == 1 && *static_cast<volatile int*>(ticket) == pc.npieces - 1;
+          int* ticket = a.counters + pc.vfirst();
+          if (ur == 0) misc->merge = step == 1 && *static_cast<volatile int*>(ticket) == pc.npieces() - 1;
           named_sync(bar, nthr);
           bool merge = misc->merge;
           if (!merge) {
-            uint8_t* slot = a.slots + static_cast<size_t>(pc.slot) * Sl::kBytes;
+            uint8_t* slot = a.slots + static_cast<size_t>(pc.slot()) * Sl::kBytes;
             float4* so4 = reinterpret_cast<float4*>(slot + Sl::kO) + ur;
             if (done) {  // (otherwise the flag voids the slot)
 #pragma unroll 1
               for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld32(tmem_o + c0, o);
-                tmem_ld_wait32(o);
+                float v[32];
+                own_o.load(c0, v);
                 if (live) {
 #pragma unroll
                   for (int k = 0; k < 8; ++k)
-                    __stcg(so4 + (c0 / 4 + k) * pc.rows,
-                           make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                       __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
+                    __stcg(so4 + (c0 / 4 + k) * rows, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
                 }
               }
             }
@@ -1343,20 +1339,21 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             if (ur == 0) __stcg(reinterpret_cast<int*>(slot + Sl::kFlag), flag);
             __threadfence();
             named_sync(bar, nthr);
-            if (ur == 0) misc->merge = atomicAdd(ticket, 1) == pc.npieces - 1;
+            if (ur == 0) misc->merge = atomicAdd(ticket, 1) == pc.npieces() - 1;
             named_sync(bar, nthr);
             merge = misc->merge;
           }
           if (merge) {
             __threadfence();
             if (step == 1) {
-              merge_rows<D>(a, pc, ur, static_cast<int>(blockIdx.x) - pc.vfirst, m_run, l_run, flag, tmem_o);
+              merge_rows<D>(a, pc, ur, static_cast<int>(blockIdx.x) - pc.vfirst(), m_run, l_run, flag, own_o);
             } else {
               merge_groups<D>(a, pc, ur, step);
             }
           }
           named_sync(bar, nthr);  // misc->merge is rewritten by the next split piece
         }
+        if (narrow) named_sync(kBarPair, kSoftmaxThreads);  // O_1 and the exchange area are read
         tc_fence_before();
         tau += T;
       }
