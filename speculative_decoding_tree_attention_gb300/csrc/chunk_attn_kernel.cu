@@ -50,7 +50,8 @@
 //
 // Precision.  S, the softmax and O are fp32.  P is rounded to the 16-bit type
 // of V for the P V product (bf16; fp16 for an E4M3 cache) and the row sum adds
-// the rounded values, so that O / l weights V exactly as the product did.
+// the rounded values, so that O / l weights V exactly as the product did.  An
+// E4M3 V row is rounded twice on its way to fp16 (its scale, the product).
 #include <climits>
 
 #include "tv_device.cuh"
@@ -209,6 +210,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Bits 0 .. n-1 of a 32-bit word (none for n <= 0, all for n >= 32).
@@ -1022,9 +1029,10 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
     } else {
       rounds(nothing, [&](int, int npieces) {
       // ------------------------------------------------------ V conversion (E4M3)
-      // Per tile: each key's row as fp16 of code x V scale (one rounding of
-      // the exact product) into converted slot t % 2, in the MN-major layout
-      // the P V MMA reads.  Keys that no row of the unit sees get zero rows
+      // Per tile: each key's row as code x V scale in fp16 (the scale and the
+      // product rounded once each) into converted slot t % 2, in the MN-major
+      // layout the P V MMA reads.  In fp16, not through fp32: 24 instructions
+      // for 16 codes instead of 40, and the converter sets an E4M3 tile's pace.  Keys that no row of the unit sees get zero rows
       // (their codes may be stale).
       if (F8 && warp >= kConvWarp) {
         const int ct = tid - kConvWarp * 32;  // 0 .. 127
@@ -1059,18 +1067,20 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
                 uint32_t h[8];
                 if (key <= hi && (key < a.sinks || key >= ext.lo)) {
                   const uint4 w = *reinterpret_cast<const uint4*>(raw + i * 1024);
-                  const float s1 = sv[k0 + 8 * i];
-                  const float2 s2 = make_float2(s1, s1);
                   const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                  // code x fp16(scale x 2^7), then x 2^-7 (scales of 1 and
+                  // more as they are): the scale keeps its 11 bits down to
+                  // 2^-21 and the product stays in range
+                  const float s = sv[k0 + 8 * i];
+                  const bool small = s < 1.0f;
+                  const uint32_t s2 = pack_f16x2(small ? s * 128.0f : s, small ? s * 128.0f : s);
+                  const uint32_t back = small ? 0x20002000u : 0x3c003c00u;  // 2^-7 or 1
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
-                    // codes -> fp16 (exact) -> fp32, times the scale, -> fp16
                     uint32_t c01, c23;
-                    e4m3x4_to_f16x2x2(ww[k], c01, c23);
-                    const float2 v01 = mul2(unpack_f16x2(c01), s2);
-                    const float2 v23 = mul2(unpack_f16x2(c23), s2);
-                    h[2 * k] = pack_f16x2(v01.x, v01.y);
-                    h[2 * k + 1] = pack_f16x2(v23.x, v23.y);
+                    e4m3x4_to_f16x2x2(ww[k], c01, c23);  // exact
+                    h[2 * k] = mul_f16x2(mul_f16x2(c01, s2), back);
+                    h[2 * k + 1] = mul_f16x2(mul_f16x2(c23, s2), back);
                   }
                 } else {
 #pragma unroll
@@ -1114,6 +1124,9 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         const bool narrow = rows <= BM;
         const int ur = narrow ? r : h * BM + r;    // row of the unit
         const bool live = ur < rows;
+        // a warp without live rows only keeps the barriers turning (what its
+        // rows of P and O hold is not used): a decode token fills one warp
+        const bool idle = ur - lane >= rows;
         const int tok = live ? ur / g : 0;
         const int pos = pc.pos0 + tok;             // position of this row
         const size_t q_row = static_cast<size_t>(pc.tok0 + tok);
@@ -1159,7 +1172,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             if (!ok) misc->abort = 1;
           }
           ++my_tiles;
-          if (!ok) {
+          if (!ok || idle) {
             mbar_arrive(&p_a[h]);
             mbar_arrive(&p_b[h]);
             continue;

@@ -5,8 +5,8 @@ error is below 1e-5 of the row's largest |v| at these lengths).  Each weight
 P is rounded to 16 bits once, by at most u = eps/2 of itself (bf16 2^-8, fp16
 2^-11), and the row sum adds the rounded weights, so an fp32 output moves by
 at most 2 u max|v| over the keys of the row (u from the numerator, u from the
-sum).  An E4M3 cache adds one fp16 rounding of each v (2^-11) and P in fp16:
-3 x 2^-11 max|v|.  The bf16 output is the fp32 one rounded once (checked bit
+sum).  An E4M3 cache adds two fp16 roundings of each v (its scale, the
+product; 2^-11 each) to the two of P in fp16: 4 x 2^-11 max|v|.  The bf16 output is the fp32 one rounded once (checked bit
 for bit)."""
 import numpy as np
 import pytest
@@ -95,7 +95,7 @@ def check(got, c, u, window=0, sinks=0, scale=None):
 
 
 U_BF16 = 2 * 2.0 ** -8
-U_FP8 = 3 * 2.0 ** -11
+U_FP8 = 4 * 2.0 ** -11
 
 SHAPES = [
     # lens, chunks, hq, hkv, d
