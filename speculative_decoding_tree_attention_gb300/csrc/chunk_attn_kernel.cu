@@ -1050,45 +1050,39 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             if (!ok) {
               misc->abort = 1;
             } else {
-              const float* sv = scl + vs * BN;
-              // thread ct: the 16 codes of columns 16c .. 16c+15 (c = ct % 8)
-              // of keys k0 + 8i, k0 = (ct / 8) % 8, i = 8 (ct / 64) .. + 7.  Raw:
-              // 128 bytes a key, 16-byte chunk c at chunk c ^ (key % 8); fp16:
-              // [8-key group][64-column half][key][128 B], 16-byte chunk q of a
-              // line at chunk q ^ (key % 8).  key % 8 = k0 for every i.
-              const int k0 = (ct >> 3) & 7, c = ct & 7, i0 = (ct >> 6) * 8;
-              const int key0 = ext.key_tile(t) * BN + k0;
-              const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + k0 * 128 + ((c ^ k0) << 4);
-              uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (c >> 2) * 1024 + k0 * 128;
-              const int q0 = (((2 * c) & 7) ^ k0) << 4, q1 = (((2 * c + 1) & 7) ^ k0) << 4;
+              // thread ct: key ct of the tile.  Raw: 128 bytes a key, 16-byte
+              // chunk c at chunk c ^ (key % 8); fp16: [8-key group][64-column
+              // half][key][128 B], 16-byte chunk q of a line at q ^ (key % 8):
+              // eight neighbouring lanes touch all banks once on either side.
+              const int key = ext.key_tile(t) * BN + ct;
+              const bool seen = key <= hi && (key < a.sinks || key >= ext.lo);
+              // code x fp16(scale x 2^7), then x 2^-7 (scales of 1 and more as
+              // they are): the scale keeps its 11 bits down to 2^-21 and the
+              // product stays in range
+              const float s = scl[vs * BN + ct];
+              const bool small = s < 1.0f;
+              const uint32_t s2 = pack_f16x2(small ? s * 128.0f : s, small ? s * 128.0f : s);
+              const uint32_t back = small ? 0x20002000u : 0x3c003c00u;  // 2^-7 or 1
+              const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + ct * 128;
+              uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (ct >> 3) * Ly::kGroupBytes + (ct & 7) * 128;
+              const int sw = (ct & 7) << 4;
+              // rolled: 91 us on four 32768-token decodes, 97 and 112 us unrolled by
+              // 4 and 8 (the kernel's loops share one instruction cache)
 #pragma unroll 1
-              for (int i = i0; i < i0 + 8; ++i) {
-                const int key = key0 + 8 * i;
+              for (int c = 0; c < 8; ++c) {
                 uint32_t h[8];
-                if (key <= hi && (key < a.sinks || key >= ext.lo)) {
-                  const uint4 w = *reinterpret_cast<const uint4*>(raw + i * 1024);
-                  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-                  // code x fp16(scale x 2^7), then x 2^-7 (scales of 1 and
-                  // more as they are): the scale keeps its 11 bits down to
-                  // 2^-21 and the product stays in range
-                  const float s = sv[k0 + 8 * i];
-                  const bool small = s < 1.0f;
-                  const uint32_t s2 = pack_f16x2(small ? s * 128.0f : s, small ? s * 128.0f : s);
-                  const uint32_t back = small ? 0x20002000u : 0x3c003c00u;  // 2^-7 or 1
+                const uint4 w = *reinterpret_cast<const uint4*>(raw + ((c << 4) ^ sw));
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    uint32_t c01, c23;
-                    e4m3x4_to_f16x2x2(ww[k], c01, c23);  // exact
-                    h[2 * k] = mul_f16x2(mul_f16x2(c01, s2), back);
-                    h[2 * k + 1] = mul_f16x2(mul_f16x2(c23, s2), back);
-                  }
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) h[k] = 0u;
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t c01, c23;
+                  e4m3x4_to_f16x2x2(ww[k], c01, c23);  // exact
+                  h[2 * k] = seen ? mul_f16x2(mul_f16x2(c01, s2), back) : 0u;
+                  h[2 * k + 1] = seen ? mul_f16x2(mul_f16x2(c23, s2), back) : 0u;
                 }
-                uint8_t* dst = v16 + i * Ly::kGroupBytes;
-                *reinterpret_cast<uint4*>(dst + q0) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(dst + q1) = make_uint4(h[4], h[5], h[6], h[7]);
+                uint8_t* line = v16 + (c >> 2) * 1024;
+                *reinterpret_cast<uint4*>(line + ((((2 * c) & 7) << 4) ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(line + ((((2 * c + 1) & 7) << 4) ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
               }
               fence_proxy_async_smem();  // generic writes, read by the MMA
             }
