@@ -505,6 +505,137 @@ int tv_chunk_attention_fp8(const tv_chunk_params* params, const uint8_t* q, cons
                            int32_t* status, void* workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
+/* ========================================================================
+ * Writing new K/V rows into the paged cache, and reading an E4M3 cache back.
+ *
+ * Token i of sequence b's chunk (rows token_offsets[b] + i, 0 <= i < C_b =
+ * token_offsets[b+1] - token_offsets[b]) belongs at position
+ * pos = seq_lens[b] - C_b + i: seq_lens counts the chunk in, as for the chunk
+ * attention that follows.  Its rows of every KV head go to row pos % 16 of page
+ * block_table[b][pos / 16].
+ *   tv_append_kv       copies bf16 rows.
+ *   tv_append_kv_fp8   quantises each row of D values: scale s = fl32(max|x| /
+ *                      448) over its finite entries, at least 2^-126, 1 for a
+ *                      row of zeros; code = the E4M3 value nearest to the real
+ *                      quotient x / s, ties to even, magnitudes above 448 (an
+ *                      infinity) saturating, NaN as 0x7F.  The cache that
+ *                      tv_tree_attention_fp8 and tv_chunk_attention_fp8 read.
+ *   tv_read_kv_fp8     the other way: bf16 rows code x scale (the fp32 product,
+ *                      rounded to nearest even).
+ * status[b]: TV_OK, also for an empty chunk; TV_ERR_BAD_TREE if seq_lens[b] <
+ * C_b, and for every sequence if token_offsets is not non-decreasing within
+ * [0, total_tokens]; TV_ERR_NO_PAGE if a position of the chunk has no page
+ * (block id < 0 or >= num_blocks, or past max_blocks_per_seq).  Of a failed
+ * sequence nothing is written (an append) or its rows read as zeros (a read;
+ * with malformed token_offsets nothing is written).  Rows past
+ * token_offsets[batch] and pool rows of other positions are left as they were.
+ * Two tokens must not share a pool row: the block tables of sequences that
+ * append do not overlap at the appended positions.
+ * ====================================================================== */
+typedef struct {
+  int32_t batch;              /* B >= 1                                      */
+  int32_t num_kv_heads;       /* Hkv                                         */
+  int32_t head_dim;           /* D: 64 or 128                                */
+  int32_t block_size;         /* must be TV_BLOCK_SIZE (16)                  */
+  int32_t max_blocks_per_seq; /* row stride of block_table                   */
+  int32_t num_blocks;         /* pages in the pool                           */
+  int32_t total_tokens;       /* rows, >= token_offsets[batch] (host copy);
+                                 0: only status is written                   */
+  int64_t kv_stride;          /* elements between the rows of k_new and v_new
+                                 (k_out, v_out), 0 => Hkv*D; a multiple of 8 */
+} tv_cache_params;            /* host struct */
+
+/* Layouts: k_new, v_new, k_out, v_out bf16 [total_tokens][Hkv][D] (rows
+ * kv_stride apart: slices of a fused projection); pools bf16 or u8
+ * [num_blocks][Hkv][16][D]; scales fp32 [num_blocks][Hkv][16]; block_table
+ * int32 [batch][max_blocks_per_seq]; seq_lens int32 [batch]; token_offsets
+ * int32 [batch+1]; status int32 [batch].  Device pointers 16-byte aligned. */
+int tv_append_kv(const tv_cache_params* params, const uint16_t* k_new, const uint16_t* v_new,
+                 const int32_t* block_table, const int32_t* seq_lens,
+                 const int32_t* token_offsets, uint16_t* k_pool, uint16_t* v_pool,
+                 int32_t* status, cudaStream_t stream);
+int tv_append_kv_fp8(const tv_cache_params* params, const uint16_t* k_new, const uint16_t* v_new,
+                     const int32_t* block_table, const int32_t* seq_lens,
+                     const int32_t* token_offsets, uint8_t* k_pool, float* k_scale,
+                     uint8_t* v_pool, float* v_scale, int32_t* status, cudaStream_t stream);
+int tv_read_kv_fp8(const tv_cache_params* params, const uint8_t* k_pool, const float* k_scale,
+                   const uint8_t* v_pool, const float* v_scale, const int32_t* block_table,
+                   const int32_t* seq_lens, const int32_t* token_offsets, uint16_t* k_out,
+                   uint16_t* v_out, int32_t* status, cudaStream_t stream);
+
+/* Plain rows to E4M3 codes and scales, by the same rule: queries and tree K/V
+ * for the E4M3 attentions.  x bf16 [tokens][heads][head_dim], tokens `stride`
+ * elements apart (0 => heads*head_dim; a multiple of 8); codes u8
+ * [tokens][heads][head_dim]; scale fp32 [tokens][heads].  head_dim 64 or 128
+ * (TV_ERR_UNSUPPORTED otherwise); tokens 0 enqueues nothing. */
+typedef struct {
+  int32_t tokens, heads, head_dim;
+  int64_t stride;
+} tv_quant_params; /* host struct */
+int tv_quantize_rows(const tv_quant_params* params, const uint16_t* x, uint8_t* codes,
+                     float* scale, cudaStream_t stream);
+
+/* tv_commit_kv of an E4M3 cache: codes and scales of the root and the accepted
+ * nodes (as tv_tree_attention_fp8 took them) are copied to the pool.  Same
+ * semantics, layouts of the index arrays and status codes. */
+int tv_commit_kv_fp8(const tv_commit_params* params, const uint8_t* k_nodes,
+                     const float* k_nodes_scale, const uint8_t* v_nodes,
+                     const float* v_nodes_scale, const int32_t* parent,
+                     const int32_t* node_offsets, const int32_t* accepted_len,
+                     const int32_t* path, const int32_t* block_table, const int32_t* prefix_lens,
+                     uint8_t* k_prefix_blocks, float* k_prefix_scale, uint8_t* v_prefix_blocks,
+                     float* v_prefix_scale, int32_t* new_prefix_lens, int32_t* status,
+                     cudaStream_t stream);
+
+/* ========================================================================
+ * Penalties for repeated tokens, biases and grammar masks on the target logits
+ * of the tree nodes, ahead of tv_accept with TV_INPUT_LOGITS.
+ *
+ * Row i of tree b holds the logits after node i.  Counted against it are the
+ * sequence's history and the drafted tokens on the path root .. i (node i's own
+ * included, the root's not: it is the last committed token, part of the
+ * history).  With c(v) = the occurrences of v in the history past the first
+ * prompt_lens[b] tokens and on the path, and seen(v) = c(v) > 0 or v among the
+ * first prompt_lens[b] tokens, in this order and each step rounded to fp32:
+ *   seen(v):   x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *              x = x - frequency[b] * c(v)
+ *   c(v) > 0:  x = x - presence[b]
+ *              x = x + bias of v (of an id listed twice the last entry holds)
+ *   bit v % 32 of word v / 32 of the row's allowed_mask clear: x = -inf
+ * A row whose mask allows nothing is all -inf.  Ids outside [0, V), in the
+ * history, the bias list or the tree, count for nothing.
+ * A sequence with a malformed tree, history or bias extent, or a rate that is
+ * not finite (a repetition not positive), gets TV_ERR_BAD_TREE and its rows
+ * unchanged (as far as they can be addressed).
+ * ====================================================================== */
+typedef struct {
+  int32_t batch;         /* 1 <= B <= 65535                                */
+  int32_t vocab;         /* V, 1 <= V < 2^18                               */
+  int32_t max_nodes;     /* >= every N_b, <= TV_MAX_NODES                  */
+  int32_t total_nodes;   /* node_offsets[batch] (host copy)                */
+  int32_t total_history; /* entries of history                             */
+  int32_t total_bias;    /* entries of bias_ids and bias_values            */
+  int32_t logits_dtype;  /* tv_out_dtype of `logits`: bf16 (0) or fp32 (1) */
+} tv_penalty_params;     /* host struct */
+
+/* Layouts: logits bf16 or fp32 [total_nodes][V]; draft_tokens, parent,
+ * node_offsets as for tv_accept; history int32 [total_history] with
+ * history_offsets int32 [batch+1], or both NULL; prompt_lens int32 [batch] or
+ * NULL (0: all history is generated); repetition, presence, frequency fp32
+ * [batch] or NULL (1, 0, 0); bias_ids int32 and bias_values fp32 [total_bias]
+ * with bias_offsets int32 [batch+1], or NULL; allowed_mask uint32
+ * [total_nodes][ceil(V/32)] or NULL; out fp32 [total_nodes][V], which may be
+ * the fp32 logits themselves (in place) and otherwise does not overlap them;
+ * status int32 [batch].  Device pointers 16-byte aligned. */
+int tv_penalize_logits(const tv_penalty_params* params, const void* logits,
+                       const int32_t* draft_tokens, const int32_t* parent,
+                       const int32_t* node_offsets, const int32_t* history,
+                       const int32_t* history_offsets, const int32_t* prompt_lens,
+                       const float* repetition, const float* presence, const float* frequency,
+                       const int32_t* bias_ids, const float* bias_values,
+                       const int32_t* bias_offsets, const uint32_t* allowed_mask, float* out,
+                       int32_t* status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

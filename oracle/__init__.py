@@ -327,3 +327,93 @@ def chunk_attention(q, k_pool, v_pool, block_table, seq_lens, token_offsets, win
                 w = np.exp(s - s.max())
                 out[r0 + i, h] = w @ v_pool[blk, h // g, at] / w.sum()
     return out
+
+
+# ------------------------------------------------------------------ cache writes and reads
+def quantize_rows(x):
+    """(codes, scale) of real rows [..., D], from the definition: scale =
+    fl32(max|finite x| / 448), at least 2^-126, 1 for a row of zeros; the code
+    of the E4M3 value nearest to x / scale (ties to the even code), saturating,
+    NaN as 0x7F.  x / scale is compared with the middle of two values as x with
+    scale times it: exact, a product of 24 by 5 bits."""
+    x = np.asarray(x, np.float64)
+    mag = np.where(np.isfinite(x), np.abs(x), 0.0).max(-1)
+    with np.errstate(over="ignore"):
+        scale = np.where(mag > 0, np.maximum((mag.astype(np.float32) / np.float32(448)), np.float32(2.0 ** -126)),
+                         np.float32(1)).astype(np.float32)
+    value = e4m3_table()[:127]
+    codes = np.empty(x.shape, np.uint8)
+    for i in np.ndindex(x.shape[:-1]):
+        s = float(scale[i])
+        middle = (value[:-1] + value[1:]) / 2 * s
+        a = np.abs(x[i])
+        lo = np.searchsorted(middle, a, side="left")    # ties down
+        hi = np.searchsorted(middle, a, side="right")   # ties up
+        c = np.where(lo % 2 == 0, lo, hi)
+        c = np.where(np.signbit(x[i]), c | 0x80, c)
+        codes[i] = np.where(np.isnan(x[i]), 0x7F, c)
+    return codes, scale
+
+
+def cache_places(block_table, seq_lens, token_offsets, num_blocks, total):
+    """(status per sequence, {row: (block, position % 16)}, rows of failed
+    sequences) of the chunks' tokens."""
+    off = [int(o) for o in token_offsets]
+    B = len(off) - 1
+    if off[0] < 0 or any(b < a for a, b in zip(off, off[1:])) or off[-1] > total:
+        return np.full(B, 5, np.int32), {}, []
+    status, places, failed = np.zeros(B, np.int32), {}, []
+    for b in range(B):
+        c, n = off[b + 1] - off[b], int(seq_lens[b])
+        if c == 0:
+            continue
+        pos = range(n - c, n)
+        blocks = [int(block_table[b][p // 16]) if 0 <= p // 16 < len(block_table[b]) else -1 for p in pos] if n >= c else []
+        if n < c:
+            status[b] = 5
+        elif any(k < 0 or k >= num_blocks for k in blocks):
+            status[b] = 7
+        rows = range(off[b], off[b + 1])
+        if status[b]:
+            failed += list(rows)
+        else:
+            places.update({r: (k, p % 16) for r, k, p in zip(rows, blocks, pos)})
+    return status, places, failed
+
+
+# ------------------------------------------------------------------ penalties
+def penalize_logits(logits, draft_tokens, parent, node_offsets, history=(), history_offsets=None,
+                    prompt_lens=None, repetition=None, presence=None, frequency=None, bias_ids=(),
+                    bias_values=(), bias_offsets=None, allowed=None):
+    """fp64 penalised rows from the definition; allowed: bool [total, V] or None."""
+    out = np.asarray(logits, np.float64).copy()
+    V = out.shape[1]
+    for b in range(len(node_offsets) - 1):
+        n0, n1 = int(node_offsets[b]), int(node_offsets[b + 1])
+        h = list(history[int(history_offsets[b]):int(history_offsets[b + 1])]) if history_offsets is not None else []
+        prompt = int(prompt_lens[b]) if prompt_lens is not None else 0
+        bias = {}
+        if bias_offsets is not None:
+            for k in range(int(bias_offsets[b]), int(bias_offsets[b + 1])):
+                bias[int(bias_ids[k])] = float(bias_values[k])
+        rep = float(repetition[b]) if repetition is not None else 1.0
+        pres = float(presence[b]) if presence is not None else 0.0
+        freq = float(frequency[b]) if frequency is not None else 0.0
+        for i in range(n1 - n0):
+            c, j = {}, i
+            for k, t in enumerate(h):
+                c[int(t)] = c.get(int(t), 0) + (1 if k >= prompt else 0)
+            while j > 0:
+                t = int(draft_tokens[n0 + j])
+                c[t] = c.get(t, 0) + 1
+                j = int(parent[n0 + j])
+            row = out[n0 + i]
+            for t, n in c.items():
+                if 0 <= t < V:
+                    x = row[t]
+                    x = x / rep if x > 0 else x * rep
+                    row[t] = x - freq * n - (pres if n > 0 else 0.0)
+            for t, x in bias.items():
+                if 0 <= t < V:
+                    row[t] += x
+    return out if allowed is None else np.where(allowed, out, -np.inf)

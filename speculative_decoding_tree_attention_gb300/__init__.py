@@ -14,6 +14,11 @@ PyTorch is used for device memory and the current CUDA stream only.
     retained_set(...)    -> mask, z_fixed, z, kept (tv_retained_set)
     chunk_attention(...) -> out, status      (tv_chunk_attention: prompts and decode tokens)
     chunk_attention_fp8(...) -> out, status  (tv_chunk_attention_fp8, E4M3 cache)
+    append_kv(...), append_kv_fp8(...) -> status (tv_append_kv, tv_append_kv_fp8)
+    read_kv_fp8(...)     -> k, v, status     (tv_read_kv_fp8)
+    quantize_rows(...)   -> codes, scale     (tv_quantize_rows)
+    commit_kv_fp8(...)   -> new_prefix_lens, status (tv_commit_kv_fp8)
+    penalize_logits(...) -> out, status      (tv_penalize_logits)
 """
 from __future__ import annotations
 
@@ -22,6 +27,8 @@ import os
 
 __all__ = ["TVError", "load", "tree_attention", "tree_attention_fp8", "accept", "commit_kv", "retained_set",
            "chunk_attention", "chunk_attention_fp8", "chunk_params", "chunk_workspace_size",
+           "append_kv", "append_kv_fp8", "read_kv_fp8", "quantize_rows", "commit_kv_fp8",
+           "penalize_logits",
            "attention_workspace_size", "attention_plan", "attention_params",
            "TV_MAX_NODES", "TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_DEVICE_TIMEOUT", "TV_ERR_NO_PAGE",
            "status_string"]
@@ -44,7 +51,9 @@ EXPORTS = ("tv_status_string", "tv_version", "tv_tree_attention_workspace_size",
            "tv_commit_kv",
            "tv_retained_set", "tv_selftest_wait_timeout", "tv_tree_attention_plan",
            "tv_tree_attention_no_alloc", "tv_tree_attention_fp8",
-           "tv_chunk_attention_workspace_size", "tv_chunk_attention", "tv_chunk_attention_fp8")
+           "tv_chunk_attention_workspace_size", "tv_chunk_attention", "tv_chunk_attention_fp8",
+           "tv_append_kv", "tv_append_kv_fp8", "tv_read_kv_fp8", "tv_quantize_rows",
+           "tv_commit_kv_fp8", "tv_penalize_logits")
 
 
 class TVError(RuntimeError):
@@ -95,6 +104,23 @@ class ChunkParams(C.Structure):
                 ("q_stride", C.c_int64)]
 
 
+class CacheParams(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("block_size", C.c_int32), ("max_blocks_per_seq", C.c_int32),
+                ("num_blocks", C.c_int32), ("total_tokens", C.c_int32), ("kv_stride", C.c_int64)]
+
+
+class QuantParams(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32),
+                ("stride", C.c_int64)]
+
+
+class PenaltyParams(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("vocab", C.c_int32), ("max_nodes", C.c_int32),
+                ("total_nodes", C.c_int32), ("total_history", C.c_int32), ("total_bias", C.c_int32),
+                ("logits_dtype", C.c_int32)]
+
+
 _lib = None
 
 
@@ -140,6 +166,18 @@ def load(path: str | None = None) -> C.CDLL:
     lib.tv_chunk_attention.restype = C.c_int
     lib.tv_chunk_attention_fp8.argtypes = [C.POINTER(ChunkParams)] + [vp] * 12 + [sz, vp]
     lib.tv_chunk_attention_fp8.restype = C.c_int
+    lib.tv_append_kv.argtypes = [C.POINTER(CacheParams)] + [vp] * 8 + [vp]
+    lib.tv_append_kv.restype = C.c_int
+    lib.tv_append_kv_fp8.argtypes = [C.POINTER(CacheParams)] + [vp] * 10 + [vp]
+    lib.tv_append_kv_fp8.restype = C.c_int
+    lib.tv_read_kv_fp8.argtypes = [C.POINTER(CacheParams)] + [vp] * 10 + [vp]
+    lib.tv_read_kv_fp8.restype = C.c_int
+    lib.tv_quantize_rows.argtypes = [C.POINTER(QuantParams)] + [vp] * 3 + [vp]
+    lib.tv_quantize_rows.restype = C.c_int
+    lib.tv_commit_kv_fp8.argtypes = [C.POINTER(CommitParams)] + [vp] * 16 + [vp]
+    lib.tv_commit_kv_fp8.restype = C.c_int
+    lib.tv_penalize_logits.argtypes = [C.POINTER(PenaltyParams)] + [vp] * 16 + [vp]
+    lib.tv_penalize_logits.restype = C.c_int
     if path is None:
         _lib = lib
     return lib
@@ -579,3 +617,239 @@ def chunk_attention_fp8(q_codes, q_scale, k_pool, k_scale, v_pool, v_scale, bloc
                   token_offsets, out, status, workspace, stream,
                   dict(max_len=max_len, window=window, sinks=sinks, softmax_scale=softmax_scale,
                        out_dtype=out_dtype))
+
+
+# ---------------------------------------------------------------- the cache
+def _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, token_offsets, fp8):
+    import torch
+    dev = _cuda("k_pool", k_pool)
+    elem = torch.uint8 if fp8 else torch.bfloat16
+    _arg("k_pool", k_pool, elem, (None, None, TV_BLOCK_SIZE, None), dev)
+    _arg("v_pool", v_pool, elem, k_pool.shape, dev)
+    if fp8:
+        _arg("k_scale", k_scale, torch.float32, k_pool.shape[:3], dev)
+        _arg("v_scale", v_scale, torch.float32, k_pool.shape[:3], dev)
+    _arg("seq_lens", seq_lens, torch.int32, (None,), dev)
+    batch = seq_lens.shape[0]
+    _arg("block_table", block_table, torch.int32, (batch, None), dev)
+    _arg("token_offsets", token_offsets, torch.int32, (batch + 1,), dev)
+    return dev, batch
+
+
+def _row_pair(names, k, v, shape, dev):
+    """Checks K and V rows (bf16, strided by tokens alike); returns their stride."""
+    import torch
+    for name, t in zip(names, (k, v)):
+        _arg(name, t, torch.bfloat16, shape, dev, strided=1)
+    if _row_stride(k) != _row_stride(v):
+        _bad(names[1], f"strided as {names[0]}")
+    return _row_stride(k)
+
+
+def _append(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, k_scale, v_pool, v_scale,
+            status, stream, fp8):
+    import torch
+    lib = load()
+    dev, batch = _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, token_offsets, fp8)
+    hkv, d = k_pool.shape[1], k_pool.shape[3]
+    stride = _row_pair(("k_new", "v_new"), k_new, v_new, (k_new.shape[0], hkv, d), dev)
+    if status is not None:
+        _arg("status", status, torch.int32, (batch,), dev)
+    prm = CacheParams(batch, hkv, d, TV_BLOCK_SIZE, block_table.shape[1], k_pool.shape[0],
+                      k_new.shape[0], stride)
+    with _on(dev, stream) as on:
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        head = [k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                token_offsets.data_ptr()]
+        if fp8:
+            rc = lib.tv_append_kv_fp8(C.byref(prm), *head, k_pool.data_ptr(), k_scale.data_ptr(),
+                                      v_pool.data_ptr(), v_scale.data_ptr(), status.data_ptr(), on.ptr)
+        else:
+            rc = lib.tv_append_kv(C.byref(prm), *head, k_pool.data_ptr(), v_pool.data_ptr(),
+                                  status.data_ptr(), on.ptr)
+    if rc != TV_OK:
+        raise TVError(rc, "tv_append_kv_fp8" if fp8 else "tv_append_kv")
+    return status
+
+
+def append_kv(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, v_pool, *, status=None,
+              stream=None):
+    """tv_append_kv: writes the K/V rows of every sequence's chunk (rows
+    token_offsets[b] .. token_offsets[b+1]-1 of k_new, v_new [total, Hkv, D]
+    bf16, which may be strided by tokens) into the last positions of its
+    seq_lens[b] cached tokens, in place in the pools [num_blocks, Hkv, 16, D].
+    Returns status; nothing is synchronised."""
+    return _append(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, None, v_pool, None,
+                   status, stream, False)
+
+
+def append_kv_fp8(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, k_scale, v_pool,
+                  v_scale, *, status=None, stream=None):
+    """tv_append_kv_fp8: append_kv into an E4M3 cache: every row becomes codes
+    (uint8 pools) and one fp32 scale ([num_blocks, Hkv, 16]).  Returns status;
+    nothing is synchronised."""
+    return _append(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, k_scale, v_pool,
+                   v_scale, status, stream, True)
+
+
+def read_kv_fp8(k_pool, k_scale, v_pool, v_scale, block_table, seq_lens, token_offsets, *,
+                total_tokens: int | None = None, k_out=None, v_out=None, status=None, stream=None):
+    """tv_read_kv_fp8: the last token_offsets[b+1] - token_offsets[b] of the
+    seq_lens[b] cached tokens of every sequence, from an E4M3 cache back to bf16
+    rows [total_tokens, Hkv, D] (total_tokens >= token_offsets[-1]; taken from
+    k_out where that is given).  Returns (k, v, status); nothing is
+    synchronised."""
+    import torch
+    lib = load()
+    dev, batch = _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, token_offsets, True)
+    hkv, d = k_pool.shape[1], k_pool.shape[3]
+    if (k_out is None) != (v_out is None) or (k_out is None and total_tokens is None):
+        raise ValueError("read_kv_fp8 needs total_tokens, or both k_out and v_out")
+    if k_out is not None and total_tokens not in (None, k_out.shape[0]):
+        _bad("total_tokens", "the rows of k_out")
+    if status is not None:
+        _arg("status", status, torch.int32, (batch,), dev)
+    with _on(dev, stream) as on:
+        if k_out is None:
+            k_out = torch.empty(int(total_tokens), hkv, d, dtype=torch.bfloat16, device=dev)
+            v_out = torch.empty_like(k_out)
+        stride = _row_pair(("k_out", "v_out"), k_out, v_out, (k_out.shape[0], hkv, d), dev)
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        prm = CacheParams(batch, hkv, d, TV_BLOCK_SIZE, block_table.shape[1], k_pool.shape[0],
+                          k_out.shape[0], stride)
+        rc = lib.tv_read_kv_fp8(C.byref(prm), k_pool.data_ptr(), k_scale.data_ptr(), v_pool.data_ptr(),
+                                v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                                token_offsets.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
+                                status.data_ptr(), on.ptr)
+    if rc != TV_OK:
+        raise TVError(rc, "tv_read_kv_fp8")
+    return k_out, v_out, status
+
+
+def quantize_rows(x, *, codes=None, scale=None, stream=None):
+    """tv_quantize_rows: bf16 rows [tokens, heads, D] (which may be strided by
+    tokens) to E4M3 codes [tokens, heads, D] uint8 and scales [tokens, heads]
+    fp32.  Returns (codes, scale); nothing is synchronised."""
+    import torch
+    lib = load()
+    dev = _cuda("x", x)
+    _arg("x", x, torch.bfloat16, (None, None, None), dev, strided=1)
+    if codes is not None:
+        _arg("codes", codes, torch.uint8, x.shape, dev)
+    if scale is not None:
+        _arg("scale", scale, torch.float32, x.shape[:2], dev)
+    with _on(dev, stream) as on:
+        if codes is None:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
+        if scale is None:
+            scale = torch.empty(x.shape[:2], dtype=torch.float32, device=dev)
+        prm = QuantParams(x.shape[0], x.shape[1], x.shape[2], _row_stride(x))
+        rc = lib.tv_quantize_rows(C.byref(prm), x.data_ptr(), codes.data_ptr(), scale.data_ptr(), on.ptr)
+    if rc != TV_OK:
+        raise TVError(rc, "tv_quantize_rows")
+    return codes, scale
+
+
+def commit_kv_fp8(k_nodes, k_nodes_scale, v_nodes, v_nodes_scale, parent, node_offsets,
+                  accepted_len, path, block_table, prefix_lens, k_prefix_blocks, k_prefix_scale,
+                  v_prefix_blocks, v_prefix_scale, *, max_nodes: int, new_prefix_lens=None,
+                  status=None, stream=None):
+    """tv_commit_kv_fp8: commit_kv of an E4M3 cache (codes and scales of the
+    tree nodes, as tree_attention_fp8 takes them, copied to the pools in place).
+    Returns (new_prefix_lens, status); nothing is synchronised."""
+    import torch
+    lib = load()
+    dev = _cuda("k_nodes", k_nodes)
+    i32, f32 = torch.int32, torch.float32
+    _arg("k_nodes", k_nodes, torch.uint8, (None, None, None), dev)
+    total, hkv, d = k_nodes.shape
+    _arg("v_nodes", v_nodes, torch.uint8, k_nodes.shape, dev)
+    _arg("k_nodes_scale", k_nodes_scale, f32, (total, hkv), dev)
+    _arg("v_nodes_scale", v_nodes_scale, f32, (total, hkv), dev)
+    _arg("prefix_lens", prefix_lens, i32, (None,), dev)
+    batch = prefix_lens.shape[0]
+    for name, t, shape in (("parent", parent, (total,)), ("node_offsets", node_offsets, (batch + 1,)),
+                           ("accepted_len", accepted_len, (batch,)), ("path", path, (batch, int(max_nodes))),
+                           ("block_table", block_table, (batch, None))):
+        _arg(name, t, i32, shape, dev)
+    _arg("k_prefix_blocks", k_prefix_blocks, torch.uint8, (None, hkv, TV_BLOCK_SIZE, d), dev)
+    _arg("v_prefix_blocks", v_prefix_blocks, torch.uint8, k_prefix_blocks.shape, dev)
+    _arg("k_prefix_scale", k_prefix_scale, f32, k_prefix_blocks.shape[:3], dev)
+    _arg("v_prefix_scale", v_prefix_scale, f32, k_prefix_blocks.shape[:3], dev)
+    if new_prefix_lens is not None:
+        _arg("new_prefix_lens", new_prefix_lens, i32, (batch,), dev)
+    if status is not None:
+        _arg("status", status, i32, (batch,), dev)
+    prm = CommitParams(batch, hkv, d, TV_BLOCK_SIZE, block_table.shape[1], k_prefix_blocks.shape[0],
+                       int(max_nodes), total)
+    with _on(dev, stream) as on:
+        if new_prefix_lens is None:
+            new_prefix_lens = torch.empty(batch, dtype=i32, device=dev)
+        if status is None:
+            status = torch.empty(batch, dtype=i32, device=dev)
+        rc = lib.tv_commit_kv_fp8(
+            C.byref(prm), k_nodes.data_ptr(), k_nodes_scale.data_ptr(), v_nodes.data_ptr(),
+            v_nodes_scale.data_ptr(), parent.data_ptr(), node_offsets.data_ptr(), accepted_len.data_ptr(),
+            path.data_ptr(), block_table.data_ptr(), prefix_lens.data_ptr(), k_prefix_blocks.data_ptr(),
+            k_prefix_scale.data_ptr(), v_prefix_blocks.data_ptr(), v_prefix_scale.data_ptr(),
+            new_prefix_lens.data_ptr(), status.data_ptr(), on.ptr)
+    if rc != TV_OK:
+        raise TVError(rc, "tv_commit_kv_fp8")
+    return new_prefix_lens, status
+
+
+# ---------------------------------------------------------------- logits
+def penalize_logits(logits, draft_tokens, parent, node_offsets, *, max_nodes: int, history=None,
+                    history_offsets=None, prompt_lens=None, repetition=None, presence=None,
+                    frequency=None, bias_ids=None, bias_values=None, bias_offsets=None,
+                    allowed_mask=None, out=None, status=None, stream=None):
+    """tv_penalize_logits: repetition, frequency and presence penalties (counted
+    over each sequence's history and each node's drafted path), biases and
+    grammar masks on the target logits [total, V] (fp32 or bf16) of tree nodes,
+    into out [total, V] fp32 (which may be fp32 logits themselves).  history
+    [H], bias_ids [E] int32 and bias_values [E] fp32 are ragged by
+    history_offsets and bias_offsets [B+1]; prompt_lens [B] int32; repetition,
+    presence, frequency [B] fp32; allowed_mask [total, ceil(V/32)] int32 or
+    uint32 bits.  Returns (out, status); nothing is synchronised."""
+    import torch
+    lib = load()
+    i32, f32 = torch.int32, torch.float32
+    dev = _cuda("logits", logits)
+    _arg("logits", logits, (f32, torch.bfloat16), (None, None), dev)
+    total, vocab = logits.shape
+    _arg("node_offsets", node_offsets, i32, (None,), dev)
+    batch = node_offsets.shape[0] - 1
+    _arg("draft_tokens", draft_tokens, i32, (total,), dev)
+    _arg("parent", parent, i32, (total,), dev)
+    if (history is None) != (history_offsets is None):
+        raise ValueError("history and history_offsets go together")
+    if len({bias_ids is None, bias_values is None, bias_offsets is None}) != 1:
+        raise ValueError("bias_ids, bias_values and bias_offsets go together")
+    n_bias = None if bias_ids is None else bias_ids.shape[0]
+    for name, t, dtype, shape in (
+            ("history", history, i32, (None,)), ("history_offsets", history_offsets, i32, (batch + 1,)),
+            ("prompt_lens", prompt_lens, i32, (batch,)), ("repetition", repetition, f32, (batch,)),
+            ("presence", presence, f32, (batch,)), ("frequency", frequency, f32, (batch,)),
+            ("bias_ids", bias_ids, i32, (None,)), ("bias_values", bias_values, f32, (n_bias,)),
+            ("bias_offsets", bias_offsets, i32, (batch + 1,)),
+            ("allowed_mask", allowed_mask, (i32, torch.uint32), (total, (vocab + 31) // 32)),
+            ("out", out, f32, (total, vocab)), ("status", status, i32, (batch,))):
+        if t is not None:
+            _arg(name, t, dtype, shape, dev)
+    prm = PenaltyParams(batch, vocab, int(max_nodes), total, 0 if history is None else history.shape[0],
+                        n_bias or 0, 1 if logits.dtype == f32 else 0)
+    p = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()  # noqa: E731
+    with _on(dev, stream) as on:
+        if out is None:
+            out = torch.empty(total, vocab, dtype=f32, device=dev)
+        if status is None:
+            status = torch.empty(batch, dtype=i32, device=dev)
+        rc = lib.tv_penalize_logits(C.byref(prm), p(logits), p(draft_tokens), p(parent), p(node_offsets),
+                                    p(history), p(history_offsets), p(prompt_lens), p(repetition),
+                                    p(presence), p(frequency), p(bias_ids), p(bias_values), p(bias_offsets),
+                                    p(allowed_mask), p(out), p(status), on.ptr)
+    if rc != TV_OK:
+        raise TVError(rc, "tv_penalize_logits")
+    return out, status

@@ -13,7 +13,8 @@
 // previous step, whose K/V this step computed) and the accepted path become
 // positions L .. L+a of the sequence: every CTA of the sequence checks the
 // path against the parent array and the pages of those positions (the same
-// decision everywhere), then copies its head's rows in 16-byte pieces.  The
+// decision everywhere), then copies its head's rows in 16-byte pieces (and, of
+// an E4M3 cache, the rows' scales).  The
 // head-0 CTA writes the status and the new prefix length, so no output needs
 // initialising.
 #include "tv_device.cuh"
@@ -61,8 +62,10 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitArgs
     a.new_prefix_lens[b] = code == kOk ? L + acc + 1 : L;
   }
   if (code != kOk) return;
-  // (acc + 1) tokens x {K, V} x D/8 pieces of 16 bytes
-  const int pieces = a.head_dim / 8;
+  // (acc + 1) tokens x {K, V} x pieces of 16 bytes of a row (D bf16 values or
+  // D E4M3 codes)
+  const int row_bytes = a.k_scale ? a.head_dim : 2 * a.head_dim;
+  const int pieces = row_bytes / 16;
   const int items = (acc + 1) * 2 * pieces;
   for (int it = tid; it < items; it += kCommitThreads) {
     const int c = it % pieces;
@@ -71,12 +74,13 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitArgs
     const int v = t == 0 ? 0 : path[t - 1];
     const int pos = L + t;
     const int blk = btab[pos / 16];
+    const size_t from = static_cast<size_t>(n0 + v) * a.hkv + kvh;
+    const size_t to = (static_cast<size_t>(blk) * a.hkv + kvh) * 16 + pos % 16;
     const uint4* src = reinterpret_cast<const uint4*>(
-        (kv ? a.v_nodes : a.k_nodes) + (static_cast<size_t>(n0 + v) * a.hkv + kvh) * a.head_dim) + c;
-    uint4* dst = reinterpret_cast<uint4*>(
-        (kv ? a.v_pool : a.k_pool) +
-        ((static_cast<size_t>(blk) * a.hkv + kvh) * 16 + pos % 16) * a.head_dim) + c;
+        static_cast<const uint8_t*>(kv ? a.v_nodes : a.k_nodes) + from * row_bytes) + c;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(kv ? a.v_pool : a.k_pool) + to * row_bytes) + c;
     *dst = __ldg(src);
+    if (a.k_scale && c == 0) (kv ? a.v_scale : a.k_scale)[to] = __ldg((kv ? a.v_nodes_scale : a.k_nodes_scale) + from);
   }
 }
 

@@ -466,11 +466,15 @@ int tv_accept_ex(const tv_accept_params* p, const tv_accept_options* opt, const 
 
 }  // extern "C"
 
-int tv_commit_kv(const tv_commit_params* p, const uint16_t* k_nodes, const uint16_t* v_nodes,
-                 const int32_t* parent, const int32_t* node_offsets, const int32_t* accepted_len,
-                 const int32_t* path, const int32_t* block_table, const int32_t* prefix_lens,
-                 uint16_t* k_prefix_blocks, uint16_t* v_prefix_blocks, int32_t* new_prefix_lens,
-                 int32_t* status, cudaStream_t stream) {
+namespace {
+
+// The shared path of tv_commit_kv and tv_commit_kv_fp8 (k_scale non-null).
+int commit_call(const tv_commit_params* p, const void* k_nodes, const float* k_nodes_scale,
+                const void* v_nodes, const float* v_nodes_scale, const int32_t* parent,
+                const int32_t* node_offsets, const int32_t* accepted_len, const int32_t* path,
+                const int32_t* block_table, const int32_t* prefix_lens, void* k_pool,
+                float* k_scale, void* v_pool, float* v_scale, int32_t* new_prefix_lens,
+                int32_t* status, cudaStream_t stream) {
   if (!p) return TV_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
   if (p->batch < 1 || p->num_kv_heads < 1 || p->block_size != TV_BLOCK_SIZE ||
@@ -480,8 +484,7 @@ int tv_commit_kv(const tv_commit_params* p, const uint16_t* k_nodes, const uint1
   if (static_cast<int64_t>(p->num_blocks) * p->num_kv_heads * 16 >= (1ll << 31))
     return TV_ERR_INVALID_ARG;
   const void* ptrs[] = {k_nodes, v_nodes, parent, node_offsets, accepted_len, path,
-                        block_table, prefix_lens, k_prefix_blocks, v_prefix_blocks,
-                        new_prefix_lens, status};
+                        block_table, prefix_lens, k_pool, v_pool, new_prefix_lens, status};
   for (const void* q : ptrs)
     if (!q || !aligned16(q)) return TV_ERR_INVALID_ARG;
   if (static_cast<const void*>(new_prefix_lens) == static_cast<const void*>(prefix_lens))
@@ -489,14 +492,18 @@ int tv_commit_kv(const tv_commit_params* p, const uint16_t* k_nodes, const uint1
   tv::CommitArgs a;
   a.k_nodes = k_nodes;
   a.v_nodes = v_nodes;
+  a.k_nodes_scale = k_nodes_scale;
+  a.v_nodes_scale = v_nodes_scale;
   a.parent = parent;
   a.node_offsets = node_offsets;
   a.accepted_len = accepted_len;
   a.path = path;
   a.block_table = block_table;
   a.prefix_lens = prefix_lens;
-  a.k_pool = k_prefix_blocks;
-  a.v_pool = v_prefix_blocks;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
   a.new_prefix_lens = new_prefix_lens;
   a.status = status;
   a.batch = p->batch;
@@ -507,6 +514,33 @@ int tv_commit_kv(const tv_commit_params* p, const uint16_t* k_nodes, const uint1
   a.max_nodes = p->max_nodes;
   a.total_nodes = p->total_nodes;
   return tv::launch_commit(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // namespace
+
+int tv_commit_kv(const tv_commit_params* p, const uint16_t* k_nodes, const uint16_t* v_nodes,
+                 const int32_t* parent, const int32_t* node_offsets, const int32_t* accepted_len,
+                 const int32_t* path, const int32_t* block_table, const int32_t* prefix_lens,
+                 uint16_t* k_prefix_blocks, uint16_t* v_prefix_blocks, int32_t* new_prefix_lens,
+                 int32_t* status, cudaStream_t stream) {
+  return commit_call(p, k_nodes, nullptr, v_nodes, nullptr, parent, node_offsets, accepted_len, path,
+                     block_table, prefix_lens, k_prefix_blocks, nullptr, v_prefix_blocks, nullptr,
+                     new_prefix_lens, status, stream);
+}
+
+int tv_commit_kv_fp8(const tv_commit_params* p, const uint8_t* k_nodes, const float* k_nodes_scale,
+                     const uint8_t* v_nodes, const float* v_nodes_scale, const int32_t* parent,
+                     const int32_t* node_offsets, const int32_t* accepted_len,
+                     const int32_t* path, const int32_t* block_table, const int32_t* prefix_lens,
+                     uint8_t* k_prefix_blocks, float* k_prefix_scale, uint8_t* v_prefix_blocks,
+                     float* v_prefix_scale, int32_t* new_prefix_lens, int32_t* status,
+                     cudaStream_t stream) {
+  const void* sc[] = {k_nodes_scale, v_nodes_scale, k_prefix_scale, v_prefix_scale};
+  for (const void* q : sc)
+    if (!q || !aligned16(q)) return TV_ERR_INVALID_ARG;
+  return commit_call(p, k_nodes, k_nodes_scale, v_nodes, v_nodes_scale, parent, node_offsets,
+                     accepted_len, path, block_table, prefix_lens, k_prefix_blocks, k_prefix_scale,
+                     v_prefix_blocks, v_prefix_scale, new_prefix_lens, status, stream);
 }
 
 int tv_retained_set(const tv_retain_params* p, const float* draft_probs, uint32_t* retained_mask,
@@ -637,4 +671,153 @@ int tv_chunk_attention_fp8(const tv_chunk_params* p, const uint8_t* q, const flo
                            cudaStream_t stream) {
   return chunk_call(p, true, q, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens,
                     token_offsets, out, status, workspace, workspace_bytes, stream);
+}
+
+namespace {
+
+// The shared path of tv_append_kv, tv_append_kv_fp8 and tv_read_kv_fp8.
+int cache_call(const tv_cache_params* p, bool read, const void* k_new, const void* v_new,
+               const int32_t* block_table, const int32_t* seq_lens, const int32_t* token_offsets,
+               const void* k_pool, const float* k_scale, const void* v_pool, const float* v_scale,
+               bool fp8, int32_t* status, cudaStream_t stream) {
+  if (!p) return TV_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
+  if (p->batch < 1 || p->num_kv_heads < 1 || p->block_size != TV_BLOCK_SIZE ||
+      p->max_blocks_per_seq < 1 || p->num_blocks < 1 || p->total_tokens < 0)
+    return TV_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(p->num_blocks) * p->num_kv_heads * 16 >= (1ll << 31))
+    return TV_ERR_INVALID_ARG;
+  if (p->num_kv_heads >= (1 << 24) || static_cast<int64_t>(p->total_tokens) * p->num_kv_heads >= (1ll << 31))
+    return TV_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(p->num_kv_heads) * p->head_dim;
+  const int64_t stride = p->kv_stride ? p->kv_stride : row;
+  if (stride < row || stride >= (1ll << 38) || stride % 8) return TV_ERR_INVALID_ARG;
+  const void* ptrs[] = {block_table, seq_lens, token_offsets, k_pool, v_pool, status};
+  for (const void* q : ptrs)
+    if (!q || !aligned16(q)) return TV_ERR_INVALID_ARG;
+  if (p->total_tokens > 0 && (!k_new || !v_new)) return TV_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new)) return TV_ERR_INVALID_ARG;
+  if (fp8 && (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)))
+    return TV_ERR_INVALID_ARG;
+  tv::CacheArgs a;
+  a.k_new = const_cast<void*>(k_new);
+  a.v_new = const_cast<void*>(v_new);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.token_offsets = token_offsets;
+  a.k_pool = const_cast<void*>(k_pool);
+  a.v_pool = const_cast<void*>(v_pool);
+  a.k_scale = const_cast<float*>(k_scale);
+  a.v_scale = const_cast<float*>(v_scale);
+  a.status = status;
+  a.kv_stride = static_cast<size_t>(stride);
+  a.batch = p->batch;
+  a.hkv = p->num_kv_heads;
+  a.head_dim = p->head_dim;
+  a.max_blocks_per_seq = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  a.total_tokens = p->total_tokens;
+  a.read = read ? 1 : 0;
+  a.tile_shift = 0;
+  return tv::launch_cache(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // namespace
+
+int tv_append_kv(const tv_cache_params* p, const uint16_t* k_new, const uint16_t* v_new,
+                 const int32_t* block_table, const int32_t* seq_lens,
+                 const int32_t* token_offsets, uint16_t* k_pool, uint16_t* v_pool,
+                 int32_t* status, cudaStream_t stream) {
+  return cache_call(p, false, k_new, v_new, block_table, seq_lens, token_offsets, k_pool, nullptr,
+                    v_pool, nullptr, false, status, stream);
+}
+
+int tv_append_kv_fp8(const tv_cache_params* p, const uint16_t* k_new, const uint16_t* v_new,
+                     const int32_t* block_table, const int32_t* seq_lens,
+                     const int32_t* token_offsets, uint8_t* k_pool, float* k_scale,
+                     uint8_t* v_pool, float* v_scale, int32_t* status, cudaStream_t stream) {
+  return cache_call(p, false, k_new, v_new, block_table, seq_lens, token_offsets, k_pool, k_scale,
+                    v_pool, v_scale, true, status, stream);
+}
+
+int tv_read_kv_fp8(const tv_cache_params* p, const uint8_t* k_pool, const float* k_scale,
+                   const uint8_t* v_pool, const float* v_scale, const int32_t* block_table,
+                   const int32_t* seq_lens, const int32_t* token_offsets, uint16_t* k_out,
+                   uint16_t* v_out, int32_t* status, cudaStream_t stream) {
+  return cache_call(p, true, k_out, v_out, block_table, seq_lens, token_offsets, k_pool, k_scale,
+                    v_pool, v_scale, true, status, stream);
+}
+
+int tv_quantize_rows(const tv_quant_params* p, const uint16_t* x, uint8_t* codes, float* scale,
+                     cudaStream_t stream) {
+  if (!p) return TV_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
+  if (p->tokens < 0 || p->heads < 1) return TV_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(p->heads) * p->head_dim;
+  const int64_t stride = p->stride ? p->stride : row;
+  if (stride < row || stride >= (1ll << 38) || stride % 8) return TV_ERR_INVALID_ARG;
+  if (p->tokens == 0) return TV_OK;
+  const void* ptrs[] = {x, codes, scale};
+  for (const void* q : ptrs)
+    if (!q || !aligned16(q)) return TV_ERR_INVALID_ARG;
+  tv::QuantArgs a;
+  a.x = x;
+  a.codes = codes;
+  a.scale = scale;
+  a.stride = static_cast<size_t>(stride);
+  a.tokens = p->tokens;
+  a.heads = p->heads;
+  a.head_dim = p->head_dim;
+  return tv::launch_quantise_rows(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+int tv_penalize_logits(const tv_penalty_params* p, const void* logits,
+                       const int32_t* draft_tokens, const int32_t* parent,
+                       const int32_t* node_offsets, const int32_t* history,
+                       const int32_t* history_offsets, const int32_t* prompt_lens,
+                       const float* repetition, const float* presence, const float* frequency,
+                       const int32_t* bias_ids, const float* bias_values,
+                       const int32_t* bias_offsets, const uint32_t* allowed_mask, float* out,
+                       int32_t* status, cudaStream_t stream) {
+  if (!p) return TV_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->batch > 65535 || p->vocab < 1 || p->vocab >= (1 << 18)) return TV_ERR_INVALID_ARG;
+  if (p->max_nodes < 1 || p->max_nodes > TV_MAX_NODES || p->total_nodes < p->batch) return TV_ERR_INVALID_ARG;
+  if (p->logits_dtype != TV_OUT_BF16 && p->logits_dtype != TV_OUT_FP32) return TV_ERR_INVALID_ARG;
+  if (p->total_history < 0 || p->total_bias < 0) return TV_ERR_INVALID_ARG;
+  const void* ptrs[] = {logits, draft_tokens, parent, node_offsets, out, status};
+  for (const void* q : ptrs)
+    if (!q || !aligned16(q)) return TV_ERR_INVALID_ARG;
+  const void* optional[] = {history, history_offsets, prompt_lens, repetition, presence, frequency,
+                            bias_ids, bias_values, bias_offsets, allowed_mask};
+  for (const void* q : optional)
+    if (q && !aligned16(q)) return TV_ERR_INVALID_ARG;
+  if (history && !history_offsets) return TV_ERR_INVALID_ARG;
+  if (bias_ids && (!bias_values || !bias_offsets)) return TV_ERR_INVALID_ARG;
+  // in place only with fp32 logits (a bf16 row is half as long as its output)
+  if (p->logits_dtype == TV_OUT_BF16 && logits == static_cast<const void*>(out)) return TV_ERR_INVALID_ARG;
+  tv::PenaltyArgs a;
+  a.logits = logits;
+  a.out = out;
+  a.tokens = draft_tokens;
+  a.parent = parent;
+  a.node_offsets = node_offsets;
+  a.history = history;
+  a.history_offsets = history_offsets;
+  a.prompt_lens = prompt_lens;
+  a.repetition = repetition;
+  a.presence = presence;
+  a.frequency = frequency;
+  a.bias_ids = bias_ids;
+  a.bias_values = bias_values;
+  a.bias_offsets = bias_offsets;
+  a.allowed_mask = allowed_mask;
+  a.status = status;
+  a.batch = p->batch;
+  a.vocab = p->vocab;
+  a.max_nodes = p->max_nodes;
+  a.total_nodes = p->total_nodes;
+  a.total_history = p->total_history;
+  a.total_bias = p->total_bias;
+  a.bf16 = p->logits_dtype == TV_OUT_BF16 ? 1 : 0;
+  return tv::launch_penalty(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }

@@ -124,21 +124,75 @@ int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream
 size_t chunk_slot_bytes(int head_dim);
 
 struct CommitArgs {
-  const uint16_t* k_nodes;    // [total_nodes][Hkv][D]
-  const uint16_t* v_nodes;
+  const void* k_nodes;        // [total_nodes][Hkv][D] bf16, or E4M3 codes (k_scale given)
+  const void* v_nodes;
+  const float* k_nodes_scale; // E4M3: [total_nodes][Hkv], else null
+  const float* v_nodes_scale;
   const int32_t* parent;      // [total_nodes]
   const int32_t* node_offsets;// [batch+1]
   const int32_t* accepted_len;// [batch]
   const int32_t* path;        // [batch][max_nodes]
   const int32_t* block_table; // [batch][max_blocks_per_seq]
   const int32_t* prefix_lens; // [batch]
-  uint16_t* k_pool;           // [num_blocks][Hkv][16][D]
-  uint16_t* v_pool;
+  void* k_pool;               // [num_blocks][Hkv][16][D]
+  void* v_pool;
+  float* k_scale;             // E4M3: [num_blocks][Hkv][16], else null
+  float* v_scale;
   int32_t* new_prefix_lens;   // [batch]
   int32_t* status;            // [batch]
   int32_t batch, hkv, head_dim, max_blocks_per_seq, num_blocks, max_nodes, total_nodes;
 };
 
 int launch_commit(const CommitArgs& a, cudaStream_t stream);
+
+// New K/V rows into the pool (bf16; E4M3 when k_scale is given), or, with
+// `read`, an E4M3 pool's rows back into bf16 rows.
+struct CacheArgs {
+  void* k_new;                // bf16 rows [total_tokens][Hkv][D], kv_stride elements apart
+  void* v_new;
+  const int32_t* block_table; // [batch][max_blocks_per_seq]
+  const int32_t* seq_lens;    // [batch] tokens, the chunk's included
+  const int32_t* token_offsets; // [batch+1]
+  void* k_pool;               // [num_blocks][Hkv][16][D]
+  void* v_pool;
+  float* k_scale;             // [num_blocks][Hkv][16] or null
+  float* v_scale;
+  int32_t* status;            // [batch]
+  size_t kv_stride;
+  int32_t batch, hkv, head_dim, max_blocks_per_seq, num_blocks, total_tokens;
+  int32_t read;
+  int32_t tile_shift;         // log2 of the tokens per CTA (set by the launcher)
+};
+int launch_cache(CacheArgs a, int sms, cudaStream_t stream);
+
+struct QuantArgs {
+  const uint16_t* x;          // bf16 [tokens][heads][D], rows `stride` elements apart
+  uint8_t* codes;             // [tokens][heads][D]
+  float* scale;               // [tokens][heads]
+  size_t stride;
+  int32_t tokens, heads, head_dim;
+};
+int launch_quantise_rows(const QuantArgs& a, int sms, cudaStream_t stream);
+
+struct PenaltyArgs {
+  const void* logits;         // [total_nodes][vocab], bf16 or fp32
+  float* out;                 // [total_nodes][vocab]
+  const int32_t* tokens;      // [total_nodes]
+  const int32_t* parent;      // [total_nodes]
+  const int32_t* node_offsets;// [batch+1]
+  const int32_t* history;     // [total_history] or null
+  const int32_t* history_offsets; // [batch+1]
+  const int32_t* prompt_lens; // [batch] or null
+  const float* repetition;    // [batch] or null
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_ids;    // [total_bias] or null
+  const float* bias_values;
+  const int32_t* bias_offsets;// [batch+1]
+  const uint32_t* allowed_mask; // [total_nodes][ceil(vocab/32)] or null
+  int32_t* status;            // [batch]
+  int32_t batch, vocab, max_nodes, total_nodes, total_history, total_bias, bf16;
+};
+int launch_penalty(const PenaltyArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace tv
