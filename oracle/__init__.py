@@ -318,14 +318,19 @@ def chunk_attention(q, k_pool, v_pool, block_table, seq_lens, token_offsets, win
     out = np.zeros(q.shape) if out is None else out
     for b, n in enumerate(np.asarray(seq_lens).tolist()):
         r0, r1 = int(token_offsets[b]), int(token_offsets[b + 1])
-        for i in range(r1 - r0):
-            p = n - (r1 - r0) + i
-            keys = np.array([k for k in range(p + 1) if not window or k > p - window or k < sinks])
-            blk, at = np.asarray(block_table)[b, keys // 16], keys % 16
-            for h in range(hq):
-                s = k_pool[blk, h // g, at] @ q[r0 + i, h] * (scale or d ** -0.5)
-                w = np.exp(s - s.max())
-                out[r0 + i, h] = w @ v_pool[blk, h // g, at] / w.sum()
+        if r1 <= r0:
+            continue
+        p = np.arange(n - (r1 - r0), n)[:, None]
+        k = np.arange(n)
+        seen = (k <= p) & ((k > p - window) | (k < sinks) if window else True)
+        blk = np.asarray(block_table)[b, k // 16]
+        used = seen.any(0)  # (pages that no row sees may be anything)
+        for h in range(hq):
+            keys = np.where(used[:, None], k_pool[np.where(used, blk, 0), h // g, k % 16], 0.0)
+            vals = np.where(used[:, None], v_pool[np.where(used, blk, 0), h // g, k % 16], 0.0)
+            s = np.where(seen, q[r0:r1, h] @ keys.T * (scale or d ** -0.5), -np.inf)
+            w = np.exp(s - s.max(1, keepdims=True))
+            out[r0:r1, h] = w @ vals / w.sum(1, keepdims=True)
     return out
 
 

@@ -135,8 +135,8 @@ struct Layout {
   static constexpr int kXchBytes = BM * 8;
   static constexpr int kBar = kXch + kXchBytes;
   // kfull, kempty [S], vfull, vempty [VS], s_full, p_a, p_b, o_done, drain,
-  // turn [2], q_full, q_empty, v16full, v16empty [2], sfull [8]
-  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 14 + (F8 ? 4 + kSclSlots : 0);
+  // turn [2], q_full, q_empty, hand [2], v16full, v16empty [2], sfull [8]
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 16 + (F8 ? 4 + kSclSlots : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kMiscBytes = 96;
   static constexpr int kTotal = kMisc + kMiscBytes;
@@ -711,7 +711,8 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   uint64_t* turn = drain + 2;             // [2]: m-tile h may issue (units with both)
   uint64_t* q_full = turn + 2;            // Q of a piece in shared memory
   uint64_t* q_empty = q_full + 1;         // the last S of both m-tiles of a piece complete
-  uint64_t* v16full = q_empty + 1;         // F8 [2]: V(t) converted (128 arrivals)
+  uint64_t* hand = q_empty + 1;           // [2]: S_1, P_1 and O_1 pass to the MMA thread of m-tile h
+  uint64_t* v16full = hand + 2;           // F8 [2]: V(t) converted (128 arrivals)
   uint64_t* v16empty = v16full + 2;       // F8 [2]: the P V of tile t complete
   uint64_t* sfull = v16empty + 2;         // F8 [8]: the scales of tile t landed (32 arrivals)
   Misc* misc = reinterpret_cast<Misc*>(smem + Ly::kMisc);
@@ -746,6 +747,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       mbar_init(&o_done[h], 1);
       mbar_init(&drain[h], 1);
       mbar_init(&turn[h], 1);
+      mbar_init(&hand[h], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
@@ -766,8 +768,9 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   // Progress kept across pieces and rounds (ring slots and barrier phases):
   // g_tile, g_piece = K/V tiles and pieces of every earlier round; my_tiles =
   // the tiles of this softmax group so far; tiles0, tiles1 = the tiles of
-  // groups 0 and 1, and my_turns = the turns of this MMA thread.
-  int g_tile = 0, g_piece = 0, my_tiles = 0, tiles0 = 0, tiles1 = 0, my_turns = 0;
+  // groups 0 and 1, my_turns and my_hands = the turns and take-overs of this MMA
+  // thread.
+  int g_tile = 0, g_piece = 0, my_tiles = 0, tiles0 = 0, tiles1 = 0, my_turns = 0, my_hands = 0;
 
   // Each role runs the scheduling rounds in a loop of its own (its registers
   // are its own too).  A round: the softmax warps build the piece list, every
@@ -957,12 +960,23 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           tiles0 += narrow ? (T + 1) / 2 : T;
           tiles1 += narrow ? T / 2 : T;
         };
+        // S_1, P_1 and O_1 belong to warp 9 in narrow pieces and to warp 10 in
+        // wide ones; MMAs of two threads are not ordered, so where the kind
+        // changes the next owner waits until the last one's are complete
+        auto is_narrow = [&](int p) { return pieces[p].ntok * g <= BM; };
+        auto hand_over = [&](int p, bool narrow) {
+          if (p + 1 < npieces && is_narrow(p + 1) != narrow && h == (narrow ? 0 : 1)) mma_commit(&hand[h ^ 1]);
+        };
+        auto take_over = [&](int p, bool narrow) {
+          if (p == 0 || is_narrow(p - 1) == narrow || h != (narrow ? 0 : 1)) return true;
+          return mbar_wait(&hand[h], my_hands++ & 1, abort_flag);
+        };
         bool ok = true;
         int tau = g_tile;
         for (int p = 0; p < npieces && ok; ++p) {
           const int T = pieces[p].t1 - pieces[p].t0;
-          const bool narrow = pieces[p].ntok * g <= BM;
-          ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag);
+          const bool narrow = is_narrow(p);
+          ok = mbar_wait(q_full, (g_piece + p) & 1, abort_flag) && take_over(p, narrow);
           if (!ok) break;
           if (narrow && h == 1) {
             // warp 9 issues for both groups: these arrivals keep the rings turning
@@ -1012,6 +1026,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           if (!ok) break;
           mma_commit(&o_done[h]);
           if (narrow) mma_commit(&o_done[1]);
+          hand_over(p, narrow);
           count(T, narrow);
           tau += T;
         }
@@ -1141,23 +1156,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           const int gt = tau + i;                    // global tile (ring slot)
           // some row of the unit does not see some key of the tile
           const bool masked = k0 + BN - 1 > pos0 || (a.window > 0 && hi - a.window >= k0 && k0 + BN > a.sinks);
-          // keys that no row of the unit sees: their V rows are cleared
-          // (stale data; P is 0 there but 0 * NaN would poison O), a row per
-          // thread, by each group before its own P_h(t) V(t).
-          if constexpr (!F8) {
-            if (ok && (k0 + BN - 1 > hi || (lo > k0 && k0 + BN > a.sinks))) {
-              const int vs = gt % kVStages;
-              mbar_wait(&vfull[vs], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
-              const int key = k0 + r;
-              if (!(key <= hi && (key < a.sinks || key >= lo))) {
-                uint8_t* row = smem + Ly::kVRing + vs * Ly::kTileBytes + (r >> 3) * Ly::kGroupBytes + (r & 7) * 128;
-#pragma unroll
-                for (int k = 0; k < 8 * Ly::kHalves; ++k)
-                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();  // generic writes, read by the MMA
-            }
-          }
           if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[h], my_tiles & 1, abort_flag));
             if constexpr (F8) {  // the keys' K scales (landed with the K tile)
@@ -1170,6 +1168,25 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             mbar_arrive(&p_a[h]);
             mbar_arrive(&p_b[h]);
             continue;
+          }
+          // keys that no row of the unit sees: their V rows are cleared
+          // (stale data; P is 0 there but 0 * NaN would poison O), a row per
+          // thread, by each group before its own P_h(t) V(t).  (After S: only
+          // then is every earlier use of the slot known to be over, and the
+          // parity waited for unambiguous.)
+          if constexpr (!F8) {
+            if (k0 + BN - 1 > hi || (lo > k0 && k0 + BN > a.sinks)) {
+              const int vs = gt % kVStages;
+              mbar_wait(&vfull[vs], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
+              const int key = k0 + r;
+              if (!(key <= hi && (key < a.sinks || key >= lo))) {
+                uint8_t* row = smem + Ly::kVRing + vs * Ly::kTileBytes + (r >> 3) * Ly::kGroupBytes + (r & 7) * 128;
+#pragma unroll
+                for (int k = 0; k < 8 * Ly::kHalves; ++k)
+                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();  // generic writes, read by the MMA
+            }
           }
           // the scores stay unscaled; the softmax scale is folded into the exponent
           float x[128];

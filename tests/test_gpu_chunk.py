@@ -138,3 +138,42 @@ def test_fp8(lens, chunks, hq, hkv, window, sinks):
     got, st = call_fp8(c, window=window, sinks=sinks)
     assert (st == 0).all()
     check(got, c, U_FP8, window, sinks)
+
+
+def mixed_batch(B, hq, hkv, d, seed, longest=700):
+    """Many sequences: decode tokens, short chunks and prompts in random order,
+    so that a CTA gets whole and split units of one and of two m-tiles in turn."""
+    g = np.random.default_rng(seed)
+    chunks = [int(g.choice([0, 1, 1, 1, g.integers(2, 40), g.integers(40, 300)])) for _ in range(B)]
+    lens = [c + int(g.integers(0, longest)) for c in chunks]
+    return make(lens, chunks, hq, hkv, d, seed)
+
+
+@pytest.mark.parametrize("B, hq, hkv, d", [(300, 8, 4, 64), (200, 8, 8, 128), (400, 16, 2, 128), (40, 28, 4, 128)])
+@pytest.mark.parametrize("window, sinks", [(0, 0), (130, 4)])
+def test_many_units_per_cta(B, hq, hkv, d, window, sinks):
+    c = mixed_batch(B, hq, hkv, d, B + window)
+    got, st = call(c, window=window, sinks=sinks)
+    assert (st == 0).all()
+    check(got, c, U_BF16, window, sinks)
+    for _ in range(3):  # a race would not repeat itself
+        again, _ = call(c, window=window, sinks=sinks)
+        np.testing.assert_array_equal(got, again)
+
+
+@pytest.mark.parametrize("window, sinks", [(0, 0), (130, 4)])
+def test_many_units_per_cta_fp8(window, sinks):
+    c = quantised(mixed_batch(250, 16, 4, 128, 5))
+    got, st = call_fp8(c, window=window, sinks=sinks)
+    assert (st == 0).all()
+    check(got, c, U_FP8, window, sinks)
+    for _ in range(3):
+        again, _ = call_fp8(c, window=window, sinks=sinks)
+        np.testing.assert_array_equal(got, again)
+
+
+def test_long_decode_is_split_and_merged():
+    c = make([20011, 4097, 9000], [1, 1, 65], 8, 1, 128, seed=3)
+    got, st = call(c)
+    assert (st == 0).all()
+    check(got, c, U_BF16)
