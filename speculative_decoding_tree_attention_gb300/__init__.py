@@ -472,59 +472,96 @@ def retained_set(draft_probs, mass: float, *, mask=None, z_fixed=None, z=None, k
 # ---------------------------------------------------------------- chunks of new tokens
 # The calls below take tensors of one CUDA device, which need not be the
 # current one, and run on `stream` or on that device's current stream; buffers
-# that they create belong to that stream.
+# that they create belong to that stream.  A call costs the host a few
+# microseconds per argument, more than the smallest of them take on the device,
+# so the checks are written for the passing case.
+
+def _torch():
+    global _t
+    if _t is None:
+        import torch
+        _t = torch
+    return _t
+
+
+_t = None
+
 
 def _bad(name, what):
     raise ValueError(f"{name} must be {what}")
 
 
-def _arg(name, t, dtype, shape, dev, strided=0):
-    """Checks one tensor argument (None passes when shape is None): a CUDA
-    tensor of `dev`, of one of the dtypes and of `shape` (None entries match
-    anything), contiguous, or with `strided` = 1 contiguous but for a first
-    stride that is at least a row."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        _bad(name, f"a tensor on {dev}")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        _bad(name, f"of type {dtype}, not {t.dtype}")
-    if len(t.shape) != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        _bad(name, f"of shape {tuple('*' if s is None else s for s in shape)}, not {tuple(t.shape)}")
-    if t.is_contiguous():
-        return
-    if not (strided and t[0].is_contiguous() and t.stride(0) >= t[0].numel()):
-        _bad(name, "contiguous" + (" but for the stride between its rows" if strided else ""))
-
-
-def _cuda(name, t):
-    if not getattr(t, "is_cuda", False):
+def _device(name, t):
+    """The device index of the tensor that the others of a call go by."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         _bad(name, "a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-class _on:
-    """Makes `dev` and the stream of the call current, so that what is
-    allocated belongs to that stream; `.ptr` is the stream's handle."""
-
-    def __init__(self, dev, stream):
-        import torch
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream must be one of {dev}")
-        self._stream = torch.cuda.current_stream(dev) if stream is None else stream
-        self._ctx = torch.cuda.stream(self._stream)
-        self.ptr = C.c_void_p(self._stream.cuda_stream)
-
-    def __enter__(self):
-        self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+def _arg(name, t, dtype, shape, dev):
+    """Checks one argument: a contiguous tensor of device `dev`, of dtype and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor) or t.get_device() != dev:
+        _bad(name, f"a tensor on CUDA device {dev}")
+    if t.dtype is not dtype:
+        _bad(name, f"of type {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        _bad(name, f"of shape {tuple(shape)}, not {tuple(t.shape)}")
+    _bad(name, "contiguous")
 
 
-def _row_stride(t):
-    """Elements between the rows of a tensor whose rows are contiguous (0: packed)."""
-    return 0 if t.is_contiguous() else t.stride(0)
+def _rows(name, t, dtype, shape, dev):
+    """_arg for rows that may lie a stride apart; returns that stride (0: packed)."""
+    try:
+        if t.is_contiguous() or t.shape[0] < 2:
+            stride = 0
+        else:
+            stride = t.stride(0)
+            if not t[0].is_contiguous() or stride < t[0].numel():
+                _bad(name, "contiguous but for the stride between its rows")
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            if stride == 0 and not t.is_contiguous() and not t[0].is_contiguous():
+                _bad(name, "contiguous but for the stride between its rows")
+            return stride
+    except (AttributeError, IndexError):
+        pass
+    _arg(name, t, dtype, shape, dev)
+    return 0
+
+
+def _dims(name, t, n):
+    """The shape of a tensor of n dimensions."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != n:
+        _bad(name, f"a tensor of {n} dimensions")
+    return t.shape
+
+
+def _run(dev, stream, call):
+    """call(stream handle) with `dev` and the stream current, so that what the
+    call allocates belongs to that stream."""
+    torch = _torch()
+    if stream is None and torch.cuda.current_device() == dev:
+        return call(_raw_stream(dev))  # (the handle alone: 3 us less than a Stream object)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        _bad("stream", f"one of CUDA device {dev}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _raw_stream(dev):
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(dev).cuda_stream if get is None else get(dev)
+
+
+def _empty(t, shape, dtype, dev):
+    return _torch().empty(shape, dtype=dtype, device=f"cuda:{dev}") if t is None else t
 
 
 def chunk_params(q, k_pool, block_table, seq_lens, *, max_len: int, window: int = 0, sinks: int = 0,
@@ -534,8 +571,9 @@ def chunk_params(q, k_pool, block_table, seq_lens, *, max_len: int, window: int 
         _bad("out_dtype", "'bf16' or 'fp32'")
     total, hq, d = q.shape
     return ChunkParams(seq_lens.shape[0], hq, k_pool.shape[1], d, k_pool.shape[2],
-                       block_table.shape[1], k_pool.shape[0], total, int(max_len), int(window),
-                       int(sinks), OUT_DTYPES[out_dtype], float(softmax_scale), _row_stride(q))
+                       block_table.shape[1], k_pool.shape[0], total, max_len, window, sinks,
+                       OUT_DTYPES[out_dtype], softmax_scale,
+                       0 if q.is_contiguous() or total < 2 else q.stride(0))
 
 
 def chunk_workspace_size(params: ChunkParams) -> int:
@@ -543,49 +581,51 @@ def chunk_workspace_size(params: ChunkParams) -> int:
 
 
 def _chunk(q, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens, token_offsets, out,
-           status, workspace, stream, kw):
-    import torch
+           status, workspace, stream, max_len, window, sinks, softmax_scale, out_dtype):
+    torch = _torch()
     lib = load()
     fp8 = q_scale is not None
-    dev = _cuda("q", q)
-    elem = torch.uint8 if fp8 else torch.bfloat16
-    _arg("q", q, elem, (None, None, None), dev, strided=1)
-    _arg("k_pool", k_pool, elem, (None, None, TV_BLOCK_SIZE, q.shape[2]), dev)
-    _arg("v_pool", v_pool, elem, k_pool.shape, dev)
+    dev = _device("q", q)
+    i32, f32, elem = torch.int32, torch.float32, torch.uint8 if fp8 else torch.bfloat16
+    qs, ps = _dims("q", q, 3), _dims("k_pool", k_pool, 4)
+    _rows("q", q, elem, qs, dev)
+    _arg("k_pool", k_pool, elem, (ps[0], ps[1], TV_BLOCK_SIZE, qs[2]), dev)
+    _arg("v_pool", v_pool, elem, ps, dev)
     if fp8:
-        _arg("q_scale", q_scale, torch.float32, q.shape[:2], dev)
-        _arg("k_scale", k_scale, torch.float32, k_pool.shape[:3], dev)
-        _arg("v_scale", v_scale, torch.float32, k_pool.shape[:3], dev)
-    _arg("seq_lens", seq_lens, torch.int32, (None,), dev)
-    batch = seq_lens.shape[0]
-    _arg("block_table", block_table, torch.int32, (batch, None), dev)
-    _arg("token_offsets", token_offsets, torch.int32, (batch + 1,), dev)
-    prm = chunk_params(q, k_pool, block_table, seq_lens, **kw)
-    odt = torch.float32 if prm.out_dtype else torch.bfloat16
+        _arg("q_scale", q_scale, f32, qs[:2], dev)
+        _arg("k_scale", k_scale, f32, ps[:3], dev)
+        _arg("v_scale", v_scale, f32, ps[:3], dev)
+    (batch,) = _dims("seq_lens", seq_lens, 1)
+    _arg("seq_lens", seq_lens, i32, (batch,), dev)
+    _arg("block_table", block_table, i32, (batch, _dims("block_table", block_table, 2)[1]), dev)
+    _arg("token_offsets", token_offsets, i32, (batch + 1,), dev)
+    prm = chunk_params(q, k_pool, block_table, seq_lens, max_len=max_len, window=window, sinks=sinks,
+                       softmax_scale=softmax_scale, out_dtype=out_dtype)
+    odt = f32 if prm.out_dtype else torch.bfloat16
     if out is not None:
-        _arg("out", out, odt, q.shape, dev)
+        _arg("out", out, odt, qs, dev)
     if status is not None:
-        _arg("status", status, torch.int32, (batch,), dev)
-    with _on(dev, stream) as on:
-        if out is None:
-            out = torch.empty(q.shape, device=dev, dtype=odt)
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(int(lib.tv_chunk_attention_workspace_size(C.byref(prm))),
-                                    dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            _bad("workspace", f"a contiguous tensor on {dev}")
-        tail = [block_table.data_ptr(), seq_lens.data_ptr(), token_offsets.data_ptr(), out.data_ptr(),
-                status.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), on.ptr]
+        _arg("status", status, i32, (batch,), dev)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _bad("workspace", f"a contiguous tensor on CUDA device {dev}")
+
+    def call(handle):
+        o, st = _empty(out, qs, odt, dev), _empty(status, batch, i32, dev)
+        ws = workspace
+        if ws is None:
+            ws = _empty(None, int(lib.tv_chunk_attention_workspace_size(C.byref(prm))), torch.uint8, dev)
+        tail = (block_table.data_ptr(), seq_lens.data_ptr(), token_offsets.data_ptr(), o.data_ptr(),
+                st.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), handle)
         if fp8:
             rc = lib.tv_chunk_attention_fp8(C.byref(prm), q.data_ptr(), q_scale.data_ptr(), k_pool.data_ptr(),
                                             k_scale.data_ptr(), v_pool.data_ptr(), v_scale.data_ptr(), *tail)
         else:
             rc = lib.tv_chunk_attention(C.byref(prm), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), *tail)
-    if rc != TV_OK:
-        raise TVError(rc, "tv_chunk_attention_fp8" if fp8 else "tv_chunk_attention")
-    return out, status
+        if rc != TV_OK:
+            raise TVError(rc, "tv_chunk_attention_fp8" if fp8 else "tv_chunk_attention")
+        return o, st
+
+    return _run(dev, stream, call)
 
 
 def chunk_attention(q, k_pool, v_pool, block_table, seq_lens, token_offsets, *, max_len: int,
@@ -600,9 +640,7 @@ def chunk_attention(q, k_pool, v_pool, block_table, seq_lens, token_offsets, *, 
     max_len an upper bound of seq_lens.  Returns (out, status); nothing is
     synchronised."""
     return _chunk(q, None, k_pool, None, v_pool, None, block_table, seq_lens, token_offsets, out,
-                  status, workspace, stream,
-                  dict(max_len=max_len, window=window, sinks=sinks, softmax_scale=softmax_scale,
-                       out_dtype=out_dtype))
+                  status, workspace, stream, max_len, window, sinks, softmax_scale, out_dtype)
 
 
 def chunk_attention_fp8(q_codes, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens,
@@ -613,64 +651,68 @@ def chunk_attention_fp8(q_codes, q_scale, k_pool, k_scale, v_pool, v_scale, bloc
     (uint8) with one fp32 scale per row of 128; q_codes and q_scale come from
     quantize_rows, the pools from append_kv_fp8.  Returns (out, status);
     nothing is synchronised."""
+    if q_scale is None:
+        _bad("q_scale", "a tensor")
     return _chunk(q_codes, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens,
-                  token_offsets, out, status, workspace, stream,
-                  dict(max_len=max_len, window=window, sinks=sinks, softmax_scale=softmax_scale,
-                       out_dtype=out_dtype))
+                  token_offsets, out, status, workspace, stream, max_len, window, sinks,
+                  softmax_scale, out_dtype)
 
 
 # ---------------------------------------------------------------- the cache
 def _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, token_offsets, fp8):
-    import torch
-    dev = _cuda("k_pool", k_pool)
-    elem = torch.uint8 if fp8 else torch.bfloat16
-    _arg("k_pool", k_pool, elem, (None, None, TV_BLOCK_SIZE, None), dev)
-    _arg("v_pool", v_pool, elem, k_pool.shape, dev)
+    torch = _torch()
+    dev = _device("k_pool", k_pool)
+    i32, elem = torch.int32, torch.uint8 if fp8 else torch.bfloat16
+    ps = _dims("k_pool", k_pool, 4)
+    _arg("k_pool", k_pool, elem, (ps[0], ps[1], TV_BLOCK_SIZE, ps[3]), dev)
+    _arg("v_pool", v_pool, elem, ps, dev)
     if fp8:
-        _arg("k_scale", k_scale, torch.float32, k_pool.shape[:3], dev)
-        _arg("v_scale", v_scale, torch.float32, k_pool.shape[:3], dev)
-    _arg("seq_lens", seq_lens, torch.int32, (None,), dev)
-    batch = seq_lens.shape[0]
-    _arg("block_table", block_table, torch.int32, (batch, None), dev)
-    _arg("token_offsets", token_offsets, torch.int32, (batch + 1,), dev)
-    return dev, batch
+        _arg("k_scale", k_scale, torch.float32, ps[:3], dev)
+        _arg("v_scale", v_scale, torch.float32, ps[:3], dev)
+    (batch,) = _dims("seq_lens", seq_lens, 1)
+    _arg("seq_lens", seq_lens, i32, (batch,), dev)
+    width = _dims("block_table", block_table, 2)[1]
+    _arg("block_table", block_table, i32, (batch, width), dev)
+    _arg("token_offsets", token_offsets, i32, (batch + 1,), dev)
+    return dev, batch, width, ps
 
 
-def _row_pair(names, k, v, shape, dev):
-    """Checks K and V rows (bf16, strided by tokens alike); returns their stride."""
-    import torch
-    for name, t in zip(names, (k, v)):
-        _arg(name, t, torch.bfloat16, shape, dev, strided=1)
-    if _row_stride(k) != _row_stride(v):
+def _row_pair(names, k, v, hkv, d, dev):
+    """Checks K and V rows (bf16, strided by tokens alike); (rows, their stride)."""
+    bf16 = _torch().bfloat16
+    shape = (_dims(names[0], k, 3)[0], hkv, d)
+    stride = _rows(names[0], k, bf16, shape, dev)
+    if _rows(names[1], v, bf16, shape, dev) != stride:
         _bad(names[1], f"strided as {names[0]}")
-    return _row_stride(k)
+    return shape[0], stride
 
 
 def _append(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, k_scale, v_pool, v_scale,
             status, stream, fp8):
-    import torch
+    i32 = _torch().int32
     lib = load()
-    dev, batch = _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, token_offsets, fp8)
-    hkv, d = k_pool.shape[1], k_pool.shape[3]
-    stride = _row_pair(("k_new", "v_new"), k_new, v_new, (k_new.shape[0], hkv, d), dev)
+    dev, batch, width, ps = _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
+                                        token_offsets, fp8)
+    total, stride = _row_pair(("k_new", "v_new"), k_new, v_new, ps[1], ps[3], dev)
     if status is not None:
-        _arg("status", status, torch.int32, (batch,), dev)
-    prm = CacheParams(batch, hkv, d, TV_BLOCK_SIZE, block_table.shape[1], k_pool.shape[0],
-                      k_new.shape[0], stride)
-    with _on(dev, stream) as on:
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        head = [k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                token_offsets.data_ptr()]
+        _arg("status", status, i32, (batch,), dev)
+    prm = CacheParams(batch, ps[1], ps[3], TV_BLOCK_SIZE, width, ps[0], total, stride)
+
+    def call(handle):
+        st = _empty(status, batch, i32, dev)
+        rows = (k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                token_offsets.data_ptr())
         if fp8:
-            rc = lib.tv_append_kv_fp8(C.byref(prm), *head, k_pool.data_ptr(), k_scale.data_ptr(),
-                                      v_pool.data_ptr(), v_scale.data_ptr(), status.data_ptr(), on.ptr)
+            rc = lib.tv_append_kv_fp8(C.byref(prm), *rows, k_pool.data_ptr(), k_scale.data_ptr(),
+                                      v_pool.data_ptr(), v_scale.data_ptr(), st.data_ptr(), handle)
         else:
-            rc = lib.tv_append_kv(C.byref(prm), *head, k_pool.data_ptr(), v_pool.data_ptr(),
-                                  status.data_ptr(), on.ptr)
-    if rc != TV_OK:
-        raise TVError(rc, "tv_append_kv_fp8" if fp8 else "tv_append_kv")
-    return status
+            rc = lib.tv_append_kv(C.byref(prm), *rows, k_pool.data_ptr(), v_pool.data_ptr(),
+                                  st.data_ptr(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_append_kv_fp8" if fp8 else "tv_append_kv")
+        return st
+
+    return _run(dev, stream, call)
 
 
 def append_kv(k_new, v_new, block_table, seq_lens, token_offsets, k_pool, v_pool, *, status=None,
@@ -700,56 +742,58 @@ def read_kv_fp8(k_pool, k_scale, v_pool, v_scale, block_table, seq_lens, token_o
     rows [total_tokens, Hkv, D] (total_tokens >= token_offsets[-1]; taken from
     k_out where that is given).  Returns (k, v, status); nothing is
     synchronised."""
-    import torch
+    torch = _torch()
     lib = load()
-    dev, batch = _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, token_offsets, True)
-    hkv, d = k_pool.shape[1], k_pool.shape[3]
+    dev, batch, width, ps = _cache_args(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
+                                        token_offsets, True)
+    hkv, d = ps[1], ps[3]
     if (k_out is None) != (v_out is None) or (k_out is None and total_tokens is None):
         raise ValueError("read_kv_fp8 needs total_tokens, or both k_out and v_out")
-    if k_out is not None and total_tokens not in (None, k_out.shape[0]):
-        _bad("total_tokens", "the rows of k_out")
+    total, stride = total_tokens, 0
+    if k_out is not None:
+        total, stride = _row_pair(("k_out", "v_out"), k_out, v_out, hkv, d, dev)
+        if total_tokens not in (None, total):
+            _bad("total_tokens", "the rows of k_out")
     if status is not None:
         _arg("status", status, torch.int32, (batch,), dev)
-    with _on(dev, stream) as on:
-        if k_out is None:
-            k_out = torch.empty(int(total_tokens), hkv, d, dtype=torch.bfloat16, device=dev)
-            v_out = torch.empty_like(k_out)
-        stride = _row_pair(("k_out", "v_out"), k_out, v_out, (k_out.shape[0], hkv, d), dev)
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        prm = CacheParams(batch, hkv, d, TV_BLOCK_SIZE, block_table.shape[1], k_pool.shape[0],
-                          k_out.shape[0], stride)
+    prm = CacheParams(batch, hkv, d, TV_BLOCK_SIZE, width, ps[0], total, stride)
+
+    def call(handle):
+        k, v = _empty(k_out, (total, hkv, d), torch.bfloat16, dev), _empty(v_out, (total, hkv, d), torch.bfloat16, dev)
+        st = _empty(status, batch, torch.int32, dev)
         rc = lib.tv_read_kv_fp8(C.byref(prm), k_pool.data_ptr(), k_scale.data_ptr(), v_pool.data_ptr(),
                                 v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                                token_offsets.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
-                                status.data_ptr(), on.ptr)
-    if rc != TV_OK:
-        raise TVError(rc, "tv_read_kv_fp8")
-    return k_out, v_out, status
+                                token_offsets.data_ptr(), k.data_ptr(), v.data_ptr(), st.data_ptr(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_read_kv_fp8")
+        return k, v, st
+
+    return _run(dev, stream, call)
 
 
 def quantize_rows(x, *, codes=None, scale=None, stream=None):
     """tv_quantize_rows: bf16 rows [tokens, heads, D] (which may be strided by
     tokens) to E4M3 codes [tokens, heads, D] uint8 and scales [tokens, heads]
     fp32.  Returns (codes, scale); nothing is synchronised."""
-    import torch
+    torch = _torch()
     lib = load()
-    dev = _cuda("x", x)
-    _arg("x", x, torch.bfloat16, (None, None, None), dev, strided=1)
+    dev = _device("x", x)
+    xs = _dims("x", x, 3)
+    stride = _rows("x", x, torch.bfloat16, xs, dev)
     if codes is not None:
-        _arg("codes", codes, torch.uint8, x.shape, dev)
+        _arg("codes", codes, torch.uint8, xs, dev)
     if scale is not None:
-        _arg("scale", scale, torch.float32, x.shape[:2], dev)
-    with _on(dev, stream) as on:
-        if codes is None:
-            codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
-        if scale is None:
-            scale = torch.empty(x.shape[:2], dtype=torch.float32, device=dev)
-        prm = QuantParams(x.shape[0], x.shape[1], x.shape[2], _row_stride(x))
-        rc = lib.tv_quantize_rows(C.byref(prm), x.data_ptr(), codes.data_ptr(), scale.data_ptr(), on.ptr)
-    if rc != TV_OK:
-        raise TVError(rc, "tv_quantize_rows")
-    return codes, scale
+        _arg("scale", scale, torch.float32, xs[:2], dev)
+    prm = QuantParams(xs[0], xs[1], xs[2], stride)
+
+    def call(handle):
+        c, s = _empty(codes, xs, torch.uint8, dev), _empty(scale, xs[:2], torch.float32, dev)
+        rc = lib.tv_quantize_rows(C.byref(prm), x.data_ptr(), c.data_ptr(), s.data_ptr(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_quantize_rows")
+        return c, s
+
+    return _run(dev, stream, call)
 
 
 def commit_kv_fp8(k_nodes, k_nodes_scale, v_nodes, v_nodes_scale, parent, node_offsets,
@@ -759,48 +803,49 @@ def commit_kv_fp8(k_nodes, k_nodes_scale, v_nodes, v_nodes_scale, parent, node_o
     """tv_commit_kv_fp8: commit_kv of an E4M3 cache (codes and scales of the
     tree nodes, as tree_attention_fp8 takes them, copied to the pools in place).
     Returns (new_prefix_lens, status); nothing is synchronised."""
-    import torch
+    torch = _torch()
     lib = load()
-    dev = _cuda("k_nodes", k_nodes)
-    i32, f32 = torch.int32, torch.float32
-    _arg("k_nodes", k_nodes, torch.uint8, (None, None, None), dev)
-    total, hkv, d = k_nodes.shape
-    _arg("v_nodes", v_nodes, torch.uint8, k_nodes.shape, dev)
-    _arg("k_nodes_scale", k_nodes_scale, f32, (total, hkv), dev)
-    _arg("v_nodes_scale", v_nodes_scale, f32, (total, hkv), dev)
-    _arg("prefix_lens", prefix_lens, i32, (None,), dev)
-    batch = prefix_lens.shape[0]
-    for name, t, shape in (("parent", parent, (total,)), ("node_offsets", node_offsets, (batch + 1,)),
-                           ("accepted_len", accepted_len, (batch,)), ("path", path, (batch, int(max_nodes))),
-                           ("block_table", block_table, (batch, None))):
-        _arg(name, t, i32, shape, dev)
-    _arg("k_prefix_blocks", k_prefix_blocks, torch.uint8, (None, hkv, TV_BLOCK_SIZE, d), dev)
-    _arg("v_prefix_blocks", v_prefix_blocks, torch.uint8, k_prefix_blocks.shape, dev)
-    _arg("k_prefix_scale", k_prefix_scale, f32, k_prefix_blocks.shape[:3], dev)
-    _arg("v_prefix_scale", v_prefix_scale, f32, k_prefix_blocks.shape[:3], dev)
-    if new_prefix_lens is not None:
-        _arg("new_prefix_lens", new_prefix_lens, i32, (batch,), dev)
-    if status is not None:
-        _arg("status", status, i32, (batch,), dev)
-    prm = CommitParams(batch, hkv, d, TV_BLOCK_SIZE, block_table.shape[1], k_prefix_blocks.shape[0],
-                       int(max_nodes), total)
-    with _on(dev, stream) as on:
-        if new_prefix_lens is None:
-            new_prefix_lens = torch.empty(batch, dtype=i32, device=dev)
-        if status is None:
-            status = torch.empty(batch, dtype=i32, device=dev)
+    dev = _device("k_nodes", k_nodes)
+    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+    total, hkv, d = _dims("k_nodes", k_nodes, 3)
+    ps = _dims("k_prefix_blocks", k_prefix_blocks, 4)
+    (batch,) = _dims("prefix_lens", prefix_lens, 1)
+    width = _dims("block_table", block_table, 2)[1]
+    for name, t, dtype, shape in (
+            ("k_nodes", k_nodes, u8, (total, hkv, d)), ("v_nodes", v_nodes, u8, (total, hkv, d)),
+            ("k_nodes_scale", k_nodes_scale, f32, (total, hkv)),
+            ("v_nodes_scale", v_nodes_scale, f32, (total, hkv)), ("parent", parent, i32, (total,)),
+            ("node_offsets", node_offsets, i32, (batch + 1,)), ("accepted_len", accepted_len, i32, (batch,)),
+            ("path", path, i32, (batch, max_nodes)), ("block_table", block_table, i32, (batch, width)),
+            ("prefix_lens", prefix_lens, i32, (batch,)),
+            ("k_prefix_blocks", k_prefix_blocks, u8, (ps[0], hkv, TV_BLOCK_SIZE, d)),
+            ("v_prefix_blocks", v_prefix_blocks, u8, ps), ("k_prefix_scale", k_prefix_scale, f32, ps[:3]),
+            ("v_prefix_scale", v_prefix_scale, f32, ps[:3]),
+            ("new_prefix_lens", new_prefix_lens, i32, (batch,)), ("status", status, i32, (batch,))):
+        if t is not None or name not in ("new_prefix_lens", "status"):
+            _arg(name, t, dtype, shape, dev)
+    prm = CommitParams(batch, hkv, d, TV_BLOCK_SIZE, width, ps[0], max_nodes, total)
+
+    def call(handle):
+        new, st = _empty(new_prefix_lens, batch, i32, dev), _empty(status, batch, i32, dev)
         rc = lib.tv_commit_kv_fp8(
             C.byref(prm), k_nodes.data_ptr(), k_nodes_scale.data_ptr(), v_nodes.data_ptr(),
             v_nodes_scale.data_ptr(), parent.data_ptr(), node_offsets.data_ptr(), accepted_len.data_ptr(),
             path.data_ptr(), block_table.data_ptr(), prefix_lens.data_ptr(), k_prefix_blocks.data_ptr(),
             k_prefix_scale.data_ptr(), v_prefix_blocks.data_ptr(), v_prefix_scale.data_ptr(),
-            new_prefix_lens.data_ptr(), status.data_ptr(), on.ptr)
-    if rc != TV_OK:
-        raise TVError(rc, "tv_commit_kv_fp8")
-    return new_prefix_lens, status
+            new.data_ptr(), st.data_ptr(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_commit_kv_fp8")
+        return new, st
+
+    return _run(dev, stream, call)
 
 
 # ---------------------------------------------------------------- logits
+def _ptr_or_null(t):
+    return None if t is None else t.data_ptr() or None
+
+
 def penalize_logits(logits, draft_tokens, parent, node_offsets, *, max_nodes: int, history=None,
                     history_offsets=None, prompt_lens=None, repetition=None, presence=None,
                     frequency=None, bias_ids=None, bias_values=None, bias_offsets=None,
@@ -813,43 +858,58 @@ def penalize_logits(logits, draft_tokens, parent, node_offsets, *, max_nodes: in
     history_offsets and bias_offsets [B+1]; prompt_lens [B] int32; repetition,
     presence, frequency [B] fp32; allowed_mask [total, ceil(V/32)] int32 or
     uint32 bits.  Returns (out, status); nothing is synchronised."""
-    import torch
+    torch = _torch()
     lib = load()
     i32, f32 = torch.int32, torch.float32
-    dev = _cuda("logits", logits)
-    _arg("logits", logits, (f32, torch.bfloat16), (None, None), dev)
-    total, vocab = logits.shape
-    _arg("node_offsets", node_offsets, i32, (None,), dev)
-    batch = node_offsets.shape[0] - 1
+    dev = _device("logits", logits)
+    total, vocab = _dims("logits", logits, 2)
+    if logits.dtype is not f32 and logits.dtype is not torch.bfloat16:
+        _bad("logits", f"of type float32 or bfloat16, not {logits.dtype}")
+    _arg("logits", logits, logits.dtype, (total, vocab), dev)
+    batch = _dims("node_offsets", node_offsets, 1)[0] - 1
+    _arg("node_offsets", node_offsets, i32, (batch + 1,), dev)
     _arg("draft_tokens", draft_tokens, i32, (total,), dev)
     _arg("parent", parent, i32, (total,), dev)
+    n_hist = n_bias = 0
     if (history is None) != (history_offsets is None):
         raise ValueError("history and history_offsets go together")
-    if len({bias_ids is None, bias_values is None, bias_offsets is None}) != 1:
+    if history is not None:
+        (n_hist,) = _dims("history", history, 1)
+        _arg("history", history, i32, (n_hist,), dev)
+        _arg("history_offsets", history_offsets, i32, (batch + 1,), dev)
+    if (bias_ids is None) != (bias_values is None) or (bias_ids is None) != (bias_offsets is None):
         raise ValueError("bias_ids, bias_values and bias_offsets go together")
-    n_bias = None if bias_ids is None else bias_ids.shape[0]
-    for name, t, dtype, shape in (
-            ("history", history, i32, (None,)), ("history_offsets", history_offsets, i32, (batch + 1,)),
-            ("prompt_lens", prompt_lens, i32, (batch,)), ("repetition", repetition, f32, (batch,)),
-            ("presence", presence, f32, (batch,)), ("frequency", frequency, f32, (batch,)),
-            ("bias_ids", bias_ids, i32, (None,)), ("bias_values", bias_values, f32, (n_bias,)),
-            ("bias_offsets", bias_offsets, i32, (batch + 1,)),
-            ("allowed_mask", allowed_mask, (i32, torch.uint32), (total, (vocab + 31) // 32)),
-            ("out", out, f32, (total, vocab)), ("status", status, i32, (batch,))):
+    if bias_ids is not None:
+        (n_bias,) = _dims("bias_ids", bias_ids, 1)
+        _arg("bias_ids", bias_ids, i32, (n_bias,), dev)
+        _arg("bias_values", bias_values, f32, (n_bias,), dev)
+        _arg("bias_offsets", bias_offsets, i32, (batch + 1,), dev)
+    if prompt_lens is not None:
+        _arg("prompt_lens", prompt_lens, i32, (batch,), dev)
+    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
         if t is not None:
-            _arg(name, t, dtype, shape, dev)
-    prm = PenaltyParams(batch, vocab, int(max_nodes), total, 0 if history is None else history.shape[0],
-                        n_bias or 0, 1 if logits.dtype == f32 else 0)
-    p = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()  # noqa: E731
-    with _on(dev, stream) as on:
-        if out is None:
-            out = torch.empty(total, vocab, dtype=f32, device=dev)
-        if status is None:
-            status = torch.empty(batch, dtype=i32, device=dev)
-        rc = lib.tv_penalize_logits(C.byref(prm), p(logits), p(draft_tokens), p(parent), p(node_offsets),
-                                    p(history), p(history_offsets), p(prompt_lens), p(repetition),
-                                    p(presence), p(frequency), p(bias_ids), p(bias_values), p(bias_offsets),
-                                    p(allowed_mask), p(out), p(status), on.ptr)
-    if rc != TV_OK:
-        raise TVError(rc, "tv_penalize_logits")
-    return out, status
+            _arg(name, t, f32, (batch,), dev)
+    if allowed_mask is not None:
+        bits = torch.uint32 if getattr(allowed_mask, "dtype", None) is torch.uint32 else i32
+        _arg("allowed_mask", allowed_mask, bits, (total, (vocab + 31) // 32), dev)
+    if out is not None:
+        _arg("out", out, f32, (total, vocab), dev)
+    if status is not None:
+        _arg("status", status, i32, (batch,), dev)
+    prm = PenaltyParams(batch, vocab, max_nodes, total, n_hist, n_bias, 1 if logits.dtype is f32 else 0)
+
+    def call(handle):
+        o, st = _empty(out, (total, vocab), f32, dev), _empty(status, batch, i32, dev)
+        p = _ptr_or_null
+        rc = lib.tv_penalize_logits(
+            C.byref(prm), p(logits), p(draft_tokens), p(parent), p(node_offsets),
+            # (an empty list has no address: none at all)
+            *((p(history), history_offsets.data_ptr()) if n_hist else (None, None)),
+            p(prompt_lens), p(repetition), p(presence), p(frequency),
+            *((p(bias_ids), p(bias_values), bias_offsets.data_ptr()) if n_bias else (None, None, None)),
+            p(allowed_mask), p(o), p(st), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_penalize_logits")
+        return o, st
+
+    return _run(dev, stream, call)
