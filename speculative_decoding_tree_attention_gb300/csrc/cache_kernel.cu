@@ -5,9 +5,17 @@
 // Quantisation of a row x of D values: s = fl32(max |x_i| / 448) over the
 // finite entries (at least 2^-126; 1 for a row of zeros), code_i = the E4M3
 // value nearest to the real quotient x_i / s, ties to even, saturating at 448;
-// NaN gives NaN.  The quotient is rounded once: q = x fl(1/s) is within 2 ulp
-// of it, and only where q lies that close to a border between two codes is the
-// quotient divided out and its remainder looked at (quantise below).
+// NaN gives NaN.
+//
+// The quotient is rounded once without dividing each value.  The middle of two
+// codes is c 2^j with c odd, c < 32, and with m = max |x_i|
+//   448 x / m = c 2^j   <=>   7 X 2^k = c A   for the 8-bit integers X, A of x
+// and m: either equal, or apart by 1 in c A < 2^13.  So a product q = x fl(1/s),
+// within 2^-22 of the quotient, rounds as it does unless 448 x / m is a middle
+// itself.  There x / s = (448 x / m) (m / (448 s)) lies on the side on which
+// 448 s rounded off m, the same for the whole row: 1/s is moved by 2^-20 to that
+// side.  Where s is exact (m a multiple of 7, or a clamped s) the middles have
+// to be met exactly: q takes one correction by its remainder.
 //
 // All of it is one read and one write of each row, bound by HBM for prompts and
 // by latency for single tokens.  A row is taken by D / 8 lanes, 16 bytes of
@@ -36,31 +44,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// A value whose E4M3 rounding is that of the real quotient x / s, given
-// inv = fl(1/s).  q = fl(x inv) is within 2 ulp of x / s, so the two round
-// alike unless q is that close to a border: the middle of two codes, where the
-// 20 mantissa bits below the code's are 0x80000 (below 2^-6 the codes are
-// equidistant: 2^-6 is added first).  There, the quotient rounded to odd (its
-// last bit set when the division leaves a remainder, whose sign the fused
-// multiply-add gives exactly) never is a border itself and rounds as x / s.
-__device__ __forceinline__ float quantise(float x, float s, float inv) {
-  const float q = x * inv;
-  const float a = fabsf(q);
-  const uint32_t z = __float_as_uint(a < 0x1p-6f ? a + 0x1p-6f : a);
-  if ((z & 0xfffffu) - 0x80000u + 8u > 16u) return q;
-  const float k = s < 1.0f ? 0x1p64f : 1.0f;  // (keeps the remainder a normal number)
-  const float xa = fabsf(x) * k, sk = s * k;
-  const float d = __fdiv_rn(xa, sk);
-  const float rem = __fmaf_rn(-d, sk, xa);
-  uint32_t bits = __float_as_uint(d);
-  if (rem != 0.0f && !(bits & 1u)) bits = rem > 0.0f ? bits + 1u : bits - 1u;
-  return copysignf(__uint_as_float(bits), x);
-}
-
 // The scale of a row of which this lane holds 8 values (w) and the LANES lanes
-// around it the rest.
+// around it the rest, and the factor that takes a value to its code's quotient.
+struct Scale {
+  float s, inv;
+  bool exact;  // 448 s is the row's largest magnitude (or s is the clamp)
+};
 template <int LANES>
-__device__ __forceinline__ float row_scale(const uint4& w) {
+__device__ __forceinline__ Scale row_scale(const uint4& w) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
   uint32_t m = 0;  // largest finite magnitude, as bf16 bits
 #pragma unroll
@@ -71,16 +62,35 @@ __device__ __forceinline__ float row_scale(const uint4& w) {
   }
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m == 0 ? 1.0f : fmaxf(__fdiv_rn(__uint_as_float(m << 16), 448.0f), 0x1p-126f);
+  const float amax = __uint_as_float(m << 16);
+  Scale r;
+  r.s = m == 0 ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f);
+  r.inv = __fdiv_rn(1.0f, r.s);
+  const float off = __fmaf_rn(-r.s, 448.0f, amax);  // (exact)
+  r.exact = off == 0.0f || r.s == 0x1p-126f || m == 0;
+  if (!r.exact) r.inv = __fmaf_rn(r.inv, off > 0.0f ? 0x1p-20f : -0x1p-20f, r.inv);
+  return r;
 }
 
-__device__ __forceinline__ uint2 row_codes(const uint4& w, float s) {
-  const float inv = __fdiv_rn(1.0f, s);
+__device__ __forceinline__ uint2 row_codes(const uint4& w, const Scale& r) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint32_t c[4];
+  float q[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) c[k] = e4m3x2(quantise(bf16_lo(v[k]), s, inv), quantise(bf16_hi(v[k]), s, inv));
-  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  for (int k = 0; k < 4; ++k) {
+    q[2 * k] = bf16_lo(v[k]) * r.inv;
+    q[2 * k + 1] = bf16_hi(v[k]) * r.inv;
+  }
+  if (r.exact) {
+    const float up = r.s < 1.0f ? 0x1p64f : 1.0f;  // (keeps the remainder a normal number)
+    const float s = r.s * up, inv = r.inv / up;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = (k & 1 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2])) * up;
+      const float rem = __fmaf_rn(-q[k], s, x);
+      if (rem > 0.0f || rem < 0.0f) q[k] = __fmaf_rn(rem, inv, q[k]);  // (not for NaN, nor -0)
+    }
+  }
+  return make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
 }
 
 // Where each token of a CTA's tile goes.
@@ -222,10 +232,10 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a) {
       if (OP == kCopy) {
         if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = w[u];
       } else if (OP == kQuantise) {
-        const float sc = row_scale<kLanes>(w[u]);  // (every lane takes part in the shuffles)
+        const Scale sc = row_scale<kLanes>(w[u]);  // (every lane takes part in the shuffles)
         if (dst[u]) {
           *reinterpret_cast<uint2*>(dst[u]) = row_codes(w[u], sc);
-          if (sub == 0) *sdst[u] = sc;
+          if (sub == 0) *sdst[u] = sc.s;
         }
       } else if (dst[u]) {
         // the fp32 product of code and scale, rounded to bf16
@@ -264,10 +274,10 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const QuantArgs
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const long long r = r0 + u * step;
-      const float s = row_scale<kLanes>(w[u]);
+      const Scale s = row_scale<kLanes>(w[u]);
       if (r >= rows) continue;
       reinterpret_cast<uint2*>(a.codes + r * D)[sub] = row_codes(w[u], s);
-      if (sub == 0) a.scale[r] = s;
+      if (sub == 0) a.scale[r] = s.s;
     }
   }
 }

@@ -102,11 +102,14 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   bool bad = !rows_ok || N > a.max_nodes || h0 < 0 || h1 < h0 || h1 > a.total_history || e0 < 0 || e1 < e0 ||
              e1 > a.total_bias || !(r.rep > 0.0f && r.rep < INFINITY) || !(fabsf(r.pres) < INFINITY) ||
              !(fabsf(r.freq) < INFINITY);
-  for (int i = tid; i < kChunk; i += kThreads) {
-    s.count[i] = 0u;
-    s.entry[i] = -1;
+  const uint4 zero = make_uint4(0, 0, 0, 0), none = make_uint4(~0u, ~0u, ~0u, ~0u);
+#pragma unroll
+  for (int i = 4 * tid; i < kChunk; i += 4 * kThreads) {
+    *reinterpret_cast<uint4*>(&s.count[i]) = zero;
+    if (a.bias_ids) *reinterpret_cast<uint4*>(&s.entry[i]) = none;
   }
-  for (int i = tid; i < kWarps * (kChunk / 32); i += kThreads) (&s.path[0][0])[i] = 0u;
+  *reinterpret_cast<uint4*>(&s.path[0][0] + 4 * tid) = zero;
+  static_assert(kWarps * (kChunk / 32) == 4 * kThreads, "one store per thread clears the bitmaps");
   __syncthreads();
   if (!bad) {
     for (int i = tid; i < N; i += kThreads) {
@@ -117,13 +120,19 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     }
     // history: ids outside the chunk (and outside the vocabulary) do not count
     const int prompt = a.prompt_lens ? max(0, __ldg(a.prompt_lens + b)) : 0;
-    for (int i = h0 + tid; i < h1; i += kThreads) {
-      const int v = __ldg(a.history + i) - c0;
-      if (v < 0 || v >= nv) continue;
-      if (i - h0 < prompt) {
-        atomicOr(&s.count[v], kPrompt);
-      } else {
-        atomicAdd(&s.count[v], 1u);
+    constexpr int kH = 8;  // entries in flight
+    for (int i0 = h0 + tid; i0 < h1; i0 += kThreads * kH) {
+      int v[kH];
+#pragma unroll
+      for (int k = 0; k < kH; ++k) v[k] = i0 + k * kThreads < h1 ? __ldg(a.history + i0 + k * kThreads) - c0 : -1;
+#pragma unroll
+      for (int k = 0; k < kH; ++k) {
+        if (v[k] < 0 || v[k] >= nv) continue;
+        if (i0 + k * kThreads - h0 < prompt) {
+          atomicOr(&s.count[v[k]], kPrompt);
+        } else {
+          atomicAdd(&s.count[v[k]], 1u);
+        }
       }
     }
     for (int i = e0 + tid; i < e1; i += kThreads) {
