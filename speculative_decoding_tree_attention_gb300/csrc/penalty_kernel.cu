@@ -15,10 +15,15 @@
 // each step one fp32 rounding.
 //
 // One CTA takes a chunk of 4096 vocabulary entries of the rows of one tree (or
-// of a share of them): it counts the sequence's history and bias list into
-// shared memory once, then each warp streams rows through it, one read and one
-// write of HBM per entry.  Path tokens are few: a row that has any in the chunk
-// gets them computed apart, from a bitmap that the stream skips.
+// of a share of them).  It counts the sequence's history and bias list into
+// shared memory once and lists the touched entries.  Each warp then streams
+// rows through: a masked copy (one read and one write of HBM per entry), after
+// which the row's touched entries are gathered again from L2 and rewritten, a
+// lane each, and so are the few tokens of the row's path, which have a count of
+// their own.  (With the penalties inside the stream every warp step met some
+// touched entry and ran their divisions for 16 of 32 lanes: 82 us instead of
+// the figures below.)
+//
 #include <math.h>
 
 #include "tv_device.cuh"
@@ -39,38 +44,58 @@ struct Shared {
     int entry[kChunk];   // last bias entry of a token
     float bias[kChunk];
   };
-  uint32_t path[kWarps][kChunk / 32];
-  int parent[kMaxNodes];
+  uint32_t path[kWarps][kChunk / 32];  // a warp's row: tokens of its path
+  uint16_t touched[kChunk];            // entries with a count or a bias
   int token[kMaxNodes];
+  int16_t parent[kMaxNodes];
+  int ntouched;
   int bad;
 };
+static_assert(sizeof(Shared) <= 49152, "four CTAs an SM, no opt-in");
 
 struct Rates {
   float rep, pres, freq;
 };
 
-__device__ __forceinline__ float apply(float x, uint32_t word, uint32_t more, float bias, bool allowed, const Rates& r) {
+__device__ __forceinline__ float apply(float x, uint32_t word, uint32_t more, float bias, const Rates& r) {
   const uint32_t c = (word & ~kPrompt) + more;
   if (c > 0 || word) x = x > 0.0f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
   if (c > 0) x = __fsub_rn(__fsub_rn(x, __fmul_rn(r.freq, static_cast<float>(c))), r.pres);
-  x = __fadd_rn(x, bias);
-  return allowed ? x : -INFINITY;
+  return __fadd_rn(x, bias);
 }
 
+// one logit of a row; read_logit's may have been written by this warp before
+// (in place), so it goes through the ordinary path
+template <bool BF16>
+__device__ __forceinline__ float read_logit(const void* row, int v) {
+  return BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[v]) << 16)
+              : static_cast<const float*>(row)[v];
+}
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* row, int v) {
   return BF16 ? __uint_as_float(static_cast<uint32_t>(__ldcs(static_cast<const uint16_t*>(row) + v)) << 16)
               : __ldcs(static_cast<const float*>(row) + v);
 }
+// four of them, as loaded
 template <bool BF16>
-__device__ __forceinline__ float4 load_logit4(const void* row, int v) {
-  if (BF16) {
-    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + v));
+struct Raw4 {
+  uint2 w;
+  __device__ __forceinline__ void load(const void* row, int v) {
+    w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + v));
+  }
+  __device__ __forceinline__ float4 value() const {
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                        __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
   }
-  return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + v));
-}
+};
+template <>
+struct Raw4<false> {
+  float4 w;
+  __device__ __forceinline__ void load(const void* row, int v) {
+    w = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + v));
+  }
+  __device__ __forceinline__ float4 value() const { return w; }
+};
 
 // BF16: the logits' type (else fp32).  VEC: rows are 4-entry aligned.
 template <bool BF16, bool VEC>
@@ -96,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   r.rep = a.repetition ? __ldg(a.repetition + b) : 1.0f;
   r.pres = a.presence ? __ldg(a.presence + b) : 0.0f;
   r.freq = a.frequency ? __ldg(a.frequency + b) : 0.0f;
-  if (tid == 0) s.bad = 0;
+  if (tid == 0) s.bad = s.ntouched = 0;
   const bool rows_ok = nodes >= 1 && n0 >= 0 && n0 + nodes <= a.total_nodes;
   const int N = rows_ok ? static_cast<int>(nodes) : 0;
   bool bad = !rows_ok || N > a.max_nodes || h0 < 0 || h1 < h0 || h1 > a.total_history || e0 < 0 || e1 < e0 ||
@@ -114,13 +139,13 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   if (!bad) {
     for (int i = tid; i < N; i += kThreads) {
       const int p = __ldg(a.parent + n0 + i);
-      s.parent[i] = p;
+      s.parent[i] = static_cast<int16_t>(p);
       s.token[i] = __ldg(a.tokens + n0 + i);
       if (i == 0 ? p != -1 : (p < 0 || p >= i)) s.bad = 1;
     }
     // history: ids outside the chunk (and outside the vocabulary) do not count
     const int prompt = a.prompt_lens ? max(0, __ldg(a.prompt_lens + b)) : 0;
-    constexpr int kH = 8;  // entries in flight
+    constexpr int kH = 16;  // entries in flight
     for (int i0 = h0 + tid; i0 < h1; i0 += kThreads * kH) {
       int v[kH];
 #pragma unroll
@@ -144,18 +169,16 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   bad = bad || s.bad;
   if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) a.status[b] = bad ? kBadTree : kOk;
   if (!rows_ok) return;
-  if (bad) {  // the rows as given
-    for (int i = tid; i < kChunk; i += kThreads) s.count[i] = 0u;
-    __syncthreads();
-  }
-  if (a.bias_ids) {
+  const bool has_bias = a.bias_ids != nullptr;
+  if (!bad) {
     for (int i = tid; i < kChunk; i += kThreads) {
-      const int e = s.entry[i];
-      s.bias[i] = e >= 0 ? __ldg(a.bias_values + e) : 0.0f;
+      const int e = has_bias ? s.entry[i] : -1;
+      if (has_bias) s.bias[i] = e >= 0 ? __ldg(a.bias_values + e) : 0.0f;
+      if (s.count[i] || e >= 0) s.touched[atomicAdd(&s.ntouched, 1)] = static_cast<uint16_t>(i);
     }
     __syncthreads();
   }
-  const bool has_bias = a.bias_ids != nullptr && !bad;
+  const int ntouched = bad ? 0 : s.ntouched;  // (bad: the rows as given)
   const uint32_t* mask = bad ? nullptr : a.allowed_mask;
   const int words = (a.vocab + 31) / 32;
   uint32_t* path = s.path[warp];
@@ -164,104 +187,109 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     const void* in = static_cast<const uint8_t*>(a.logits) + row * a.vocab * (BF16 ? 2 : 4);
     float* out = a.out + row * a.vocab;
     const uint32_t* mrow = mask ? mask + row * words : nullptr;
-    // the drafted tokens of the path in this chunk: lane k looks at every 32nd
-    // ancestor from the node up; the first node with a token computes it
-    bool any = false;
-    if (!bad) {
-      int j = i;
-      for (int k = 0; k < lane && j > 0; ++k) j = s.parent[j];
-      while (__any_sync(0xffffffffu, j > 0)) {
-        const int v = j > 0 ? s.token[j] - c0 : -1;
-        bool mine = v >= 0 && v < nv;
-        if (mine) {
-          uint32_t more = 0;
-          for (int m = i; m > 0; m = s.parent[m]) {
-            if (s.token[m] != v + c0) continue;
-            if (more == 0 && m != j) {  // (a node nearer to i has it)
-              mine = false;
-              break;
-            }
-            ++more;
+    // a masked copy, 1024 entries (a mask word a lane) at a time, the next ones
+    // in flight while these are stored
+    Raw4<BF16> x[8];
+    uint32_t mw = ~0u;
+    auto fetch = [&](int b0) {
+      if (VEC) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int v = b0 + 128 * u + 4 * lane;
+          if (v < nv) x[u].load(in, c0 + v);
+        }
+      }
+      if (mrow && b0 + 32 * lane < nv) mw = __ldg(mrow + ((c0 + b0) >> 5) + lane);
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int b0 = 0; b0 < nv; b0 += 1024) {
+      const uint32_t word = mw;
+      if (VEC) {
+        float4 y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) y[u] = x[u].value();
+        fetch(b0 + 1024);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int v = b0 + 128 * u + 4 * lane;
+          const uint32_t ok = __shfl_sync(0xffffffffu, word, 4 * u + (lane >> 3)) >> (v & 31);
+          if (v < nv)
+            *reinterpret_cast<float4*>(out + c0 + v) =
+                make_float4(ok & 1u ? y[u].x : -INFINITY, ok & 2u ? y[u].y : -INFINITY,
+                            ok & 4u ? y[u].z : -INFINITY, ok & 8u ? y[u].w : -INFINITY);
+        }
+      } else {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          constexpr int kU = 16;
+          float z[kU];
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int v = b0 + 512 * half + 32 * u + lane;
+            if (v < nv) z[u] = load_logit<BF16>(in, c0 + v);
           }
-          if (mine) {
-            const bool ok = !mrow || (__ldg(mrow + ((c0 + v) >> 5)) >> ((c0 + v) & 31) & 1u);
-            const float x = load_logit<BF16>(in, c0 + v);
-            out[c0 + v] = apply(x, s.count[v], more, has_bias ? s.bias[v] : 0.0f, ok, r);
-            atomicOr(&path[v >> 5], 1u << (v & 31));
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int v = b0 + 512 * half + 32 * u + lane;
+            const uint32_t ok = __shfl_sync(0xffffffffu, word, 16 * half + u) >> lane & 1u;
+            if (v < nv) out[c0 + v] = ok ? z[u] : -INFINITY;
           }
         }
-        any |= __any_sync(0xffffffffu, mine);
-        for (int k = 0; k < 32 && j > 0; ++k) j = s.parent[j];
+        fetch(b0 + 1024);
       }
-      __syncwarp();
     }
-    if (VEC) {
-      constexpr int kU = 4;
-#pragma unroll 1
-      for (int q0 = 4 * lane; q0 < nv; q0 += 128 * kU) {
-        float4 x[kU];
-        uint32_t ok[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int v = q0 + 128 * u;
-          if (v >= nv) continue;
-          x[u] = load_logit4<BF16>(in, c0 + v);
-          ok[u] = mrow ? __ldg(mrow + ((c0 + v) >> 5)) >> (v & 31) : 15u;
+    if (bad) continue;
+    __syncwarp();
+    // From here on entries are read again, each before it is rewritten: an
+    // allowed one still holds its logit in place, a masked one stays -inf.
+    auto allowed = [&](int v) { return !mrow || (__ldg(mrow + ((c0 + v) >> 5)) >> (v & 31) & 1u); };
+    // the drafted tokens of the path in this chunk: lane k looks at every 32nd
+    // ancestor from the node up; the node nearest to the row computes a token
+    bool any = false;
+    int j = i;
+    for (int k = 0; k < lane && j > 0; ++k) j = s.parent[j];
+    while (__any_sync(0xffffffffu, j > 0)) {
+      const int v = j > 0 ? s.token[j] - c0 : -1;
+      bool mine = v >= 0 && v < nv;
+      if (mine) {
+        uint32_t more = 0;
+        for (int m = i; m > 0; m = s.parent[m]) {
+          if (s.token[m] != v + c0) continue;
+          if (more == 0 && m != j) {
+            mine = false;
+            break;
+          }
+          ++more;
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int v = q0 + 128 * u;
-          if (v >= nv) continue;
-          const uint4 c = *reinterpret_cast<const uint4*>(&s.count[v]);
-          float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (has_bias) bias = *reinterpret_cast<const float4*>(&s.bias[v]);
-          float4 y;
-          if ((c.x | c.y | c.z | c.w) == 0u) {
-            y = make_float4(x[u].x + bias.x, x[u].y + bias.y, x[u].z + bias.z, x[u].w + bias.w);
-            if (!has_bias) y = x[u];  // (keeps a -0)
-            y.x = ok[u] & 1u ? y.x : -INFINITY;
-            y.y = ok[u] & 2u ? y.y : -INFINITY;
-            y.z = ok[u] & 4u ? y.z : -INFINITY;
-            y.w = ok[u] & 8u ? y.w : -INFINITY;
-          } else {
-            y.x = apply(x[u].x, c.x, 0, bias.x, ok[u] & 1u, r);
-            y.y = apply(x[u].y, c.y, 0, bias.y, ok[u] & 2u, r);
-            y.z = apply(x[u].z, c.z, 0, bias.z, ok[u] & 4u, r);
-            y.w = apply(x[u].w, c.w, 0, bias.w, ok[u] & 8u, r);
-          }
-          const uint32_t skip = any ? path[v >> 5] >> (v & 31) & 15u : 0u;
-          if (skip == 0u) {
-            __stcs(reinterpret_cast<float4*>(out + c0 + v), y);
-          } else {
-            if (!(skip & 1u)) out[c0 + v] = y.x;
-            if (!(skip & 2u)) out[c0 + v + 1] = y.y;
-            if (!(skip & 4u)) out[c0 + v + 2] = y.z;
-            if (!(skip & 8u)) out[c0 + v + 3] = y.w;
-          }
+        if (mine) {
+          if (allowed(v))
+            out[c0 + v] = apply(read_logit<BF16>(in, c0 + v), s.count[v], more, has_bias ? s.bias[v] : 0.0f, r);
+          atomicOr(&path[v >> 5], 1u << (v & 31));
         }
       }
-    } else {
-      constexpr int kU = 8;
-#pragma unroll 1
-      for (int q0 = lane; q0 < nv; q0 += 32 * kU) {
-        float x[kU];
-        uint32_t ok[kU];
+      any |= __any_sync(0xffffffffu, mine);
+      for (int k = 0; k < 32 && j > 0; ++k) j = s.parent[j];
+    }
+    __syncwarp();
+    // the touched entries that are not on the path
+    constexpr int kT = 8;  // gathers in flight
+    for (int k0 = lane; k0 < ntouched; k0 += 32 * kT) {
+      int v[kT];
+      uint32_t ok[kT];
+      float x[kT];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int v = q0 + 32 * u;
-          if (v >= nv) continue;
-          x[u] = load_logit<BF16>(in, c0 + v);
-          ok[u] = mrow ? __ldg(mrow + ((c0 + v) >> 5)) >> (v & 31) & 1u : 1u;
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int v = q0 + 32 * u;
-          if (v >= nv || (any && (path[v >> 5] >> (v & 31) & 1u))) continue;
-          const float y = s.count[v] || has_bias ? apply(x[u], s.count[v], 0, has_bias ? s.bias[v] : 0.0f, ok[u], r)
-                                                 : (ok[u] ? x[u] : -INFINITY);
-          __stcs(out + c0 + v, y);
-        }
+      for (int u = 0; u < kT; ++u) {
+        v[u] = k0 + 32 * u < ntouched ? s.touched[k0 + 32 * u] : -1;
+        ok[u] = 0;
+        if (v[u] < 0) continue;
+        ok[u] = mrow ? __ldg(mrow + ((c0 + v[u]) >> 5)) >> (v[u] & 31) & 1u : 1u;
+        x[u] = read_logit<BF16>(in, c0 + v[u]);
       }
+#pragma unroll
+      for (int u = 0; u < kT; ++u)
+        if (ok[u] && !(any && (path[v[u] >> 5] >> (v[u] & 31) & 1u)))
+          out[c0 + v[u]] = apply(x[u], s.count[v[u]], 0, has_bias ? s.bias[v[u]] : 0.0f, r);
     }
     if (any) {
       __syncwarp();
@@ -275,11 +303,11 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
 
 int launch_penalty(const PenaltyArgs& a, int sms, cudaStream_t stream) {
   const int chunks = (a.vocab + kChunk - 1) / kChunk;
-  // shares of a tree's rows: enough CTAs to fill the SMs (5 fit one), at least
+  // shares of a tree's rows: enough CTAs to fill the SMs (4 fit one), at least
   // a row per warp
   const long long base = static_cast<long long>(chunks) * a.batch;
   const int most = (a.max_nodes + kWarps - 1) / kWarps;
-  long long shares = (5ll * sms + base - 1) / base;
+  long long shares = (4ll * sms + base - 1) / base;
   shares = shares < 1 ? 1 : (shares > most ? most : shares);
   const dim3 grid(chunks, a.batch, static_cast<unsigned>(shares));
   const bool vec = a.vocab % 4 == 0;  // (row starts are then 16-byte aligned, bf16 rows 8-byte)
