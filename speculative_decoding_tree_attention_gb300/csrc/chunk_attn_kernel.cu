@@ -14,13 +14,17 @@
 // that any of its rows sees: the tiles of the sinks, then the tiles from the
 // start of the first row's window to the last row's position.
 //
-// Work.  Persistent grid, one CTA per SM.  The key tiles of all units lie on
-// one line ordered (sequence, unit, KV head, tile), cut into equal contiguous
-// ranges, one per CTA, computed on the device from the lengths.  A single
-// decode token of one sequence and a long prompt are split the same way.  A
-// range boundary inside a unit splits it into pieces: each leaves its
-// unnormalised O and (m, l) in a workspace slot, and the last piece to take a
-// ticket merges all slots in piece order, so results do not depend on timing.
+// Work.  Persistent grid, one CTA per SM.  All units lie on one line ordered
+// (sequence, unit, KV head), cut into equal contiguous ranges, one per CTA,
+// computed on the device from the lengths.  A single decode token of one
+// sequence and a long prompt are split the same way.  A unit takes as much of
+// the line as it has key tiles, and kPieceTiles more for what a piece costs
+// besides its tiles (Q, the first S, the last P V, the output: about 4.5 us to
+// 1.5 us a tile; with the tiles alone, the CTAs with the first units of four
+// 1600-token prompts ran 129 us and those with the last 55).  A range boundary
+// inside a unit splits it into pieces: each leaves its unnormalised O and
+// (m, l) in a workspace slot, and the last piece to take a ticket merges all
+// slots in piece order, so results do not depend on timing.
 //
 // One CTA has 384 threads (512 for an E4M3 cache):
 //   warps 8, 11 load the K tiles, and the V tiles and Q, by TMA: one box per
@@ -84,6 +88,10 @@ struct Shares {
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxPieces = 16;        // pieces per scheduling round
 constexpr int kSclSlots = 8;          // E4M3: scale slots (tile tau in slot tau % 8)
+
+constexpr int kPieceTiles = kChunkPieceTiles;
+// a unit is not cut within this many tiles of its ends
+constexpr int kMinCut = 2;
 
 // Named barriers (0 is __syncthreads): softmax group 0 alone, both groups, all.
 constexpr int kBarGroup0 = 1;
@@ -327,10 +335,18 @@ struct Line {
   }
 };
 
+// The key tile at which a range boundary at offset x of a unit of T tiles cuts
+// it (0: before it, T: after it).
+__device__ __forceinline__ int cut_at(int x, int T) {
+  const int t = x - kPieceTiles;
+  if (t >= T) return T;
+  return t < kMinCut ? 0 : (t > T - kMinCut ? T : t);
+}
+
 // Builds this CTA's pieces of scheduling round `round` into shared memory
 // (the 256 softmax threads).  `line` is filled in round 0.  Sequences are
 // taken 256 at a time, and the units of such a chunk 256 at a time, one per
-// thread: the tiles of a unit are hkv consecutive runs of T on the line.  In
+// thread: a unit is hkv consecutive runs of T + kPieceTiles on the line.  In
 // round 0 the rows of malformed sequences are zeroed and their status recorded.
 template <int D, bool F8>
 __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int sid, Line* line) {
@@ -395,26 +411,31 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
           xu = j - seq_u[xi];
           x = unit_of(a, seq_ctx[xi], seq_c[xi], xu);
         }
-        const int len = have ? x.T * a.hkv : 0;
+        const int run = x.T + kPieceTiles;
+        const int len = have ? run * a.hkv : 0;
         int tot;
         const int c0 = cum + scan256(len, scratch, sid, &tot);
         cum += tot;
         if (pass == 0) continue;
-        // KV heads [h0, h1) of this unit meet [s_v, e_v)
+        // KV heads [h0, h1) of this unit have tiles in [s_v, e_v)
         int h0 = 0, h1 = 0;
         if (have && c0 < e_v && c0 + len > s_v) {
-          h0 = max(0, s_v - c0) / x.T;
-          h1 = (min(e_v - c0, len) + x.T - 1) / x.T;
+          h0 = max(0, s_v - c0) / run;
+          h1 = (min(e_v - c0, len) + run - 1) / run;
+          if (cut_at(s_v - c0 - h0 * run, x.T) == x.T) ++h0;
+          if (h1 > h0 && cut_at(e_v - c0 - (h1 - 1) * run, x.T) == 0) --h1;
+          // (a range within one unit may have neither)
+          if (h1 == h0 + 1 && cut_at(s_v - c0 - h0 * run, x.T) >= cut_at(e_v - c0 - h0 * run, x.T)) h1 = h0;
         }
         int ptot;
-        int k = count + scan256(h1 - h0, scratch, sid, &ptot) - round * kMaxPieces;
+        int k = count + scan256(max(0, h1 - h0), scratch, sid, &ptot) - round * kMaxPieces;
         count += ptot;
 #pragma unroll 1
         for (int h = h0; h < h1; ++h, ++k) {
           if (k < 0 || k >= kMaxPieces) continue;
-          const int u0 = c0 + h * x.T;  // line position of the unit's first tile
+          const int u0 = c0 + h * run;  // line position of the unit
           Piece& pc = pieces[k];
-          const int t0 = max(s_v - u0, 0), t1 = min(e_v - u0, x.T);
+          const int t0 = cut_at(s_v - u0, x.T), t1 = cut_at(e_v - u0, x.T);
           pc.b = base + xi;
           pc.kvh = h;
           pc.tok0 = seq_n0[xi] + xu * a.unit_tokens;
@@ -424,8 +445,13 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
           pc.t1 = t1;
           int vf = v, np = 1;
           if (t0 > 0 || t1 < x.T) {
+            // the CTAs of the unit's first and last tiles: every one between
+            // them has a piece
             vf = line->owner(u0);
-            np = line->owner(u0 + x.T - 1) - vf + 1;
+            while (cut_at(line->start(vf + 1) - u0, x.T) == 0) ++vf;
+            int vl = line->owner(u0 + run - 1);
+            while (cut_at(line->start(vl) - u0, x.T) == x.T) --vl;
+            np = vl - vf + 1;
           }
           pc.cut = np << 16 | vf;
         }
@@ -434,7 +460,7 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
       named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
     }
     if (pass == 0) {
-      line->V = max(1, min(a.vctas, cum / max(1, a.min_tiles)));
+      line->V = max(1, min(a.vctas, cum / max(1, a.min_range)));
       line->q = cum / line->V;
       line->r = cum % line->V;
       line->rV = 1.0f / static_cast<float>(line->V);

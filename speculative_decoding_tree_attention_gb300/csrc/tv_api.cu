@@ -132,6 +132,9 @@ bool encode_pool(CUtensorMap* m, const void* pool, int D, uint64_t pages, bool f
   return encode(m, pool, 5, dims, str, box);
 }
 
+// Shortest range of the chunk attention's line that a CTA is given.
+constexpr int kMinRange = 5;
+
 struct ChunkPlan {
   int unit_tokens;  // tokens of a unit
   int vctas;        // CTAs (ranges of the line of key tiles)
@@ -140,7 +143,7 @@ struct ChunkPlan {
 
 // Launch plan of the chunk attention for `sms` SMs: a unit is as many whole
 // tokens as give at most 256 packed rows; the CTAs share the line of key tiles
-// (at most `wmax` by the host hints) in ranges of at least kMinTiles.
+// (at most `wmax` by the host hints) in ranges of at least kMinRange.
 // Workspace: a ticket counter per CTA, then two partial-result slots per CTA.
 bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
   if (!p || sms < 1) return false;
@@ -162,10 +165,10 @@ bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
   if (p->window > 0)  // the sinks' tiles, and the tiles that a unit's windows meet
     tiles = std::min(tiles, (static_cast<int64_t>(p->sinks) + 127) / 128 +
                                 (static_cast<int64_t>(p->window) + pl.unit_tokens + 253) / 128);
-  const int64_t wmax = units * p->num_kv_heads * std::max<int64_t>(tiles, 1);
+  const int64_t wmax = units * p->num_kv_heads * (std::max<int64_t>(tiles, 1) + tv::kChunkPieceTiles);
   if (units * p->num_kv_heads >= (1ll << 31) || wmax >= (1ll << 31)) return false;  // counted in 32 bits
   // at most 4096 CTAs: the range boundaries are fp32 products below 2^24
-  pl.vctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms, wmax / kMinTiles, 4096})));
+  pl.vctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms, wmax / kMinRange, 4096})));
   pl.workspace = (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256 +
                  2 * static_cast<size_t>(pl.vctas) * tv::chunk_slot_bytes(p->head_dim);
   *out = pl;
@@ -639,7 +642,7 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
   a.total_tokens = p->total_tokens;
   a.unit_tokens = pl.unit_tokens;
   a.vctas = pl.vctas;
-  a.min_tiles = kMinTiles;
+  a.min_range = kMinRange;
   a.window = p->window;
   a.sinks = p->sinks;
   a.out_fp32 = p->out_dtype == TV_OUT_FP32 ? 1 : 0;

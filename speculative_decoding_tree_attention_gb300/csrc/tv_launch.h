@@ -91,6 +91,10 @@ int launch_tree_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t 
 // Bytes of one partial-result slot: 256 rows of fp32 O, (m, l) per row, a flag.
 size_t attn_slot_bytes(int head_dim);
 
+// What a piece of a unit costs besides its key tiles, in tiles (the line of
+// work counts it for every unit).
+constexpr int kChunkPieceTiles = 3;
+
 struct ChunkArgs {
   const int32_t* block_table; // [batch][max_blocks_per_seq]
   const int32_t* seq_lens;    // [batch] cached tokens, the chunk's included
@@ -104,7 +108,7 @@ struct ChunkArgs {
   int32_t max_blocks_per_seq, num_blocks, max_len, total_tokens;
   int32_t unit_tokens;        // tokens of a unit: floor(256 / group)
   int32_t vctas;              // CTAs launched
-  int32_t min_tiles;          // fewest key tiles a CTA is given
+  int32_t min_range;          // shortest range of the line a CTA is given
   int32_t window, sinks;      // window 0: every earlier key
   int32_t out_fp32;
   int32_t fp8;                // E4M3 codes with one fp32 scale per row
