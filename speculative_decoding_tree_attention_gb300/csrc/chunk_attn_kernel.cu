@@ -17,11 +17,12 @@
 // Work.  Persistent grid, one CTA per SM.  All units lie on one line ordered
 // (sequence, unit, KV head), cut into equal contiguous ranges, one per CTA,
 // computed on the device from the lengths.  A single decode token of one
-// sequence and a long prompt are split the same way.  A unit takes as much of
-// the line as it has key tiles, and kPieceTiles more for what a piece costs
-// besides its tiles (Q, the first S, the last P V, the output: about 4.5 us to
-// 1.5 us a tile; with the tiles alone, the CTAs with the first units of four
-// 1600-token prompts ran 129 us and those with the last 55).  A range boundary
+// sequence and a long prompt are split the same way.  A unit's length on the
+// line is its cost: kWide for each key tile of two m-tiles, kNarrow for one of
+// one (about 2.0 and 1.3 us), and kFixed for what a piece costs besides (Q, the
+// first S, the last P V, the output: about 5 us).  With the tiles alone, the
+// CTAs with the first units of four 1600-token prompts ran 129 us and those with
+// the last 55.  A range boundary
 // inside a unit splits it into pieces: each leaves its unnormalised O and
 // (m, l) in a workspace slot, and the last piece to take a ticket merges all
 // slots in piece order, so results do not depend on timing.
@@ -89,7 +90,10 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxPieces = 16;        // pieces per scheduling round
 constexpr int kSclSlots = 8;          // E4M3: scale slots (tile tau in slot tau % 8)
 
-constexpr int kPieceTiles = kChunkPieceTiles;
+// cost of a key tile of a unit with one and with two m-tiles, and of a piece
+constexpr int kNarrow = 2;
+constexpr int kWide = kChunkTileCost;
+constexpr int kFixed = kChunkPieceCost;
 // a unit is not cut within this many tiles of its ends
 constexpr int kMinCut = 2;
 
@@ -335,10 +339,10 @@ struct Line {
   }
 };
 
-// The key tile at which a range boundary at offset x of a unit of T tiles cuts
-// it (0: before it, T: after it).
-__device__ __forceinline__ int cut_at(int x, int T) {
-  const int t = x - kPieceTiles;
+// The key tile at which a range boundary at offset x of a unit of T tiles of
+// cost w cuts it (0: before it, T: after it).
+__device__ __forceinline__ int cut_at(int x, int T, int w) {
+  const int t = x < kFixed ? 0 : (w == kWide ? (x - kFixed) / kWide : (x - kFixed) / kNarrow);
   if (t >= T) return T;
   return t < kMinCut ? 0 : (t > T - kMinCut ? T : t);
 }
@@ -346,7 +350,7 @@ __device__ __forceinline__ int cut_at(int x, int T) {
 // Builds this CTA's pieces of scheduling round `round` into shared memory
 // (the 256 softmax threads).  `line` is filled in round 0.  Sequences are
 // taken 256 at a time, and the units of such a chunk 256 at a time, one per
-// thread: a unit is hkv consecutive runs of T + kPieceTiles on the line.  In
+// thread: a unit is hkv consecutive runs of the line, one per KV head.  In
 // round 0 the rows of malformed sequences are zeroed and their status recorded.
 template <int D, bool F8>
 __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int sid, Line* line) {
@@ -411,7 +415,8 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
           xu = j - seq_u[xi];
           x = unit_of(a, seq_ctx[xi], seq_c[xi], xu);
         }
-        const int run = x.T + kPieceTiles;
+        const int w = x.ntok * a.group > BM ? kWide : kNarrow;
+        const int run = x.T * w + kFixed;
         const int len = have ? run * a.hkv : 0;
         int tot;
         const int c0 = cum + scan256(len, scratch, sid, &tot);
@@ -422,10 +427,10 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
         if (have && c0 < e_v && c0 + len > s_v) {
           h0 = max(0, s_v - c0) / run;
           h1 = (min(e_v - c0, len) + run - 1) / run;
-          if (cut_at(s_v - c0 - h0 * run, x.T) == x.T) ++h0;
-          if (h1 > h0 && cut_at(e_v - c0 - (h1 - 1) * run, x.T) == 0) --h1;
+          if (cut_at(s_v - c0 - h0 * run, x.T, w) == x.T) ++h0;
+          if (h1 > h0 && cut_at(e_v - c0 - (h1 - 1) * run, x.T, w) == 0) --h1;
           // (a range within one unit may have neither)
-          if (h1 == h0 + 1 && cut_at(s_v - c0 - h0 * run, x.T) >= cut_at(e_v - c0 - h0 * run, x.T)) h1 = h0;
+          if (h1 == h0 + 1 && cut_at(s_v - c0 - h0 * run, x.T, w) >= cut_at(e_v - c0 - h0 * run, x.T, w)) h1 = h0;
         }
         int ptot;
         int k = count + scan256(max(0, h1 - h0), scratch, sid, &ptot) - round * kMaxPieces;
@@ -435,7 +440,7 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
           if (k < 0 || k >= kMaxPieces) continue;
           const int u0 = c0 + h * run;  // line position of the unit
           Piece& pc = pieces[k];
-          const int t0 = cut_at(s_v - u0, x.T), t1 = cut_at(e_v - u0, x.T);
+          const int t0 = cut_at(s_v - u0, x.T, w), t1 = cut_at(e_v - u0, x.T, w);
           pc.b = base + xi;
           pc.kvh = h;
           pc.tok0 = seq_n0[xi] + xu * a.unit_tokens;
@@ -448,9 +453,9 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
             // the CTAs of the unit's first and last tiles: every one between
             // them has a piece
             vf = line->owner(u0);
-            while (cut_at(line->start(vf + 1) - u0, x.T) == 0) ++vf;
+            while (cut_at(line->start(vf + 1) - u0, x.T, w) == 0) ++vf;
             int vl = line->owner(u0 + run - 1);
-            while (cut_at(line->start(vl) - u0, x.T) == x.T) --vl;
+            while (cut_at(line->start(vl) - u0, x.T, w) == x.T) --vl;
             np = vl - vf + 1;
           }
           pc.cut = np << 16 | vf;

@@ -133,7 +133,7 @@ bool encode_pool(CUtensorMap* m, const void* pool, int D, uint64_t pages, bool f
 }
 
 // Shortest range of the chunk attention's line that a CTA is given.
-constexpr int kMinRange = 5;
+constexpr int kMinRange = 14;
 
 struct ChunkPlan {
   int unit_tokens;  // tokens of a unit
@@ -142,7 +142,7 @@ struct ChunkPlan {
 };
 
 // Launch plan of the chunk attention for `sms` SMs: a unit is as many whole
-// tokens as give at most 256 packed rows; the CTAs share the line of key tiles
+// tokens as give at most 256 packed rows; the CTAs share the line of work
 // (at most `wmax` by the host hints) in ranges of at least kMinRange.
 // Workspace: a ticket counter per CTA, then two partial-result slots per CTA.
 bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
@@ -165,7 +165,8 @@ bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
   if (p->window > 0)  // the sinks' tiles, and the tiles that a unit's windows meet
     tiles = std::min(tiles, (static_cast<int64_t>(p->sinks) + 127) / 128 +
                                 (static_cast<int64_t>(p->window) + pl.unit_tokens + 253) / 128);
-  const int64_t wmax = units * p->num_kv_heads * (std::max<int64_t>(tiles, 1) + tv::kChunkPieceTiles);
+  const int64_t wmax =
+      units * p->num_kv_heads * (std::max<int64_t>(tiles, 1) * tv::kChunkTileCost + tv::kChunkPieceCost);
   if (units * p->num_kv_heads >= (1ll << 31) || wmax >= (1ll << 31)) return false;  // counted in 32 bits
   // at most 4096 CTAs: the range boundaries are fp32 products below 2^24
   pl.vctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms, wmax / kMinRange, 4096})));

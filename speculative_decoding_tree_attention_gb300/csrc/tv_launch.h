@@ -91,9 +91,10 @@ int launch_tree_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t 
 // Bytes of one partial-result slot: 256 rows of fp32 O, (m, l) per row, a flag.
 size_t attn_slot_bytes(int head_dim);
 
-// What a piece of a unit costs besides its key tiles, in tiles (the line of
-// work counts it for every unit).
-constexpr int kChunkPieceTiles = 3;
+// Costs on the chunk attention's line of work: of a key tile of a full unit,
+// and of a piece besides its tiles.
+constexpr int kChunkTileCost = 3;
+constexpr int kChunkPieceCost = 8;
 
 struct ChunkArgs {
   const int32_t* block_table; // [batch][max_blocks_per_seq]
