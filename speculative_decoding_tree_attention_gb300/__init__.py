@@ -548,8 +548,8 @@ def _run(dev, stream, call):
         return call(_raw_stream(dev))  # (the handle alone: 3 us less than a Stream object)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    elif stream.device.index != dev:
-        _bad("stream", f"one of CUDA device {dev}")
+    elif not isinstance(stream, torch.cuda.Stream) or stream.device.index != dev:
+        _bad("stream", f"a stream of CUDA device {dev}")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 

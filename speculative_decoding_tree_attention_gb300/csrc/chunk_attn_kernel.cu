@@ -1195,18 +1195,13 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             if (!ok) misc->abort = 1;
           }
           ++my_tiles;
-          if (!ok || idle) {
-            mbar_arrive(&p_a[h]);
-            mbar_arrive(&p_b[h]);
-            continue;
-          }
           // keys that no row of the unit sees: their V rows are cleared
           // (stale data; P is 0 there but 0 * NaN would poison O), a row per
           // thread, by each group before its own P_h(t) V(t).  (After S: only
           // then is every earlier use of the slot known to be over, and the
           // parity waited for unambiguous.)
           if constexpr (!F8) {
-            if (k0 + BN - 1 > hi || (lo > k0 && k0 + BN > a.sinks)) {
+            if (ok && (k0 + BN - 1 > hi || (lo > k0 && k0 + BN > a.sinks))) {
               const int vs = gt % kVStages;
               mbar_wait(&vfull[vs], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
               const int key = k0 + r;
@@ -1218,6 +1213,11 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               }
               fence_proxy_async_smem();  // generic writes, read by the MMA
             }
+          }
+          if (!ok || idle) {
+            mbar_arrive(&p_a[h]);
+            mbar_arrive(&p_b[h]);
+            continue;
           }
           // the scores stay unscaled; the softmax scale is folded into the exponent
           float x[128];

@@ -256,3 +256,69 @@ def test_commit_fp8(num):
                 want_s[table[b, pos // 16], :, pos % 16] = scale[off[b] + node].cpu().numpy()
         np.testing.assert_array_equal(got.cpu().numpy(), want)
         np.testing.assert_array_equal(got_s.cpu().numpy(), want_s)
+
+
+def test_blocks_past_32_bit_offsets():
+    """Writing to and reading from pages whose offsets pass 2^31 and 2^32."""
+    ensure_built()
+    hkv, d, blocks = 2, 128, 1_060_000  # 4.3e9 codes a pool
+    k_pool, v_pool = (torch.empty(blocks, hkv, 16, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    k_scale, v_scale = (torch.empty(blocks, hkv, 16, device="cuda") for _ in range(2))
+    table = i32([[blocks - 1, 3, blocks - 7]])
+    lens, off = i32([45]), i32([0, 45])
+    kt, k = bf16(np.random.default_rng(0).standard_normal((45, hkv, d)))
+    vt, v = bf16(np.random.default_rng(1).standard_normal((45, hkv, d)))
+    st = tv.append_kv_fp8(kt, vt, table, lens, off, k_pool, k_scale, v_pool, v_scale)
+    back_k, back_v, st2 = tv.read_kv_fp8(k_pool, k_scale, v_pool, v_scale, table, lens, off, total_tokens=45)
+    assert st.item() == 0 and st2.item() == 0
+    for x, got in ((k, back_k), (v, back_v)):
+        codes, scale = oracle.quantize_rows(x)
+        want = torch.from_numpy((oracle.e4m3_table()[codes].astype(np.float32) * scale[..., None])).to(torch.bfloat16)
+        assert torch.equal(got.cpu(), want)
+    wide = torch.empty(blocks, hkv, 16, d, dtype=torch.bfloat16, device="cuda")
+    st = tv.append_kv(kt, vt, table, lens, off, wide, wide.clone())
+    assert st.item() == 0
+    assert torch.equal(wide[blocks - 1].transpose(0, 1), kt[:16]) and torch.equal(wide[blocks - 7].transpose(0, 1)[:13], kt[32:])
+
+
+def test_side_stream_and_graph():
+    ensure_built()
+    table, seq, off, blocks = batch([40, 19], [40, 3], 4)
+    x = torch.randn(43, 2, 128, device="cuda").to(torch.bfloat16)
+    pools = [torch.zeros(blocks, 2, 16, 128, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    scales = [torch.zeros(blocks, 2, 16, device="cuda") for _ in range(4)]
+    args = (x, x, i32(table), i32(seq), i32(off))
+    tv.append_kv_fp8(*args, pools[0], scales[0], pools[1], scales[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    tv.append_kv_fp8(*args, pools[2], scales[2], pools[3], scales[3], stream=side)
+    side.synchronize()
+    assert torch.equal(pools[0], pools[2]) and torch.equal(scales[1], scales[3])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tv.append_kv_fp8(*args, pools[2], scales[2], pools[3], scales[3])
+        k, _, _ = tv.read_kv_fp8(pools[2], scales[2], pools[3], scales[3], *args[2:], total_tokens=43)
+    x.mul_(3.0)
+    g.replay()
+    tv.append_kv_fp8(*args, pools[0], scales[0], pools[1], scales[1])
+    want, _, _ = tv.read_kv_fp8(pools[0], scales[0], pools[1], scales[1], *args[2:], total_tokens=43)
+    assert torch.equal(k, want)
+
+
+def test_binding_refuses_bad_tensors():
+    ensure_built()
+    table, seq, off, blocks = batch([40], [40], 4)
+    k = torch.zeros(40, 2, 128, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(blocks, 2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    at = (i32(table), i32(seq), i32(off))
+    for args in ((k.float(), k, *at, pool, pool), (k, k[:39], *at, pool, pool), (k[:, :1], k[:, :1], *at, pool, pool),
+                 (k, k, i32(table).long(), *at[1:], pool, pool), (k, k, *at, pool, pool[:, :1]),
+                 (k, k, at[0], at[1], i32([0]), pool, pool), (k, k, *at, pool, pool.cpu()),
+                 (k.transpose(0, 1), k, *at, pool, pool), (k, torch.zeros(40, 4, 128, dtype=torch.bfloat16, device="cuda")[:, :2], *at, pool, pool),
+                 (k, k, *at, pool.float(), pool.float())):
+        with pytest.raises(ValueError):
+            tv.append_kv(*args)
+    with pytest.raises(ValueError):
+        tv.read_kv_fp8(pool.to(torch.uint8), pool[..., 0].float(), pool.to(torch.uint8), pool[..., 0].float(), *at)
+    with pytest.raises(ValueError):
+        tv.append_kv(k, k, *at, pool, pool, stream=7)

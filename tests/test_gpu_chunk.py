@@ -177,3 +177,215 @@ def test_long_decode_is_split_and_merged():
     got, st = call(c)
     assert (st == 0).all()
     check(got, c, U_BF16)
+
+
+# ------------------------------------------------------------------ what a caller may hand over
+def test_malformed_sequences_are_zeroed_and_reported():
+    c = make([40, 50, 60, 33, 20], [8, 50, 1, 3, 20], 8, 2, 128, seed=1)
+    good, st = call(c)
+    assert (st == 0).all()
+
+    def rows(b):
+        return slice(int(c["off"][b]), int(c["off"][b + 1]))
+
+    for kind, b in (("len", 0), ("max", 2), ("block", 3), ("page", 1)):
+        bad = dict(c, lens=c["lens"].copy(), table=c["table"].copy())
+        if kind == "len":
+            bad["lens"][b] = 7          # shorter than its chunk
+        if kind == "max":
+            bad["lens"][b] = 61         # above max_len
+        if kind == "block":
+            bad["table"][b, 1] = -7
+        if kind == "page":
+            bad["table"][b, 3] = bad["k"].shape[0]
+        got, st = call(bad, max_len=60, fill=5.0)
+        assert st.tolist() == [5 if i == b else 0 for i in range(5)], kind
+        assert (got[rows(b)] == 0).all()
+        for i in range(5):
+            if i != b:
+                np.testing.assert_array_equal(got[rows(i)], good[rows(i)])
+    # offsets: a chunk of negative length, and rows past the end
+    for off in ([0, 8, 4, 5, 8, 28], [0, 8, 58, 59, 62, 200]):
+        got, st = call(dict(c, off=np.asarray(off, np.int32)), max_len=60)
+        assert (st == 5).any() and np.isfinite(got).all()
+
+
+def test_rows_behind_the_last_sequence_stay():
+    c = make([30, 9], [5, 9], 4, 2, 64, seed=2, extra_rows=7)
+    for dt in ("fp32", "bf16"):
+        got, st = call(c, out_dtype=dt, fill=-3.0)
+        assert (st == 0).all() and (got[14:] == -3.0).all() and (got[:14] != -3.0).any()
+    c = make([30, 9], [0, 0], 4, 2, 64, seed=2, extra_rows=3)
+    got, st = call(c, fill=-3.0)
+    assert (st == 0).all() and (got == -3.0).all()
+
+
+def test_no_rows_at_all():
+    c = make([30, 9], [0, 0], 4, 2, 64, seed=2)
+    got, st = call(c)
+    assert got.shape == (0, 4, 64) and (st == 0).all()
+
+
+def poisoned(c, window, sinks):
+    """The cache with NaN in every place that no row of its sequence's chunk
+    sees, and no page where a whole page is unseen."""
+    out = dict(c, k=np.full_like(c["k"], np.nan), v=np.full_like(c["v"], np.nan),
+               table=np.full_like(c["table"], -1))
+    for b, n in enumerate(c["lens"]):
+        first = int(n) - int(c["off"][b + 1] - c["off"][b])
+        if first == n:
+            continue
+        for p in range(int(n)):
+            if not window or p > first - window or p < sinks:
+                blk = out["table"][b, p // 16] = c["table"][b, p // 16]
+                out["k"][blk, :, p % 16] = c["k"][blk, :, p % 16]
+                out["v"][blk, :, p % 16] = c["v"][blk, :, p % 16]
+    return out
+
+
+@pytest.mark.parametrize("window, sinks", [(0, 0), (1, 0), (50, 0), (50, 4), (130, 20), (300, 129)])
+@pytest.mark.parametrize("d, group", [(64, 1), (128, 4)])
+def test_unseen_places_do_not_matter(window, sinks, d, group):
+    """Freed pages, stale page tails and evicted positions may hold NaN.  A
+    chunk of one unit: a place that some row sees, others may not."""
+    c = make([900, 33, 400, 131], [1, 5, 30, 1], 2 * group, 2, d, seed=window + sinks)
+    bad = poisoned(c, window, sinks)
+    a, st = call(c, window=window, sinks=sinks)
+    b, st2 = call(bad, window=window, sinks=sinks)
+    assert (st == 0).all() and (st2 == 0).all()
+    np.testing.assert_array_equal(a, b)
+
+
+def test_unseen_places_do_not_matter_fp8():
+    c = quantised(make([900, 33, 400], [1, 5, 30], 4, 2, 128, seed=9))
+    for window, sinks in ((0, 0), (50, 4)):
+        a, _ = call_fp8(c, window=window, sinks=sinks)
+        bad = dict(c, table=np.full_like(c["table"], -1))
+        for k in ("k", "v"):
+            bad[k + "_codes"] = np.full_like(c[k + "_codes"], 0x7F)
+            bad[k + "_scale"] = np.full_like(c[k + "_scale"], np.nan)
+        for b, n in enumerate(c["lens"]):
+            first = int(n) - int(c["off"][b + 1] - c["off"][b])
+            for p in range(int(n)):
+                if not window or p > first - window or p < sinks:
+                    blk = bad["table"][b, p // 16] = c["table"][b, p // 16]
+                    for k in ("k_codes", "v_codes", "k_scale", "v_scale"):
+                        bad[k][blk, :, p % 16] = c[k][blk, :, p % 16]
+        got, st = call_fp8(bad, window=window, sinks=sinks)
+        assert (st == 0).all()
+        np.testing.assert_array_equal(a, got)
+
+
+@pytest.mark.parametrize("hq, hkv, d", [(256, 1, 64), (100, 1, 128), (129, 1, 64), (48, 16, 128)])
+def test_groups_of_every_size(hq, hkv, d):
+    """g = 256: one token per unit; 129: one token, two m-tiles; 3: 85 tokens."""
+    c = make([150, 20], [90, 3], hq, hkv, d, seed=hq)
+    got, st = call(c)
+    assert (st == 0).all()
+    check(got, c, U_BF16)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 4.0])
+def test_softmax_scale(scale):
+    """Flat and peaked rows; scores of large magnitude rescale the accumulators."""
+    c = make([300, 60], [40, 60], 4, 2, 64, seed=4, std=2.0)
+    got, st = call(c, softmax_scale=scale)
+    assert (st == 0).all()
+    check(got, c, U_BF16, scale=scale)
+
+
+def test_growing_scores_rescale():
+    """Keys that grow with their position: the running maximum moves by more
+    than 2^8 many times."""
+    c = make([1000], [70], 2, 1, 64, seed=5)
+    ramp = np.linspace(0.1, 12, 1000)
+    for p in range(1000):
+        blk = c["table"][0, p // 16]
+        row = np.full(64, ramp[p])
+        c["k"][blk, :, p % 16] = wl.bf16_bits_to_f32(wl.to_bf16_bits(row))
+    c["q"][:] = wl.bf16_bits_to_f32(wl.to_bf16_bits(np.abs(c["q"]) + 0.5))
+    got, st = call(c)
+    assert (st == 0).all()
+    check(got, c, U_BF16)
+
+
+def test_strided_queries_and_given_buffers():
+    ensure_built()
+    c = make([64, 200], [64, 9], 8, 2, 128, seed=6)
+    qkv = torch.randn(73, 12, 128, device="cuda").to(torch.bfloat16)
+    qkv[:, :8] = dev(c["q"], torch.bfloat16)
+    rest = [dev(c[k], torch.bfloat16) for k in ("k", "v")] + [dev(c[k]) for k in ("table", "lens", "off")]
+    want, _ = tv.chunk_attention(qkv[:, :8].contiguous(), *rest, max_len=200)
+    out = torch.empty(73, 8, 128, dtype=torch.bfloat16, device="cuda")
+    st = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    prm = tv.chunk_params(qkv[:, :8], rest[0], rest[2], rest[3], max_len=200)
+    assert prm.q_stride == 12 * 128
+    ws = torch.full((tv.chunk_workspace_size(prm),), 0xFF, dtype=torch.uint8, device="cuda")
+    got, st2 = tv.chunk_attention(qkv[:, :8], *rest, max_len=200, out=out, status=st, workspace=ws)
+    assert got is out and st2 is st and torch.equal(got, want) and (st == 0).all()
+    with pytest.raises(tv.TVError):
+        tv.chunk_attention(qkv[:, :8], *rest, max_len=200, workspace=ws[:-256])
+    for bad in (qkv[:, 1:9, :64], qkv[:, :8].transpose(0, 1), qkv[:, :8].float(), qkv[:, ::2][:, :4]):
+        with pytest.raises((ValueError, tv.TVError)):
+            tv.chunk_attention(bad, *rest, max_len=200)
+    with pytest.raises(ValueError):
+        tv.chunk_attention(qkv[:, :8], rest[0], rest[1].float(), *rest[2:], max_len=200)
+    with pytest.raises(ValueError):
+        tv.chunk_attention(qkv[:, :8], *rest[:3], rest[3].long(), rest[4], max_len=200)
+    with pytest.raises(tv.TVError):
+        tv.chunk_attention(qkv[:, :8], *rest, max_len=400)  # more pages than a table row has
+
+
+def test_side_stream_and_graphs():
+    """A call on another stream, and two captured graphs with workspaces of
+    their own replayed at once and again on new inputs."""
+    ensure_built()
+    a, b = make([700, 30], [1, 30], 8, 2, 128, seed=7), make([90, 2000], [40, 1], 8, 2, 128, seed=8)
+    graphs, outs, args, want = [], [], [], []
+    for c in (a, b):
+        t = [dev(c[k], torch.bfloat16) for k in ("q", "k", "v")] + [dev(c[k]) for k in ("table", "lens", "off")]
+        want.append(tv.chunk_attention(*t, max_len=2000 if c is b else 700)[0].clone())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got, _ = tv.chunk_attention(*t, max_len=2000 if c is b else 700, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want[-1])
+        prm = tv.chunk_params(t[0], t[1], t[3], t[4], max_len=2000 if c is b else 700)
+        ws = torch.empty(tv.chunk_workspace_size(prm), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out, _ = tv.chunk_attention(*t, max_len=2000 if c is b else 700, workspace=ws)
+        graphs.append(g), outs.append(out), args.append((t, ws))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for rep in range(3):
+        for s, g in ((s1, graphs[0]), (s2, graphs[1])):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+            o.zero_()
+    args[0][0][0].mul_(0.5)  # the graph reads its inputs anew
+    graphs[0].replay()
+    fresh, _ = tv.chunk_attention(*args[0][0], max_len=700)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], fresh) and not torch.equal(fresh, want[0])
+
+
+def test_blocks_past_32_bit_offsets():
+    """Pages whose byte and element offsets pass 2^31 (and 2^32)."""
+    ensure_built()
+    hkv, d, blocks = 1, 128, 1_200_000  # 2.46e9 elements, 4.9 GB a pool
+    small = make([50, 700], [3, 1], 4, hkv, d, seed=11)
+    n = small["k"].shape[0]
+    ids = (blocks - 1 - 3 * np.arange(n)).astype(np.int32)
+    pools = [torch.empty(blocks, hkv, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for pool, x in zip(pools, (small["k"], small["v"])):
+        pool[torch.from_numpy(ids).long().cuda()] = dev(x, torch.bfloat16)
+    table = np.where(small["table"] >= 0, ids[np.maximum(small["table"], 0)], -1)
+    out, st = tv.chunk_attention(dev(small["q"], torch.bfloat16), *pools, dev(table), dev(small["lens"]),
+                                 dev(small["off"]), max_len=700, out_dtype="fp32")
+    assert (st == 0).all()
+    want, _ = call(small)
+    np.testing.assert_array_equal(out.cpu().numpy(), want)

@@ -170,3 +170,39 @@ def test_malformed_sequences_keep_their_rows():
     got, st = call(good, max_nodes=6)  # a tree larger than max_nodes
     assert st.tolist() == [0, 0, 5, 0]
     np.testing.assert_array_equal(got[11:18], good["logits"][11:18])
+
+
+def test_graph_side_stream_and_refusals():
+    c = make([20, 9], 3000, [50, 0], 4, 3, True)
+    want, _ = call(c)
+    side = torch.cuda.Stream()
+    got, _ = call(c, stream=side)
+    np.testing.assert_array_equal(got, want)
+    t = {k: torch.from_numpy(np.ascontiguousarray(v)).cuda() for k, v in c.items() if k != "allowed"}
+    mask = torch.from_numpy(words(c["allowed"])).cuda()
+    first = [t.pop(k) for k in ("logits", "draft_tokens", "parent", "node_offsets")]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, st = tv.penalize_logits(*first, max_nodes=20, allowed_mask=mask.view(torch.uint32), **t)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(out.cpu().numpy(), want)
+    for kw in (dict(t, history=None), dict(t, bias_offsets=None), dict(t, repetition=t["repetition"].double()),
+               dict(t, allowed_mask=mask[:, :-1].contiguous()), dict(t, out=out[:5]), dict(t, presence=t["presence"][:1]),
+               dict(t, out=out.t()), dict(t, allowed_mask=mask.float())):
+        with pytest.raises(ValueError):
+            tv.penalize_logits(*first, max_nodes=20, **kw)
+    with pytest.raises(ValueError):
+        tv.penalize_logits(first[0].half(), *first[1:], max_nodes=20)
+    with pytest.raises(tv.TVError):
+        tv.penalize_logits(first[0].bfloat16(), *first[1:], max_nodes=600)
+
+
+def test_large_rows_at_odd_widths():
+    for vocab in (151936, 128255):
+        c = make([70], vocab, [500], vocab, 20, True)
+        got, st = call(c)
+        assert (st == 0).all()
+        check(got, c)
