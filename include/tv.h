@@ -602,8 +602,8 @@ int tv_commit_kv_fp8(const tv_commit_params* params, const uint8_t* k_nodes,
  *   c(v) > 0:  x = x - presence[b]
  *              x = x + bias of v (of an id listed twice the last entry holds)
  *   bit v % 32 of word v / 32 of the row's allowed_mask clear: x = -inf
- * A row whose mask allows nothing is all -inf.  Ids outside [0, V), in the
- * history, the bias list or the tree, count for nothing.
+ * A logit of -inf stays -inf; a row whose mask allows nothing is all -inf.  Ids
+ * outside [0, V), in the history, the bias list or the tree, count for nothing.
  * A sequence with a malformed tree, history or bias extent, or a rate that is
  * not finite (a repetition not positive), gets TV_ERR_BAD_TREE and its rows
  * unchanged (as far as they can be addressed).

@@ -14,16 +14,21 @@
 //   mask bit 0: x = -inf
 // each step one fp32 rounding.
 //
-// One CTA takes a chunk of 4096 vocabulary entries of the rows of one tree (or
+// One CTA takes a chunk of 2048 vocabulary entries of the rows of one tree (or
 // of a share of them).  It counts the sequence's history and bias list into
-// shared memory once and lists the touched entries.  Each warp then streams
-// rows through: a masked copy (one read and one write of HBM per entry), after
-// which the row's touched entries are gathered again from L2 and rewritten, a
-// lane each, and so are the few tokens of the row's path, which have a count of
-// their own.  (With the penalties inside the stream every warp step met some
-// touched entry and ran their divisions for 16 of 32 lanes: 82 us instead of
-// the figures below.)
+// shared memory once and lists the touched entries, ascending.  Each warp then
+// streams rows through, one read and one write of HBM per entry: a masked copy
+// that also passes through shared memory, 512 entries at a time, from where the
+// touched ones are rewritten, a lane each.  The few tokens of the row's path,
+// which have a count of their own, come last.  With the penalties inside the
+// stream every warp step met some touched entry and ran their divisions for 16
+// of 32 lanes (82 us, the first case below); gathering the touched entries again
+// from L2 took longer than the copy (48 us).
 //
+// Bound: HBM; per entry 4 (fp32) or 2 (bf16) bytes read, 4 written, a mask bit.
+// 16 trees of 26 or 64 nodes, V = 32000, bf16, histories of 512 to 4096: 36 us
+// (4.0 TB/s: each tree's history is counted by all of its 16 chunks' CTAs).
+// 4 trees of 128 nodes, V = 151936, fp32, histories of 1600: 112 us (5.7 TB/s).
 #include <math.h>
 
 #include "tv_device.cuh"
@@ -34,7 +39,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 4096;
+constexpr int kChunk = 2048;
+constexpr int kBlock = 512;     // entries that pass through shared memory at a time
 constexpr int kMaxNodes = 512;
 constexpr uint32_t kPrompt = 0x80000000u;  // count word: in the prompt; low 31 bits: generated
 
@@ -45,13 +51,15 @@ struct Shared {
     float bias[kChunk];
   };
   uint32_t path[kWarps][kChunk / 32];  // a warp's row: tokens of its path
-  uint16_t touched[kChunk];            // entries with a count or a bias
+  float block[kWarps][kBlock];         // a warp's row: entries on their way
+  uint16_t touched[kChunk];            // entries with a count or a bias, ascending
+  uint32_t mark[kChunk / 32];          // a bit for each of them
+  int before[kChunk / 32 + 1];         // marks in earlier words
   int token[kMaxNodes];
   int16_t parent[kMaxNodes];
-  int ntouched;
   int bad;
 };
-static_assert(sizeof(Shared) <= 49152, "four CTAs an SM, no opt-in");
+static_assert(sizeof(Shared) <= 45 * 1024, "five CTAs an SM, no opt-in");
 
 struct Rates {
   float rep, pres, freq;
@@ -64,24 +72,18 @@ __device__ __forceinline__ float apply(float x, uint32_t word, uint32_t more, fl
   return __fadd_rn(x, bias);
 }
 
-// one logit of a row; read_logit's may have been written by this warp before
-// (in place), so it goes through the ordinary path
-template <bool BF16>
-__device__ __forceinline__ float read_logit(const void* row, int v) {
-  return BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[v]) << 16)
-              : static_cast<const float*>(row)[v];
-}
+// one logit of a row (with plain loads: the rows may be rewritten in place)
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* row, int v) {
-  return BF16 ? __uint_as_float(static_cast<uint32_t>(__ldcs(static_cast<const uint16_t*>(row) + v)) << 16)
-              : __ldcs(static_cast<const float*>(row) + v);
+  return BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[v]) << 16)
+              : static_cast<const float*>(row)[v];
 }
 // four of them, as loaded
 template <bool BF16>
 struct Raw4 {
   uint2 w;
   __device__ __forceinline__ void load(const void* row, int v) {
-    w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + v));
+    w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + v);
   }
   __device__ __forceinline__ float4 value() const {
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
@@ -92,7 +94,7 @@ template <>
 struct Raw4<false> {
   float4 w;
   __device__ __forceinline__ void load(const void* row, int v) {
-    w = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + v));
+    w = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + v);
   }
   __device__ __forceinline__ float4 value() const { return w; }
 };
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   r.rep = a.repetition ? __ldg(a.repetition + b) : 1.0f;
   r.pres = a.presence ? __ldg(a.presence + b) : 0.0f;
   r.freq = a.frequency ? __ldg(a.frequency + b) : 0.0f;
-  if (tid == 0) s.bad = s.ntouched = 0;
+  if (tid == 0) s.bad = 0;
   const bool rows_ok = nodes >= 1 && n0 >= 0 && n0 + nodes <= a.total_nodes;
   const int N = rows_ok ? static_cast<int>(nodes) : 0;
   bool bad = !rows_ok || N > a.max_nodes || h0 < 0 || h1 < h0 || h1 > a.total_history || e0 < 0 || e1 < e0 ||
@@ -133,8 +135,7 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     *reinterpret_cast<uint4*>(&s.count[i]) = zero;
     if (a.bias_ids) *reinterpret_cast<uint4*>(&s.entry[i]) = none;
   }
-  *reinterpret_cast<uint4*>(&s.path[0][0] + 4 * tid) = zero;
-  static_assert(kWarps * (kChunk / 32) == 4 * kThreads, "one store per thread clears the bitmaps");
+  if (tid < kWarps * (kChunk / 32) / 4) *reinterpret_cast<uint4*>(&s.path[0][0] + 4 * tid) = zero;
   __syncthreads();
   if (!bad) {
     for (int i = tid; i < N; i += kThreads) {
@@ -171,131 +172,156 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   if (!rows_ok) return;
   const bool has_bias = a.bias_ids != nullptr;
   if (!bad) {
-    for (int i = tid; i < kChunk; i += kThreads) {
-      const int e = has_bias ? s.entry[i] : -1;
-      if (has_bias) s.bias[i] = e >= 0 ? __ldg(a.bias_values + e) : 0.0f;
-      if (s.count[i] || e >= 0) s.touched[atomicAdd(&s.ntouched, 1)] = static_cast<uint16_t>(i);
+    // the marks, their prefix counts, and the list
+    constexpr int kWords = kChunk / 32 / kWarps;  // per warp
+    int v = (warp * kWords) * 32 + lane;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k, v += 32) {
+      const int e = has_bias ? s.entry[v] : -1;
+      if (has_bias) s.bias[v] = e >= 0 ? __ldg(a.bias_values + e) : 0.0f;
+      const uint32_t m = __ballot_sync(0xffffffffu, s.count[v] != 0u || e >= 0);
+      if (lane == 0) s.mark[warp * kWords + k] = m;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < kChunk / 1024; ++k) {
+        const int c = __popc(s.mark[32 * k + lane]);
+        int x = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        s.before[32 * k + lane] = n + x - c;
+        n += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) s.before[kChunk / 32] = n;
+    }
+    __syncthreads();
+    v = (warp * kWords) * 32 + lane;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k, v += 32) {
+      const uint32_t m = s.mark[v >> 5];
+      if (m >> lane & 1u) s.touched[s.before[v >> 5] + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(v);
     }
     __syncthreads();
   }
-  const int ntouched = bad ? 0 : s.ntouched;  // (bad: the rows as given)
+  const bool any_touched = !bad && s.before[kChunk / 32] > 0;  // (bad: the rows as given)
   const uint32_t* mask = bad ? nullptr : a.allowed_mask;
   const int words = (a.vocab + 31) / 32;
   uint32_t* path = s.path[warp];
+  float* block = s.block[warp];
   for (int i = blockIdx.z * kWarps + warp; i < N; i += gridDim.z * kWarps) {
     const size_t row = static_cast<size_t>(n0 + i);
     const void* in = static_cast<const uint8_t*>(a.logits) + row * a.vocab * (BF16 ? 2 : 4);
     float* out = a.out + row * a.vocab;
     const uint32_t* mrow = mask ? mask + row * words : nullptr;
-    // a masked copy, 1024 entries (a mask word a lane) at a time, the next ones
-    // in flight while these are stored
+    // the next entries of the row, in flight: 1024 as loaded, a mask word a lane
     Raw4<BF16> x[8];
+    float z[VEC ? 1 : 32];
     uint32_t mw = ~0u;
     auto fetch = [&](int b0) {
-      if (VEC) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int v = b0 + 128 * u + 4 * lane;
-          if (v < nv) x[u].load(in, c0 + v);
+      for (int u = 0; u < (VEC ? 8 : 32); ++u) {
+        const int v = b0 + (VEC ? 128 * u + 4 * lane : 32 * u + lane);
+        if (v >= nv) continue;
+        if constexpr (VEC) {
+          x[u].load(in, c0 + v);
+        } else {
+          z[u] = load_logit<BF16>(in, c0 + v);
         }
       }
       if (mrow && b0 + 32 * lane < nv) mw = __ldg(mrow + ((c0 + b0) >> 5) + lane);
     };
     fetch(0);
+    // marks the drafted tokens of the path in this chunk: lane k looks at every
+    // 32nd ancestor from the node up
+    bool any = false;
+    if (!bad) {
+      int j = i;
+      for (int k = 0; k < lane && j > 0; ++k) j = s.parent[j];
+      while (__any_sync(0xffffffffu, j > 0)) {
+        const int v = j > 0 ? s.token[j] - c0 : -1;
+        const bool mine = v >= 0 && v < nv;
+        if (mine) atomicOr(&path[v >> 5], 1u << (v & 31));
+        any |= __any_sync(0xffffffffu, mine);
+        for (int k = 0; k < 32 && j > 0; ++k) j = s.parent[j];
+      }
+      __syncwarp();
+    }
+    // the masked copy, and the touched entries that are not on the path
 #pragma unroll 1
     for (int b0 = 0; b0 < nv; b0 += 1024) {
       const uint32_t word = mw;
-      if (VEC) {
-        float4 y[8];
+      float4 y[VEC ? 8 : 1];
+      float w[VEC ? 1 : 32];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] = x[u].value();
-        fetch(b0 + 1024);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int v = b0 + 128 * u + 4 * lane;
-          const uint32_t ok = __shfl_sync(0xffffffffu, word, 4 * u + (lane >> 3)) >> (v & 31);
-          if (v < nv)
-            *reinterpret_cast<float4*>(out + c0 + v) =
-                make_float4(ok & 1u ? y[u].x : -INFINITY, ok & 2u ? y[u].y : -INFINITY,
-                            ok & 4u ? y[u].z : -INFINITY, ok & 8u ? y[u].w : -INFINITY);
+      for (int u = 0; u < (VEC ? 8 : 32); ++u) {
+        if constexpr (VEC) {
+          y[u] = x[u].value();
+        } else {
+          w[u] = z[u];
         }
-      } else {
+      }
+      fetch(b0 + 1024);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          constexpr int kU = 16;
-          float z[kU];
+      for (int half = 0; half < 2; ++half) {
+        const int h0 = b0 + kBlock * half;
+        if (h0 >= nv) break;
 #pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const int v = b0 + 512 * half + 32 * u + lane;
-            if (v < nv) z[u] = load_logit<BF16>(in, c0 + v);
-          }
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const int v = b0 + 512 * half + 32 * u + lane;
-            const uint32_t ok = __shfl_sync(0xffffffffu, word, 16 * half + u) >> lane & 1u;
-            if (v < nv) out[c0 + v] = ok ? z[u] : -INFINITY;
+        for (int q = 0; q < (VEC ? 4 : 16); ++q) {
+          if constexpr (VEC) {
+            const int u = 4 * half + q, v = b0 + 128 * u + 4 * lane;
+            const uint32_t ok = __shfl_sync(0xffffffffu, word, 4 * u + (lane >> 3)) >> (v & 31);
+            const float4 t = make_float4(ok & 1u ? y[u].x : -INFINITY, ok & 2u ? y[u].y : -INFINITY,
+                                         ok & 4u ? y[u].z : -INFINITY, ok & 8u ? y[u].w : -INFINITY);
+            if (v < nv) *reinterpret_cast<float4*>(out + c0 + v) = t;
+            if (any_touched) *reinterpret_cast<float4*>(block + 128 * q + 4 * lane) = t;
+          } else {
+            const int u = 16 * half + q, v = b0 + 32 * u + lane;
+            const float t = __shfl_sync(0xffffffffu, word, u) >> lane & 1u ? w[u] : -INFINITY;
+            if (v < nv) out[c0 + v] = t;
+            if (any_touched) block[32 * q + lane] = t;
           }
         }
-        fetch(b0 + 1024);
+        if (!any_touched) continue;
+        __syncwarp();
+        const int k1 = s.before[(h0 + kBlock) >> 5];
+        for (int k = s.before[h0 >> 5] + lane; k < k1; k += 32) {
+          const int v = s.touched[k];
+          const float t = block[v - h0];
+          if (t != -INFINITY && !(any && (path[v >> 5] >> (v & 31) & 1u)))
+            out[c0 + v] = apply(t, s.count[v], 0, has_bias ? s.bias[v] : 0.0f, r);
+        }
+        __syncwarp();
       }
     }
-    if (bad) continue;
-    __syncwarp();
-    // From here on entries are read again, each before it is rewritten: an
+    if (!any) continue;
+    // the path's tokens: the node nearest to the row computes a token.  An
     // allowed one still holds its logit in place, a masked one stays -inf.
-    auto allowed = [&](int v) { return !mrow || (__ldg(mrow + ((c0 + v) >> 5)) >> (v & 31) & 1u); };
-    // the drafted tokens of the path in this chunk: lane k looks at every 32nd
-    // ancestor from the node up; the node nearest to the row computes a token
-    bool any = false;
     int j = i;
     for (int k = 0; k < lane && j > 0; ++k) j = s.parent[j];
     while (__any_sync(0xffffffffu, j > 0)) {
       const int v = j > 0 ? s.token[j] - c0 : -1;
-      bool mine = v >= 0 && v < nv;
-      if (mine) {
+      if (v >= 0 && v < nv) {
         uint32_t more = 0;
         for (int m = i; m > 0; m = s.parent[m]) {
           if (s.token[m] != v + c0) continue;
-          if (more == 0 && m != j) {
-            mine = false;
-            break;
-          }
+          if (more == 0 && m != j) break;
           ++more;
         }
-        if (mine) {
-          if (allowed(v))
-            out[c0 + v] = apply(read_logit<BF16>(in, c0 + v), s.count[v], more, has_bias ? s.bias[v] : 0.0f, r);
-          atomicOr(&path[v >> 5], 1u << (v & 31));
+        if (more > 0 && (!mrow || (__ldg(mrow + ((c0 + v) >> 5)) >> (v & 31) & 1u))) {
+          const float t = load_logit<BF16>(in, c0 + v);
+          if (t != -INFINITY) out[c0 + v] = apply(t, s.count[v], more, has_bias ? s.bias[v] : 0.0f, r);
         }
       }
-      any |= __any_sync(0xffffffffu, mine);
       for (int k = 0; k < 32 && j > 0; ++k) j = s.parent[j];
     }
     __syncwarp();
-    // the touched entries that are not on the path
-    constexpr int kT = 8;  // gathers in flight
-    for (int k0 = lane; k0 < ntouched; k0 += 32 * kT) {
-      int v[kT];
-      uint32_t ok[kT];
-      float x[kT];
-#pragma unroll
-      for (int u = 0; u < kT; ++u) {
-        v[u] = k0 + 32 * u < ntouched ? s.touched[k0 + 32 * u] : -1;
-        ok[u] = 0;
-        if (v[u] < 0) continue;
-        ok[u] = mrow ? __ldg(mrow + ((c0 + v[u]) >> 5)) >> (v[u] & 31) & 1u : 1u;
-        x[u] = read_logit<BF16>(in, c0 + v[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < kT; ++u)
-        if (ok[u] && !(any && (path[v[u] >> 5] >> (v[u] & 31) & 1u)))
-          out[c0 + v[u]] = apply(x[u], s.count[v[u]], 0, has_bias ? s.bias[v[u]] : 0.0f, r);
-    }
-    if (any) {
-      __syncwarp();
-      for (int k = lane; k < kChunk / 32; k += 32) path[k] = 0u;
-      __syncwarp();
-    }
+    for (int k = lane; k < kChunk / 32; k += 32) path[k] = 0u;
+    __syncwarp();
   }
 }
 
@@ -303,11 +329,11 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
 
 int launch_penalty(const PenaltyArgs& a, int sms, cudaStream_t stream) {
   const int chunks = (a.vocab + kChunk - 1) / kChunk;
-  // shares of a tree's rows: enough CTAs to fill the SMs (4 fit one), at least
+  // shares of a tree's rows: enough CTAs to fill the SMs (5 fit one), at least
   // a row per warp
   const long long base = static_cast<long long>(chunks) * a.batch;
   const int most = (a.max_nodes + kWarps - 1) / kWarps;
-  long long shares = (4ll * sms + base - 1) / base;
+  long long shares = (5ll * sms + base - 1) / base;
   shares = shares < 1 ? 1 : (shares > most ? most : shares);
   const dim3 grid(chunks, a.batch, static_cast<unsigned>(shares));
   const bool vec = a.vocab % 4 == 0;  // (row starts are then 16-byte aligned, bf16 rows 8-byte)
