@@ -28,7 +28,7 @@
 // Bound: HBM; per entry 4 (fp32) or 2 (bf16) bytes read, 4 written, a mask bit.
 // 16 trees of 26 or 64 nodes, V = 32000, bf16, histories of 512 to 4096: 36 us
 // (4.0 TB/s: each tree's history is counted by all of its 16 chunks' CTAs).
-// 4 trees of 128 nodes, V = 151936, fp32, histories of 1600: 112 us (5.7 TB/s).
+// 4 trees of 128 nodes, V = 151936, fp32, histories of 1600: 107 us (5.9 TB/s).
 #include <math.h>
 
 #include "tv_device.cuh"
@@ -59,7 +59,7 @@ struct Shared {
   int16_t parent[kMaxNodes];
   int bad;
 };
-static_assert(sizeof(Shared) <= 45 * 1024, "five CTAs an SM, no opt-in");
+static_assert(sizeof(Shared) <= 45 * 1024, "no opt-in, and no fewer CTAs an SM than the registers allow");
 
 struct Rates {
   float rep, pres, freq;
@@ -218,13 +218,16 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     const void* in = static_cast<const uint8_t*>(a.logits) + row * a.vocab * (BF16 ? 2 : 4);
     float* out = a.out + row * a.vocab;
     const uint32_t* mrow = mask ? mask + row * words : nullptr;
-    // the next entries of the row, in flight: 1024 as loaded, a mask word a lane
-    Raw4<BF16> x[8];
-    float z[VEC ? 1 : 32];
+    // the next entries of the row, in flight as loaded, a mask word a lane.  (fp32
+    // with 1024 of them: 100 registers a thread, 112 us for the second case)
+    constexpr int kStep = BF16 ? 1024 : 512;
+    constexpr int kLoads = kStep / (VEC ? 128 : 32);
+    Raw4<BF16> x[VEC ? kLoads : 1];
+    float z[VEC ? 1 : kLoads];
     uint32_t mw = ~0u;
     auto fetch = [&](int b0) {
 #pragma unroll
-      for (int u = 0; u < (VEC ? 8 : 32); ++u) {
+      for (int u = 0; u < kLoads; ++u) {
         const int v = b0 + (VEC ? 128 * u + 4 * lane : 32 * u + lane);
         if (v >= nv) continue;
         if constexpr (VEC) {
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
           z[u] = load_logit<BF16>(in, c0 + v);
         }
       }
-      if (mrow && b0 + 32 * lane < nv) mw = __ldg(mrow + ((c0 + b0) >> 5) + lane);
+      if (mrow && lane < kStep / 32 && b0 + 32 * lane < nv) mw = __ldg(mrow + ((c0 + b0) >> 5) + lane);
     };
     fetch(0);
     // marks the drafted tokens of the path in this chunk: lane k looks at every
@@ -253,21 +256,21 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     }
     // the masked copy, and the touched entries that are not on the path
 #pragma unroll 1
-    for (int b0 = 0; b0 < nv; b0 += 1024) {
+    for (int b0 = 0; b0 < nv; b0 += kStep) {
       const uint32_t word = mw;
-      float4 y[VEC ? 8 : 1];
-      float w[VEC ? 1 : 32];
+      float4 y[VEC ? kLoads : 1];
+      float w[VEC ? 1 : kLoads];
 #pragma unroll
-      for (int u = 0; u < (VEC ? 8 : 32); ++u) {
+      for (int u = 0; u < kLoads; ++u) {
         if constexpr (VEC) {
           y[u] = x[u].value();
         } else {
           w[u] = z[u];
         }
       }
-      fetch(b0 + 1024);
+      fetch(b0 + kStep);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int half = 0; half < kStep / kBlock; ++half) {
         const int h0 = b0 + kBlock * half;
         if (h0 >= nv) break;
 #pragma unroll
@@ -329,8 +332,8 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
 
 int launch_penalty(const PenaltyArgs& a, int sms, cudaStream_t stream) {
   const int chunks = (a.vocab + kChunk - 1) / kChunk;
-  // shares of a tree's rows: enough CTAs to fill the SMs (5 fit one), at least
-  // a row per warp
+  // shares of a tree's rows: 5 CTAs an SM, two or three of them at a time (2
+  // an SM: 44 and 121 us, 8: 37 and 110), at least a row per warp
   const long long base = static_cast<long long>(chunks) * a.batch;
   const int most = (a.max_nodes + kWarps - 1) / kWarps;
   long long shares = (5ll * sms + base - 1) / base;
