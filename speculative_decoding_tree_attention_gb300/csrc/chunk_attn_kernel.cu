@@ -615,9 +615,10 @@ struct OwnO {
 //
 // A thread per row (more than half as many rows as threads): piece `own` from
 // TMEM and registers (bit for bit what its slot would hold), the others from
-// their slots, 64 columns of a piece in flight.  Writing and reading its own
-// slot too, 16 columns at a time, took 28000 clocks of a 250-row unit.
-template <int D>
+// their slots, W columns of a piece in flight.  (Writing and reading its own
+// slot too, 16 columns at a time, took 28000 clocks of a 250-row unit.  E4M3: W
+// = 32; 64 spill, four 32768-token decodes 92 us instead of 86.)
+template <int D, int W>
 __device__ void merge_rows(const ChunkArgs& a, const Piece& pc, int ur, int own, float m_own, float l_own,
                            int bad, const OwnO<D>& o) {
   const Slots<D> sl(a, pc);
@@ -634,34 +635,34 @@ __device__ void merge_rows(const ChunkArgs& a, const Piece& pc, int ur, int own,
   const QuadRows quad =
       quad_rows<D>(a, static_cast<size_t>(pc.tok0 + row / a.group) * a.hq + pc.kvh * a.group + row % a.group, live);
 #pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 64) {
+  for (int c0 = 0; c0 < D; c0 += W) {
     float l = 0.0f;
-    float acc[64];
+    float acc[W];
 #pragma unroll
-    for (int k = 0; k < 64; ++k) acc[k] = 0.0f;
+    for (int k = 0; k < W; ++k) acc[k] = 0.0f;
 #pragma unroll 1
     for (int s = 0; s < np; ++s) {
-      float x[64];
+      float x[W];
       float2 ml = make_float2(m_own, l_own);
       if (s == own) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) o.load(c0 + c, *reinterpret_cast<float(*)[32]>(&x[c]));
+        for (int c = 0; c < W; c += 32) o.load(c0 + c, *reinterpret_cast<float(*)[32]>(&x[c]));
       } else {
         ml = sl.ml(s, row);
         const float4* o4 = sl.o(s, row) + (c0 / 4) * rows;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) *reinterpret_cast<float4*>(&x[4 * k]) = __ldcg(o4 + k * rows);
+        for (int k = 0; k < W / 4; ++k) *reinterpret_cast<float4*>(&x[4 * k]) = __ldcg(o4 + k * rows);
       }
       const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
       l += w * ml.y;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) acc[k] += w * x[k];
+      for (int k = 0; k < W; ++k) acc[k] += w * x[k];
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 64; ++k) acc[k] = bad ? 0.0f : acc[k] * inv;
+    for (int k = 0; k < W; ++k) acc[k] = bad ? 0.0f : acc[k] * inv;
 #pragma unroll
-    for (int c = 0; c < 64; c += 32)
+    for (int c = 0; c < W; c += 32)
       store_rows32(a, quad, c0 + c, *reinterpret_cast<const float(*)[32]>(&acc[c]));
   }
 }
@@ -1112,8 +1113,8 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + ct * 128;
               uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (ct >> 3) * Ly::kGroupBytes + (ct & 7) * 128;
               const int sw = (ct & 7) << 4;
-              // rolled: 91 us on four 32768-token decodes, 97 and 112 us unrolled by
-              // 4 and 8 (the kernel's loops share one instruction cache)
+              // rolled: unrolled by 4 and 8 four 32768-token decodes take 6 and 21 us
+              // more (the kernel's loops share one instruction cache)
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {
                 uint32_t h[8];
@@ -1172,10 +1173,12 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
         const size_t q_row = static_cast<size_t>(pc.tok0 + tok);
         const int head = pc.kvh * g + (live ? ur - tok * g : 0);
         // E4M3: the row's scale is folded into the exponent factor (kept above
-        // 0, so that a masked -inf never meets a factor of 0)
+        // 0, so that a masked -inf never meets a factor of 0; NaN stays)
         float cq = a.scale_log2;
-        if constexpr (F8)
-          if (live) cq = fmaxf(a.scale_log2 * __ldg(a.q_scale + q_row * a.hq + head), 1e-37f);
+        if constexpr (F8) {
+          if (live) cq = a.scale_log2 * __ldg(a.q_scale + q_row * a.hq + head);
+          if (cq < 1e-37f) cq = 1e-37f;
+        }
 
         float m_run = -INFINITY;  // running max (log2 units)
         float l_run = 0.0f;       // row sum against m_run
@@ -1206,10 +1209,11 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               mbar_wait(&vfull[vs], (gt / kVStages) & 1, abort_flag);  // acquire the TMA writes
               const int key = k0 + r;
               if (!(key <= hi && (key < a.sinks || key >= lo))) {
+                // (eight neighbouring rows, eight chunks: every bank once)
                 uint8_t* row = smem + Ly::kVRing + vs * Ly::kTileBytes + (r >> 3) * Ly::kGroupBytes + (r & 7) * 128;
 #pragma unroll
                 for (int k = 0; k < 8 * Ly::kHalves; ++k)
-                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(row + (k >> 3) * 1024 + ((k ^ r) & 7) * 16) = make_uint4(0, 0, 0, 0);
               }
               fence_proxy_async_smem();  // generic writes, read by the MMA
             }
@@ -1401,7 +1405,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           if (merge) {
             __threadfence();
             if (step == 1) {
-              merge_rows<D>(a, pc, ur, static_cast<int>(blockIdx.x) - pc.vfirst(), m_run, l_run, flag, own_o);
+              merge_rows<D, F8 ? 32 : 64>(a, pc, ur, static_cast<int>(blockIdx.x) - pc.vfirst(), m_run, l_run, flag, own_o);
             } else {
               merge_groups<D>(a, pc, ur, step);
             }

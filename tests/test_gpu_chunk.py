@@ -276,6 +276,23 @@ def test_unseen_places_do_not_matter_fp8():
         np.testing.assert_array_equal(a, got)
 
 
+def test_a_query_scale_that_is_nan_shows():
+    """The rows of that query are NaN, not weighted by something else; the rows
+    of the others do not change."""
+    c = quantised(make([200, 40], [70, 3], 4, 2, 128, seed=13))
+    want, _ = call_fp8(c)
+    bad = dict(c, q_scale=c["q_scale"].copy())
+    hit = [(0, 1), (69, 3), (71, 0)]
+    for t, h in hit:
+        bad["q_scale"][t, h] = np.nan
+    got, st = call_fp8(bad)
+    assert (st == 0).all()
+    for t, h in hit:
+        assert np.isnan(got[t, h]).all()
+        got[t, h] = want[t, h]
+    np.testing.assert_array_equal(got, want)
+
+
 @pytest.mark.parametrize("hq, hkv, d", [(256, 1, 64), (100, 1, 128), (129, 1, 64), (48, 16, 128)])
 def test_groups_of_every_size(hq, hkv, d):
     """g = 256: one token per unit; 129: one token, two m-tiles; 3: 85 tokens."""
