@@ -448,7 +448,8 @@ int tv_commit_kv(const tv_commit_params* params, const uint16_t* k_nodes,
  *     token_offsets[batch] are left as they were.
  *   - A sequence with a malformed extent (C_b < 0, C_b > seq_lens[b], rows past
  *     total_tokens, seq_lens[b] > max_len) or a bad block id of a page that it
- *     sees gets status TV_ERR_BAD_TREE and all-zero rows.
+ *     sees gets status TV_ERR_BAD_TREE and all-zero rows.  So do all sequences
+ *     after one with C_b < 0 (their rows would be counted twice).
  * Inputs bf16, accumulation and softmax fp32, output bf16 or fp32; P is rounded
  * to bf16 for the P V product, so the fp32 output carries that rounding.
  * Repeated calls agree bit for bit.
@@ -467,7 +468,7 @@ typedef struct {
   int32_t window;             /* 0: every earlier token, else >= 1             */
   int32_t sinks;              /* first tokens that stay visible next to a window */
   int32_t out_dtype;          /* tv_out_dtype of `out`                         */
-  float softmax_scale;        /* 0 => 1/sqrt(D)                                */
+  float softmax_scale;        /* finite, >= 0; 0 => 1/sqrt(D)                  */
   int64_t q_stride;           /* elements between the rows of q (a slice of a
                                  fused projection), 0 => Hq*D; rows 16-byte aligned */
 } tv_chunk_params;            /* host struct */
@@ -613,8 +614,8 @@ typedef struct {
   int32_t vocab;         /* V, 1 <= V < 2^18                               */
   int32_t max_nodes;     /* >= every N_b, <= TV_MAX_NODES                  */
   int32_t total_nodes;   /* node_offsets[batch] (host copy)                */
-  int32_t total_history; /* entries of history                             */
-  int32_t total_bias;    /* entries of bias_ids and bias_values            */
+  int32_t total_history; /* entries of history, <= 2^30                    */
+  int32_t total_bias;    /* entries of bias_ids and bias_values, <= 2^30   */
   int32_t logits_dtype;  /* tv_out_dtype of `logits`: bf16 (0) or fp32 (1) */
 } tv_penalty_params;     /* host struct */
 

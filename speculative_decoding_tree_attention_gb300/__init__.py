@@ -564,11 +564,19 @@ def _empty(t, shape, dtype, dev):
     return _torch().empty(shape, dtype=dtype, device=f"cuda:{dev}") if t is None else t
 
 
+def _int32(**counts):
+    """Refuses what ctypes would cut to its low 32 bits."""
+    for name, n in counts.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            _bad(name, "a 32-bit count")
+
+
 def chunk_params(q, k_pool, block_table, seq_lens, *, max_len: int, window: int = 0, sinks: int = 0,
                  softmax_scale: float = 0.0, out_dtype: str = "bf16") -> ChunkParams:
     """The parameters of a chunk_attention or chunk_attention_fp8 call."""
     if out_dtype not in OUT_DTYPES:
         _bad("out_dtype", "'bf16' or 'fp32'")
+    _int32(max_len=max_len, window=window, sinks=sinks)
     total, hq, d = q.shape
     return ChunkParams(seq_lens.shape[0], hq, k_pool.shape[1], d, k_pool.shape[2],
                        block_table.shape[1], k_pool.shape[0], total, max_len, window, sinks,
@@ -824,6 +832,7 @@ def commit_kv_fp8(k_nodes, k_nodes_scale, v_nodes, v_nodes_scale, parent, node_o
             ("new_prefix_lens", new_prefix_lens, i32, (batch,)), ("status", status, i32, (batch,))):
         if t is not None or name not in ("new_prefix_lens", "status"):
             _arg(name, t, dtype, shape, dev)
+    _int32(max_nodes=max_nodes)
     prm = CommitParams(batch, hkv, d, TV_BLOCK_SIZE, width, ps[0], max_nodes, total)
 
     def call(handle):
@@ -896,6 +905,7 @@ def penalize_logits(logits, draft_tokens, parent, node_offsets, *, max_nodes: in
         _arg("out", out, f32, (total, vocab), dev)
     if status is not None:
         _arg("status", status, i32, (batch,), dev)
+    _int32(max_nodes=max_nodes, history=n_hist, bias_ids=n_bias)
     prm = PenaltyParams(batch, vocab, max_nodes, total, n_hist, n_bias, 1 if logits.dtype is f32 else 0)
 
     def call(handle):

@@ -163,6 +163,7 @@ struct Layout {
 
 struct Misc {
   uint32_t tmem_base;
+  int decrease;               // the first sequence whose chunk has a negative length
   int abort;
   int npieces;                // pieces of this round
   int more;                   // another round follows
@@ -365,17 +366,23 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
 
   int units = 0;      // units of the current chunk of sequences
   int loaded = -1;    // the chunk in shared memory
+  int decrease = round == 0 ? INT_MAX : misc->decrease;  // known to the current pass
   auto load_chunk = [&](int base) {
     if (loaded == base) return;
     const int b = base + sid;
     SeqInfo s;
     s.units = s.n0 = s.C = s.len = s.bad = 0;
-    if (b < a.batch) s = seq_info(a, b);
+    if (b < a.batch) {
+      s = seq_info(a, b);
+      if (s.bad && __ldg(a.token_offsets + b + 1) < s.n0) atomicMin(&misc->decrease, b);
+      if (b > misc->decrease) s.C = s.units = 0, s.bad = 1;
+    }
     if (round == 0 && s.bad && b % gridDim.x == blockIdx.x) {
       record_status(a.status, b, kBadTree);
       misc->zero_needed = 1;
     }
     seq_u[sid] = scan256(s.units, scratch, sid, &units);
+    if (misc->decrease < decrease) units = 0;  // (the pass is repeated)
     seq_n0[sid] = s.n0;
     seq_c[sid] = s.C;
     seq_ctx[sid] = s.len - s.C;
@@ -464,6 +471,14 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
       kept = pass == 0 && a.batch <= kSoftmaxThreads && units <= kSoftmaxThreads;
       named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
     }
+    if (pass == 0 && misc->decrease < decrease) {
+      // Where the offsets decrease, later sequences' rows are counted twice: the
+      // line could pass 32 bits.  Once more without them.
+      decrease = misc->decrease;
+      loaded = pass = -1;
+      kept = false;
+      continue;
+    }
     if (pass == 0) {
       line->V = max(1, min(a.vctas, cum / max(1, a.min_range)));
       line->q = cum / line->V;
@@ -477,8 +492,10 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
     const size_t row_bytes = static_cast<size_t>(a.hq) * D * (a.out_fp32 ? 4 : 2);
 #pragma unroll 1
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-      if (!seq_info(a, b).bad) continue;
-      const long long n0 = a.token_offsets[b], n1 = a.token_offsets[b + 1];
+      if (!seq_info(a, b).bad && b <= misc->decrease) continue;
+      // (behind a decrease: only rows that no sound sequence has)
+      const long long n0 = max(a.token_offsets[b], b > misc->decrease ? a.token_offsets[misc->decrease] : INT_MIN);
+      const long long n1 = a.token_offsets[b + 1];
       if (n0 < 0 || n1 <= n0 || n1 > a.total_tokens) continue;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
 #pragma unroll 1
@@ -757,6 +774,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   if (tid == 0) {
     misc->abort = 0;
     misc->zero_needed = 0;
+    misc->decrease = INT_MAX;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 2);  // one arrival per m-tile

@@ -1,6 +1,7 @@
 // tv_api.cu -- the C ABI of libtv (include/tv.h): argument checks on the host,
 // launch configuration, TMA tensor maps, and launches on the caller's stream.
 // The library allocates nothing and never synchronises.
+#include <cfloat>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -155,6 +156,7 @@ bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
   if (p->max_len < 0 || p->max_len > INT32_MAX - 256) return false;
   if ((p->max_len + 15) / 16 > p->max_blocks_per_seq) return false;
   if (p->window < 0 || p->sinks < 0) return false;
+  if (!(p->softmax_scale >= 0.0f && p->softmax_scale <= FLT_MAX)) return false;
   if (p->out_dtype != TV_OUT_BF16 && p->out_dtype != TV_OUT_FP32) return false;
   if (static_cast<int64_t>(p->num_blocks) * p->num_kv_heads * 16 >= (1ll << 31)) return false;
   if (static_cast<int64_t>(p->total_tokens) * p->num_q_heads >= (1ll << 31)) return false;
@@ -167,7 +169,7 @@ bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
                                 (static_cast<int64_t>(p->window) + pl.unit_tokens + 253) / 128);
   const int64_t wmax =
       units * p->num_kv_heads * (std::max<int64_t>(tiles, 1) * tv::kChunkTileCost + tv::kChunkPieceCost);
-  if (units * p->num_kv_heads >= (1ll << 31) || wmax >= (1ll << 31)) return false;  // counted in 32 bits
+  if (wmax >= (1ll << 31)) return false;  // counted in 32 bits
   // at most 4096 CTAs: the range boundaries are fp32 products below 2^24
   pl.vctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms, wmax / kMinRange, 4096})));
   pl.workspace = (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256 +
@@ -644,8 +646,9 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
   a.unit_tokens = pl.unit_tokens;
   a.vctas = pl.vctas;
   a.min_range = kMinRange;
-  a.window = p->window;
-  a.sinks = p->sinks;
+  // a window of max_len or more hides nothing; neither count overflows in the kernel
+  a.window = p->window >= p->max_len ? 0 : p->window;
+  a.sinks = std::min(p->sinks, p->max_len);
   a.out_fp32 = p->out_dtype == TV_OUT_FP32 ? 1 : 0;
   a.fp8 = fp8 ? 1 : 0;
   const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
@@ -787,7 +790,8 @@ int tv_penalize_logits(const tv_penalty_params* p, const void* logits,
   if (p->batch < 1 || p->batch > 65535 || p->vocab < 1 || p->vocab >= (1 << 18)) return TV_ERR_INVALID_ARG;
   if (p->max_nodes < 1 || p->max_nodes > TV_MAX_NODES || p->total_nodes < p->batch) return TV_ERR_INVALID_ARG;
   if (p->logits_dtype != TV_OUT_BF16 && p->logits_dtype != TV_OUT_FP32) return TV_ERR_INVALID_ARG;
-  if (p->total_history < 0 || p->total_bias < 0) return TV_ERR_INVALID_ARG;
+  if (p->total_history < 0 || p->total_history > (1 << 30) || p->total_bias < 0 || p->total_bias > (1 << 30))
+    return TV_ERR_INVALID_ARG;
   const void* ptrs[] = {logits, draft_tokens, parent, node_offsets, out, status};
   for (const void* q : ptrs)
     if (!q || !aligned16(q)) return TV_ERR_INVALID_ARG;
@@ -797,8 +801,13 @@ int tv_penalize_logits(const tv_penalty_params* p, const void* logits,
     if (q && !aligned16(q)) return TV_ERR_INVALID_ARG;
   if (history && !history_offsets) return TV_ERR_INVALID_ARG;
   if (bias_ids && (!bias_values || !bias_offsets)) return TV_ERR_INVALID_ARG;
-  // in place only with fp32 logits (a bf16 row is half as long as its output)
-  if (p->logits_dtype == TV_OUT_BF16 && logits == static_cast<const void*>(out)) return TV_ERR_INVALID_ARG;
+  // in place with fp32 logits, which no other row's output may lie over (a bf16
+  // row is half as long as its output)
+  const uint64_t entries = static_cast<uint64_t>(p->total_nodes) * p->vocab;
+  const uint64_t in0 = reinterpret_cast<uintptr_t>(logits), out0 = reinterpret_cast<uintptr_t>(out);
+  const bool bf16 = p->logits_dtype == TV_OUT_BF16;
+  if ((bf16 || in0 != out0) && in0 < out0 + entries * 4 && out0 < in0 + entries * (bf16 ? 2 : 4))
+    return TV_ERR_INVALID_ARG;
   tv::PenaltyArgs a;
   a.logits = logits;
   a.out = out;

@@ -210,6 +210,28 @@ def test_malformed_sequences_are_zeroed_and_reported():
         assert (st == 5).any() and np.isfinite(got).all()
 
 
+def test_decreasing_offsets_end_the_batch():
+    """What comes after a chunk of negative length is malformed too: its rows
+    would be counted twice.  The second batch, so counted, has a line of work of
+    more than 2^31."""
+    c = make([40, 50, 60, 33, 20], [8, 50, 1, 3, 20], 8, 2, 128, seed=1)
+    good, _ = call(c)
+    got, st = call(dict(c, off=np.asarray([0, 8, 58, 50, 53, 73], np.int32)), max_len=60, fill=5.0)
+    assert st.tolist() == [0, 0, 5, 5, 5]
+    np.testing.assert_array_equal(got[:58], good[:58])  # (some of these are rows of sequences 3 and 4 too)
+    assert (got[58:73] == 0).all() and (got[73:] == 5.0).all()
+    for B in (128, 600):
+        n, top = 8192, 1 << 20
+        pool = torch.zeros(1, 64, 16, 64, dtype=torch.bfloat16, device="cuda")
+        q = torch.zeros(n, 64, 64, dtype=torch.bfloat16, device="cuda")
+        table = torch.zeros(B, top // 16, dtype=torch.int32, device="cuda")
+        off = torch.tensor([n * (b % 2) for b in range(B + 1)], dtype=torch.int32, device="cuda")
+        lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+        lens[2:] = top  # (the first sequence is sound: 8192 tokens over themselves)
+        _, st = tv.chunk_attention(q, pool, pool, table, lens, off, max_len=top)
+        assert st.tolist() == [0] + [5] * (B - 1)
+
+
 def test_rows_behind_the_last_sequence_stay():
     c = make([30, 9], [5, 9], 4, 2, 64, seed=2, extra_rows=7)
     for dt in ("fp32", "bf16"):

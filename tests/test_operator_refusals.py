@@ -32,7 +32,8 @@ BAD_CHUNK = [dict(batch=0), dict(num_q_heads=0), dict(num_q_heads=9), dict(num_k
              dict(max_len=129), dict(max_len=2 ** 31 - 1, max_blocks_per_seq=2 ** 30), dict(window=-1),
              dict(sinks=-1), dict(out_dtype=2), dict(num_blocks=2 ** 27, num_kv_heads=2),
              dict(total_tokens=2 ** 29), dict(q_stride=1023), dict(q_stride=8 * 128 + 4), dict(q_stride=-1024),
-             dict(q_stride=2 ** 40)]
+             dict(q_stride=2 ** 40), dict(softmax_scale=-0.1), dict(softmax_scale=float("nan")),
+             dict(softmax_scale=float("inf"))]
 
 
 @pytest.mark.parametrize("bad", BAD_CHUNK)
@@ -148,7 +149,8 @@ def penalty(**kw):
 
 @pytest.mark.parametrize("bad", [dict(batch=0), dict(batch=65536, total_nodes=70000), dict(vocab=0),
                                  dict(vocab=1 << 18), dict(max_nodes=0), dict(max_nodes=513), dict(total_nodes=1),
-                                 dict(total_history=-1), dict(total_bias=-1), dict(logits_dtype=2)])
+                                 dict(total_history=-1), dict(total_bias=-1), dict(logits_dtype=2),
+                                 dict(total_history=2 ** 30 + 1), dict(total_bias=2 ** 31 - 1)])
 def test_penalty_arguments(lib, bad):
     assert lib.tv_penalize_logits(C.byref(penalty(**bad)), *[P] * 16, None) == tv.TV_ERR_INVALID_ARG
 
@@ -166,6 +168,27 @@ def test_penalty_pointers(lib):
         assert lib.tv_penalize_logits(C.byref(penalty()), *args, None) == tv.TV_ERR_INVALID_ARG
     args = [P] * 16  # bf16 logits cannot be their own output
     assert lib.tv_penalize_logits(C.byref(penalty(logits_dtype=0)), *args, None) == tv.TV_ERR_INVALID_ARG
+
+
+def test_penalty_outputs_over_other_logits(lib):
+    """out may be fp32 logits themselves; any other overlap is refused.  10 rows
+    of 100: 4000 bytes of fp32, 2000 of bf16."""
+    def at(logits, out, dtype):
+        args = [P] * 16
+        args[0], args[14] = C.c_void_p(logits), C.c_void_p(out)
+        return lib.tv_penalize_logits(C.byref(penalty(logits_dtype=dtype)), *args, None)
+    for dtype, size in ((1, 4000), (0, 2000)):
+        for logits, out in ((1 << 20, (1 << 20) + 16), ((1 << 20) + 400, 1 << 20), (1 << 20, (1 << 20) + size - 16),
+                            ((1 << 20) + 4000 - 16, 1 << 20)):
+            assert at(logits, out, dtype) == tv.TV_ERR_INVALID_ARG
+
+
+def test_binding_counts_of_64_bits():
+    q, pool, table = torch.zeros(2, 2, 128), torch.zeros(2, 2, 16, 128), torch.zeros(1, 4, dtype=torch.int32)
+    lens = torch.zeros(1, dtype=torch.int32)
+    for kw in (dict(max_len=2 ** 32 + 5), dict(max_len=5, window=2 ** 31), dict(max_len=5, sinks=2 ** 32)):
+        with pytest.raises(ValueError):
+            tv.chunk_params(q, pool, table, lens, **kw)
 
 
 def test_binding_wants_cuda_tensors():
