@@ -163,7 +163,6 @@ struct Layout {
 
 struct Misc {
   uint32_t tmem_base;
-  int decrease;               // the first sequence whose chunk has a negative length
   int abort;
   int npieces;                // pieces of this round
   int more;                   // another round follows
@@ -281,7 +280,7 @@ __device__ __forceinline__ SeqInfo seq_info(const ChunkArgs& a, int b) {
   s.n0 = __ldg(a.token_offsets + b);
   const long long c = static_cast<long long>(__ldg(a.token_offsets + b + 1)) - s.n0;
   s.len = __ldg(a.seq_lens + b);
-  s.bad = c < 0 || (c > 0 && (s.n0 < 0 || s.n0 + c > a.total_tokens || s.len < c || s.len > a.max_len));
+  s.bad = c < 0 || b > __ldcg(a.counters + a.vctas) || (c > 0 && (s.n0 < 0 || s.n0 + c > a.total_tokens || s.len < c || s.len > a.max_len));
   s.C = s.bad ? 0 : static_cast<int>(c);
   s.units = (s.C + a.unit_tokens - 1) / a.unit_tokens;
   return s;
@@ -366,23 +365,17 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
 
   int units = 0;      // units of the current chunk of sequences
   int loaded = -1;    // the chunk in shared memory
-  int decrease = round == 0 ? INT_MAX : misc->decrease;  // known to the current pass
   auto load_chunk = [&](int base) {
     if (loaded == base) return;
     const int b = base + sid;
     SeqInfo s;
     s.units = s.n0 = s.C = s.len = s.bad = 0;
-    if (b < a.batch) {
-      s = seq_info(a, b);
-      if (s.bad && __ldg(a.token_offsets + b + 1) < s.n0) atomicMin(&misc->decrease, b);
-      if (b > misc->decrease) s.C = s.units = 0, s.bad = 1;
-    }
+    if (b < a.batch) s = seq_info(a, b);
     if (round == 0 && s.bad && b % gridDim.x == blockIdx.x) {
       record_status(a.status, b, kBadTree);
       misc->zero_needed = 1;
     }
     seq_u[sid] = scan256(s.units, scratch, sid, &units);
-    if (misc->decrease < decrease) units = 0;  // (the pass is repeated)
     seq_n0[sid] = s.n0;
     seq_c[sid] = s.C;
     seq_ctx[sid] = s.len - s.C;
@@ -471,14 +464,6 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
       kept = pass == 0 && a.batch <= kSoftmaxThreads && units <= kSoftmaxThreads;
       named_sync(kBarPair, kSoftmaxThreads);  // the sequence arrays are rewritten
     }
-    if (pass == 0 && misc->decrease < decrease) {
-      // Where the offsets decrease, later sequences' rows are counted twice: the
-      // line could pass 32 bits.  Once more without them.
-      decrease = misc->decrease;
-      loaded = pass = -1;
-      kept = false;
-      continue;
-    }
     if (pass == 0) {
       line->V = max(1, min(a.vctas, cum / max(1, a.min_range)));
       line->q = cum / line->V;
@@ -492,9 +477,10 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
     const size_t row_bytes = static_cast<size_t>(a.hq) * D * (a.out_fp32 ? 4 : 2);
 #pragma unroll 1
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-      if (!seq_info(a, b).bad && b <= misc->decrease) continue;
+      if (!seq_info(a, b).bad) continue;
       // (behind a decrease: only rows that no sound sequence has)
-      const long long n0 = max(a.token_offsets[b], b > misc->decrease ? a.token_offsets[misc->decrease] : INT_MIN);
+      const int end = __ldcg(a.counters + a.vctas);
+      const long long n0 = max(a.token_offsets[b], b > end ? a.token_offsets[end] : INT_MIN);
       const long long n1 = a.token_offsets[b + 1];
       if (n0 < 0 || n1 <= n0 || n1 > a.total_tokens) continue;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
@@ -728,13 +714,25 @@ __device__ void merge_groups(const ChunkArgs& a, const Piece& pc, int ur, int st
   }
 }
 
-// status and the ticket counters start at zero.  The attention kernel may
-// start while this one runs (programmatic dependent launch); it waits for its
-// end before it touches either.
-__global__ void chunk_init_kernel(int32_t* status, int batch, int32_t* counters, int n) {
+// status and the ticket counters start at zero; behind the counters stands the
+// first sequence whose chunk has a negative length.  (The rows of the sequences
+// after it would be counted twice, and the line of work could pass 32 bits: they
+// are malformed too.  Found here, because a few instructions more in the
+// schedule changed the E4M3 kernel's loops: its decode 88 -> 98 us.)  The
+// attention kernel may start while this one runs (programmatic dependent
+// launch); it waits for its end before it touches any of them.
+__global__ void chunk_init_kernel(const int32_t* token_offsets, int32_t* status, int batch, int32_t* counters, int n) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = threadIdx.x; i < batch; i += blockDim.x) status[i] = kOk;
+  __shared__ int decrease;
+  if (threadIdx.x == 0) decrease = INT_MAX;
+  __syncthreads();
+  for (int i = threadIdx.x; i < batch; i += blockDim.x) {
+    status[i] = kOk;
+    if (__ldg(token_offsets + i + 1) < __ldg(token_offsets + i)) atomicMin(&decrease, i);
+  }
   for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+  __syncthreads();
+  if (threadIdx.x == 0) counters[n] = decrease;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -774,7 +772,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
   if (tid == 0) {
     misc->abort = 0;
     misc->zero_needed = 0;
-    misc->decrease = INT_MAX;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 2);  // one arrival per m-tile
@@ -1469,7 +1466,7 @@ size_t chunk_slot_bytes(int head_dim) {
 }
 
 int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
-  chunk_init_kernel<<<1, 256, 0, stream>>>(a.status, a.batch, a.counters, a.total_tokens > 0 ? a.vctas : 0);
+  chunk_init_kernel<<<1, 256, 0, stream>>>(a.token_offsets, a.status, a.batch, a.counters, a.vctas);
   if (cudaGetLastError() != cudaSuccess) return -1;
   if (a.total_tokens == 0) return 0;
   if (a.fp8) return launch<128, true>(a, maps, stream);
