@@ -22,6 +22,10 @@
 // by latency for single tokens.  A row is taken by D / 8 lanes, 16 bytes of
 // bf16 and 8 codes each; the rows of a CTA are ordered (K or V, head, token), so
 // that neighbouring rows of a page are written together.
+//
+// Measured (8 KV heads, D = 128): the K/V of 4 x 8192 tokens to E4M3 51 us (3.9
+// TB/s; the same bytes moved without the arithmetic 34 us), of 16 tokens 4 us;
+// 4 x 32768 tokens read back to bf16 149 us (5.5 TB/s), 1001 tokens 4 us.
 #include <climits>
 
 #include "tv_device.cuh"
@@ -31,7 +35,8 @@ namespace tv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 32;   // tokens of a CTA
+constexpr int kMaxTile = 32;   // tokens of a CTA: one per lane of the warp that finds their sequences
+static_assert(kMaxTile == 32, "place_tokens: a lane per token");
 constexpr int kNoPage = 7;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -94,7 +94,7 @@ size_t attn_slot_bytes(int head_dim);
 // Costs on the chunk attention's line of work: of a key tile of a full unit,
 // and of a piece besides its tiles.
 constexpr int kChunkTileCost = 3;
-constexpr int kChunkPieceCost = 8;
+constexpr int kChunkPieceCost = 6;
 
 struct ChunkArgs {
   const int32_t* block_table; // [batch][max_blocks_per_seq]
