@@ -89,6 +89,21 @@ def test_against_fp64(nodes, vocab, hist, biases, masked):
     check(got, c)
 
 
+@pytest.mark.parametrize("vocab", [2047, 2049, 8192, 9001, 32000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_ids_all_over_the_vocabulary(vocab, in_place):
+    """Histories, paths and biases meet every part of a row, its ends included,
+    and one another."""
+    c = make([64, 1, 17], vocab, [500, 0, 90], vocab, biases=30, masked=True)
+    g = np.random.default_rng(vocab)
+    pool = np.concatenate([[0, 1, vocab - 1, vocab // 2, 511, 512, 1023, 1024, 2046], g.integers(0, vocab, 40)])
+    for k in ("draft_tokens", "history", "bias_ids"):
+        c[k] = g.choice(pool, c[k].shape).astype(np.int32)
+    got, st = call(c, in_place=in_place)
+    assert (st == 0).all()
+    check(got, c)
+
+
 @pytest.mark.parametrize("vocab", [1000, 1001])
 def test_bf16_logits_and_in_place(vocab):
     c = make([12, 30], vocab, [20, 50], 1, 4, True)
