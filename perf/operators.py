@@ -51,18 +51,18 @@ def listed():
     return [
         # one new token for each of 16 serving sequences: a plain decode step,
         # bound by one read of the cache
-        _attend("decode 16 x 512-4096", "attend", 16, 32, 8, 128, (511, 4095), (1, 1)),
+        _attend("decode, 16 x 512-4096", "attend", 16, 32, 8, 128, (511, 4095), (1, 1)),
         # four multimodal prompts prefilled from an empty cache, 28/4 heads
-        _attend("prompt 4 x 1600", "attend", 4, 28, 4, 128, (0, 0), (1600, 1600)),
+        _attend("prompt, 4 x 1600", "attend", 4, 28, 4, 128, (0, 0), (1600, 1600)),
         # a 2048-token chunk of a long prompt with 32768 tokens already cached
-        _attend("long 2048 over 32768", "attend", 1, 64, 8, 128, (32768, 32768), (2048, 2048)),
+        _attend("long, 2048 over 32768", "attend", 1, 64, 8, 128, (32768, 32768), (2048, 2048)),
         # prompts, chunks and single tokens in one batch, of odd lengths, under
         # a 1024-token window with 4 first tokens kept
-        _attend("mixed window 1024", "attend", 12, 32, 8, 128, (0, 5003), (1, 701), 1024, 4),
+        _attend("mixed, window 1024", "attend", 12, 32, 8, 128, (0, 5003), (1, 701), 1024, 4),
         # decode over long E4M3 caches: half the bytes of bf16
-        _attend("fp8 decode 4 x 32768", "attend_fp8", 4, 64, 8, 128, (32000, 32767), (1, 1)),
+        _attend("fp8 decode, 4 x 32768", "attend_fp8", 4, 64, 8, 128, (32000, 32767), (1, 1)),
         # chunks of prompts over E4M3 caches of odd lengths
-        _attend("fp8 chunks 8 x 513", "attend_fp8", 8, 32, 8, 128, (512, 3999), (65, 513)),
+        _attend("fp8 chunks, 8 x 513", "attend_fp8", 8, 32, 8, 128, (512, 3999), (65, 513)),
         # the K/V of one decode step written into the E4M3 cache: latency
         _move("append 16 tokens", "append", "e4m3", 16, 8, 128, (511, 4095), (1, 1)),
         # the K/V of whole prompts written into the E4M3 cache: bandwidth
@@ -72,9 +72,9 @@ def listed():
         # the caches of four long sequences read back
         _move("read 4 x 32768", "read", "e4m3", 4, 8, 128, (0, 0), (32768, 32768)),
         # the target rows of one serving verification step, bf16 from the head
-        _penalize("16 trees V 32000", 16, (26, 64), 5, 32000, (512, 4096), 16, True, "bf16"),
+        _penalize("16 trees, V 32000", 16, (26, 64), 5, 32000, (512, 4096), 16, True, "bf16"),
         # the multimodal step's rows, fp32, with a grammar mask for every node
-        _penalize("4 trees V 151936", 4, (128, 128), 8, 151936, (1600, 1600), 300, True, "fp32"),
+        _penalize("4 trees, V 151936", 4, (128, 128), 8, 151936, (1600, 1600), 300, True, "fp32"),
     ]
 
 
