@@ -150,7 +150,7 @@ __device__ void place_tokens(const CacheArgs& a, Tile& tl, int t0, int n) {
   for (int i = tid; i < a.batch; i += kThreads) {
     const int o = __ldg(a.token_offsets + i), next = __ldg(a.token_offsets + i + 1);
     if (o < 0 || next < o || next > a.total_tokens) tl.bad_offsets = 1;
-    if (o < t0 + n) atomicAdd(&tl.hist[max(0, o - t0)], 1);
+    if (o < t0 + n) atomicAdd(&tl.hist[max(o, t0) - t0], 1);  // (o - t0 of a malformed o may wrap)
   }
   __syncthreads();
   const bool bad = tl.bad_offsets != 0;
