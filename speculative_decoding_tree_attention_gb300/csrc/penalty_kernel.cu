@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     if (!any) continue;
     // the path's tokens: the node nearest to the row computes a token.  An
     // allowed one still holds its logit in place, a masked one stays -inf.
+    __syncwarp();  // other lanes stored the copies that are rewritten (and, in place, read) here
     int j = i;
     for (int k = 0; k < lane && j > 0; ++k) j = s.parent[j];
     while (__any_sync(0xffffffffu, j > 0)) {
