@@ -607,7 +607,9 @@ int tv_commit_kv_fp8(const tv_commit_params* params, const uint8_t* k_nodes,
  * outside [0, V), in the history, the bias list or the tree, count for nothing.
  * A sequence with a malformed tree, history or bias extent, or a rate that is
  * not finite (a repetition not positive), gets TV_ERR_BAD_TREE and its rows
- * unchanged (as far as they can be addressed).
+ * unchanged (as far as they can be addressed).  So do all sequences after one
+ * whose node_offsets decrease: of their rows, those that an earlier sequence has
+ * are that sequence's.
  * ====================================================================== */
 typedef struct {
   int32_t batch;         /* 1 <= B <= 65535                                */

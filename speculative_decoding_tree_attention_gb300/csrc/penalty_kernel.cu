@@ -58,6 +58,7 @@ struct Shared {
   int token[kMaxNodes];
   int16_t parent[kMaxNodes];
   int bad;
+  int decrease;                        // the first tree with fewer than 0 nodes (this one: none before it)
 };
 static_assert(sizeof(Shared) <= 45 * 1024, "no opt-in, and no fewer CTAs an SM than the registers allow");
 
@@ -99,9 +100,11 @@ struct Raw4<false> {
   __device__ __forceinline__ float4 value() const { return w; }
 };
 
-// BF16: the logits' type (else fp32).  VEC: rows are 4-entry aligned.
+// BF16: the logits' type (else fp32).  VEC: rows are 4-entry aligned.  Three CTAs
+// an SM (single bf16 entries: two): left to itself the compiler took 64 registers
+// and spilled, the second case above 114 us instead of 107.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) {
+__global__ void __launch_bounds__(kThreads, BF16 && !VEC ? 2 : 3) penalty_kernel(const PenaltyArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
   const int c0 = blockIdx.x * kChunk, b = blockIdx.y;
@@ -123,7 +126,10 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   r.rep = a.repetition ? __ldg(a.repetition + b) : 1.0f;
   r.pres = a.presence ? __ldg(a.presence + b) : 0.0f;
   r.freq = a.frequency ? __ldg(a.frequency + b) : 0.0f;
-  if (tid == 0) s.bad = 0;
+  if (tid == 0) {
+    s.bad = 0;
+    s.decrease = b;
+  }
   const bool rows_ok = nodes >= 1 && n0 >= 0 && n0 + nodes <= a.total_nodes;
   const int N = rows_ok ? static_cast<int>(nodes) : 0;
   bool bad = !rows_ok || N > a.max_nodes || h0 < 0 || h1 < h0 || h1 > a.total_history || e0 < 0 || e1 < e0 ||
@@ -137,6 +143,16 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   }
   if (tid < kWarps * (kChunk / 32) / 4) *reinterpret_cast<uint4*>(&s.path[0][0] + 4 * tid) = zero;
   __syncthreads();
+  // trees behind a decreasing offset may have rows of the trees before it: they
+  // are malformed.  (16 and 4 trees: no time; 4096 trees of one node, V = 32000:
+  // 772 -> 829 us; the loads of 8 steps in flight, 4 offsets a load took as long)
+  bool dec = false;
+#pragma unroll 8
+  for (int i = tid; i < b; i += kThreads) dec |= __ldg(a.node_offsets + i + 1) < __ldg(a.node_offsets + i);
+  if (dec) {
+    for (int i = tid; i < b; i += kThreads)
+      if (__ldg(a.node_offsets + i + 1) < __ldg(a.node_offsets + i)) atomicMin(&s.decrease, i);
+  }
   if (!bad) {
     for (int i = tid; i < N; i += kThreads) {
       const int p = __ldg(a.parent + n0 + i);
@@ -167,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
     }
   }
   __syncthreads();
-  bad = bad || s.bad;
+  bad = bad || s.bad || s.decrease < b;
   if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) a.status[b] = bad ? kBadTree : kOk;
   if (!rows_ok) return;
   const bool has_bias = a.bias_ids != nullptr;
@@ -213,7 +229,13 @@ __global__ void __launch_bounds__(kThreads) penalty_kernel(const PenaltyArgs a) 
   const int words = (a.vocab + 31) / 32;
   uint32_t* path = s.path[warp];
   float* block = s.block[warp];
-  for (int i = blockIdx.z * kWarps + warp; i < N; i += gridDim.z * kWarps) {
+  // (behind a decrease: only rows that no sound tree has)
+  int row0 = blockIdx.z * kWarps + warp;
+  if (s.decrease < b) {
+    const int skip = min(max(__ldg(a.node_offsets + s.decrease), n0) - n0, N), step = gridDim.z * kWarps;
+    if (skip > row0) row0 += (skip - row0 + step - 1) / step * step;
+  }
+  for (int i = row0; i < N; i += gridDim.z * kWarps) {
     const size_t row = static_cast<size_t>(n0 + i);
     const void* in = static_cast<const uint8_t*>(a.logits) + row * a.vocab * (BF16 ? 2 : 4);
     float* out = a.out + row * a.vocab;

@@ -49,3 +49,58 @@ def test_cache_lengths_at_the_ends_of_32_bits(length):
     st = tv.append_kv(x, x, i32(np.arange(8).reshape(2, 4)), i32([length, 20]), i32([0, 20, 40]), pool, pool.clone())
     assert st.tolist() == [7 if length == HIGH else BAD_TREE, 0]
     assert (pool[:4] == 0).all() and torch.equal(pool[4, 0], x[20:36, 0])
+
+
+# ------------------------------------------------------------------ penalties
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_penalties_behind_decreasing_offsets(in_place, dtype):
+    """Trees behind a negative one are malformed; rows that they share with a
+    sound tree are penalised once, by that tree, and the others stay."""
+    if in_place and dtype is torch.bfloat16:
+        return
+    ensure_built()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.randn(20, 5000, device="cuda", generator=g) * 3).to(dtype)
+    history = torch.randint(0, 5000, (400,), device="cuda", generator=g, dtype=torch.int32)
+    tokens = torch.randint(0, 5000, (20,), device="cuda", generator=g, dtype=torch.int32)
+    parent = i32([-1] + list(range(9)) + [-1] + list(range(9)))
+    kw = dict(max_nodes=20, history=history, repetition=torch.tensor([1.5, 1.2, 3.0, 0.5, 2.0], device="cuda"))
+    # rows of (first sound trees, then the decrease): 0..9 | 10..4 | 5..14, 15..17, 18..19
+    for off, first in (([0, 10, 5, 15, 18, 20], 10), ([0, 10, LOW, 3, 12, 20], 10), ([0, 10, 9, 10, 15, 15], 10)):
+        kw["history_offsets"] = i32([0, 80, 160, 240, 320, 400])
+        par = parent.clone()
+        one, st = tv.penalize_logits(x, tokens, par, i32([0, 10]), max_nodes=20, history=history,
+                                     history_offsets=i32([0, 80]), repetition=kw["repetition"][:1])
+        assert st.tolist() == [0]
+        buf = x.clone()
+        out = buf if in_place else torch.full((20, 5000), 7.0, device="cuda")
+        got, st = tv.penalize_logits(buf, tokens, par, i32(off), out=out, **kw)
+        assert st.tolist() == [0] + [BAD_TREE] * 4, off
+        assert torch.equal(got[:first], one[:first])
+        kept = x.float()[first:]
+        # rows of a malformed tree hold their logits, rows of none what they held
+        last = max(off[2:])
+        assert torch.equal(got[first:last], kept[:last - first])
+        assert in_place or (got[last:] == 7.0).all()
+        if off[-1] == 20 and off[1] == 10 and off[2] == 5:
+            assert last == 20
+
+
+def test_penalties_of_many_trees():
+    """More trees than a block has threads, and a decrease far down the batch."""
+    ensure_built()
+    B = 1500
+    x = torch.randn(B, 40, device="cuda")
+    tokens, parent = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    kw = dict(max_nodes=1, history=torch.arange(B, dtype=torch.int32, device="cuda") % 40,
+              history_offsets=i32(np.arange(B + 1)), presence=torch.ones(B, device="cuda"))
+    want, st = tv.penalize_logits(x, tokens, parent, i32(np.arange(B + 1)), **kw)
+    hit = torch.zeros(B, 40, device="cuda")
+    hit[torch.arange(B), torch.arange(B) % 40] = 1.0
+    assert (st == 0).all() and torch.equal(want, x - hit)
+    off = np.arange(B + 1)
+    off[1301:] -= 2  # tree 1300 has -1 nodes; the trees behind it share rows 1299 and on
+    got, st = tv.penalize_logits(x, tokens, parent, i32(off), out=torch.full_like(x, 9.0), **kw)
+    assert (st[:1300] == 0).all() and (st[1300:] == BAD_TREE).all()
+    assert torch.equal(got[:1300], want[:1300]) and torch.equal(got[1300:B - 2], x[1300:B - 2]) and (got[B - 2:] == 9.0).all()
