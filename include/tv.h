@@ -626,7 +626,8 @@ typedef struct {
  * history_offsets int32 [batch+1], or both NULL; prompt_lens int32 [batch] or
  * NULL (0: all history is generated); repetition, presence, frequency fp32
  * [batch] or NULL (1, 0, 0); bias_ids int32 and bias_values fp32 [total_bias]
- * with bias_offsets int32 [batch+1], or NULL; allowed_mask uint32
+ * with bias_offsets int32 [batch+1], or NULL (a list without entries may be NULL
+ * with its offsets given: they are checked); allowed_mask uint32
  * [total_nodes][ceil(V/32)] or NULL; out fp32 [total_nodes][V], which may be
  * the fp32 logits themselves (in place) and otherwise does not overlap them;
  * status int32 [batch].  Device pointers 16-byte aligned. */

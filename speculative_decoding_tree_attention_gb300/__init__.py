@@ -913,10 +913,9 @@ def penalize_logits(logits, draft_tokens, parent, node_offsets, *, max_nodes: in
         p = _ptr_or_null
         rc = lib.tv_penalize_logits(
             C.byref(prm), p(logits), p(draft_tokens), p(parent), p(node_offsets),
-            # (an empty list has no address: none at all)
-            *((p(history), history_offsets.data_ptr()) if n_hist else (None, None)),
+            p(history), p(history_offsets),  # (an empty list has no address)
             p(prompt_lens), p(repetition), p(presence), p(frequency),
-            *((p(bias_ids), p(bias_values), bias_offsets.data_ptr()) if n_bias else (None, None, None)),
+            p(bias_ids), p(bias_values), p(bias_offsets),
             p(allowed_mask), p(o), p(st), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_penalize_logits")

@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kThreads, BF16 && !VEC ? 2 : 3) penalty_kernel
   const int n0 = __ldg(a.node_offsets + b);
   const long long nodes = static_cast<long long>(__ldg(a.node_offsets + b + 1)) - n0;
   int h0 = 0, h1 = 0;
-  if (a.history) {
+  if (a.history_offsets) {  // (of an empty list too)
     h0 = __ldg(a.history_offsets + b);
     h1 = __ldg(a.history_offsets + b + 1);
   }
   int e0 = 0, e1 = 0;
-  if (a.bias_ids) {
+  if (a.bias_offsets) {
     e0 = __ldg(a.bias_offsets + b);
     e1 = __ldg(a.bias_offsets + b + 1);
   }

@@ -815,15 +815,16 @@ int tv_penalize_logits(const tv_penalty_params* p, const void* logits,
   a.tokens = draft_tokens;
   a.parent = parent;
   a.node_offsets = node_offsets;
+  // an empty list may have no address, but its extents are checked
   a.history = history;
-  a.history_offsets = history_offsets;
+  a.history_offsets = history || p->total_history == 0 ? history_offsets : nullptr;
   a.prompt_lens = prompt_lens;
   a.repetition = repetition;
   a.presence = presence;
   a.frequency = frequency;
   a.bias_ids = bias_ids;
   a.bias_values = bias_values;
-  a.bias_offsets = bias_offsets;
+  a.bias_offsets = bias_ids || p->total_bias == 0 ? bias_offsets : nullptr;
   a.allowed_mask = allowed_mask;
   a.status = status;
   a.batch = p->batch;

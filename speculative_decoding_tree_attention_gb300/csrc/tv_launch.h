@@ -187,7 +187,7 @@ struct PenaltyArgs {
   const int32_t* parent;      // [total_nodes]
   const int32_t* node_offsets;// [batch+1]
   const int32_t* history;     // [total_history] or null
-  const int32_t* history_offsets; // [batch+1]
+  const int32_t* history_offsets; // [batch+1]; null: no history (as bias_offsets)
   const int32_t* prompt_lens; // [batch] or null
   const float* repetition;    // [batch] or null
   const float* presence;

@@ -104,3 +104,23 @@ def test_penalties_of_many_trees():
     got, st = tv.penalize_logits(x, tokens, parent, i32(off), out=torch.full_like(x, 9.0), **kw)
     assert (st[:1300] == 0).all() and (st[1300:] == BAD_TREE).all()
     assert torch.equal(got[:1300], want[:1300]) and torch.equal(got[1300:B - 2], x[1300:B - 2]) and (got[B - 2:] == 9.0).all()
+
+
+@pytest.mark.parametrize("off, bad", [([0, 0, 0], []), ([0, 5, 5], [0, 1]), ([0, 0, 1], [1]), ([-1, 0, 0], [0]),
+                                      ([2, 1, 1], [0, 1]), ([1, 1, 1], [0, 1])])
+@pytest.mark.parametrize("what", ["history", "bias"])
+def test_penalty_extents_of_an_empty_list(off, bad, what):
+    """A list without entries has extents too: one outside [0, 0] is malformed."""
+    ensure_built()
+    x = torch.randn(4, 100, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    kw = dict(history=none, history_offsets=i32(off)) if what == "history" else \
+        dict(bias_ids=none, bias_values=none.float(), bias_offsets=i32(off))
+    got, st = tv.penalize_logits(x, i32([3, 7, 3, 9]), i32([-1, 0, -1, 0]), i32([0, 2, 4]), max_nodes=2,
+                                 presence=torch.ones(2, device="cuda"), **kw)
+    assert st.tolist() == [BAD_TREE if b in bad else 0 for b in range(2)]
+    want = x.clone()
+    for b, (row, token) in enumerate(((1, 7), (3, 9))):
+        if b not in bad:
+            want[row, token] -= 1.0
+    assert torch.equal(got, want)
