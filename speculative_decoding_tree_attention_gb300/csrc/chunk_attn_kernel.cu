@@ -904,6 +904,13 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           const int page = good ? page_id * a.hkv + kvh : a.num_blocks * a.hkv;  // out of bounds: zero fill
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, abort_flag));
           if (!ok) break;
+          // malformed block id: zeros, reported.  (Ahead of the arrival, which
+          // carries it to the softmax that reads it.)
+          if (!is_v && !good && page_id != kUnseen) {
+            piece_bad[p] = 1;
+            record_status(a.status, pc.b, kBadTree);
+          }
+          __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&full[st], Ly::kKTileBytes);
           __syncwarp();
           if (lane < kPages) {
@@ -924,10 +931,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             const size_t idx = from >= 0 ? static_cast<size_t>(from) * 16 + (lane & 3) * 4 : 0;
             cpa16_zfill(scl_ring + (is_v ? st : tau % kSclSlots) * BN + 4 * lane, scales + idx, from >= 0 ? 16 : 0);
             cpa_arrive_noinc(is_v ? &vfull[st] : &sfull[tau % kSclSlots]);
-          }
-          if (!is_v && !good && page_id != kUnseen) {  // malformed block id: zeros, reported
-            piece_bad[p] = 1;
-            record_status(a.status, pc.b, kBadTree);
           }
           ++tau;
           if (++st == stages) {

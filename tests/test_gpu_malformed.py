@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import speculative_decoding_tree_attention_gb300 as tv
+from test_gpu_chunk import call, call_fp8, make, quantised
 from tv_testlib import ensure_built
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +125,23 @@ def test_penalty_extents_of_an_empty_list(off, bad, what):
         if b not in bad:
             want[row, token] -= 1.0
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ chunk attention
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [0, 3, 1000, -1])
+def test_chunk_bad_page_of_a_split_unit(fp8, page):
+    """A decode token's cache is shared out over many CTAs; one of them meets the
+    bad page and all of the sequence's rows are zeros, each time."""
+    c = make([16411, 700, 5], [1, 1, 1], 8, 2, 128, seed=4)
+    run = call_fp8 if fp8 else call
+    c = quantised(c) if fp8 else c
+    good, st = run(c)
+    assert (st == 0).all()
+    bad = dict(c, table=c["table"].copy())
+    bad["table"][0, page if page >= 0 else (16411 - 1) // 16] = c["k"].shape[0]
+    for _ in range(10):
+        got, st = run(bad)
+        assert st.tolist() == [BAD_TREE, 0, 0]
+        assert (got[0] == 0).all()
+        np.testing.assert_array_equal(got[1:], good[1:])
