@@ -727,7 +727,10 @@ __device__ void merge_groups(const ChunkArgs& a, const Piece& pc, int ur, int st
 // schedule changed the E4M3 kernel's loops: its decode 88 -> 98 us.)  The
 // attention kernel may start while this one runs (programmatic dependent
 // launch); it waits for its end before it touches any of them.
-__global__ void chunk_init_kernel(const int32_t* token_offsets, int32_t* status, int batch, int32_t* counters, int n) {
+// Without any rows (`empty`) it is the only one, and a sequence that has some is
+// malformed.
+__global__ void chunk_init_kernel(const int32_t* token_offsets, int32_t* status, int batch, int32_t* counters, int n,
+                                  bool empty) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int decrease;
   if (threadIdx.x == 0) decrease = INT_MAX;
@@ -739,6 +742,10 @@ __global__ void chunk_init_kernel(const int32_t* token_offsets, int32_t* status,
   for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
   __syncthreads();
   if (threadIdx.x == 0) counters[n] = decrease;
+  if (empty) {
+    for (int i = threadIdx.x; i < batch; i += blockDim.x)
+      if (i > decrease || __ldg(token_offsets + i + 1) != __ldg(token_offsets + i)) status[i] = kBadTree;
+  }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -1475,7 +1482,8 @@ size_t chunk_slot_bytes(int head_dim) {
 }
 
 int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
-  chunk_init_kernel<<<1, 256, 0, stream>>>(a.token_offsets, a.status, a.batch, a.counters, a.vctas);
+  chunk_init_kernel<<<1, 256, 0, stream>>>(a.token_offsets, a.status, a.batch, a.counters, a.vctas,
+                                           a.total_tokens == 0);
   if (cudaGetLastError() != cudaSuccess) return -1;
   if (a.total_tokens == 0) return 0;
   if (a.fp8) return launch<128, true>(a, maps, stream);

@@ -145,3 +145,20 @@ def test_chunk_bad_page_of_a_split_unit(fp8, page):
         assert st.tolist() == [BAD_TREE, 0, 0]
         assert (got[0] == 0).all()
         np.testing.assert_array_equal(got[1:], good[1:])
+@pytest.mark.parametrize("off, want", [([0, 0, 0, 0], [0, 0, 0]), ([0, 5, 5, 5], [5, 0, 0]), ([0, 0, 1, 2], [0, 5, 5]),
+                                       ([0, 0, -1, -1], [0, 5, 5]), ([3, 3, 3, 3], [0, 0, 0]), ([LOW, HIGH, HIGH, 0], [5, 0, 5])])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_offsets_without_rows(off, want, fp8):
+    """Without rows every sequence that has some, or lies behind a decrease, is malformed."""
+    ensure_built()
+    lens, table = i32([30, 40, 50]), i32(np.arange(12).reshape(3, 4))
+    elem = torch.uint8 if fp8 else torch.bfloat16
+    pool = torch.zeros(12, 2, 16, 128, dtype=elem, device="cuda")
+    q = torch.empty(0, 4, 128, dtype=elem, device="cuda")
+    if fp8:
+        scale = torch.ones(12, 2, 16, device="cuda")
+        out, st = tv.chunk_attention_fp8(q, torch.empty(0, 4, device="cuda"), pool, scale, pool, scale, table, lens,
+                                         i32(off), max_len=50)
+    else:
+        out, st = tv.chunk_attention(q, pool, pool, table, lens, i32(off), max_len=50)
+    assert st.tolist() == want and out.shape == (0, 4, 128)
