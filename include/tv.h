@@ -448,8 +448,10 @@ int tv_commit_kv(const tv_commit_params* params, const uint16_t* k_nodes,
  *     token_offsets[batch] are left as they were.
  *   - A sequence with a malformed extent (C_b < 0, C_b > seq_lens[b], rows past
  *     total_tokens, seq_lens[b] > max_len) or a bad block id of a page that it
- *     sees gets status TV_ERR_BAD_TREE and all-zero rows.  So do all sequences
- *     after one with C_b < 0 (their rows would be counted twice).
+ *     sees gets status TV_ERR_BAD_TREE and all-zero rows (those of [0,
+ *     total_tokens)).  So do all sequences after one with C_b < 0 (their rows
+ *     would be counted twice): of their rows, those that an earlier sequence has
+ *     are that sequence's.
  * Inputs bf16, accumulation and softmax fp32, output bf16 or fp32; P is rounded
  * to bf16 for the P V product, so the fp32 output carries that rounding.
  * Repeated calls agree bit for bit.

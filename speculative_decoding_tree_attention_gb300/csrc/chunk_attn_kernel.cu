@@ -486,9 +486,9 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
       if (!seq_info(a, b).bad) continue;
       // (behind a decrease: only rows that no sound sequence has)
       const int end = __ldcg(a.counters + a.vctas);
-      const long long n0 = max(a.token_offsets[b], b > end ? a.token_offsets[end] : INT_MIN);
-      const long long n1 = a.token_offsets[b + 1];
-      if (n0 < 0 || n1 <= n0 || n1 > a.total_tokens) continue;
+      const long long n0 = max(0, max(a.token_offsets[b], b > end ? a.token_offsets[end] : 0));
+      const long long n1 = min(a.token_offsets[b + 1], a.total_tokens);
+      if (n1 <= n0) continue;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
 #pragma unroll 1
       for (size_t k = sid; k < (n1 - n0) * row_bytes / 16; k += kSoftmaxThreads) dst[k] = make_uint4(0, 0, 0, 0);

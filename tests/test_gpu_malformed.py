@@ -162,3 +162,27 @@ def test_chunk_offsets_without_rows(off, want, fp8):
     else:
         out, st = tv.chunk_attention(q, pool, pool, table, lens, i32(off), max_len=50)
     assert st.tolist() == want and out.shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("out_dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("off, bad, zero", [
+    ([0, 8, 58, 59, 62, 200], [4], (62, 82)),         # rows past the end: those that are there
+    ([0, 8, 58, 59, 62, HIGH], [4], (62, 82)),
+    ([-5, 8, 58, 59, 62, 82], [0], (0, 8)),           # rows before the first
+    ([LOW, 8, 58, 59, 62, 82], [0], (0, 8)),
+    ([0, 8, 58, 59, 90, 95], [3, 4], (59, 82)),       # one past the end, one wholly behind it
+    ([0, 90, 58, 59, 62, 82], [0, 1, 2, 3, 4], (0, 82)),  # past the end, and a decrease behind it
+    ([0, 8, 58, LOW, 62, 80], [2, 3, 4], (58, 80)),   # a decrease: only rows that no sound sequence has
+])
+def test_chunk_rows_outside_the_output(off, bad, zero, out_dtype):
+    """Of a malformed sequence every row that is there and is no sound
+    sequence's reads as zeros, and no other row changes."""
+    c = make([40, 50, 60, 33, 20], [8, 50, 1, 3, 20], 8, 2, 128, seed=1)
+    good, _ = call(c, out_dtype=out_dtype)
+    got, st = call(dict(c, off=np.asarray(off, np.int32)), max_len=60, fill=5.0, out_dtype=out_dtype)
+    assert st.tolist() == [BAD_TREE if b in bad else 0 for b in range(5)]
+    want = np.full_like(good, 5.0)
+    for b in set(range(5)) - set(bad):
+        want[off[b]:off[b + 1]] = good[off[b]:off[b + 1]]
+    want[zero[0]:zero[1]] = 0.0
+    np.testing.assert_array_equal(got, want)
