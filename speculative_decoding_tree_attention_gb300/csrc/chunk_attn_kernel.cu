@@ -94,6 +94,7 @@ struct Shares {
 // 2^8 and the row sum below 2^8 x keys, well inside fp32 (and fp16 for P)
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxPieces = 16;        // pieces per scheduling round
+constexpr int kCheckThreads = 256;    // of the kernel that checks the sequences
 constexpr int kSclSlots = 8;          // E4M3: scale slots (tile tau in slot tau % 8)
 
 // cost of a key tile of a unit with one and with two m-tiles, and of a piece
@@ -156,7 +157,7 @@ struct Layout {
   // turn [2], q_full, q_empty, hand [2], v16full, v16empty [2], sfull [8]
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 16 + (F8 ? 4 + kSclSlots : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kMiscBytes = 96;
+  static constexpr int kMiscBytes = 32;
   static constexpr int kTotal = kMisc + kMiscBytes;
   static constexpr int kAlloc = kTotal + 1024;  // slack for 1024-byte alignment
   // the schedule's scratch (a chunk of 256 sequences) lies over Q, which is
@@ -173,8 +174,6 @@ struct Misc {
   int npieces;                // pieces of this round
   int more;                   // another round follows
   int merge;                  // this CTA merges the current split unit
-  int zero_needed;            // a malformed sequence's rows are zeroed by this CTA
-  int piece_bad[kMaxPieces];  // a block id of the piece was out of range
 };
 static_assert(sizeof(Misc) <= Layout<128, true>::kMiscBytes, "Misc fits its area");
 
@@ -277,17 +276,15 @@ __device__ __forceinline__ Unit unit_of(const ChunkArgs& a, int ctx, int C, int 
 
 struct SeqInfo {
   int n0, C, len;
-  int units;        // per KV head; 0 for an empty chunk or a malformed one
-  int bad;          // the extent is malformed
+  int units;        // per KV head; 0 for an empty chunk or a malformed sequence
 };
 
 __device__ __forceinline__ SeqInfo seq_info(const ChunkArgs& a, int b) {
   SeqInfo s;
   s.n0 = __ldg(a.token_offsets + b);
-  const long long c = static_cast<long long>(__ldg(a.token_offsets + b + 1)) - s.n0;
   s.len = __ldg(a.seq_lens + b);
-  s.bad = c < 0 || b > __ldcg(a.counters + a.vctas) || (c > 0 && (s.n0 < 0 || s.n0 + c > a.total_tokens || s.len < c || s.len > a.max_len));
-  s.C = s.bad ? 0 : static_cast<int>(c);
+  const bool bad = __ldcg(a.status + b) == kBadTree;
+  s.C = bad ? 0 : __ldg(a.token_offsets + b + 1) - s.n0;
   s.units = (s.C + a.unit_tokens - 1) / a.unit_tokens;
   return s;
 }
@@ -356,8 +353,7 @@ __device__ __forceinline__ int cut_at(int x, int T, int w) {
 // Builds this CTA's pieces of scheduling round `round` into shared memory
 // (the 256 softmax threads).  `line` is filled in round 0.  Sequences are
 // taken 256 at a time, and the units of such a chunk 256 at a time, one per
-// thread: a unit is hkv consecutive runs of the line, one per KV head.  In
-// round 0 the rows of malformed sequences are zeroed and their status recorded.
+// thread: a unit is hkv consecutive runs of the line, one per KV head.
 template <int D, bool F8>
 __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int sid, Line* line) {
   using Ly = Layout<D, F8>;
@@ -375,12 +371,8 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
     if (loaded == base) return;
     const int b = base + sid;
     SeqInfo s;
-    s.units = s.n0 = s.C = s.len = s.bad = 0;
+    s.units = s.n0 = s.C = s.len = 0;
     if (b < a.batch) s = seq_info(a, b);
-    if (round == 0 && s.bad && b % gridDim.x == blockIdx.x) {
-      record_status(a.status, b, kBadTree);
-      misc->zero_needed = 1;
-    }
     seq_u[sid] = scan256(s.units, scratch, sid, &units);
     seq_n0[sid] = s.n0;
     seq_c[sid] = s.C;
@@ -478,27 +470,10 @@ __device__ void build_schedule(const ChunkArgs& a, uint8_t* smem, int round, int
       line->VW = cum > 0 ? static_cast<float>(line->V) / static_cast<float>(cum) : 0.0f;
     }
   }
-  if (round == 0 && misc->zero_needed) {
-    // the rows of a malformed sequence that can be addressed get zeros
-    const size_t row_bytes = static_cast<size_t>(a.hq) * D * (a.out_fp32 ? 4 : 2);
-#pragma unroll 1
-    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-      if (!seq_info(a, b).bad) continue;
-      // (behind a decrease: only rows that no sound sequence has)
-      const int end = __ldcg(a.counters + a.vctas);
-      const long long n0 = max(0, max(a.token_offsets[b], b > end ? a.token_offsets[end] : 0));
-      const long long n1 = min(a.token_offsets[b + 1], a.total_tokens);
-      if (n1 <= n0) continue;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + n0 * row_bytes);
-#pragma unroll 1
-      for (size_t k = sid; k < (n1 - n0) * row_bytes / 16; k += kSoftmaxThreads) dst[k] = make_uint4(0, 0, 0, 0);
-    }
-  }
   if (sid == 0) {
     const int n = count - round * kMaxPieces;
     misc->npieces = max(0, min(kMaxPieces, n));
     misc->more = n > kMaxPieces;
-    for (int k = 0; k < kMaxPieces; ++k) misc->piece_bad[k] = 0;
   }
   fence_proxy_async_smem();  // the scratch lies where TMA writes Q
 }
@@ -720,31 +695,50 @@ __device__ void merge_groups(const ChunkArgs& a, const Piece& pc, int ur, int st
   }
 }
 
-// status and the ticket counters start at zero; behind the counters stands the
-// first sequence whose chunk has a negative length.  (The rows of the sequences
-// after it would be counted twice, and the line of work could pass 32 bits: they
-// are malformed too.  Found here, because a few instructions more in the
-// schedule changed the E4M3 kernel's loops: its decode 88 -> 98 us.)  The
-// attention kernel may start while this one runs (programmatic dependent
-// launch); it waits for its end before it touches any of them.
-// Without any rows (`empty`) it is the only one, and a sequence that has some is
-// malformed.
-__global__ void chunk_init_kernel(const int32_t* token_offsets, int32_t* status, int batch, int32_t* counters, int n,
-                                  bool empty) {
+// Runs first: a CTA per sequence checks its extent and every page that some row
+// of it sees, writes its status and zeroes the rows of a malformed one, so that
+// the attention kernel meets sound sequences only.  The rows of sequences behind a
+// chunk of negative length would be counted twice, and the line of work could pass
+// 32 bits: they are malformed too, and rows that an earlier sequence has are not
+// theirs.  The attention kernel may start while this one runs (programmatic
+// dependent launch); it waits for its end before it reads a status.
+__global__ void __launch_bounds__(kCheckThreads) chunk_check_kernel(const __grid_constant__ ChunkArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int decrease;
-  if (threadIdx.x == 0) decrease = INT_MAX;
+  const int tid = threadIdx.x;
+  if (tid == 0) decrease = INT_MAX;
   __syncthreads();
-  for (int i = threadIdx.x; i < batch; i += blockDim.x) {
-    status[i] = kOk;
-    if (__ldg(token_offsets + i + 1) < __ldg(token_offsets + i)) atomicMin(&decrease, i);
-  }
-  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+  for (int i = tid; i < a.batch; i += kCheckThreads)
+    if (__ldg(a.token_offsets + i + 1) < __ldg(a.token_offsets + i)) atomicMin(&decrease, i);
+  if (blockIdx.x == 0)
+    for (int i = tid; i < a.vctas; i += kCheckThreads) a.counters[i] = 0;  // tickets
   __syncthreads();
-  if (threadIdx.x == 0) counters[n] = decrease;
-  if (empty) {
-    for (int i = threadIdx.x; i < batch; i += blockDim.x)
-      if (i > decrease || __ldg(token_offsets + i + 1) != __ldg(token_offsets + i)) status[i] = kBadTree;
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    const int n0 = __ldg(a.token_offsets + b), n1 = __ldg(a.token_offsets + b + 1), len = __ldg(a.seq_lens + b);
+    const long long c = static_cast<long long>(n1) - n0;
+    bool bad = c < 0 || b > decrease || (c > 0 && (n0 < 0 || n1 > a.total_tokens || len < c || len > a.max_len));
+    if (!bad && c > 0) {
+      // pages [0, s) of the sinks and [w, the last one]
+      const int ctx = len - static_cast<int>(c);
+      const int lo = extent_of(a, ctx).lo;  // (the first token's: no later row sees more)
+      const int w = lo / 16, s = min((a.sinks + 15) / 16, w);
+      const int pages = s + (len - 1) / 16 + 1 - w;
+      const int32_t* table = a.block_table + static_cast<size_t>(b) * a.max_blocks_per_seq;
+#pragma unroll 8
+      for (int i = tid; i < pages; i += kCheckThreads) {
+        const int blk = __ldg(table + (i < s ? i : i - s + w));
+        bad |= blk < 0 || blk >= a.num_blocks;
+      }
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) a.status[b] = bad ? kBadTree : kOk;
+    if (!bad) continue;
+    const size_t row_bytes = static_cast<size_t>(a.hq) * a.head_dim * (a.out_fp32 ? 4 : 2);
+    const long long r0 = max(0, max(n0, b > decrease ? __ldg(a.token_offsets + decrease) : 0));
+    const long long r1 = min(n1, a.total_tokens);
+    if (r1 <= r0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + r0 * row_bytes);
+    for (size_t k = tid; k < (r1 - r0) * row_bytes / 16; k += kCheckThreads) dst[k] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -784,7 +778,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
 
   if (tid == 0) {
     misc->abort = 0;
-    misc->zero_needed = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 2);  // one arrival per m-tile
@@ -867,7 +860,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       // (One warp polling for both took 3300 clocks a tile, more than an E4M3
       // tile has at the HBM rate.)
       constexpr int kPages = BN / 16;
-      constexpr int kUnseen = INT_MIN;  // no row of the unit sees the page -> zeros
+      constexpr int kUnseen = -1;  // no row of the unit sees the page -> zeros
       const bool is_v = warp == kVWarp;
       const int stages = is_v ? kVStages : kStages;
       uint64_t* full = is_v ? vfull : kfull;
@@ -876,7 +869,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       const CUtensorMap* map = is_v ? &maps.v_pool : &maps.k_pool;
       const float* scales = is_v ? a.v_scale : a.k_scale;
       float* scl_ring = reinterpret_cast<float*>(smem + (is_v ? Ly::kVScl : Ly::kScl));
-      volatile int* piece_bad = misc->piece_bad;
       bool ok = true;
       int tau = g_tile;
       int st = g_tile % stages, ph = (g_tile / stages) & 1;  // ring slot and phase of tile tau
@@ -911,13 +903,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           const int page = good ? page_id * a.hkv + kvh : a.num_blocks * a.hkv;  // out of bounds: zero fill
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, abort_flag));
           if (!ok) break;
-          // malformed block id: zeros, reported.  (Ahead of the arrival, which
-          // carries it to the softmax that reads it.)
-          if (!is_v && !good && page_id != kUnseen) {
-            piece_bad[p] = 1;
-            record_status(a.status, pc.b, kBadTree);
-          }
-          __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&full[st], Ly::kKTileBytes);
           __syncwarp();
           if (lane < kPages) {
@@ -1184,7 +1169,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tmem_s = tmem + h * BN + lane_off;
       const uint32_t tmem_o = tmem + 256 + h * D + lane_off;
-      volatile int* piece_bad = misc->piece_bad;
       bool ok = true;
       int tau = g_tile;  // global index of the piece's first tile
       for (int p = 0; p < npieces; ++p) {
@@ -1362,7 +1346,6 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             record_status(a.status, pc.b, kDeviceTimeout);
           }
         }
-        const bool bad = piece_bad[p] != 0;
         tc_fence_after();
         OwnO<D> own_o = {tmem_o, false, 1.0f, 0.0f};
         if (narrow) {
@@ -1393,7 +1376,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               float v[32];
               own_o.load(c0, v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = bad ? 0.0f : v[k] * inv_l;
+              for (int k = 0; k < 32; ++k) v[k] *= inv_l;
               store_rows32(a, quad, c0, v);
             }
           }
@@ -1405,7 +1388,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           const int nthr = narrow ? BM : kSoftmaxThreads;
           const int bar = narrow ? kBarGroup0 : kBarPair;
           const int step = nthr / rows;
-          const int flag = (bad || !done) ? 1 : 0;
+          const int flag = done ? 0 : 1;
           int* ticket = a.counters + pc.vfirst();
           if (ur == 0) misc->merge = step == 1 && *static_cast<volatile int*>(ticket) == pc.npieces() - 1;
           named_sync(bar, nthr);
@@ -1481,9 +1464,8 @@ size_t chunk_slot_bytes(int head_dim) {
   return head_dim == 64 ? Slot<64>::kBytes : Slot<128>::kBytes;
 }
 
-int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
-  chunk_init_kernel<<<1, 256, 0, stream>>>(a.token_offsets, a.status, a.batch, a.counters, a.vctas,
-                                           a.total_tokens == 0);
+int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, int sms, cudaStream_t stream) {
+  chunk_check_kernel<<<a.batch < sms ? a.batch : sms, kCheckThreads, 0, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return -1;
   if (a.total_tokens == 0) return 0;
   if (a.fp8) return launch<128, true>(a, maps, stream);

@@ -145,8 +145,7 @@ struct ChunkPlan {
 // Launch plan of the chunk attention for `sms` SMs: a unit is as many whole
 // tokens as give at most 256 packed rows; the CTAs share the line of work
 // (at most `wmax` by the host hints) in ranges of at least kMinRange.
-// Workspace: a ticket counter per CTA and one more word, then two partial-result
-// slots per CTA.
+// Workspace: a ticket counter per CTA, then two partial-result slots per CTA.
 bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
   if (!p || sms < 1) return false;
   if (p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1) return false;
@@ -173,7 +172,7 @@ bool plan_chunk(const tv_chunk_params* p, int sms, ChunkPlan* out) {
   if (wmax >= (1ll << 31)) return false;  // counted in 32 bits
   // at most 4096 CTAs: the range boundaries are fp32 products below 2^24
   pl.vctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms, wmax / kMinRange, 4096})));
-  pl.workspace = (static_cast<size_t>(pl.vctas + 1) * 4 + 255) / 256 * 256 +
+  pl.workspace = (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256 +
                  2 * static_cast<size_t>(pl.vctas) * tv::chunk_slot_bytes(p->head_dim);
   *out = pl;
   return true;
@@ -634,7 +633,7 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
   a.out = out;
   a.status = status;
   a.counters = static_cast<int32_t*>(workspace);
-  a.slots = static_cast<uint8_t*>(workspace) + (static_cast<size_t>(pl.vctas + 1) * 4 + 255) / 256 * 256;
+  a.slots = static_cast<uint8_t*>(workspace) + (static_cast<size_t>(pl.vctas) * 4 + 255) / 256 * 256;
   a.batch = p->batch;
   a.hq = p->num_q_heads;
   a.hkv = p->num_kv_heads;
@@ -657,7 +656,7 @@ int chunk_call(const tv_chunk_params* p, bool fp8, const void* q, const float* q
   a.q_scale = q_scale;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  return tv::launch_chunk_attention(a, maps, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+  return tv::launch_chunk_attention(a, maps, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }
 
 }  // namespace

@@ -102,8 +102,7 @@ struct ChunkArgs {
   const int32_t* token_offsets; // [batch+1]
   void* out;                  // [total_tokens][Hq][D], bf16 or fp32 (out_fp32)
   int32_t* status;            // [batch]
-  int32_t* counters;          // [vctas] ticket counters of split units (zeroed per call), then the
-                              // first sequence whose chunk has a negative length
+  int32_t* counters;          // [vctas] ticket counters of split units (zeroed per call)
   uint8_t* slots;             // [2 * vctas] partial-result slots of chunk_slot_bytes(D)
   int32_t q_tokens;           // tokens of a Q box: min(unit_tokens, total_tokens)
   int32_t batch, hq, hkv, group, head_dim;
@@ -126,7 +125,7 @@ struct ChunkMaps {
   CUtensorMap v_pool;
 };
 
-int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream);
+int launch_chunk_attention(const ChunkArgs& a, const ChunkMaps& maps, int sms, cudaStream_t stream);
 size_t chunk_slot_bytes(int head_dim);
 
 struct CommitArgs {

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import speculative_decoding_tree_attention_gb300 as tv
-from test_gpu_chunk import call, call_fp8, make, quantised
+from test_gpu_chunk import U_BF16, U_FP8, call, call_fp8, check, make, quantised
 from tv_testlib import ensure_built
 
 pytestmark = pytest.mark.gpu
@@ -128,6 +128,18 @@ def test_penalty_extents_of_an_empty_list(off, bad, what):
 
 
 # ------------------------------------------------------------------ chunk attention
+def check_all_but(got, good, c, zero, fp8, window, sinks):
+    """The rows of sequences `zero` are zeros.  The others are theirs: within the
+    tolerance, not bit for bit, because they are split otherwise where the work of
+    a sequence goes."""
+    got = got.copy()
+    for b in zero:
+        rows = slice(int(c["off"][b]), int(c["off"][b + 1]))
+        assert (got[rows] == 0).all(), b
+        got[rows] = good[rows]
+    check(got, c, U_FP8 if fp8 else U_BF16, window, sinks)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("page", [0, 3, 1000, -1])
 def test_chunk_bad_page_of_a_split_unit(fp8, page):
@@ -143,8 +155,9 @@ def test_chunk_bad_page_of_a_split_unit(fp8, page):
     for _ in range(10):
         got, st = run(bad)
         assert st.tolist() == [BAD_TREE, 0, 0]
-        assert (got[0] == 0).all()
-        np.testing.assert_array_equal(got[1:], good[1:])
+        check_all_but(got, good, c, [0], fp8, 0, 0)
+
+
 @pytest.mark.parametrize("off, want", [([0, 0, 0, 0], [0, 0, 0]), ([0, 5, 5, 5], [5, 0, 0]), ([0, 0, 1, 2], [0, 5, 5]),
                                        ([0, 0, -1, -1], [0, 5, 5]), ([3, 3, 3, 3], [0, 0, 0]), ([LOW, HIGH, HIGH, 0], [5, 0, 5])])
 @pytest.mark.parametrize("fp8", [False, True])
@@ -186,3 +199,76 @@ def test_chunk_rows_outside_the_output(off, bad, zero, out_dtype):
         want[off[b]:off[b + 1]] = good[off[b]:off[b + 1]]
     want[zero[0]:zero[1]] = 0.0
     np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window, sinks", [(0, 0), (200, 20)])
+@pytest.mark.parametrize("page", ["first", "middle", "last", "evicted"])
+def test_chunk_bad_page_zeroes_the_whole_sequence(fp8, window, sinks, page):
+    """A prompt of many units, of which some do not see the bad page: every row
+    of the sequence is zeros.  A page that no row sees may be anything."""
+    lens, chunks = [1203, 901, 40, 611], [1, 700, 40, 611]
+    c = make(lens, chunks, 8, 2, 128, seed=11)
+    run = call_fp8 if fp8 else call
+    c = quantised(c) if fp8 else c
+    kw = dict(window=window, sinks=sinks)
+    good, st = run(c, **kw)
+    assert (st == 0).all()
+    first = 901 - 700
+    at = {"first": 0, "middle": 500 // 16, "last": 900 // 16, "evicted": sinks // 16 + 1}[page]
+    if page == "evicted" and not window:
+        return
+    for value in (-1, c["k"].shape[0], LOW, HIGH):
+        bad = dict(c, table=c["table"].copy())
+        bad["table"][1, at] = value
+        got, st = run(bad, **kw)
+        seen = not window or at * 16 < sinks or at * 16 + 15 > first - window
+        assert st.tolist() == [0, BAD_TREE if seen else 0, 0, 0]
+        check_all_but(got, good, c, [1] if seen else [], fp8, window, sinks)
+        again, _ = run(bad, **kw)
+        np.testing.assert_array_equal(got, again)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_every_page_is_looked_at(fp8):
+    """Windows, sinks and chunks of many sizes: the status and the rows follow
+    from the pages that some row of the sequence sees."""
+    g = np.random.default_rng(3)
+    run = call_fp8 if fp8 else call
+    for rep in range(12):
+        chunks = [int(x) for x in g.integers(1, 400, 4)]
+        lens = [x + int(g.integers(0, 600)) for x in chunks]
+        window, sinks = int(g.choice([0, 1, 16, 100, 500])), int(g.choice([0, 1, 16, 40]))
+        c = make(lens, chunks, 4, 2, 128, seed=100 + rep)
+        c = quantised(c) if fp8 else c
+        good, _ = run(c, window=window, sinks=sinks)
+        bad, status = dict(c, table=c["table"].copy()), []
+        for b in range(4):
+            at = int(g.integers(0, -(-lens[b] // 16)))
+            bad["table"][b, at] = int(g.choice([-1, c["k"].shape[0], HIGH, LOW]))
+            keys = np.arange(lens[b])
+            seen = keys > lens[b] - chunks[b] - window if window else keys >= 0
+            seen |= keys < sinks
+            status.append(BAD_TREE if seen[at * 16:at * 16 + 16].any() else 0)
+        got, st = run(bad, window=window, sinks=sinks)
+        assert st.tolist() == status
+        check_all_but(got, good, c, [b for b in range(4) if status[b]], fp8, window, sinks)
+
+
+def test_chunk_pages_of_many_sequences():
+    """More sequences than a launch of the check has CTAs, long tables, and a bad
+    page here and there."""
+    g = np.random.default_rng(8)
+    B = 700
+    lens = [int(x) for x in g.integers(1, 40, B)]
+    lens[5], lens[650] = 5003, 9001
+    c = make(lens, [1] * B, 2, 1, 64, seed=1)
+    good, st = call(c)
+    assert (st == 0).all()
+    hit = [0, 5, 151, 152, 304, 650, 699]
+    bad = dict(c, table=c["table"].copy())
+    for b in hit:
+        bad["table"][b, (lens[b] - 1) // 16] = -1
+    got, st = call(bad)
+    assert np.flatnonzero(st).tolist() == hit and (st[hit] == BAD_TREE).all()
+    check_all_but(got, good, c, hit, False, 0, 0)
