@@ -494,8 +494,8 @@ int tv_chunk_attention(const tv_chunk_params* params, const uint16_t* q, const u
                        cudaStream_t stream);
 
 /* The same over an E4M3 cache (tv_append_kv_fp8), in the formats of
- * tv_tree_attention_fp8; S on the tensor cores over the codes, each V row in
- * fp16 (its scale and the product code x scale rounded once each), P in fp16:
+ * tv_tree_attention_fp8 and with its values: S on the tensor cores over the
+ * codes, V as the fp32 product code x scale rounded to fp16, P in fp16:
  * q u8 codes [total_tokens][Hq][128] with
  * q_scale fp32 [total_tokens][Hq] (tv_quantize_rows), pools u8 [num_blocks]
  * [Hkv][16][128] with scales fp32 [num_blocks][Hkv][16].  Scales are positive;

@@ -61,8 +61,10 @@
 //
 // Precision.  S, the softmax and O are fp32.  P is rounded to the 16-bit type
 // of V for the P V product (bf16; fp16 for an E4M3 cache) and the row sum adds
-// the rounded values, so that O / l weights V exactly as the product did.  An
-// E4M3 V row is rounded twice on its way to fp16 (its scale, the product).
+// the rounded values, so that O / l weights V exactly as the product did.  V of
+// an E4M3 cache is the fp32 product of code and scale rounded to fp16.  (In fp16
+// arithmetic, the scale rounded too, four 32768-token decodes took 86 us instead
+// of 90, and a cached V had another value here than in the tree attention.)
 #include <climits>
 
 #include "tv_device.cuh"
@@ -227,12 +229,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // Bits 0 .. n-1 of a 32-bit word (none for n <= 0, all for n >= 32).
@@ -1092,11 +1088,10 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
     } else {
       rounds(nothing, [&](int, int npieces) {
       // ------------------------------------------------------ V conversion (E4M3)
-      // Per tile: each key's row as code x V scale in fp16 (the scale and the
-      // product rounded once each) into converted slot t % 2, in the MN-major
-      // layout the P V MMA reads.  In fp16, not through fp32: 24 instructions
-      // for 16 codes instead of 40, and the converter sets an E4M3 tile's pace.  Keys that no row of the unit sees get zero rows
-      // (their codes may be stale).
+      // Per tile: each key's row as the fp32 product code x V scale, rounded once
+      // to fp16 (the value that the tree attention takes too), into converted slot
+      // t % 2, in the MN-major layout the P V MMA reads.  Keys that no row of the
+      // unit sees get zero rows (their codes may be stale).
       if (F8 && warp >= kConvWarp) {
         const int ct = tid - kConvWarp * 32;  // 0 .. 127
         const float* scl = reinterpret_cast<const float*>(smem + Ly::kVScl);
@@ -1119,18 +1114,13 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
               // eight neighbouring lanes touch all banks once on either side.
               const int key = ext.key_tile(t) * BN + ct;
               const bool seen = key <= hi && (key < a.sinks || key >= ext.lo);
-              // code x fp16(scale x 2^7), then x 2^-7 (scales of 1 and more as
-              // they are): the scale keeps its 11 bits down to 2^-21 and the
-              // product stays in range
-              const float s = scl[vs * BN + ct];
-              const bool small = s < 1.0f;
-              const uint32_t s2 = pack_f16x2(small ? s * 128.0f : s, small ? s * 128.0f : s);
-              const uint32_t back = small ? 0x20002000u : 0x3c003c00u;  // 2^-7 or 1
+              const float s = seen ? scl[vs * BN + ct] : 0.0f;
+              const float2 s2 = make_float2(s, s);
               const uint8_t* raw = smem + Ly::kVRing + vs * Ly::kKTileBytes + ct * 128;
               uint8_t* v16 = smem + Ly::kV16 + (tau & 1) * Ly::kTileBytes + (ct >> 3) * Ly::kGroupBytes + (ct & 7) * 128;
               const int sw = (ct & 7) << 4;
-              // rolled: unrolled by 4 and 8 four 32768-token decodes take 6 and 21 us
-              // more (the kernel's loops share one instruction cache)
+              // rolled: unrolled by 4 four 32768-token decodes take 9 us more (the
+              // kernel's loops share one instruction cache)
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {
                 uint32_t h[8];
@@ -1139,9 +1129,10 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   uint32_t c01, c23;
-                  e4m3x4_to_f16x2x2(ww[k], c01, c23);  // exact
-                  h[2 * k] = seen ? mul_f16x2(mul_f16x2(c01, s2), back) : 0u;
-                  h[2 * k + 1] = seen ? mul_f16x2(mul_f16x2(c23, s2), back) : 0u;
+                  e4m3x4_to_f16x2x2(seen ? ww[k] : 0u, c01, c23);  // exact
+                  const float2 v01 = mul2(unpack_f16x2(c01), s2), v23 = mul2(unpack_f16x2(c23), s2);
+                  h[2 * k] = pack_f16x2(v01.x, v01.y);
+                  h[2 * k + 1] = pack_f16x2(v23.x, v23.y);
                 }
                 uint8_t* line = v16 + (c >> 2) * 1024;
                 *reinterpret_cast<uint4*>(line + ((((2 * c) & 7) << 4) ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
