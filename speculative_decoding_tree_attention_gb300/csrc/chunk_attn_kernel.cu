@@ -65,6 +65,7 @@
 // an E4M3 cache is the fp32 product of code and scale rounded to fp16.  (In fp16
 // arithmetic, the scale rounded too, four 32768-token decodes took 86 us instead
 // of 90, and a cached V had another value here than in the tree attention.)
+// P of an E4M3 cache is raised by 2^7 (kRaiseLog2).
 #include <climits>
 
 #include "tv_device.cuh"
@@ -92,9 +93,14 @@ struct Shares {
   static constexpr int kSoftmaxRegs = F8 ? 184 : 208;
   static constexpr int kOtherRegs = F8 ? 72 : 80;
 };
-// the running max moves only when a tile exceeds it by 2^8: P stays below
-// 2^8 and the row sum below 2^8 x keys, well inside fp32 (and fp16 for P)
+// m_run moves only when a tile's maximum exceeds it by 2^8 more than when it was
+// set: P stays below 2^8 and the row sum below 2^8 x keys, well inside fp32.
 constexpr float kRescaleLog2 = 8.0f;
+// Over E4M3 m_run is set 7 below the maximum, so that the fp16 P of the largest
+// weights lies between 2^7 and 2^15: weights keep their 11 bits down to 2^-21 of
+// the largest instead of 2^-14, and are lost below 2^-32 instead of 2^-25 (with
+// 131072 keys, 2^-8 of the whole).  O and the row sum carry the same factor.
+constexpr float kRaiseLog2 = 7.0f;
 constexpr int kMaxPieces = 16;        // pieces per scheduling round
 constexpr int kCheckThreads = 256;    // of the kernel that checks the sequences
 constexpr int kSclSlots = 8;          // E4M3: scale slots (tile tau in slot tau % 8)
@@ -229,6 +235,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+// Two values -> fp16 (nearest even; 65504 at most): at scores past 2^24, whose
+// differences are off by more than 1, P could pass 2^16 by rounding alone.
+__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // Bits 0 .. n-1 of a 32-bit word (none for n <= 0, all for n >= 32).
@@ -1186,7 +1200,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
           if (cq < 1e-37f) cq = 1e-37f;
         }
 
-        float m_run = -INFINITY;  // running max (log2 units)
+        float m_run = -INFINITY;  // what P is taken against: a running max (log2 units; kRaiseLog2 below it)
         float l_run = 0.0f;       // row sum against m_run
         const Extent ext = extent_of(a, pc.pos0);
         const int t0 = pc.t0, lo = ext.lo, hi = pc.hi(), pos0 = pc.pos0;
@@ -1273,10 +1287,12 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             mx[c] = fmax3(u[0], u[1], fmaxf(u[2], u[3]));
           }
           const float smax = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cq;
-          const bool up = live && smax > m_run + kRescaleLog2;  // (the first visible score too)
+          constexpr float kRaise = F8 ? kRaiseLog2 : 0.0f;
+          const bool up = live && smax > m_run + (kRescaleLog2 + kRaise);  // (the first visible score too)
           if (__any_sync(0xffffffffu, up)) {
-            const float alpha = up ? exp2f(m_run - smax) : 1.0f;
-            if (up) m_run = smax;
+            const float m_new = smax - kRaise;
+            const float alpha = up ? exp2f(m_run - m_new) : 1.0f;
+            if (up) m_run = m_new;
             // O holds P(..t-1) V against the old max; P_h(t-1) V is complete
             // (S_h(t), which this thread has seen complete, was issued after it)
             // (the piece's first P V overwrites O)
@@ -1302,7 +1318,7 @@ __global__ void __launch_bounds__(Shares<F8>::kThreads, 1)
             for (int k = 0; k < 16; ++k) {
               const float2 e = fma2(make_float2(x[32 * q4 + 2 * k], x[32 * q4 + 2 * k + 1]), sc2, nm2);
               const float e0 = ex2_approx(e.x), e1 = ex2_approx(e.y);
-              pk[q4][k] = F8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+              pk[q4][k] = F8 ? pack_f16x2_sat(e0, e1) : pack_bf16x2(e0, e1);
             }
             tmem_st16(tmem_s + 16 * q4, pk[q4]);
             if (q4 == 1 || q4 == 3) {
