@@ -438,7 +438,9 @@ int tv_commit_kv(const tv_commit_params* params, const uint16_t* k_nodes,
  *   k <= p with  window == 0  or  k > p - window  or  k < sinks:
  * causal, optionally with a sliding window of `window` tokens (the token
  * itself included) next to which the first `sinks` tokens stay visible.  Every
- * row sees at least itself.
+ * row sees at least itself.  (The tree attentions have no window: they see the
+ * whole prefix, so the trees of a windowed layer can be verified with them only
+ * while the prefix and a path together are no longer than the window.)
  *   - Pages that no row of the chunk sees are not read: their block-table
  *     entries may hold anything (a windowed cache frees them).  Cached values
  *     at positions that no row sees do not matter; a non-finite V at a position
@@ -521,8 +523,11 @@ int tv_chunk_attention_fp8(const tv_chunk_params* params, const uint8_t* q, cons
  *                      448) over its finite entries, at least 2^-126, 1 for a
  *                      row of zeros; code = the E4M3 value nearest to the real
  *                      quotient x / s, ties to even, magnitudes above 448 (an
- *                      infinity) saturating, NaN as 0x7F.  The cache that
- *                      tv_tree_attention_fp8 and tv_chunk_attention_fp8 read.
+ *                      infinity) saturating, NaN as 0x7F.  With D = 128, the
+ *                      cache that tv_tree_attention_fp8 and
+ *                      tv_chunk_attention_fp8 read; they take V in fp16, so rows
+ *                      of V beyond 65504 (stored here as they are) become
+ *                      infinite there.  With D = 64 tv_read_kv_fp8 alone reads it.
  *   tv_read_kv_fp8     the other way: bf16 rows code x scale (the fp32 product,
  *                      rounded to nearest even).
  * status[b]: TV_OK, also for an empty chunk; TV_ERR_BAD_TREE if seq_lens[b] <
@@ -615,7 +620,7 @@ int tv_commit_kv_fp8(const tv_commit_params* params, const uint8_t* k_nodes,
  * ====================================================================== */
 typedef struct {
   int32_t batch;         /* 1 <= B <= 65535                                */
-  int32_t vocab;         /* V, 1 <= V < 2^18                               */
+  int32_t vocab;         /* V, 1 <= V < 2^18: as tv_accept, which takes the rows next */
   int32_t max_nodes;     /* >= every N_b, <= TV_MAX_NODES                  */
   int32_t total_nodes;   /* node_offsets[batch] (host copy)                */
   int32_t total_history; /* entries of history, <= 2^30                    */

@@ -23,9 +23,10 @@
 // bf16 and 8 codes each; the rows of a CTA are ordered (K or V, head, token), so
 // that neighbouring rows of a page are written together.
 //
-// Measured (8 KV heads, D = 128): the K/V of 4 x 8192 tokens to E4M3 51 us (3.9
-// TB/s; the same bytes moved without the arithmetic 34 us), of 16 tokens 4 us;
-// 4 x 32768 tokens read back to bf16 149 us (5.5 TB/s), 1001 tokens 4 us.
+// Measured (8 KV heads, D = 128; device time, the call replayed): the K/V of 4 x
+// 8192 tokens to E4M3 52 us (3.9 TB/s; the same bytes moved without the arithmetic
+// 34 us; with a cold L2 56), of 16 tokens 4 us; 4 x 32768 tokens read back to bf16
+// 149 us (5.5 TB/s), 1001 tokens 4 us.
 #include <climits>
 
 #include "tv_device.cuh"

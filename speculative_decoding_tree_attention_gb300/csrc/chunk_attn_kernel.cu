@@ -14,6 +14,9 @@
 // that any of its rows sees: the tiles of the sinks, then the tiles from the
 // start of the first row's window to the last row's position.
 //
+// A small kernel runs first (chunk_check_kernel): it checks every sequence and the
+// pages that it sees, and malformed ones take no further part.
+//
 // Work.  Persistent grid, one CTA per SM.  All units lie on one line ordered
 // (sequence, unit, KV head), cut into equal contiguous ranges, one per CTA,
 // computed on the device from the lengths.  A single decode token of one
@@ -54,10 +57,10 @@
 // TV_ERR_DEVICE_TIMEOUT for its sequence, drains its copies and returns.
 //
 // Bound: the tensor pipe for chunks (a chain S, softmax, P V, S per m-tile keeps
-// it 61 % busy), HBM for decode.  Measured, D = 128: 2048 tokens over 32768, 64/8
-// heads, 1.65 ms (1.38 PFLOP/s); four 1600-token prompts, 32/8 heads, 97 us; 16
-// decode tokens over 512 to 4096, 32/8 heads, 42 us (3.9 TB/s); 4 over 32768 in
-// E4M3, 64/8 heads, 89 us (3.1 TB/s).
+// it 60 % busy), HBM for decode.  Measured, D = 128 (device time, the call
+// replayed): 2048 tokens over 32768, 64/8 heads, 1.66 ms (1.36 PFLOP/s); four
+// 1600-token prompts, 28/4 heads, 97 us; 16 decode tokens over 512 to 4096, 32/8
+// heads, 42 us (3.9 TB/s); 4 over 32768 in E4M3, 64/8 heads, 91 us (3.0 TB/s).
 //
 // Precision.  S, the softmax and O are fp32.  P is rounded to the 16-bit type
 // of V for the P V product (bf16; fp16 for an E4M3 cache) and the row sum adds

@@ -26,9 +26,10 @@
 // from L2 took longer than the copy (48 us).
 //
 // Bound: HBM; per entry 4 (fp32) or 2 (bf16) bytes read, 4 written, a mask bit.
-// 16 trees of 26 or 64 nodes, V = 32000, bf16, histories of 512 to 4096: 36 us
-// (4.0 TB/s: each tree's history is counted by all of its 16 chunks' CTAs).
-// 4 trees of 128 nodes, V = 151936, fp32, histories of 1600: 107 us (5.9 TB/s).
+// 16 trees of 26 or 64 nodes, V = 32000, bf16, histories of 512 to 4096: 37 us
+// (3.9 TB/s: each tree's history is counted by all of its 16 chunks' CTAs).
+// 4 trees of 128 nodes, V = 151936, fp32, histories of 1600: 106 us (5.9 TB/s).
+// (Device time, the call replayed; with a cold L2 40 and 108 us.)
 #include <math.h>
 
 #include "tv_device.cuh"

@@ -92,7 +92,9 @@ int launch_tree_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t 
 size_t attn_slot_bytes(int head_dim);
 
 // Costs on the chunk attention's line of work: of a key tile of a full unit,
-// and of a piece besides its tiles.
+// and of a piece besides its tiles.  (Piece costs of 4, 6, 8 and 10: 1600-token
+// prompts 98, 97, 100 and 102 us, window 1024 100, 103, 103 and 108, E4M3 decode
+// 93, 91, 92 and 92.)
 constexpr int kChunkTileCost = 3;
 constexpr int kChunkPieceCost = 6;
 
