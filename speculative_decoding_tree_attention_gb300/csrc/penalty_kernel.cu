@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(kThreads, BF16 && !VEC ? 2 : 3) penalty_kernel
   const int c0 = blockIdx.x * kChunk, b = blockIdx.y;
   const int nv = min(kChunk, a.vocab - c0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n0 = __ldg(a.node_offsets + b);
-  const long long nodes = static_cast<long long>(__ldg(a.node_offsets + b + 1)) - n0;
+  // the tree's rows, of a malformed one those that are there
+  const int from = __ldg(a.node_offsets + b), to = __ldg(a.node_offsets + b + 1);
+  const int n0 = max(from, 0), N = max(min(to, a.total_nodes), n0) - n0;
   int h0 = 0, h1 = 0;
   if (a.history_offsets) {  // (of an empty list too)
     h0 = __ldg(a.history_offsets + b);
@@ -131,11 +132,9 @@ __global__ void __launch_bounds__(kThreads, BF16 && !VEC ? 2 : 3) penalty_kernel
     s.bad = 0;
     s.decrease = b;
   }
-  const bool rows_ok = nodes >= 1 && n0 >= 0 && n0 + nodes <= a.total_nodes;
-  const int N = rows_ok ? static_cast<int>(nodes) : 0;
-  bool bad = !rows_ok || N > a.max_nodes || h0 < 0 || h1 < h0 || h1 > a.total_history || e0 < 0 || e1 < e0 ||
-             e1 > a.total_bias || !(r.rep > 0.0f && r.rep < INFINITY) || !(fabsf(r.pres) < INFINITY) ||
-             !(fabsf(r.freq) < INFINITY);
+  bool bad = from < 0 || to <= from || to > a.total_nodes || N > a.max_nodes || h0 < 0 || h1 < h0 ||
+             h1 > a.total_history || e0 < 0 || e1 < e0 || e1 > a.total_bias || !(r.rep > 0.0f && r.rep < INFINITY) ||
+             !(fabsf(r.pres) < INFINITY) || !(fabsf(r.freq) < INFINITY);
   const uint4 zero = make_uint4(0, 0, 0, 0), none = make_uint4(~0u, ~0u, ~0u, ~0u);
 #pragma unroll
   for (int i = 4 * tid; i < kChunk; i += 4 * kThreads) {
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && !VEC ? 2 : 3) penalty_kernel
   __syncthreads();
   bad = bad || s.bad || s.decrease < b;
   if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) a.status[b] = bad ? kBadTree : kOk;
-  if (!rows_ok) return;
+  if (N == 0) return;
   const bool has_bias = a.bias_ids != nullptr;
   if (!bad) {
     // the marks, their prefix counts, and the list

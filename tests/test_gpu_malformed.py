@@ -127,6 +127,43 @@ def test_penalty_extents_of_an_empty_list(off, bad, what):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [64, 5001])
+@pytest.mark.parametrize("off, bad, kept", [
+    ([0, 10, 15, 30], [2], (15, 20)),       # rows past the last: those that are there
+    ([0, 10, 15, HIGH], [2], (15, 20)),
+    ([-4, 10, 15, 20], [0], (0, 10)),       # rows before the first
+    ([LOW, 10, 15, 20], [0], (0, 10)),
+    ([0, 10, 25, 30], [1, 2], (10, 20)),    # one past the last row, one wholly behind it
+    ([0, 10, 10, 20], [1], (0, 0)),         # a tree without nodes
+    ([HIGH, HIGH, HIGH, HIGH], [0, 1, 2], (0, 0)),
+    ([0, 10, 30, 20], [1, 2], (10, 20)),    # past the last row, and a decrease behind it
+])
+def test_penalties_of_rows_outside_the_logits(off, bad, kept, vocab, dtype):
+    """Of a malformed tree the rows that are there keep their logits; rows of no
+    tree keep what the output held."""
+    ensure_built()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(20, vocab, device="cuda", generator=g).to(dtype)
+    tokens = torch.randint(0, vocab, (20,), device="cuda", generator=g, dtype=torch.int32)
+    parent = torch.full((20,), -1, dtype=torch.int32, device="cuda")
+    for b in range(3):
+        if b not in bad:
+            n = off[b + 1] - off[b]
+            parent[off[b]:off[b + 1]] = i32([-1] + list(range(n - 1)))
+    out, st = tv.penalize_logits(x, tokens, parent, i32(off), max_nodes=20, presence=torch.ones(3, device="cuda"),
+                                 out=torch.full((20, vocab), 7.0, device="cuda"))
+    assert st.tolist() == [BAD_TREE if b in bad else 0 for b in range(3)]
+    want = torch.full((20, vocab), 7.0, device="cuda")
+    want[kept[0]:kept[1]] = x.float()[kept[0]:kept[1]]
+    for b in set(range(3)) - set(bad):
+        want[off[b]:off[b + 1]] = x.float()[off[b]:off[b + 1]]
+        for r in range(off[b], off[b + 1]):
+            seen = tokens[off[b] + 1:r + 1].long().unique()
+            want[r, seen] -= 1.0
+    assert torch.equal(out, want)
+
+
 # ------------------------------------------------------------------ chunk attention
 def check_all_but(got, good, c, zero, fp8, window, sinks):
     """The rows of sequences `zero` are zeros.  The others are theirs: within the
