@@ -614,7 +614,8 @@ def _chunk(q, q_scale, k_pool, k_scale, v_pool, v_scale, block_table, seq_lens, 
         _arg("out", out, odt, qs, dev)
     if status is not None:
         _arg("status", status, i32, (batch,), dev)
-    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+    if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev
+                                      and workspace.is_contiguous()):
         _bad("workspace", f"a contiguous tensor on CUDA device {dev}")
 
     def call(handle):

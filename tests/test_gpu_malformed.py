@@ -309,3 +309,10 @@ def test_chunk_pages_of_many_sequences():
     got, st = call(bad)
     assert np.flatnonzero(st).tolist() == hit and (st[hit] == BAD_TREE).all()
     check_all_but(got, good, c, hit, False, 0, 0)
+
+
+def test_chunk_workspace_that_is_no_tensor():
+    c = make([20], [3], 4, 2, 64, seed=0)
+    for bad in ([0] * 1024, 4096, torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(2, 1 << 20, device="cuda").t()):
+        with pytest.raises(ValueError):
+            call(c, workspace=bad)
