@@ -488,7 +488,9 @@ size_t tv_chunk_attention_workspace_size(const tv_chunk_params* params);
  * bf16 [num_blocks][Hkv][16][D]; block_table int32 [batch][max_blocks_per_seq];
  * seq_lens int32 [batch]; token_offsets int32 [batch+1]; out [total_tokens]
  * [Hq][D]; status int32 [batch].  All device pointers 16-byte aligned.
- * TV_ERR_UNSUPPORTED: a head_dim other than 64 and 128, or Hq / Hkv > 256. */
+ * TV_ERR_UNSUPPORTED: a head_dim other than 64 and 128, or Hq / Hkv > 256.
+ * TV_ERR_INVALID_ARG also where the work is too long to be counted in 32 bits: a
+ * whole prompt of 2^19 tokens with 64/8 heads is taken, one of 2^20 in parts. */
 int tv_chunk_attention(const tv_chunk_params* params, const uint16_t* q, const uint16_t* k_pool,
                        const uint16_t* v_pool, const int32_t* block_table,
                        const int32_t* seq_lens, const int32_t* token_offsets, void* out,
