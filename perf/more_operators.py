@@ -487,7 +487,7 @@ def _own(s):
             s["keep"] = {"block_table_out": torch.empty_like(s["table"]), "ref_counts_out": torch.empty_like(s["refs"]),
                          "page_map": torch.empty_like(s["refs"]), "count": empty(2, i32),
                          "moves": empty((max(1, s["refs"].shape[0] // 2), 3), i32)}
-        r = tv.compact_pages(s["table"], s["refs"], status=s["status"], workspace=s["workspace"], **s["keep"])
+        r = tv.compact_pages(s["table"], s["refs"], status=s["status"], **s["keep"])
         tv.copy_pages(r["moves"], s["k"], s["v"], count=r["count"][1:], **scales)
         return {"table": r["block_table"], "refs": r["ref_counts"], "page_map": r["page_map"], "count": r["count"][:1], **_values(s)}
     if "copies" not in s:
