@@ -649,6 +649,231 @@ int tv_penalize_logits(const tv_penalty_params* params, const void* logits,
                        const int32_t* bias_offsets, const uint32_t* allowed_mask, float* out,
                        int32_t* status, cudaStream_t stream);
 
+/* ========================================================================
+ * Norm of every query and key head and its rotation by the token's position,
+ * in one pass, ahead of tv_append_kv, tv_quantize_rows and the attentions
+ * (which take rotated rows).
+ *
+ * A head x of D values of token t becomes, with weights w given (q_weight for
+ * queries, k_weight for keys; NULL: no norm),
+ *   x = x / sqrt(mean(x^2) + eps) * w,
+ * and of its first R = rotary_dim values pair i < R/2, (x_i, x_{i+R/2}), or
+ * (x_2i, x_2i+1) with `interleaved`, turns by
+ *   theta = positions[axis_of_pair[i]][t] * frequencies[i]:
+ *   (a, b) -> scale * (a cos theta - b sin theta, a sin theta + b cos theta).
+ * The other values stay as they are (normed).  Several axes serve images and
+ * video: of a text token all positions are the same, of an image's its time, row
+ * and column; a list of sections, or axes taken in turn, is a choice of
+ * axis_of_pair.  Tree nodes have the position prefix length + depth.  Frequencies
+ * of the other sign turn back.
+ * Arithmetic: fp32, one rounding to bf16.  An angle's fraction of a turn is
+ * computed in 64-bit fixed point, off by at most |position| 2^-64 turns for
+ * |frequency| <= 2 pi: far positions lose nothing.  A frequency that is not
+ * finite makes its pairs NaN.  The norm's sum of squares overflows fp32 from
+ * values near 2^60 on, and a row of zeros with eps = 0 is NaN.
+ * In place: q_out may be q with the same stride, k_out k with its own; other
+ * overlaps of an output with an input or with the other output are refused.
+ * ====================================================================== */
+#define TV_MAX_POSITION_AXES 4
+typedef struct {
+  int32_t tokens;         /* T rows; 0 enqueues nothing                         */
+  int32_t num_q_heads;    /* Hq >= 1                                            */
+  int32_t num_kv_heads;   /* Hkv >= 0 (0: queries alone)                        */
+  int32_t head_dim;       /* D: 64 or 128                                       */
+  int32_t rotary_dim;     /* R: even, 0 <= R <= D (0: norms alone)              */
+  int32_t interleaved;    /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1)       */
+  int32_t num_axes;       /* rows of positions, 1 .. TV_MAX_POSITION_AXES       */
+  int32_t weight_dtype;   /* tv_out_dtype of the weights: bf16 (0) or fp32 (1)  */
+  float eps;              /* >= 0                                               */
+  float scale;            /* of the turned values (a long-context rule's factor), 0 => 1 */
+  int64_t q_stride;       /* elements between the rows of q, 0 => Hq*D; multiples of 8 */
+  int64_t k_stride;       /* ... of k, 0 => Hkv*D                               */
+  int64_t q_out_stride;
+  int64_t k_out_stride;
+  uint8_t axis_of_pair[64]; /* position axis of pair i < R/2                    */
+} tv_rotate_params;       /* host struct */
+
+/* Layouts: q, q_out bf16 [T][Hq][D], k, k_out bf16 [T][Hkv][D] (rows a stride
+ * apart: slices of a fused projection); q_weight, k_weight [D] or NULL;
+ * positions int32 [num_axes][T]; frequencies fp64 [R/2], radians a position (NULL
+ * with R = 0, as positions).  k and k_out may be NULL with num_kv_heads = 0.
+ * Device pointers 16-byte aligned. */
+int tv_rotate_qk(const tv_rotate_params* params, const uint16_t* q, const uint16_t* k,
+                 const void* q_weight, const void* k_weight, const int32_t* positions,
+                 const double* frequencies, uint16_t* q_out, uint16_t* k_out,
+                 cudaStream_t stream);
+
+/* ========================================================================
+ * The next beams of every request: the S best continuations over its K beams
+ * and the vocabulary.
+ *
+ * Request b has rows b*K .. b*K + K-1.  Row r with score s_r (the sum of its
+ * tokens' log-probabilities) and logits x offers, for every token v,
+ *   score d = s_r + x_v - LSE(x), length lengths[r] + 1;
+ * a row with finished[r] != 0 offers itself once: token end_token, score s_r,
+ * length lengths[r]; its logits are not read.  Candidates are ordered by
+ *   key = d / max(length, 1)^length_penalty, then the lower row, then the lower
+ * token, and the first S are written, in order: token, parent row (of all rows,
+ * as tv_fork_pages takes it), score, length, and whether the continuation has
+ * ended (its parent had, or its token is end_token).  S = 2K candidates hold K
+ * that have not ended, whatever ends.
+ * A logit of -inf or NaN and a row with score -inf offer nothing; where fewer than
+ * S candidates are left the rest is token -1, parent -1, score -inf, length 0,
+ * finished 0.  A score that is NaN or +inf, a logit of +inf in a row that is read,
+ * or a length below 0 or above 2^24 gives the request TV_ERR_BAD_TREE and such
+ * entries throughout.
+ * Within a row the order is exact.  LSE is off by about 1e-7 (fp32 exps and sums,
+ * joined in fp64), so candidates of different rows whose scores are closer than
+ * that may come in either order, the same in every call; scores are rounded once
+ * to fp32.
+ * ====================================================================== */
+#define TV_MAX_BEAMS 64
+#define TV_MAX_BEAM_SELECT 64
+typedef struct {
+  int32_t batch;         /* 1 <= B <= 65535                                    */
+  int32_t beams;         /* K, 1 .. TV_MAX_BEAMS                               */
+  int32_t select;        /* S, 1 .. TV_MAX_BEAM_SELECT                         */
+  int32_t vocab;         /* V, 1 <= V < 2^18                                   */
+  int32_t logits_dtype;  /* tv_out_dtype of the logits: bf16 (0) or fp32 (1)   */
+  int32_t end_token;     /* -1: none, else below V                             */
+  float length_penalty;  /* -4 .. 4; 0: keys are scores                        */
+  int64_t logits_stride; /* entries between the rows of logits, 0 => V         */
+} tv_beam_params;        /* host struct */
+
+/* Bytes of device workspace (0 if the parameters are invalid): of each part of a
+ * row (at most 8184 entries) its maximum, sum and S best.  Contents need no
+ * initialisation; calls that overlap on the GPU need distinct workspaces. */
+size_t tv_beam_select_workspace_size(const tv_beam_params* params);
+
+/* Layouts: logits bf16 or fp32 [B*K][V] (rows logits_stride apart); scores fp32
+ * [B*K]; lengths, finished int32 [B*K] or NULL (lengths may be NULL only with
+ * length_penalty 0 and lengths_out NULL); tokens, parents int32 [B][S]; scores_out
+ * fp32 [B][S]; lengths_out, finished_out int32 [B][S] or NULL; status int32 [B].
+ * scores_out, lengths_out and finished_out do not overlap the arrays that they
+ * follow.  Device pointers 16-byte aligned. */
+int tv_beam_select(const tv_beam_params* params, const void* logits, const float* scores,
+                   const int32_t* lengths, const int32_t* finished, int32_t* tokens,
+                   int32_t* parents, float* scores_out, int32_t* lengths_out,
+                   int32_t* finished_out, int32_t* status, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* ========================================================================
+ * The pages of the paged cache: given to sequences, taken back, passed on to the
+ * children of a beam step (or of a shared prompt), compacted, copied.
+ *
+ * An entry >= 0 of a block-table row is a reference to a page; a negative one is
+ * none.  ref_counts[p] counts the references to page p, and the caller's own
+ * besides; a page is free where it is 0.  The caller keeps ref_counts[p] at least
+ * the number of entries that name p (a table of -1 and counts of 0 to begin with);
+ * the calls keep it so.  Where it is not, no call reads or writes out of range, and
+ * that is all.  An entry >= num_blocks names nothing.
+ * Pages are given lowest number first, to rows in order: the same tables and
+ * counts give the same result.  Calls on the same counts must not overlap.
+ * ====================================================================== */
+typedef struct {
+  int32_t rows;               /* 1 <= R <= 65536 rows of block_table           */
+  int32_t new_rows;           /* tv_fork_pages: 1 <= R' <= 65536; else unused  */
+  int32_t block_size;         /* must be TV_BLOCK_SIZE (16)                    */
+  int32_t max_blocks_per_seq; /* row stride of the block tables                */
+  int32_t num_blocks;         /* pages in the pool, <= 2^30                    */
+  int32_t sinks;              /* tv_free_pages: first tokens that are kept     */
+} tv_page_params;             /* host struct */
+
+/* Bytes of device workspace of tv_alloc_pages and tv_fork_pages (0 if the
+ * parameters are invalid).  Contents need no initialisation; calls that overlap on
+ * the GPU need distinct workspaces. */
+size_t tv_pages_workspace_size(const tv_page_params* params);
+
+/* Pages for the positions [begin[b], end[b]) of every row: entries that lack one
+ * (below 0) get a free page, whose count becomes 1.  status[b]: TV_OK, also where
+ * nothing was lacking; TV_ERR_NO_PAGE, and the row unchanged, if its pages do not
+ * fit behind those that all rows before it lack (theirs count whether they fit or
+ * not); TV_ERR_BAD_TREE, and the row unchanged, if begin < 0, end < 0 or end > 16 *
+ * max_blocks_per_seq, or one of these entries is >= num_blocks.
+ * block_table int32 [R][max_blocks_per_seq] and ref_counts int32 [num_blocks] are
+ * changed in place; begin int32 [R] or NULL (0); end int32 [R]; status int32 [R].
+ * Device pointers 16-byte aligned. */
+int tv_alloc_pages(const tv_page_params* params, int32_t* block_table, int32_t* ref_counts,
+                   const int32_t* begin, const int32_t* end, int32_t* status, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Takes back the pages of every row outside its positions [keep_begin[b],
+ * keep_end[b]): the entries of whole pages below keep_begin (but for those of the
+ * first `sinks` tokens: what a sliding window no longer sees) and of pages from
+ * keep_end on (a sequence that has ended: keep_end 0) become -1, and their pages'
+ * counts are lowered.  keep_begin int32 [R] or NULL (0), keep_end int32 [R] or NULL
+ * (everything from keep_begin on is kept); status[b]: TV_OK; TV_ERR_BAD_TREE if a
+ * position is negative (the row unchanged) or such an entry was >= num_blocks (it
+ * becomes -1 as well).  In place, layouts as tv_alloc_pages. */
+int tv_free_pages(const tv_page_params* params, int32_t* block_table, int32_t* ref_counts,
+                  const int32_t* keep_begin, const int32_t* keep_end, int32_t* status,
+                  cudaStream_t stream);
+
+/* New rows from old ones: row i of block_table_out continues row parents[i] of
+ * block_table (-1: an empty row, length 0), seq_lens_out[i] = its length.  The old
+ * rows are used up: their references pass to the new ones, or are given back.
+ *   - Pages that the length fills are shared by all children of a row.
+ *   - The page that it fills in part, which the children go on to write, stays with
+ *     the first child (the lowest i) where nobody else refers to it; every other
+ *     child gets a free page for it and an entry of `copies` (source page,
+ *     destination page, tokens to copy) for tv_copy_pages; (-1, -1, 0) where there
+ *     is nothing to copy.  Free pages are those that were free before the call.
+ *   - Entries past the length (pages given ahead) pass to the first child.
+ * status[i]: TV_OK; TV_ERR_BAD_TREE if parents[i] is not a row, or its row's length
+ * is negative or longer than the row, or the partly filled page is missing or has
+ * no count; TV_ERR_NO_PAGE if no page was left for the copy: row i is empty then,
+ * length 0, and refers to nothing.  An entry >= num_blocks becomes -1 in the rows
+ * that continue it, which get TV_ERR_BAD_TREE and are otherwise whole.
+ * block_table int32 [R][max_blocks_per_seq], seq_lens int32 [R], parents int32
+ * [R']; ref_counts int32 [num_blocks], in place; block_table_out int32 [R']
+ * [max_blocks_per_seq], seq_lens_out int32 [R'], which are no inputs of the call;
+ * copies int32 [R'][3]; status int32 [R'].  Device pointers 16-byte aligned. */
+int tv_fork_pages(const tv_page_params* params, const int32_t* block_table,
+                  const int32_t* seq_lens, const int32_t* parents, int32_t* ref_counts,
+                  int32_t* block_table_out, int32_t* seq_lens_out, int32_t* copies,
+                  int32_t* status, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* Moves the pages in use together: of N pages with a count other than 0, those
+ * numbered N and above move to the free numbers below N, in order.  moves[k] =
+ * (source, destination, 16) for tv_copy_pages, k < count[1]; count[0] = N;
+ * page_map[p] = the new number of page p, -1 of a free one (for references that
+ * the caller holds); ref_counts_out and block_table_out are the counts and tables
+ * in new numbers.  status[b]: TV_OK; TV_ERR_BAD_TREE if an entry of the row names a
+ * free page or is >= num_blocks (it becomes -1).
+ * ref_counts_out may be ref_counts, and block_table_out block_table; no other two
+ * arrays overlap.  moves int32 [max(1, num_blocks / 2)][3] (entries from count[1] on
+ * are left as they were), count int32 [2], page_map int32 [num_blocks].  Device
+ * pointers 16-byte aligned. */
+int tv_compact_pages(const tv_page_params* params, const int32_t* block_table,
+                     const int32_t* ref_counts, int32_t* block_table_out,
+                     int32_t* ref_counts_out, int32_t* page_map, int32_t* moves,
+                     int32_t* count, int32_t* status, cudaStream_t stream);
+
+/* Copies pages within the pools of K and V, for every layer: entry i of `copies`
+ * is (source, destination, tokens): the first `tokens` rows (of 16) of every head.
+ * Entries from count[0] on (count NULL: none) are left out.  No destination is
+ * another entry's source or destination.  status[i]: TV_OK, also of an entry whose
+ * pages are both negative (nothing to copy) or the same; TV_ERR_NO_PAGE, and
+ * nothing copied, if one is not in the pool or tokens is not in 0 .. 16. */
+typedef struct {
+  int32_t entries;      /* of copies; 0 enqueues nothing                      */
+  int32_t layers;       /* L >= 1 pools, one behind another                   */
+  int32_t num_kv_heads; /* Hkv                                                */
+  int32_t head_dim;     /* D: 64 or 128                                       */
+  int32_t block_size;   /* must be TV_BLOCK_SIZE (16)                         */
+  int32_t num_blocks;   /* pages in a layer's pool                            */
+} tv_copy_params;       /* host struct */
+
+/* Layouts: copies int32 [entries][3]; count int32 [1] (4-byte aligned) or NULL;
+ * pools bf16 [L][num_blocks][Hkv][16][D]; status int32 [entries].  _fp8: pools u8,
+ * scales fp32 [L][num_blocks][Hkv][16].  Device pointers 16-byte aligned. */
+int tv_copy_pages(const tv_copy_params* params, const int32_t* copies, const int32_t* count,
+                  uint16_t* k_pool, uint16_t* v_pool, int32_t* status, cudaStream_t stream);
+int tv_copy_pages_fp8(const tv_copy_params* params, const int32_t* copies, const int32_t* count,
+                      uint8_t* k_pool, float* k_scale, uint8_t* v_pool, float* v_scale,
+                      int32_t* status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,9 +13,11 @@ follows.  The one step without arithmetic, the commit of the accepted path
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 import subprocess
 import threading
+from fractions import Fraction
 
 import numpy as np
 
@@ -422,3 +424,162 @@ def penalize_logits(logits, draft_tokens, parent, node_offsets, history=(), hist
                 if 0 <= t < V:
                     row[t] += x
     return out if allowed is None else np.where(allowed, out, -np.inf)
+
+
+# ------------------------------------------------------------------ head norms and positions
+_TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889184615632812572417997256069650684234136,
+                   10 ** 99)
+
+
+def rotate(x, positions, frequencies, weight=None, eps=1e-6, axes=None, interleaved=False, scale=1.0):
+    """Rows x [T, H, D] normed and turned, in fp64; positions [axes, T]."""
+    x = np.asarray(x, np.float64).copy()
+    if weight is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    n = len(frequencies)
+    for i in range(n):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+        f = float(frequencies[i])
+        pos = np.asarray(positions[axes[i] if axes is not None else 0], np.int64)
+        turn = pos * f
+        if np.abs(turn).max(initial=0) >= 2.0 ** 20:  # whole turns taken off the exact product
+            turn = np.array([float(Fraction(int(p)) * Fraction(f) % _TWO_PI) for p in pos])
+        c, s = scale * np.cos(turn)[:, None], scale * np.sin(turn)[:, None]
+        x[..., a], x[..., b] = x[..., a] * c - x[..., b] * s, x[..., a] * s + x[..., b] * c
+    return x
+
+
+# ------------------------------------------------------------------ beams
+def beam_select(logits, scores, beams, select, lengths=None, finished=None, end_token=-1, length_penalty=0.0):
+    """(token, parent row, score, length, finished, key) lists of every request, from
+    the definition in fp64; None for a request that is refused."""
+    out = []
+    for b in range(len(scores) // beams):
+        found, bad = [], False
+        for r in range(b * beams, (b + 1) * beams):
+            s = float(scores[r])
+            n = int(lengths[r]) if lengths is not None else 0
+            ended = finished is not None and int(finished[r]) != 0
+            bad |= math.isnan(s) or s == math.inf or n < 0 or n > 1 << 24
+            if bad or s == -math.inf:
+                continue
+            if ended:
+                found.append((s / max(n, 1) ** length_penalty, r, end_token, s, n, 1))
+                continue
+            x = np.asarray(logits[r], np.float64)
+            x = np.where(np.isnan(x), -np.inf, x)
+            if x.max() == np.inf:
+                bad = True
+            if bad or x.max() == -np.inf:
+                continue
+            lse = x.max() + math.log(np.exp(x - x.max()).sum())
+            for v in np.lexsort((np.arange(len(x)), -x))[:select]:
+                if x[v] > -np.inf:
+                    d = s + float(x[v]) - lse
+                    found.append((d / max(n + 1, 1) ** length_penalty, r, int(v), d, n + 1, int(v == end_token)))
+        if bad:
+            out.append(None)
+            continue
+        # (within a row by logit: the order that they are in)
+        found = [c + (i,) for i, c in enumerate(found)]
+        found.sort(key=lambda c: (-c[0], c[1], c[6]))
+        found = found[:select] + [(-math.inf, -1, -1, -math.inf, 0, 0, 0)] * (select - len(found))
+        out.append([(t, r, d, n, e, k) for k, r, t, d, n, e, _ in found])
+    return out
+
+
+# ------------------------------------------------------------------ pages
+def _page_count(tokens):
+    return -(-tokens // 16)
+
+
+def alloc_pages(table, refs, begin, end):
+    """Status per row; table (lists) and refs change in place."""
+    free = [p for p, n in enumerate(refs) if n == 0]
+    at, status = 0, []
+    for row, lo, hi in zip(table, begin, end):
+        if lo < 0 or hi < 0 or hi > 16 * len(row) or any(e >= len(refs) for e in row[lo // 16:_page_count(hi)]):
+            status.append(5)
+            continue
+        lack = [t for t in range(lo // 16, _page_count(hi)) if row[t] < 0]
+        fits = not lack or at + len(lack) <= len(free)
+        status.append(0 if fits else 7)
+        if fits:
+            for i, t in enumerate(lack):
+                row[t] = free[at + i]
+                refs[row[t]] = 1
+        at += len(lack)
+    return status
+
+
+def free_pages(table, refs, keep_begin, keep_end, sinks=0):
+    status = []
+    for row, lo, hi in zip(table, keep_begin, keep_end):
+        bad = lo < 0 or hi < 0
+        for t in range(len(row) if not bad else 0):
+            if (t < lo // 16 and t >= _page_count(sinks)) or t >= _page_count(hi):
+                if row[t] >= len(refs):
+                    bad = True
+                elif row[t] >= 0:
+                    refs[row[t]] -= 1
+                if row[t] >= 0:
+                    row[t] = -1
+        status.append(5 if bad else 0)
+    return status
+
+
+def fork_pages(table, lens, parents, refs):
+    """(new table, new lengths, copies, status); refs change in place."""
+    free = [p for p, n in enumerate(refs) if n == 0]
+    before, width, pages = list(refs), len(table[0]), len(refs)
+    new, ends, copies, status, at, seen = [], [], [], [], 0, set()
+    for p in parents:
+        row, copy, code, end = [-1] * width, (-1, -1, 0), 0, 0
+        if p < -1 or p >= len(table) or (p >= 0 and not 0 <= lens[p] <= 16 * width):
+            code = 5
+        elif p >= 0:
+            first, full, part = p not in seen, lens[p] // 16, lens[p] % 16
+            seen.add(p)
+            e = table[p][full] if part else None
+            if part and (e < 0 or e >= pages or before[e] < 1):
+                code = 5
+            else:
+                row = [x if t < full + (part > 0) or first else -1 for t, x in enumerate(table[p])]
+                if part and (not first or before[e] > 1):
+                    if at < len(free):
+                        copy = (e, free[at], part)
+                        row[full] = free[at]
+                    else:
+                        row, code = [-1] * width, 7
+                    at += 1
+                if code == 0:
+                    end = lens[p]
+                    if any(x >= pages for x in row):
+                        code = 5
+                    row = [-1 if x < 0 or x >= pages else x for x in row]
+        new.append(row)
+        ends.append(end)
+        copies.append(copy)
+        status.append(code)
+    for rows, by in ((table, -1), (new, 1)):
+        for row in rows:
+            for e in row:
+                if 0 <= e < pages:
+                    refs[e] += by
+    return new, ends, copies, status
+
+
+def compact_pages(table, refs):
+    """(new table, new refs, page map, moves, pages in use, status)."""
+    n = sum(r != 0 for r in refs)
+    to = [p if r else -1 for p, r in enumerate(refs)]
+    moves = list(zip([p for p in range(n, len(refs)) if refs[p]], [p for p in range(n) if not refs[p]]))
+    for src, dst in moves:
+        to[src] = dst
+    counts = [0] * len(refs)
+    for p, r in enumerate(refs):
+        if r:
+            counts[to[p]] = r
+    new = [[to[e] if 0 <= e < len(refs) else -1 for e in row] for row in table]
+    status = [5 if any(e >= 0 and x < 0 for e, x in zip(row, out)) else 0 for row, out in zip(table, new)]
+    return new, counts, to, [(s, d, 16) for s, d in moves], n, status

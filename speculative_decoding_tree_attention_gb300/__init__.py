@@ -19,6 +19,12 @@ PyTorch is used for device memory and the current CUDA stream only.
     quantize_rows(...)   -> codes, scale     (tv_quantize_rows)
     commit_kv_fp8(...)   -> new_prefix_lens, status (tv_commit_kv_fp8)
     penalize_logits(...) -> out, status      (tv_penalize_logits)
+    rotate_qk(...)       -> q, k             (tv_rotate_qk: head norms and positions)
+    beam_select(...)     -> dict of outputs  (tv_beam_select)
+    alloc_pages(...), free_pages(...) -> status (tv_alloc_pages, tv_free_pages)
+    fork_pages(...)      -> block_table, seq_lens, copies, status (tv_fork_pages)
+    compact_pages(...)   -> dict of outputs  (tv_compact_pages)
+    copy_pages(...)      -> status           (tv_copy_pages, tv_copy_pages_fp8)
 """
 from __future__ import annotations
 
@@ -28,7 +34,8 @@ import os
 __all__ = ["TVError", "load", "tree_attention", "tree_attention_fp8", "accept", "commit_kv", "retained_set",
            "chunk_attention", "chunk_attention_fp8", "chunk_params", "chunk_workspace_size",
            "append_kv", "append_kv_fp8", "read_kv_fp8", "quantize_rows", "commit_kv_fp8",
-           "penalize_logits",
+           "penalize_logits", "rotate_qk", "rotary_axes", "beam_select", "beam_workspace_size",
+           "alloc_pages", "free_pages", "fork_pages", "compact_pages", "copy_pages", "page_workspace_size",
            "attention_workspace_size", "attention_plan", "attention_params",
            "TV_MAX_NODES", "TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_DEVICE_TIMEOUT", "TV_ERR_NO_PAGE",
            "status_string"]
@@ -53,7 +60,9 @@ EXPORTS = ("tv_status_string", "tv_version", "tv_tree_attention_workspace_size",
            "tv_tree_attention_no_alloc", "tv_tree_attention_fp8",
            "tv_chunk_attention_workspace_size", "tv_chunk_attention", "tv_chunk_attention_fp8",
            "tv_append_kv", "tv_append_kv_fp8", "tv_read_kv_fp8", "tv_quantize_rows",
-           "tv_commit_kv_fp8", "tv_penalize_logits")
+           "tv_commit_kv_fp8", "tv_penalize_logits", "tv_rotate_qk", "tv_beam_select_workspace_size",
+           "tv_beam_select", "tv_pages_workspace_size", "tv_alloc_pages", "tv_free_pages", "tv_fork_pages",
+           "tv_compact_pages", "tv_copy_pages", "tv_copy_pages_fp8")
 
 
 class TVError(RuntimeError):
@@ -121,6 +130,30 @@ class PenaltyParams(C.Structure):
                 ("logits_dtype", C.c_int32)]
 
 
+class RotateParams(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("num_axes", C.c_int32), ("weight_dtype", C.c_int32), ("eps", C.c_float), ("scale", C.c_float),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("q_out_stride", C.c_int64),
+                ("k_out_stride", C.c_int64), ("axis_of_pair", C.c_uint8 * 64)]
+
+
+class BeamParams(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("beams", C.c_int32), ("select", C.c_int32), ("vocab", C.c_int32),
+                ("logits_dtype", C.c_int32), ("end_token", C.c_int32), ("length_penalty", C.c_float),
+                ("logits_stride", C.c_int64)]
+
+
+class PageParams(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("new_rows", C.c_int32), ("block_size", C.c_int32),
+                ("max_blocks_per_seq", C.c_int32), ("num_blocks", C.c_int32), ("sinks", C.c_int32)]
+
+
+class CopyParams(C.Structure):
+    _fields_ = [("entries", C.c_int32), ("layers", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("block_size", C.c_int32), ("num_blocks", C.c_int32)]
+
+
 _lib = None
 
 
@@ -178,6 +211,26 @@ def load(path: str | None = None) -> C.CDLL:
     lib.tv_commit_kv_fp8.restype = C.c_int
     lib.tv_penalize_logits.argtypes = [C.POINTER(PenaltyParams)] + [vp] * 16 + [vp]
     lib.tv_penalize_logits.restype = C.c_int
+    lib.tv_rotate_qk.argtypes = [C.POINTER(RotateParams)] + [vp] * 8 + [vp]
+    lib.tv_rotate_qk.restype = C.c_int
+    lib.tv_beam_select_workspace_size.argtypes = [C.POINTER(BeamParams)]
+    lib.tv_beam_select_workspace_size.restype = sz
+    lib.tv_beam_select.argtypes = [C.POINTER(BeamParams)] + [vp] * 11 + [sz, vp]
+    lib.tv_beam_select.restype = C.c_int
+    lib.tv_pages_workspace_size.argtypes = [C.POINTER(PageParams)]
+    lib.tv_pages_workspace_size.restype = sz
+    lib.tv_alloc_pages.argtypes = [C.POINTER(PageParams)] + [vp] * 6 + [sz, vp]
+    lib.tv_alloc_pages.restype = C.c_int
+    lib.tv_free_pages.argtypes = [C.POINTER(PageParams)] + [vp] * 5 + [vp]
+    lib.tv_free_pages.restype = C.c_int
+    lib.tv_fork_pages.argtypes = [C.POINTER(PageParams)] + [vp] * 9 + [sz, vp]
+    lib.tv_fork_pages.restype = C.c_int
+    lib.tv_compact_pages.argtypes = [C.POINTER(PageParams)] + [vp] * 8 + [vp]
+    lib.tv_compact_pages.restype = C.c_int
+    lib.tv_copy_pages.argtypes = [C.POINTER(CopyParams)] + [vp] * 5 + [vp]
+    lib.tv_copy_pages.restype = C.c_int
+    lib.tv_copy_pages_fp8.argtypes = [C.POINTER(CopyParams)] + [vp] * 7 + [vp]
+    lib.tv_copy_pages_fp8.restype = C.c_int
     if path is None:
         _lib = lib
     return lib
@@ -921,5 +974,351 @@ def penalize_logits(logits, draft_tokens, parent, node_offsets, *, max_nodes: in
         if rc != TV_OK:
             raise TVError(rc, "tv_penalize_logits")
         return o, st
+
+    return _run(dev, stream, call)
+
+
+# ---------------------------------------------------------------- positions
+def rotary_axes(sections, interleaved: bool = False) -> tuple:
+    """The position axis of every pair, for rotate_qk: sections[a] pairs of axis
+    a, one section behind another (time, height, width), or, interleaved, with
+    pair i of axis i % len(sections) as long as that axis has pairs left and of
+    axis 0 from there on."""
+    n = [int(x) for x in sections]
+    if not n or min(n) < 0:
+        _bad("sections", "numbers of pairs")
+    if not interleaved:
+        return tuple(a for a, k in enumerate(n) for _ in range(k))
+    turn = len(n)
+    return tuple(i % turn if i % turn and i // turn < n[i % turn] else 0 for i in range(sum(n)))
+
+
+_NO_AXES = (C.c_uint8 * 64)()
+
+
+def rotate_qk(q, k, positions, frequencies, *, q_weight=None, k_weight=None, eps: float = 1e-6, axes=None,
+              interleaved: bool = False, scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """tv_rotate_qk: the norm of every head (where its weights are given) and the
+    rotation of its first 2 len(frequencies) values by the token's position.  q
+    [T, Hq, D], k [T, Hkv, D] or None, bf16, which may be strided by tokens, as may
+    q_out and k_out (which may be q and k themselves); positions [T] or [axes, T]
+    int32 and frequencies [R/2] fp64, or both None; axes: the row of positions that
+    each pair goes by (rotary_axes; None: row 0); q_weight, k_weight [D] bf16 or
+    fp32.  Returns (q_out, k_out); nothing is synchronised."""
+    torch = _torch()
+    lib = load()
+    dev = _device("q", q)
+    bf16 = torch.bfloat16
+    qs = _dims("q", q, 3)
+    total, hq, d = qs
+    q_stride = _rows("q", q, bf16, qs, dev)
+    ks, k_stride = (total, 0, d), 0
+    if k is not None:
+        ks = (total, _dims("k", k, 3)[1], d)
+        k_stride = _rows("k", k, bf16, ks, dev)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight go with k")
+    if (positions is None) != (frequencies is None):
+        raise ValueError("positions and frequencies go together")
+    pairs, rows = 0, 1
+    if frequencies is not None:
+        (pairs,) = _dims("frequencies", frequencies, 1)
+        _arg("frequencies", frequencies, torch.float64, (pairs,), dev)
+        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+            _bad("positions", "a tensor of 1 or 2 dimensions")
+        shape = positions.shape
+        if len(shape) == 2:
+            rows = shape[0]
+        _arg("positions", positions, torch.int32, (total,) if len(shape) == 1 else (rows, total), dev)
+    of_pair = _NO_AXES
+    if axes is not None:
+        if len(axes) != pairs or pairs > 64:
+            _bad("axes", "an axis for each frequency")
+        try:
+            of_pair = (C.c_uint8 * 64).from_buffer_copy(bytes(axes).ljust(64, b"\0"))
+        except (TypeError, ValueError):
+            _bad("axes", "small whole numbers")
+    fp32 = False
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            fp32 = getattr(t, "dtype", None) is torch.float32
+            _arg(name, t, torch.float32 if fp32 else bf16, (d,), dev)
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        _bad("k_weight", "of the type of q_weight")
+    if scale == 0.0:
+        _bad("scale", "above 0")
+    qo_stride = _rows("q_out", q_out, bf16, qs, dev) if q_out is not None else 0
+    ko_stride = _rows("k_out", k_out, bf16, ks, dev) if k_out is not None else 0
+    prm = RotateParams(total, hq, ks[1], d, 2 * pairs, 1 if interleaved else 0, rows, 1 if fp32 else 0, eps, scale,
+                       q_stride, k_stride, qo_stride, ko_stride, of_pair)
+
+    def call(handle):
+        p = _ptr_or_null
+        qo = _empty(q_out, qs, bf16, dev)
+        ko = None if k is None else _empty(k_out, ks, bf16, dev)
+        rc = lib.tv_rotate_qk(C.byref(prm), p(q), p(k), p(q_weight), p(k_weight), p(positions), p(frequencies),
+                              p(qo), p(ko), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_rotate_qk")
+        return qo, ko
+
+    return _run(dev, stream, call)
+
+
+# ---------------------------------------------------------------- beams
+def _beam_params(logits, beams, select, end_token, length_penalty):
+    torch = _torch()
+    rows, vocab = _dims("logits", logits, 2)
+    if logits.dtype is not torch.float32 and logits.dtype is not torch.bfloat16:
+        _bad("logits", f"of type float32 or bfloat16, not {logits.dtype}")
+    if not isinstance(beams, int) or beams < 1 or rows % beams:
+        _bad("beams", "a number that divides the rows of logits")
+    _int32(beams=beams, select=select, end_token=end_token)
+    return BeamParams(rows // beams, beams, select, vocab, 1 if logits.dtype is torch.float32 else 0, end_token,
+                      length_penalty, 0)
+
+
+def beam_workspace_size(logits, *, beams: int, select: int | None = None) -> int:
+    """Bytes of the workspace of a beam_select call."""
+    prm = _beam_params(logits, beams, beams if select is None else select, -1, 0.0)
+    return int(load().tv_beam_select_workspace_size(C.byref(prm)))
+
+
+def beam_select(logits, scores, *, beams: int, select: int | None = None, lengths=None, finished=None,
+                end_token: int = -1, length_penalty: float = 0.0, tokens=None, parents=None, scores_out=None,
+                lengths_out=None, finished_out=None, status=None, workspace=None, stream=None):
+    """tv_beam_select: the `select` (None: `beams`) best continuations of every
+    request, in order, over its `beams` rows of logits [B*beams, V] (fp32 or bf16,
+    which may be strided by rows) with scores [B*beams] fp32; lengths, finished
+    [B*beams] int32.  Returns a dict: tokens, parents (rows of logits), scores,
+    finished [B, select], lengths (None without lengths) and status [B]; nothing is
+    synchronised."""
+    torch = _torch()
+    lib = load()
+    i32, f32 = torch.int32, torch.float32
+    dev = _device("logits", logits)
+    prm = _beam_params(logits, beams, beams if select is None else select, end_token, length_penalty)
+    rows = logits.shape[0]
+    prm.logits_stride = _rows("logits", logits, logits.dtype, logits.shape, dev)
+    shape = (prm.batch, prm.select)
+    _arg("scores", scores, f32, (rows,), dev)
+    for name, t in (("lengths", lengths), ("finished", finished)):
+        if t is not None:
+            _arg(name, t, i32, (rows,), dev)
+    for name, t in (("tokens", tokens), ("parents", parents), ("lengths_out", lengths_out), ("finished_out", finished_out)):
+        if t is not None:
+            _arg(name, t, i32, shape, dev)
+    if scores_out is not None:
+        _arg("scores_out", scores_out, f32, shape, dev)
+    if status is not None:
+        _arg("status", status, i32, (prm.batch,), dev)
+    if lengths is None and lengths_out is not None:
+        raise ValueError("lengths_out goes with lengths")
+    _workspace(workspace, dev)
+
+    def call(handle):
+        p = _ptr_or_null
+        tok, par, fin = (_empty(t, shape, i32, dev) for t in (tokens, parents, finished_out))
+        sc, st = _empty(scores_out, shape, f32, dev), _empty(status, prm.batch, i32, dev)
+        ln = None if lengths is None else _empty(lengths_out, shape, i32, dev)
+        ws = workspace
+        if ws is None:
+            ws = _empty(None, int(lib.tv_beam_select_workspace_size(C.byref(prm))), torch.uint8, dev)
+        rc = lib.tv_beam_select(C.byref(prm), p(logits), p(scores), p(lengths), p(finished), p(tok), p(par), p(sc),
+                                p(ln), p(fin), p(st), p(ws), ws.numel() * ws.element_size(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_beam_select")
+        return {"tokens": tok, "parents": par, "scores": sc, "lengths": ln, "finished": fin, "status": st}
+
+    return _run(dev, stream, call)
+
+
+# ---------------------------------------------------------------- pages
+def _workspace(t, dev):
+    if t is not None and not (isinstance(t, _torch().Tensor) and t.get_device() == dev and t.is_contiguous()):
+        _bad("workspace", f"a contiguous tensor on CUDA device {dev}")
+
+
+def _page_args(block_table, ref_counts, new_rows=0, sinks=0):
+    """(device, parameters) of a call on a block table [R, max_blocks] and counts [num_blocks]."""
+    i32 = _torch().int32
+    dev = _device("block_table", block_table)
+    rows, width = _dims("block_table", block_table, 2)
+    _arg("block_table", block_table, i32, (rows, width), dev)
+    (pages,) = _dims("ref_counts", ref_counts, 1)
+    _arg("ref_counts", ref_counts, i32, (pages,), dev)
+    return dev, PageParams(rows, new_rows, TV_BLOCK_SIZE, width, pages, sinks)
+
+
+def page_workspace_size(block_table, ref_counts, *, new_rows: int = 0) -> int:
+    """Bytes of the workspace of an alloc_pages or fork_pages call."""
+    (rows, width), (pages,) = _dims("block_table", block_table, 2), _dims("ref_counts", ref_counts, 1)
+    prm = PageParams(rows, new_rows, TV_BLOCK_SIZE, width, pages, 0)
+    return int(load().tv_pages_workspace_size(C.byref(prm)))
+
+
+def alloc_pages(block_table, ref_counts, end, *, begin=None, status=None, workspace=None, stream=None):
+    """tv_alloc_pages: free pages for the positions [begin[b], end[b]) (begin None:
+    0) of every row of block_table [R, max_blocks] whose entries are negative there,
+    in place there and in ref_counts [num_blocks]; all int32.  Returns status [R];
+    nothing is synchronised."""
+    torch = _torch()
+    lib = load()
+    i32 = torch.int32
+    dev, prm = _page_args(block_table, ref_counts)
+    _arg("end", end, i32, (prm.rows,), dev)
+    if begin is not None:
+        _arg("begin", begin, i32, (prm.rows,), dev)
+    if status is not None:
+        _arg("status", status, i32, (prm.rows,), dev)
+    _workspace(workspace, dev)
+
+    def call(handle):
+        st, ws = _empty(status, prm.rows, i32, dev), workspace
+        if ws is None:
+            ws = _empty(None, int(lib.tv_pages_workspace_size(C.byref(prm))), torch.uint8, dev)
+        p = _ptr_or_null
+        rc = lib.tv_alloc_pages(C.byref(prm), p(block_table), p(ref_counts), p(begin), p(end), p(st), p(ws),
+                                ws.numel() * ws.element_size(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_alloc_pages")
+        return st
+
+    return _run(dev, stream, call)
+
+
+def free_pages(block_table, ref_counts, *, keep_begin=None, keep_end=None, sinks: int = 0, status=None, stream=None):
+    """tv_free_pages: takes back the pages of every row outside its positions
+    [keep_begin[b], keep_end[b]) but for those of the first `sinks` tokens (None: 0,
+    and everything), in place in block_table [R, max_blocks] and ref_counts
+    [num_blocks]; all int32.  Returns status [R]; nothing is synchronised."""
+    i32 = _torch().int32
+    lib = load()
+    _int32(sinks=sinks)
+    dev, prm = _page_args(block_table, ref_counts, 0, sinks)
+    for name, t in (("keep_begin", keep_begin), ("keep_end", keep_end), ("status", status)):
+        if t is not None:
+            _arg(name, t, i32, (prm.rows,), dev)
+
+    def call(handle):
+        st, p = _empty(status, prm.rows, i32, dev), _ptr_or_null
+        rc = lib.tv_free_pages(C.byref(prm), p(block_table), p(ref_counts), p(keep_begin), p(keep_end), p(st), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_free_pages")
+        return st
+
+    return _run(dev, stream, call)
+
+
+def fork_pages(block_table, seq_lens, parents, ref_counts, *, block_table_out=None, seq_lens_out=None, copies=None,
+               status=None, workspace=None, stream=None):
+    """tv_fork_pages: new rows that continue the rows parents [R'] (-1: empty) of
+    block_table [R, max_blocks] with seq_lens [R]; the old rows are used up, and
+    ref_counts [num_blocks] changes in place; all int32.  copies [R', 3] (source,
+    destination, tokens) is what copy_pages has to do before the new rows are read.
+    Returns (block_table_out, seq_lens_out, copies, status); nothing is
+    synchronised."""
+    torch = _torch()
+    lib = load()
+    i32 = torch.int32
+    (new,) = _dims("parents", parents, 1)
+    dev, prm = _page_args(block_table, ref_counts, new)
+    _arg("seq_lens", seq_lens, i32, (prm.rows,), dev)
+    _arg("parents", parents, i32, (new,), dev)
+    shape = (new, prm.max_blocks_per_seq)
+    for name, t, dims in (("block_table_out", block_table_out, shape), ("seq_lens_out", seq_lens_out, (new,)),
+                          ("copies", copies, (new, 3)), ("status", status, (new,))):
+        if t is not None:
+            _arg(name, t, i32, dims, dev)
+    _workspace(workspace, dev)
+
+    def call(handle):
+        out, lens = _empty(block_table_out, shape, i32, dev), _empty(seq_lens_out, new, i32, dev)
+        cp, st, ws = _empty(copies, (new, 3), i32, dev), _empty(status, new, i32, dev), workspace
+        if ws is None:
+            ws = _empty(None, int(lib.tv_pages_workspace_size(C.byref(prm))), torch.uint8, dev)
+        p = _ptr_or_null
+        rc = lib.tv_fork_pages(C.byref(prm), p(block_table), p(seq_lens), p(parents), p(ref_counts), p(out), p(lens),
+                               p(cp), p(st), p(ws), ws.numel() * ws.element_size(), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_fork_pages")
+        return out, lens, cp, st
+
+    return _run(dev, stream, call)
+
+
+def compact_pages(block_table, ref_counts, *, block_table_out=None, ref_counts_out=None, page_map=None, moves=None,
+                  count=None, status=None, stream=None):
+    """tv_compact_pages: the pages in use get the lowest numbers.  block_table [R,
+    max_blocks] and ref_counts [num_blocks] int32, which may be their own outputs.
+    Returns a dict: block_table, ref_counts, page_map [num_blocks] (new numbers, -1
+    of free pages), moves [max(1, num_blocks // 2), 3] (the first count[1] entries are
+    what copy_pages has to do: copy_pages(moves, ..., count=count[1:])), count [2]
+    (pages in use, moves) and status [R]; nothing is synchronised."""
+    i32 = _torch().int32
+    lib = load()
+    dev, prm = _page_args(block_table, ref_counts)
+    rows, pages = prm.rows, prm.num_blocks
+    shape, most = (rows, prm.max_blocks_per_seq), max(1, pages // 2)
+    for name, t, dims in (("block_table_out", block_table_out, shape), ("ref_counts_out", ref_counts_out, (pages,)),
+                          ("page_map", page_map, (pages,)), ("moves", moves, (most, 3)), ("count", count, (2,)),
+                          ("status", status, (rows,))):
+        if t is not None:
+            _arg(name, t, i32, dims, dev)
+
+    def call(handle):
+        out, refs = _empty(block_table_out, shape, i32, dev), _empty(ref_counts_out, pages, i32, dev)
+        to, mv = _empty(page_map, pages, i32, dev), _empty(moves, (most, 3), i32, dev)
+        n, st, p = _empty(count, 2, i32, dev), _empty(status, rows, i32, dev), _ptr_or_null
+        rc = lib.tv_compact_pages(C.byref(prm), p(block_table), p(ref_counts), p(out), p(refs), p(to), p(mv), p(n),
+                                  p(st), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_compact_pages")
+        return {"block_table": out, "ref_counts": refs, "page_map": to, "moves": mv, "count": n, "status": st}
+
+    return _run(dev, stream, call)
+
+
+def copy_pages(copies, k_pool, v_pool, k_scale=None, v_scale=None, *, count=None, status=None, stream=None):
+    """tv_copy_pages, tv_copy_pages_fp8 (with scales): copies pages within the pools
+    of K and V, [num_blocks, Hkv, 16, D] or [layers, num_blocks, Hkv, 16, D], bf16, or
+    uint8 codes with fp32 scales [..., Hkv, 16]; copies [n, 3] int32 (source,
+    destination, tokens), of which the first count [1] (int32; None: all) are done.
+    Returns status [n]; nothing is synchronised."""
+    torch = _torch()
+    lib = load()
+    i32 = torch.int32
+    dev = _device("copies", copies)
+    n = _dims("copies", copies, 2)[0]
+    _arg("copies", copies, i32, (n, 3), dev)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    fp8 = k_scale is not None
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() not in (4, 5):
+        _bad("k_pool", "a tensor of 4 or 5 dimensions")
+    ps = k_pool.shape
+    layers, (blocks, hkv, _, d) = 1 if len(ps) == 4 else ps[0], ps[-4:]
+    elem = torch.uint8 if fp8 else torch.bfloat16
+    _arg("k_pool", k_pool, elem, ps[:-2] + (TV_BLOCK_SIZE, d), dev)
+    _arg("v_pool", v_pool, elem, ps, dev)
+    if fp8:
+        _arg("k_scale", k_scale, torch.float32, ps[:-1], dev)
+        _arg("v_scale", v_scale, torch.float32, ps[:-1], dev)
+    if count is not None:
+        _arg("count", count, i32, (1,), dev)
+    if status is not None:
+        _arg("status", status, i32, (n,), dev)
+    prm = CopyParams(n, layers, hkv, d, TV_BLOCK_SIZE, blocks)
+
+    def call(handle):
+        st, p = _empty(status, n, i32, dev), _ptr_or_null
+        if fp8:
+            rc = lib.tv_copy_pages_fp8(C.byref(prm), p(copies), p(count), p(k_pool), p(k_scale), p(v_pool), p(v_scale),
+                                       p(st), handle)
+        else:
+            rc = lib.tv_copy_pages(C.byref(prm), p(copies), p(count), p(k_pool), p(v_pool), p(st), handle)
+        if rc != TV_OK:
+            raise TVError(rc, "tv_copy_pages_fp8" if fp8 else "tv_copy_pages")
+        return st
 
     return _run(dev, stream, call)

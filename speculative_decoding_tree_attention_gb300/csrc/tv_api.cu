@@ -835,3 +835,322 @@ int tv_penalize_logits(const tv_penalty_params* p, const void* logits,
   a.bf16 = p->logits_dtype == TV_OUT_BF16 ? 1 : 0;
   return tv::launch_penalty(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }
+
+namespace {
+
+// The bytes [p, p + n) and [q, q + m) have some in common.
+bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n && m && a < b + m && b < a + n;
+}
+
+// Rows of `row` elements, `stride` apart.
+struct RowSpan {
+  const uint16_t* p;
+  int64_t row, stride;
+};
+// Some element of `rows` rows of x lies in one of y.  Rows of one stride that
+// interleave (the slices of a fused projection) do not, if they miss each other
+// within a stride.
+bool rows_overlap(const RowSpan& x, const RowSpan& y, int64_t rows) {
+  const uint64_t n = static_cast<uint64_t>((rows - 1) * x.stride + x.row) * 2;
+  const uint64_t m = static_cast<uint64_t>((rows - 1) * y.stride + y.row) * 2;
+  if (!overlap(x.p, n, y.p, m)) return false;
+  if (x.stride != y.stride) return true;
+  const int64_t bytes = reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p);
+  if (bytes % 2) return true;
+  const int64_t apart = ((bytes / 2) % x.stride + x.stride) % x.stride;
+  return apart < x.row || apart + y.row > x.stride;
+}
+
+}  // namespace
+
+int tv_rotate_qk(const tv_rotate_params* p, const uint16_t* q, const uint16_t* k,
+                 const void* q_weight, const void* k_weight, const int32_t* positions,
+                 const double* frequencies, uint16_t* q_out, uint16_t* k_out,
+                 cudaStream_t stream) {
+  if (!p) return TV_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
+  if (p->tokens < 0 || p->num_q_heads < 1 || p->num_kv_heads < 0) return TV_ERR_INVALID_ARG;
+  if (p->num_q_heads > (1 << 20) || p->num_kv_heads > (1 << 20)) return TV_ERR_INVALID_ARG;
+  const int64_t heads = static_cast<int64_t>(p->num_q_heads) + p->num_kv_heads;
+  if (p->tokens * heads >= (1ll << 40)) return TV_ERR_INVALID_ARG;
+  if (p->rotary_dim < 0 || p->rotary_dim > p->head_dim || p->rotary_dim % 2) return TV_ERR_INVALID_ARG;
+  if (p->interleaved != 0 && p->interleaved != 1) return TV_ERR_INVALID_ARG;
+  if (p->num_axes < 1 || p->num_axes > TV_MAX_POSITION_AXES) return TV_ERR_INVALID_ARG;
+  if (p->weight_dtype != TV_OUT_BF16 && p->weight_dtype != TV_OUT_FP32) return TV_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.0f && p->eps <= FLT_MAX) || !(p->scale >= 0.0f && p->scale <= FLT_MAX)) return TV_ERR_INVALID_ARG;
+  for (int i = 0; i < p->rotary_dim / 2; ++i)
+    if (p->axis_of_pair[i] >= p->num_axes) return TV_ERR_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
+  const int64_t k_row = static_cast<int64_t>(p->num_kv_heads) * p->head_dim;
+  const int64_t strides[4] = {p->q_stride ? p->q_stride : q_row, p->k_stride ? p->k_stride : k_row,
+                              p->q_out_stride ? p->q_out_stride : q_row, p->k_out_stride ? p->k_out_stride : k_row};
+  for (int i = 0; i < 4; ++i)
+    if (strides[i] < (i % 2 ? k_row : q_row) || strides[i] >= (1ll << 38) || strides[i] % 8) return TV_ERR_INVALID_ARG;
+  if (p->tokens == 0) return TV_OK;
+  const bool keys = p->num_kv_heads > 0;
+  if (!q || !q_out || (keys && (!k || !k_out))) return TV_ERR_INVALID_ARG;
+  if (p->rotary_dim > 0 && (!positions || !frequencies)) return TV_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, q_weight, k_weight, positions, frequencies, q_out, k_out};
+  for (const void* x : ptrs)
+    if (!aligned16(x)) return TV_ERR_INVALID_ARG;
+  const RowSpan qs{q, q_row, strides[0]}, ks{k, k_row, strides[1]}, qo{q_out, q_row, strides[2]}, ko{k_out, k_row, strides[3]};
+  const bool q_here = q == q_out && strides[0] == strides[2], k_here = k == k_out && strides[1] == strides[3];
+  if (!q_here && rows_overlap(qs, qo, p->tokens)) return TV_ERR_INVALID_ARG;
+  if (keys && ((!k_here && rows_overlap(ks, ko, p->tokens)) || rows_overlap(qo, ko, p->tokens) ||
+               rows_overlap(qs, ko, p->tokens) || rows_overlap(ks, qo, p->tokens)))
+    return TV_ERR_INVALID_ARG;
+  tv::RotateArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.q = q;
+  a.k = k;
+  a.q_weight = q_weight;
+  a.k_weight = keys ? k_weight : nullptr;
+  a.positions = positions;
+  a.frequencies = frequencies;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_stride = static_cast<size_t>(strides[0]);
+  a.k_stride = static_cast<size_t>(strides[1]);
+  a.q_out_stride = static_cast<size_t>(strides[2]);
+  a.k_out_stride = static_cast<size_t>(strides[3]);
+  a.tokens = p->tokens;
+  a.hq = p->num_q_heads;
+  a.hkv = p->num_kv_heads;
+  a.head_dim = p->head_dim;
+  a.rotary_dim = p->rotary_dim;
+  a.interleaved = p->interleaved;
+  a.weight_fp32 = p->weight_dtype == TV_OUT_FP32 ? 1 : 0;
+  a.eps = p->eps;
+  a.scale = p->scale > 0.0f ? p->scale : 1.0f;
+  std::memcpy(a.axis, p->axis_of_pair, sizeof a.axis);
+  return tv::launch_rotate(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+namespace {
+
+bool beam_valid(const tv_beam_params* p) {
+  if (!p || p->batch < 1 || p->batch > 65535 || p->vocab < 1 || p->vocab >= (1 << 18)) return false;
+  if (p->beams < 1 || p->beams > tv::beam_max_beams() || p->select < 1 || p->select > tv::beam_max_select()) return false;
+  if (p->logits_dtype != TV_OUT_BF16 && p->logits_dtype != TV_OUT_FP32) return false;
+  if (p->end_token < -1 || p->end_token >= p->vocab) return false;
+  if (!(p->length_penalty >= -4.0f && p->length_penalty <= 4.0f)) return false;  // NaN fails too
+  return p->logits_stride == 0 || (p->logits_stride >= p->vocab && p->logits_stride < (1ll << 38));
+}
+
+// Bytes of the parts' maxima and sums, rounded to whole 256.
+size_t beam_stats_bytes(const tv_beam_params* p) {
+  return (static_cast<size_t>(p->batch) * p->beams * tv::beam_parts(p->vocab) * 8 + 255) / 256 * 256;
+}
+
+}  // namespace
+
+size_t tv_beam_select_workspace_size(const tv_beam_params* p) {
+  if (!beam_valid(p)) return 0;
+  return beam_stats_bytes(p) + static_cast<size_t>(p->batch) * p->beams * tv::beam_parts(p->vocab) * p->select * 8;
+}
+
+int tv_beam_select(const tv_beam_params* p, const void* logits, const float* scores,
+                   const int32_t* lengths, const int32_t* finished, int32_t* tokens,
+                   int32_t* parents, float* scores_out, int32_t* lengths_out,
+                   int32_t* finished_out, int32_t* status, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream) {
+  if (!beam_valid(p)) return TV_ERR_INVALID_ARG;
+  const void* ptrs[] = {logits, scores, tokens, parents, scores_out, status};
+  for (const void* x : ptrs)
+    if (!x || !aligned16(x)) return TV_ERR_INVALID_ARG;
+  const void* optional[] = {lengths, finished, lengths_out, finished_out};
+  for (const void* x : optional)
+    if (!aligned16(x)) return TV_ERR_INVALID_ARG;
+  if (!lengths && (lengths_out || p->length_penalty != 0.0f)) return TV_ERR_INVALID_ARG;
+  // (a request's merge reads these while another's writes)
+  const uint64_t in = static_cast<uint64_t>(p->batch) * p->beams * 4, out = static_cast<uint64_t>(p->batch) * p->select * 4;
+  const void* outs[] = {tokens, parents, scores_out, lengths_out, finished_out};
+  const void* ins[] = {scores, lengths, finished};
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o && i && overlap(o, out, i, in)) return TV_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < tv_beam_select_workspace_size(p) || !aligned16(workspace))
+    return TV_ERR_WORKSPACE;
+  tv::BeamArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.logits = logits;
+  a.scores = scores;
+  a.lengths = lengths;
+  a.finished = finished;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.scores_out = scores_out;
+  a.lengths_out = lengths_out;
+  a.finished_out = finished_out;
+  a.status = status;
+  a.stats = static_cast<float2*>(workspace);
+  a.lists = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + beam_stats_bytes(p));
+  a.stride = static_cast<size_t>(p->logits_stride ? p->logits_stride : p->vocab);
+  a.batch = p->batch;
+  a.beams = p->beams;
+  a.select = p->select;
+  a.vocab = p->vocab;
+  a.bf16 = p->logits_dtype == TV_OUT_BF16 ? 1 : 0;
+  a.end_token = p->end_token;
+  a.parts = tv::beam_parts(p->vocab);
+  // equal parts, of whole 16-byte words of either type
+  a.chunk = ((p->vocab + a.parts - 1) / a.parts + 7) / 8 * 8;
+  a.length_penalty = p->length_penalty;
+  return tv::launch_beam_select(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+namespace {
+
+bool pages_valid(const tv_page_params* p) {
+  return p && p->rows >= 1 && p->rows <= 65536 && p->block_size == TV_BLOCK_SIZE && p->max_blocks_per_seq >= 1 &&
+         p->num_blocks >= 1 && p->num_blocks <= (1 << 30);
+}
+
+tv::PageArgs page_args(const tv_page_params* p, const int32_t* block_table, const int32_t* ref_counts, int32_t* status) {
+  tv::PageArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.block_table = const_cast<int32_t*>(block_table);
+  a.ref_counts = const_cast<int32_t*>(ref_counts);
+  a.status = status;
+  a.rows = p->rows;
+  a.new_rows = p->new_rows;
+  a.width = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  return a;
+}
+
+// (free pages in order, then the first child of every row)
+size_t page_list_bytes(const tv_page_params* p) { return (static_cast<size_t>(p->num_blocks) * 4 + 255) / 256 * 256; }
+
+template <size_t N>
+bool all_given(const void* const (&ptrs)[N]) {
+  for (const void* x : ptrs)
+    if (!x || !aligned16(x)) return false;
+  return true;
+}
+
+}  // namespace
+
+size_t tv_pages_workspace_size(const tv_page_params* p) {
+  return pages_valid(p) ? page_list_bytes(p) + static_cast<size_t>(p->rows) * 4 : 0;
+}
+
+int tv_alloc_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_counts,
+                   const int32_t* begin, const int32_t* end, int32_t* status, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream) {
+  if (!pages_valid(p)) return TV_ERR_INVALID_ARG;
+  if (!all_given({block_table, ref_counts, end, status}) || !aligned16(begin)) return TV_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
+  tv::PageArgs a = page_args(p, block_table, ref_counts, status);
+  a.begin = begin;
+  a.end = end;
+  a.list = static_cast<int32_t*>(workspace);
+  return tv::launch_alloc_pages(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+int tv_free_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_counts,
+                  const int32_t* keep_begin, const int32_t* keep_end, int32_t* status,
+                  cudaStream_t stream) {
+  if (!pages_valid(p) || p->sinks < 0) return TV_ERR_INVALID_ARG;
+  if (!all_given({block_table, ref_counts, status}) || !aligned16(keep_begin) || !aligned16(keep_end))
+    return TV_ERR_INVALID_ARG;
+  tv::PageArgs a = page_args(p, block_table, ref_counts, status);
+  a.keep_begin = keep_begin;
+  a.keep_end = keep_end;
+  a.sinks = p->sinks;
+  return tv::launch_free_pages(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+int tv_fork_pages(const tv_page_params* p, const int32_t* block_table,
+                  const int32_t* seq_lens, const int32_t* parents, int32_t* ref_counts,
+                  int32_t* block_table_out, int32_t* seq_lens_out, int32_t* copies,
+                  int32_t* status, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream) {
+  if (!pages_valid(p) || p->new_rows < 1 || p->new_rows > 65536) return TV_ERR_INVALID_ARG;
+  if (!all_given({block_table, seq_lens, parents, ref_counts, block_table_out, seq_lens_out, copies, status}))
+    return TV_ERR_INVALID_ARG;
+  const uint64_t row = static_cast<uint64_t>(p->max_blocks_per_seq) * 4;
+  if (overlap(block_table, p->rows * row, block_table_out, p->new_rows * row) ||
+      overlap(seq_lens, p->rows * 4ull, seq_lens_out, p->new_rows * 4ull) ||
+      overlap(parents, p->new_rows * 4ull, seq_lens_out, p->new_rows * 4ull))
+    return TV_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
+  tv::PageArgs a = page_args(p, block_table, ref_counts, status);
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.table_out = block_table_out;
+  a.lens_out = seq_lens_out;
+  a.copies = copies;
+  a.list = static_cast<int32_t*>(workspace);
+  a.first = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + page_list_bytes(p));
+  return tv::launch_fork_pages(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+int tv_compact_pages(const tv_page_params* p, const int32_t* block_table,
+                     const int32_t* ref_counts, int32_t* block_table_out,
+                     int32_t* ref_counts_out, int32_t* page_map, int32_t* moves,
+                     int32_t* count, int32_t* status, cudaStream_t stream) {
+  if (!pages_valid(p)) return TV_ERR_INVALID_ARG;
+  if (!all_given({block_table, ref_counts, block_table_out, ref_counts_out, page_map, moves, count, status}))
+    return TV_ERR_INVALID_ARG;
+  const uint64_t table = static_cast<uint64_t>(p->rows) * p->max_blocks_per_seq * 4, pages = p->num_blocks * 4ull;
+  if (block_table != block_table_out && overlap(block_table, table, block_table_out, table)) return TV_ERR_INVALID_ARG;
+  if (ref_counts != ref_counts_out && overlap(ref_counts, pages, ref_counts_out, pages)) return TV_ERR_INVALID_ARG;
+  if (overlap(page_map, pages, ref_counts, pages) || overlap(page_map, pages, ref_counts_out, pages)) return TV_ERR_INVALID_ARG;
+  tv::PageArgs a = page_args(p, block_table, ref_counts, status);
+  a.table_out = block_table_out;
+  a.refs_out = ref_counts_out;
+  a.page_map = page_map;
+  a.copies = moves;
+  a.count = count;
+  return tv::launch_compact_pages(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+namespace {
+
+// The shared path of tv_copy_pages and tv_copy_pages_fp8 (scales given).
+int copy_call(const tv_copy_params* p, const int32_t* copies, const int32_t* count, bool fp8, void* k_pool,
+              float* k_scale, void* v_pool, float* v_scale, int32_t* status, cudaStream_t stream) {
+  if (!p) return TV_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
+  if (p->entries < 0 || p->layers < 1 || p->num_kv_heads < 1 || p->block_size != TV_BLOCK_SIZE || p->num_blocks < 1)
+    return TV_ERR_INVALID_ARG;
+  if (p->layers > (1 << 16) || p->num_kv_heads > (1 << 16) ||
+      static_cast<int64_t>(p->num_blocks) * p->num_kv_heads * 16 >= (1ll << 31))
+    return TV_ERR_INVALID_ARG;
+  if (p->entries == 0) return TV_OK;
+  if (!all_given({copies, k_pool, v_pool, status}) || reinterpret_cast<uintptr_t>(count) % 4) return TV_ERR_INVALID_ARG;
+  if (fp8 && !all_given({k_scale, v_scale})) return TV_ERR_INVALID_ARG;
+  tv::CopyArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.copies = copies;
+  a.count = count;
+  a.pool[0] = k_pool;
+  a.pool[1] = v_pool;
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.status = status;
+  a.row_bytes = p->head_dim * (fp8 ? 1 : 2);
+  a.scale_stride = static_cast<size_t>(p->num_blocks) * p->num_kv_heads * 16;
+  a.layer_stride = a.scale_stride * a.row_bytes;
+  a.entries = p->entries;
+  a.layers = p->layers;
+  a.num_blocks = p->num_blocks;
+  a.hkv = p->num_kv_heads;
+  return tv::launch_copy_pages(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // namespace
+
+int tv_copy_pages(const tv_copy_params* p, const int32_t* copies, const int32_t* count,
+                  uint16_t* k_pool, uint16_t* v_pool, int32_t* status, cudaStream_t stream) {
+  return copy_call(p, copies, count, false, k_pool, nullptr, v_pool, nullptr, status, stream);
+}
+
+int tv_copy_pages_fp8(const tv_copy_params* p, const int32_t* copies, const int32_t* count,
+                      uint8_t* k_pool, float* k_scale, uint8_t* v_pool, float* v_scale,
+                      int32_t* status, cudaStream_t stream) {
+  return copy_call(p, copies, count, true, k_pool, k_scale, v_pool, v_scale, status, stream);
+}

@@ -202,4 +202,86 @@ struct PenaltyArgs {
 };
 int launch_penalty(const PenaltyArgs& a, int sms, cudaStream_t stream);
 
+constexpr int kMaxAxes = 4;
+constexpr int kMaxPairs = 64;  // of a head of 128
+
+// Norm of every head and rotation by the position.
+struct RotateArgs {
+  const uint16_t* q;          // bf16 [tokens][Hq][D], rows q_stride elements apart
+  const uint16_t* k;          // [tokens][Hkv][D]
+  const void* q_weight;       // [D] bf16 or fp32, or null: no norm
+  const void* k_weight;
+  const int32_t* positions;   // [axes][tokens]
+  const double* frequencies;  // [rotary_dim / 2] radians a position
+  uint16_t* q_out;
+  uint16_t* k_out;
+  size_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int32_t tokens, hq, hkv, head_dim, rotary_dim;
+  int32_t interleaved;        // pairs (2i, 2i + 1), else (i, i + rotary_dim / 2)
+  int32_t weight_fp32;
+  float eps, scale;
+  int32_t items;              // warps that share a token (set by the launcher)
+  uint8_t axis[kMaxPairs];    // position axis of each pair
+};
+int launch_rotate(RotateArgs a, int sms, cudaStream_t stream);
+
+struct BeamArgs {
+  const void* logits;         // [batch * beams][vocab], rows `stride` entries apart
+  const float* scores;        // [batch * beams]
+  const int32_t* lengths;     // [batch * beams] or null
+  const int32_t* finished;    // [batch * beams] or null
+  int32_t* tokens;            // [batch][select]
+  int32_t* parents;
+  float* scores_out;
+  int32_t* lengths_out;       // or null
+  int32_t* finished_out;      // or null
+  int32_t* status;            // [batch]
+  float2* stats;              // [batch * beams][parts] maximum and sum (workspace)
+  float2* lists;              // [batch][select][beams][parts] logit and token, best first
+  size_t stride;
+  int32_t batch, beams, select, vocab, bf16, end_token, parts, chunk;
+  float length_penalty;
+};
+int launch_beam_select(const BeamArgs& a, cudaStream_t stream);
+int beam_parts(int vocab);
+int beam_max_select();
+int beam_max_beams();
+int beam_part_entries();  // the most entries of a part
+
+struct PageArgs {
+  int32_t* block_table;       // [rows][width]
+  int32_t* ref_counts;        // [num_blocks]
+  const int32_t* begin;       // alloc: [rows] first positions that need a page, or null
+  const int32_t* end;         // alloc: [rows] their ends
+  const int32_t* keep_begin;  // free: [rows] or null
+  const int32_t* keep_end;    // free: [rows] or null
+  const int32_t* seq_lens;    // fork: [rows]
+  const int32_t* parents;     // fork: [new_rows]
+  int32_t* table_out;         // fork: [new_rows][width], compact: [rows][width]
+  int32_t* lens_out;          // fork: [new_rows]
+  int32_t* copies;            // fork: [new_rows][3], compact: [num_blocks / 2][3] (source, destination, tokens)
+  int32_t* refs_out;          // compact: [num_blocks]
+  int32_t* page_map;          // compact: [num_blocks]
+  int32_t* count;             // compact: [2] pages in use, moves
+  int32_t* status;            // [rows], fork: [new_rows]
+  int32_t* list;              // workspace: free pages in order
+  int32_t* first;             // workspace: fork: [rows] first child of a row
+  int32_t rows, new_rows, width, num_blocks, sinks;
+};
+int launch_alloc_pages(const PageArgs& a, cudaStream_t stream);
+int launch_free_pages(const PageArgs& a, cudaStream_t stream);
+int launch_fork_pages(const PageArgs& a, cudaStream_t stream);
+int launch_compact_pages(const PageArgs& a, cudaStream_t stream);
+
+struct CopyArgs {
+  const int32_t* copies;      // [entries][3] source, destination, tokens
+  const int32_t* count;       // [1] or null: all entries
+  void* pool[2];              // K, V: [layers][num_blocks][Hkv][16][D]
+  float* scale[2];            // E4M3: [layers][num_blocks][Hkv][16], else null
+  int32_t* status;            // [entries]
+  size_t layer_stride, scale_stride;  // bytes between layers, values between layers of the scales
+  int32_t entries, layers, num_blocks, hkv, row_bytes;
+};
+int launch_copy_pages(const CopyArgs& a, int sms, cudaStream_t stream);
+
 }  // namespace tv
