@@ -740,17 +740,19 @@ typedef struct {
   int64_t logits_stride; /* entries between the rows of logits, 0 => V         */
 } tv_beam_params;        /* host struct */
 
-/* Bytes of device workspace (0 if the parameters are invalid): of each part of a
- * row (at most 8184 entries) its maximum, sum and S best.  Contents need no
- * initialisation; calls that overlap on the GPU need distinct workspaces. */
+/* Bytes of device workspace for these parameters on the current device (0 if they
+ * are invalid): of each part of a row (at most 64) its maximum, sum and S best, of
+ * each row a factor.
+ * Contents need no initialisation; calls that overlap on the GPU need distinct
+ * workspaces. */
 size_t tv_beam_select_workspace_size(const tv_beam_params* params);
 
 /* Layouts: logits bf16 or fp32 [B*K][V] (rows logits_stride apart); scores fp32
  * [B*K]; lengths, finished int32 [B*K] or NULL (lengths may be NULL only with
  * length_penalty 0 and lengths_out NULL); tokens, parents int32 [B][S]; scores_out
  * fp32 [B][S]; lengths_out, finished_out int32 [B][S] or NULL; status int32 [B].
- * scores_out, lengths_out and finished_out do not overlap the arrays that they
- * follow.  Device pointers 16-byte aligned. */
+ * Outputs that overlap scores, lengths, finished or each other are refused.  Device
+ * pointers 16-byte aligned. */
 int tv_beam_select(const tv_beam_params* params, const void* logits, const float* scores,
                    const int32_t* lengths, const int32_t* finished, int32_t* tokens,
                    int32_t* parents, float* scores_out, int32_t* lengths_out,
@@ -768,7 +770,9 @@ int tv_beam_select(const tv_beam_params* params, const void* logits, const float
  * the calls keep it so.  Where it is not, no call reads or writes out of range, and
  * that is all.  An entry >= num_blocks names nothing.
  * Pages are given lowest number first, to rows in order: the same tables and
- * counts give the same result.  Calls on the same counts must not overlap.
+ * counts give the same result.  Calls on the same counts must not overlap on the
+ * GPU.  Arrays of a call that overlap are refused (TV_ERR_INVALID_ARG) but for the
+ * two that tv_compact_pages names.
  * ====================================================================== */
 typedef struct {
   int32_t rows;               /* 1 <= R <= 65536 rows of block_table           */
@@ -841,8 +845,7 @@ int tv_fork_pages(const tv_page_params* params, const int32_t* block_table,
  * the caller holds); ref_counts_out and block_table_out are the counts and tables
  * in new numbers.  status[b]: TV_OK; TV_ERR_BAD_TREE if an entry of the row names a
  * free page or is >= num_blocks (it becomes -1).
- * ref_counts_out may be ref_counts, and block_table_out block_table; no other two
- * arrays overlap.  moves int32 [max(1, num_blocks / 2)][3] (entries from count[1] on
+ * ref_counts_out may be ref_counts, and block_table_out block_table.  moves int32 [max(1, num_blocks / 2)][3] (entries from count[1] on
  * are left as they were), count int32 [2], page_map int32 [num_blocks].  Device
  * pointers 16-byte aligned. */
 int tv_compact_pages(const tv_page_params* params, const int32_t* block_table,

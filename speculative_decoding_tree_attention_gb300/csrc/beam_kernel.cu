@@ -7,14 +7,18 @@
 // an ended beam offers itself once, at s_r.  Candidates are ordered by
 // key = d / max(len, 1)^alpha, then the lower beam, then the lower token.
 //
-// One pass over the logits.  beam_rows_kernel: a CTA takes a part of a row (at
-// most 8184 entries, 32 a thread, which stay in registers), and finds the part's
-// maximum, its sum and its S best entries.  Those are found without sorting: if
-// of W warps each has c threads whose largest entry is at least t, and W c >= S,
-// no entry below t is among the S best.  So t is the least over the warps of
-// their c-th largest thread maximum; the entries from t on, a few more than S, go
-// to shared memory and are ranked by counting.  Within a row the order is exact:
-// it is that of the logits.
+// One pass over the logits.  beam_rows_kernel: a warp takes a part of a row, four
+// 16-byte words a lane at a time.  Each lane keeps a running maximum and the sum of
+// exps against it.  Entries from a bound on go to the warp's list in shared memory.
+// The bound: if of W warps each has c lanes whose largest entry so far is at least
+// t, and W c >= S, S entries of the row at least are no worse than t; the 8 warps of
+// a CTA, which work on one row, take the least of their c-th largest.  So after the
+// first words the bound is near the S-th best of what eight warps have seen, and few
+// entries pass it: most words cost their exps, a packed maximum and one comparison.
+// (A bound of the warp's own let 22 entries of the first words pass it and took
+// 62 us instead of .. below.)  Bounds rise with time and differ from run to run, the
+// S best do not: they pass every bound.  Within a row the order is exact: it is that
+// of the logits, and of equal ones the lower token.
 //
 // beam_merge_kernel: a CTA per request joins the parts of each row to its LSE
 // and picks the S best of all rows' lists the same way: in fp32 with an error
@@ -28,6 +32,7 @@
 //
 // Bound: HBM, one read of the logits; for few requests the latency of two
 // dependent kernels.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -39,12 +44,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPart = 8192;          // entries that a CTA's threads hold
 constexpr int kMaxSelect = 64;
 constexpr int kMaxBeams = 64;
-constexpr int kMaxParts = 33;        // of a row of 2^18 - 1 entries
+constexpr int kMaxParts = 64;        // of a row
 constexpr int kMaxLength = 1 << 24;
-constexpr int kFound = 1024;         // candidates that are ranked by counting
+constexpr int kWords = 4;            // 16-byte words that a lane has in flight
+constexpr int kList = 2 * kMaxSelect + 16 + 32 * 8;  // entries of a warp's list: a word of every lane past its limit
+constexpr int kFound = 1024;         // candidates that the merge ranks by counting
 constexpr int kHeld = 8;             // candidates that a thread of the merge holds
 
 // A float's place in the order of values (all NaN aside), as a signed integer.
@@ -67,162 +73,326 @@ __device__ __forceinline__ float nth_largest(float mine, int n, float& top) {
   return of_ordered(best);
 }
 
-struct PartSmem {
-  float top[kWarps], nth[kWarps], sum[kWarps];
-  float value[kFound];
-  int index[kFound];
-  unsigned long long best[2];
-  int found;
+// A warp's list: entries above its bound.
+struct List {
+  float value[kList];   // -inf: taken
+  int index[kList];
+  float2 best[kMaxSelect];
+  int count;
 };
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 3) beam_rows_kernel(const BeamArgs a) {
-  constexpr int kEach = BF16 ? 8 : 4;            // entries of 16 bytes
-  constexpr int kLoads = kPart / kThreads / kEach;
-  __shared__ PartSmem s;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int part = blockIdx.x % a.parts, row = blockIdx.x / a.parts;
-  if (a.finished && a.finished[row] != 0) return;
-  if (!(a.scores[row] > -INFINITY)) return;      // (nothing, or NaN: the merge sees it)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c0 = part * a.chunk, c1 = min(c0 + a.chunk, a.vocab);
-  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + static_cast<size_t>(row) * a.stride * (16 / kEach);
-  // whole 16-byte words, from the one that holds entry c0 on
-  const int before = static_cast<int>((reinterpret_cast<uintptr_t>(base + static_cast<size_t>(c0) * (16 / kEach)) & 15) / (16 / kEach));
-  const int start = c0 - before;
-  const uint32_t none = BF16 ? 0xff80ff80u : 0xff800000u;
-  uint4 w[kLoads];
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int e = start + (tid + j * kThreads) * kEach;
-    w[j] = make_uint4(none, none, none, none);
-    if (e >= c0 && e + kEach <= c1) {
-      w[j] = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<size_t>(e) * (16 / kEach)));
-    } else if (e + kEach > c0 && e < c1) {
-      uint32_t x[4] = {none, none, none, none};
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (e + i < c0 || e + i >= c1) continue;
-        if (BF16) {
-          const uint32_t v = reinterpret_cast<const uint16_t*>(base)[e + i];
-          x[i / 2] = i % 2 ? (x[i / 2] & 0xffffu) | v << 16 : (x[i / 2] & 0xffff0000u) | v;
-        } else {
-          x[i % 4] = reinterpret_cast<const uint32_t*>(base)[e + i];
-        }
-      }
-      w[j] = make_uint4(x[0], x[1], x[2], x[3]);
+// Keeps the best n of the list's `count` entries, in order, in l.best and at the
+// list's front; returns how many there are.
+__device__ int keep_best(List& l, int count, int n) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (count <= 64) {  // each entry's rank by counting
+    for (int j = lane; j < count; j += 32) {
+      const float x = l.value[j];
+      const int k = l.index[j];
+      int rank = 0;
+#pragma unroll 4
+      for (int o = 0; o < count; ++o) rank += l.value[o] > x || (l.value[o] == x && l.index[o] < k);
+      if (rank < n) l.best[rank] = make_float2(x, __int_as_float(k));
+    }
+    const int kept = min(count, n);
+    __syncwarp();
+    for (int j = lane; j < kept; j += 32) {
+      l.value[j] = l.best[j].x;
+      l.index[j] = __float_as_int(l.best[j].y);
+    }
+    __syncwarp();
+    return kept;
+  }
+  float v = -INFINITY;
+  int i = INT_MAX, slot = 0;
+  const auto scan = [&] {
+    v = -INFINITY, i = INT_MAX;
+    for (int j = lane; j < count; j += 32) {
+      const float x = l.value[j];
+      const int k = l.index[j];
+      if (x > v || (x == v && k < i)) v = x, i = k, slot = j;
+    }
+  };
+  scan();
+  int kept = 0;
+  for (; kept < n; ++kept) {
+    const int key = ordered(v), top = __reduce_max_sync(0xffffffffu, key);
+    if (top == ordered(-INFINITY)) break;
+    const int first = __reduce_min_sync(0xffffffffu, key == top ? i : INT_MAX);
+    if (key == top && i == first) {
+      l.best[kept] = make_float2(v, __int_as_float(i));
+      l.value[slot] = -INFINITY;
+      scan();
     }
   }
-  // entry i of word j; NaN counts as -inf
-  const auto entry = [&](int j, int i) {
-    const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-    const float v = BF16 ? __uint_as_float(i % 2 ? x[i / 2] & 0xffff0000u : x[i / 2] << 16) : __uint_as_float(x[i % 4]);
-    return fmaxf(v, -INFINITY);
-  };
-  float mine = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) mine = fmaxf(mine, entry(j, i));
-  // warps whose threads all hold entries, and how many maxima each gives
-  const int full = min(kThreads, (c1 - start + kEach - 1) / kEach) / 32;
-  const int give = full > 0 && a.select <= 32 * full ? (a.select + full - 1) / full : 0;
-  float top;
-  const float nth = nth_largest(mine, give > 0 ? give : 1, top);
-  if (lane == 0) {
-    s.top[warp] = top;
-    s.nth[warp] = nth;
+  __syncwarp();
+  for (int j = lane; j < kept; j += 32) {
+    l.value[j] = l.best[j].x;
+    l.index[j] = __float_as_int(l.best[j].y);
   }
-  if (tid == 0) s.found = 0;
-  __syncthreads();
-  float m = s.top[0], t = INFINITY;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    m = fmaxf(m, s.top[i]);
-    if (i < full) t = fminf(t, s.nth[i]);
-  }
-  if (give == 0) t = -INFINITY;
-  const size_t lists = static_cast<size_t>(a.beams) * a.parts;
-  float2* list = a.lists + static_cast<size_t>(row / a.beams) * a.select * lists +
-                 static_cast<size_t>(row % a.beams) * a.parts + part;
-  // exp(x - m), 2^(d hi + d lo) with d = x - m; (lo > 0: -inf stays so)
-  const float hi = 1.44269502162933349609f, lo = 1.92596298e-8f;
-  const float ref = isinf(m) ? 0.0f : m;  // (nothing, or a +inf that the merge refuses)
-  float sum = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    float some = 0.0f;
+  __syncwarp();
+  return kept;
+}
+
+// A part of a row: entries [c0, c1) from `base` on, in 16-byte words, the first of
+// which holds entry c0.
+template <bool BF16>
+struct Part {
+  static constexpr int kEach = BF16 ? 8 : 4;  // entries of a word
+  const uint8_t* base;
+  int c0, c1, start;
+  __device__ __forceinline__ int entry_of(int word) const { return start + word * kEach; }
+  // a word; entries outside of the part -inf
+  __device__ __forceinline__ uint4 load(int word) const {
+    const uint32_t none = BF16 ? 0xff80ff80u : 0xff800000u;
+    const int e = entry_of(word);
+    if (e >= c0 && e + kEach <= c1) return __ldcs(reinterpret_cast<const uint4*>(base + static_cast<long long>(e) * (16 / kEach)));
+    uint32_t x[4] = {none, none, none, none};
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const float d = entry(j, i) - ref;
-      some += ex2_approx(fmaf(d, hi, d * lo));
+      if (e + i < c0 || e + i >= c1) continue;
+      if (BF16) {
+        const uint32_t v = reinterpret_cast<const uint16_t*>(base)[e + i];
+        x[i / 2] = i % 2 ? (x[i / 2] & 0xffffu) | v << 16 : (x[i / 2] & 0xffff0000u) | v;
+      } else {
+        x[i % 4] = reinterpret_cast<const uint32_t*>(base)[e + i];
+      }
     }
-    sum += some;
+    return make_uint4(x[0], x[1], x[2], x[3]);
   }
-  if (mine >= t) {
+};
+// A word's values, two by two.
+template <bool BF16>
+__device__ __forceinline__ void values_of(const uint4& w, float2 (&v)[BF16 ? 4 : 2]) {
+  if constexpr (BF16) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u));
+  } else {
+    v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+}
+// NaN as -inf
+template <bool BF16>
+__device__ __forceinline__ uint4 without_nan(uint4 w) {
+  uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const float x = entry(j, i);
-        if (x >= t && x > -INFINITY) {
-          const int at = atomicAdd(&s.found, 1);
-          if (at < kFound) {
-            s.value[at] = x;
-            s.index[at] = start + (tid + j * kThreads) * kEach + i;
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      if ((x[i] & 0x7fffu) > 0x7f80u) x[i] = (x[i] & 0xffff0000u) | 0xff80u;
+      if ((x[i] & 0x7fff0000u) > 0x7f800000u) x[i] = (x[i] & 0xffffu) | 0xff800000u;
+    } else if ((x[i] & 0x7fffffffu) > 0x7f800000u) {
+      x[i] = 0xff800000u;
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// exp(d) for d = x - m <= 0 as 2^(d hi + d lo)   (lo > 0: -inf stays so)
+constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596298e-8f;
+__device__ __forceinline__ float exp_of(float d) { return ex2_approx(fmaf(d, kLog2eHi, d * kLog2eLo)); }
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The largest value of a word (of numbers and NaN, that of the numbers).
+template <bool BF16>
+__device__ __forceinline__ float top_of(const uint4& w) {
+  if constexpr (BF16) {
+    const uint32_t m = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+}
+
+// The four words of each lane from word w0 on.
+template <bool BF16>
+__device__ __forceinline__ void load_words(const Part<BF16>& p, int w0, uint4 (&w)[kWords]) {
+  const int lane = threadIdx.x & 31;
+  if (p.entry_of(w0) >= p.c0 && p.entry_of(w0 + 32 * kWords) <= p.c1) {
+    const uint4* at = reinterpret_cast<const uint4*>(p.base + static_cast<long long>(p.entry_of(w0 + lane)) * (16 / p.kEach));
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = __ldcs(at + j * 32);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = p.load(w0 + j * 32 + lane);
+  }
+}
+
+// What the warps of a CTA share: the c-th largest of the lanes' maxima of each
+// (+inf of warps without a part).
+struct Bounds {
+  float4 nth[kWarps / 4];
+  __device__ __forceinline__ float least() const {
+    static_assert(kWarps == 8, "two words");
+    const volatile float* v = &nth[0].x;
+    return fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
+  }
+};
+
+// A warp's pass over its part: the entries that may be among the row's best into l,
+// the part's maximum and the sum of exp(x - maximum).
+//
+// The sums are of 2^(x log2 e + c), c = -fl(m hi) with m the lane's maximum so far:
+// x hi + c is rounded once, near 0 where it counts, then x lo added.  Where a sum is
+// NaN (a NaN among the entries) or the maximum beyond 2^20 (a part that is masked by
+// the lowest value), the pass is done again (SAFE), without NaN and from x - m.
+template <bool BF16, bool SAFE>
+__device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warps, int select, float& m, float& sum) {
+  constexpr int kPairs = BF16 ? 4 : 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach;
+  const int limit = 2 * select + 16, give = (select + warps - 1) / warps;
+  const float floor = SAFE ? -FLT_MAX : -0x1p126f;  // (not -inf: nothing minus nothing)
+  m = floor;
+  if (lane == 0) l.count = 0;
+  float t = -INFINITY, high = -INFINITY;
+  float c = -m * kLog2eHi;
+  float2 acc = make_float2(0.0f, 0.0f);
+  uint4 next[kWords];
+  load_words<BF16>(p, 0, next);
+  for (int w0 = 0, turn = 0; w0 < words; w0 += 32 * kWords, ++turn) {
+    uint4 w[kWords];
+    float g[kWords];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      w[j] = SAFE ? without_nan<BF16>(next[j]) : next[j];
+      g[j] = top_of<BF16>(w[j]);
+    }
+    if (w0 + 32 * kWords < words) load_words<BF16>(p, w0 + 32 * kWords, next);
+    const float top = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
+    high = fmaxf(high, top);
+    if (top > m) {
+      if (SAFE) {
+        const float f = exp_of(m - top);
+        acc.x *= f, acc.y *= f;
+      } else {
+        const float to = -top * kLog2eHi, f = ex2_approx(to - c);
+        acc.x *= f, acc.y *= f;
+        c = to;
+      }
+      m = top;
+    }
+    if ((turn & (turn + 1)) == 0) {  // (turns 0, 1, 3, 7, ..)
+      float unused;
+      const float nth = give <= 32 ? nth_largest(high, give, unused) : -INFINITY;
+      if (lane == 0) reinterpret_cast<volatile float*>(bounds)[warp] = nth;
+      if (!SAFE && turn == 0) __syncthreads();  // (nobody starts without a bound)
+    }
+    t = fmaxf(t, bounds->least());
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      float2 v[kPairs];
+      values_of<BF16>(w[j], v);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        float2 e;
+        if (SAFE) {
+          const float2 d = add2(v[i], make_float2(-m, -m));
+          e = fma2(d, make_float2(kLog2eHi, kLog2eHi), mul2(d, make_float2(kLog2eLo, kLog2eLo)));
+        } else {
+          e = fma2(v[i], make_float2(kLog2eLo, kLog2eLo), fma2(v[i], make_float2(kLog2eHi, kLog2eHi), make_float2(c, c)));
+        }
+        acc = add2(acc, make_float2(ex2_approx(e.x), ex2_approx(e.y)));
+      }
+    }
+    if (!__any_sync(0xffffffffu, top >= t)) continue;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      if (!__any_sync(0xffffffffu, g[j] >= t)) continue;
+      __syncwarp();
+      if (l.count > limit) {
+        const int kept = keep_best(l, l.count, select);
+        if (lane == 0) l.count = kept;
+        // (of equal ones the later token does not count)
+        if (kept == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1] + 0.0f) + 1));
+        __syncwarp();
+      }
+      if (g[j] >= t) {
+        float2 v[kPairs];
+        values_of<BF16>(w[j], v);
+        const int e = p.entry_of(w0 + j * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < 2 * kPairs; ++i) {
+          const float x = i % 2 ? v[i / 2].y : v[i / 2].x;
+          if (x >= t && x > -INFINITY) {
+            const int at = atomicAdd(&l.count, 1);
+            l.value[at] = x + 0.0f;  // (one zero)
+            l.index[at] = e + i;
           }
         }
       }
+    }
   }
+  sum = acc.x + acc.y;
+  const float all = of_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
+  const bool fails = __any_sync(0xffffffffu, sum != sum) || (!SAFE && !(fabsf(all) <= 0x1p20f));
+  if (!SAFE) {
+    // from 2^-c to exp(m): by 2^(-c - m log2 e), next to 1
+    const float y = -0.69314718f * fmaf(m, kLog2eLo, fmaf(m, kLog2eHi, c));
+    sum = fabsf(y) < 0x1p-8f ? fmaf(sum, fmaf(y * y, 0.5f, y), sum) : sum * expf(y);
+  }
+  // the lanes' sums against the warp's maximum
+  sum = m < all - 256.0f ? 0.0f : sum * exp_of(m - all);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s.sum[warp] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    float all = 0.0f;
-    for (int i = 0; i < kWarps; ++i) all += s.sum[i];
-    a.stats[static_cast<size_t>(row) * a.parts + part] = make_float2(m, all);
+  m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(high)));
+  if (m == -INFINITY) {  // nothing (but NaN)
+    sum = 0.0f;
+    return true;
   }
-  const int found = s.found;
-  if (found <= kFound) {
-    for (int i = tid; i < found; i += kThreads) {
-      const float x = s.value[i];
-      const int v = s.index[i];
-      int rank = 0;
-      for (int j = 0; j < found; ++j) rank += s.value[j] > x || (s.value[j] == x && s.index[j] < v);
-      if (rank < a.select) list[rank * lists] = make_float2(x, __int_as_float(v));
-    }
-    for (int i = found + tid; i < a.select; i += kThreads) list[i * lists] = make_float2(-INFINITY, __int_as_float(-1));
+  return !fails;
+}
+
+// CTAs behind those of the parts: 1 / len^alpha of a row per thread (its fp64 power
+// would stand in the merge's way).
+__device__ void row_inverses(const BeamArgs& a, int row) {
+  if (row >= a.batch * a.beams) return;
+  const bool ended = a.finished && a.finished[row] != 0;
+  const int len = max(min(a.lengths[row], kMaxLength) + (ended ? 0 : 1), 1);
+  a.inverse[row] = a.length_penalty == 1.0f ? 1.0 / len : pow(static_cast<double>(len), -static_cast<double>(a.length_penalty));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a) {
+  __shared__ List lists[kWarps];
+  __shared__ Bounds bounds;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ctas = (a.parts + kWarps - 1) / kWarps;  // of a row
+  const int row = blockIdx.x / ctas, first = (blockIdx.x - row * ctas) * kWarps, part = first + warp;
+  const int warps = min(kWarps, a.parts - first);
+  if (threadIdx.x < kWarps) reinterpret_cast<float*>(&bounds)[threadIdx.x] = static_cast<int>(threadIdx.x) < warps ? -INFINITY : INFINITY;
+  __syncthreads();
+  if (row >= a.batch * a.beams) {
+    row_inverses(a, (blockIdx.x - a.batch * a.beams * ctas) * kThreads + threadIdx.x);
     return;
   }
-  // so many equal entries: the best after the last one, S times
-  unsigned long long last = ~0ull;
-  if (tid < 2) s.best[tid] = 0;
-  __syncthreads();
-  for (int r = 0; r < a.select; ++r) {
-    unsigned long long best = 0;
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const float x = entry(j, i) + 0.0f;  // (one zero)
-        const uint32_t v = start + (tid + j * kThreads) * kEach + i;
-        const unsigned long long key =
-            static_cast<unsigned long long>(static_cast<uint32_t>(ordered(x)) ^ 0x80000000u) << 32 | (0xffffffffu - v);
-        if (x > -INFINITY && key < last && key > best) best = key;
-      }
-    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-    if (lane == 0) atomicMax(&s.best[r & 1], best);
-    __syncthreads();
-    last = s.best[r & 1];
-    __syncthreads();
-    if (tid == 0) {
-      s.best[r & 1] = 0;  // (used again two rounds on, past the next barrier)
-      const float x = of_ordered(static_cast<int>(static_cast<uint32_t>(last >> 32) ^ 0x80000000u));
-      list[r * lists] = last ? make_float2(x, __uint_as_float(0xffffffffu - static_cast<uint32_t>(last)))
-                             : make_float2(-INFINITY, __int_as_float(-1));
-    }
+  if (warp >= warps) return;
+  if (a.finished && a.finished[row] != 0) return;
+  if (!(a.scores[row] > -INFINITY)) return;      // (nothing, or NaN: the merge sees it)
+  Part<BF16> p;
+  p.base = static_cast<const uint8_t*>(a.logits) + static_cast<size_t>(row) * a.stride * (16 / p.kEach);
+  p.c0 = min(part * a.chunk, a.vocab), p.c1 = min(p.c0 + a.chunk, a.vocab);
+  p.start = p.c0 - static_cast<int>((reinterpret_cast<uintptr_t>(p.base + static_cast<size_t>(p.c0) * (16 / p.kEach)) & 15) / (16 / p.kEach));
+  List& l = lists[warp];
+  float m, sum;
+  if (!part_pass<BF16, false>(p, l, &bounds, warps, a.select, m, sum)) {
+    __syncwarp();
+    part_pass<BF16, true>(p, l, &bounds, warps, a.select, m, sum);
   }
+  if (lane == 0) a.stats[static_cast<size_t>(row) * a.parts + part] = make_float2(m, sum);
+  __syncwarp();
+  const int count = keep_best(l, l.count, a.select);
+  const size_t all = static_cast<size_t>(a.beams) * a.parts;
+  float2* list = a.lists + static_cast<size_t>(row / a.beams) * a.select * all + static_cast<size_t>(row % a.beams) * a.parts + part;
+  for (int i = lane; i < a.select; i += 32)
+    list[i * all] = i < count ? make_float2(l.value[i], __int_as_float(l.index[i])) : make_float2(-INFINITY, __int_as_float(-1));
 }
 
 enum State { kDead, kLive, kEnded };
@@ -256,76 +426,103 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   __shared__ MergeSmem s;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = a.beams, S = a.select;
-  if (tid == 0) s.bad = 0;
-  __syncthreads();
-  // (what the caller gave; the rows kernel's results only after the wait)
-  for (int k = tid; k < K; k += kThreads) {
-    const size_t row = static_cast<size_t>(b) * K + k;
-    const float score = a.scores[row];
-    const bool ended = a.finished && a.finished[row] != 0;
-    int len = a.lengths ? a.lengths[row] : 0;
-    if (!(score < INFINITY) || len < 0 || len > kMaxLength) s.bad = 1;
-    s.state[k] = !(score > -INFINITY) ? kDead : ended ? kEnded : kLive;
-    len = max(len + (ended ? 0 : 1), 1);
-    s.inverse[k] = a.length_penalty == 0.0f   ? 1.0
-                   : a.length_penalty == 1.0f ? 1.0 / len
-                                              : pow(static_cast<double>(len), -static_cast<double>(a.length_penalty));
-    s.base[k] = score;
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __syncthreads();
-  // LSE of each live row, a warp a row
-  for (int k = warp; k < K; k += kWarps) {
-    if (s.state[k] != kLive) continue;
-    const float2* part = a.stats + (static_cast<size_t>(b) * K + k) * a.parts;
-    float m = -INFINITY;
-    for (int p = lane; p < a.parts; p += 32) m = fmaxf(m, part[p].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float sum = 0.0f;
-    if (!isinf(m))
-      for (int p = lane; p < a.parts; p += 32) sum += part[p].y * expf(part[p].x - m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncwarp();
-    if (lane == 0) {
-      if (m == INFINITY) s.bad = 1;
-      if (isinf(m)) {
-        s.state[k] = kDead;
-      } else {
-        // log of sum = 2^e f with f in [1, 2)
-        const int e = (__float_as_int(sum) >> 23) - 127;
-        const float f = __int_as_float(__float_as_int(sum) - (e << 23));
-        s.base[k] -= static_cast<double>(m) + e * 0.69314718055994531 + static_cast<double>(logf(f));
-      }
-      s.approx[k] = make_float2(static_cast<float>(s.base[k]), static_cast<float>(s.inverse[k]));
-    }
-  }
-  __syncthreads();
-  const bool bad = s.bad != 0;
-  if (tid == 0) {
+  // what the caller gave, by warp 0 (the rows kernel's results only after the wait)
+  if (warp == 0) {
+    bool bad = false;
     int live = 0, ended = 0;
-    for (int k = 0; k < K; ++k) {
-      if (s.state[k] == kLive) s.live[live++] = k;
-      if (s.state[k] == kEnded) {  // its one candidate, at the lowest place of its beam
-        s.key[ended] = ordered_key(s.base[k] * s.inverse[k]);
-        s.value[ended] = 0.0f;
-        s.at[ended++] = k << 18;
+    for (int k0 = 0; k0 < K; k0 += 32) {
+      const int k = k0 + lane;
+      int state = kDead;
+      if (k < K) {
+        const size_t row = static_cast<size_t>(b) * K + k;
+        const float score = a.scores[row];
+        const int len = a.lengths ? a.lengths[row] : 0;
+        bad |= !(score < INFINITY) || len < 0 || len > kMaxLength;
+        if (score > -INFINITY) state = a.finished && a.finished[row] != 0 ? kEnded : kLive;
+        s.state[k] = state;
+        s.base[k] = score;
+        s.inverse[k] = 1.0;
       }
+      const unsigned lives = __ballot_sync(0xffffffffu, state == kLive), ends = __ballot_sync(0xffffffffu, state == kEnded);
+      const unsigned below = (1u << lane) - 1;
+      if (state == kLive) s.live[live + __popc(lives & below)] = k;
+      if (state == kEnded) s.at[ended + __popc(ends & below)] = k << 18;  // (one candidate, at the lowest place of its beam)
+      live += __popc(lives);
+      ended += __popc(ends);
     }
-    s.lives = bad ? 0 : live;
-    s.ended = s.found = bad ? 0 : ended;
-    a.status[b] = bad ? kBadTree : kOk;
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      s.lives = live;
+      s.ended = s.found = ended;
+      s.bad = bad;
+    }
   }
   __syncthreads();
   const int own = s.lives * a.parts, total = own * S;
   const size_t lists = static_cast<size_t>(K) * a.parts;
   const float2* all = a.lists + static_cast<size_t>(b) * S * lists;
+  // exact quotients of numbers below 2^18 by ones below 2^13
+  const uint32_t by_own = own > 1 ? 0xffffffffu / own + 1 : 0, by_parts = a.parts > 1 ? 0xffffffffu / a.parts + 1 : 0;
+  const auto over = [](int c, uint32_t by) { return by ? static_cast<int>(__umulhi(c, by)) : c; };
   // entry r of list q of the live beams, and the list's beam
-  const auto beam_of = [&](int q) { return s.live[q / a.parts]; };
+  const auto beam_of = [&](int q) { return s.live[over(q, by_parts)]; };
   const auto entry = [&](int q, int r) {
-    return all[r * lists + static_cast<size_t>(beam_of(q)) * a.parts + q % a.parts];
+    const int n = over(q, by_parts);
+    return all[r * lists + static_cast<size_t>(s.live[n]) * a.parts + (q - n * a.parts)];
   };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // A few candidates of each thread, rank by rank over the lists; the lists of a beam
+  // over all warps, whose bounds count alike below (in order, the warps with the
+  // worst beams' lists let 10 times as many candidates pass).
+  const int place = lane * kWarps + warp;
+  float2 held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int c = place + j * kThreads, r = over(c, by_own);
+    held[j] = c < total ? entry(c - r * own, r) : make_float2(-INFINITY, 0.0f);
+  }
+  // LSE of each live row, a warp a row
+  for (int n = warp; n < s.lives; n += kWarps) {
+    const int k = s.live[n];
+    const size_t row = static_cast<size_t>(b) * K + k;
+    const float2* part = a.stats + row * a.parts;
+    const float2 x = lane < a.parts ? part[lane] : make_float2(-INFINITY, 0.0f);
+    const float2 y = lane + 32 < a.parts ? part[lane + 32] : make_float2(-INFINITY, 0.0f);
+    const double inverse = a.length_penalty != 0.0f ? a.inverse[row] : 1.0;
+    const float m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(fmaxf(x.x, y.x))));
+    float sum = isinf(m) ? 0.0f : x.y * expf(x.x - m) + y.y * expf(y.x - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      if (m == INFINITY) s.bad = 1;
+      if (!isinf(m)) {  // (else all its candidates are -inf)
+        // log of sum = 2^e f with f in [1, 2)
+        const int e = (__float_as_int(sum) >> 23) - 127;
+        const float f = __int_as_float(__float_as_int(sum) - (e << 23));
+        s.base[k] -= static_cast<double>(m) + e * 0.69314718055994531 + static_cast<double>(logf(f));
+      }
+      s.inverse[k] = inverse;
+      s.approx[k] = make_float2(static_cast<float>(s.base[k]), static_cast<float>(inverse));
+    }
+  }
+  for (int i = tid; i < s.ended; i += kThreads) {
+    const int k = s.at[i] >> 18;
+    if (a.length_penalty != 0.0f) s.inverse[k] = a.inverse[static_cast<size_t>(b) * K + k];
+    s.key[i] = ordered_key(s.base[k] * s.inverse[k]);
+    s.value[i] = 0.0f;
+  }
+  __syncthreads();
+  if (tid == 0) a.status[b] = s.bad ? kBadTree : kOk;
+  if (s.bad) {
+    for (int i = tid; i < S; i += kThreads) {
+      const size_t o = static_cast<size_t>(b) * S + i;
+      a.tokens[o] = a.parents[o] = -1;
+      a.scores_out[o] = -INFINITY;
+      if (a.lengths_out) a.lengths_out[o] = 0;
+      if (a.finished_out) a.finished_out[o] = 0;
+    }
+    return;
+  }
   // a key in fp32, and how far that may be off
   const auto approx = [&](float x, int k, float& off) {
     const float2 p = s.approx[k];
@@ -341,42 +538,34 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
       s.at[at] = k << 18 | __float_as_int(e.y);
     }
   };
-  // A bound: S candidates at least are no worse.  From a few entries of each
-  // thread, rank by rank over the lists.
-  float2 held[kHeld];
+  // a bound: S candidates at least are no worse
   float top = -INFINITY, unused;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
-    const int c = tid + j * kThreads, r = own ? c / own : 0, q = c - r * own;
-    held[j] = make_float2(-INFINITY, 0.0f);
-    if (c < total) {
-      float off;
-      held[j] = entry(q, r);
-      const float v = approx(held[j].x, beam_of(q), off);
-      top = fmaxf(top, v - off);  // (NaN: none)
-    }
+    const int c = place + j * kThreads;
+    if (!(held[j].x > -INFINITY)) continue;
+    float off;
+    const float v = approx(held[j].x, beam_of(c - over(c, by_own) * own), off);
+    top = fmaxf(top, v - off);  // (NaN: none)
   }
   for (int q = kThreads * kHeld + tid; q < own; q += kThreads) {  // (more lists than that)
     float off;
     const float v = approx(entry(q, 0).x, beam_of(q), off);
     top = fmaxf(top, v - off);
   }
-  const int full = min(total, kThreads) / 32;
-  const int give = full > 0 && S <= 32 * full ? (S + full - 1) / full : 0;
-  const float nth = nth_largest(top, give > 0 ? give : 1, unused);
+  const int give = (S + kWarps - 1) / kWarps;
+  const float nth = nth_largest(top, give, unused);  // (-inf where a warp has not that many)
   if (lane == 0) s.nth[warp] = nth;
   __syncthreads();
-  float t = INFINITY;
+  float t = s.nth[0];
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i)
-    if (i < full) t = fminf(t, s.nth[i]);
-  if (give == 0) t = -INFINITY;
+  for (int i = 1; i < kWarps; ++i) t = fminf(t, s.nth[i]);
   if (total <= kThreads * kHeld) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      const int c = tid + j * kThreads;
+      const int c = place + j * kThreads;
       if (!(held[j].x > -INFINITY)) continue;
-      const int k = beam_of(c % own);
+      const int k = beam_of(c - over(c, by_own) * own);
       float off;
       const float v = approx(held[j].x, k, off);
       if (!(v + off < t)) keep(held[j], k);
@@ -425,6 +614,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
       const unsigned long long key = s.key[i];
       const int at = s.at[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < found; ++j) rank += better(s.key[j], s.at[j], key, at);
       if (rank < S) put(rank, s.value[i], at);
     }
@@ -477,17 +667,28 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
 
 }  // namespace
 
-int beam_parts(int vocab) { return (vocab + kPart - 8 - 1) / (kPart - 8); }
 int beam_max_select() { return kMaxSelect; }
 int beam_max_beams() { return kMaxBeams; }
-int beam_part_entries() { return kPart - 8; }
+
+// Parts of a row: whole CTAs, about six for every SM over all rows, so that the last
+// ones leave few SMs idle (with as many as are resident, 4, the busiest SM had a
+// sixth more than its share of 512 rows), of whole 512 entries at least.
+void plan_beam_parts(BeamArgs& a, int sms) {
+  const long long rows = static_cast<long long>(a.batch) * a.beams;
+  const long long most = min((a.vocab + 511) / 512, kMaxParts), want = (6ll * sms + rows - 1) / rows * kWarps;
+  const int parts = static_cast<int>(want < most ? want : most);
+  a.chunk = ((a.vocab + parts - 1) / parts + 511) / 512 * 512;
+  a.parts = (a.vocab + a.chunk - 1) / a.chunk;
+}
 
 int launch_beam_select(const BeamArgs& a, cudaStream_t stream) {
-  const unsigned rows = static_cast<unsigned>(a.batch) * a.beams * a.parts;
+  const long long rows = static_cast<long long>(a.batch) * a.beams;
+  const long long ctas = rows * ((a.parts + kWarps - 1) / kWarps) + (a.length_penalty != 0.0f ? (rows + kThreads - 1) / kThreads : 0);
+  const unsigned grid = static_cast<unsigned>(ctas);
   if (a.bf16) {
-    beam_rows_kernel<true><<<rows, kThreads, 0, stream>>>(a);
+    beam_rows_kernel<true><<<grid, kThreads, 0, stream>>>(a);
   } else {
-    beam_rows_kernel<false><<<rows, kThreads, 0, stream>>>(a);
+    beam_rows_kernel<false><<<grid, kThreads, 0, stream>>>(a);
   }
   if (cudaGetLastError() != cudaSuccess) return -1;
   // the merge's CTAs may start while the last rows are read; they wait for them

@@ -844,6 +844,22 @@ bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
   return n && m && a < b + m && b < a + n;
 }
 
+struct Span {
+  const void* p;
+  uint64_t bytes;
+};
+// Some output has bytes in common with an input or with another output.
+template <size_t N, size_t M>
+bool clash(const Span (&outs)[N], const Span (&ins)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (size_t j = i + 1; j < N; ++j)
+      if (outs[i].p && outs[j].p && overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+    for (size_t j = 0; j < M; ++j)
+      if (outs[i].p && ins[j].p && overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
+  }
+  return false;
+}
+
 // Rows of `row` elements, `stride` apart.
 struct RowSpan {
   const uint16_t* p;
@@ -939,16 +955,34 @@ bool beam_valid(const tv_beam_params* p) {
   return p->logits_stride == 0 || (p->logits_stride >= p->vocab && p->logits_stride < (1ll << 38));
 }
 
-// Bytes of the parts' maxima and sums, rounded to whole 256.
-size_t beam_stats_bytes(const tv_beam_params* p) {
-  return (static_cast<size_t>(p->batch) * p->beams * tv::beam_parts(p->vocab) * 8 + 255) / 256 * 256;
+// The sizes and parts of a call, and the bytes of its workspace: the parts' maxima
+// and sums and the rows' factors (whole 256 each), and all.
+tv::BeamArgs beam_args(const tv_beam_params* p, size_t* stats, size_t* factors, size_t* bytes) {
+  tv::BeamArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.stride = static_cast<size_t>(p->logits_stride ? p->logits_stride : p->vocab);
+  a.batch = p->batch;
+  a.beams = p->beams;
+  a.select = p->select;
+  a.vocab = p->vocab;
+  a.bf16 = p->logits_dtype == TV_OUT_BF16 ? 1 : 0;
+  a.end_token = p->end_token;
+  a.length_penalty = p->length_penalty;
+  tv::plan_beam_parts(a, sm_count());
+  const size_t parts = static_cast<size_t>(p->batch) * p->beams * a.parts;
+  *stats = (parts * 8 + 255) / 256 * 256;
+  *factors = (static_cast<size_t>(p->batch) * p->beams * 8 + 255) / 256 * 256;
+  *bytes = *stats + *factors + parts * p->select * 8;
+  return a;
 }
 
 }  // namespace
 
 size_t tv_beam_select_workspace_size(const tv_beam_params* p) {
   if (!beam_valid(p)) return 0;
-  return beam_stats_bytes(p) + static_cast<size_t>(p->batch) * p->beams * tv::beam_parts(p->vocab) * p->select * 8;
+  size_t stats, factors, bytes;
+  beam_args(p, &stats, &factors, &bytes);
+  return bytes;
 }
 
 int tv_beam_select(const tv_beam_params* p, const void* logits, const float* scores,
@@ -964,17 +998,14 @@ int tv_beam_select(const tv_beam_params* p, const void* logits, const float* sco
   for (const void* x : optional)
     if (!aligned16(x)) return TV_ERR_INVALID_ARG;
   if (!lengths && (lengths_out || p->length_penalty != 0.0f)) return TV_ERR_INVALID_ARG;
-  // (a request's merge reads these while another's writes)
+  // (a request's merge reads its input while another's writes)
   const uint64_t in = static_cast<uint64_t>(p->batch) * p->beams * 4, out = static_cast<uint64_t>(p->batch) * p->select * 4;
-  const void* outs[] = {tokens, parents, scores_out, lengths_out, finished_out};
-  const void* ins[] = {scores, lengths, finished};
-  for (const void* o : outs)
-    for (const void* i : ins)
-      if (o && i && overlap(o, out, i, in)) return TV_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < tv_beam_select_workspace_size(p) || !aligned16(workspace))
-    return TV_ERR_WORKSPACE;
-  tv::BeamArgs a;
-  std::memset(&a, 0, sizeof a);
+  if (clash({{tokens, out}, {parents, out}, {scores_out, out}, {lengths_out, out}, {finished_out, out}, {status, p->batch * 4ull}},
+            {{scores, in}, {lengths, in}, {finished, in}}))
+    return TV_ERR_INVALID_ARG;
+  size_t stats, factors, bytes;
+  tv::BeamArgs a = beam_args(p, &stats, &factors, &bytes);
+  if (!workspace || workspace_bytes < bytes || !aligned16(workspace)) return TV_ERR_WORKSPACE;
   a.logits = logits;
   a.scores = scores;
   a.lengths = lengths;
@@ -986,18 +1017,8 @@ int tv_beam_select(const tv_beam_params* p, const void* logits, const float* sco
   a.finished_out = finished_out;
   a.status = status;
   a.stats = static_cast<float2*>(workspace);
-  a.lists = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + beam_stats_bytes(p));
-  a.stride = static_cast<size_t>(p->logits_stride ? p->logits_stride : p->vocab);
-  a.batch = p->batch;
-  a.beams = p->beams;
-  a.select = p->select;
-  a.vocab = p->vocab;
-  a.bf16 = p->logits_dtype == TV_OUT_BF16 ? 1 : 0;
-  a.end_token = p->end_token;
-  a.parts = tv::beam_parts(p->vocab);
-  // equal parts, of whole 16-byte words of either type
-  a.chunk = ((p->vocab + a.parts - 1) / a.parts + 7) / 8 * 8;
-  a.length_penalty = p->length_penalty;
+  a.inverse = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + stats);
+  a.lists = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + stats + factors);
   return tv::launch_beam_select(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }
 
@@ -1043,6 +1064,10 @@ int tv_alloc_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_c
   if (!pages_valid(p)) return TV_ERR_INVALID_ARG;
   if (!all_given({block_table, ref_counts, end, status}) || !aligned16(begin)) return TV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
+  const uint64_t word = static_cast<uint64_t>(p->rows) * 4;
+  if (clash({{block_table, word * p->max_blocks_per_seq}, {ref_counts, p->num_blocks * 4ull}, {status, word}},
+            {{begin, word}, {end, word}}))
+    return TV_ERR_INVALID_ARG;
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
   a.begin = begin;
   a.end = end;
@@ -1055,6 +1080,10 @@ int tv_free_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_co
                   cudaStream_t stream) {
   if (!pages_valid(p) || p->sinks < 0) return TV_ERR_INVALID_ARG;
   if (!all_given({block_table, ref_counts, status}) || !aligned16(keep_begin) || !aligned16(keep_end))
+    return TV_ERR_INVALID_ARG;
+  const uint64_t word = static_cast<uint64_t>(p->rows) * 4;
+  if (clash({{block_table, word * p->max_blocks_per_seq}, {ref_counts, p->num_blocks * 4ull}, {status, word}},
+            {{keep_begin, word}, {keep_end, word}}))
     return TV_ERR_INVALID_ARG;
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
   a.keep_begin = keep_begin;
@@ -1071,10 +1100,10 @@ int tv_fork_pages(const tv_page_params* p, const int32_t* block_table,
   if (!pages_valid(p) || p->new_rows < 1 || p->new_rows > 65536) return TV_ERR_INVALID_ARG;
   if (!all_given({block_table, seq_lens, parents, ref_counts, block_table_out, seq_lens_out, copies, status}))
     return TV_ERR_INVALID_ARG;
-  const uint64_t row = static_cast<uint64_t>(p->max_blocks_per_seq) * 4;
-  if (overlap(block_table, p->rows * row, block_table_out, p->new_rows * row) ||
-      overlap(seq_lens, p->rows * 4ull, seq_lens_out, p->new_rows * 4ull) ||
-      overlap(parents, p->new_rows * 4ull, seq_lens_out, p->new_rows * 4ull))
+  const uint64_t row = static_cast<uint64_t>(p->max_blocks_per_seq) * 4, rows = p->rows, children = p->new_rows;
+  if (clash({{ref_counts, p->num_blocks * 4ull}, {block_table_out, children * row}, {seq_lens_out, children * 4},
+             {copies, children * 12}, {status, children * 4}},
+            {{block_table, rows * row}, {seq_lens, rows * 4}, {parents, children * 4}}))
     return TV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
@@ -1096,9 +1125,12 @@ int tv_compact_pages(const tv_page_params* p, const int32_t* block_table,
   if (!all_given({block_table, ref_counts, block_table_out, ref_counts_out, page_map, moves, count, status}))
     return TV_ERR_INVALID_ARG;
   const uint64_t table = static_cast<uint64_t>(p->rows) * p->max_blocks_per_seq * 4, pages = p->num_blocks * 4ull;
-  if (block_table != block_table_out && overlap(block_table, table, block_table_out, table)) return TV_ERR_INVALID_ARG;
-  if (ref_counts != ref_counts_out && overlap(ref_counts, pages, ref_counts_out, pages)) return TV_ERR_INVALID_ARG;
-  if (overlap(page_map, pages, ref_counts, pages) || overlap(page_map, pages, ref_counts_out, pages)) return TV_ERR_INVALID_ARG;
+  const uint64_t move_bytes = (p->num_blocks > 1 ? p->num_blocks / 2 : 1) * 12ull;
+  if (clash({{block_table_out, table}, {ref_counts_out, pages}, {page_map, pages}, {moves, move_bytes}, {count, 8},
+             {status, p->rows * 4ull}},
+            {{block_table == block_table_out ? nullptr : block_table, table},
+             {ref_counts == ref_counts_out ? nullptr : ref_counts, pages}}))
+    return TV_ERR_INVALID_ARG;
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
   a.table_out = block_table_out;
   a.refs_out = ref_counts_out;

@@ -238,15 +238,15 @@ struct BeamArgs {
   int32_t* status;            // [batch]
   float2* stats;              // [batch * beams][parts] maximum and sum (workspace)
   float2* lists;              // [batch][select][beams][parts] logit and token, best first
+  double* inverse;            // [batch * beams] 1 / length^length_penalty, where that is not 0
   size_t stride;
   int32_t batch, beams, select, vocab, bf16, end_token, parts, chunk;
   float length_penalty;
 };
 int launch_beam_select(const BeamArgs& a, cudaStream_t stream);
-int beam_parts(int vocab);
+void plan_beam_parts(BeamArgs& a, int sms);  // parts and chunk
 int beam_max_select();
 int beam_max_beams();
-int beam_part_entries();  // the most entries of a part
 
 struct PageArgs {
   int32_t* block_table;       // [rows][width]

@@ -57,7 +57,7 @@ CASES = [  # batch, beams, select, V, type, penalty, seed
     (2, 1, 3, 2, torch.bfloat16, 0.0, 2),
     (1, 4, 4, 1000, torch.float32, 0.0, 3),
     (3, 5, 10, 1001, torch.bfloat16, 0.7, 4),     # rows that are not 16-byte aligned
-    (2, 3, 6, 8185, torch.float32, 1.0, 5),       # one entry more than a part holds
+    (2, 3, 6, 8193, torch.float32, 1.0, 5),       # a part of one entry
     (2, 2, 64, 8184, torch.bfloat16, -0.5, 6),
     (2, 8, 16, 32000, torch.bfloat16, 0.6, 7),
     (1, 64, 64, 4099, torch.float32, 0.0, 8),
