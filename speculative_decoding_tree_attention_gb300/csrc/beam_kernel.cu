@@ -15,8 +15,8 @@
 // a CTA, which work on one row, take the least of their c-th largest.  So after the
 // first words the bound is near the S-th best of what eight warps have seen, and few
 // entries pass it: most words cost their exps, a packed maximum and one comparison.
-// (A bound of the warp's own let 22 entries of the first words pass it and took
-// 62 us instead of .. below.)  Bounds rise with time and differ from run to run, the
+// (A bound of the
+// warp's own let 22 entries of every 1024 pass it: 62 us instead of .. below.)  Bounds rise with time and differ from run to run, the
 // S best do not: they pass every bound.  Within a row the order is exact: it is that
 // of the logits, and of equal ones the lower token.
 //
@@ -49,7 +49,8 @@ constexpr int kMaxBeams = 64;
 constexpr int kMaxParts = 64;        // of a row
 constexpr int kMaxLength = 1 << 24;
 constexpr int kWords = 4;            // 16-byte words that a lane has in flight
-constexpr int kList = 2 * kMaxSelect + 16 + 32 * 8;  // entries of a warp's list: a word of every lane past its limit
+constexpr int kStages = 2;           // of them
+constexpr int kList = 2 * kMaxSelect + 16;  // entries of a warp's list
 constexpr int kFound = 1024;         // candidates that the merge ranks by counting
 constexpr int kHeld = 8;             // candidates that a thread of the merge holds
 
@@ -73,12 +74,12 @@ __device__ __forceinline__ float nth_largest(float mine, int n, float& top) {
   return of_ordered(best);
 }
 
-// A warp's list: entries above its bound.
+// A warp's words on their way, and its list: entries from its bound on.
 struct List {
+  uint4 ring[kStages][32 * kWords];
   float value[kList];   // -inf: taken
   int index[kList];
   float2 best[kMaxSelect];
-  int count;
 };
 
 // Keeps the best n of the list's `count` entries, in order, in l.best and at the
@@ -210,19 +211,21 @@ __device__ __forceinline__ float top_of(const uint4& w) {
   }
 }
 
-// The four words of each lane from word w0 on.
+// The four words of each lane from word w0 on, on their way into a stage.
 template <bool BF16>
-__device__ __forceinline__ void load_words(const Part<BF16>& p, int w0, uint4 (&w)[kWords]) {
+__device__ __forceinline__ void fetch_words(const Part<BF16>& p, int w0, uint4* stage) {
   const int lane = threadIdx.x & 31;
   if (p.entry_of(w0) >= p.c0 && p.entry_of(w0 + 32 * kWords) <= p.c1) {
-    const uint4* at = reinterpret_cast<const uint4*>(p.base + static_cast<long long>(p.entry_of(w0 + lane)) * (16 / p.kEach));
+    const uint8_t* at = p.base + static_cast<long long>(p.entry_of(w0 + lane)) * (16 / p.kEach);
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = __ldcs(at + j * 32);
+    for (int j = 0; j < kWords; ++j) cpa16(stage + j * 32 + lane, at + j * 512);
   } else {
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = p.load(w0 + j * 32 + lane);
+#pragma unroll 1
+    for (int j = 0; j < kWords; ++j) stage[j * 32 + lane] = p.load(w0 + j * 32 + lane);
   }
 }
+__device__ __forceinline__ void commit_words() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_words() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
 
 // What the warps of a CTA share: the c-th largest of the lanes' maxima of each
 // (+inf of warps without a part).
@@ -236,35 +239,48 @@ struct Bounds {
 };
 
 // A warp's pass over its part: the entries that may be among the row's best into l,
-// the part's maximum and the sum of exp(x - maximum).
+// the part's maximum and the sum of exp(x - maximum).  Returns whether it is done.
 //
-// The sums are of 2^(x log2 e + c), c = -fl(m hi) with m the lane's maximum so far:
-// x hi + c is rounded once, near 0 where it counts, then x lo added.  Where a sum is
-// NaN (a NaN among the entries) or the maximum beyond 2^20 (a part that is masked by
-// the lowest value), the pass is done again (SAFE), without NaN and from x - m.
+// The sums are of 2^(x hi + c), hi = fl(log2 e), c = -fl(m hi) with m the lane's
+// maximum so far: rounded once, near 0 where it counts.  (hi is log2 e but for 1.3e-8
+// of it: an entry 10 below the maximum counts 1.3e-7 too much or too little, below
+// the approximate power's own error.)  Where a sum is NaN (a NaN among the entries)
+// or the maximum beyond 2^20 (a part that is masked by the lowest value), the pass
+// is done again (SAFE), without NaN and from x - m.
 template <bool BF16, bool SAFE>
-__device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warps, int select, float& m, float& sum) {
+__device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warps, int select, float& m, float& sum, int& count) {
   constexpr int kPairs = BF16 ? 4 : 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach;
-  const int limit = 2 * select + 16, give = (select + warps - 1) / warps;
-  const float floor = SAFE ? -FLT_MAX : -0x1p126f;  // (not -inf: nothing minus nothing)
-  m = floor;
-  if (lane == 0) l.count = 0;
-  float t = -INFINITY, high = -INFINITY;
+  const int give = (select + warps - 1) / warps;
+  m = SAFE ? -FLT_MAX : -0x1p126f;  // (not -inf: nothing minus nothing)
+  count = 0;
+  float t = -FLT_MAX, high = -INFINITY;  // (-inf is no candidate)
   float c = -m * kLog2eHi;
   float2 acc = make_float2(0.0f, 0.0f);
-  uint4 next[kWords];
-  load_words<BF16>(p, 0, next);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i * 32 * kWords < words) fetch_words<BF16>(p, i * 32 * kWords, l.ring[i]);
+    commit_words();
+  }
   for (int w0 = 0, turn = 0; w0 < words; w0 += 32 * kWords, ++turn) {
+    const int ahead = w0 + (kStages - 1) * 32 * kWords;
+    if (ahead < words) fetch_words<BF16>(p, ahead, l.ring[(turn + kStages - 1) % kStages]);
+    commit_words();
+    wait_words();
+    uint4* stage = l.ring[turn % kStages];
     uint4 w[kWords];
     float g[kWords];
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
-      w[j] = SAFE ? without_nan<BF16>(next[j]) : next[j];
+      w[j] = stage[j * 32 + lane];
+      if (SAFE) {
+        w[j] = without_nan<BF16>(w[j]);
+        stage[j * 32 + lane] = w[j];
+      }
       g[j] = top_of<BF16>(w[j]);
     }
-    if (w0 + 32 * kWords < words) load_words<BF16>(p, w0 + 32 * kWords, next);
     const float top = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
     high = fmaxf(high, top);
     if (top > m) {
@@ -284,7 +300,6 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
       if (lane == 0) reinterpret_cast<volatile float*>(bounds)[warp] = nth;
       if (!SAFE && turn == 0) __syncthreads();  // (nobody starts without a bound)
     }
-    t = fmaxf(t, bounds->least());
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
       float2 v[kPairs];
@@ -296,45 +311,47 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
           const float2 d = add2(v[i], make_float2(-m, -m));
           e = fma2(d, make_float2(kLog2eHi, kLog2eHi), mul2(d, make_float2(kLog2eLo, kLog2eLo)));
         } else {
-          e = fma2(v[i], make_float2(kLog2eLo, kLog2eLo), fma2(v[i], make_float2(kLog2eHi, kLog2eHi), make_float2(c, c)));
+          e = fma2(v[i], make_float2(kLog2eHi, kLog2eHi), make_float2(c, c));
         }
         acc = add2(acc, make_float2(ex2_approx(e.x), ex2_approx(e.y)));
       }
     }
     if (!__any_sync(0xffffffffu, top >= t)) continue;
+    __syncwarp();  // (every lane's words are seen by the others)
+    t = fmaxf(t, bounds->least());
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
-      if (!__any_sync(0xffffffffu, g[j] >= t)) continue;
-      __syncwarp();
-      if (l.count > limit) {
-        const int kept = keep_best(l, l.count, select);
-        if (lane == 0) l.count = kept;
-        // (of equal ones the later token does not count)
-        if (kept == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1] + 0.0f) + 1));
-        __syncwarp();
-      }
-      if (g[j] >= t) {
-        float2 v[kPairs];
-        values_of<BF16>(w[j], v);
-        const int e = p.entry_of(w0 + j * 32 + lane);
-#pragma unroll
-        for (int i = 0; i < 2 * kPairs; ++i) {
-          const float x = i % 2 ? v[i / 2].y : v[i / 2].x;
-          if (x >= t && x > -INFINITY) {
-            const int at = atomicAdd(&l.count, 1);
-            l.value[at] = x + 0.0f;  // (one zero)
-            l.index[at] = e + i;
-          }
+      // word by word, an entry a lane
+      for (unsigned has = __ballot_sync(0xffffffffu, g[j] >= t); has; has &= has - 1) {
+        const int word = j * 32 + __ffs(has) - 1;
+        if (count + p.kEach > kList) {
+          count = keep_best(l, count, select);
+          // (of equal ones the later token does not count)
+          if (count == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1]) + 1));
         }
+        float x = -INFINITY;
+        if (lane < p.kEach) {
+          x = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(stage + word)[lane]) << 16)
+                   : reinterpret_cast<const float*>(stage + word)[lane];
+          x += 0.0f;  // (one zero)
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= t);
+        if (x >= t) {
+          const int at = count + __popc(hit & ((1u << lane) - 1));
+          l.value[at] = x;
+          l.index[at] = p.entry_of(w0 + word) + lane;
+        }
+        count += __popc(hit);
       }
     }
+    __syncwarp();  // (the stage is filled again next)
   }
   sum = acc.x + acc.y;
   const float all = of_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
   const bool fails = __any_sync(0xffffffffu, sum != sum) || (!SAFE && !(fabsf(all) <= 0x1p20f));
   if (!SAFE) {
-    // from 2^-c to exp(m): by 2^(-c - m log2 e), next to 1
-    const float y = -0.69314718f * fmaf(m, kLog2eLo, fmaf(m, kLog2eHi, c));
+    // as of 2^((x - m) hi): by 2^(-c - m hi), next to 1
+    const float y = -0.69314718f * fmaf(m, kLog2eHi, c);
     sum = fabsf(y) < 0x1p-8f ? fmaf(sum, fmaf(y * y, 0.5f, y), sum) : sum * expf(y);
   }
   // the lanes' sums against the warp's maximum
@@ -360,7 +377,8 @@ __device__ void row_inverses(const BeamArgs& a, int row) {
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a) {
-  __shared__ List lists[kWarps];
+  extern __shared__ __align__(16) uint8_t raw[];
+  List* lists = reinterpret_cast<List*>(raw);
   __shared__ Bounds bounds;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -382,13 +400,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
   p.start = p.c0 - static_cast<int>((reinterpret_cast<uintptr_t>(p.base + static_cast<size_t>(p.c0) * (16 / p.kEach)) & 15) / (16 / p.kEach));
   List& l = lists[warp];
   float m, sum;
-  if (!part_pass<BF16, false>(p, l, &bounds, warps, a.select, m, sum)) {
-    __syncwarp();
-    part_pass<BF16, true>(p, l, &bounds, warps, a.select, m, sum);
-  }
+  int count;
+  if (!part_pass<BF16, false>(p, l, &bounds, warps, a.select, m, sum, count))
+    part_pass<BF16, true>(p, l, &bounds, warps, a.select, m, sum, count);
   if (lane == 0) a.stats[static_cast<size_t>(row) * a.parts + part] = make_float2(m, sum);
-  __syncwarp();
-  const int count = keep_best(l, l.count, a.select);
+  count = keep_best(l, count, a.select);
   const size_t all = static_cast<size_t>(a.beams) * a.parts;
   float2* list = a.lists + static_cast<size_t>(row / a.beams) * a.select * all + static_cast<size_t>(row % a.beams) * a.parts + part;
   for (int i = lane; i < a.select; i += 32)
@@ -685,11 +701,13 @@ int launch_beam_select(const BeamArgs& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.batch) * a.beams;
   const long long ctas = rows * ((a.parts + kWarps - 1) / kWarps) + (a.length_penalty != 0.0f ? (rows + kThreads - 1) / kThreads : 0);
   const unsigned grid = static_cast<unsigned>(ctas);
-  if (a.bf16) {
-    beam_rows_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    beam_rows_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-  }
+  const int smem = kWarps * sizeof(List);
+  static_assert(kWarps * sizeof(List) <= 56 * 1024, "four CTAs an SM");
+  const auto kernel = a.bf16 ? beam_rows_kernel<true> : beam_rows_kernel<false>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return -1;
+  kernel<<<grid, kThreads, smem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return -1;
   // the merge's CTAs may start while the last rows are read; they wait for them
   cudaLaunchConfig_t cfg = {};
