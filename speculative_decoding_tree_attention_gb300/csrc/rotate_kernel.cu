@@ -18,8 +18,11 @@
 // A row is taken by D / 8 lanes that hold four pairs each, so that both values of
 // a pair are in one lane: pairs (i, i + R/2) as 8 bytes of each half, pairs
 // (2i, 2i+1) as 16 bytes; halves that are not 8 bytes aligned (R / 2 no multiple
-// of 4) value by value.  Sine and cosine of a lane's pairs are computed once for
-// all heads that a warp takes of a token.  Bound: HBM, one read and one write of
+// of 4) value by value.  A warp takes a token's heads, or a share of them.  Sine and
+// cosine of the token's pairs are computed once, a lane a pair, and joined with the
+// weights: with A = w_a cos, B = w_b sin, C = w_a sin, D = w_b cos a pair costs two
+// products, two fused ones and two products by the root, two values an instruction.
+// The first rows are on their way meanwhile.  Bound: HBM, one read and one write of
 // each row; latency for single tokens.
 #include "tv_device.cuh"
 #include "tv_launch.h"
@@ -32,18 +35,31 @@ constexpr int kWarps = kThreads / 32;
 
 enum Layout { kHalves, kNeighbours, kHalvesByValue };
 
-struct Angles {
+struct Shared {
   uint64_t turn[kMaxPairs];  // f / 2 pi, a fraction of 2^64
   float scale[kMaxPairs];    // of sine and cosine; NaN where f is not finite
   uint8_t axis[kMaxPairs];
+  float weight[2][2 * kMaxPairs];          // of queries and keys
+  float2 angle[kWarps][kMaxPairs];         // of a warp's token: cosine and sine
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float bf16_of(uint16_t w) { return __uint_as_float(static_cast<uint32_t>(w) << 16); }
 
-__device__ void fill_angles(const RotateArgs& a, Angles& s) {
+__device__ void fill_shared(const RotateArgs& a, Shared& s) {
   const int i = threadIdx.x;
+  if (i >= kThreads - 2 * kMaxPairs) {  // (the other half of the threads)
+    const int d = i - (kThreads - 2 * kMaxPairs);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const void* w = k ? a.k_weight : a.q_weight;
+      float v = 1.0f;
+      if (w && d < a.head_dim)
+        v = a.weight_fp32 ? static_cast<const float*>(w)[d] : bf16_of(static_cast<const uint16_t*>(w)[d]);
+      s.weight[k][d] = v;
+    }
+  }
   if (i < a.rotary_dim / 2) {
     const double f = a.frequencies[i];
     const double inverse = 0.15915494309189535, rest = -9.839338337591243e-18;  // 1 / 2 pi
@@ -111,152 +127,184 @@ struct Row {
       }
     }
   }
-  // value j of the first and of the second of the pairs
-  __device__ __forceinline__ void values(float (&x)[4], float (&y)[4]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (L == kHalves) {
-        x[j] = j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-        y[j] = j % 2 ? bf16_hi(w[2 + j / 2]) : bf16_lo(w[2 + j / 2]);
-      } else {
-        x[j] = bf16_lo(w[j]);
-        y[j] = bf16_hi(w[j]);
-      }
-    }
-  }
-  __device__ __forceinline__ void set(const float (&x)[4], const float (&y)[4]) {
+  // the pairs' first and second values, two by two
+  __device__ __forceinline__ void values(float2 (&x)[2], float2 (&y)[2]) const {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (L == kHalves) {
-        w[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-        w[2 + j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+        x[j] = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
+        y[j] = make_float2(bf16_lo(w[2 + j]), bf16_hi(w[2 + j]));
       } else {
-        w[2 * j] = pack_bf16x2(x[2 * j], y[2 * j]);
-        w[2 * j + 1] = pack_bf16x2(x[2 * j + 1], y[2 * j + 1]);
+        x[j] = make_float2(bf16_lo(w[2 * j]), bf16_lo(w[2 * j + 1]));
+        y[j] = make_float2(bf16_hi(w[2 * j]), bf16_hi(w[2 * j + 1]));
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&x)[2], const float2 (&y)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (L == kHalves) {
+        w[j] = pack_bf16x2(x[j].x, x[j].y);
+        w[2 + j] = pack_bf16x2(y[j].x, y[j].y);
+      } else {
+        w[2 * j] = pack_bf16x2(x[j].x, y[j].x);
+        w[2 * j + 1] = pack_bf16x2(x[j].y, y[j].y);
       }
     }
   }
 };
 
-// A lane's weights of its values.
-template <int D, Layout L>
-__device__ __forceinline__ void load_weights(const void* w, bool fp32, int sub, int rot, float (&x)[4], float (&y)[4]) {
+// What a lane turns its pairs by (a pair that is not turned: its weights alone).
+struct Turn {
+  float2 a[2], b[2], c[2], d[2];  // (b: with the other sign)
+};
+template <int D, Layout L, bool ALL>
+__device__ __forceinline__ void fill_turn(const Shared& s, int key, int sub, int rot, Turn& r) {
+  const float2* angle = s.angle[threadIdx.x >> 5];
+  const float* weight = s.weight[key];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    x[j] = y[j] = 1.0f;
-    if (!w) continue;
     const int p = pair_of<D, L>(sub, j);
-    int i = first_of<D, L>(p, rot), k = second_of<D, L>(p, rot);
-    if (L == kHalves && 8 * sub >= rot) i = 8 * sub + j, k = 8 * sub + 4 + j;
-    x[j] = fp32 ? static_cast<const float*>(w)[i] : bf16_of(static_cast<const uint16_t*>(w)[i]);
-    y[j] = fp32 ? static_cast<const float*>(w)[k] : bf16_of(static_cast<const uint16_t*>(w)[k]);
+    const bool turned = ALL || 2 * p < rot;
+    const bool run = L == kHalves && !turned;  // (eight values in a row)
+    const float wx = weight[run ? 8 * sub + j : first_of<D, L>(p, rot)];
+    const float wy = weight[run ? 8 * sub + 4 + j : second_of<D, L>(p, rot)];
+    const float2 cs = turned ? angle[p] : make_float2(1.0f, 0.0f);
+    (j % 2 ? r.a[j / 2].y : r.a[j / 2].x) = wx * cs.x;
+    (j % 2 ? r.b[j / 2].y : r.b[j / 2].x) = -wy * cs.y;
+    (j % 2 ? r.c[j / 2].y : r.c[j / 2].x) = wx * cs.y;
+    (j % 2 ? r.d[j / 2].y : r.d[j / 2].x) = wy * cs.x;
+  }
+}
+
+// ALL: every value of a head is turned.
+template <int D, Layout L, bool ALL>
+__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows that a warp takes at once
+  constexpr int kUnroll = 4;
+  __shared__ Shared s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
+  const int rot = a.rotary_dim;
+  const long long it = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const int t = static_cast<int>(it / a.items);
+  const bool here = t < a.tokens;
+  // steps of kRows heads, of the queries and then of the keys; this warp's share
+  const int q_steps = (a.hq + kRows - 1) / kRows, steps = q_steps + (a.hkv + kRows - 1) / kRows;
+  const int each = (steps + a.items - 1) / a.items;
+  const int g0 = static_cast<int>(it - static_cast<long long>(t) * a.items) * each, g1 = here ? min(g0 + each, steps) : g0;
+  Row<D, L> r[kUnroll];
+  // rows of step g on, of queries or keys
+  const auto load = [&](int g, int end, bool key) {
+    const int heads = key ? a.hkv : a.hq, h0 = (key ? g - q_steps : g) * kRows + lane / kLanes;
+    const uint16_t* in = (key ? a.k + t * a.k_stride : a.q + t * a.q_stride) + static_cast<size_t>(h0) * D;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (g + u < end && h0 + u * kRows < heads) {
+        r[u].load(in + u * kRows * D, sub, rot);
+      } else {
+        r[u].w[0] = r[u].w[1] = r[u].w[2] = r[u].w[3] = 0;
+      }
+    }
+  };
+  int pos[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = lane + 32 * i;
+    pos[i] = here && 2 * p < rot ? a.positions[static_cast<size_t>(a.axis[p]) * a.tokens + t] : 0;
+  }
+  if (g0 < g1) load(g0, g0 < q_steps ? min(g1, q_steps) : g1, g0 >= q_steps);
+  fill_shared(a, s);
+  __syncthreads();
+  if (g0 >= g1) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = lane + 32 * i;
+    if (2 * p < rot) {
+      const uint64_t phase = s.turn[p] * static_cast<uint64_t>(static_cast<long long>(pos[i]));
+      float c, n;
+      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &n, &c);
+      s.angle[warp][p] = make_float2(c * s.scale[p], n * s.scale[p]);
+    }
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int key = 0; key < 2; ++key) {
+    const int from = key ? max(g0, q_steps) : g0, to = key ? g1 : min(g1, q_steps);
+    if (from >= to) continue;
+    const bool norm = (key ? a.k_weight : a.q_weight) != nullptr;
+    const int heads = key ? a.hkv : a.hq;
+    Turn turn;
+    fill_turn<D, L, ALL>(s, key, sub, rot, turn);
+    for (int g = from; g < to; g += kUnroll) {
+      if (g != g0) load(g, to, key);
+      const int h0 = (key ? g - q_steps : g) * kRows + lane / kLanes;
+      uint16_t* out = (key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride) + static_cast<size_t>(h0) * D;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float2 x[2], y[2];
+        r[u].values(x, y);
+        float inv = 1.0f;
+        if (norm) {
+          const float2 two = fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1]))));
+          float sum = two.x + two.y;
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          inv = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 n = make_float2(inv, inv);
+          const float2 b = mul2(n, fma2(x[j], turn.a[j], mul2(y[j], turn.b[j])));
+          const float2 d = mul2(n, fma2(y[j], turn.d[j], mul2(x[j], turn.c[j])));
+          if (ALL) {
+            x[j] = b, y[j] = d;
+          } else {  // (a value that is not turned is none of its neighbour's business, infinite or not)
+            const int p = pair_of<D, L>(sub, 2 * j), q = pair_of<D, L>(sub, 2 * j + 1);
+            x[j].x = 2 * p < rot ? b.x : x[j].x * turn.a[j].x * inv;
+            y[j].x = 2 * p < rot ? d.x : y[j].x * turn.d[j].x * inv;
+            x[j].y = 2 * q < rot ? b.y : x[j].y * turn.a[j].y * inv;
+            y[j].y = 2 * q < rot ? d.y : y[j].y * turn.d[j].y * inv;
+          }
+        }
+        r[u].set(x, y);
+        if (g + u < to && h0 + u * kRows < heads) r[u].store(out + u * kRows * D, sub, rot);
+      }
+    }
   }
 }
 
 template <int D, Layout L>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  constexpr int kUnroll = 4;
-  __shared__ Angles s;
-  fill_angles(a, s);
-  const int lane = threadIdx.x & 31, sub = lane % kLanes;
-  const int rot = a.rotary_dim;
-  float qx[4], qy[4], kx[4], ky[4];
-  load_weights<D, L>(a.q_weight, a.weight_fp32, sub, rot, qx, qy);
-  load_weights<D, L>(a.k_weight, a.weight_fp32, sub, rot, kx, ky);
-  __syncthreads();
-  const int heads = a.hq + a.hkv;
-  const int each = ((heads + kRows - 1) / kRows + a.items - 1) / a.items * kRows;  // heads of an item
-  const long long all = static_cast<long long>(a.tokens) * a.items;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < all;
-       it += static_cast<long long>(gridDim.x) * kWarps) {
-    const int t = static_cast<int>(it / a.items);
-    const int h0 = static_cast<int>(it - static_cast<long long>(t) * a.items) * each;
-    const int h1 = min(h0 + each, heads);
-    float c[4], n[4];
-    bool turned[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int p = pair_of<D, L>(sub, j);
-      turned[j] = 2 * p < rot;
-      c[j] = n[j] = 0.0f;
-      if (turned[j]) {
-        const long long pos = a.positions[static_cast<size_t>(s.axis[p]) * a.tokens + t];
-        const uint64_t phase = s.turn[p] * static_cast<uint64_t>(pos);
-        sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &n[j], &c[j]);
-        c[j] *= s.scale[p];
-        n[j] *= s.scale[p];
-      }
-    }
-    for (int g = h0; g < h1; g += kRows * kUnroll) {  // (uniform over the warp)
-      Row<D, L> r[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = g + u * kRows + lane / kLanes;
-        if (h < h1) {
-          r[u].load(h < a.hq ? a.q + t * a.q_stride + static_cast<size_t>(h) * D
-                             : a.k + t * a.k_stride + static_cast<size_t>(h - a.hq) * D, sub, rot);
-        } else {
-          r[u].w[0] = r[u].w[1] = r[u].w[2] = r[u].w[3] = 0;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = g + u * kRows + lane / kLanes;
-        const bool q = h < a.hq;
-        float x[4], y[4];
-        r[u].values(x, y);
-        if (a.q_weight || a.k_weight) {
-          float sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum = fmaf(x[j], x[j], fmaf(y[j], y[j], sum));
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (q ? a.q_weight : a.k_weight) {
-            const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[j] = x[j] * inv * (q ? qx[j] : kx[j]);
-              y[j] = y[j] * inv * (q ? qy[j] : ky[j]);
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float b = x[j] * c[j] - y[j] * n[j], d = x[j] * n[j] + y[j] * c[j];
-          if (turned[j]) x[j] = b, y[j] = d;
-        }
-        r[u].set(x, y);
-        if (h < h1)
-          r[u].store(q ? a.q_out + t * a.q_out_stride + static_cast<size_t>(h) * D
-                       : a.k_out + t * a.k_out_stride + static_cast<size_t>(h - a.hq) * D, sub, rot);
-      }
-    }
+void launch_rotate_l(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
+  if (a.rotary_dim == D) {
+    rotate_kernel<D, L, true><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    rotate_kernel<D, L, false><<<grid, kThreads, 0, stream>>>(a);
   }
 }
 
 template <int D>
-void launch_rotate_d(const RotateArgs& a, int grid, cudaStream_t stream) {
+void launch_rotate_d(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
   if (a.interleaved) {
-    rotate_kernel<D, kNeighbours><<<grid, kThreads, 0, stream>>>(a);
+    launch_rotate_l<D, kNeighbours>(a, grid, stream);
   } else if (a.rotary_dim % 8 == 0) {
-    rotate_kernel<D, kHalves><<<grid, kThreads, 0, stream>>>(a);
+    launch_rotate_l<D, kHalves>(a, grid, stream);
   } else {
-    rotate_kernel<D, kHalvesByValue><<<grid, kThreads, 0, stream>>>(a);
+    rotate_kernel<D, kHalvesByValue, false><<<grid, kThreads, 0, stream>>>(a);
   }
 }
 
 }  // namespace
 
 int launch_rotate(RotateArgs a, int sms, cudaStream_t stream) {
-  // Warps that share a token: enough that every SM has 32 of them four times
-  // over, at most one for each group of heads that a warp takes at once.
-  const long long want = 128ll * sms;
-  const int rows = 256 / a.head_dim, groups = (a.hq + a.hkv + rows - 1) / rows;
+  // Warps that share a token: enough for about eight CTAs on every SM, at most one
+  // for each step of heads.
+  const long long want = 8ll * kWarps * sms;
+  const int rows = 256 / a.head_dim, steps = (a.hq + rows - 1) / rows + (a.hkv + rows - 1) / rows;
   const long long share = (want + a.tokens - 1) / a.tokens;
-  a.items = static_cast<int>(share < groups ? share : groups);
-  const long long ctas = (static_cast<long long>(a.tokens) * a.items + kWarps - 1) / kWarps, most = 4ll * sms;
-  const int grid = static_cast<int>(ctas < most ? ctas : most);
+  a.items = static_cast<int>(share < steps ? share : steps);
+  const long long ctas = (static_cast<long long>(a.tokens) * a.items + kWarps - 1) / kWarps;
+  if (ctas > 0x7fffffffll) return -1;
+  const unsigned grid = static_cast<unsigned>(ctas);
   if (a.head_dim == 128) {
     launch_rotate_d<128>(a, grid, stream);
   } else {
