@@ -570,17 +570,20 @@ def _arg(name, t, dtype, shape, dev):
 def _rows(name, t, dtype, shape, dev):
     """_arg for rows that may lie a stride apart; returns that stride (0: packed)."""
     try:
-        if t.is_contiguous() or t.shape[0] < 2:
-            stride = 0
-        else:
-            stride = t.stride(0)
-            if not t[0].is_contiguous() or stride < t[0].numel():
-                _bad(name, "contiguous but for the stride between its rows")
         if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-            if stride == 0 and not t.is_contiguous() and not t[0].is_contiguous():
+            if t.is_contiguous():
+                return 0
+            stride, inner = t.stride(), 1
+            for i in range(len(shape) - 1, 0, -1):
+                if stride[i] != inner and shape[i] != 1:
+                    _bad(name, "contiguous but for the stride between its rows")
+                inner *= shape[i]
+            if shape[0] < 2:
+                return 0
+            if stride[0] < inner:
                 _bad(name, "contiguous but for the stride between its rows")
-            return stride
-    except (AttributeError, IndexError):
+            return stride[0]
+    except AttributeError:
         pass
     _arg(name, t, dtype, shape, dev)
     return 0
@@ -993,7 +996,8 @@ def rotary_axes(sections, interleaved: bool = False) -> tuple:
     return tuple(i % turn if i % turn and i // turn < n[i % turn] else 0 for i in range(sum(n)))
 
 
-_NO_AXES = (C.c_uint8 * 64)()
+_Axes = C.c_uint8 * 64
+_NO_AXES = _Axes()
 
 
 def rotate_qk(q, k, positions, frequencies, *, q_weight=None, k_weight=None, eps: float = 1e-6, axes=None,
@@ -1035,9 +1039,11 @@ def rotate_qk(q, k, positions, frequencies, *, q_weight=None, k_weight=None, eps
         if len(axes) != pairs or pairs > 64:
             _bad("axes", "an axis for each frequency")
         try:
-            of_pair = (C.c_uint8 * 64).from_buffer_copy(bytes(axes).ljust(64, b"\0"))
+            of_pair = _Axes.from_buffer_copy(bytes(axes).ljust(64, b"\0"))
         except (TypeError, ValueError):
             _bad("axes", "small whole numbers")
+    if pairs > 64:
+        _bad("frequencies", "at most 64")
     fp32 = False
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
         if t is not None:

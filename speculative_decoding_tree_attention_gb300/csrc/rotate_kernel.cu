@@ -181,7 +181,7 @@ __device__ __forceinline__ void fill_turn(const Shared& s, int key, int sub, int
 template <int D, Layout L, bool ALL>
 __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows that a warp takes at once
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = 3;
   __shared__ Shared s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
   const int rot = a.rotary_dim;
@@ -206,12 +206,10 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a)
       }
     }
   };
-  int pos[2];
+  int pos[kMaxAxes];  // the token's position on every axis
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = lane + 32 * i;
-    pos[i] = here && 2 * p < rot ? a.positions[static_cast<size_t>(a.axis[p]) * a.tokens + t] : 0;
-  }
+  for (int i = 0; i < kMaxAxes; ++i)
+    pos[i] = here && rot > 0 && i < a.axes ? a.positions[static_cast<size_t>(i) * a.tokens + t] : 0;
   if (g0 < g1) load(g0, g0 < q_steps ? min(g1, q_steps) : g1, g0 >= q_steps);
   fill_shared(a, s);
   __syncthreads();
@@ -220,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a)
   for (int i = 0; i < 2; ++i) {
     const int p = lane + 32 * i;
     if (2 * p < rot) {
-      const uint64_t phase = s.turn[p] * static_cast<uint64_t>(static_cast<long long>(pos[i]));
+      const int axis = s.axis[p];
+      const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+      const uint64_t phase = s.turn[p] * static_cast<uint64_t>(static_cast<long long>(at));
       float c, n;
       sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &n, &c);
       s.angle[warp][p] = make_float2(c * s.scale[p], n * s.scale[p]);
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a)
       uint16_t* out = (key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride) + static_cast<size_t>(h0) * D;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
+        if (g + u >= to) break;  // (uniform over the warp)
         float2 x[2], y[2];
         r[u].values(x, y);
         float inv = 1.0f;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a)
           }
         }
         r[u].set(x, y);
-        if (g + u < to && h0 + u * kRows < heads) r[u].store(out + u * kRows * D, sub, rot);
+        if (h0 + u * kRows < heads) r[u].store(out + u * kRows * D, sub, rot);
       }
     }
   }
@@ -296,12 +297,13 @@ void launch_rotate_d(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
 }  // namespace
 
 int launch_rotate(RotateArgs a, int sms, cudaStream_t stream) {
-  // Warps that share a token: enough for about eight CTAs on every SM, at most one
-  // for each step of heads.
+  // Warps that share a token: enough for about eight CTAs on every SM, of four steps
+  // of heads each at least, which are on their way together; with few tokens of one.
   const long long want = 8ll * kWarps * sms;
   const int rows = 256 / a.head_dim, steps = (a.hq + rows - 1) / rows + (a.hkv + rows - 1) / rows;
   const long long share = (want + a.tokens - 1) / a.tokens;
-  a.items = static_cast<int>(share < steps ? share : steps);
+  const int most = (steps + 3) / 4;
+  a.items = static_cast<int>(share < most ? share : static_cast<long long>(a.tokens) * most < 4ll * sms ? steps : most);
   const long long ctas = (static_cast<long long>(a.tokens) * a.items + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffffll) return -1;
   const unsigned grid = static_cast<unsigned>(ctas);

@@ -936,6 +936,7 @@ int tv_rotate_qk(const tv_rotate_params* p, const uint16_t* q, const uint16_t* k
   a.hkv = p->num_kv_heads;
   a.head_dim = p->head_dim;
   a.rotary_dim = p->rotary_dim;
+  a.axes = p->num_axes;
   a.interleaved = p->interleaved;
   a.weight_fp32 = p->weight_dtype == TV_OUT_FP32 ? 1 : 0;
   a.eps = p->eps;

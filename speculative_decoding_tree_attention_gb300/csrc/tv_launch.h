@@ -216,7 +216,7 @@ struct RotateArgs {
   uint16_t* q_out;
   uint16_t* k_out;
   size_t q_stride, k_stride, q_out_stride, k_out_stride;
-  int32_t tokens, hq, hkv, head_dim, rotary_dim;
+  int32_t tokens, hq, hkv, head_dim, rotary_dim, axes;
   int32_t interleaved;        // pairs (2i, 2i + 1), else (i, i + rotary_dim / 2)
   int32_t weight_fp32;
   float eps, scale;

@@ -105,10 +105,12 @@ def test_beam_arguments(lib, bad):
 def test_beam_pointers_and_workspace(lib):
     p = beams()
     need = lib.tv_beam_select_workspace_size(C.byref(p))
-    # a part a row: a maximum and a sum, a factor (rounded to 256 bytes in all), and 6 entries
-    assert need == 2 * 256 + 6 * 6 * 8
+    # two parts a row (of whole 512 entries): a maximum and a sum each, a factor a
+    # row (rounded to 256 bytes in all), and 6 entries a part
+    assert need == 2 * 256 + 12 * 6 * 8
     big = beams(batch=64, beams=8, select=16, vocab=128256)
-    assert lib.tv_beam_select_workspace_size(C.byref(big)) == 512 * 8 + 512 * 9 * 8 * (1 + 16)  # 9 parts a row: 32 warps an SM
+    # two CTAs of 8 warps a row: six for every SM
+    assert lib.tv_beam_select_workspace_size(C.byref(big)) == 512 * 8 + 512 * 16 * 8 * (1 + 16)
 
     def call(args):
         return lib.tv_beam_select(C.byref(p), *args, at(20), C.c_size_t(need), None)
