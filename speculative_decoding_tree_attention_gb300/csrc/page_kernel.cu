@@ -12,8 +12,9 @@
 // does both: every CTA counts a slice of the pages and of the rows, the totals go
 // through distributed shared memory, the free pages' numbers through the caller's
 // workspace, with a cluster barrier between; one launch, and the slices are
-// read from the same L2.  What touches whole tables (a release, the rows of a
-// fork, the new numbers of a compaction) is a kernel with a CTA per row.
+// read from the same L2.  A small pool takes one CTA and its own barriers.  What
+// touches whole tables (a release, the rows of a fork, the new numbers of a
+// compaction) is a kernel with a CTA per row, but for the rows of a small fork.
 //
 // Bound: latency (three dependent passes and two cluster barriers) for small
 // pools; the cluster's reads of the counts for large ones; HBM for the copies.
@@ -30,15 +31,33 @@ namespace {
 
 constexpr int kNoPage = 7;
 constexpr int kPage = 16;
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;          // CTAs of a cluster, most
 constexpr int kThreads = 1024;       // of a CTA of the cluster
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowThreads = 256;     // of a CTA of the kernels over tables
-constexpr int kRowsOfCta = 65536 / kCluster;
+constexpr int kAhead = 8;            // entries of a row that a lane has in flight
+constexpr int kSmallPool = 16384;    // pages that one CTA counts
+constexpr int kFewEntries = 16384;   // table entries that a CTA writes beside its other work
 
 __device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage > 0); }
 
 // ---------------------------------------------------------------- scans of a cluster
+// The C CTAs of a kernel: a cluster, or one.
+template <int C>
+struct Group {
+  __device__ __forceinline__ static int rank() {
+    if constexpr (C > 1) return static_cast<int>(cg::this_cluster().block_rank());
+    return 0;
+  }
+  // every thread's writes before are seen after, in all C CTAs
+  __device__ __forceinline__ static void sync() {
+    if constexpr (C > 1) {
+      cg::this_cluster().sync();
+    } else {
+      __syncthreads();
+    }
+  }
+};
 struct ScanSmem {
   int warp[2][kWarps];     // of this CTA's warps: exclusive sums
   int total[2];            // of this CTA
@@ -66,13 +85,15 @@ __device__ void scan_warps(ScanSmem& s, int which, int n) {
   __syncthreads();
 }
 
-// The CTAs' totals, after a cluster barrier: (those of the CTAs before this one, all).
-__device__ int2 cluster_totals(cg::cluster_group& cl, ScanSmem& s, int which) {
-  if (threadIdx.x < kCluster) s.mine[which][threadIdx.x] = *cl.map_shared_rank(&s.total[which], threadIdx.x);
+// The CTAs' totals, after a barrier of the group: (those of the CTAs before this one, all).
+template <int C>
+__device__ int2 group_totals(ScanSmem& s, int which) {
+  if constexpr (C == 1) return make_int2(0, s.total[which]);
+  if (threadIdx.x < C) s.mine[which][threadIdx.x] = *cg::this_cluster().map_shared_rank(&s.total[which], threadIdx.x);
   __syncthreads();
   int before = 0, all = 0;
-  for (int i = 0; i < kCluster; ++i) {
-    if (i < static_cast<int>(cl.block_rank())) before += s.mine[which][i];
+  for (int i = 0; i < C; ++i) {
+    if (i < Group<C>::rank()) before += s.mine[which][i];
     all += s.mine[which][i];
   }
   return make_int2(before, all);
@@ -82,9 +103,10 @@ __device__ int2 cluster_totals(cg::cluster_group& cl, ScanSmem& s, int which) {
 struct Share {
   int p0, p1;
 };
+template <int C>
 __device__ __forceinline__ Share share_of(int pages, int rank) {
   const int runs = (pages + 127) / 128;
-  const int warps = kCluster * kWarps, w = rank * kWarps + static_cast<int>(threadIdx.x >> 5);
+  const int warps = C * kWarps, w = rank * kWarps + static_cast<int>(threadIdx.x >> 5);
   const int each = runs / warps, extra = runs % warps;
   Share s;
   s.p0 = (w * each + min(w, extra)) * 128;
@@ -130,17 +152,22 @@ __device__ int count_free(const int32_t* refs, const Share& sh, int end) {
 // the warp's first free page.
 __device__ void list_free(const int32_t* refs, const Share& sh, int rank, int want, int32_t* list) {
   const int lane = threadIdx.x & 31;
-  for (int q = sh.p0; q < sh.p1 && rank < want; q += 128) {
-    const int p = q + lane * 4;
-    const int m = free_mask(counts_of(refs, p, sh.p1, 1)), n = __popc(m);
-    int at = rank + warp_before(n);
+  for (int q0 = sh.p0; q0 < sh.p1 && rank < want; q0 += 4 * 128) {
+    int m[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (m >> j & 1) {
-        if (at < want) list[at] = p + j;
-        ++at;
-      }
-    rank += warp_sum(n);
+    for (int i = 0; i < 4; ++i) m[i] = free_mask(counts_of(refs, q0 + i * 128 + lane * 4, sh.p1, 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = q0 + i * 128 + lane * 4, n = __popc(m[i]);
+      int at = rank + warp_before(n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (m[i] >> j & 1) {
+          if (at < want) list[at] = p + j;
+          ++at;
+        }
+      rank += warp_sum(n);
+    }
   }
 }
 
@@ -159,14 +186,14 @@ __device__ __forceinline__ Range range_of(const PageArgs& a, int b) {
 
 // (dynamic shared memory: the needs of the CTA's rows, then their exclusive sums;
 // -1: a row that is refused)
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
+template <int C>
+__global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
   extern __shared__ int need[];
   __shared__ ScanSmem s;
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = static_cast<int>(cl.block_rank()), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Share sh = share_of(a.num_blocks, rank);
+  const int rank = Group<C>::rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Share sh = share_of<C>(a.num_blocks, rank);
   const int mine = count_free(a.ref_counts, sh, a.num_blocks);
-  const int each = (a.rows + kCluster - 1) / kCluster;
+  const int each = (a.rows + C - 1) / C;
   const int b0 = min(rank * each, a.rows), n = min(each, a.rows - b0);
   // how many entries of each row lack a page
   for (int i = warp; i < n; i += kWarps) {
@@ -191,20 +218,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) all
   for (int i = i0; i < i1; ++i) sum += max(need[i], 0);
   const int before = warp_before(sum);
   scan_warps(s, 1, __shfl_sync(0xffffffffu, before + sum, 31));
-  cl.sync();
-  const int2 free_pages = cluster_totals(cl, s, 0), needed = cluster_totals(cl, s, 1);
+  Group<C>::sync();
+  const int2 free_pages = group_totals<C>(s, 0), needed = group_totals<C>(s, 1);
   if (needed.y > 0) list_free(a.ref_counts, sh, free_pages.x + s.warp[0][warp], min(needed.y, free_pages.y), a.list);
-  cl.sync();  // the list is written, and no CTA reads another's shared memory any more
   // rows in order, each with its place in the list
   int at = needed.x + s.warp[1][warp] + before;
-  __syncthreads();
   for (int i = i0; i < i1; ++i) {
     const int lack = need[i];
     // as its place: refused -1, without a page -2
     need[i] = lack < 0 ? -1 : lack > 0 && lack > free_pages.y - at ? -2 : at;
     at += max(lack, 0);
   }
-  __syncthreads();
+  Group<C>::sync();  // the list is written, and no CTA reads another's shared memory any more
   for (int i = warp; i < n; i += kWarps) {
     const int b = b0 + i;
     int place = need[i];
@@ -212,16 +237,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) all
     if (place < 0 || needed.y == 0) continue;
     const Range r = range_of(a, b);
     int32_t* row = a.block_table + static_cast<size_t>(b) * a.width;
-    for (int q = r.t0; q < r.t1; q += 32) {
-      const int t = q + lane;
-      const bool lacks = t < r.t1 && row[t] < 0;
-      const unsigned m = __ballot_sync(0xffffffffu, lacks);
-      if (lacks) {
-        const int p = a.list[place + __popc(m & ((1u << lane) - 1))];
-        row[t] = p;
-        a.ref_counts[p] = 1;
+    for (int q = r.t0; q < r.t1; q += 32 * kAhead) {
+      bool lacks[kAhead];
+      int from[kAhead], page[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int t = q + j * 32 + lane;
+        lacks[j] = t < r.t1 && row[t] < 0;
       }
-      place += __popc(m);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const unsigned m = __ballot_sync(0xffffffffu, lacks[j]);
+        from[j] = place + __popc(m & ((1u << lane) - 1));
+        place += __popc(m);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) page[j] = lacks[j] ? a.list[from[j]] : 0;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (lacks[j]) {
+          row[q + j * 32 + lane] = page[j];
+          a.ref_counts[page[j]] = 1;
+        }
     }
   }
 }
@@ -235,15 +272,22 @@ __global__ void __launch_bounds__(kRowThreads) free_kernel(const PageArgs a) {
     // entries below `low` but for the first tokens', and from `high` on
     const int low = begin / kPage, high = pages_of(end), first = pages_of(a.sinks);
     int32_t* row = a.block_table + static_cast<size_t>(b) * a.width;
-    for (int t = threadIdx.x; t < a.width; t += kRowThreads) {
-      if (!((t < low && t >= first) || t >= high)) continue;
-      const int e = row[t];
-      if (e < 0) continue;
-      row[t] = -1;
-      if (e < a.num_blocks) {
-        atomicSub(a.ref_counts + e, 1);
-      } else {
-        bad = true;
+    for (int t0 = threadIdx.x; t0 < a.width; t0 += kRowThreads * kAhead) {
+      int e[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int t = t0 + j * kRowThreads;
+        e[j] = t < a.width && ((t < low && t >= first) || t >= high) ? row[t] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (e[j] < 0) continue;
+        row[t0 + j * kRowThreads] = -1;
+        if (e[j] < a.num_blocks) {
+          atomicSub(a.ref_counts + e[j], 1);
+        } else {
+          bad = true;
+        }
       }
     }
   }
@@ -267,23 +311,77 @@ __device__ __forceinline__ Child child_of(const PageArgs& a, int i) {
   return c;
 }
 
-// Who takes over a parent's last page, and the pages and copies of the others.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fork_plan_kernel(const PageArgs a) {
+// New row i of a fork, and what becomes of old row i, by the threads from `first`
+// on in steps of `step`.  Returns whether an entry that a child continues names
+// nothing.
+__device__ bool fork_row(const PageArgs& a, int i, int first, int step) {
+  bool bad = false;
+  if (i < a.new_rows) {
+    const int code = a.status[i], p = a.parents[i];
+    int32_t* out = a.table_out + static_cast<size_t>(i) * a.width;
+    if (code != kOk || p < 0) {
+      for (int t = first; t < a.width; t += step) out[t] = -1;
+    } else {
+      const bool takes = a.first[p] == i;
+      const int len = a.seq_lens[p], whole = len / kPage, part = len % kPage > 0;
+      const int src = a.copies[3 * static_cast<size_t>(i)], dst = a.copies[3 * static_cast<size_t>(i) + 1];
+      const int32_t* in = a.block_table + static_cast<size_t>(p) * a.width;
+      for (int t0 = first; t0 < a.width; t0 += step * kAhead) {
+        int entry[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) entry[j] = t0 + j * step < a.width ? in[t0 + j * step] : -1;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int t = t0 + j * step;
+          if (t >= a.width) break;
+          int e = entry[j];
+          if (t >= whole + part && !takes) e = -1;  // the first child has the spare ones
+          if (e >= a.num_blocks) bad = true, e = -1;
+          if (t == whole && part && dst >= 0) {
+            if (takes) atomicSub(a.ref_counts + src, 1);
+            e = dst;
+          } else if (e >= 0 && !takes) {
+            atomicAdd(a.ref_counts + e, 1);
+          }
+          out[t] = max(e, -1);
+        }
+      }
+    }
+  }
+  // nobody takes over the references of a row without a (first) child
+  if (i < a.rows && a.first[i] == INT_MAX) {
+    const int32_t* in = a.block_table + static_cast<size_t>(i) * a.width;
+    for (int t0 = first; t0 < a.width; t0 += step * kAhead) {
+      int entry[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) entry[j] = t0 + j * step < a.width ? in[t0 + j * step] : -1;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (entry[j] >= 0 && entry[j] < a.num_blocks) atomicSub(a.ref_counts + entry[j], 1);
+    }
+  }
+  return bad;
+}
+
+// Who takes over a parent's last page, and the pages and copies of the others;
+// with ROWS the rows too.
+template <int C, bool ROWS>
+__global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PageArgs a) {
   __shared__ ScanSmem s;
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = static_cast<int>(cl.block_rank()), warp = threadIdx.x >> 5;
-  for (int i = rank * kThreads + threadIdx.x; i < a.rows; i += kCluster * kThreads) a.first[i] = INT_MAX;
-  const Share sh = share_of(a.num_blocks, rank);
+  const int rank = Group<C>::rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = rank * kThreads + threadIdx.x; i < a.rows; i += C * kThreads) a.first[i] = INT_MAX;
+  const Share sh = share_of<C>(a.num_blocks, rank);
   const int mine = count_free(a.ref_counts, sh, a.num_blocks);
-  cl.sync();
-  for (int i = rank * kThreads + threadIdx.x; i < a.new_rows; i += kCluster * kThreads) {
+  Group<C>::sync();
+  for (int i = rank * kThreads + threadIdx.x; i < a.new_rows; i += C * kThreads) {
     const Child c = child_of(a, i);
     if (c.code == kOk && c.parent >= 0) atomicMin(a.first + c.parent, i);
   }
   scan_warps(s, 0, mine);
-  cl.sync();
+  Group<C>::sync();
   // a run of children per thread: how many of them need a page
-  const int each = (a.new_rows + kCluster - 1) / kCluster;
+  const int each = (a.new_rows + C - 1) / C;
   const int b0 = min(rank * each, a.new_rows), n = min(each, a.new_rows - b0);
   const int run = (n + kThreads - 1) / kThreads, i0 = min(static_cast<int>(threadIdx.x) * run, n), i1 = min(i0 + run, n);
   // the page that a child has to copy, -1: none, -2: it should have one but there is none
@@ -291,8 +389,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
     if (c.code != kOk || c.len % kPage == 0) return -1;
     const int e = a.block_table[static_cast<size_t>(c.parent) * a.width + c.len / kPage];
     if (e < 0 || e >= a.num_blocks) return -2;
-    if (a.ref_counts[e] < 1) return -2;
-    return a.first[c.parent] != i || a.ref_counts[e] > 1 ? e : -1;
+    const int refs = a.ref_counts[e];
+    if (refs < 1) return -2;
+    return a.first[c.parent] != i || refs > 1 ? e : -1;
   };
   int sum = 0;
   for (int i = i0; i < i1; ++i) {
@@ -302,10 +401,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
   }
   const int before = warp_before(sum);
   scan_warps(s, 1, __shfl_sync(0xffffffffu, before + sum, 31));
-  cl.sync();
-  const int2 free_pages = cluster_totals(cl, s, 0), needed = cluster_totals(cl, s, 1);
+  Group<C>::sync();
+  const int2 free_pages = group_totals<C>(s, 0), needed = group_totals<C>(s, 1);
   if (needed.y > 0) list_free(a.ref_counts, sh, free_pages.x + s.warp[0][warp], min(needed.y, free_pages.y), a.list);
-  cl.sync();
+  Group<C>::sync();
   int at = needed.x + s.warp[1][warp] + before;
   for (int i = i0; i < i1; ++i) {
     const int b = b0 + i;
@@ -330,61 +429,35 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
     copy[1] = dst;
     copy[2] = dst >= 0 ? c.len % kPage : 0;
   }
+  if (!ROWS) return;
+  Group<C>::sync();
+  for (int i = rank * kWarps + warp; i < max(a.rows, a.new_rows); i += C * kWarps) {
+    const bool bad = fork_row(a, i, lane, 32);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) a.status[i] = kBadTree;
+  }
 }
 
-// New row i of a fork, and what becomes of old row i.
 __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PageArgs a) {
-  const int i = blockIdx.x;
-  bool bad = false;
-  if (i < a.new_rows) {
-    const int code = a.status[i], p = a.parents[i];
-    int32_t* out = a.table_out + static_cast<size_t>(i) * a.width;
-    if (code != kOk || p < 0) {
-      for (int t = threadIdx.x; t < a.width; t += kRowThreads) out[t] = -1;
-    } else {
-      const bool takes = a.first[p] == i;
-      const int len = a.seq_lens[p], whole = len / kPage, part = len % kPage > 0;
-      const int src = a.copies[3 * static_cast<size_t>(i)], dst = a.copies[3 * static_cast<size_t>(i) + 1];
-      const int32_t* in = a.block_table + static_cast<size_t>(p) * a.width;
-      for (int t = threadIdx.x; t < a.width; t += kRowThreads) {
-        int e = in[t];
-        if (t >= whole + part && !takes) e = -1;  // the first child has the spare ones
-        if (e >= a.num_blocks) bad = true, e = -1;
-        if (t == whole && part && dst >= 0) {
-          if (takes) atomicSub(a.ref_counts + src, 1);
-          e = dst;
-        } else if (e >= 0 && !takes) {
-          atomicAdd(a.ref_counts + e, 1);
-        }
-        out[t] = max(e, -1);
-      }
-    }
-  }
-  // nobody takes over the references of a row without a (first) child
-  if (i < a.rows && a.first[i] == INT_MAX) {
-    const int32_t* in = a.block_table + static_cast<size_t>(i) * a.width;
-    for (int t = threadIdx.x; t < a.width; t += kRowThreads) {
-      const int e = in[t];
-      if (e >= 0 && e < a.num_blocks) atomicSub(a.ref_counts + e, 1);
-    }
-  }
-  if (__syncthreads_or(bad) && threadIdx.x == 0) a.status[i] = kBadTree;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool bad = fork_row(a, blockIdx.x, threadIdx.x, kRowThreads);
+  if (__syncthreads_or(bad) && threadIdx.x == 0) a.status[blockIdx.x] = kBadTree;
 }
 
 // ---------------------------------------------------------------- compact
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) compact_plan_kernel(const PageArgs a) {
+template <int C>
+__global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PageArgs a) {
   __shared__ ScanSmem s;
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = static_cast<int>(cl.block_rank()), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Share sh = share_of(a.num_blocks, rank);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int rank = Group<C>::rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Share sh = share_of<C>(a.num_blocks, rank);
   scan_warps(s, 0, count_free(a.ref_counts, sh, a.num_blocks));
-  cl.sync();
-  const int2 free_pages = cluster_totals(cl, s, 0);
+  Group<C>::sync();
+  const int2 free_pages = group_totals<C>(s, 0);
   const int live = a.num_blocks - free_pages.y;
   // the holes: free pages below `live`, as many as pages in use from there on
   scan_warps(s, 1, count_free(a.ref_counts, sh, live));
-  cl.sync();
-  const int holes = cluster_totals(cl, s, 1).y;
+  Group<C>::sync();
+  const int holes = group_totals<C>(s, 1).y;
   int frees = free_pages.x + s.warp[0][warp];
   for (int q = sh.p0; q < sh.p1; q += 128) {
     const int p = q + lane * 4;
@@ -422,8 +495,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
     a.count[0] = live;
     a.count[1] = holes;
   }
-  cl.sync();
-  for (int i = rank * kThreads + threadIdx.x; i < holes; i += kCluster * kThreads) {
+  Group<C>::sync();
+  for (int i = rank * kThreads + threadIdx.x; i < holes; i += C * kThreads) {
     const int src = a.copies[3 * static_cast<size_t>(i)], dst = a.copies[3 * static_cast<size_t>(i) + 1];
     a.page_map[src] = dst;
     a.refs_out[dst] = a.ref_counts[src];
@@ -435,14 +508,21 @@ __global__ void __launch_bounds__(kRowThreads) renumber_kernel(const PageArgs a)
   const int b = blockIdx.x;
   const int32_t* in = a.block_table + static_cast<size_t>(b) * a.width;
   int32_t* out = a.table_out + static_cast<size_t>(b) * a.width;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   bool bad = false;
-  for (int t = threadIdx.x; t < a.width; t += kRowThreads) {
-    int e = in[t];
-    if (e >= 0) {
-      e = e < a.num_blocks ? a.page_map[e] : -1;
-      bad |= e < 0;
-    }
-    out[t] = max(e, -1);
+  for (int t0 = threadIdx.x; t0 < a.width; t0 += kRowThreads * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) e[j] = t0 + j * kRowThreads < a.width ? in[t0 + j * kRowThreads] : -1;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (e[j] >= 0) {
+        e[j] = e[j] < a.num_blocks ? a.page_map[e[j]] : -1;
+        bad |= e[j] < 0;
+      }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (t0 + j * kRowThreads < a.width) out[t0 + j * kRowThreads] = max(e[j], -1);
   }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) a.status[b] = bad ? kBadTree : kOk;
@@ -450,31 +530,46 @@ __global__ void __launch_bounds__(kRowThreads) renumber_kernel(const PageArgs a)
 
 // ---------------------------------------------------------------- copies
 constexpr int kCopyThreads = 256;
+constexpr int kInFlight = 8;  // 16-byte words of a thread
 
+// A CTA takes a slice of the K or V page of an entry in a layer.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int entries = a.count ? max(0, min(a.count[0], a.entries)) : a.entries;
-  const int per = 2 * a.layers;  // K and V of every layer
+  const int per = 2 * a.layers * a.slices;  // of an entry
   const long long all = static_cast<long long>(entries) * per;
-  const int vecs = a.row_bytes / 16, heads = a.hkv;
-  const size_t page = static_cast<size_t>(heads) * kPage * a.row_bytes;
+  const int heads = a.hkv, row_words = a.row_bytes / 16, shift = 31 - __clz(row_words);
+  const int words = heads * kPage * row_words, slice_words = (words + a.slices - 1) / a.slices;
   for (long long w = blockIdx.x; w < all; w += gridDim.x) {
     const int i = static_cast<int>(w / per), which = static_cast<int>(w - static_cast<long long>(i) * per);
-    const int layer = which >> 1, kv = which & 1;
+    const int slice = which % a.slices, kv = which / a.slices & 1, layer = which / a.slices >> 1;
     const int src = a.copies[3 * static_cast<size_t>(i)], dst = a.copies[3 * static_cast<size_t>(i) + 1];
     const int tokens = a.copies[3 * static_cast<size_t>(i) + 2];
     const bool none = src < 0 && dst < 0;
     const bool good = src >= 0 && dst >= 0 && src < a.num_blocks && dst < a.num_blocks && tokens >= 0 && tokens <= kPage;
     if (which == 0 && threadIdx.x == 0) a.status[i] = none || good ? kOk : kNoPage;
     if (!good || src == dst) continue;
-    const uint8_t* from = static_cast<const uint8_t*>(kv ? a.pool[1] : a.pool[0]) + layer * a.layer_stride + src * page;
-    uint8_t* to = static_cast<uint8_t*>(kv ? a.pool[1] : a.pool[0]) + layer * a.layer_stride + dst * page;
-    const int all_vecs = heads * kPage * vecs;
-    for (int j = threadIdx.x; j < all_vecs; j += kCopyThreads)
-      if (j / vecs % kPage < tokens) reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(from)[j];
-    if (a.scale[0]) {
-      float* scales = kv ? a.scale[1] : a.scale[0];
-      const float* sf = scales + layer * a.scale_stride + static_cast<size_t>(src) * heads * kPage;
-      float* st = scales + layer * a.scale_stride + static_cast<size_t>(dst) * heads * kPage;
+    uint8_t* pool = static_cast<uint8_t*>(kv ? a.pool[1] : a.pool[0]) + layer * a.layer_stride;
+    const uint4* from = reinterpret_cast<const uint4*>(pool) + static_cast<size_t>(src) * words;
+    uint4* to = reinterpret_cast<uint4*>(pool) + static_cast<size_t>(dst) * words;
+    const int j0 = slice * slice_words, j1 = min(j0 + slice_words, words);
+    for (int q = j0 + threadIdx.x; q < j1; q += kCopyThreads * kInFlight) {
+      uint4 x[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int j = q + u * kCopyThreads;
+        if (j < j1 && (j >> shift) % kPage < tokens) x[u] = from[j];
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int j = q + u * kCopyThreads;
+        if (j < j1 && (j >> shift) % kPage < tokens) to[j] = x[u];
+      }
+    }
+    if (a.scale[0] && slice == 0) {
+      float* scales = (kv ? a.scale[1] : a.scale[0]) + layer * a.scale_stride;
+      const float* sf = scales + static_cast<size_t>(src) * heads * kPage;
+      float* st = scales + static_cast<size_t>(dst) * heads * kPage;
       for (int j = threadIdx.x; j < heads * kPage; j += kCopyThreads)
         if (j % kPage < tokens) st[j] = sf[j];
     }
@@ -483,13 +578,48 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? 0 : -1; }
 
+// A kernel of C CTAs of a cluster.
+template <int C>
+int launch_group(void (*kernel)(PageArgs), const PageArgs& a, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? 0 : -1;
+}
+
+// A kernel that may be set up while the one before it in the stream ends, for
+// whose results it waits.
+template <typename Args>
+int launch_behind(void (*kernel)(Args), const Args& a, unsigned grid, unsigned threads, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? 0 : -1;
+}
+
+// One CTA for a pool whose counts it reads in a few loads a thread.
+bool small(const PageArgs& a) { return a.num_blocks <= kSmallPool && a.rows <= kThreads && a.new_rows <= kThreads; }
+
 }  // namespace
 
 int launch_alloc_pages(const PageArgs& a, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>((a.rows + kCluster - 1) / kCluster) * 4;
-  static_assert(kRowsOfCta * 4 <= 40 * 1024, "no opt-in");
-  alloc_kernel<<<kCluster, kThreads, smem, stream>>>(a);
-  return launched();
+  static_assert(65536 / kCluster * 4 <= 40 * 1024, "no opt-in");
+  if (small(a)) return launch_group<1>(alloc_kernel<1>, a, static_cast<size_t>(a.rows) * 4, stream);
+  return launch_group<kCluster>(alloc_kernel<kCluster>, a, static_cast<size_t>((a.rows + kCluster - 1) / kCluster) * 4, stream);
 }
 
 int launch_free_pages(const PageArgs& a, cudaStream_t stream) {
@@ -498,23 +628,31 @@ int launch_free_pages(const PageArgs& a, cudaStream_t stream) {
 }
 
 int launch_fork_pages(const PageArgs& a, cudaStream_t stream) {
-  fork_plan_kernel<<<kCluster, kThreads, 0, stream>>>(a);
-  if (launched()) return -1;
-  fork_rows_kernel<<<a.rows > a.new_rows ? a.rows : a.new_rows, kRowThreads, 0, stream>>>(a);
-  return launched();
+  const int rows = a.rows > a.new_rows ? a.rows : a.new_rows;
+  const bool one = small(a);
+  // few entries are done by the same CTAs
+  if (static_cast<long long>(rows) * a.width <= (one ? 1 : kCluster) * kFewEntries)
+    return one ? launch_group<1>(fork_plan_kernel<1, true>, a, 0, stream)
+               : launch_group<kCluster>(fork_plan_kernel<kCluster, true>, a, 0, stream);
+  if (one ? launch_group<1>(fork_plan_kernel<1, false>, a, 0, stream)
+          : launch_group<kCluster>(fork_plan_kernel<kCluster, false>, a, 0, stream))
+    return -1;
+  return launch_behind(fork_rows_kernel, a, static_cast<unsigned>(rows), kRowThreads, stream);
 }
 
 int launch_compact_pages(const PageArgs& a, cudaStream_t stream) {
-  compact_plan_kernel<<<kCluster, kThreads, 0, stream>>>(a);
-  if (launched()) return -1;
-  renumber_kernel<<<a.rows, kRowThreads, 0, stream>>>(a);
-  return launched();
+  if (small(a) ? launch_group<1>(compact_plan_kernel<1>, a, 0, stream)
+               : launch_group<kCluster>(compact_plan_kernel<kCluster>, a, 0, stream))
+    return -1;
+  return launch_behind(renumber_kernel, a, static_cast<unsigned>(a.rows), kRowThreads, stream);
 }
 
-int launch_copy_pages(const CopyArgs& a, int sms, cudaStream_t stream) {
-  const long long all = 2ll * a.entries * a.layers, most = 8ll * sms;
-  copy_kernel<<<static_cast<int>(all < most ? all : most), kCopyThreads, 0, stream>>>(a);
-  return launched();
+int launch_copy_pages(CopyArgs a, int sms, cudaStream_t stream) {
+  // few entries: several CTAs a page, so that every SM has four
+  const long long pages = 2ll * a.entries * a.layers, want = 4ll * sms / pages;
+  a.slices = static_cast<int>(want < 1 ? 1 : want < 8 ? want : 8);
+  const long long all = pages * a.slices, most = 8ll * sms;
+  return launch_behind(copy_kernel, a, static_cast<unsigned>(all < most ? all : most), kCopyThreads, stream);
 }
 
 }  // namespace tv

@@ -281,7 +281,8 @@ struct CopyArgs {
   int32_t* status;            // [entries]
   size_t layer_stride, scale_stride;  // bytes between layers, values between layers of the scales
   int32_t entries, layers, num_blocks, hkv, row_bytes;
+  int32_t slices;             // CTAs that share a page (set by the launcher)
 };
-int launch_copy_pages(const CopyArgs& a, int sms, cudaStream_t stream);
+int launch_copy_pages(CopyArgs a, int sms, cudaStream_t stream);
 
 }  // namespace tv
