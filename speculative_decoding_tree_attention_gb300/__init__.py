@@ -546,9 +546,12 @@ def _bad(name, what):
 
 def _device(name, t):
     """The device index of the tensor that the others of a call go by."""
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
-        _bad(name, "a CUDA tensor")
-    return t.get_device()
+    try:
+        if t.is_cuda:
+            return t.get_device()
+    except AttributeError:
+        pass
+    _bad(name, "a CUDA tensor")
 
 
 def _arg(name, t, dtype, shape, dev):
@@ -591,16 +594,39 @@ def _rows(name, t, dtype, shape, dev):
 
 def _dims(name, t, n):
     """The shape of a tensor of n dimensions."""
-    if not isinstance(t, _torch().Tensor) or t.dim() != n:
-        _bad(name, f"a tensor of {n} dimensions")
-    return t.shape
+    try:
+        if t.dim() == n:
+            return t.shape
+    except AttributeError:
+        pass
+    _bad(name, f"a tensor of {n} dimensions")
+
+
+def _ints(dev, needed, optional=()):
+    """_arg for int32 arguments, (name, tensor, shape) each; optional ones may be None."""
+    i32 = _torch().int32
+    for name, t, shape in needed:
+        try:
+            if t.dtype is i32 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _arg(name, t, i32, shape, dev)
+    for name, t, shape in optional:
+        if t is not None:
+            try:
+                if t.dtype is i32 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+                    continue
+            except AttributeError:
+                pass
+            _arg(name, t, i32, shape, dev)
 
 
 def _run(dev, stream, call):
     """call(stream handle) with `dev` and the stream current, so that what the
     call allocates belongs to that stream."""
     torch = _torch()
-    if stream is None and torch.cuda.current_device() == dev:
+    if stream is None and torch._C._cuda_getDevice() == dev:  # (CUDA is up: the arguments are there)
         return call(_raw_stream(dev))  # (the handle alone: 3 us less than a Stream object)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
@@ -611,9 +637,15 @@ def _run(dev, stream, call):
 
 
 def _raw_stream(dev):
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch.cuda.current_stream(dev).cuda_stream if get is None else get(dev)
+    global _raw
+    if _raw is None:
+        torch = _torch()
+        _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw(dev)
+
+
+_raw = None
 
 
 def _empty(t, shape, dtype, dev):
@@ -1059,11 +1091,14 @@ def rotate_qk(q, k, positions, frequencies, *, q_weight=None, k_weight=None, eps
                        q_stride, k_stride, qo_stride, ko_stride, of_pair)
 
     def call(handle):
-        p = _ptr_or_null
-        qo = _empty(q_out, qs, bf16, dev)
-        ko = None if k is None else _empty(k_out, ks, bf16, dev)
-        rc = lib.tv_rotate_qk(C.byref(prm), p(q), p(k), p(q_weight), p(k_weight), p(positions), p(frequencies),
-                              p(qo), p(ko), handle)
+        qo = q.new_empty(qs) if q_out is None else q_out
+        ko = k_out if k is None or k_out is not None else k.new_empty(ks)
+        rc = lib.tv_rotate_qk(C.byref(prm), q.data_ptr(), None if k is None else k.data_ptr(),
+                              None if q_weight is None else q_weight.data_ptr(),
+                              None if k_weight is None else k_weight.data_ptr(),
+                              None if positions is None else positions.data_ptr(),
+                              None if frequencies is None else frequencies.data_ptr(), qo.data_ptr(),
+                              None if ko is None else ko.data_ptr(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_rotate_qk")
         return qo, ko
@@ -1106,32 +1141,32 @@ def beam_select(logits, scores, *, beams: int, select: int | None = None, length
     prm = _beam_params(logits, beams, beams if select is None else select, end_token, length_penalty)
     rows = logits.shape[0]
     prm.logits_stride = _rows("logits", logits, logits.dtype, logits.shape, dev)
-    shape = (prm.batch, prm.select)
-    _arg("scores", scores, f32, (rows,), dev)
-    for name, t in (("lengths", lengths), ("finished", finished)):
-        if t is not None:
-            _arg(name, t, i32, (rows,), dev)
-    for name, t in (("tokens", tokens), ("parents", parents), ("lengths_out", lengths_out), ("finished_out", finished_out)):
-        if t is not None:
-            _arg(name, t, i32, shape, dev)
+    shape, one, per_row = (prm.batch, prm.select), (prm.batch,), (rows,)
+    _arg("scores", scores, f32, per_row, dev)
+    _ints(dev, (), (("lengths", lengths, per_row), ("finished", finished, per_row), ("tokens", tokens, shape),
+                    ("parents", parents, shape), ("lengths_out", lengths_out, shape),
+                    ("finished_out", finished_out, shape), ("status", status, one)))
     if scores_out is not None:
         _arg("scores_out", scores_out, f32, shape, dev)
-    if status is not None:
-        _arg("status", status, i32, (prm.batch,), dev)
     if lengths is None and lengths_out is not None:
         raise ValueError("lengths_out goes with lengths")
     _workspace(workspace, dev)
 
     def call(handle):
-        p = _ptr_or_null
-        tok, par, fin = (_empty(t, shape, i32, dev) for t in (tokens, parents, finished_out))
-        sc, st = _empty(scores_out, shape, f32, dev), _empty(status, prm.batch, i32, dev)
-        ln = None if lengths is None else _empty(lengths_out, shape, i32, dev)
+        tok = scores.new_empty(shape, dtype=i32) if tokens is None else tokens
+        par = scores.new_empty(shape, dtype=i32) if parents is None else parents
+        fin = scores.new_empty(shape, dtype=i32) if finished_out is None else finished_out
+        sc = scores.new_empty(shape) if scores_out is None else scores_out
+        st = scores.new_empty(one, dtype=i32) if status is None else status
+        ln = lengths_out if lengths is None or lengths_out is not None else scores.new_empty(shape, dtype=i32)
         ws = workspace
         if ws is None:
-            ws = _empty(None, int(lib.tv_beam_select_workspace_size(C.byref(prm))), torch.uint8, dev)
-        rc = lib.tv_beam_select(C.byref(prm), p(logits), p(scores), p(lengths), p(finished), p(tok), p(par), p(sc),
-                                p(ln), p(fin), p(st), p(ws), ws.numel() * ws.element_size(), handle)
+            ws = scores.new_empty(int(lib.tv_beam_select_workspace_size(C.byref(prm))), dtype=torch.uint8)
+        rc = lib.tv_beam_select(C.byref(prm), logits.data_ptr(), scores.data_ptr(),
+                                None if lengths is None else lengths.data_ptr(),
+                                None if finished is None else finished.data_ptr(), tok.data_ptr(), par.data_ptr(),
+                                sc.data_ptr(), None if ln is None else ln.data_ptr(), fin.data_ptr(), st.data_ptr(),
+                                ws.data_ptr(), ws.numel() * ws.element_size(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_beam_select")
         return {"tokens": tok, "parents": par, "scores": sc, "lengths": ln, "finished": fin, "status": st}
@@ -1147,12 +1182,10 @@ def _workspace(t, dev):
 
 def _page_args(block_table, ref_counts, new_rows=0, sinks=0):
     """(device, parameters) of a call on a block table [R, max_blocks] and counts [num_blocks]."""
-    i32 = _torch().int32
     dev = _device("block_table", block_table)
     rows, width = _dims("block_table", block_table, 2)
-    _arg("block_table", block_table, i32, (rows, width), dev)
     (pages,) = _dims("ref_counts", ref_counts, 1)
-    _arg("ref_counts", ref_counts, i32, (pages,), dev)
+    _ints(dev, (("block_table", block_table, (rows, width)), ("ref_counts", ref_counts, (pages,))))
     return dev, PageParams(rows, new_rows, TV_BLOCK_SIZE, width, pages, sinks)
 
 
@@ -1168,24 +1201,19 @@ def alloc_pages(block_table, ref_counts, end, *, begin=None, status=None, worksp
     0) of every row of block_table [R, max_blocks] whose entries are negative there,
     in place there and in ref_counts [num_blocks]; all int32.  Returns status [R];
     nothing is synchronised."""
-    torch = _torch()
     lib = load()
-    i32 = torch.int32
     dev, prm = _page_args(block_table, ref_counts)
-    _arg("end", end, i32, (prm.rows,), dev)
-    if begin is not None:
-        _arg("begin", begin, i32, (prm.rows,), dev)
-    if status is not None:
-        _arg("status", status, i32, (prm.rows,), dev)
+    rows = (prm.rows,)
+    _ints(dev, (("end", end, rows),), (("begin", begin, rows), ("status", status, rows)))
     _workspace(workspace, dev)
 
     def call(handle):
-        st, ws = _empty(status, prm.rows, i32, dev), workspace
+        st, ws = block_table.new_empty(rows) if status is None else status, workspace
         if ws is None:
-            ws = _empty(None, int(lib.tv_pages_workspace_size(C.byref(prm))), torch.uint8, dev)
-        p = _ptr_or_null
-        rc = lib.tv_alloc_pages(C.byref(prm), p(block_table), p(ref_counts), p(begin), p(end), p(st), p(ws),
-                                ws.numel() * ws.element_size(), handle)
+            ws = block_table.new_empty(int(lib.tv_pages_workspace_size(C.byref(prm))), dtype=_torch().uint8)
+        rc = lib.tv_alloc_pages(C.byref(prm), block_table.data_ptr(), ref_counts.data_ptr(),
+                                None if begin is None else begin.data_ptr(), end.data_ptr(), st.data_ptr(),
+                                ws.data_ptr(), ws.numel() * ws.element_size(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_alloc_pages")
         return st
@@ -1198,17 +1226,17 @@ def free_pages(block_table, ref_counts, *, keep_begin=None, keep_end=None, sinks
     [keep_begin[b], keep_end[b]) but for those of the first `sinks` tokens (None: 0,
     and everything), in place in block_table [R, max_blocks] and ref_counts
     [num_blocks]; all int32.  Returns status [R]; nothing is synchronised."""
-    i32 = _torch().int32
     lib = load()
     _int32(sinks=sinks)
     dev, prm = _page_args(block_table, ref_counts, 0, sinks)
-    for name, t in (("keep_begin", keep_begin), ("keep_end", keep_end), ("status", status)):
-        if t is not None:
-            _arg(name, t, i32, (prm.rows,), dev)
+    rows = (prm.rows,)
+    _ints(dev, (), (("keep_begin", keep_begin, rows), ("keep_end", keep_end, rows), ("status", status, rows)))
 
     def call(handle):
-        st, p = _empty(status, prm.rows, i32, dev), _ptr_or_null
-        rc = lib.tv_free_pages(C.byref(prm), p(block_table), p(ref_counts), p(keep_begin), p(keep_end), p(st), handle)
+        st = block_table.new_empty(rows) if status is None else status
+        rc = lib.tv_free_pages(C.byref(prm), block_table.data_ptr(), ref_counts.data_ptr(),
+                               None if keep_begin is None else keep_begin.data_ptr(),
+                               None if keep_end is None else keep_end.data_ptr(), st.data_ptr(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_free_pages")
         return st
@@ -1224,28 +1252,26 @@ def fork_pages(block_table, seq_lens, parents, ref_counts, *, block_table_out=No
     destination, tokens) is what copy_pages has to do before the new rows are read.
     Returns (block_table_out, seq_lens_out, copies, status); nothing is
     synchronised."""
-    torch = _torch()
     lib = load()
-    i32 = torch.int32
     (new,) = _dims("parents", parents, 1)
     dev, prm = _page_args(block_table, ref_counts, new)
-    _arg("seq_lens", seq_lens, i32, (prm.rows,), dev)
-    _arg("parents", parents, i32, (new,), dev)
-    shape = (new, prm.max_blocks_per_seq)
-    for name, t, dims in (("block_table_out", block_table_out, shape), ("seq_lens_out", seq_lens_out, (new,)),
-                          ("copies", copies, (new, 3)), ("status", status, (new,))):
-        if t is not None:
-            _arg(name, t, i32, dims, dev)
+    children, shape, three = (new,), (new, prm.max_blocks_per_seq), (new, 3)
+    _ints(dev, (("seq_lens", seq_lens, (prm.rows,)), ("parents", parents, children)),
+          (("block_table_out", block_table_out, shape), ("seq_lens_out", seq_lens_out, children),
+           ("copies", copies, three), ("status", status, children)))
     _workspace(workspace, dev)
 
     def call(handle):
-        out, lens = _empty(block_table_out, shape, i32, dev), _empty(seq_lens_out, new, i32, dev)
-        cp, st, ws = _empty(copies, (new, 3), i32, dev), _empty(status, new, i32, dev), workspace
+        new_empty = block_table.new_empty
+        out = new_empty(shape) if block_table_out is None else block_table_out
+        lens = new_empty(children) if seq_lens_out is None else seq_lens_out
+        cp = new_empty(three) if copies is None else copies
+        st, ws = new_empty(children) if status is None else status, workspace
         if ws is None:
-            ws = _empty(None, int(lib.tv_pages_workspace_size(C.byref(prm))), torch.uint8, dev)
-        p = _ptr_or_null
-        rc = lib.tv_fork_pages(C.byref(prm), p(block_table), p(seq_lens), p(parents), p(ref_counts), p(out), p(lens),
-                               p(cp), p(st), p(ws), ws.numel() * ws.element_size(), handle)
+            ws = new_empty(int(lib.tv_pages_workspace_size(C.byref(prm))), dtype=_torch().uint8)
+        rc = lib.tv_fork_pages(C.byref(prm), block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(),
+                               ref_counts.data_ptr(), out.data_ptr(), lens.data_ptr(), cp.data_ptr(), st.data_ptr(),
+                               ws.data_ptr(), ws.numel() * ws.element_size(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_fork_pages")
         return out, lens, cp, st
@@ -1261,23 +1287,24 @@ def compact_pages(block_table, ref_counts, *, block_table_out=None, ref_counts_o
     of free pages), moves [max(1, num_blocks // 2), 3] (the first count[1] entries are
     what copy_pages has to do: copy_pages(moves, ..., count=count[1:])), count [2]
     (pages in use, moves) and status [R]; nothing is synchronised."""
-    i32 = _torch().int32
     lib = load()
     dev, prm = _page_args(block_table, ref_counts)
-    rows, pages = prm.rows, prm.num_blocks
-    shape, most = (rows, prm.max_blocks_per_seq), max(1, pages // 2)
-    for name, t, dims in (("block_table_out", block_table_out, shape), ("ref_counts_out", ref_counts_out, (pages,)),
-                          ("page_map", page_map, (pages,)), ("moves", moves, (most, 3)), ("count", count, (2,)),
-                          ("status", status, (rows,))):
-        if t is not None:
-            _arg(name, t, i32, dims, dev)
+    shape, pages, rows = (prm.rows, prm.max_blocks_per_seq), (prm.num_blocks,), (prm.rows,)
+    three = (max(1, prm.num_blocks // 2), 3)
+    _ints(dev, (), (("block_table_out", block_table_out, shape), ("ref_counts_out", ref_counts_out, pages),
+                    ("page_map", page_map, pages), ("moves", moves, three), ("count", count, (2,)),
+                    ("status", status, rows)))
 
     def call(handle):
-        out, refs = _empty(block_table_out, shape, i32, dev), _empty(ref_counts_out, pages, i32, dev)
-        to, mv = _empty(page_map, pages, i32, dev), _empty(moves, (most, 3), i32, dev)
-        n, st, p = _empty(count, 2, i32, dev), _empty(status, rows, i32, dev), _ptr_or_null
-        rc = lib.tv_compact_pages(C.byref(prm), p(block_table), p(ref_counts), p(out), p(refs), p(to), p(mv), p(n),
-                                  p(st), handle)
+        new_empty = block_table.new_empty
+        out = new_empty(shape) if block_table_out is None else block_table_out
+        refs = new_empty(pages) if ref_counts_out is None else ref_counts_out
+        to = new_empty(pages) if page_map is None else page_map
+        mv = new_empty(three) if moves is None else moves
+        n = new_empty((2,)) if count is None else count
+        st = new_empty(rows) if status is None else status
+        rc = lib.tv_compact_pages(C.byref(prm), block_table.data_ptr(), ref_counts.data_ptr(), out.data_ptr(),
+                                  refs.data_ptr(), to.data_ptr(), mv.data_ptr(), n.data_ptr(), st.data_ptr(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_compact_pages")
         return {"block_table": out, "ref_counts": refs, "page_map": to, "moves": mv, "count": n, "status": st}
@@ -1293,36 +1320,33 @@ def copy_pages(copies, k_pool, v_pool, k_scale=None, v_scale=None, *, count=None
     Returns status [n]; nothing is synchronised."""
     torch = _torch()
     lib = load()
-    i32 = torch.int32
     dev = _device("copies", copies)
     n = _dims("copies", copies, 2)[0]
-    _arg("copies", copies, i32, (n, 3), dev)
+    _ints(dev, (("copies", copies, (n, 3)),), (("count", count, (1,)), ("status", status, (n,))))
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale go together")
     fp8 = k_scale is not None
     if not isinstance(k_pool, torch.Tensor) or k_pool.dim() not in (4, 5):
         _bad("k_pool", "a tensor of 4 or 5 dimensions")
     ps = k_pool.shape
-    layers, (blocks, hkv, _, d) = 1 if len(ps) == 4 else ps[0], ps[-4:]
+    layers, (blocks, hkv, page, d) = 1 if len(ps) == 4 else ps[0], ps[-4:]
     elem = torch.uint8 if fp8 else torch.bfloat16
-    _arg("k_pool", k_pool, elem, ps[:-2] + (TV_BLOCK_SIZE, d), dev)
+    _arg("k_pool", k_pool, elem, ps if page == TV_BLOCK_SIZE else ps[:-2] + (TV_BLOCK_SIZE, d), dev)
     _arg("v_pool", v_pool, elem, ps, dev)
     if fp8:
         _arg("k_scale", k_scale, torch.float32, ps[:-1], dev)
         _arg("v_scale", v_scale, torch.float32, ps[:-1], dev)
-    if count is not None:
-        _arg("count", count, i32, (1,), dev)
-    if status is not None:
-        _arg("status", status, i32, (n,), dev)
     prm = CopyParams(n, layers, hkv, d, TV_BLOCK_SIZE, blocks)
 
     def call(handle):
-        st, p = _empty(status, n, i32, dev), _ptr_or_null
+        st = copies.new_empty((n,)) if status is None else status
+        some = None if count is None else count.data_ptr()
         if fp8:
-            rc = lib.tv_copy_pages_fp8(C.byref(prm), p(copies), p(count), p(k_pool), p(k_scale), p(v_pool), p(v_scale),
-                                       p(st), handle)
+            rc = lib.tv_copy_pages_fp8(C.byref(prm), copies.data_ptr(), some, k_pool.data_ptr(), k_scale.data_ptr(),
+                                       v_pool.data_ptr(), v_scale.data_ptr(), st.data_ptr(), handle)
         else:
-            rc = lib.tv_copy_pages(C.byref(prm), p(copies), p(count), p(k_pool), p(v_pool), p(st), handle)
+            rc = lib.tv_copy_pages(C.byref(prm), copies.data_ptr(), some, k_pool.data_ptr(), v_pool.data_ptr(),
+                                   st.data_ptr(), handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_copy_pages_fp8" if fp8 else "tv_copy_pages")
         return st

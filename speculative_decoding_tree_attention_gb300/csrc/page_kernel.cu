@@ -8,7 +8,7 @@
 // whose order does not matter.
 //
 // Giving pages out needs two scans, of the free pages and of the rows' needs,
-// that meet: the k-th page needed is the k-th free one.  One cluster of 8 CTAs
+// that meet: the k-th page needed is the k-th free one.  One cluster of 8 or 16 CTAs
 // does both: every CTA counts a slice of the pages and of the rows, the totals go
 // through distributed shared memory, the free pages' numbers through the caller's
 // workspace, with a cluster barrier between; one launch, and the slices are
@@ -31,12 +31,11 @@ namespace {
 
 constexpr int kNoPage = 7;
 constexpr int kPage = 16;
-constexpr int kCluster = 8;          // CTAs of a cluster, most
+constexpr int kCluster = 16;         // CTAs of a cluster, most
 constexpr int kThreads = 1024;       // of a CTA of the cluster
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowThreads = 256;     // of a CTA of the kernels over tables
 constexpr int kAhead = 8;            // entries of a row that a lane has in flight
-constexpr int kSmallPool = 16384;    // pages that one CTA counts
 constexpr int kFewEntries = 16384;   // table entries that a CTA writes beside its other work
 
 __device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage > 0); }
@@ -592,6 +591,7 @@ int launch_group(void (*kernel)(PageArgs), const PageArgs& a, size_t smem, cudaS
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
+  if (C > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? 0 : -1;
 }
 
@@ -611,15 +611,24 @@ int launch_behind(void (*kernel)(Args), const Args& a, unsigned grid, unsigned t
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? 0 : -1;
 }
 
-// One CTA for a pool whose counts it reads in a few loads a thread.
-bool small(const PageArgs& a) { return a.num_blocks <= kSmallPool && a.rows <= kThreads && a.new_rows <= kThreads; }
+// How many CTAs: one for a pool that it reads in a few loads a thread, `most` pages
+// (which spares two cluster barriers, about 2 us; its work behind the counts differs
+// by kernel), 8 up to 2^18 pages, then 16 (512 rows over 650000 pages: alloc 31 us
+// with 8, 23 with 16; 8 rows over 4000 pages: 10 us with 8, 12 with 16).
+int ctas_for(const PageArgs& a, int most) {
+  if (a.num_blocks <= most && a.rows <= kThreads && a.new_rows <= kThreads) return 1;
+  return a.num_blocks < (1 << 18) ? 8 : kCluster;
+}
 
 }  // namespace
 
 int launch_alloc_pages(const PageArgs& a, cudaStream_t stream) {
-  static_assert(65536 / kCluster * 4 <= 40 * 1024, "no opt-in");
-  if (small(a)) return launch_group<1>(alloc_kernel<1>, a, static_cast<size_t>(a.rows) * 4, stream);
-  return launch_group<kCluster>(alloc_kernel<kCluster>, a, static_cast<size_t>((a.rows + kCluster - 1) / kCluster) * 4, stream);
+  static_assert(65536 / 8 * 4 <= 40 * 1024, "no opt-in");
+  const int ctas = ctas_for(a, 16384);
+  const size_t smem = static_cast<size_t>((a.rows + ctas - 1) / ctas) * 4;
+  return ctas == 1   ? launch_group<1>(alloc_kernel<1>, a, smem, stream)
+         : ctas == 8 ? launch_group<8>(alloc_kernel<8>, a, smem, stream)
+                     : launch_group<kCluster>(alloc_kernel<kCluster>, a, smem, stream);
 }
 
 int launch_free_pages(const PageArgs& a, cudaStream_t stream) {
@@ -627,22 +636,31 @@ int launch_free_pages(const PageArgs& a, cudaStream_t stream) {
   return launched();
 }
 
+namespace {
+
+template <bool ROWS>
+int launch_fork_plan(const PageArgs& a, int ctas, cudaStream_t stream) {
+  return ctas == 1   ? launch_group<1>(fork_plan_kernel<1, ROWS>, a, 0, stream)
+         : ctas == 8 ? launch_group<8>(fork_plan_kernel<8, ROWS>, a, 0, stream)
+                     : launch_group<kCluster>(fork_plan_kernel<kCluster, ROWS>, a, 0, stream);
+}
+
+}  // namespace
+
 int launch_fork_pages(const PageArgs& a, cudaStream_t stream) {
-  const int rows = a.rows > a.new_rows ? a.rows : a.new_rows;
-  const bool one = small(a);
+  const int rows = a.rows > a.new_rows ? a.rows : a.new_rows, ctas = ctas_for(a, 32768);
   // few entries are done by the same CTAs
-  if (static_cast<long long>(rows) * a.width <= (one ? 1 : kCluster) * kFewEntries)
-    return one ? launch_group<1>(fork_plan_kernel<1, true>, a, 0, stream)
-               : launch_group<kCluster>(fork_plan_kernel<kCluster, true>, a, 0, stream);
-  if (one ? launch_group<1>(fork_plan_kernel<1, false>, a, 0, stream)
-          : launch_group<kCluster>(fork_plan_kernel<kCluster, false>, a, 0, stream))
-    return -1;
+  if (static_cast<long long>(rows) * a.width <= static_cast<long long>(ctas) * kFewEntries)
+    return launch_fork_plan<true>(a, ctas, stream);
+  if (launch_fork_plan<false>(a, ctas, stream)) return -1;
   return launch_behind(fork_rows_kernel, a, static_cast<unsigned>(rows), kRowThreads, stream);
 }
 
 int launch_compact_pages(const PageArgs& a, cudaStream_t stream) {
-  if (small(a) ? launch_group<1>(compact_plan_kernel<1>, a, 0, stream)
-               : launch_group<kCluster>(compact_plan_kernel<kCluster>, a, 0, stream))
+  const int ctas = ctas_for(a, 4096);
+  if (ctas == 1   ? launch_group<1>(compact_plan_kernel<1>, a, 0, stream)
+      : ctas == 8 ? launch_group<8>(compact_plan_kernel<8>, a, 0, stream)
+                  : launch_group<kCluster>(compact_plan_kernel<kCluster>, a, 0, stream))
     return -1;
   return launch_behind(renumber_kernel, a, static_cast<unsigned>(a.rows), kRowThreads, stream);
 }
