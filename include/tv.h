@@ -869,8 +869,8 @@ typedef struct {
 } tv_copy_params;       /* host struct */
 
 /* Layouts: copies int32 [entries][3]; count int32 [1] (4-byte aligned) or NULL;
- * pools bf16 [L][num_blocks][Hkv][16][D]; status int32 [entries].  _fp8: pools u8,
- * scales fp32 [L][num_blocks][Hkv][16].  Device pointers 16-byte aligned. */
+ * pools bf16 [L][num_blocks][Hkv][16][D]; status int32 [entries] or NULL.  _fp8:
+ * pools u8, scales fp32 [L][num_blocks][Hkv][16].  Device pointers 16-byte aligned. */
 int tv_copy_pages(const tv_copy_params* params, const int32_t* copies, const int32_t* count,
                   uint16_t* k_pool, uint16_t* v_pool, int32_t* status, cudaStream_t stream);
 int tv_copy_pages_fp8(const tv_copy_params* params, const int32_t* copies, const int32_t* count,

@@ -24,7 +24,7 @@ PyTorch is used for device memory and the current CUDA stream only.
     alloc_pages(...), free_pages(...) -> status (tv_alloc_pages, tv_free_pages)
     fork_pages(...)      -> block_table, seq_lens, copies, status (tv_fork_pages)
     compact_pages(...)   -> dict of outputs  (tv_compact_pages)
-    copy_pages(...)      -> status           (tv_copy_pages, tv_copy_pages_fp8)
+    copy_pages(...)      -> status, where given (tv_copy_pages, tv_copy_pages_fp8)
 """
 from __future__ import annotations
 
@@ -577,7 +577,7 @@ def _rows(name, t, dtype, shape, dev):
             if t.is_contiguous():
                 return 0
             stride, inner = t.stride(), 1
-            for i in range(len(shape) - 1, 0, -1):
+            for i in (2, 1) if len(shape) == 3 else range(len(shape) - 1, 0, -1):
                 if stride[i] != inner and shape[i] != 1:
                     _bad(name, "contiguous but for the stride between its rows")
                 inner *= shape[i]
@@ -1316,8 +1316,9 @@ def copy_pages(copies, k_pool, v_pool, k_scale=None, v_scale=None, *, count=None
     """tv_copy_pages, tv_copy_pages_fp8 (with scales): copies pages within the pools
     of K and V, [num_blocks, Hkv, 16, D] or [layers, num_blocks, Hkv, 16, D], bf16, or
     uint8 codes with fp32 scales [..., Hkv, 16]; copies [n, 3] int32 (source,
-    destination, tokens), of which the first count [1] (int32; None: all) are done.
-    Returns status [n]; nothing is synchronised."""
+    destination, tokens), of which the first count [1] (int32; None: all) are done;
+    status [n] int32, where the caller wants one.  Returns status; nothing is
+    synchronised."""
     torch = _torch()
     lib = load()
     dev = _device("copies", copies)
@@ -1328,8 +1329,11 @@ def copy_pages(copies, k_pool, v_pool, k_scale=None, v_scale=None, *, count=None
     fp8 = k_scale is not None
     if not isinstance(k_pool, torch.Tensor) or k_pool.dim() not in (4, 5):
         _bad("k_pool", "a tensor of 4 or 5 dimensions")
-    ps = k_pool.shape
-    layers, (blocks, hkv, page, d) = 1 if len(ps) == 4 else ps[0], ps[-4:]
+    ps, layers = k_pool.shape, 1
+    if len(ps) == 5:
+        layers, blocks, hkv, page, d = ps
+    else:
+        blocks, hkv, page, d = ps
     elem = torch.uint8 if fp8 else torch.bfloat16
     _arg("k_pool", k_pool, elem, ps if page == TV_BLOCK_SIZE else ps[:-2] + (TV_BLOCK_SIZE, d), dev)
     _arg("v_pool", v_pool, elem, ps, dev)
@@ -1339,16 +1343,15 @@ def copy_pages(copies, k_pool, v_pool, k_scale=None, v_scale=None, *, count=None
     prm = CopyParams(n, layers, hkv, d, TV_BLOCK_SIZE, blocks)
 
     def call(handle):
-        st = copies.new_empty((n,)) if status is None else status
+        st = None if status is None else status.data_ptr()  # (to make one costs as much as the rest)
         some = None if count is None else count.data_ptr()
         if fp8:
             rc = lib.tv_copy_pages_fp8(C.byref(prm), copies.data_ptr(), some, k_pool.data_ptr(), k_scale.data_ptr(),
-                                       v_pool.data_ptr(), v_scale.data_ptr(), st.data_ptr(), handle)
+                                       v_pool.data_ptr(), v_scale.data_ptr(), st, handle)
         else:
-            rc = lib.tv_copy_pages(C.byref(prm), copies.data_ptr(), some, k_pool.data_ptr(), v_pool.data_ptr(),
-                                   st.data_ptr(), handle)
+            rc = lib.tv_copy_pages(C.byref(prm), copies.data_ptr(), some, k_pool.data_ptr(), v_pool.data_ptr(), st, handle)
         if rc != TV_OK:
             raise TVError(rc, "tv_copy_pages_fp8" if fp8 else "tv_copy_pages")
-        return st
+        return status
 
     return _run(dev, stream, call)

@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
     const int tokens = a.copies[3 * static_cast<size_t>(i) + 2];
     const bool none = src < 0 && dst < 0;
     const bool good = src >= 0 && dst >= 0 && src < a.num_blocks && dst < a.num_blocks && tokens >= 0 && tokens <= kPage;
-    if (which == 0 && threadIdx.x == 0) a.status[i] = none || good ? kOk : kNoPage;
+    if (a.status && which == 0 && threadIdx.x == 0) a.status[i] = none || good ? kOk : kNoPage;
     if (!good || src == dst) continue;
     uint8_t* pool = static_cast<uint8_t*>(kv ? a.pool[1] : a.pool[0]) + layer * a.layer_stride;
     const uint4* from = reinterpret_cast<const uint4*>(pool) + static_cast<size_t>(src) * words;

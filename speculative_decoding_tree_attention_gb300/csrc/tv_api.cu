@@ -1154,7 +1154,8 @@ int copy_call(const tv_copy_params* p, const int32_t* copies, const int32_t* cou
       static_cast<int64_t>(p->num_blocks) * p->num_kv_heads * 16 >= (1ll << 31))
     return TV_ERR_INVALID_ARG;
   if (p->entries == 0) return TV_OK;
-  if (!all_given({copies, k_pool, v_pool, status}) || reinterpret_cast<uintptr_t>(count) % 4) return TV_ERR_INVALID_ARG;
+  if (!all_given({copies, k_pool, v_pool}) || !aligned16(status) || reinterpret_cast<uintptr_t>(count) % 4)
+    return TV_ERR_INVALID_ARG;
   if (fp8 && !all_given({k_scale, v_scale})) return TV_ERR_INVALID_ARG;
   tv::CopyArgs a;
   std::memset(&a, 0, sizeof a);

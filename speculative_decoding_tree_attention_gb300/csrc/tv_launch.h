@@ -278,7 +278,7 @@ struct CopyArgs {
   const int32_t* count;       // [1] or null: all entries
   void* pool[2];              // K, V: [layers][num_blocks][Hkv][16][D]
   float* scale[2];            // E4M3: [layers][num_blocks][Hkv][16], else null
-  int32_t* status;            // [entries]
+  int32_t* status;            // [entries] or null
   size_t layer_stride, scale_stride;  // bytes between layers, values between layers of the scales
   int32_t entries, layers, num_blocks, hkv, row_bytes;
   int32_t slices;             // CTAs that share a page (set by the launcher)
