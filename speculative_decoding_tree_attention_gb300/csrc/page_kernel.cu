@@ -36,6 +36,8 @@ constexpr int kThreads = 1024;       // of a CTA of the cluster
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowThreads = 256;     // of a CTA of the kernels over tables
 constexpr int kAhead = 8;            // entries of a row that a lane has in flight
+constexpr int kMaxCuts = 8;          // pieces of a row, most
+constexpr int kNeeds = 8192;         // pieces' needs that a CTA holds
 constexpr int kFewEntries = 16384;   // table entries that a CTA writes beside its other work
 
 __device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage > 0); }
@@ -57,74 +59,15 @@ struct Group {
     }
   }
 };
+struct Totals {
+  int before[2], all[2];  // of two numbers: the sum of the CTAs before this one, and of all
+};
 struct ScanSmem {
-  int warp[2][kWarps];     // of this CTA's warps: exclusive sums
-  int total[2];            // of this CTA
-  int mine[2][kCluster];   // the CTAs' totals
-  int more;
+  int warp[2][kWarps];  // of this CTA's warps: exclusive sums of two numbers
+  int total[2];         // of this CTA
+  Totals sums;
 };
 
-// Exclusive sums over the CTA's warps of a number per warp (lane 0's), into
-// s.warp[which], the CTA's total into s.total[which].  For all threads.
-__device__ void scan_warps(ScanSmem& s, int which, int n) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) s.warp[which][warp] = n;
-  __syncthreads();
-  if (warp == 0) {
-    const int v = s.warp[which][lane];
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    s.warp[which][lane] = x - v;
-    if (lane == 31) s.total[which] = x;
-  }
-  __syncthreads();
-}
-
-// The CTAs' totals, after a barrier of the group: (those of the CTAs before this one, all).
-template <int C>
-__device__ int2 group_totals(ScanSmem& s, int which) {
-  if constexpr (C == 1) return make_int2(0, s.total[which]);
-  if (threadIdx.x < C) s.mine[which][threadIdx.x] = *cg::this_cluster().map_shared_rank(&s.total[which], threadIdx.x);
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < C; ++i) {
-    if (i < Group<C>::rank()) before += s.mine[which][i];
-    all += s.mine[which][i];
-  }
-  return make_int2(before, all);
-}
-
-// A warp's share of the pages: whole runs of 128 pages.
-struct Share {
-  int p0, p1;
-};
-template <int C>
-__device__ __forceinline__ Share share_of(int pages, int rank) {
-  const int runs = (pages + 127) / 128;
-  const int warps = C * kWarps, w = rank * kWarps + static_cast<int>(threadIdx.x >> 5);
-  const int each = runs / warps, extra = runs % warps;
-  Share s;
-  s.p0 = (w * each + min(w, extra)) * 128;
-  s.p1 = min(s.p0 + (each + (w < extra)) * 128, pages);
-  s.p0 = min(s.p0, pages);
-  return s;
-}
-// The counts of a lane's four pages from p on (past `end`: `fill`).
-__device__ __forceinline__ int4 counts_of(const int32_t* refs, int p, int end, int fill) {
-  if (p + 4 <= end) return *reinterpret_cast<const int4*>(refs + p);
-  int4 r = make_int4(fill, fill, fill, fill);
-  if (p < end) r.x = refs[p];
-  if (p + 1 < end) r.y = refs[p + 1];
-  if (p + 2 < end) r.z = refs[p + 2];
-  return r;
-}
-__device__ __forceinline__ int free_mask(int4 r) {
-  return (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
-}
 __device__ __forceinline__ int warp_sum(int n) { return __reduce_add_sync(0xffffffffu, n); }
 __device__ __forceinline__ int warp_before(int n) {  // exclusive sum over the lanes
   const int lane = threadIdx.x & 31;
@@ -137,37 +80,182 @@ __device__ __forceinline__ int warp_before(int n) {  // exclusive sum over the l
   return x - n;
 }
 
+// Exclusive sums over the CTA's warps of two numbers per warp into s.warp, the CTA's
+// totals into s.total.  For all threads.
+__device__ void scan_warps(ScanSmem& s, int n, int m) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane < 2) s.warp[lane][warp] = lane ? m : n;
+  __syncthreads();
+  if (warp < 2) {
+    const int v = s.warp[warp][lane], x = warp_before(v);
+    s.warp[warp][lane] = x;
+    if (lane == 31) s.total[warp] = x + v;
+  }
+  __syncthreads();
+}
+
+// The CTAs' totals, after a barrier of the group.
+template <int C>
+__device__ Totals group_totals(ScanSmem& s) {
+  Totals r;
+  if constexpr (C == 1) {
+    r.before[0] = r.before[1] = 0;
+    r.all[0] = s.total[0];
+    r.all[1] = s.total[1];
+  } else {
+    static_assert(2 * C <= 32, "a lane a number");
+    if (threadIdx.x < 32) {
+      const int which = threadIdx.x / C, cta = threadIdx.x % C;
+      const int x = which < 2 ? *cg::this_cluster().map_shared_rank(&s.total[which], cta) : 0;
+      const int low = cta < Group<C>::rank() ? x : 0;
+      const int before0 = warp_sum(which == 0 ? low : 0), before1 = warp_sum(which == 1 ? low : 0);
+      const int all0 = warp_sum(which == 0 ? x : 0), all1 = warp_sum(which == 1 ? x : 0);
+      if (threadIdx.x == 0) s.sums = {{before0, before1}, {all0, all1}};
+    }
+    __syncthreads();
+    r = s.sums;
+  }
+  return r;
+}
+
+// A warp's share of the pages: whole runs of 128 pages, four a lane.
+constexpr int kRun = 128;
+struct Share {
+  int p0, p1;
+};
+template <int C>
+__device__ __forceinline__ Share share_of(int pages, int rank) {
+  const int runs = (pages + kRun - 1) / kRun;
+  const int warps = C * kWarps, w = rank * kWarps + static_cast<int>(threadIdx.x >> 5);
+  const int each = runs / warps, extra = runs % warps;
+  Share s;
+  s.p0 = (w * each + min(w, extra)) * kRun;
+  s.p1 = min(s.p0 + (each + (w < extra)) * kRun, pages);
+  s.p0 = min(s.p0, pages);
+  return s;
+}
+// The counts of four pages from p on (past `end`: 1).
+__device__ __forceinline__ int4 counts_of(const int32_t* refs, int p, int end) {
+  if (p + 4 <= end) return *reinterpret_cast<const int4*>(refs + p);
+  int4 r = make_int4(1, 1, 1, 1);
+  if (p < end) r.x = refs[p];
+  if (p + 1 < end) r.y = refs[p + 1];
+  if (p + 2 < end) r.z = refs[p + 2];
+  return r;
+}
+// A lane's pages of the four runs from q on.
+struct Runs {
+  int4 r[4];
+  __device__ __forceinline__ void load(const int32_t* refs, int q, int end) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = counts_of(refs, page(q, i), end);
+  }
+  __device__ __forceinline__ static int page(int q, int i) { return q + i * kRun + (threadIdx.x & 31) * 4; }
+  // a bit for each free page of the i-th four
+  __device__ __forceinline__ unsigned free_mask(int i) const {
+    return (r[i].x == 0) | (r[i].y == 0) << 1 | (r[i].z == 0) << 2 | (r[i].w == 0) << 3;
+  }
+  __device__ __forceinline__ int free_pages() const {
+    return __popc(free_mask(0) | free_mask(1) << 4 | free_mask(2) << 8 | free_mask(3) << 12);
+  }
+};
+
 // Free pages of a warp's share (of the pages below `end`).
 __device__ int count_free(const int32_t* refs, const Share& sh, int end) {
-  const int lane = threadIdx.x & 31;
+  const int p1 = min(sh.p1, end);
   int n = 0;
-#pragma unroll 4
-  for (int p = sh.p0 + lane * 4; p < min(sh.p1, end); p += 128)
-    n += __popc(free_mask(counts_of(refs, p, min(sh.p1, end), 1)));
+  for (int q = sh.p0; q < p1; q += 8 * kRun) {  // (eight runs on their way)
+    Runs x, y;
+    x.load(refs, q, p1);
+    y.load(refs, q + 4 * kRun, p1);
+    n += x.free_pages() + y.free_pages();
+  }
   return warp_sum(n);
 }
 
-// The first `want` free pages of the pool, in order, into list; `rank` is that of
-// the warp's first free page.
-__device__ void list_free(const int32_t* refs, const Share& sh, int rank, int want, int32_t* list) {
-  const int lane = threadIdx.x & 31;
-  for (int q0 = sh.p0; q0 < sh.p1 && rank < want; q0 += 4 * 128) {
-    int m[4];
+// The pool in at most kSegments segments, whole runs, dealt out to the warps of all
+// CTAs in turn: the pages that a call takes, the lowest, are then everybody's work
+// (as consecutive shares they were that of the first CTAs: 13000 of 38000 clocks).
+constexpr int kSegments = kPageSegments;
+struct Segments {
+  int pages;  // of a segment
+  int count;
+};
+__device__ __forceinline__ Segments segments_of(int pages) {
+  Segments s;
+  const int runs = (pages + kRun - 1) / kRun, each = (runs + kSegments - 1) / kSegments;
+  s.pages = each * kRun;
+  s.count = (runs + each - 1) / each;
+  return s;
+}
+// Free pages of every segment, into counts.
+template <int C>
+__device__ void count_segments(const PageArgs& a, const Segments& g) {
+  constexpr int kAtOnce = 6;  // segments on their way
+  const int lane = threadIdx.x & 31, step = C * kWarps;
+  for (int i = static_cast<int>(threadIdx.x >> 5) * C + Group<C>::rank(); i < g.count; i += kAtOnce * step) {
+    int n[kAtOnce] = {};
+    for (int k = lane * 4; k < g.pages; k += kRun) {
+      int4 r[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = free_mask(counts_of(refs, q0 + i * 128 + lane * 4, sh.p1, 1));
+      for (int j = 0; j < kAtOnce; ++j)
+        r[j] = i + j * step < g.count ? counts_of(a.ref_counts, (i + j * step) * g.pages + k, a.num_blocks) : make_int4(1, 1, 1, 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = q0 + i * 128 + lane * 4, n = __popc(m[i]);
-      int at = rank + warp_before(n);
+      for (int j = 0; j < kAtOnce; ++j) n[j] += (r[j].x == 0) + (r[j].y == 0) + (r[j].z == 0) + (r[j].w == 0);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (m[i] >> j & 1) {
-          if (at < want) list[at] = p + j;
-          ++at;
-        }
-      rank += warp_sum(n);
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int all = warp_sum(n[j]);
+      if (lane == 0 && i + j * step < g.count) a.counts[i + j * step] = all;
     }
   }
+}
+// After a barrier of the group: the free pages before each segment into before;
+// returns how many there are.
+__device__ int scan_segments(const PageArgs& a, const Segments& g, ScanSmem& s, int* before) {
+  static_assert(kSegments == 4 * kThreads, "four a thread");
+  const int i = static_cast<int>(threadIdx.x) * 4;
+  int n[4], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    n[j] = i + j < g.count ? a.counts[i + j] : 0;
+    sum += n[j];
+  }
+  const int lanes = warp_before(sum);
+  scan_warps(s, __shfl_sync(0xffffffffu, lanes + sum, 31), 0);
+  int at = s.warp[0][threadIdx.x >> 5] + lanes;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    before[i + j] = at;
+    at += n[j];
+  }
+  __syncthreads();
+  return s.total[0];
+}
+
+// The first `want` free pages of a share, in order, into list; `rank` is that of its
+// first free page.
+__device__ void list_free(const int32_t* refs, const Share& sh, int rank, int want, int32_t* list) {
+  for (int q = sh.p0; q < sh.p1 && rank < want; q += kRun) {
+    const int p = q + (threadIdx.x & 31) * 4;
+    const int4 r = counts_of(refs, p, sh.p1);
+    const int c[4] = {r.x, r.y, r.z, r.w}, n = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+    int at = rank + warp_before(n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c[j] == 0) {
+        if (at < want) list[at] = p + j;
+        ++at;
+      }
+    rank += warp_sum(n);
+  }
+}
+
+// The first `want` free pages of the pool, in order, into a.list.
+template <int C>
+__device__ void list_segments(const PageArgs& a, const Segments& g, const int* before, int want) {
+  for (int i = static_cast<int>(threadIdx.x >> 5) * C + Group<C>::rank(); i < g.count && before[i] < want; i += C * kWarps)
+    list_free(a.ref_counts, {i * g.pages, min((i + 1) * g.pages, a.num_blocks)}, before[i], want, a.list);
 }
 
 // ---------------------------------------------------------------- alloc
@@ -183,75 +271,108 @@ __device__ __forceinline__ Range range_of(const PageArgs& a, int b) {
   return r;
 }
 
-// (dynamic shared memory: the needs of the CTA's rows, then their exclusive sums;
-// -1: a row that is refused)
+// A row is cut into a.cuts pieces of a.piece entries from its range's first on, a
+// warp a piece.  Dynamic shared memory: the pieces' needs (-1: an entry that names
+// nothing), the rows' places in the list (-1: refused, -2: without a page) and ranges.
 template <int C>
 __global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
   extern __shared__ int need[];
-  __shared__ ScanSmem s;
+  __shared__ ScanSmem s, of_segments;
+  __shared__ int free_before[kSegments];
   const int rank = Group<C>::rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Share sh = share_of<C>(a.num_blocks, rank);
-  const int mine = count_free(a.ref_counts, sh, a.num_blocks);
+  const Segments g = segments_of(a.num_blocks);
   const int each = (a.rows + C - 1) / C;
-  const int b0 = min(rank * each, a.rows), n = min(each, a.rows - b0);
-  // how many entries of each row lack a page
-  for (int i = warp; i < n; i += kWarps) {
+  const int b0 = min(rank * each, a.rows), n = min(each, a.rows - b0), pieces = n * a.cuts;
+  int* place = need + each * a.cuts;
+  int* first = place + each;
+  int* last = first + each;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const Range r = range_of(a, b0 + i);
-    const int32_t* row = a.block_table + static_cast<size_t>(b0 + i) * a.width;
-    int lack = 0;
-    bool bad = r.code != kOk;
-#pragma unroll 8
-    for (int t = r.t0 + lane; t < r.t1; t += 32) {
-      const int e = row[t];
-      lack += e < 0;
-      bad |= e >= a.num_blocks;
-    }
-    lack = warp_sum(lack);
-    if (__any_sync(0xffffffffu, bad)) lack = -1;
-    if (lane == 0) need[i] = lack;
+    first[i] = r.code == kOk ? r.t0 : -1;
+    last[i] = r.t1;
   }
-  scan_warps(s, 0, mine);
+  count_segments<C>(a, g);
+  __syncthreads();
+  // how many entries of each piece lack a page
+  for (int i = warp; i < pieces; i += kWarps) {
+    const int b = i / a.cuts, q0 = first[b] + (i - b * a.cuts) * a.piece, q1 = min(q0 + a.piece, last[b]);
+    int lack = 0;
+    bool bad = first[b] < 0;
+    if (!bad && q0 < q1) {
+      const int32_t* row = a.block_table + static_cast<size_t>(b0 + b) * a.width;
+      for (int t = q0 + lane; t < q1; t += 32 * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) e[j] = t + j * 32 < q1 ? row[t + j * 32] : 0;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          lack += e[j] < 0;
+          bad |= e[j] >= a.num_blocks;
+        }
+      }
+      lack = warp_sum(lack);
+      bad = __any_sync(0xffffffffu, bad);
+    }
+    if (lane == 0) need[i] = bad ? -1 : lack;
+  }
+  __syncthreads();
   // exclusive sums of the rows' needs: a run of rows per thread
   const int run = (n + kThreads - 1) / kThreads, i0 = min(static_cast<int>(threadIdx.x) * run, n), i1 = min(i0 + run, n);
   int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += max(need[i], 0);
-  const int before = warp_before(sum);
-  scan_warps(s, 1, __shfl_sync(0xffffffffu, before + sum, 31));
-  Group<C>::sync();
-  const int2 free_pages = group_totals<C>(s, 0), needed = group_totals<C>(s, 1);
-  if (needed.y > 0) list_free(a.ref_counts, sh, free_pages.x + s.warp[0][warp], min(needed.y, free_pages.y), a.list);
-  // rows in order, each with its place in the list
-  int at = needed.x + s.warp[1][warp] + before;
   for (int i = i0; i < i1; ++i) {
-    const int lack = need[i];
-    // as its place: refused -1, without a page -2
-    need[i] = lack < 0 ? -1 : lack > 0 && lack > free_pages.y - at ? -2 : at;
+    int lack = 0;
+    bool bad = false;
+    for (int k = 0; k < a.cuts; ++k) {
+      const int x = need[i * a.cuts + k];
+      bad |= x < 0;
+      lack += x;
+    }
+    place[i] = bad ? -1 : lack;
+    sum += bad ? 0 : lack;
+  }
+  const int before = warp_before(sum);
+  scan_warps(s, 0, warp_sum(sum));
+  Group<C>::sync();
+  const Totals needs = group_totals<C>(s);
+  const int wanted = needs.all[1], own = needs.before[1] + s.warp[1][warp] + before;
+  int frees = 0;
+  if (wanted > 0) {  // (a decode step mostly finds nothing lacking)
+    frees = scan_segments(a, g, of_segments, free_before);
+    list_segments<C>(a, g, free_before, min(wanted, frees));
+  }
+  int at = own;
+  for (int i = i0; i < i1; ++i) {
+    const int lack = place[i];
+    place[i] = lack < 0 ? -1 : lack > 0 && lack > frees - at ? -2 : at;
     at += max(lack, 0);
   }
   Group<C>::sync();  // the list is written, and no CTA reads another's shared memory any more
-  for (int i = warp; i < n; i += kWarps) {
-    const int b = b0 + i;
-    int place = need[i];
-    if (lane == 0) a.status[b] = place == -1 ? kBadTree : place == -2 ? kNoPage : kOk;
-    if (place < 0 || needed.y == 0) continue;
-    const Range r = range_of(a, b);
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    a.status[b0 + i] = place[i] == -1 ? kBadTree : place[i] == -2 ? kNoPage : kOk;
+  if (wanted == 0) return;
+  for (int i = warp; i < pieces; i += kWarps) {
+    const int k = i % a.cuts, b = b0 + i / a.cuts;
+    int from = place[i / a.cuts];
+    if (from < 0 || need[i] == 0) continue;
+    for (int j = 0; j < k; ++j) from += need[i - k + j];
+    const int q0 = first[i / a.cuts] + k * a.piece, q1 = min(q0 + a.piece, last[i / a.cuts]);
     int32_t* row = a.block_table + static_cast<size_t>(b) * a.width;
-    for (int q = r.t0; q < r.t1; q += 32 * kAhead) {
+    for (int q = q0; q < q1; q += 32 * kAhead) {
       bool lacks[kAhead];
-      int from[kAhead], page[kAhead];
+      int at_list[kAhead], page[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int t = q + j * 32 + lane;
-        lacks[j] = t < r.t1 && row[t] < 0;
+        lacks[j] = t < q1 && row[t] < 0;
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const unsigned m = __ballot_sync(0xffffffffu, lacks[j]);
-        from[j] = place + __popc(m & ((1u << lane) - 1));
-        place += __popc(m);
+        at_list[j] = from + __popc(m & ((1u << lane) - 1));
+        from += __popc(m);
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) page[j] = lacks[j] ? a.list[from[j]] : 0;
+      for (int j = 0; j < kAhead; ++j) page[j] = lacks[j] ? a.list[at_list[j]] : 0;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
         if (lacks[j]) {
@@ -366,18 +487,18 @@ __device__ bool fork_row(const PageArgs& a, int i, int first, int step) {
 // with ROWS the rows too.
 template <int C, bool ROWS>
 __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PageArgs a) {
-  __shared__ ScanSmem s;
+  __shared__ ScanSmem s, of_segments;
+  __shared__ int free_before[kSegments];
   const int rank = Group<C>::rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = rank * kThreads + threadIdx.x; i < a.rows; i += C * kThreads) a.first[i] = INT_MAX;
-  const Share sh = share_of<C>(a.num_blocks, rank);
-  const int mine = count_free(a.ref_counts, sh, a.num_blocks);
+  const Segments g = segments_of(a.num_blocks);
+  count_segments<C>(a, g);
   Group<C>::sync();
   for (int i = rank * kThreads + threadIdx.x; i < a.new_rows; i += C * kThreads) {
     const Child c = child_of(a, i);
     if (c.code == kOk && c.parent >= 0) atomicMin(a.first + c.parent, i);
   }
-  scan_warps(s, 0, mine);
   Group<C>::sync();
   // a run of children per thread: how many of them need a page
   const int each = (a.new_rows + C - 1) / C;
@@ -399,12 +520,15 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PageArgs a) {
     sum += src >= 0;
   }
   const int before = warp_before(sum);
-  scan_warps(s, 1, __shfl_sync(0xffffffffu, before + sum, 31));
+  scan_warps(s, 0, warp_sum(sum));
   Group<C>::sync();
-  const int2 free_pages = group_totals<C>(s, 0), needed = group_totals<C>(s, 1);
-  if (needed.y > 0) list_free(a.ref_counts, sh, free_pages.x + s.warp[0][warp], min(needed.y, free_pages.y), a.list);
-  Group<C>::sync();
-  int at = needed.x + s.warp[1][warp] + before;
+  const Totals needs = group_totals<C>(s);
+  int at = needs.before[1] + s.warp[1][warp] + before, frees = 0;
+  if (needs.all[1] > 0) {
+    frees = scan_segments(a, g, of_segments, free_before);
+    list_segments<C>(a, g, free_before, min(needs.all[1], frees));
+  }
+  Group<C>::sync();  // the list is written, and no CTA reads another's shared memory any more
   for (int i = i0; i < i1; ++i) {
     const int b = b0 + i;
     const Child c = child_of(a, b);
@@ -412,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PageArgs a) {
     const int src = copy[0];
     int code = src == -2 ? kBadTree : c.code, dst = -1;
     if (src >= 0) {
-      if (at < free_pages.y) {
+      if (at < frees) {
         dst = a.list[at];
         a.ref_counts[dst] = 1;
       } else {
@@ -447,46 +571,45 @@ template <int C>
 __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PageArgs a) {
   __shared__ ScanSmem s;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rank = Group<C>::rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = Group<C>::rank(), warp = threadIdx.x >> 5;
   const Share sh = share_of<C>(a.num_blocks, rank);
-  scan_warps(s, 0, count_free(a.ref_counts, sh, a.num_blocks));
+  const int mine = count_free(a.ref_counts, sh, a.num_blocks);
+  scan_warps(s, mine, 0);
   Group<C>::sync();
-  const int2 free_pages = group_totals<C>(s, 0);
-  const int live = a.num_blocks - free_pages.y;
+  const Totals free_pages = group_totals<C>(s);
+  const int live = a.num_blocks - free_pages.all[0], first = free_pages.before[0] + s.warp[0][warp];
   // the holes: free pages below `live`, as many as pages in use from there on
-  scan_warps(s, 1, count_free(a.ref_counts, sh, live));
+  scan_warps(s, mine, count_free(a.ref_counts, sh, live));  // (another CTA may read the first total still: it stays)
   Group<C>::sync();
-  const int holes = group_totals<C>(s, 1).y;
-  int frees = free_pages.x + s.warp[0][warp];
-  for (int q = sh.p0; q < sh.p1; q += 128) {
-    const int p = q + lane * 4;
-    const int4 r = counts_of(a.ref_counts, p, sh.p1, 1);
-    const int m = free_mask(r), n = __popc(m);
+  const int holes = group_totals<C>(s).all[1];
+  int frees = first;
+  for (int q = sh.p0; q < sh.p1; q += kRun) {
+    const int p = q + static_cast<int>(threadIdx.x & 31) * 4;
+    const int4 r = counts_of(a.ref_counts, p, sh.p1);
+    const int c[4] = {r.x, r.y, r.z, r.w}, n = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     int f = frees + warp_before(n);  // free pages before this one
-    const int count[4] = {r.x, r.y, r.z, r.w};
+    int to[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int page = p + j;
-      if (page >= sh.p1) break;
-      const bool is_free = m >> j & 1;
-      if (page < live) {
-        a.page_map[page] = is_free ? -1 : page;
-        if (is_free) {
-          a.copies[3 * static_cast<size_t>(f) + 1] = page;
-          a.copies[3 * static_cast<size_t>(f) + 2] = kPage;
-        } else {
-          a.refs_out[page] = count[j];
-        }
-      } else {
-        if (is_free) {
-          a.page_map[page] = -1;
-          a.refs_out[page] = 0;
-        } else {
-          // pages in use from `live` on, before this one
-          a.copies[3 * static_cast<size_t>(page - live - (f - holes))] = page;
-        }
+      const bool is_free = c[j] == 0;
+      // (a page in use from `live` on gets its number below, past a barrier)
+      to[j] = !is_free && page < live ? page : -1;
+      if (is_free && page < live) {
+        a.copies[3 * static_cast<size_t>(f) + 1] = page;
+        a.copies[3 * static_cast<size_t>(f) + 2] = kPage;
+      } else if (!is_free && page >= live && page < sh.p1) {
+        a.copies[3 * static_cast<size_t>(page - live - (f - holes))] = page;
       }
       f += is_free;
+    }
+    if (p + 4 <= sh.p1) {
+      *reinterpret_cast<int4*>(a.page_map + p) = make_int4(to[0], to[1], to[2], to[3]);
+      *reinterpret_cast<int4*>(a.refs_out + p) = r;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (p + j < sh.p1) a.page_map[p + j] = to[j], a.refs_out[p + j] = c[j];
     }
     frees += warp_sum(n);
   }
@@ -622,13 +745,21 @@ int ctas_for(const PageArgs& a, int most) {
 
 }  // namespace
 
-int launch_alloc_pages(const PageArgs& a, cudaStream_t stream) {
-  static_assert(65536 / 8 * 4 <= 40 * 1024, "no opt-in");
-  const int ctas = ctas_for(a, 16384);
-  const size_t smem = static_cast<size_t>((a.rows + ctas - 1) / ctas) * 4;
-  return ctas == 1   ? launch_group<1>(alloc_kernel<1>, a, smem, stream)
-         : ctas == 8 ? launch_group<8>(alloc_kernel<8>, a, smem, stream)
-                     : launch_group<kCluster>(alloc_kernel<kCluster>, a, smem, stream);
+int launch_alloc_pages(PageArgs a, cudaStream_t stream) {
+  const int ctas = ctas_for(a, 16384), each = (a.rows + ctas - 1) / ctas;
+  // pieces of a row: of 256 entries (what a warp has in flight) at least, as many as a
+  // CTA has room for
+  int cuts = (a.width + 255) / 256;
+  cuts = cuts < kMaxCuts ? cuts : kMaxCuts;
+  a.cuts = cuts < kNeeds / each ? cuts : (kNeeds / each > 1 ? kNeeds / each : 1);
+  a.piece = (a.width + a.cuts - 1) / a.cuts;
+  const size_t smem = static_cast<size_t>(each) * (a.cuts + 3) * 4;  // (65536 rows are 8192 for each of 8 CTAs: 128 KB)
+  const auto kernel = ctas == 1 ? alloc_kernel<1> : ctas == 8 ? alloc_kernel<8> : alloc_kernel<kCluster>;
+  if (smem > 24 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return -1;
+  return ctas == 1   ? launch_group<1>(kernel, a, smem, stream)
+         : ctas == 8 ? launch_group<8>(kernel, a, smem, stream)
+                     : launch_group<kCluster>(kernel, a, smem, stream);
 }
 
 int launch_free_pages(const PageArgs& a, cudaStream_t stream) {

@@ -1043,8 +1043,16 @@ tv::PageArgs page_args(const tv_page_params* p, const int32_t* block_table, cons
   return a;
 }
 
-// (free pages in order, then the first child of every row)
+// Bytes of the workspace's first two parts, whole 256 each: free pages in order, and
+// the first child of every row; the counts of the pool's segments follow.
 size_t page_list_bytes(const tv_page_params* p) { return (static_cast<size_t>(p->num_blocks) * 4 + 255) / 256 * 256; }
+size_t page_first_bytes(const tv_page_params* p) { return (static_cast<size_t>(p->rows) * 4 + 255) / 256 * 256; }
+void page_workspace(const tv_page_params* p, void* workspace, tv::PageArgs* a) {
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  a->list = reinterpret_cast<int32_t*>(at);
+  a->first = reinterpret_cast<int32_t*>(at + page_list_bytes(p));
+  a->counts = reinterpret_cast<int32_t*>(at + page_list_bytes(p) + page_first_bytes(p));
+}
 
 template <size_t N>
 bool all_given(const void* const (&ptrs)[N]) {
@@ -1056,7 +1064,7 @@ bool all_given(const void* const (&ptrs)[N]) {
 }  // namespace
 
 size_t tv_pages_workspace_size(const tv_page_params* p) {
-  return pages_valid(p) ? page_list_bytes(p) + static_cast<size_t>(p->rows) * 4 : 0;
+  return pages_valid(p) ? page_list_bytes(p) + page_first_bytes(p) + tv::kPageSegments * 4 : 0;
 }
 
 int tv_alloc_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_counts,
@@ -1072,7 +1080,7 @@ int tv_alloc_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_c
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
   a.begin = begin;
   a.end = end;
-  a.list = static_cast<int32_t*>(workspace);
+  page_workspace(p, workspace, &a);
   return tv::launch_alloc_pages(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }
 
@@ -1113,8 +1121,7 @@ int tv_fork_pages(const tv_page_params* p, const int32_t* block_table,
   a.table_out = block_table_out;
   a.lens_out = seq_lens_out;
   a.copies = copies;
-  a.list = static_cast<int32_t*>(workspace);
-  a.first = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + page_list_bytes(p));
+  page_workspace(p, workspace, &a);
   return tv::launch_fork_pages(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }
 

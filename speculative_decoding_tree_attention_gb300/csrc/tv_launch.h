@@ -266,9 +266,12 @@ struct PageArgs {
   int32_t* status;            // [rows], fork: [new_rows]
   int32_t* list;              // workspace: free pages in order
   int32_t* first;             // workspace: fork: [rows] first child of a row
+  int32_t* counts;            // workspace: [kPageSegments] free pages of the pool's segments
   int32_t rows, new_rows, width, num_blocks, sinks;
+  int32_t cuts, piece;        // alloc: pieces of a row and their entries (set by the launcher)
 };
-int launch_alloc_pages(const PageArgs& a, cudaStream_t stream);
+constexpr int kPageSegments = 4096;
+int launch_alloc_pages(PageArgs a, cudaStream_t stream);
 int launch_free_pages(const PageArgs& a, cudaStream_t stream);
 int launch_fork_pages(const PageArgs& a, cudaStream_t stream);
 int launch_compact_pages(const PageArgs& a, cudaStream_t stream);

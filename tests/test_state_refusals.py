@@ -164,7 +164,8 @@ def test_page_arguments_of_one_call(lib):
 def test_page_pointers_and_workspace(lib):
     p = pages()
     need = lib.tv_pages_workspace_size(C.byref(p))
-    assert need == 512 + 16  # a list of all pages, rounded to 256 bytes, and a word a row
+    # a list of all pages, a word a row (256 bytes at least each), 4096 words
+    assert need == 512 + 256 + 4096 * 4
     size = C.c_size_t(need)
     each_pointer(5, {0, 1, 3, 4}, lambda a: lib.tv_alloc_pages(C.byref(p), *a, at(9), size, None))
     each_pointer(5, {0, 1, 4}, lambda a: lib.tv_free_pages(C.byref(p), *a, None))
