@@ -259,11 +259,9 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
   float c = -m * kLog2eHi;
   float2 acc = make_float2(0.0f, 0.0f);
   __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i * 32 * kWords < words) fetch_words<BF16>(p, i * 32 * kWords, l.ring[i]);
-    commit_words();
-  }
+  static_assert(kStages == 2, "one stage ahead");
+  if (SAFE) fetch_words<BF16>(p, 0, l.ring[0]);  // (else the caller's)
+  commit_words();
   for (int w0 = 0, turn = 0; w0 < words; w0 += 32 * kWords, ++turn) {
     const int ahead = w0 + (kStages - 1) * 32 * kWords;
     if (ahead < words) fetch_words<BF16>(p, ahead, l.ring[(turn + kStages - 1) % kStages]);
@@ -294,7 +292,7 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
       }
       m = top;
     }
-    if ((turn & (turn + 1)) == 0) {  // (turns 0, 1, 3, 7, ..)
+    if (turn < 4 || turn % 4 == 3) {
       float unused;
       const float nth = give <= 32 ? nth_largest(high, give, unused) : -INFINITY;
       if (lane == 0) reinterpret_cast<volatile float*>(bounds)[warp] = nth;
@@ -392,13 +390,18 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
     return;
   }
   if (warp >= warps) return;
-  if (a.finished && a.finished[row] != 0) return;
-  if (!(a.scores[row] > -INFINITY)) return;      // (nothing, or NaN: the merge sees it)
+  const int ended = a.finished ? a.finished[row] : 0;
+  const float score = a.scores[row];
   Part<BF16> p;
   p.base = static_cast<const uint8_t*>(a.logits) + static_cast<size_t>(row) * a.stride * (16 / p.kEach);
   p.c0 = min(part * a.chunk, a.vocab), p.c1 = min(p.c0 + a.chunk, a.vocab);
   p.start = p.c0 - static_cast<int>((reinterpret_cast<uintptr_t>(p.base + static_cast<size_t>(p.c0) * (16 / p.kEach)) & 15) / (16 / p.kEach));
   List& l = lists[warp];
+  fetch_words<BF16>(p, 0, l.ring[0]);  // (on their way while the row's state arrives)
+  if (ended != 0 || !(score > -INFINITY)) {  // (nothing, or NaN: the merge sees it)
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   float m, sum;
   int count;
   if (!part_pass<BF16, false>(p, l, &bounds, warps, a.select, m, sum, count))
