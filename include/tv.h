@@ -676,9 +676,9 @@ int tv_penalize_logits(const tv_penalty_params* params, const void* logits,
  * ====================================================================== */
 #define TV_MAX_POSITION_AXES 4
 typedef struct {
-  int32_t tokens;         /* T rows; 0 enqueues nothing                         */
-  int32_t num_q_heads;    /* Hq >= 1                                            */
-  int32_t num_kv_heads;   /* Hkv >= 0 (0: queries alone)                        */
+  int32_t tokens;         /* T rows, <= 2^30; 0 enqueues nothing                */
+  int32_t num_q_heads;    /* 1 <= Hq <= 2^20; T * (Hq + Hkv) < 2^40             */
+  int32_t num_kv_heads;   /* 0 <= Hkv <= 2^20 (0: queries alone)                */
   int32_t head_dim;       /* D: 64 or 128                                       */
   int32_t rotary_dim;     /* R: even, 0 <= R <= D (0: norms alone)              */
   int32_t interleaved;    /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1)       */

@@ -472,10 +472,10 @@ def beam_select(logits, scores, beams, select, lengths=None, finished=None, end_
                 bad = True
             if bad or x.max() == -np.inf:
                 continue
-            lse = x.max() + math.log(np.exp(x - x.max()).sum())
+            total = math.log(np.exp(x - x.max()).sum())
             for v in np.lexsort((np.arange(len(x)), -x))[:select]:
                 if x[v] > -np.inf:
-                    d = s + float(x[v]) - lse
+                    d = s + (float(x[v] - x.max()) - total)  # (the maximum off first: it may be 1e38)
                     found.append((d / max(n + 1, 1) ** length_penalty, r, int(v), d, n + 1, int(v == end_token)))
         if bad:
             out.append(None)

@@ -1120,9 +1120,9 @@ def _beam_params(logits, beams, select, end_token, length_penalty):
 
 
 def beam_workspace_size(logits, *, beams: int, select: int | None = None) -> int:
-    """Bytes of the workspace of a beam_select call."""
+    """Bytes of the workspace of a beam_select call on the logits' device."""
     prm = _beam_params(logits, beams, beams if select is None else select, -1, 0.0)
-    return int(load().tv_beam_select_workspace_size(C.byref(prm)))
+    return _run(_device("logits", logits), None, lambda _: int(load().tv_beam_select_workspace_size(C.byref(prm))))
 
 
 def beam_select(logits, scores, *, beams: int, select: int | None = None, lengths=None, finished=None,

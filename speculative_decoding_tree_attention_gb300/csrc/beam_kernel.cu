@@ -8,30 +8,35 @@
 // key = d / max(len, 1)^alpha, then the lower beam, then the lower token.
 //
 // One pass over the logits.  beam_rows_kernel: a warp takes a part of a row, four
-// 16-byte words a lane at a time.  Each lane keeps a running maximum and the sum of
-// exps against it.  Entries from a bound on go to the warp's list in shared memory.
-// The bound: if of W warps each has c lanes whose largest entry so far is at least
-// t, and W c >= S, S entries of the row at least are no worse than t; the 8 warps of
-// a CTA, which work on one row, take the least of their c-th largest.  So after the
-// first words the bound is near the S-th best of what eight warps have seen, and few
-// entries pass it: most words cost their exps, a packed maximum and one comparison.
-// (A bound of the
-// warp's own let 22 entries of every 1024 pass it: 62 us instead of .. below.)  Bounds rise with time and differ from run to run, the
-// S best do not: they pass every bound.  Within a row the order is exact: it is that
-// of the logits, and of equal ones the lower token.
+// 16-byte words a lane at a time, the next four on their way to shared memory.  Each
+// lane keeps a running maximum and the sum of exps against it.  Entries from a bound
+// on go to the warp's list in shared memory.  The bound: if of W warps each has c
+// lanes whose largest entry so far is at least t, and W c >= S, S entries of the row
+// at least are no worse than t; the 8 warps of a CTA, which work on one row, take the
+// least of their c-th largest.  So after the first words the bound is near the S-th
+// best of what eight warps have seen, and few entries pass it: most words cost their
+// exps, a packed maximum and one comparison; one that has an entry from the bound on
+// is looked at by all lanes, an entry a lane.  (Bounds rise with time and differ from
+// run to run, the S best do not: they pass every bound.)  Within a row the order is
+// exact: it is that of the logits, and of equal ones the lower token.
 //
 // beam_merge_kernel: a CTA per request joins the parts of each row to its LSE
 // and picks the S best of all rows' lists the same way: in fp32 with an error
 // bound that keeps every candidate that may be among them, those few in fp64.
 //
-// LSE: exps and their sums in fp32 against the part's own maximum (x - m rounded
-// once, its product with log2 e in two pieces), joined in fp32 and added to m in
-// fp64: off by about 1e-7, less than the rounding of a score near 20 to fp32
-// (1e-6).  Candidates of different beams that lie closer than that may come in
-// either order, the same in every call.
+// LSE: exps and their sums in fp32 against the lane's own maximum, joined in fp32
+// and added to the maximum in fp64: off by about 1e-7, less than the rounding of a
+// score near 20 to fp32 (1e-6).  Candidates of different beams that lie closer than
+// that may come in either order, the same in every call.
 //
-// Bound: HBM, one read of the logits; for few requests the latency of two
-// dependent kernels.
+// Bound: instruction issue (68 % busy) at half of the HBM rate; for few requests the
+// latency of two dependent kernels.  Measured (device time, the call replayed): 64
+// requests of 8 beams, V = 128256, bf16, S = 16: 38.3 us (3.3 TB/s); 1 of 4, V = 32000,
+// fp32: 10.3 us.  On the way, the first case: a CTA per 8192 entries, entries in
+// registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
+// bound (22 of every 1024 entries passed it) 71; the shared bound, entries pushed by
+// the lanes that have them 53 (a third of the instructions were theirs, and they
+// spilled); words from shared memory, looked at by all lanes 39.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -417,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
 enum State { kDead, kLive, kEnded };
 
 struct MergeSmem {
-  double base[kMaxBeams];    // score - LSE; of an ended beam the score
+  double base[kMaxBeams];    // score - log sum; of an ended beam the score
+  float top[kMaxBeams];      // the row's maximum
   double inverse[kMaxBeams]; // 1 / len^alpha
   unsigned long long key[kFound + kMaxBeams];  // in the order of the keys' values
   float value[kFound + kMaxBeams];             // logit
@@ -518,8 +524,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
         // log of sum = 2^e f with f in [1, 2)
         const int e = (__float_as_int(sum) >> 23) - 127;
         const float f = __int_as_float(__float_as_int(sum) - (e << 23));
-        s.base[k] -= static_cast<double>(m) + e * 0.69314718055994531 + static_cast<double>(logf(f));
+        s.base[k] -= e * 0.69314718055994531 + static_cast<double>(logf(f));
       }
+      s.top[k] = m;
       s.inverse[k] = inverse;
       s.approx[k] = make_float2(static_cast<float>(s.base[k]), static_cast<float>(inverse));
     }
@@ -545,10 +552,13 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   // a key in fp32, and how far that may be off
   const auto approx = [&](float x, int k, float& off) {
     const float2 p = s.approx[k];
-    off = p.y * (0x1p-22f * (fabsf(x) + fabsf(p.x)));
-    return (x + p.x) * p.y;
+    const float d = x - s.top[k];
+    off = p.y * (0x1p-22f * (fabsf(d) + fabsf(p.x)));
+    return (d + p.x) * p.y;
   };
-  const auto key_of = [&](float x, int k) { return ordered_key((s.base[k] + static_cast<double>(x)) * s.inverse[k]); };
+  // (the maximum off first: rows of the type's lowest value have scores too)
+  const auto score_of = [&](float x, int k) { return s.base[k] + (static_cast<double>(x) - static_cast<double>(s.top[k])); };
+  const auto key_of = [&](float x, int k) { return ordered_key(score_of(x, k) * s.inverse[k]); };
   const auto keep = [&](float2 e, int k) {
     const int at = atomicAdd(&s.found, 1);
     if (at < kFound + kMaxBeams) {
@@ -616,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     const int token = ended ? a.end_token : at & ((1 << 18) - 1);
     a.tokens[o] = token;
     a.parents[o] = static_cast<int>(row);
-    a.scores_out[o] = static_cast<float>(ended ? s.base[k] : s.base[k] + static_cast<double>(x));
+    a.scores_out[o] = static_cast<float>(ended ? s.base[k] : score_of(x, k));
     if (a.lengths_out) a.lengths_out[o] = a.lengths[row] + (ended ? 0 : 1);
     if (a.finished_out) a.finished_out[o] = ended || (a.end_token >= 0 && token == a.end_token);
   };

@@ -9,15 +9,20 @@
 //
 // Giving pages out needs two scans, of the free pages and of the rows' needs,
 // that meet: the k-th page needed is the k-th free one.  One cluster of 8 or 16 CTAs
-// does both: every CTA counts a slice of the pages and of the rows, the totals go
-// through distributed shared memory, the free pages' numbers through the caller's
-// workspace, with a cluster barrier between; one launch, and the slices are
-// read from the same L2.  A small pool takes one CTA and its own barriers.  What
-// touches whole tables (a release, the rows of a fork, the new numbers of a
-// compaction) is a kernel with a CTA per row, but for the rows of a small fork.
+// does both: the rows' needs are scanned by runs of rows, their totals exchanged
+// through distributed shared memory; the pool is counted in segments that are dealt
+// out to all warps, and the segments' counts and the free pages' numbers go through
+// the caller's workspace, with cluster barriers between.  A small pool takes one CTA
+// and its own barriers.  What touches whole tables (a release, the rows of a fork,
+// the new numbers of a compaction) is a kernel with a CTA per row, but for the rows
+// of a small fork; it is set up while the plan before it ends.
 //
-// Bound: latency (three dependent passes and two cluster barriers) for small
-// pools; the cluster's reads of the counts for large ones; HBM for the copies.
+// Bound: latency (dependent passes and barriers) for small pools; the cluster's reads
+// of the counts for large ones; HBM for the copies.  Measured (device time, the calls
+// replayed): 32 of 512 rows of up to 2048 entries replaced, 690000 pages: free and
+// alloc 22 us; a fork of 512 rows of 290 entries with its copies 17.4 us; 2100 pages of
+// 64 KB moved: plan, tables and copies 57 us, the copies at 6.8 TB/s.  Each CTA with a
+// share of consecutive pages, a warp per row: 27 us for the first.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -735,9 +740,10 @@ int launch_behind(void (*kernel)(Args), const Args& a, unsigned grid, unsigned t
 }
 
 // How many CTAs: one for a pool that it reads in a few loads a thread, `most` pages
-// (which spares two cluster barriers, about 2 us; its work behind the counts differs
-// by kernel), 8 up to 2^18 pages, then 16 (512 rows over 650000 pages: alloc 31 us
-// with 8, 23 with 16; 8 rows over 4000 pages: 10 us with 8, 12 with 16).
+// (which spares the cluster barriers: 16 rows over 3500 pages 8.3 us instead of 11
+// with free_pages; its work behind the counts differs by kernel: a fork over 17400
+// pages 17.4 us, with 8 CTAs 18.5; a compaction of 8400 pages 58.9, with 8 57.4), 8 up
+// to 2^18 pages, then 16 (512 rows over 690000 pages 36 us, with 16 27).
 int ctas_for(const PageArgs& a, int most) {
   if (a.num_blocks <= most && a.rows <= kThreads && a.new_rows <= kThreads) return 1;
   return a.num_blocks < (1 << 18) ? 8 : kCluster;

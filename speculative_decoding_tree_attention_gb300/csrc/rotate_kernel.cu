@@ -22,8 +22,14 @@
 // cosine of the token's pairs are computed once, a lane a pair, and joined with the
 // weights: with A = w_a cos, B = w_b sin, C = w_a sin, D = w_b cos a pair costs two
 // products, two fused ones and two products by the root, two values an instruction.
-// The first rows are on their way meanwhile.  Bound: HBM, one read and one write of
-// each row; latency for single tokens.
+// The first rows are on their way meanwhile.
+//
+// Bound: HBM, one read and one write of each row; latency for single tokens.
+// Measured (device time, the call replayed, norms): 8192 tokens of 64/8 heads of 128
+// 57 us (5.3 TB/s, 0.78 of the copy rate), 16 tokens of 32/8 heads 4.2 us.  With sines
+// by every lane for its own pairs and norm, weights and rotation one after the other
+// 80 us; with the next rows loaded ahead of the present ones' arithmetic 60 (fewer
+// warps fit), two or four rows in flight instead of three 60 and 57.
 #include "tv_device.cuh"
 #include "tv_launch.h"
 
@@ -181,7 +187,7 @@ __device__ __forceinline__ void fill_turn(const Shared& s, int key, int sub, int
 template <int D, Layout L, bool ALL>
 __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows that a warp takes at once
-  constexpr int kUnroll = 3;
+  constexpr int kUnroll = 3;  // rows of a lane in flight
   __shared__ Shared s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
   const int rot = a.rotary_dim;

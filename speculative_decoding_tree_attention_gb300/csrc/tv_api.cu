@@ -887,7 +887,7 @@ int tv_rotate_qk(const tv_rotate_params* p, const uint16_t* q, const uint16_t* k
                  cudaStream_t stream) {
   if (!p) return TV_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return TV_ERR_UNSUPPORTED;
-  if (p->tokens < 0 || p->num_q_heads < 1 || p->num_kv_heads < 0) return TV_ERR_INVALID_ARG;
+  if (p->tokens < 0 || p->tokens > (1 << 30) || p->num_q_heads < 1 || p->num_kv_heads < 0) return TV_ERR_INVALID_ARG;
   if (p->num_q_heads > (1 << 20) || p->num_kv_heads > (1 << 20)) return TV_ERR_INVALID_ARG;
   const int64_t heads = static_cast<int64_t>(p->num_q_heads) + p->num_kv_heads;
   if (p->tokens * heads >= (1ll << 40)) return TV_ERR_INVALID_ARG;

@@ -196,8 +196,27 @@ def test_extremes():
     logits[0, 7], logits[1, 9] = 3.3e38, -3.2e38
     got = run(logits.cuda(), [-1e30, -1e-30], 2, 3)
     assert got["tokens"][0].tolist() == [9, 7, 0] and got["parents"][0].tolist() == [1, 0, 1] and got["status"][0] == 0
-    # (a score of -1e-30 goes under in fp64 next to logits of 1e38)
-    np.testing.assert_allclose(got["scores"][0], [0.0, -1e30, -1e37], rtol=1e-6, atol=1e-29)
+    np.testing.assert_allclose(got["scores"][0], [-1e-30, -1e30, -1e37], rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_masks_of_the_lowest_value(dtype):
+    """Masks that are finite: rows of which some, few, and no entries are above them."""
+    ensure_built()
+    low = torch.finfo(dtype).min
+    logits, scores, lengths, g = make(3, 4, 20000, dtype, 21)
+    logits[torch.from_numpy(g.random((12, 20000)) < 0.5)] = low
+    logits[4:8][torch.from_numpy(g.random((4, 20000)) < 0.9999)] = low
+    logits[8] = low             # nothing but masks: all tokens alike
+    logits[9, :19000] = low     # whole parts of masks
+    logits[10] = low
+    logits[10, 5] = 1e30        # and next to the largest
+    ref = oracle.beam_select(logits.double().numpy(), scores, 4, 8, lengths)
+    got = run(logits.cuda(), scores, 4, 8, lengths)
+    compare(got, ref, lengths)
+    row = run(logits[8:9].cuda(), scores[8:9], 1, 3)
+    assert row["tokens"][0].tolist() == [0, 1, 2]
+    np.testing.assert_allclose(row["scores"][0], scores[8] - math.log(20000), rtol=0, atol=LSE + 2.0 ** -24 * 64)
 
 
 def test_strided_rows_streams_graphs_and_workspaces():

@@ -50,7 +50,7 @@ def rotate(axes=(0,) * 64, **kw):
                                  dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=511),
                                  dict(q_stride=516), dict(k_stride=248), dict(k_out_stride=-256),
                                  dict(q_out_stride=2 ** 39), dict(num_q_heads=2 ** 20 + 1),
-                                 dict(tokens=2 ** 31 - 1, num_q_heads=2 ** 20),
+                                 dict(tokens=2 ** 30, num_q_heads=2 ** 20), dict(tokens=2 ** 30 + 1),
                                  dict(axes=(0,) * 63 + (1,)), dict(axes=(3,) + (0,) * 63, num_axes=3)])
 def test_rotate_arguments(lib, bad):
     assert lib.tv_rotate_qk(C.byref(rotate(**bad)), *[at(i) for i in range(8)], None) == tv.TV_ERR_INVALID_ARG
