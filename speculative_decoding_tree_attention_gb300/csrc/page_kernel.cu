@@ -20,7 +20,7 @@
 // Bound: latency (dependent passes and barriers) for small pools; the cluster's reads
 // of the counts for large ones; HBM for the copies.  Measured (device time, the calls
 // replayed): 32 of 512 rows of up to 2048 entries replaced, 690000 pages: free and
-// alloc 22 us; a fork of 512 rows of 290 entries with its copies 17.4 us; 2100 pages of
+// alloc 22 us; a fork of 512 rows of 263 entries with its copies 16.5 us; 2100 pages of
 // 64 KB moved: plan, tables and copies 57 us, the copies at 6.8 TB/s.  Each CTA with a
 // share of consecutive pages, a warp per row: 27 us for the first.
 #include <cooperative_groups.h>
@@ -739,20 +739,22 @@ int launch_behind(void (*kernel)(Args), const Args& a, unsigned grid, unsigned t
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? 0 : -1;
 }
 
-// How many CTAs: one for a pool that it reads in a few loads a thread, `most` pages
-// (which spares the cluster barriers: 16 rows over 3500 pages 8.3 us instead of 11
-// with free_pages; its work behind the counts differs by kernel: a fork over 17400
-// pages 17.4 us, with 8 CTAs 18.5; a compaction of 8400 pages 58.9, with 8 57.4), 8 up
-// to 2^18 pages, then 16 (512 rows over 690000 pages 36 us, with 16 27).
+// How many CTAs: one for a pool of at most `most` pages (it spares the cluster
+// barriers), 8 below 2^17 pages, then 16.  Device times with 1, 8 and 16 CTAs, us:
+// free and alloc, 3550 pages 8.2, 9.3, 10.3; 9900 11.3, 10.2, 10.3; 141000 -, 15.4,
+// 13.3; 690000 -, 32.8, 22.6.  Compaction and copies, 1600 pages 11.3, 13.3, 13.4; 8780
+// 57.1, 57.1, 57.4; 13800 27.7, 25.6, 25.7 (smaller pages); 198000 -, 224, 218.  Fork and
+// copies (its children do not divide as well), 1360 pages 12.1, 15.4, 16.4;
+// 17400 16.5, 17.9, 20.9; 25900 17.7, 17.5, 24.4.
 int ctas_for(const PageArgs& a, int most) {
   if (a.num_blocks <= most && a.rows <= kThreads && a.new_rows <= kThreads) return 1;
-  return a.num_blocks < (1 << 18) ? 8 : kCluster;
+  return a.num_blocks < (1 << 17) ? 8 : kCluster;
 }
 
 }  // namespace
 
 int launch_alloc_pages(PageArgs a, cudaStream_t stream) {
-  const int ctas = ctas_for(a, 16384), each = (a.rows + ctas - 1) / ctas;
+  const int ctas = ctas_for(a, 6144), each = (a.rows + ctas - 1) / ctas;
   // pieces of a row: of 256 entries (what a warp has in flight) at least, as many as a
   // CTA has room for
   int cuts = (a.width + 255) / 256;
@@ -785,8 +787,9 @@ int launch_fork_plan(const PageArgs& a, int ctas, cudaStream_t stream) {
 }  // namespace
 
 int launch_fork_pages(const PageArgs& a, cudaStream_t stream) {
-  const int rows = a.rows > a.new_rows ? a.rows : a.new_rows, ctas = ctas_for(a, 32768);
-  // few entries are done by the same CTAs
+  const int rows = a.rows > a.new_rows ? a.rows : a.new_rows, ctas = ctas_for(a, 24576);
+  // few entries are done by the same CTAs: 32 rows of 253 entries take 0.8 us more on
+  // the device (12.1, with copies), but the host spends 2 us less on a call (18.3)
   if (static_cast<long long>(rows) * a.width <= static_cast<long long>(ctas) * kFewEntries)
     return launch_fork_plan<true>(a, ctas, stream);
   if (launch_fork_plan<false>(a, ctas, stream)) return -1;
@@ -794,7 +797,7 @@ int launch_fork_pages(const PageArgs& a, cudaStream_t stream) {
 }
 
 int launch_compact_pages(const PageArgs& a, cudaStream_t stream) {
-  const int ctas = ctas_for(a, 4096);
+  const int ctas = ctas_for(a, 6144);
   if (ctas == 1   ? launch_group<1>(compact_plan_kernel<1>, a, 0, stream)
       : ctas == 8 ? launch_group<8>(compact_plan_kernel<8>, a, 0, stream)
                   : launch_group<kCluster>(compact_plan_kernel<kCluster>, a, 0, stream))

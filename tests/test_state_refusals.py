@@ -146,7 +146,7 @@ def page_calls(lib, p, args=lambda n: [at(i) for i in range(n)]):
 
 
 @pytest.mark.parametrize("bad", [dict(rows=0), dict(rows=65537), dict(block_size=32), dict(max_blocks_per_seq=0),
-                                 dict(num_blocks=0), dict(num_blocks=2 ** 30 + 1)])
+                                 dict(max_blocks_per_seq=2 ** 27 + 1), dict(num_blocks=0), dict(num_blocks=2 ** 30 + 1)])
 def test_page_arguments(lib, bad):
     p = pages(**bad)
     for rc in page_calls(lib, p):
