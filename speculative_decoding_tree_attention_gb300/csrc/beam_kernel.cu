@@ -426,12 +426,12 @@ struct MergeSmem {
   float top[kMaxBeams];      // the row's maximum
   double inverse[kMaxBeams]; // 1 / len^alpha
   unsigned long long key[kFound + kMaxBeams];  // in the order of the keys' values
-  float value[kFound + kMaxBeams];             // logit
+  float value[kFound + kMaxBeams];             // logit, then score
   int at[kFound + kMaxBeams];                  // beam * 2^18 + token
   float2 approx[kMaxBeams];  // (base, inverse) in fp32
   unsigned long long best_key[kWarps];
   int best_at[kWarps], best_list[kWarps];
-  int state[kMaxBeams];
+  int state[kMaxBeams], length[kMaxBeams];
   int live[kMaxBeams];       // the live beams, in order
   float nth[kWarps];
   uint8_t next[kMaxBeams * kMaxParts];  // of each list, the next entry
@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
         bad |= !(score < INFINITY) || len < 0 || len > kMaxLength;
         if (score > -INFINITY) state = a.finished && a.finished[row] != 0 ? kEnded : kLive;
         s.state[k] = state;
+        s.length[k] = len;
         s.base[k] = score;
         s.inverse[k] = 1.0;
       }
@@ -534,8 +535,6 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   for (int i = tid; i < s.ended; i += kThreads) {
     const int k = s.at[i] >> 18;
     if (a.length_penalty != 0.0f) s.inverse[k] = a.inverse[static_cast<size_t>(b) * K + k];
-    s.key[i] = ordered_key(s.base[k] * s.inverse[k]);
-    s.value[i] = 0.0f;
   }
   __syncthreads();
   if (tid == 0) a.status[b] = s.bad ? kBadTree : kOk;
@@ -557,12 +556,12 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     return (d + p.x) * p.y;
   };
   // (the maximum off first: rows of the type's lowest value have scores too)
-  const auto score_of = [&](float x, int k) { return s.base[k] + (static_cast<double>(x) - static_cast<double>(s.top[k])); };
-  const auto key_of = [&](float x, int k) { return ordered_key(score_of(x, k) * s.inverse[k]); };
+  const auto score_of = [&](float x, int k) {
+    return s.state[k] == kEnded ? s.base[k] : s.base[k] + (static_cast<double>(x) - static_cast<double>(s.top[k]));
+  };
   const auto keep = [&](float2 e, int k) {
     const int at = atomicAdd(&s.found, 1);
     if (at < kFound + kMaxBeams) {
-      s.key[at] = key_of(e.x, k);
       s.value[at] = e.x;
       s.at[at] = k << 18 | __float_as_int(e.y);
     }
@@ -619,15 +618,15 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     }
   }
   __syncthreads();
-  const auto put = [&](int rank, float x, int at) {
+  const auto put = [&](int rank, float score, int at) {
     const int k = at >> 18;
-    const size_t row = static_cast<size_t>(b) * K + k, o = static_cast<size_t>(b) * S + rank;
+    const size_t o = static_cast<size_t>(b) * S + rank;
     const bool ended = s.state[k] == kEnded;
     const int token = ended ? a.end_token : at & ((1 << 18) - 1);
     a.tokens[o] = token;
-    a.parents[o] = static_cast<int>(row);
-    a.scores_out[o] = static_cast<float>(ended ? s.base[k] : score_of(x, k));
-    if (a.lengths_out) a.lengths_out[o] = a.lengths[row] + (ended ? 0 : 1);
+    a.parents[o] = b * K + k;
+    a.scores_out[o] = score;
+    if (a.lengths_out) a.lengths_out[o] = s.length[k] + (ended ? 0 : 1);
     if (a.finished_out) a.finished_out[o] = ended || (a.end_token >= 0 && token == a.end_token);
   };
   const auto put_none = [&](int rank) {
@@ -637,7 +636,15 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     if (a.lengths_out) a.lengths_out[o] = 0;
     if (a.finished_out) a.finished_out[o] = 0;
   };
+  // scores and keys of the few (of all ended beams, the first), in fp64
   const int found = s.found;
+  for (int i = tid; i < min(found, kFound + kMaxBeams); i += kThreads) {
+    const int k = s.at[i] >> 18;
+    const double score = score_of(s.value[i], k);
+    s.value[i] = static_cast<float>(score);
+    s.key[i] = ordered_key(score * s.inverse[k]);
+  }
+  __syncthreads();
   if (found <= kFound + kMaxBeams) {
     for (int i = tid; i < found; i += kThreads) {
       const unsigned long long key = s.key[i];
@@ -664,7 +671,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
       const float2 e = entry(q, r);
       const int k = beam_of(q), place = k << 18 | __float_as_int(e.y);
       if (!(e.x > -INFINITY)) continue;
-      const unsigned long long v = key_of(e.x, k);
+      const unsigned long long v = ordered_key(score_of(e.x, k) * s.inverse[k]);
       if (better(v, place, key, at)) key = v, at = place, list = q;
     }
     for (int i = tid, j = 0; i < s.ended; i += kThreads, ++j)
@@ -683,11 +690,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
       if (tid == 0) put_none(rank);
     } else if (list >= 0) {
       if (tid == list % kThreads) {
-        put(rank, entry(list, s.next[list]).x, at);
+        put(rank, static_cast<float>(score_of(entry(list, s.next[list]).x, at >> 18)), at);
         s.next[list] += 1;
       }
     } else if (tid == (-2 - list) % kThreads) {
-      put(rank, 0.0f, at);
+      put(rank, s.value[-2 - list], at);
       ended_left &= ~(1u << ((-2 - list) / kThreads));
     }
     __syncthreads();
