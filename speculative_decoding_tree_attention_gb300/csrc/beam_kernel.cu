@@ -29,14 +29,14 @@
 // score near 20 to fp32 (1e-6).  Candidates of different beams that lie closer than
 // that may come in either order, the same in every call.
 //
-// Bound: instruction issue (68 % busy) at half of the HBM rate; for few requests the
+// Bound: instruction issue (two thirds busy) at half of the HBM rate; for few requests the
 // latency of two dependent kernels.  Measured (device time, the call replayed): 64
-// requests of 8 beams, V = 128256, bf16, S = 16: 38.3 us (3.3 TB/s); 1 of 4, V = 32000,
-// fp32: 10.3 us.  On the way, the first case: a CTA per 8192 entries, entries in
+// requests of 8 beams, V = 128256, bf16, S = 16: 35.8 us (3.5 TB/s); 1 of 4, V = 32000,
+// fp32: 9.3 us.  On the way, the first case: a CTA per 8192 entries, entries in
 // registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
 // bound (22 of every 1024 entries passed it) 71; the shared bound, entries pushed by
 // the lanes that have them 53 (a third of the instructions were theirs, and they
-// spilled); words from shared memory, looked at by all lanes 39.
+// spilled); words from shared memory, looked at by all lanes one after the other 38.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -85,6 +85,7 @@ struct List {
   float value[kList];   // -inf: taken
   int index[kList];
   float2 best[kMaxSelect];
+  uint8_t words[32 * kWords];  // of the stage, those that have entries for the list
 };
 
 // Keeps the best n of the list's `count` entries, in order, in l.best and at the
@@ -322,30 +323,37 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
     if (!__any_sync(0xffffffffu, top >= t)) continue;
     __syncwarp();  // (every lane's words are seen by the others)
     t = fmaxf(t, bounds->least());
+    int some = 0;
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
-      // word by word, an entry a lane
-      for (unsigned has = __ballot_sync(0xffffffffu, g[j] >= t); has; has &= has - 1) {
-        const int word = j * 32 + __ffs(has) - 1;
-        if (count + p.kEach > kList) {
-          count = keep_best(l, count, select);
-          // (of equal ones the later token does not count)
-          if (count == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1]) + 1));
-        }
-        float x = -INFINITY;
-        if (lane < p.kEach) {
-          x = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(stage + word)[lane]) << 16)
-                   : reinterpret_cast<const float*>(stage + word)[lane];
-          x += 0.0f;  // (one zero)
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, x >= t);
-        if (x >= t) {
-          const int at = count + __popc(hit & ((1u << lane) - 1));
-          l.value[at] = x;
-          l.index[at] = p.entry_of(w0 + word) + lane;
-        }
-        count += __popc(hit);
+      const unsigned has = __ballot_sync(0xffffffffu, g[j] >= t);
+      if (g[j] >= t) l.words[some + __popc(has & ((1u << lane) - 1))] = static_cast<uint8_t>(j * 32 + lane);
+      some += __popc(has);
+    }
+    __syncwarp();
+    // an entry a lane, of four bf16 words or eight of fp32
+    for (int q = 0; q < some; q += 32 / p.kEach) {
+      if (count + 32 > kList) {
+        count = keep_best(l, count, select);
+        // (of equal ones the later token does not count)
+        if (count == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1]) + 1));
       }
+      const int at = q + lane / p.kEach, i = lane % p.kEach;
+      float x = -INFINITY;
+      int word = 0;
+      if (at < some) {
+        word = l.words[at];
+        x = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(stage + word)[i]) << 16)
+                 : reinterpret_cast<const float*>(stage + word)[i];
+        x += 0.0f;  // (one zero)
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, x >= t);
+      if (x >= t) {
+        const int to = count + __popc(hit & ((1u << lane) - 1));
+        l.value[to] = x;
+        l.index[to] = p.entry_of(w0 + word) + i;
+      }
+      count += __popc(hit);
     }
     __syncwarp();  // (the stage is filled again next)
   }
