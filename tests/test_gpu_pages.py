@@ -54,7 +54,7 @@ def consistent(table, refs):
 SIZES = [  # rows, entries a row, pages
     (1, 1, 1), (1, 3, 5), (3, 7, 40), (16, 257, 3000), (70, 33, 1025), (5, 2100, 127), (300, 40, 9001),
     (9, 130, 100003), (1100, 9, 16384), (2500, 3, 70000),
-    (40, 2500, 300001), (600, 30, 700000)]
+    (40, 2500, 300001), (600, 30, 700000), (700, 500, 200000)]
 
 
 @pytest.mark.parametrize("rows, width, pages", SIZES)
