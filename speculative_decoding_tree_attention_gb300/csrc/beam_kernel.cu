@@ -10,11 +10,11 @@
 // One pass over the logits.  beam_rows_kernel: a warp takes a part of a row, four
 // 16-byte words a lane at a time, the next four on their way to shared memory.  Each
 // lane keeps a running maximum and the sum of exps against it.  Entries from a bound
-// on go to the warp's list in shared memory.  The bound: if of W warps each has c
-// lanes whose largest entry so far is at least t, and W c >= S, S entries of the row
-// at least are no worse than t; the 8 warps of a CTA, which work on one row, take the
-// least of their c-th largest.  So after the first words the bound is near the S-th
-// best of what eight warps have seen, and few entries pass it: most words cost their
+// on go to the warp's list in shared memory.  The bound: if warp w has c_w lanes whose
+// largest entry so far is at least t, and the c_w add up to S, S entries of the row
+// are no worse than t; the 8 warps of a CTA, which work on one row, take the least of
+// their c_w-th largest, c_w about S / 8.  So after the first words the bound is near the
+// S-th best of what eight warps have seen, and few entries pass it: most words cost their
 // exps, a packed maximum and one comparison; one that has an entry from the bound on
 // is looked at by all lanes, an entry a lane.  (Bounds rise with time and differ from
 // run to run, the S best do not: they pass every bound.)  Within a row the order is
@@ -227,13 +227,20 @@ __device__ __forceinline__ void fetch_words(const Part<BF16>& p, int w0, uint4* 
     for (int j = 0; j < kWords; ++j) cpa16(stage + j * 32 + lane, at + j * 512);
   } else {
 #pragma unroll 1
-    for (int j = 0; j < kWords; ++j) stage[j * 32 + lane] = p.load(w0 + j * 32 + lane);
+    for (int j = 0; j < kWords; ++j) {
+      const int w = w0 + j * 32 + lane, e = p.entry_of(w);
+      if (e >= p.c0 && e + p.kEach <= p.c1) {
+        cpa16(stage + j * 32 + lane, p.base + static_cast<long long>(e) * (16 / p.kEach));
+      } else {
+        stage[j * 32 + lane] = p.load(w);
+      }
+    }
   }
 }
 __device__ __forceinline__ void commit_words() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_words() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
 
-// What the warps of a CTA share: the c-th largest of the lanes' maxima of each
+// What the warps of a CTA share: the c_w-th largest of the lanes' maxima of each
 // (+inf of warps without a part).
 struct Bounds {
   float4 nth[kWarps / 4];
@@ -258,7 +265,7 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
   constexpr int kPairs = BF16 ? 4 : 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach;
-  const int give = (select + warps - 1) / warps;
+  const int give = max(1, select / warps + (warp < select % warps));
   m = SAFE ? -FLT_MAX : -0x1p126f;  // (not -inf: nothing minus nothing)
   count = 0;
   float t = -FLT_MAX, high = -INFINITY;  // (-inf is no candidate)
@@ -394,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ctas = (a.parts + kWarps - 1) / kWarps;  // of a row
-  const int row = blockIdx.x / ctas, first = (blockIdx.x - row * ctas) * kWarps, part = first + warp;
-  const int warps = min(kWarps, a.parts - first);
+  const int row = blockIdx.x / ctas, cta = blockIdx.x - row * ctas;
+  const int first = cta * a.each + min(cta, a.more), warps = a.each + (cta < a.more), part = first + warp;
   if (threadIdx.x < kWarps) reinterpret_cast<float*>(&bounds)[threadIdx.x] = static_cast<int>(threadIdx.x) < warps ? -INFINITY : INFINITY;
   __syncthreads();
   if (row >= a.batch * a.beams) {
@@ -714,15 +721,20 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
 int beam_max_select() { return kMaxSelect; }
 int beam_max_beams() { return kMaxBeams; }
 
-// Parts of a row: whole CTAs, about six for every SM over all rows, so that the last
-// ones leave few SMs idle (with as many as are resident, 4, the busiest SM had a
-// sixth more than its share of 512 rows), of whole 512 entries at least.
+// Parts of a row, of whole 512 entries: as many as 8 warps a CTA and six CTAs for every
+// SM over all rows make, so that the last ones leave few SMs idle (with as many as are
+// resident, 4, the busiest SM had a sixth more than its share of 512 rows).  A row's
+// CTAs share them evenly: one that is left with few warps has a worse bound (1 request
+// of 32 beams, S = 64, V 151936: 41.0 us with the rest in the last CTA, 36.9 so; 4 of
+// 16, S = 32: 25.6 and 22.6).
 void plan_beam_parts(BeamArgs& a, int sms) {
   const long long rows = static_cast<long long>(a.batch) * a.beams;
   const long long most = min((a.vocab + 511) / 512, kMaxParts), want = (6ll * sms + rows - 1) / rows * kWarps;
   const int parts = static_cast<int>(want < most ? want : most);
   a.chunk = ((a.vocab + parts - 1) / parts + 511) / 512 * 512;
   a.parts = (a.vocab + a.chunk - 1) / a.chunk;
+  const int ctas = (a.parts + kWarps - 1) / kWarps;
+  a.each = a.parts / ctas, a.more = a.parts % ctas;
 }
 
 int launch_beam_select(const BeamArgs& a, cudaStream_t stream) {

@@ -241,10 +241,11 @@ struct BeamArgs {
   double* inverse;            // [batch * beams] 1 / length^length_penalty, where that is not 0
   size_t stride;
   int32_t batch, beams, select, vocab, bf16, end_token, parts, chunk;
+  int32_t each, more;         // a row's CTAs take each parts, the first more of them one more
   float length_penalty;
 };
 int launch_beam_select(const BeamArgs& a, cudaStream_t stream);
-void plan_beam_parts(BeamArgs& a, int sms);  // parts and chunk
+void plan_beam_parts(BeamArgs& a, int sms);  // parts, chunk, each, more
 int beam_max_select();
 int beam_max_beams();
 
