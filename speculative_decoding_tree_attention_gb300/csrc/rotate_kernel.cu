@@ -18,18 +18,23 @@
 // A row is taken by D / 8 lanes that hold four pairs each, so that both values of
 // a pair are in one lane: pairs (i, i + R/2) as 8 bytes of each half, pairs
 // (2i, 2i+1) as 16 bytes; halves that are not 8 bytes aligned (R / 2 no multiple
-// of 4) value by value.  A warp takes a token's heads, or a share of them.  Sine and
-// cosine of the token's pairs are computed once, a lane a pair, and joined with the
-// weights: with A = w_a cos, B = w_b sin, C = w_a sin, D = w_b cos a pair costs two
-// products, two fused ones and two products by the root, two values an instruction.
-// The first rows are on their way meanwhile.
+// of 4) value by value.  Sine and cosine of a token's pairs are computed once per warp,
+// a lane a pair, and joined with the weights: with A = w_a cos, B = w_b sin, C = w_a
+// sin, D = w_b cos a pair costs two products, two fused ones and two products by the
+// root, two values an instruction.
+//
+// Two kernels.  Few rows: a warp takes a token's heads or a share of them, three rows a
+// lane in flight, the first while the angles are computed.  Many rows: a warp takes a
+// stretch of rows over several tokens, which come to shared memory two batches of eight
+// rows ahead (cp.async: no registers).
 //
 // Bound: HBM, one read and one write of each row; latency for single tokens.
 // Measured (device time, the call replayed, norms): 8192 tokens of 64/8 heads of 128
-// 57 us (5.3 TB/s, 0.78 of the copy rate), 16 tokens of 32/8 heads 4.2 us.  With sines
-// by every lane for its own pairs and norm, weights and rotation one after the other
-// 80 us; with the next rows loaded ahead of the present ones' arithmetic 60 (fewer
-// warps fit), two or four rows in flight instead of three 60 and 57.
+// 49.7 us (6.1 TB/s, 0.90 of the copy rate), 4 x 1600 of 28/4 on three axes 20.5, 16
+// tokens of 32/8 heads 4.2.  Before: with sines by every lane for its own pairs and
+// norm, weights and rotation one after the other 80 us for the first; the kernel of few
+// rows 57, with two or four rows in flight 60 and 57; stretches in batches of 6 rows 4
+// CTAs an SM 50.3, of 2 rows and 8 stages 70.
 #include "tv_device.cuh"
 #include "tv_launch.h"
 
@@ -160,6 +165,24 @@ struct Row {
   }
 };
 
+// Cosine and sine of the pairs of a warp's token, a lane a pair.
+__device__ __forceinline__ void fill_angles(Shared& s, const int (&pos)[kMaxAxes], int rot) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = lane + 32 * i;
+    if (2 * p < rot) {
+      const int axis = s.axis[p];
+      const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+      const uint64_t phase = s.turn[p] * static_cast<uint64_t>(static_cast<long long>(at));
+      float c, n;
+      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &n, &c);
+      s.angle[warp][p] = make_float2(c * s.scale[p], n * s.scale[p]);
+    }
+  }
+  __syncwarp();
+}
+
 // What a lane turns its pairs by (a pair that is not turned: its weights alone).
 struct Turn {
   float2 a[2], b[2], c[2], d[2];  // (b: with the other sign)
@@ -181,6 +204,38 @@ __device__ __forceinline__ void fill_turn(const Shared& s, int key, int sub, int
     (j % 2 ? r.c[j / 2].y : r.c[j / 2].x) = wx * cs.y;
     (j % 2 ? r.d[j / 2].y : r.d[j / 2].x) = wy * cs.x;
   }
+}
+
+// A row normalised and turned.
+template <int D, Layout L, bool ALL>
+__device__ __forceinline__ void turn_row(Row<D, L>& r, const Turn& turn, bool norm, float eps, int sub, int rot) {
+  constexpr int kLanes = D / 8;
+  float2 x[2], y[2];
+  r.values(x, y);
+  float inv = 1.0f;
+  if (norm) {
+    const float2 two = fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1]))));
+    float sum = two.x + two.y;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    inv = rsqrtf(fmaf(sum, 1.0f / D, eps));
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 n = make_float2(inv, inv);
+    const float2 b = mul2(n, fma2(x[j], turn.a[j], mul2(y[j], turn.b[j])));
+    const float2 d = mul2(n, fma2(y[j], turn.d[j], mul2(x[j], turn.c[j])));
+    if (ALL) {
+      x[j] = b, y[j] = d;
+    } else {  // (a value that is not turned is none of its neighbour's business, infinite or not)
+      const int p = pair_of<D, L>(sub, 2 * j), q = pair_of<D, L>(sub, 2 * j + 1);
+      x[j].x = 2 * p < rot ? b.x : x[j].x * turn.a[j].x * inv;
+      y[j].x = 2 * p < rot ? d.x : y[j].x * turn.d[j].x * inv;
+      x[j].y = 2 * q < rot ? b.y : x[j].y * turn.a[j].y * inv;
+      y[j].y = 2 * q < rot ? d.y : y[j].y * turn.d[j].y * inv;
+    }
+  }
+  r.set(x, y);
 }
 
 // ALL: every value of a head is turned.
@@ -220,19 +275,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a)
   fill_shared(a, s);
   __syncthreads();
   if (g0 >= g1) return;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = lane + 32 * i;
-    if (2 * p < rot) {
-      const int axis = s.axis[p];
-      const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-      const uint64_t phase = s.turn[p] * static_cast<uint64_t>(static_cast<long long>(at));
-      float c, n;
-      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &n, &c);
-      s.angle[warp][p] = make_float2(c * s.scale[p], n * s.scale[p]);
-    }
-  }
-  __syncwarp();
+  fill_angles(s, pos, rot);
 #pragma unroll 1
   for (int key = 0; key < 2; ++key) {
     const int from = key ? max(g0, q_steps) : g0, to = key ? g1 : min(g1, q_steps);
@@ -248,77 +291,150 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateArgs a)
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (g + u >= to) break;  // (uniform over the warp)
-        float2 x[2], y[2];
-        r[u].values(x, y);
-        float inv = 1.0f;
-        if (norm) {
-          const float2 two = fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1]))));
-          float sum = two.x + two.y;
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          inv = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 n = make_float2(inv, inv);
-          const float2 b = mul2(n, fma2(x[j], turn.a[j], mul2(y[j], turn.b[j])));
-          const float2 d = mul2(n, fma2(y[j], turn.d[j], mul2(x[j], turn.c[j])));
-          if (ALL) {
-            x[j] = b, y[j] = d;
-          } else {  // (a value that is not turned is none of its neighbour's business, infinite or not)
-            const int p = pair_of<D, L>(sub, 2 * j), q = pair_of<D, L>(sub, 2 * j + 1);
-            x[j].x = 2 * p < rot ? b.x : x[j].x * turn.a[j].x * inv;
-            y[j].x = 2 * p < rot ? d.x : y[j].x * turn.d[j].x * inv;
-            x[j].y = 2 * q < rot ? b.y : x[j].y * turn.a[j].y * inv;
-            y[j].y = 2 * q < rot ? d.y : y[j].y * turn.d[j].y * inv;
-          }
-        }
-        r[u].set(x, y);
+        turn_row<D, L, ALL>(r[u], turn, norm, a.eps, sub, rot);
         if (h0 + u * kRows < heads) r[u].store(out + u * kRows * D, sub, rot);
       }
     }
   }
 }
 
-template <int D, Layout L>
-void launch_rotate_l(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
-  if (a.rotary_dim == D) {
-    rotate_kernel<D, L, true><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    rotate_kernel<D, L, false><<<grid, kThreads, 0, stream>>>(a);
+// The same of many rows: a warp takes a stretch of all tokens' steps, in batches of one
+// token's queries or keys, which come to shared memory while the ones before are turned.
+constexpr int kBatch = 4, kStages = 3, kResident = 3;
+constexpr int kRing = kWarps * kStages * kBatch * 512;  // bytes
+template <int D, Layout L, bool ALL>
+__global__ void __launch_bounds__(kThreads, kResident) rotate_stream_kernel(const RotateArgs a) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  __shared__ Shared s;
+  extern __shared__ __align__(16) uint4 ring[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
+  const int rot = a.rotary_dim;
+  uint4* mine = ring + warp * (kStages * kBatch * 32);
+  const int q_steps = (a.hq + kRows - 1) / kRows, steps = q_steps + (a.hkv + kRows - 1) / kRows;
+  const long long begin = (static_cast<long long>(blockIdx.x) * kWarps + warp) * a.each;
+  const long long rest = static_cast<long long>(a.tokens) * steps - begin;
+  int left = rest > a.each ? a.each : rest > 0 ? static_cast<int>(rest) : 0;  // steps of the stretch
+  int t = static_cast<int>(begin / steps), g = static_cast<int>(begin % steps);  // the next one's token and place
+  // steps of the next batch
+  const auto batch = [&](int g, int left) { return min(kBatch, min(left, (g < q_steps ? q_steps : steps) - g)); };
+  int l_left = left, l_t = t, l_g = g;  // of the loads
+  const auto fetch = [&](int stage) {
+    if (l_left > 0) {
+      const bool key = l_g >= q_steps;
+      const int heads = key ? a.hkv : a.hq, h0 = (key ? l_g - q_steps : l_g) * kRows + lane / kLanes;
+      const int n = batch(l_g, l_left);
+      const uint16_t* in = (key ? a.k + l_t * a.k_stride : a.q + l_t * a.q_stride) + static_cast<size_t>(h0) * D + 8 * sub;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (u < n && h0 + u * kRows < heads) cpa16(mine + (stage * kBatch + u) * 32 + lane, in + u * kRows * D);
+      l_left -= n;
+      l_g += n;
+      if (l_g == steps) l_g = 0, ++l_t;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  int pos[kMaxAxes];  // the next token's position on every axis
+  const auto place = [&](int token) {
+#pragma unroll
+    for (int i = 0; i < kMaxAxes; ++i)
+      pos[i] = token < a.tokens && rot > 0 && i < a.axes ? a.positions[static_cast<size_t>(i) * a.tokens + token] : 0;
+  };
+  place(left > 0 ? t : a.tokens);
+  fill_shared(a, s);
+  __syncthreads();
+  Turn turn;
+  int stage = 0, ahead = kStages - 1;
+  for (bool first = true; left > 0; first = false) {
+    fetch(ahead);
+    ahead = ahead + 1 == kStages ? 0 : ahead + 1;
+    const bool key = g >= q_steps;
+    if (first || g == 0) {
+      fill_angles(s, pos, rot);
+      place(t + 1);
+    }
+    if (first || g == 0 || g == q_steps) fill_turn<D, L, ALL>(s, key, sub, rot, turn);
+    const bool norm = (key ? a.k_weight : a.q_weight) != nullptr;
+    const int heads = key ? a.hkv : a.hq, h0 = (key ? g - q_steps : g) * kRows + lane / kLanes;
+    const int n = batch(g, left);
+    uint16_t* out = (key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride) + static_cast<size_t>(h0) * D;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(mine + stage * kBatch * 32 + (lane - sub));
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (u >= n) break;  // (uniform over the warp)
+      Row<D, L> r;
+      r.load(row + u * 256, sub, rot);
+      turn_row<D, L, ALL>(r, turn, norm, a.eps, sub, rot);
+      if (h0 + u * kRows < heads) r.store(out + u * kRows * D, sub, rot);
+    }
+    __syncwarp();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    left -= n;
+    g += n;
+    if (g == steps) g = 0, ++t;
   }
 }
 
-template <int D>
-void launch_rotate_d(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
-  if (a.interleaved) {
-    launch_rotate_l<D, kNeighbours>(a, grid, stream);
-  } else if (a.rotary_dim % 8 == 0) {
-    launch_rotate_l<D, kHalves>(a, grid, stream);
+template <int D, Layout L, bool ALL>
+int start(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
+  if (a.each == 0) {
+    rotate_kernel<D, L, ALL><<<grid, kThreads, 0, stream>>>(a);
   } else {
-    rotate_kernel<D, kHalvesByValue, false><<<grid, kThreads, 0, stream>>>(a);
+    if (cudaFuncSetAttribute(rotate_stream_kernel<D, L, ALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess)
+      return -1;
+    rotate_stream_kernel<D, L, ALL><<<grid, kThreads, kRing, stream>>>(a);
   }
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int D, Layout L>
+int launch_rotate_l(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
+  return a.rotary_dim == D ? start<D, L, true>(a, grid, stream) : start<D, L, false>(a, grid, stream);
+}
+
+template <int D>
+int launch_rotate_d(const RotateArgs& a, unsigned grid, cudaStream_t stream) {
+  if (a.interleaved) return launch_rotate_l<D, kNeighbours>(a, grid, stream);
+  if (a.rotary_dim % 8 == 0) return launch_rotate_l<D, kHalves>(a, grid, stream);
+  return start<D, kHalvesByValue, false>(a, grid, stream);
 }
 
 }  // namespace
 
 int launch_rotate(RotateArgs a, int sms, cudaStream_t stream) {
-  // Warps that share a token: enough for about eight CTAs on every SM, of four steps
-  // of heads each at least, which are on their way together; with few tokens of one.
-  const long long want = 8ll * kWarps * sms;
   const int rows = 256 / a.head_dim, steps = (a.hq + rows - 1) / rows + (a.hkv + rows - 1) / rows;
-  const long long share = (want + a.tokens - 1) / a.tokens;
-  const int most = (steps + 3) / 4;
-  a.items = static_cast<int>(share < most ? share : static_cast<long long>(a.tokens) * most < 4ll * sms ? steps : most);
-  const long long ctas = (static_cast<long long>(a.tokens) * a.items + kWarps - 1) / kWarps;
+  const long long all = static_cast<long long>(a.tokens) * steps, resident = static_cast<long long>(sms) * kResident * kWarps;
+  long long ctas;
+  if (all < 8 * resident) {
+    // Few rows (up to some 900 tokens of 64/8 heads), where the first loads count most:
+    // warps that share a token, enough for about eight CTAs on every SM, of four steps
+    // of heads each at least, which are on their way together; with few tokens of one.
+    // (1000 tokens of 28/4: 7.2 us, as a stretch for each warp 8.2; 1024 of 64/8, 10
+    // steps a warp: 11.4 and 10.3.)
+    const long long share = (8ll * kWarps * sms + a.tokens - 1) / a.tokens;
+    const int most = (steps + 3) / 4;
+    a.items = static_cast<int>(share < most ? share : static_cast<long long>(a.tokens) * most < 4ll * sms ? steps : most);
+    ctas = (static_cast<long long>(a.tokens) * a.items + kWarps - 1) / kWarps;
+  } else if (all < 48 * resident) {
+    // One wave of CTAs, a stretch each: angles of as few tokens as can be (2048 tokens of
+    // 64/8 heads 14.4 us, in stretches of 18 steps 17.5; 6400 of 28/4 20.5 and 22.6).
+    a.each = static_cast<int>((all + resident - 1) / resident);
+    ctas = (all + static_cast<long long>(a.each) * kWarps - 1) / (static_cast<long long>(a.each) * kWarps);
+  } else {
+    // More than L2 holds: CTAs of short stretches, about 18 steps and whole parts or
+    // whole numbers of tokens, handed out in order, so that what is read and written at
+    // a time lies together (8192 tokens of 64/8 heads 50.2 us, in one wave 57.6; 16384
+    // 93.1 and 112.7; 25600 of 28/4 72.8 and 81.0).
+    const int parts = (steps + 9) / 18;
+    a.each = parts > 1 ? (steps + parts - 1) / parts : steps >= 18 ? steps : 18 / steps * steps;
+    ctas = (all + static_cast<long long>(a.each) * kWarps - 1) / (static_cast<long long>(a.each) * kWarps);
+  }
   if (ctas > 0x7fffffffll) return -1;
   const unsigned grid = static_cast<unsigned>(ctas);
-  if (a.head_dim == 128) {
-    launch_rotate_d<128>(a, grid, stream);
-  } else {
-    launch_rotate_d<64>(a, grid, stream);
-  }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return a.head_dim == 128 ? launch_rotate_d<128>(a, grid, stream) : launch_rotate_d<64>(a, grid, stream);
 }
 
 }  // namespace tv

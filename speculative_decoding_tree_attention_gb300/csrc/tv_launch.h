@@ -220,7 +220,7 @@ struct RotateArgs {
   int32_t interleaved;        // pairs (2i, 2i + 1), else (i, i + rotary_dim / 2)
   int32_t weight_fp32;
   float eps, scale;
-  int32_t items;              // warps that share a token (set by the launcher)
+  int32_t items, each;        // warps that share a token, or steps of a warp (set by the launcher)
   uint8_t axis[kMaxPairs];    // position axis of each pair
 };
 int launch_rotate(RotateArgs a, int sms, cudaStream_t stream);

@@ -185,3 +185,53 @@ def test_no_tokens_and_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want2)
+
+
+MANY = [  # as CASES, of so many rows that warps take stretches of them
+    (3500, 28, 4, 128, 64, 3, False, True, torch.float32),
+    (15001, 4, 3, 128, 61, 2, False, True, torch.bfloat16),
+    (9001, 9, 2, 64, 32, 1, True, False, None),
+    (31000, 1, 0, 128, 16, 1, False, True, torch.bfloat16),
+    (60001, 5, 1, 128, 64, 1, False, True, torch.bfloat16),    # more rows than L2 holds
+    (3601, 100, 3, 128, 64, 1, False, True, torch.bfloat16),
+    (2, 59000, 1, 64, 32, 1, False, True, torch.bfloat16),
+    (1, 400001, 3, 128, 64, 1, True, True, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_many_rows(case):
+    """Some tokens' heads against fp64; all of them, strided and in place, against calls
+    of few rows each, which another kernel takes: each within a rounding to bf16 and the
+    arithmetic of the same value, of a row of at most `most`."""
+    ensure_built()
+    t, hq, hkv, d, pairs, n_axes, interleaved, norms, wt = case
+    torch.manual_seed(t)
+    wide = torch.randn(t, hq + hkv + 1, d, device="cuda").to(torch.bfloat16)
+    before = wide.clone()
+    q, k = wide[:, :hq], wide[:, hq:hq + hkv] if hkv else None
+    g = np.random.default_rng(t)
+    pos = g.integers(-40000, 40000, (n_axes, t)).astype(np.int32)
+    axes = tuple(int(x) for x in g.integers(0, n_axes, pairs)) if n_axes > 1 else None
+    w = (1 + 0.3 * torch.randn(d)).to(wt) if norms else None
+    freq = frequencies(pairs)
+    p, f, dw = torch.from_numpy(pos).cuda(), freq.cuda(), None if w is None else w.cuda()
+    kw = dict(eps=1e-5, axes=axes, interleaved=interleaved, scale=1.25)
+    assert tv.rotate_qk(q, k, p, f, q_weight=dw, k_weight=dw if hkv else None, q_out=q, k_out=k, **kw)[0] is q
+    assert torch.equal(wide[:, hq + hkv:], before[:, hq + hkv:])
+    some = sorted({0, t - 1, *g.integers(0, t, 40).tolist()})
+    heads = sorted({0, hq - 1, *g.integers(0, hq, 40).tolist()})
+    pick = lambda x, h: x[some][:, h].cpu()  # noqa: E731
+    check(pick(q, heads).cuda(), pick(before, heads), pos[:, some], freq, w, 1e-5, axes, interleaved, 1.25)
+    if hkv:
+        last = list(range(hq, hq + hkv))
+        check(pick(wide, last).cuda(), pick(before, last), pos[:, some], freq, w, 1e-5, axes, interleaved, 1.25)
+    # few tokens at a time, and of one token's many heads few at a time
+    step, part = max(1, 10000 // (hq + hkv)), 10000
+    for t0 in range(0, t, step):
+        for h0 in range(0, hq + hkv, part):
+            x = before[t0:t0 + step, h0:min(h0 + part, hq + hkv)].contiguous()
+            want, _ = tv.rotate_qk(x, None, p[:, t0:t0 + step].clone(), f, q_weight=dw, **kw)
+            got = wide[t0:t0 + step, h0:h0 + part][:, :x.shape[1]]
+            most = want.float().abs().amax(-1, keepdim=True)
+            assert ((got.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -17 * most).all(), (t0, h0)
