@@ -778,7 +778,8 @@ typedef struct {
   int32_t rows;               /* 1 <= R <= 65536 rows of block_table           */
   int32_t new_rows;           /* tv_fork_pages: 1 <= R' <= 65536; else unused  */
   int32_t block_size;         /* must be TV_BLOCK_SIZE (16)                    */
-  int32_t max_blocks_per_seq; /* row stride of the block tables, <= 2^27       */
+  int32_t max_blocks_per_seq; /* row stride of the block tables, <= 2^27, and
+                                 R times it < 2^31                             */
   int32_t num_blocks;         /* pages in the pool, <= 2^30                    */
   int32_t sinks;              /* tv_free_pages: first tokens that are kept     */
 } tv_page_params;             /* host struct */

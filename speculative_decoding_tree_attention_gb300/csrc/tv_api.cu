@@ -1027,7 +1027,8 @@ namespace {
 
 bool pages_valid(const tv_page_params* p) {
   return p && p->rows >= 1 && p->rows <= 65536 && p->block_size == TV_BLOCK_SIZE && p->max_blocks_per_seq >= 1 &&
-         p->max_blocks_per_seq <= (1 << 27) && p->num_blocks >= 1 && p->num_blocks <= (1 << 30);
+         p->max_blocks_per_seq <= (1 << 27) && p->num_blocks >= 1 && p->num_blocks <= (1 << 30) &&
+         static_cast<int64_t>(p->rows) * p->max_blocks_per_seq < (1ll << 31);  // needs are summed in 32 bits
 }
 
 tv::PageArgs page_args(const tv_page_params* p, const int32_t* block_table, const int32_t* ref_counts, int32_t* status) {

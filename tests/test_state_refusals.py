@@ -154,6 +154,16 @@ def test_page_arguments(lib, bad):
     assert lib.tv_pages_workspace_size(C.byref(p)) == 0
 
 
+def test_tables_whose_needs_pass_32_bits(lib):
+    """Rows that lack 2^31 pages in all would wrap the sums of what they need."""
+    p = pages(rows=65536, max_blocks_per_seq=32768)
+    for rc in page_calls(lib, p):
+        assert rc == tv.TV_ERR_INVALID_ARG
+    assert lib.tv_pages_workspace_size(C.byref(p)) == 0
+    p = pages(rows=65536, max_blocks_per_seq=32767)
+    assert lib.tv_pages_workspace_size(C.byref(p)) > 0
+
+
 def test_page_arguments_of_one_call(lib):
     ok = C.c_size_t(1 << 30)
     assert lib.tv_free_pages(C.byref(pages(sinks=-1)), *[at(i) for i in range(5)], None) == tv.TV_ERR_INVALID_ARG
