@@ -13,16 +13,18 @@
 // through distributed shared memory; the pool is counted in segments that are dealt
 // out to all warps, and the segments' counts and the free pages' numbers go through
 // the caller's workspace, with cluster barriers between.  A small pool takes one CTA
-// and its own barriers.  What touches whole tables (a release, the rows of a fork,
+// and its own barriers; of a large one the counts and needs are found and the pages
+// written by kernels of the whole GPU, the cluster's between.  What touches whole tables (a release, the rows of a fork,
 // the new numbers of a compaction) is a kernel with a CTA per row, but for the rows
 // of a small fork; it is set up while the plan before it ends.
 //
 // Bound: latency (dependent passes and barriers) for small pools; the cluster's reads
-// of the counts for large ones; HBM for the copies.  Measured (device time, the calls
+// of low segments for large ones; HBM for the copies.  Measured (device time, the calls
 // replayed): 32 of 512 rows of up to 2048 entries replaced, 690000 pages: free and
-// alloc 22 us; a fork of 512 rows of 263 entries with its copies 16.5 us; 2100 pages of
-// 64 KB moved: plan, tables and copies 57 us, the copies at 6.8 TB/s.  Each CTA with a
-// share of consecutive pages, a warp per row: 27 us for the first.
+// alloc 14.4 us; a fork of 512 rows of 263 entries with its copies 16.5 us; 2100 pages of
+// 64 KB moved: plan, tables and copies 57 us, the copies at 6.8 TB/s.  The first
+// by the cluster alone 22 us, each CTA of which had a share of consecutive pages and its
+// warps a row each 27 us.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -41,7 +43,6 @@ constexpr int kThreads = 1024;       // of a CTA of the cluster
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowThreads = 256;     // of a CTA of the kernels over tables
 constexpr int kAhead = 8;            // entries of a row that a lane has in flight
-constexpr int kMaxCuts = 8;          // pieces of a row, most
 constexpr int kNeeds = 8192;         // pieces' needs that a CTA holds
 constexpr int kFewEntries = 16384;   // table entries that a CTA writes beside its other work
 
@@ -276,10 +277,56 @@ __device__ __forceinline__ Range range_of(const PageArgs& a, int b) {
   return r;
 }
 
+// How many of a row's entries [q0, q1) lack a page (-1: one names nothing), by a warp.
+__device__ int piece_needs(const PageArgs& a, const int32_t* row, int q0, int q1) {
+  const int lane = threadIdx.x & 31;
+  int lack = 0;
+  bool bad = false;
+  for (int t = q0 + lane; t < q1; t += 32 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) e[j] = t + j * 32 < q1 ? row[t + j * 32] : 0;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      lack += e[j] < 0;
+      bad |= e[j] >= a.num_blocks;
+    }
+  }
+  lack = warp_sum(lack);
+  return __any_sync(0xffffffffu, bad) ? -1 : lack;
+}
+// Gives those the list's pages from `from` on.
+__device__ void fill_piece(const PageArgs& a, int32_t* row, int q0, int q1, int from) {
+  const int lane = threadIdx.x & 31;
+  for (int q = q0; q < q1; q += 32 * kAhead) {
+    bool lacks[kAhead];
+    int at_list[kAhead], page[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = q + j * 32 + lane;
+      lacks[j] = t < q1 && row[t] < 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const unsigned m = __ballot_sync(0xffffffffu, lacks[j]);
+      at_list[j] = from + __popc(m & ((1u << lane) - 1));
+      from += __popc(m);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) page[j] = lacks[j] ? a.list[at_list[j]] : 0;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (lacks[j]) {
+        row[q + j * 32 + lane] = page[j];
+        a.ref_counts[page[j]] = 1;
+      }
+  }
+}
+
 // A row is cut into a.cuts pieces of a.piece entries from its range's first on, a
 // warp a piece.  Dynamic shared memory: the pieces' needs (-1: an entry that names
 // nothing), the rows' places in the list (-1: refused, -2: without a page) and ranges.
-template <int C>
+template <int C, bool SPLIT>
 __global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
   extern __shared__ int need[];
   __shared__ ScanSmem s, of_segments;
@@ -291,34 +338,24 @@ __global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
   int* place = need + each * a.cuts;
   int* first = place + each;
   int* last = first + each;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Range r = range_of(a, b0 + i);
-    first[i] = r.code == kOk ? r.t0 : -1;
-    last[i] = r.t1;
-  }
-  count_segments<C>(a, g);
-  __syncthreads();
-  // how many entries of each piece lack a page
-  for (int i = warp; i < pieces; i += kWarps) {
-    const int b = i / a.cuts, q0 = first[b] + (i - b * a.cuts) * a.piece, q1 = min(q0 + a.piece, last[b]);
-    int lack = 0;
-    bool bad = first[b] < 0;
-    if (!bad && q0 < q1) {
-      const int32_t* row = a.block_table + static_cast<size_t>(b0 + b) * a.width;
-      for (int t = q0 + lane; t < q1; t += 32 * kAhead) {
-        int e[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) e[j] = t + j * 32 < q1 ? row[t + j * 32] : 0;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          lack += e[j] < 0;
-          bad |= e[j] >= a.num_blocks;
-        }
-      }
-      lack = warp_sum(lack);
-      bad = __any_sync(0xffffffffu, bad);
+  if constexpr (SPLIT) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i < pieces; i += kThreads) need[i] = a.needs[b0 * a.cuts + i];
+  } else {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const Range r = range_of(a, b0 + i);
+      first[i] = r.code == kOk ? r.t0 : -1;
+      last[i] = r.t1;
     }
-    if (lane == 0) need[i] = bad ? -1 : lack;
+    count_segments<C>(a, g);
+    __syncthreads();
+    // how many entries of each piece lack a page
+    for (int i = warp; i < pieces; i += kWarps) {
+      const int b = i / a.cuts, q0 = first[b] + (i - b * a.cuts) * a.piece, q1 = min(q0 + a.piece, last[b]);
+      const int lack = first[b] < 0 ? -1 : piece_needs(a, a.block_table + static_cast<size_t>(b0 + b) * a.width, q0, q1);
+      if (lane == 0) need[i] = lack;
+    }
   }
   __syncthreads();
   // exclusive sums of the rows' needs: a run of rows per thread
@@ -352,9 +389,11 @@ __global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
     at += max(lack, 0);
   }
   Group<C>::sync();  // the list is written, and no CTA reads another's shared memory any more
-  for (int i = threadIdx.x; i < n; i += kThreads)
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     a.status[b0 + i] = place[i] == -1 ? kBadTree : place[i] == -2 ? kNoPage : kOk;
-  if (wanted == 0) return;
+    if (SPLIT) a.first[b0 + i] = place[i];
+  }
+  if (SPLIT || wanted == 0) return;
   for (int i = warp; i < pieces; i += kWarps) {
     const int k = i % a.cuts, b = b0 + i / a.cuts;
     int from = place[i / a.cuts];
@@ -362,30 +401,47 @@ __global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
     for (int j = 0; j < k; ++j) from += need[i - k + j];
     const int q0 = first[i / a.cuts] + k * a.piece, q1 = min(q0 + a.piece, last[i / a.cuts]);
     int32_t* row = a.block_table + static_cast<size_t>(b) * a.width;
-    for (int q = q0; q < q1; q += 32 * kAhead) {
-      bool lacks[kAhead];
-      int at_list[kAhead], page[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int t = q + j * 32 + lane;
-        lacks[j] = t < q1 && row[t] < 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const unsigned m = __ballot_sync(0xffffffffu, lacks[j]);
-        at_list[j] = from + __popc(m & ((1u << lane) - 1));
-        from += __popc(m);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) page[j] = lacks[j] ? a.list[at_list[j]] : 0;
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (lacks[j]) {
-          row[q + j * 32 + lane] = page[j];
-          a.ref_counts[page[j]] = 1;
-        }
-    }
+    fill_piece(a, row, q0, q1, from);
   }
+}
+
+// The same of a large pool in three kernels, the second and third set up while the one
+// before ends.  First, all over the GPU, a warp for each segment's free pages and each
+// piece's needs (8.6 of the cluster's 19 us at 690000 pages and 512 rows); then the plan
+// by the cluster (alloc_kernel with SPLIT); and again a warp a piece (its 5 us).
+__global__ void __launch_bounds__(kRowThreads) survey_kernel(const PageArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, w = static_cast<int>(blockIdx.x) * (kRowThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+  const Segments g = segments_of(a.num_blocks);
+  if (w < g.count) {
+    const int end = min((w + 1) * g.pages, a.num_blocks);
+    int n = 0;
+    for (int q = w * g.pages; q < end; q += 4 * kRun) {
+      Runs x;
+      x.load(a.ref_counts, q, end);
+      n += x.free_pages();
+    }
+    n = warp_sum(n);
+    if (lane == 0) a.counts[w] = n;
+  } else if (w - g.count < a.rows * a.cuts) {
+    const int i = w - g.count, b = i / a.cuts;
+    const Range r = range_of(a, b);
+    const int q0 = r.t0 + (i - b * a.cuts) * a.piece;
+    const int lack = r.code != kOk ? -1 : piece_needs(a, a.block_table + static_cast<size_t>(b) * a.width, q0, min(q0 + a.piece, r.t1));
+    if (lane == 0) a.needs[i] = lack;
+  }
+}
+__global__ void __launch_bounds__(kRowThreads) fill_kernel(const PageArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i = static_cast<int>(blockIdx.x) * (kRowThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+  if (i >= a.rows * a.cuts) return;
+  const int b = i / a.cuts, k = i - b * a.cuts;
+  int from = a.first[b];
+  if (from < 0 || a.needs[i] == 0) return;
+  for (int j = 0; j < k; ++j) from += a.needs[i - k + j];
+  const Range r = range_of(a, b);
+  const int q0 = r.t0 + k * a.piece;
+  fill_piece(a, a.block_table + static_cast<size_t>(b) * a.width, q0, min(q0 + a.piece, r.t1), from);
 }
 
 // ---------------------------------------------------------------- free
@@ -705,20 +761,22 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? 0 : -1; }
 
-// A kernel of C CTAs of a cluster.
+// A kernel of C CTAs of a cluster; `behind`: as launch_behind's.
 template <int C>
-int launch_group(void (*kernel)(PageArgs), const PageArgs& a, size_t smem, cudaStream_t stream) {
+int launch_group(void (*kernel)(PageArgs), const PageArgs& a, size_t smem, cudaStream_t stream, bool behind = false) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  cfg.numAttrs = C == 1 ? 0 : behind ? 2 : 1;
   if (C > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? 0 : -1;
 }
@@ -742,13 +800,13 @@ int launch_behind(void (*kernel)(Args), const Args& a, unsigned grid, unsigned t
 // How many CTAs: one for a pool of at most `most` pages (it spares the cluster
 // barriers), 8 below 2^17 pages, then 16.  Device times with 1, 8 and 16 CTAs, us:
 // free and alloc, 3550 pages 8.2, 9.3, 10.3; 9900 11.3, 10.2, 10.3; 141000 -, 15.4,
-// 13.3; 690000 -, 32.8, 22.6.  Compaction and copies, 1600 pages 11.3, 13.3, 13.4; 8780
+// 13.3 (now in three kernels, 11.9); 690000 -, 32.8, 22.6 (14.4).  Compaction and copies, 1600 pages 11.3, 13.3, 13.4; 8780
 // 57.1, 57.1, 57.4; 13800 27.7, 25.6, 25.7 (smaller pages); 198000 -, 224, 218.  Fork and
 // copies (its children do not divide as well), 1360 pages 12.1, 15.4, 16.4;
 // 17400 16.5, 17.9, 20.9; 25900 17.7, 17.5, 24.4.
 int ctas_for(const PageArgs& a, int most) {
   if (a.num_blocks <= most && a.rows <= kThreads && a.new_rows <= kThreads) return 1;
-  return a.num_blocks < (1 << 17) ? 8 : kCluster;
+  return a.num_blocks < kManyPages ? 8 : kCluster;
 }
 
 }  // namespace
@@ -762,12 +820,14 @@ int launch_alloc_pages(PageArgs a, cudaStream_t stream) {
   a.cuts = cuts < kNeeds / each ? cuts : (kNeeds / each > 1 ? kNeeds / each : 1);
   a.piece = (a.width + a.cuts - 1) / a.cuts;
   const size_t smem = static_cast<size_t>(each) * (a.cuts + 3) * 4;  // (65536 rows are 8192 for each of 8 CTAs: 128 KB)
-  const auto kernel = ctas == 1 ? alloc_kernel<1> : ctas == 8 ? alloc_kernel<8> : alloc_kernel<kCluster>;
+  const auto kernel = ctas == 1 ? alloc_kernel<1, false> : ctas == 8 ? alloc_kernel<8, false> : alloc_kernel<kCluster, true>;
   if (smem > 24 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return -1;
-  return ctas == 1   ? launch_group<1>(kernel, a, smem, stream)
-         : ctas == 8 ? launch_group<8>(kernel, a, smem, stream)
-                     : launch_group<kCluster>(kernel, a, smem, stream);
+  if (ctas <= 8) return ctas == 1 ? launch_group<1>(kernel, a, smem, stream) : launch_group<8>(kernel, a, smem, stream);
+  const int warps = kRowThreads / 32, pieces = a.rows * a.cuts;
+  survey_kernel<<<static_cast<unsigned>((kSegments + pieces + warps - 1) / warps), kRowThreads, 0, stream>>>(a);
+  if (launched() || launch_group<kCluster>(kernel, a, smem, stream, true)) return -1;
+  return launch_behind(fill_kernel, a, static_cast<unsigned>((pieces + warps - 1) / warps), kRowThreads, stream);
 }
 
 int launch_free_pages(const PageArgs& a, cudaStream_t stream) {

@@ -1045,14 +1045,17 @@ tv::PageArgs page_args(const tv_page_params* p, const int32_t* block_table, cons
 }
 
 // Bytes of the workspace's first two parts, whole 256 each: free pages in order, and
-// the first child of every row; the counts of the pool's segments follow.
+// the first child of every row; the counts of the pool's segments and, of a large
+// pool, the needs of pieces of rows follow.
 size_t page_list_bytes(const tv_page_params* p) { return (static_cast<size_t>(p->num_blocks) * 4 + 255) / 256 * 256; }
 size_t page_first_bytes(const tv_page_params* p) { return (static_cast<size_t>(p->rows) * 4 + 255) / 256 * 256; }
+size_t page_need_bytes(const tv_page_params* p) { return p->num_blocks < tv::kManyPages ? 0 : static_cast<size_t>(p->rows) * tv::kMaxCuts * 4; }
 void page_workspace(const tv_page_params* p, void* workspace, tv::PageArgs* a) {
   uint8_t* at = static_cast<uint8_t*>(workspace);
   a->list = reinterpret_cast<int32_t*>(at);
   a->first = reinterpret_cast<int32_t*>(at + page_list_bytes(p));
   a->counts = reinterpret_cast<int32_t*>(at + page_list_bytes(p) + page_first_bytes(p));
+  a->needs = a->counts + tv::kPageSegments;
 }
 
 template <size_t N>
@@ -1065,7 +1068,7 @@ bool all_given(const void* const (&ptrs)[N]) {
 }  // namespace
 
 size_t tv_pages_workspace_size(const tv_page_params* p) {
-  return pages_valid(p) ? page_list_bytes(p) + page_first_bytes(p) + tv::kPageSegments * 4 : 0;
+  return pages_valid(p) ? page_list_bytes(p) + page_first_bytes(p) + tv::kPageSegments * 4 + page_need_bytes(p) : 0;
 }
 
 int tv_alloc_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_counts,

@@ -266,12 +266,15 @@ struct PageArgs {
   int32_t* count;             // compact: [2] pages in use, moves
   int32_t* status;            // [rows], fork: [new_rows]
   int32_t* list;              // workspace: free pages in order
-  int32_t* first;             // workspace: fork: [rows] first child of a row
+  int32_t* first;             // workspace: [rows] fork: first child of a row; alloc of kManyPages: its place in the list
   int32_t* counts;            // workspace: [kPageSegments] free pages of the pool's segments
+  int32_t* needs;             // workspace: alloc of kManyPages: [rows][kMaxCuts] entries of a row's pieces that lack a page
   int32_t rows, new_rows, width, num_blocks, sinks;
   int32_t cuts, piece;        // alloc: pieces of a row and their entries (set by the launcher)
 };
 constexpr int kPageSegments = 4096;
+constexpr int kManyPages = 1 << 17;  // of a pool whose allocation takes the whole GPU
+constexpr int kMaxCuts = 8;          // pieces of a row, most
 int launch_alloc_pages(PageArgs a, cudaStream_t stream);
 int launch_free_pages(const PageArgs& a, cudaStream_t stream);
 int launch_fork_pages(const PageArgs& a, cudaStream_t stream);
