@@ -21,7 +21,7 @@
 // Bound: latency (dependent passes and barriers) for small pools; the cluster's reads
 // of low segments for large ones; HBM for the copies.  Measured (device time, the calls
 // replayed): 32 of 512 rows of up to 2048 entries replaced, 690000 pages: free and
-// alloc 14.4 us; a fork of 512 rows of 263 entries with its copies 16.5 us; 2100 pages of
+// alloc 13.4 us; a fork of 512 rows of 263 entries with its copies 16.5 us; 2100 pages of
 // 64 KB moved: plan, tables and copies 57 us, the copies at 6.8 TB/s.  The first
 // by the cluster alone 22 us, each CTA of which had a share of consecutive pages and its
 // warps a row each 27 us.
@@ -295,28 +295,33 @@ __device__ int piece_needs(const PageArgs& a, const int32_t* row, int q0, int q1
   lack = warp_sum(lack);
   return __any_sync(0xffffffffu, bad) ? -1 : lack;
 }
-// Gives those the list's pages from `from` on.
-__device__ void fill_piece(const PageArgs& a, int32_t* row, int q0, int q1, int from) {
+// Which of a lane's entries from q on lack one, a bit each.
+__device__ __forceinline__ unsigned lacking(const int32_t* row, int q, int q1) {
+  unsigned r = 0;
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int t = q + j * 32 + static_cast<int>(threadIdx.x & 31);
+    r |= static_cast<unsigned>(t < q1 && row[t] < 0) << j;
+  }
+  return r;
+}
+// Gives those of [q0, q1) the list's pages from `from` on; `lacks` is lacking(row, q0, q1).
+__device__ __forceinline__ void fill_piece(const PageArgs& a, int32_t* row, int q0, int q1, int from, unsigned lacks) {
   const int lane = threadIdx.x & 31;
   for (int q = q0; q < q1; q += 32 * kAhead) {
-    bool lacks[kAhead];
+    if (q > q0) lacks = lacking(row, q, q1);
     int at_list[kAhead], page[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int t = q + j * 32 + lane;
-      lacks[j] = t < q1 && row[t] < 0;
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const unsigned m = __ballot_sync(0xffffffffu, lacks[j]);
+      const unsigned m = __ballot_sync(0xffffffffu, lacks >> j & 1u);
       at_list[j] = from + __popc(m & ((1u << lane) - 1));
       from += __popc(m);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) page[j] = lacks[j] ? a.list[at_list[j]] : 0;
+    for (int j = 0; j < kAhead; ++j) page[j] = lacks >> j & 1u ? a.list[at_list[j]] : 0;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (lacks[j]) {
+      if (lacks >> j & 1u) {
         row[q + j * 32 + lane] = page[j];
         a.ref_counts[page[j]] = 1;
       }
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) alloc_kernel(const PageArgs a) {
     for (int j = 0; j < k; ++j) from += need[i - k + j];
     const int q0 = first[i / a.cuts] + k * a.piece, q1 = min(q0 + a.piece, last[i / a.cuts]);
     int32_t* row = a.block_table + static_cast<size_t>(b) * a.width;
-    fill_piece(a, row, q0, q1, from);
+    fill_piece(a, row, q0, q1, from, lacking(row, q0, q1));
   }
 }
 
@@ -432,16 +437,19 @@ __global__ void __launch_bounds__(kRowThreads) survey_kernel(const PageArgs a) {
   }
 }
 __global__ void __launch_bounds__(kRowThreads) fill_kernel(const PageArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = static_cast<int>(blockIdx.x) * (kRowThreads / 32) + static_cast<int>(threadIdx.x >> 5);
-  if (i >= a.rows * a.cuts) return;
-  const int b = i / a.cuts, k = i - b * a.cuts;
-  int from = a.first[b];
-  if (from < 0 || a.needs[i] == 0) return;
-  for (int j = 0; j < k; ++j) from += a.needs[i - k + j];
+  const int lane = threadIdx.x & 31, i = static_cast<int>(blockIdx.x) * (kRowThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+  const bool here = i < a.rows * a.cuts;
+  const int b = here ? i / a.cuts : 0, k = here ? i - b * a.cuts : 0;
+  // (what the kernels before do not write)
   const Range r = range_of(a, b);
-  const int q0 = r.t0 + k * a.piece;
-  fill_piece(a, a.block_table + static_cast<size_t>(b) * a.width, q0, min(q0 + a.piece, r.t1), from);
+  const int q0 = r.t0 + k * a.piece, q1 = min(q0 + a.piece, r.t1);
+  int32_t* row = a.block_table + static_cast<size_t>(b) * a.width;
+  const unsigned lacks = r.code == kOk ? lacking(row, q0, q1) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!here) return;
+  const int place = a.first[b], need = lane <= k ? a.needs[i - k + lane] : 0;
+  if (place < 0 || __shfl_sync(0xffffffffu, need, k) == 0) return;
+  fill_piece(a, row, q0, q1, place + warp_sum(lane < k ? need : 0), lacks);
 }
 
 // ---------------------------------------------------------------- free
@@ -800,7 +808,7 @@ int launch_behind(void (*kernel)(Args), const Args& a, unsigned grid, unsigned t
 // How many CTAs: one for a pool of at most `most` pages (it spares the cluster
 // barriers), 8 below 2^17 pages, then 16.  Device times with 1, 8 and 16 CTAs, us:
 // free and alloc, 3550 pages 8.2, 9.3, 10.3; 9900 11.3, 10.2, 10.3; 141000 -, 15.4,
-// 13.3 (now in three kernels, 11.9); 690000 -, 32.8, 22.6 (14.4).  Compaction and copies, 1600 pages 11.3, 13.3, 13.4; 8780
+// 13.3 (now in three kernels, 11.3); 690000 -, 32.8, 22.6 (13.4).  Compaction and copies, 1600 pages 11.3, 13.3, 13.4; 8780
 // 57.1, 57.1, 57.4; 13800 27.7, 25.6, 25.7 (smaller pages); 198000 -, 224, 218.  Fork and
 // copies (its children do not divide as well), 1360 pages 12.1, 15.4, 16.4;
 // 17400 16.5, 17.9, 20.9; 25900 17.7, 17.5, 24.4.
