@@ -323,6 +323,62 @@ def test_streams_and_graphs():
     same(got["block_table"], oracle.compact_pages(table, refs)[0])
 
 
+@pytest.mark.parametrize("held, full", [(90000, False), (180000, True)])
+def test_a_large_pool_call_behind_call_in_graphs(held, full):
+    """Allocations and releases of a pool that the whole GPU surveys, captured and
+    replayed: malformed rows, and a pool that runs out."""
+    ensure_built()
+    pages, rows, width = 200003, 90, 1300
+    table, refs, lens, g = sequences(rows, width, pages, 21, 0.4)
+    for p in g.permutation(pages)[:held].tolist():  # the caller's own references
+        refs[p] += 1
+    table[7][2] = pages                             # names nothing
+    ends = [[int(x) for x in g.integers(0, 16 * width + 1, rows)] for _ in range(2)]
+    ends[0][5], ends[1][11] = -1, 16 * width + 1
+    keep = [int(x) for x in g.integers(0, 16 * width + 1, rows)]
+    t0, r0 = i32(table), i32(refs)
+    t, r, e, kp = t0.clone(), r0.clone(), [i32(x) for x in ends], i32(keep)
+    st = [torch.zeros(rows, dtype=torch.int32, device="cuda") for _ in range(3)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    ws = [torch.full((tv.page_workspace_size(t, r),), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for graph, w in zip(graphs, ws):
+        with torch.cuda.graph(graph):
+            tv.alloc_pages(t, r, e[0], status=st[0], workspace=w)
+            tv.free_pages(t, r, keep_end=kp, status=st[1])
+            tv.alloc_pages(t, r, e[1], status=st[2], workspace=w)
+    want = [oracle.alloc_pages(table, refs, [0] * rows, ends[0]), oracle.free_pages(table, refs, [0] * rows, keep),
+            oracle.alloc_pages(table, refs, [0] * rows, ends[1])]
+    assert 0 in want[0] and 5 in want[0] and (7 in want[0]) == full
+    for graph in graphs + graphs:
+        t.copy_(t0)
+        r.copy_(r0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(st, want):
+            same(x, y)
+        same(t, table)
+        same(r, refs)
+
+
+def test_a_large_pool_of_many_rows_and_of_long_ones():
+    ensure_built()
+    rows = 65536
+    t = torch.full((rows, 2), -1, dtype=torch.int32, device="cuda")
+    r = torch.zeros(2 * rows, dtype=torch.int32, device="cuda")
+    n = torch.full((rows,), 17, dtype=torch.int32, device="cuda")
+    assert (tv.alloc_pages(t, r, n) == 0).all() and (r == 1).all()
+    assert torch.equal(t.view(-1), torch.arange(2 * rows, dtype=torch.int32, device="cuda"))
+    t = torch.full((2, 70000), -1, dtype=torch.int32, device="cuda")
+    t[0, ::3] = 140000
+    r = torch.zeros(140001, dtype=torch.int32, device="cuda")
+    r[140000] = 1
+    st = tv.alloc_pages(t, r, i32([16 * 70000, 16 * 70000]))
+    assert (st == 0).all() and (r[:116666] == 1).all() and (r[116666:140000] == 0).all()
+    mine = torch.ones(70000, dtype=torch.bool, device="cuda")
+    mine[::3] = False
+    assert torch.equal(torch.cat([t[0][mine], t[1]]), torch.arange(116666, dtype=torch.int32, device="cuda"))
+
+
 def test_limits():
     ensure_built()
     for call in (lambda t, r, w: tv.alloc_pages(t, r, i32([5]), workspace=w),
