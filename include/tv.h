@@ -672,7 +672,8 @@ int tv_penalize_logits(const tv_penalty_params* params, const void* logits,
  * finite makes its pairs NaN.  The norm's sum of squares overflows fp32 from
  * values near 2^60 on, and a row of zeros with eps = 0 is NaN.
  * In place: q_out may be q with the same stride, k_out k with its own; other
- * overlaps of an output with an input or with the other output are refused.
+ * overlaps of an output with an input or with the other output are refused (of the
+ * weights, positions and frequencies also between its rows).
  * ====================================================================== */
 #define TV_MAX_POSITION_AXES 4
 typedef struct {
@@ -751,7 +752,7 @@ size_t tv_beam_select_workspace_size(const tv_beam_params* params);
  * [B*K]; lengths, finished int32 [B*K] or NULL (lengths may be NULL only with
  * length_penalty 0 and lengths_out NULL); tokens, parents int32 [B][S]; scores_out
  * fp32 [B][S]; lengths_out, finished_out int32 [B][S] or NULL; status int32 [B].
- * Outputs that overlap scores, lengths, finished or each other are refused.  Device
+ * Outputs or a workspace that overlap an input or each other are refused.  Device
  * pointers 16-byte aligned. */
 int tv_beam_select(const tv_beam_params* params, const void* logits, const float* scores,
                    const int32_t* lengths, const int32_t* finished, int32_t* tokens,
@@ -846,9 +847,9 @@ int tv_fork_pages(const tv_page_params* params, const int32_t* block_table,
  * the caller holds); ref_counts_out and block_table_out are the counts and tables
  * in new numbers.  status[b]: TV_OK; TV_ERR_BAD_TREE if an entry of the row names a
  * free page or is >= num_blocks (it becomes -1).
- * ref_counts_out may be ref_counts, and block_table_out block_table.  moves int32 [max(1, num_blocks / 2)][3] (entries from count[1] on
- * are left as they were), count int32 [2], page_map int32 [num_blocks].  Device
- * pointers 16-byte aligned. */
+ * ref_counts_out may be ref_counts, and block_table_out block_table.  moves int32
+ * [max(1, num_blocks / 2)][3] (entries from count[1] on are left as they were), count
+ * int32 [2], page_map int32 [num_blocks].  Device pointers 16-byte aligned. */
 int tv_compact_pages(const tv_page_params* params, const int32_t* block_table,
                      const int32_t* ref_counts, int32_t* block_table_out,
                      int32_t* ref_counts_out, int32_t* page_map, int32_t* moves,

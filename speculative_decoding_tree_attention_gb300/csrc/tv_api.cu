@@ -917,6 +917,12 @@ int tv_rotate_qk(const tv_rotate_params* p, const uint16_t* q, const uint16_t* k
   if (keys && ((!k_here && rows_overlap(ks, ko, p->tokens)) || rows_overlap(qo, ko, p->tokens) ||
                rows_overlap(qs, ko, p->tokens) || rows_overlap(ks, qo, p->tokens)))
     return TV_ERR_INVALID_ARG;
+  const uint64_t weight = p->head_dim * (p->weight_dtype == TV_OUT_FP32 ? 4ull : 2ull);
+  const auto all_rows = [&](const RowSpan& x) { return static_cast<uint64_t>((p->tokens - 1) * x.stride + x.row) * 2; };
+  const Span small[] = {{q_weight, weight}, {keys ? k_weight : nullptr, weight},
+                        {p->rotary_dim > 0 ? positions : nullptr, static_cast<uint64_t>(p->num_axes) * p->tokens * 4},
+                        {frequencies, p->rotary_dim * 4ull}};
+  if (clash({{q_out, all_rows(qo)}}, small) || (keys && clash({{k_out, all_rows(ko)}}, small))) return TV_ERR_INVALID_ARG;
   tv::RotateArgs a;
   std::memset(&a, 0, sizeof a);
   a.q = q;
@@ -1001,11 +1007,13 @@ int tv_beam_select(const tv_beam_params* p, const void* logits, const float* sco
   if (!lengths && (lengths_out || p->length_penalty != 0.0f)) return TV_ERR_INVALID_ARG;
   // (a request's merge reads its input while another's writes)
   const uint64_t in = static_cast<uint64_t>(p->batch) * p->beams * 4, out = static_cast<uint64_t>(p->batch) * p->select * 4;
-  if (clash({{tokens, out}, {parents, out}, {scores_out, out}, {lengths_out, out}, {finished_out, out}, {status, p->batch * 4ull}},
-            {{scores, in}, {lengths, in}, {finished, in}}))
-    return TV_ERR_INVALID_ARG;
   size_t stats, factors, bytes;
   tv::BeamArgs a = beam_args(p, &stats, &factors, &bytes);
+  const uint64_t x = ((static_cast<uint64_t>(p->batch) * p->beams - 1) * a.stride + p->vocab) * (a.bf16 ? 2 : 4);
+  if (clash({{tokens, out}, {parents, out}, {scores_out, out}, {lengths_out, out}, {finished_out, out}, {status, p->batch * 4ull},
+             {workspace, bytes}},
+            {{logits, x}, {scores, in}, {lengths, in}, {finished, in}}))
+    return TV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < bytes || !aligned16(workspace)) return TV_ERR_WORKSPACE;
   a.logits = logits;
   a.scores = scores;
@@ -1078,7 +1086,8 @@ int tv_alloc_pages(const tv_page_params* p, int32_t* block_table, int32_t* ref_c
   if (!all_given({block_table, ref_counts, end, status}) || !aligned16(begin)) return TV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
   const uint64_t word = static_cast<uint64_t>(p->rows) * 4;
-  if (clash({{block_table, word * p->max_blocks_per_seq}, {ref_counts, p->num_blocks * 4ull}, {status, word}},
+  if (clash({{block_table, word * p->max_blocks_per_seq}, {ref_counts, p->num_blocks * 4ull}, {status, word},
+             {workspace, tv_pages_workspace_size(p)}},
             {{begin, word}, {end, word}}))
     return TV_ERR_INVALID_ARG;
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
@@ -1115,7 +1124,7 @@ int tv_fork_pages(const tv_page_params* p, const int32_t* block_table,
     return TV_ERR_INVALID_ARG;
   const uint64_t row = static_cast<uint64_t>(p->max_blocks_per_seq) * 4, rows = p->rows, children = p->new_rows;
   if (clash({{ref_counts, p->num_blocks * 4ull}, {block_table_out, children * row}, {seq_lens_out, children * 4},
-             {copies, children * 12}, {status, children * 4}},
+             {copies, children * 12}, {status, children * 4}, {workspace, tv_pages_workspace_size(p)}},
             {{block_table, rows * row}, {seq_lens, rows * 4}, {parents, children * 4}}))
     return TV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
@@ -1184,6 +1193,10 @@ int copy_call(const tv_copy_params* p, const int32_t* copies, const int32_t* cou
   a.layers = p->layers;
   a.num_blocks = p->num_blocks;
   a.hkv = p->num_kv_heads;
+  const uint64_t pool = a.layer_stride * p->layers, scales = fp8 ? a.scale_stride * p->layers * 4 : 0;
+  if (clash({{k_pool, pool}, {v_pool, pool}, {k_scale, scales}, {v_scale, scales}, {status, p->entries * 4ull}},
+            {{copies, p->entries * 12ull}, {count, 4}}))
+    return TV_ERR_INVALID_ARG;
   return tv::launch_copy_pages(a, sm_count(), stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }
 

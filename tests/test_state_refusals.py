@@ -84,6 +84,17 @@ def test_rotate_overlaps(lib):
         assert call(q, k, qo, ko, **strides) == tv.TV_ERR_INVALID_ARG
 
 
+def test_rotate_outputs_over_small_inputs(lib):
+    """The weights (256 bytes), positions (20) and frequencies (512) of 5 tokens, at or
+    next to the ends of q_out (5120 bytes) and k_out (2560)."""
+    for o, rows in ((6, 5120), (7, 2560)):
+        for i, size in ((2, 256), (3, 256), (4, 20), (5, 512)):
+            for shift in (0, -((rows - 1) // 16 * 16), (size - 1) // 16 * 16):
+                args = [at(j) for j in range(8)]
+                args[o] = C.c_void_p(args[i].value + shift)
+                assert lib.tv_rotate_qk(C.byref(rotate()), *args, None) == tv.TV_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------ beams
 def beams(**kw):
     base = dict(batch=2, beams=3, select=6, vocab=1000, logits_dtype=1, end_token=2, length_penalty=0.5, logits_stride=0)
@@ -129,6 +140,22 @@ def test_beam_pointers_and_workspace(lib):
                 args = [at(j) for j in range(10)]
                 args[o] = C.c_void_p(args[i].value + shift)
                 assert call(args) == tv.TV_ERR_INVALID_ARG
+
+
+def test_beam_overlaps_of_logits_and_workspace(lib):
+    p = beams()
+    need = lib.tv_beam_select_workspace_size(C.byref(p))
+
+    def call(args, ws=at(20)):
+        return lib.tv_beam_select(C.byref(p), *args, ws, C.c_size_t(need), None)
+    for o in (4, 5, 6, 7, 8, 9):  # logits: 6 rows of 1000 fp32
+        args = [at(j) for j in range(10)]
+        args[o] = C.c_void_p(args[0].value + 6 * 4000 - 16)
+        assert call(args) == tv.TV_ERR_INVALID_ARG
+    for i in range(10):
+        args = [at(j) for j in range(10)]
+        assert call(args, args[i]) == tv.TV_ERR_INVALID_ARG
+        assert call(args, C.c_void_p(args[i].value - need // 16 * 16 + 16)) == tv.TV_ERR_INVALID_ARG
 
 
 # ------------------------------------------------------------------ pages
@@ -211,8 +238,6 @@ def test_page_overlaps(lib):
     for i, o in ((0, 3), (0, 4), (0, 5), (0, 6), (0, 7), (1, 2), (1, 4), (1, 5), (1, 6), (1, 7), (2, 3), (2, 4), (3, 4),
                  (4, 5), (3, 5), (2, 7)):
         assert compact(i, o, 0) == tv.TV_ERR_INVALID_ARG
-
-
     args = [at(j) for j in range(5)]
     for i, o in ((0, 1), (0, 4), (1, 4), (1, 2), (3, 0), (4, 3), (2, 4)):
         a = list(args)
@@ -248,6 +273,27 @@ def test_copy_pointers(lib):
                 assert call(args) == tv.TV_ERR_INVALID_ARG
     assert lib.tv_copy_pages(C.byref(copy(head_dim=96)), *[at(i) for i in range(5)], None) == tv.TV_ERR_UNSUPPORTED
     assert lib.tv_copy_pages(C.byref(copy(entries=0)), *[None] * 5, None) == tv.TV_OK
+
+
+def test_page_workspace_and_copy_overlaps(lib):
+    p = pages()
+    need = lib.tv_pages_workspace_size(C.byref(p))
+    size = C.c_size_t(need)
+    for n, call in ((5, lib.tv_alloc_pages), (8, lib.tv_fork_pages)):
+        for i in range(n):
+            for shift in (0, -((need - 1) // 16 * 16)):
+                args = [at(j) for j in range(n)]
+                assert call(C.byref(p), *args, C.c_void_p(args[i].value + shift), size, None) == tv.TV_ERR_INVALID_ARG
+    q = copy()
+    # copies (48 bytes), count (4), pools of 100 pages of 2 heads
+    for n, call, outs in ((5, lib.tv_copy_pages, {2: 819200, 3: 819200, 4: 16}),
+                          (7, lib.tv_copy_pages_fp8, {2: 409600, 3: 12800, 4: 409600, 5: 12800, 6: 16})):
+        for o, size in outs.items():
+            for i in set(range(n)) - {o}:
+                for shift in (0, -((size - 1) // 16 * 16)):
+                    args = [at(j) for j in range(n)]
+                    args[o] = C.c_void_p(args[i].value + shift)
+                    assert call(C.byref(q), *args, None) == tv.TV_ERR_INVALID_ARG, (n, o, i)
 
 
 # ------------------------------------------------------------------ the binding
