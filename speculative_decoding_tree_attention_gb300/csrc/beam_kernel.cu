@@ -7,18 +7,15 @@
 // an ended beam offers itself once, at s_r.  Candidates are ordered by
 // key = d / max(len, 1)^alpha, then the lower beam, then the lower token.
 //
-// One pass over the logits.  beam_rows_kernel: a warp takes a part of a row, four
-// 16-byte words a lane at a time, the next four on their way to shared memory.  Each
-// lane keeps a running maximum and the sum of exps against it.  Entries from a bound
-// on go to the warp's list in shared memory.  The bound: if warp w has c_w lanes whose
-// largest entry so far is at least t, and the c_w add up to S, S entries of the row
-// are no worse than t; the 8 warps of a CTA, which work on one row, take the least of
-// their c_w-th largest, c_w about S / 8.  So after the first words the bound is near the
-// S-th best of what eight warps have seen, and few entries pass it: most words cost their
-// exps, a packed maximum and one comparison; one that has an entry from the bound on
-// is looked at by all lanes, an entry a lane.  (Bounds rise with time and differ from
-// run to run, the S best do not: they pass every bound.)  Within a row the order is
-// exact: it is that of the logits, and of equal ones the lower token.
+// beam_rows_kernel: a warp takes a part of a row, four 16-byte words a lane at a time,
+// the next ones on their way to shared memory.  Each lane keeps a running maximum and
+// the sum of exps against it, and notes the largest entry of its words of every turn.
+// After its part each warp tells a bound: if warp w has c_w lanes whose largest entry is
+// at least t, and the c_w add up to S, S entries of the row are no worse than t; the 8
+// warps of a CTA, which work on one row, take the least of their c_w-th largest, c_w
+// about S / 8.  Few noted entries pass it (3 to 6 of 512 of a warp); their words are
+// read again, an entry a lane, and ranked into the warp's list.  Within a row the order
+// is exact: it is that of the logits, and of equal ones the lower token.
 //
 // beam_merge_kernel: a CTA per request joins the parts of each row to its LSE
 // and picks the S best of all rows' lists the same way: in fp32 with an error
@@ -29,14 +26,17 @@
 // score near 20 to fp32 (1e-6).  Candidates of different beams that lie closer than
 // that may come in either order, the same in every call.
 //
-// Bound: instruction issue (two thirds busy) at half of the HBM rate; for few requests the
-// latency of two dependent kernels.  Measured (device time, the call replayed): 64
-// requests of 8 beams, V = 128256, bf16, S = 16: 35.8 us (3.5 TB/s); 1 of 4, V = 32000,
-// fp32: 9.3 us.  On the way, the first case: a CTA per 8192 entries, entries in
-// registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
-// bound (22 of every 1024 entries passed it) 71; the shared bound, entries pushed by
-// the lanes that have them 53 (a third of the instructions were theirs, and they
-// spilled); words from shared memory, looked at by all lanes one after the other 38.
+// Bound: HBM for large calls (the rows take 22 us of the first one here at 6 TB/s, but up
+// to 27 where 4 instead of 3 of 512 CTAs are on an SM), with the merge's 5 us behind; for
+// few requests the latency of two dependent kernels.  Measured (device time, the call
+// replayed): 64 requests of 8 beams, V = 128256, bf16, S = 16: 36 us; 32 of 8, V = 32000,
+// fp32: 15.4; 1 of 4: 9.3.  On the way, the first case: a CTA per 8192 entries, entries
+// in registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
+// bound that rises as it reads 71; bounds shared by a CTA's warps while they read 53;
+// words from shared memory, looked at by all lanes 36, the second 18.8 (a quarter of the
+// instructions was a look at words that had an entry from the bound on, in most turns).
+// The barrier that such a late bound asks for, ranks by a list's scan and noted entries
+// of every turn in the bound: 40.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -51,7 +51,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSelect = 64;
 constexpr int kMaxBeams = 64;
-constexpr int kMaxParts = 64;        // of a row
+constexpr int kMaxParts = 32;        // of a row
 constexpr int kMaxLength = 1 << 24;
 constexpr int kWords = 4;            // 16-byte words that a lane has in flight
 constexpr int kStages = 2;           // of them
@@ -85,7 +85,6 @@ struct List {
   float value[kList];   // -inf: taken
   int index[kList];
   float2 best[kMaxSelect];
-  uint8_t words[32 * kWords];  // of the stage, those that have entries for the list
 };
 
 // Keeps the best n of the list's `count` entries, in order, in l.best and at the
@@ -206,6 +205,16 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// Two words' larger values, place by place (a number rather than NaN).
+template <bool BF16>
+__device__ __forceinline__ uint4 most_of(const uint4& a, const uint4& b) {
+  if constexpr (BF16) {
+    return make_uint4(max_bf16x2(a.x, b.x), max_bf16x2(a.y, b.y), max_bf16x2(a.z, b.z), max_bf16x2(a.w, b.w));
+  } else {
+    const auto most = [](uint32_t x, uint32_t y) { return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y))); };
+    return make_uint4(most(a.x, b.x), most(a.y, b.y), most(a.z, b.z), most(a.w, b.w));
+  }
+}
 // The largest value of a word (of numbers and NaN, that of the numbers).
 template <bool BF16>
 __device__ __forceinline__ float top_of(const uint4& w) {
@@ -217,6 +226,10 @@ __device__ __forceinline__ float top_of(const uint4& w) {
   }
 }
 
+// Where word i of a stage is: lane l's are 4 l .. 4 l + 3, and eight lanes' j-th ones lie
+// in different banks.
+__device__ __forceinline__ int place_of(int i) { return (i & ~3) | ((i ^ i >> 3) & 3); }
+
 // The four words of each lane from word w0 on, on their way into a stage.
 template <bool BF16>
 __device__ __forceinline__ void fetch_words(const Part<BF16>& p, int w0, uint4* stage) {
@@ -224,15 +237,15 @@ __device__ __forceinline__ void fetch_words(const Part<BF16>& p, int w0, uint4* 
   if (p.entry_of(w0) >= p.c0 && p.entry_of(w0 + 32 * kWords) <= p.c1) {
     const uint8_t* at = p.base + static_cast<long long>(p.entry_of(w0 + lane)) * (16 / p.kEach);
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) cpa16(stage + j * 32 + lane, at + j * 512);
+    for (int j = 0; j < kWords; ++j) cpa16(stage + place_of(j * 32 + lane), at + j * 512);
   } else {
 #pragma unroll 1
     for (int j = 0; j < kWords; ++j) {
       const int w = w0 + j * 32 + lane, e = p.entry_of(w);
       if (e >= p.c0 && e + p.kEach <= p.c1) {
-        cpa16(stage + j * 32 + lane, p.base + static_cast<long long>(e) * (16 / p.kEach));
+        cpa16(stage + place_of(j * 32 + lane), p.base + static_cast<long long>(e) * (16 / p.kEach));
       } else {
-        stage[j * 32 + lane] = p.load(w);
+        stage[place_of(j * 32 + lane)] = p.load(w);
       }
     }
   }
@@ -240,19 +253,15 @@ __device__ __forceinline__ void fetch_words(const Part<BF16>& p, int w0, uint4* 
 __device__ __forceinline__ void commit_words() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_words() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
 
-// What the warps of a CTA share: the c_w-th largest of the lanes' maxima of each
-// (+inf of warps without a part).
+// What the warps of a CTA share: the c_w-th largest of the lanes' maxima of each (+inf
+// of warps without a part, NaN: not known yet).
 struct Bounds {
-  float4 nth[kWarps / 4];
-  __device__ __forceinline__ float least() const {
-    static_assert(kWarps == 8, "two words");
-    const volatile float* v = &nth[0].x;
-    return fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
-  }
+  float nth[kWarps];
 };
 
-// A warp's pass over its part: the entries that may be among the row's best into l,
-// the part's maximum and the sum of exp(x - maximum).  Returns whether it is done.
+// One pass over a part by a warp: the maximum m and sum of exp(x - m), and of every
+// lane's words of every turn the largest entry, as the upper half of its place in the
+// order (of fp32 rounded down, as the bound's is), in tops.  Returns whether it is done.
 //
 // The sums are of 2^(x hi + c), hi = fl(log2 e), c = -fl(m hi) with m the lane's
 // maximum so far: rounded once, near 0 where it counts.  (hi is log2 e but for 1.3e-8
@@ -261,39 +270,37 @@ struct Bounds {
 // or the maximum beyond 2^20 (a part that is masked by the lowest value), the pass
 // is done again (SAFE), without NaN and from x - m.
 template <bool BF16, bool SAFE>
-__device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warps, int select, float& m, float& sum, int& count) {
+__device__ bool part_pass(const Part<BF16>& p, List& l, int16_t* tops, Bounds* bounds, int give, float& m, float& sum) {
   constexpr int kPairs = BF16 ? 4 : 2;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach;
-  const int give = max(1, select / warps + (warp < select % warps));
   m = SAFE ? -FLT_MAX : -0x1p126f;  // (not -inf: nothing minus nothing)
-  count = 0;
-  float t = -FLT_MAX, high = -INFINITY;  // (-inf is no candidate)
+  float high = -INFINITY;
   float c = -m * kLog2eHi;
   float2 acc = make_float2(0.0f, 0.0f);
-  __syncwarp();
-  static_assert(kStages == 2, "one stage ahead");
-  if (SAFE) fetch_words<BF16>(p, 0, l.ring[0]);  // (else the caller's)
-  commit_words();
+  // (the first stages are the caller's)
   for (int w0 = 0, turn = 0; w0 < words; w0 += 32 * kWords, ++turn) {
-    const int ahead = w0 + (kStages - 1) * 32 * kWords;
-    if (ahead < words) fetch_words<BF16>(p, ahead, l.ring[(turn + kStages - 1) % kStages]);
-    commit_words();
     wait_words();
+    __syncwarp();
     uint4* stage = l.ring[turn % kStages];
     uint4 w[kWords];
-    float g[kWords];
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
-      w[j] = stage[j * 32 + lane];
-      if (SAFE) {
-        w[j] = without_nan<BF16>(w[j]);
-        stage[j * 32 + lane] = w[j];
-      }
-      g[j] = top_of<BF16>(w[j]);
+      w[j] = stage[place_of(lane * kWords + j)];
+      if (SAFE) w[j] = without_nan<BF16>(w[j]);
     }
-    const float top = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
+    __syncwarp();
+    const int ahead = w0 + kStages * 32 * kWords;
+    if (ahead < words) fetch_words<BF16>(p, ahead, stage);
+    commit_words();
+    const float top = fmaxf(top_of<BF16>(most_of<BF16>(most_of<BF16>(w[0], w[1]), most_of<BF16>(w[2], w[3]))), -INFINITY);
+    if (!SAFE) tops[turn * 32 + lane] = static_cast<int16_t>(ordered(top + 0.0f) >> 16);
     high = fmaxf(high, top);
+    if (!SAFE && w0 + 32 * kWords >= words) {  // (the last turn)
+      float unused;
+      const float nth = give <= 32 ? nth_largest(high, give, unused) : -INFINITY;
+      if (lane == 0) reinterpret_cast<volatile float*>(bounds->nth)[threadIdx.x >> 5] = nth;
+    }
     if (top > m) {
       if (SAFE) {
         const float f = exp_of(m - top);
@@ -304,12 +311,6 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
         c = to;
       }
       m = top;
-    }
-    if (turn < 4 || turn % 4 == 3) {
-      float unused;
-      const float nth = give <= 32 ? nth_largest(high, give, unused) : -INFINITY;
-      if (lane == 0) reinterpret_cast<volatile float*>(bounds)[warp] = nth;
-      if (!SAFE && turn == 0) __syncthreads();  // (nobody starts without a bound)
     }
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
@@ -327,42 +328,6 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
         acc = add2(acc, make_float2(ex2_approx(e.x), ex2_approx(e.y)));
       }
     }
-    if (!__any_sync(0xffffffffu, top >= t)) continue;
-    __syncwarp();  // (every lane's words are seen by the others)
-    t = fmaxf(t, bounds->least());
-    int some = 0;
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) {
-      const unsigned has = __ballot_sync(0xffffffffu, g[j] >= t);
-      if (g[j] >= t) l.words[some + __popc(has & ((1u << lane) - 1))] = static_cast<uint8_t>(j * 32 + lane);
-      some += __popc(has);
-    }
-    __syncwarp();
-    // an entry a lane, of four bf16 words or eight of fp32
-    for (int q = 0; q < some; q += 32 / p.kEach) {
-      if (count + 32 > kList) {
-        count = keep_best(l, count, select);
-        // (of equal ones the later token does not count)
-        if (count == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1]) + 1));
-      }
-      const int at = q + lane / p.kEach, i = lane % p.kEach;
-      float x = -INFINITY;
-      int word = 0;
-      if (at < some) {
-        word = l.words[at];
-        x = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(stage + word)[i]) << 16)
-                 : reinterpret_cast<const float*>(stage + word)[i];
-        x += 0.0f;  // (one zero)
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, x >= t);
-      if (x >= t) {
-        const int to = count + __popc(hit & ((1u << lane) - 1));
-        l.value[to] = x;
-        l.index[to] = p.entry_of(w0 + word) + i;
-      }
-      count += __popc(hit);
-    }
-    __syncwarp();  // (the stage is filled again next)
   }
   sum = acc.x + acc.y;
   const float all = of_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
@@ -384,6 +349,81 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, Bounds* bounds, int warp
   return !fails;
 }
 
+// The first stages of a part's words on their way.
+template <bool BF16>
+__device__ __forceinline__ void start_words(const Part<BF16>& p, List& l) {
+  const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach;
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) {
+    if (i == 0 || i * 32 * kWords < words) fetch_words<BF16>(p, i * 32 * kWords, l.ring[i]);
+    commit_words();
+  }
+}
+
+// The part's entries from the CTA's bound on into the warp's list; returns how many
+// there are.  For all warps of the CTA that have parts.
+template <bool BF16>
+__device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const Bounds* bounds, int select) {
+  const int lane = threadIdx.x & 31;
+  const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach, turns = (words + 32 * kWords - 1) / (32 * kWords);
+  // (every warp tells its own whatever the others do)
+  float t = NAN;
+  for (int i = 0; i < 1 << 20 && __any_sync(0xffffffffu, t != t); ++i)
+    t = lane < kWarps ? reinterpret_cast<const volatile float*>(bounds->nth)[lane] : INFINITY;
+  t = of_ordered(__reduce_min_sync(0xffffffffu, ordered(t == t ? t : -INFINITY)));
+  t = fmaxf(t, -FLT_MAX);  // (-inf is no candidate)
+  uint16_t* codes = reinterpret_cast<uint16_t*>(l.ring);
+  constexpr int kCodes = sizeof(l.ring) / 2, kOf = kWords * p.kEach, kAtOnce = 32 / kOf, kFly = 8 / kAtOnce;
+  int n = 0, count = 0;
+  const auto look = [&] {
+    __syncwarp();
+    for (int q = 0; q < n; q += kFly * kAtOnce) {
+      float x[kFly];
+      int at[kFly];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        const int k = q + u * kAtOnce + lane / kOf, code = k < n ? codes[k] : 0;
+        at[u] = p.entry_of(((code >> 5) * 32 + (code & 31)) * kWords) + lane % kOf;
+        x[u] = -INFINITY;
+        if (k < n && at[u] >= p.c0 && at[u] < p.c1)
+          x[u] = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.base)[at[u]]) << 16)
+                      : reinterpret_cast<const float*>(p.base)[at[u]];
+        x[u] += 0.0f;  // (one zero)
+      }
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        const unsigned hit = __ballot_sync(0xffffffffu, x[u] >= t);
+        if (hit == 0) continue;
+        if (count + 32 > kList) {
+          count = keep_best(l, count, select);
+          // (of equal ones the later token does not count)
+          if (count == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1]) + 1));
+        }
+        const unsigned still = __ballot_sync(0xffffffffu, x[u] >= t);
+        if (x[u] >= t) {
+          const int to = count + __popc(still & ((1u << lane) - 1));
+          l.value[to] = x[u];
+          l.index[to] = at[u];
+        }
+        count += __popc(still);
+      }
+    }
+    n = 0;
+    __syncwarp();
+  };
+  const int key = ordered(t) >> 16;
+#pragma unroll 4
+  for (int i = 0; i < turns; ++i) {
+    const bool is = tops[i * 32 + lane] >= key;
+    const unsigned has = __ballot_sync(0xffffffffu, is);
+    if (is) codes[n + __popc(has & ((1u << lane) - 1))] = static_cast<uint16_t>(i * 32 + lane);
+    n += __popc(has);
+    if (n + 32 > kCodes) look();
+  }
+  look();
+  return count;
+}
+
 // CTAs behind those of the parts: 1 / len^alpha of a row per thread (its fp64 power
 // would stand in the merge's way).
 __device__ void row_inverses(const BeamArgs& a, int row) {
@@ -397,13 +437,14 @@ template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   List* lists = reinterpret_cast<List*>(raw);
+  int16_t* tops = reinterpret_cast<int16_t*>(raw + kWarps * sizeof(List)) + (threadIdx.x >> 5) * a.turns * 32;
   __shared__ Bounds bounds;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ctas = (a.parts + kWarps - 1) / kWarps;  // of a row
   const int row = blockIdx.x / ctas, cta = blockIdx.x - row * ctas;
   const int first = cta * a.each + min(cta, a.more), warps = a.each + (cta < a.more), part = first + warp;
-  if (threadIdx.x < kWarps) reinterpret_cast<float*>(&bounds)[threadIdx.x] = static_cast<int>(threadIdx.x) < warps ? -INFINITY : INFINITY;
+  if (threadIdx.x < kWarps) reinterpret_cast<float*>(&bounds)[threadIdx.x] = static_cast<int>(threadIdx.x) < warps ? NAN : INFINITY;
   __syncthreads();
   if (row >= a.batch * a.beams) {
     row_inverses(a, (blockIdx.x - a.batch * a.beams * ctas) * kThreads + threadIdx.x);
@@ -417,19 +458,36 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
   p.c0 = min(part * a.chunk, a.vocab), p.c1 = min(p.c0 + a.chunk, a.vocab);
   p.start = p.c0 - static_cast<int>((reinterpret_cast<uintptr_t>(p.base + static_cast<size_t>(p.c0) * (16 / p.kEach)) & 15) / (16 / p.kEach));
   List& l = lists[warp];
-  fetch_words<BF16>(p, 0, l.ring[0]);  // (on their way while the row's state arrives)
+  start_words<BF16>(p, l);  // (on their way while the row's state arrives)
   if (ended != 0 || !(score > -INFINITY)) {  // (nothing, or NaN: the merge sees it)
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
+  const int give = max(1, a.select / warps + (warp < a.select % warps));
   float m, sum;
-  int count;
-  if (!part_pass<BF16, false>(p, l, &bounds, warps, a.select, m, sum, count))
-    part_pass<BF16, true>(p, l, &bounds, warps, a.select, m, sum, count);
+  if (!part_pass<BF16, false>(p, l, tops, &bounds, give, m, sum)) {
+    start_words<BF16>(p, l);
+    part_pass<BF16, true>(p, l, tops, &bounds, give, m, sum);
+  }
   if (lane == 0) a.stats[static_cast<size_t>(row) * a.parts + part] = make_float2(m, sum);
-  count = keep_best(l, count, a.select);
+  int count = collect<BF16>(p, l, tops, &bounds, a.select);
   const size_t all = static_cast<size_t>(a.beams) * a.parts;
   float2* list = a.lists + static_cast<size_t>(row / a.beams) * a.select * all + static_cast<size_t>(row % a.beams) * a.parts + part;
+  if (count <= 32) {  // each entry's rank, a lane an entry
+    const float x = lane < count ? l.value[lane] : -INFINITY;
+    const int k = lane < count ? l.index[lane] : -1;
+    int rank = 0;
+#pragma unroll 4
+    for (int o = 0; o < count; ++o) {
+      const float y = __shfl_sync(0xffffffffu, x, o);
+      rank += y > x || (y == x && o < lane && lane < count);
+    }
+    if (lane >= count) rank = lane;
+    if (rank < a.select) list[rank * all] = make_float2(x, __int_as_float(k));
+    if (32 + lane < a.select) list[(32 + lane) * all] = make_float2(-INFINITY, __int_as_float(-1));
+    return;
+  }
+  count = keep_best(l, count, a.select);
   for (int i = lane; i < a.select; i += 32)
     list[i * all] = i < count ? make_float2(l.value[i], __int_as_float(l.index[i])) : make_float2(-INFINITY, __int_as_float(-1));
 }
@@ -528,10 +586,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     const size_t row = static_cast<size_t>(b) * K + k;
     const float2* part = a.stats + row * a.parts;
     const float2 x = lane < a.parts ? part[lane] : make_float2(-INFINITY, 0.0f);
-    const float2 y = lane + 32 < a.parts ? part[lane + 32] : make_float2(-INFINITY, 0.0f);
     const double inverse = a.length_penalty != 0.0f ? a.inverse[row] : 1.0;
-    const float m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(fmaxf(x.x, y.x))));
-    float sum = isinf(m) ? 0.0f : x.y * expf(x.x - m) + y.y * expf(y.x - m);
+    const float m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(x.x)));
+    float sum = isinf(m) ? 0.0f : x.y * expf(x.x - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
@@ -721,19 +778,20 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
 int beam_max_select() { return kMaxSelect; }
 int beam_max_beams() { return kMaxBeams; }
 
-// Parts of a row, of whole 512 entries: as many as 8 warps a CTA and six CTAs for every
-// SM over all rows make, so that the last ones leave few SMs idle (with as many as are
-// resident, 4, the busiest SM had a sixth more than its share of 512 rows).  A row's
-// CTAs share them evenly: one that is left with few warps has a worse bound (1 request
-// of 32 beams, S = 64, V 151936: 41.0 us with the rest in the last CTA, 36.9 so; 4 of
-// 16, S = 32: 25.6 and 22.6).
+// Parts of a row, of whole 512 entries: as many whole CTAs a row as leave no more than
+// are resident, 4 an SM, but 32 parts at most, whose lists the merge reads (V = 151936, 1
+// request of 32 beams, S = 64: 22.6 us, of 64 parts 30.8, of 16 24.8; 4 of 16, S = 32:
+// 18.5, 24.7 and 19.6).  A row's CTAs share them evenly: one that is left with few warps
+// has a worse bound.
 void plan_beam_parts(BeamArgs& a, int sms) {
-  const long long rows = static_cast<long long>(a.batch) * a.beams;
-  const long long most = min((a.vocab + 511) / 512, kMaxParts), want = (6ll * sms + rows - 1) / rows * kWarps;
+  const long long rows = static_cast<long long>(a.batch) * a.beams, fit = 4ll * sms / rows;
+  const long long most = min((a.vocab + 511) / 512, kMaxParts), want = (fit > 1 ? fit : 1) * kWarps;
   const int parts = static_cast<int>(want < most ? want : most);
   a.chunk = ((a.vocab + parts - 1) / parts + 511) / 512 * 512;
   a.parts = (a.vocab + a.chunk - 1) / a.chunk;
   const int ctas = (a.parts + kWarps - 1) / kWarps;
+  const int entries = 32 * kWords * (a.bf16 ? 8 : 4);  // of a turn
+  a.turns = (a.chunk + 7 + entries - 1) / entries;  // (a part may begin inside a word)
   a.each = a.parts / ctas, a.more = a.parts % ctas;
 }
 
@@ -741,10 +799,10 @@ int launch_beam_select(const BeamArgs& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.batch) * a.beams;
   const long long ctas = rows * ((a.parts + kWarps - 1) / kWarps) + (a.length_penalty != 0.0f ? (rows + kThreads - 1) / kThreads : 0);
   const unsigned grid = static_cast<unsigned>(ctas);
-  const int smem = kWarps * sizeof(List);
-  static_assert(kWarps * sizeof(List) <= 56 * 1024, "four CTAs an SM");
+  const int smem = kWarps * (static_cast<int>(sizeof(List)) + a.turns * 64);
+  static_assert(sizeof(List) % 16 == 0, "words");
   const auto kernel = a.bf16 ? beam_rows_kernel<true> : beam_rows_kernel<false>;
-  if (smem > 48 * 1024 &&
+  if (smem > 47 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return -1;
   kernel<<<grid, kThreads, smem, stream>>>(a);

@@ -242,6 +242,7 @@ struct BeamArgs {
   size_t stride;
   int32_t batch, beams, select, vocab, bf16, end_token, parts, chunk;
   int32_t each, more;         // a row's CTAs take each parts, the first more of them one more
+  int32_t turns;              // of a part, most
   float length_penalty;
 };
 int launch_beam_select(const BeamArgs& a, cudaStream_t stream);

@@ -120,8 +120,8 @@ def test_beam_pointers_and_workspace(lib):
     # row (rounded to 256 bytes in all), and 6 entries a part
     assert need == 2 * 256 + 12 * 6 * 8
     big = beams(batch=64, beams=8, select=16, vocab=128256)
-    # two CTAs of 8 warps a row: six for every SM
-    assert lib.tv_beam_select_workspace_size(C.byref(big)) == 512 * 8 + 512 * 16 * 8 * (1 + 16)
+    # a CTA of 8 warps a row: four for every SM
+    assert lib.tv_beam_select_workspace_size(C.byref(big)) == 512 * 8 + 512 * 8 * 8 * (1 + 16)
 
     def call(args):
         return lib.tv_beam_select(C.byref(p), *args, at(20), C.c_size_t(need), None)
