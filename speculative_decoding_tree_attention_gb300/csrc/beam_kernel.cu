@@ -26,9 +26,10 @@
 // score near 20 to fp32 (1e-6).  Candidates of different beams that lie closer than
 // that may come in either order, the same in every call.
 //
-// Bound: HBM for large calls (the rows take 22 us of the first one here at 6 TB/s, but up
-// to 27 where 4 instead of 3 of 512 CTAs are on an SM), with the merge's 5 us behind; for
-// few requests the latency of two dependent kernels.  Measured (device time, the call
+// Bound: HBM for large calls (18 us of the first one here are the pass over the logits,
+// near 7 TB/s; then the bound and the lists, 3 to 4, up to 4 more where 4 instead of 3 of
+// the 512 CTAs are on an SM, and the merge's 5); for few requests the latency of two
+// dependent kernels.  Measured (device time, the call
 // replayed): 64 requests of 8 beams, V = 128256, bf16, S = 16: 36 us; 32 of 8, V = 32000,
 // fp32: 15.4; 1 of 4: 9.3.  On the way, the first case: a CTA per 8192 entries, entries
 // in registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
