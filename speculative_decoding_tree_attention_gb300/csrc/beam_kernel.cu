@@ -313,6 +313,7 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, int16_t* tops, Bounds* b
       }
       m = top;
     }
+    float2 part = make_float2(0.0f, 0.0f);  // (a turn's by itself: few roundings of each term)
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
       float2 v[kPairs];
@@ -326,9 +327,10 @@ __device__ bool part_pass(const Part<BF16>& p, List& l, int16_t* tops, Bounds* b
         } else {
           e = fma2(v[i], make_float2(kLog2eHi, kLog2eHi), make_float2(c, c));
         }
-        acc = add2(acc, make_float2(ex2_approx(e.x), ex2_approx(e.y)));
+        part = add2(part, make_float2(ex2_approx(e.x), ex2_approx(e.y)));
       }
     }
+    acc = add2(acc, part);
   }
   sum = acc.x + acc.y;
   const float all = of_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
@@ -376,9 +378,14 @@ __device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const 
   uint16_t* codes = reinterpret_cast<uint16_t*>(l.ring);
   constexpr int kCodes = sizeof(l.ring) / 2, kOf = kWords * p.kEach, kAtOnce = 32 / kOf, kFly = 8 / kAtOnce;
   int n = 0, count = 0;
+  bool raised = false;
   const auto look = [&] {
     __syncwarp();
     for (int q = 0; q < n; q += kFly * kAtOnce) {
+      if (raised) {  // (by now none of these may pass)
+        const int k = q + lane;
+        if (!__any_sync(0xffffffffu, lane < kFly * kAtOnce && k < n && tops[codes[min(k, n - 1)]] >= ordered(t) >> 16)) continue;
+      }
       float x[kFly];
       int at[kFly];
 #pragma unroll
@@ -397,8 +404,9 @@ __device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const 
         if (hit == 0) continue;
         if (count + 32 > kList) {
           count = keep_best(l, count, select);
-          // (of equal ones the later token does not count)
-          if (count == select) t = fmaxf(t, of_ordered(ordered(l.value[select - 1]) + 1));
+          // (of equal ones the later token does not count: from the type's next value on)
+          if (count == select) t = fmaxf(t, of_ordered((ordered(l.value[select - 1]) | (BF16 ? 0xffff : 0)) + 1));
+          raised = true;
         }
         const unsigned still = __ballot_sync(0xffffffffu, x[u] >= t);
         if (x[u] >= t) {
@@ -412,14 +420,40 @@ __device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const 
     n = 0;
     __syncwarp();
   };
-  const int key = ordered(t) >> 16;
+  // the lanes' words of turns that pass
+  const auto gather = [&](bool all) {
+    const int key = ordered(t) >> 16;
 #pragma unroll 4
-  for (int i = 0; i < turns; ++i) {
-    const bool is = tops[i * 32 + lane] >= key;
-    const unsigned has = __ballot_sync(0xffffffffu, is);
-    if (is) codes[n + __popc(has & ((1u << lane) - 1))] = static_cast<uint16_t>(i * 32 + lane);
-    n += __popc(has);
-    if (n + 32 > kCodes) look();
+    for (int i = 0; i < turns; ++i) {
+      const bool is = tops[i * 32 + lane] >= key;
+      const unsigned has = __ballot_sync(0xffffffffu, is);
+      if (is) codes[n + __popc(has & ((1u << lane) - 1))] = static_cast<uint16_t>(i * 32 + lane);
+      n += __popc(has);
+      if (n + 32 > kCodes) {
+        if (!all) return;
+        look();
+      }
+    }
+  };
+  gather(false);
+  if (n > 32 + 4 * (select / kWarps)) {
+    // The warps' words are not alike (a mask over some, a row that rises): the bound of
+    // this warp's words alone, the largest that `select` of them are at or above.
+    int low = ordered(t) >> 16, high = SHRT_MAX;
+    while (low < high) {
+      const int middle = (low + high + 1) >> 1;
+      int some = 0;
+      for (int i = 0; i < turns; ++i) some += tops[i * 32 + lane] >= middle;
+      if (static_cast<int>(__reduce_add_sync(0xffffffffu, some)) >= select) {
+        low = middle;
+      } else {
+        high = middle - 1;
+      }
+    }
+    t = fmaxf(t, of_ordered(low << 16));
+    n = 0;
+    __syncwarp();
+    gather(true);
   }
   look();
   return count;

@@ -274,3 +274,27 @@ def test_repeated_calls_agree_bit_for_bit():
         b = run(x, scores, 8, 16, lengths)
         for k in a:
             np.testing.assert_array_equal(a[k], b[k])
+
+
+def test_many_long_rows():
+    """Rows of one CTA each and of the largest vocabulary: 65 turns of a warp, whose sums
+    are 16 of a turn, 65 of turns, 5 of lanes and 8 of parts: 94 2^-24, below 2^-17 with
+    the rest."""
+    ensure_built()
+    batch, beams, select, vocab = 170, 4, 8, 262143
+    g = torch.Generator(device="cuda").manual_seed(41)
+    logits = torch.randn(batch * beams, vocab, device="cuda", generator=g) * 3
+    scores = -20 * torch.rand(batch * beams, device="cuda", generator=g)
+    got = tv.beam_select(logits, scores, beams=beams, select=select)
+    sure = 0
+    some = range(0, batch, 7)
+    for b in some:
+        rows = slice(b * beams, (b + 1) * beams)
+        x = logits[rows].double()
+        best, at = (scores[rows].double()[:, None] + x - x.logsumexp(-1, keepdim=True)).flatten().topk(select + 1)
+        assert (got["scores"][b].double() - best[:select]).abs().max() <= LSE + 2.0 ** -24 * 40
+        if (best[:-1] - best[1:]).min() > 2.0 ** -15:
+            sure += 1
+            assert torch.equal(got["tokens"][b].long(), at[:select] % vocab)
+            assert torch.equal(got["parents"][b].long(), b * beams + at[:select] // vocab)
+    assert sure > len(some) // 2 and (got["status"] == 0).all()
