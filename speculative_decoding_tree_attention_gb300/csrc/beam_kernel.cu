@@ -13,8 +13,10 @@
 // After its part each warp tells a bound: if warp w has c_w lanes whose largest entry is
 // at least t, and the c_w add up to S, S entries of the row are no worse than t; the 8
 // warps of a CTA, which work on one row, take the least of their c_w-th largest, c_w
-// about S / 8.  Few noted entries pass it (3 to 6 of 512 of a warp); their words are
-// read again, an entry a lane, and ranked into the warp's list.  Within a row the order
+// about S / 8.  Few noted entries pass it (3 to 6 of 512 of a warp; where many do, as
+// with a mask over some warps' parts, the warps tell bounds of their own notes and take
+// the best: 64 x 8 of V = 128256 with the upper half masked 64 us, without 151); their
+// words are read again, an entry a lane, and ranked into the warp's list.  Within a row the order
 // is exact: it is that of the logits, and of equal ones the lower token.
 //
 // beam_merge_kernel: a CTA per request joins the parts of each row to its LSE
@@ -30,7 +32,7 @@
 // near 7 TB/s; then the bound and the lists, 3 to 4, up to 4 more where 4 instead of 3 of
 // the 512 CTAs are on an SM, and the merge's 5); for few requests the latency of two
 // dependent kernels.  Measured (device time, the call
-// replayed): 64 requests of 8 beams, V = 128256, bf16, S = 16: 36 us; 32 of 8, V = 32000,
+// replayed): 64 requests of 8 beams, V = 128256, bf16, S = 16: 35 us; 32 of 8, V = 32000,
 // fp32: 15.4; 1 of 4: 9.3.  On the way, the first case: a CTA per 8192 entries, entries
 // in registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
 // bound that rises as it reads 71; bounds shared by a CTA's warps while they read 53;
@@ -254,11 +256,20 @@ __device__ __forceinline__ void fetch_words(const Part<BF16>& p, int w0, uint4* 
 __device__ __forceinline__ void commit_words() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_words() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
 
-// What the warps of a CTA share: the c_w-th largest of the lanes' maxima of each (+inf
-// of warps without a part, NaN: not known yet).
+// What the warps of a CTA tell each other: the c_w-th largest of their lanes' maxima
+// (+inf of warps without a part) and, where that leaves many, a bound of their own (-inf:
+// none).  NaN: not known yet.
 struct Bounds {
-  float nth[kWarps];
+  float nth[kWarps], own[kWarps];
 };
+// All warps' (every warp tells its own whatever the others do): that of warp `lane`.
+__device__ __forceinline__ float told(const float* of, float others) {
+  const int lane = threadIdx.x & 31;
+  float t = NAN;
+  for (int i = 0; i < 1 << 20 && __any_sync(0xffffffffu, t != t); ++i)
+    t = lane < kWarps ? reinterpret_cast<const volatile float*>(of)[lane] : others;
+  return t == t ? t : -INFINITY;
+}
 
 // One pass over a part by a warp: the maximum m and sum of exp(x - m), and of every
 // lane's words of every turn the largest entry, as the upper half of its place in the
@@ -366,14 +377,10 @@ __device__ __forceinline__ void start_words(const Part<BF16>& p, List& l) {
 // The part's entries from the CTA's bound on into the warp's list; returns how many
 // there are.  For all warps of the CTA that have parts.
 template <bool BF16>
-__device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const Bounds* bounds, int select) {
-  const int lane = threadIdx.x & 31;
+__device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, Bounds* bounds, int select) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int words = (p.c1 - p.start + p.kEach - 1) / p.kEach, turns = (words + 32 * kWords - 1) / (32 * kWords);
-  // (every warp tells its own whatever the others do)
-  float t = NAN;
-  for (int i = 0; i < 1 << 20 && __any_sync(0xffffffffu, t != t); ++i)
-    t = lane < kWarps ? reinterpret_cast<const volatile float*>(bounds->nth)[lane] : INFINITY;
-  t = of_ordered(__reduce_min_sync(0xffffffffu, ordered(t == t ? t : -INFINITY)));
+  float t = of_ordered(__reduce_min_sync(0xffffffffu, ordered(told(bounds->nth, INFINITY))));
   t = fmaxf(t, -FLT_MAX);  // (-inf is no candidate)
   uint16_t* codes = reinterpret_cast<uint16_t*>(l.ring);
   constexpr int kCodes = sizeof(l.ring) / 2, kOf = kWords * p.kEach, kAtOnce = 32 / kOf, kFly = 8 / kAtOnce;
@@ -436,13 +443,17 @@ __device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const 
     }
   };
   gather(false);
-  if (n > 32 + 4 * (select / kWarps)) {
-    // The warps' words are not alike (a mask over some, a row that rises): the bound of
-    // this warp's words alone, the largest that `select` of them are at or above.
+  volatile float* own = reinterpret_cast<volatile float*>(bounds->own);
+  if (n <= 32 + 4 * (select / kWarps)) {
+    if (lane == 0) own[warp] = -INFINITY;
+  } else {
+    // The warps' words are not alike (a mask over some, a row that rises): the best of
+    // the bounds of single warps' words, the largest that `select` of them are at or above.
     int low = ordered(t) >> 16, high = SHRT_MAX;
     while (low < high) {
       const int middle = (low + high + 1) >> 1;
       int some = 0;
+#pragma unroll 4
       for (int i = 0; i < turns; ++i) some += tops[i * 32 + lane] >= middle;
       if (static_cast<int>(__reduce_add_sync(0xffffffffu, some)) >= select) {
         low = middle;
@@ -450,7 +461,8 @@ __device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, const 
         high = middle - 1;
       }
     }
-    t = fmaxf(t, of_ordered(low << 16));
+    if (lane == 0) own[warp] = of_ordered(low << 16);
+    t = fmaxf(t, of_ordered(__reduce_max_sync(0xffffffffu, ordered(told(bounds->own, -INFINITY)))));
     n = 0;
     __syncwarp();
     gather(true);
@@ -479,7 +491,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
   const int ctas = (a.parts + kWarps - 1) / kWarps;  // of a row
   const int row = blockIdx.x / ctas, cta = blockIdx.x - row * ctas;
   const int first = cta * a.each + min(cta, a.more), warps = a.each + (cta < a.more), part = first + warp;
-  if (threadIdx.x < kWarps) reinterpret_cast<float*>(&bounds)[threadIdx.x] = static_cast<int>(threadIdx.x) < warps ? NAN : INFINITY;
+  if (threadIdx.x < kWarps) {
+    const bool here = static_cast<int>(threadIdx.x) < warps;
+    bounds.nth[threadIdx.x] = here ? NAN : INFINITY;
+    bounds.own[threadIdx.x] = here ? NAN : -INFINITY;
+  }
   __syncthreads();
   if (row >= a.batch * a.beams) {
     row_inverses(a, (blockIdx.x - a.batch * a.beams * ctas) * kThreads + threadIdx.x);
