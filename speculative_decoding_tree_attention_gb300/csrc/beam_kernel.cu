@@ -16,8 +16,8 @@
 // about S / 8.  Few noted entries pass it (3 to 6 of 512 of a warp; where many do, as
 // with a mask over some warps' parts, the warps tell bounds of their own notes and take
 // the best: 64 x 8 of V = 128256 with the upper half masked 64 us, without 151); their
-// words are read again, an entry a lane, and ranked into the warp's list.  Within a row the order
-// is exact: it is that of the logits, and of equal ones the lower token.
+// words are read again, an entry a lane, and ranked into the warp's list.  Within a row
+// the order is exact: it is that of the logits, and of equal ones the lower token.
 //
 // beam_merge_kernel: a CTA per request joins the parts of each row to its LSE
 // and picks the S best of all rows' lists the same way: in fp32 with an error

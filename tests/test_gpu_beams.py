@@ -298,3 +298,37 @@ def test_many_long_rows():
             assert torch.equal(got["tokens"][b].long(), at[:select] % vocab)
             assert torch.equal(got["parents"][b].long(), b * beams + at[:select] // vocab)
     assert sure > len(some) // 2 and (got["status"] == 0).all()
+
+
+def unlike(kind, dtype, vocab, seed):
+    """Two requests of three beams whose best are all in some parts of a row."""
+    logits, scores, lengths, g = make(2, 3, vocab, dtype, seed)
+    if kind == "upper half":
+        logits[:, vocab // 2:] = -INF
+    elif kind == "lowest value":
+        logits[:, vocab // 3:] = torch.finfo(dtype).min
+    elif kind == "few":
+        keep = logits[:, 1000:1300].clone()
+        logits[:] = -INF
+        logits[:, 1000:1300] = keep
+    elif kind == "rising":
+        logits[:] = (torch.arange(vocab) * 2.0 ** -10).to(dtype)
+    elif kind == "falling":
+        logits[:] = (torch.arange(vocab, 0, -1) * 2.0 ** -10).to(dtype)
+    elif kind == "last":
+        logits[:, -5:] += 20
+    return logits, scores, lengths
+
+
+KINDS = ["upper half", "lowest value", "few", "rising", "falling", "last"]
+
+
+@pytest.mark.parametrize("select", [5, 16, 64])
+@pytest.mark.parametrize("kind", KINDS)
+def test_parts_that_are_not_alike(kind, select):
+    ensure_built()
+    for dtype in (torch.float32, torch.bfloat16):
+        for vocab in (40000, 9001):
+            logits, scores, lengths = unlike(kind, dtype, vocab, 51)
+            ref = oracle.beam_select(logits.double().numpy(), scores, 3, select, lengths)
+            compare(run(logits.cuda(), scores, 3, select, lengths), ref, lengths)
