@@ -723,7 +723,9 @@ int tv_rotate_qk(const tv_rotate_params* params, const uint16_t* q, const uint16
  * finished 0.  A score that is NaN or +inf, a logit of +inf in a row that is read,
  * or a length below 0 or above 2^24 gives the request TV_ERR_BAD_TREE and such
  * entries throughout.
- * Within a row the order is exact.  LSE is off by about 1e-7 (fp32 exps and sums,
+ * Within a row the order is exact, that of the logits and of equal ones the lower
+ * token, also where a large score or logit leaves the keys of a row one value in fp64,
+ * in which rows are compared.  LSE is off by about 1e-7 (fp32 exps and sums,
  * joined in fp64), so candidates of different rows whose scores are closer than
  * that may come in either order, the same in every call; scores are rounded once
  * to fp32.

@@ -21,7 +21,8 @@
 //
 // beam_merge_kernel: a CTA per request joins the parts of each row to its LSE
 // and picks the S best of all rows' lists the same way: in fp32 with an error
-// bound that keeps every candidate that may be among them, those few in fp64.
+// bound that keeps every candidate that may be among them, those few in fp64; equal keys
+// there by beam, logit and token.
 //
 // LSE: exps and their sums in fp32 against the lane's own maximum, joined in fp32
 // and added to the maximum in fp64: off by about 1e-7, less than the rounding of a
@@ -550,11 +551,13 @@ struct MergeSmem {
   float top[kMaxBeams];      // the row's maximum
   double inverse[kMaxBeams]; // 1 / len^alpha
   unsigned long long key[kFound + kMaxBeams];  // in the order of the keys' values
-  float value[kFound + kMaxBeams];             // logit, then score
+  float logit[kFound + kMaxBeams];
+  float score[kFound + kMaxBeams];
   int at[kFound + kMaxBeams];                  // beam * 2^18 + token
   float2 approx[kMaxBeams];  // (base, inverse) in fp32
   unsigned long long best_key[kWarps];
-  int best_at[kWarps], best_list[kWarps];
+  unsigned long long best_place[kWarps];
+  int best_list[kWarps];
   int state[kMaxBeams], length[kMaxBeams];
   int live[kMaxBeams];       // the live beams, in order
   float nth[kWarps];
@@ -567,7 +570,18 @@ __device__ __forceinline__ unsigned long long ordered_key(double x) {
   const long long b = __double_as_longlong(x + 0.0);  // (one zero)
   return static_cast<unsigned long long>(b) ^ (b < 0 ? ~0ull : 1ull << 63);
 }
-__device__ __forceinline__ bool better(unsigned long long k, int i, unsigned long long l, int j) {
+// Among equal keys: beam, then the logit downwards, then the token.  (Where a score or a
+// row's maximum is so large that the keys of different logits round to one value, the
+// order within the row is still that of the logits.)
+__device__ __forceinline__ unsigned long long place_in_order(int at, float logit) {
+  const uint32_t down = 0x7fffffffu - static_cast<uint32_t>(ordered(logit));
+  return static_cast<unsigned long long>(at >> 18) << 50 | static_cast<unsigned long long>(down) << 18 | static_cast<unsigned>(at & ((1 << 18) - 1));
+}
+__device__ __forceinline__ int at_of(unsigned long long place) {
+  return static_cast<int>(place >> 50) << 18 | (static_cast<int>(place) & ((1 << 18) - 1));
+}
+template <typename T>
+__device__ __forceinline__ bool better(unsigned long long k, T i, unsigned long long l, T j) {
   return k > l || (k == l && i < j);
 }
 
@@ -596,7 +610,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
       const unsigned lives = __ballot_sync(0xffffffffu, state == kLive), ends = __ballot_sync(0xffffffffu, state == kEnded);
       const unsigned below = (1u << lane) - 1;
       if (state == kLive) s.live[live + __popc(lives & below)] = k;
-      if (state == kEnded) s.at[ended + __popc(ends & below)] = k << 18;  // (one candidate, at the lowest place of its beam)
+      if (state == kEnded) s.at[ended + __popc(ends & below)] = k << 18;  // (its one candidate)
       live += __popc(lives);
       ended += __popc(ends);
     }
@@ -685,7 +699,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   const auto keep = [&](float2 e, int k) {
     const int at = atomicAdd(&s.found, 1);
     if (at < kFound + kMaxBeams) {
-      s.value[at] = e.x;
+      s.logit[at] = e.x;
       s.at[at] = k << 18 | __float_as_int(e.y);
     }
   };
@@ -761,21 +775,32 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   };
   // scores and keys of the few (of all ended beams, the first), in fp64
   const int found = s.found;
+  // Whether a smaller logit of a row may have the same key: the next one is at least
+  // 2^-24 |x| below, and the roundings of a score and its key add up to less than 2^-50 of
+  // its terms.
+  bool alike = false;
   for (int i = tid; i < min(found, kFound + kMaxBeams); i += kThreads) {
     const int k = s.at[i] >> 18;
-    const double score = score_of(s.value[i], k);
-    s.value[i] = static_cast<float>(score);
+    const float x = s.logit[i];
+    const double score = score_of(x, k);
+    alike |= i >= s.ended && !(fabsf(x) > 0x1p-25f * (fabsf(s.approx[k].x) + fabsf(x - s.top[k])));
+    s.score[i] = static_cast<float>(score);
     s.key[i] = ordered_key(score * s.inverse[k]);
   }
-  __syncthreads();
+  alike = __syncthreads_or(alike);
   if (found <= kFound + kMaxBeams) {
     for (int i = tid; i < found; i += kThreads) {
       const unsigned long long key = s.key[i];
       const int at = s.at[i];
       int rank = 0;
+      if (alike) {
+        const unsigned long long place = place_in_order(at, s.logit[i]);
+        for (int j = 0; j < found; ++j) rank += better(s.key[j], place_in_order(s.at[j], s.logit[j]), key, place);
+      } else {  // (equal keys of a row are equal logits: beam and token decide)
 #pragma unroll 4
-      for (int j = 0; j < found; ++j) rank += better(s.key[j], s.at[j], key, at);
-      if (rank < S) put(rank, s.value[i], at);
+        for (int j = 0; j < found; ++j) rank += better(s.key[j], s.at[j], key, at);
+      }
+      if (rank < S) put(rank, s.score[i], at);
     }
     for (int i = found + tid; i < S; i += kThreads) put_none(i);
     return;
@@ -786,38 +811,41 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   unsigned ended_left = 0;  // of the ended beams' candidates, a thread's (two at most) that are not taken
   for (int i = tid, j = 0; i < s.ended; i += kThreads, ++j) ended_left |= 1u << j;
   for (int rank = 0; rank < S; ++rank) {
-    unsigned long long key = 0;
-    int at = INT_MAX, list = -1;
+    unsigned long long key = 0, place = ~0ull;
+    int list = -1;
     for (int q = tid; q < own; q += kThreads) {
       const int r = s.next[q];
       if (r >= S) continue;
       const float2 e = entry(q, r);
-      const int k = beam_of(q), place = k << 18 | __float_as_int(e.y);
       if (!(e.x > -INFINITY)) continue;
-      const unsigned long long v = ordered_key(score_of(e.x, k) * s.inverse[k]);
-      if (better(v, place, key, at)) key = v, at = place, list = q;
+      const int k = beam_of(q);
+      const unsigned long long v = ordered_key(score_of(e.x, k) * s.inverse[k]), p = place_in_order(k << 18 | __float_as_int(e.y), e.x);
+      if (better(v, p, key, place)) key = v, place = p, list = q;
     }
-    for (int i = tid, j = 0; i < s.ended; i += kThreads, ++j)
-      if ((ended_left >> j & 1u) && better(s.key[i], s.at[i], key, at)) key = s.key[i], at = s.at[i], list = -2 - i;
+    for (int i = tid, j = 0; i < s.ended; i += kThreads, ++j) {
+      const unsigned long long p = place_in_order(s.at[i], 0.0f);
+      if ((ended_left >> j & 1u) && better(s.key[i], p, key, place)) key = s.key[i], place = p, list = -2 - i;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, key, o);
-      const int a2 = __shfl_xor_sync(0xffffffffu, at, o), l2 = __shfl_xor_sync(0xffffffffu, list, o);
-      if (better(k2, a2, key, at)) key = k2, at = a2, list = l2;
+      const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, key, o), p2 = __shfl_xor_sync(0xffffffffu, place, o);
+      const int l2 = __shfl_xor_sync(0xffffffffu, list, o);
+      if (better(k2, p2, key, place)) key = k2, place = p2, list = l2;
     }
-    if (lane == 0) s.best_key[warp] = key, s.best_at[warp] = at, s.best_list[warp] = list;
+    if (lane == 0) s.best_key[warp] = key, s.best_place[warp] = place, s.best_list[warp] = list;
     __syncthreads();
     for (int i = 0; i < kWarps; ++i)
-      if (better(s.best_key[i], s.best_at[i], key, at)) key = s.best_key[i], at = s.best_at[i], list = s.best_list[i];
+      if (better(s.best_key[i], s.best_place[i], key, place)) key = s.best_key[i], place = s.best_place[i], list = s.best_list[i];
     if (list == -1) {
       if (tid == 0) put_none(rank);
     } else if (list >= 0) {
       if (tid == list % kThreads) {
+        const int at = at_of(place);
         put(rank, static_cast<float>(score_of(entry(list, s.next[list]).x, at >> 18)), at);
         s.next[list] += 1;
       }
     } else if (tid == (-2 - list) % kThreads) {
-      put(rank, s.value[-2 - list], at);
+      put(rank, s.score[-2 - list], at_of(place));
       ended_left &= ~(1u << ((-2 - list) / kThreads));
     }
     __syncthreads();
