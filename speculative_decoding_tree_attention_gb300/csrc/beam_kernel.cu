@@ -857,6 +857,18 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
 int beam_max_select() { return kMaxSelect; }
 int beam_max_beams() { return kMaxBeams; }
 
+namespace {
+
+// Turns of a part of `entries` entries, which may begin inside a word, and the shared
+// memory of a CTA whose parts have that many.
+int turns_of(int entries, bool bf16) {
+  const int each = 32 * kWords * (bf16 ? 8 : 4);
+  return (entries + 7 + each - 1) / each;
+}
+int smem_of(int turns) { return kWarps * (static_cast<int>(sizeof(List)) + turns * 64); }
+
+}  // namespace
+
 // Parts of a row, of whole 512 entries: as many whole CTAs a row as leave no more than
 // are resident, 4 an SM, but 32 parts at most, whose lists the merge reads (V = 151936, 1
 // request of 32 beams, S = 64: 22.6 us, of 64 parts 30.8, of 16 24.8; 4 of 16, S = 32:
@@ -869,8 +881,7 @@ void plan_beam_parts(BeamArgs& a, int sms) {
   a.chunk = ((a.vocab + parts - 1) / parts + 511) / 512 * 512;
   a.parts = (a.vocab + a.chunk - 1) / a.chunk;
   const int ctas = (a.parts + kWarps - 1) / kWarps;
-  const int entries = 32 * kWords * (a.bf16 ? 8 : 4);  // of a turn
-  a.turns = (a.chunk + 7 + entries - 1) / entries;  // (a part may begin inside a word)
+  a.turns = turns_of(a.chunk, a.bf16);
   a.each = a.parts / ctas, a.more = a.parts % ctas;
 }
 
@@ -878,11 +889,13 @@ int launch_beam_select(const BeamArgs& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.batch) * a.beams;
   const long long ctas = rows * ((a.parts + kWarps - 1) / kWarps) + (a.length_penalty != 0.0f ? (rows + kThreads - 1) / kThreads : 0);
   const unsigned grid = static_cast<unsigned>(ctas);
-  const int smem = kWarps * (static_cast<int>(sizeof(List)) + a.turns * 64);
+  const int smem = smem_of(a.turns);
   static_assert(sizeof(List) % 16 == 0, "words");
   const auto kernel = a.bf16 ? beam_rows_kernel<true> : beam_rows_kernel<false>;
+  // (the kernel's limit is all host threads': always that of the longest part)
+  const int limit = smem_of(turns_of((1 << 18) / kWarps, a.bf16));
   if (smem > 47 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess)
     return -1;
   kernel<<<grid, kThreads, smem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return -1;

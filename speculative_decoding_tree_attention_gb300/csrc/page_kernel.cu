@@ -28,6 +28,8 @@
 #include <cooperative_groups.h>
 #include <limits.h>
 
+#include <algorithm>
+
 #include "tv_device.cuh"
 #include "tv_launch.h"
 
@@ -43,6 +45,7 @@ constexpr int kThreads = 1024;       // of a CTA of the cluster
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowThreads = 256;     // of a CTA of the kernels over tables
 constexpr int kAhead = 8;            // entries of a row that a lane has in flight
+constexpr int kMaxRows = 65536;      // of a table
 constexpr int kNeeds = 8192;         // pieces' needs that a CTA holds
 constexpr int kFewEntries = 16384;   // table entries that a CTA writes beside its other work
 
@@ -829,7 +832,9 @@ int launch_alloc_pages(PageArgs a, cudaStream_t stream) {
   a.piece = (a.width + a.cuts - 1) / a.cuts;
   const size_t smem = static_cast<size_t>(each) * (a.cuts + 3) * 4;  // (65536 rows are 8192 for each of 8 CTAs: 128 KB)
   const auto kernel = ctas == 1 ? alloc_kernel<1, false> : ctas == 8 ? alloc_kernel<8, false> : alloc_kernel<kCluster, true>;
-  if (smem > 24 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+  // (the kernel's limit is all host threads': always that of the most rows)
+  const int most = ctas == 1 ? kThreads : kMaxRows / ctas, limit = (std::max(kNeeds, most) + 3 * most) * 4;
+  if (smem > 24 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess)
     return -1;
   if (ctas <= 8) return ctas == 1 ? launch_group<1>(kernel, a, smem, stream) : launch_group<8>(kernel, a, smem, stream);
   const int warps = kRowThreads / 32, pieces = a.rows * a.cuts;
