@@ -1046,7 +1046,6 @@ tv::PageArgs page_args(const tv_page_params* p, const int32_t* block_table, cons
   a.ref_counts = const_cast<int32_t*>(ref_counts);
   a.status = status;
   a.rows = p->rows;
-  a.new_rows = p->new_rows;
   a.width = p->max_blocks_per_seq;
   a.num_blocks = p->num_blocks;
   return a;
@@ -1129,6 +1128,7 @@ int tv_fork_pages(const tv_page_params* p, const int32_t* block_table,
     return TV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < tv_pages_workspace_size(p) || !aligned16(workspace)) return TV_ERR_WORKSPACE;
   tv::PageArgs a = page_args(p, block_table, ref_counts, status);
+  a.new_rows = p->new_rows;
   a.seq_lens = seq_lens;
   a.parents = parents;
   a.table_out = block_table_out;
