@@ -639,6 +639,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
   // over all warps, whose bounds count alike below (in order, the warps with the
   // worst beams' lists let 10 times as many candidates pass).
   const int place = lane * kWarps + warp;
+  static_assert(kMaxBeams * kMaxParts <= kThreads * kHeld, "every list's first entry");
   float2 held[kHeld];
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
@@ -712,11 +713,6 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     float off;
     const float v = approx(held[j].x, beam_of(c - over(c, by_own) * own), off);
     top = fmaxf(top, v - off);  // (NaN: none)
-  }
-  for (int q = kThreads * kHeld + tid; q < own; q += kThreads) {  // (more lists than that)
-    float off;
-    const float v = approx(entry(q, 0).x, beam_of(q), off);
-    top = fmaxf(top, v - off);
   }
   const int give = (S + kWarps - 1) / kWarps;
   const float nth = nth_largest(top, give, unused);  // (-inf where a warp has not that many)
