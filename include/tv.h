@@ -725,8 +725,9 @@ int tv_rotate_qk(const tv_rotate_params* params, const uint16_t* q, const uint16
  * entries throughout.
  * Within a row the order is exact, that of the logits and of equal ones the lower
  * token, also where a large score or logit leaves the keys of a row one value in fp64,
- * in which rows are compared.  LSE is off by about 1e-7 (fp32 exps and sums,
- * joined in fp64), so candidates of different rows whose scores are closer than
+ * in which rows are compared.  LSE is off by less than 2^-15 (fp32 exps and sums; by
+ * less than 2^-17 where a row's largest entry is not reached in many small steps, and
+ * ordinarily by 1e-7), so candidates of different rows whose scores are closer than
  * that may come in either order, the same in every call; scores are rounded once
  * to fp32.
  * ====================================================================== */

@@ -24,10 +24,13 @@
 // bound that keeps every candidate that may be among them, those few in fp64; equal keys
 // there by beam, logit and token.
 //
-// LSE: exps and their sums in fp32 against the lane's own maximum, joined in fp32
-// and added to the maximum in fp64: off by about 1e-7, less than the rounding of a
-// score near 20 to fp32 (1e-6).  Candidates of different beams that lie closer than
-// that may come in either order, the same in every call.
+// LSE: exps and their sums in fp32 against the lane's own maximum, lanes and parts joined
+// in fp32, the logarithm and the maximum added in fp64: off by less than 2^-15, the sum of
+// its operations' bounds, of which 2^-15.7 are the factors of up to 64 turns that each
+// raise the maximum a little; without those 2^-17.  Measured: 2e-7 at most on random rows,
+// 4e-6 on rows made for it (a peak of every lane, then equal entries).  Candidates of
+// different beams that lie closer than that may come in either order, the same in every
+// call.
 //
 // Bound: HBM for large calls (18 us of the first one here are the pass over the logits,
 // near 7 TB/s; then the bound and the lists, 3 to 4, up to 4 more where 4 instead of 3 of
