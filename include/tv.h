@@ -827,6 +827,9 @@ int tv_free_pages(const tv_page_params* params, int32_t* block_table, int32_t* r
  *     child gets a free page for it and an entry of `copies` (source page,
  *     destination page, tokens to copy) for tv_copy_pages; (-1, -1, 0) where there
  *     is nothing to copy.  Free pages are those that were free before the call.
+ *     tv_copy_pages has to be enqueued before any call that gives out, moves or writes
+ *     pages or reads the new rows: a source may be free from here on (of rows that
+ *     share a half-filled page every child gets a copy, and nobody keeps the page).
  *   - Entries past the length (pages given ahead) pass to the first child.
  * status[i]: TV_OK; TV_ERR_BAD_TREE if parents[i] is not a row, or its row's length
  * is negative or longer than the row, or the partly filled page is missing or has
@@ -848,8 +851,10 @@ int tv_fork_pages(const tv_page_params* params, const int32_t* block_table,
  * (source, destination, 16) for tv_copy_pages, k < count[1]; count[0] = N;
  * page_map[p] = the new number of page p, -1 of a free one (for references that
  * the caller holds); ref_counts_out and block_table_out are the counts and tables
- * in new numbers.  status[b]: TV_OK; TV_ERR_BAD_TREE if an entry of the row names a
- * free page or is >= num_blocks (it becomes -1).
+ * in new numbers.  tv_copy_pages has to be enqueued before any call that gives out,
+ * moves, writes or reads pages by them: the sources are free there.  status[b]: TV_OK;
+ * TV_ERR_BAD_TREE if an entry of the row names a free page or is >= num_blocks (it
+ * becomes -1).
  * ref_counts_out may be ref_counts, and block_table_out block_table.  moves int32
  * [max(1, num_blocks / 2)][3] (entries from count[1] on are left as they were), count
  * int32 [2], page_map int32 [num_blocks].  Device pointers 16-byte aligned. */

@@ -1249,7 +1249,8 @@ def fork_pages(block_table, seq_lens, parents, ref_counts, *, block_table_out=No
     """tv_fork_pages: new rows that continue the rows parents [R'] (-1: empty) of
     block_table [R, max_blocks] with seq_lens [R]; the old rows are used up, and
     ref_counts [num_blocks] changes in place; all int32.  copies [R', 3] (source,
-    destination, tokens) is what copy_pages has to do before the new rows are read.
+    destination, tokens) is what copy_pages has to do before the new rows are read and
+    before any other call gives out, moves or writes pages (a source may be free by now).
     Returns (block_table_out, seq_lens_out, copies, status); nothing is
     synchronised."""
     lib = load()
@@ -1285,8 +1286,9 @@ def compact_pages(block_table, ref_counts, *, block_table_out=None, ref_counts_o
     max_blocks] and ref_counts [num_blocks] int32, which may be their own outputs.
     Returns a dict: block_table, ref_counts, page_map [num_blocks] (new numbers, -1
     of free pages), moves [max(1, num_blocks // 2), 3] (the first count[1] entries are
-    what copy_pages has to do: copy_pages(moves, ..., count=count[1:])), count [2]
-    (pages in use, moves) and status [R]; nothing is synchronised."""
+    what copy_pages has to do, before any other call gives out, moves, writes or reads
+    pages: copy_pages(moves, ..., count=count[1:])), count [2] (pages in use, moves) and
+    status [R]; nothing is synchronised."""
     lib = load()
     dev, prm = _page_args(block_table, ref_counts)
     shape, pages, rows = (prm.rows, prm.max_blocks_per_seq), (prm.num_blocks,), (prm.rows,)
