@@ -1223,9 +1223,10 @@ def alloc_pages(block_table, ref_counts, end, *, begin=None, status=None, worksp
 
 def free_pages(block_table, ref_counts, *, keep_begin=None, keep_end=None, sinks: int = 0, status=None, stream=None):
     """tv_free_pages: takes back the pages of every row outside its positions
-    [keep_begin[b], keep_end[b]) but for those of the first `sinks` tokens (None: 0,
-    and everything), in place in block_table [R, max_blocks] and ref_counts
-    [num_blocks]; all int32.  Returns status [R]; nothing is synchronised."""
+    [keep_begin[b], keep_end[b]) (None: 0, and everything); below keep_begin the pages
+    of the first `sinks` tokens stay, from keep_end on none do; in place in block_table
+    [R, max_blocks] and ref_counts [num_blocks]; all int32.  Returns status [R]; nothing
+    is synchronised."""
     lib = load()
     _int32(sinks=sinks)
     dev, prm = _page_args(block_table, ref_counts, 0, sinks)

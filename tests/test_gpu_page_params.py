@@ -1,5 +1,5 @@
-"""tv_page_params' fields that a call does not use: whatever they hold, the
-result is the same."""
+"""Fields of tv_page_params: what a call does not use may hold anything, the
+result is the same; and which pages `sinks` keeps."""
 import ctypes as C
 
 import pytest
@@ -35,3 +35,15 @@ def test_allocation_and_compaction(new_rows, sinks):
         assert lib.tv_compact_pages(C.byref(prm), t, r, o, c, p, m, x, s, stream) == tv.TV_OK
         results.append([y.tolist() for y in (table, refs, status, out, counts, to, moves, count[:2])])
     assert results[0] == results[1]
+
+
+def test_sinks_stay_below_the_kept_tokens_only():
+    """The first tokens' pages stay when a window moves on, and go with an ended row."""
+    ensure_built()
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    refs = torch.ones(12, dtype=torch.int32, device="cuda")
+    begin, end = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([33, 64, 0], [64, 0, 16]))
+    status = tv.free_pages(table, refs, keep_begin=begin, keep_end=end, sinks=20)
+    assert status.tolist() == [0, 0, 0]
+    assert table.tolist() == [[0, 1, 2, 3], [-1] * 4, [8, -1, -1, -1]]
+    assert refs.tolist() == [1, 1, 1, 1, 0, 0, 0, 0, 1, 0, 0, 0]
