@@ -626,7 +626,10 @@ def _run(dev, stream, call):
     """call(stream handle) with `dev` and the stream current, so that what the
     call allocates belongs to that stream."""
     torch = _torch()
-    if stream is None and torch._C._cuda_getDevice() == dev:  # (CUDA is up: the arguments are there)
+    global _current
+    if _current is None:  # (CUDA is up: the arguments are there)
+        _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if stream is None and _current() == dev:
         return call(_raw_stream(dev))  # (the handle alone: 3 us less than a Stream object)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
@@ -645,7 +648,7 @@ def _raw_stream(dev):
     return _raw(dev)
 
 
-_raw = None
+_raw = _current = None
 
 
 def _empty(t, shape, dtype, dev):
