@@ -475,13 +475,13 @@ __device__ int collect(const Part<BF16>& p, List& l, const int16_t* tops, Bounds
   return count;
 }
 
-// CTAs behind those of the parts: 1 / len^alpha of a row per thread (its fp64 power
-// would stand in the merge's way).
-__device__ void row_inverses(const BeamArgs& a, int row) {
+// CTAs behind those of the parts: len^alpha of a row per thread (its fp64 power would
+// stand in the merge's way).
+__device__ void row_powers(const BeamArgs& a, int row) {
   if (row >= a.batch * a.beams) return;
   const bool ended = a.finished && a.finished[row] != 0;
   const int len = max(min(a.lengths[row], kMaxLength) + (ended ? 0 : 1), 1);
-  a.inverse[row] = a.length_penalty == 1.0f ? 1.0 / len : pow(static_cast<double>(len), -static_cast<double>(a.length_penalty));
+  a.power[row] = a.length_penalty == 1.0f ? len : pow(static_cast<double>(len), static_cast<double>(a.length_penalty));
 }
 
 template <bool BF16>
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamArgs a
   }
   __syncthreads();
   if (row >= a.batch * a.beams) {
-    row_inverses(a, (blockIdx.x - a.batch * a.beams * ctas) * kThreads + threadIdx.x);
+    row_powers(a, (blockIdx.x - a.batch * a.beams * ctas) * kThreads + threadIdx.x);
     return;
   }
   if (warp >= warps) return;
@@ -552,12 +552,12 @@ enum State { kDead, kLive, kEnded };
 struct MergeSmem {
   double base[kMaxBeams];    // score - log sum; of an ended beam the score
   float top[kMaxBeams];      // the row's maximum
-  double inverse[kMaxBeams]; // 1 / len^alpha
+  double2 power[kMaxBeams];  // len^alpha and its inverse
   unsigned long long key[kFound + kMaxBeams];  // in the order of the keys' values
   float logit[kFound + kMaxBeams];
   float score[kFound + kMaxBeams];
   int at[kFound + kMaxBeams];                  // beam * 2^18 + token
-  float2 approx[kMaxBeams];  // (base, inverse) in fp32
+  float2 approx[kMaxBeams];  // (base, 1 / power) in fp32
   unsigned long long best_key[kWarps];
   unsigned long long best_place[kWarps];
   int best_list[kWarps];
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
         s.state[k] = state;
         s.length[k] = len;
         s.base[k] = score;
-        s.inverse[k] = 1.0;
+        s.power[k] = make_double2(1.0, 1.0);
       }
       const unsigned lives = __ballot_sync(0xffffffffu, state == kLive), ends = __ballot_sync(0xffffffffu, state == kEnded);
       const unsigned below = (1u << lane) - 1;
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     const size_t row = static_cast<size_t>(b) * K + k;
     const float2* part = a.stats + row * a.parts;
     const float2 x = lane < a.parts ? part[lane] : make_float2(-INFINITY, 0.0f);
-    const double inverse = a.length_penalty != 0.0f ? a.inverse[row] : 1.0;
+    const double power = a.length_penalty != 0.0f ? a.power[row] : 1.0, inverse = a.length_penalty != 0.0f ? 1.0 / power : 1.0;
     const float m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(x.x)));
     float sum = isinf(m) ? 0.0f : x.y * expf(x.x - m);
 #pragma unroll
@@ -669,13 +669,15 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
         s.base[k] -= e * 0.69314718055994531 + static_cast<double>(logf(f));
       }
       s.top[k] = m;
-      s.inverse[k] = inverse;
+      s.power[k] = make_double2(power, inverse);
       s.approx[k] = make_float2(static_cast<float>(s.base[k]), static_cast<float>(inverse));
     }
   }
   for (int i = tid; i < s.ended; i += kThreads) {
     const int k = s.at[i] >> 18;
-    if (a.length_penalty != 0.0f) s.inverse[k] = a.inverse[static_cast<size_t>(b) * K + k];
+    if (a.length_penalty == 0.0f) break;
+    const double power = a.power[static_cast<size_t>(b) * K + k];
+    s.power[k] = make_double2(power, 1.0 / power);
   }
   __syncthreads();
   if (tid == 0) a.status[b] = s.bad ? kBadTree : kOk;
@@ -689,16 +691,24 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     }
     return;
   }
-  // a key in fp32, and how far that may be off
+  // a key in fp32, and how far that may be off: half a step each of d, the base, their
+  // sum, the inverse, their product, and of the key with `off` added
   const auto approx = [&](float x, int k, float& off) {
     const float2 p = s.approx[k];
     const float d = x - s.top[k];
-    off = p.y * (0x1p-22f * (fabsf(d) + fabsf(p.x)));
+    off = p.y * (0x1p-21f * (fabsf(d) + fabsf(p.x)));
     return (d + p.x) * p.y;
   };
   // (the maximum off first: rows of the type's lowest value have scores too)
   const auto score_of = [&](float x, int k) {
     return s.state[k] == kEnded ? s.base[k] : s.base[k] + (static_cast<double>(x) - static_cast<double>(s.top[k]));
+  };
+  // (the quotient, a product by the inverse with what that leaves added: equal means of
+  // different lengths have one key)
+  const auto key_of = [&](double score, int k) {
+    const double2 p = s.power[k];
+    const double q = score * p.y;
+    return ordered_key(fma(fma(-q, p.x, score), p.y, q));
   };
   const auto keep = [&](float2 e, int k) {
     const int at = atomicAdd(&s.found, 1);
@@ -784,7 +794,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     const double score = score_of(x, k);
     alike |= i >= s.ended && !(fabsf(x) > 0x1p-25f * (fabsf(s.approx[k].x) + fabsf(x - s.top[k])));
     s.score[i] = static_cast<float>(score);
-    s.key[i] = ordered_key(score * s.inverse[k]);
+    s.key[i] = key_of(score, k);
   }
   alike = __syncthreads_or(alike);
   if (found <= kFound + kMaxBeams) {
@@ -818,7 +828,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
       const float2 e = entry(q, r);
       if (!(e.x > -INFINITY)) continue;
       const int k = beam_of(q);
-      const unsigned long long v = ordered_key(score_of(e.x, k) * s.inverse[k]), p = place_in_order(k << 18 | __float_as_int(e.y), e.x);
+      const unsigned long long v = key_of(score_of(e.x, k), k), p = place_in_order(k << 18 | __float_as_int(e.y), e.x);
       if (better(v, p, key, place)) key = v, place = p, list = q;
     }
     for (int i = tid, j = 0; i < s.ended; i += kThreads, ++j) {

@@ -1026,7 +1026,7 @@ int tv_beam_select(const tv_beam_params* p, const void* logits, const float* sco
   a.finished_out = finished_out;
   a.status = status;
   a.stats = static_cast<float2*>(workspace);
-  a.inverse = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + stats);
+  a.power = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + stats);
   a.lists = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + stats + factors);
   return tv::launch_beam_select(a, stream) == 0 ? TV_OK : TV_ERR_CUDA;
 }

@@ -238,7 +238,7 @@ struct BeamArgs {
   int32_t* status;            // [batch]
   float2* stats;              // [batch * beams][parts] maximum and sum (workspace)
   float2* lists;              // [batch][select][beams][parts] logit and token, best first
-  double* inverse;            // [batch * beams] 1 / length^length_penalty, where that is not 0
+  double* power;              // [batch * beams] length^length_penalty, where that exponent is not 0
   size_t stride;
   int32_t batch, beams, select, vocab, bf16, end_token, parts, chunk;
   int32_t each, more;         // a row's CTAs take each parts, the first more of them one more
