@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     const size_t row = static_cast<size_t>(b) * K + k;
     const float2* part = a.stats + row * a.parts;
     const float2 x = lane < a.parts ? part[lane] : make_float2(-INFINITY, 0.0f);
-    const double power = a.length_penalty != 0.0f ? a.power[row] : 1.0, inverse = a.length_penalty != 0.0f ? 1.0 / power : 1.0;
+    const float power = a.length_penalty != 0.0f ? static_cast<float>(a.power[row]) : 1.0f;
     const float m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(x.x)));
     float sum = isinf(m) ? 0.0f : x.y * expf(x.x - m);
 #pragma unroll
@@ -669,13 +669,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
         s.base[k] -= e * 0.69314718055994531 + static_cast<double>(logf(f));
       }
       s.top[k] = m;
-      s.power[k] = make_double2(power, inverse);
-      s.approx[k] = make_float2(static_cast<float>(s.base[k]), static_cast<float>(inverse));
+      s.approx[k] = make_float2(static_cast<float>(s.base[k]), 1.0f / power);
     }
   }
-  for (int i = tid; i < s.ended; i += kThreads) {
-    const int k = s.at[i] >> 18;
-    if (a.length_penalty == 0.0f) break;
+  // (a lane a beam: a warp's fp64 division takes as long for one lane as for 32)
+  if (const int k = tid - (kThreads - kMaxBeams); a.length_penalty != 0.0f && k >= 0 && k < K) {
     const double power = a.power[static_cast<size_t>(b) * K + k];
     s.power[k] = make_double2(power, 1.0 / power);
   }
@@ -692,7 +690,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     return;
   }
   // a key in fp32, and how far that may be off: half a step each of d, the base, their
-  // sum, the inverse, their product, and of the key with `off` added
+  // sum, the power, its inverse, their product, and of the key with `off` added
   const auto approx = [&](float x, int k, float& off) {
     const float2 p = s.approx[k];
     const float d = x - s.top[k];
