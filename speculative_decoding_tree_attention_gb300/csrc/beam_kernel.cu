@@ -649,13 +649,18 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
     const int c = place + j * kThreads, r = over(c, by_own);
     held[j] = c < total ? entry(c - r * own, r) : make_float2(-INFINITY, 0.0f);
   }
+  // len^alpha of each beam, a lane a beam, and its inverse (to 2^-46: keys add what their
+  // product by it leaves)
+  const int own_beam = tid - (kThreads - kMaxBeams);
+  const bool powers = a.length_penalty != 0.0f && own_beam >= 0 && own_beam < K;
+  const double power = powers ? a.power[static_cast<size_t>(b) * K + own_beam] : 1.0;
   // LSE of each live row, a warp a row
   for (int n = warp; n < s.lives; n += kWarps) {
     const int k = s.live[n];
     const size_t row = static_cast<size_t>(b) * K + k;
     const float2* part = a.stats + row * a.parts;
     const float2 x = lane < a.parts ? part[lane] : make_float2(-INFINITY, 0.0f);
-    const float power = a.length_penalty != 0.0f ? static_cast<float>(a.power[row]) : 1.0f;
+    const float divisor = a.length_penalty != 0.0f ? static_cast<float>(a.power[row]) : 1.0f;
     const float m = of_ordered(__reduce_max_sync(0xffffffffu, ordered(x.x)));
     float sum = isinf(m) ? 0.0f : x.y * expf(x.x - m);
 #pragma unroll
@@ -669,13 +674,12 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) 
         s.base[k] -= e * 0.69314718055994531 + static_cast<double>(logf(f));
       }
       s.top[k] = m;
-      s.approx[k] = make_float2(static_cast<float>(s.base[k]), 1.0f / power);
+      s.approx[k] = make_float2(static_cast<float>(s.base[k]), 1.0f / divisor);
     }
   }
-  // (a lane a beam: a warp's fp64 division takes as long for one lane as for 32)
-  if (const int k = tid - (kThreads - kMaxBeams); a.length_penalty != 0.0f && k >= 0 && k < K) {
-    const double power = a.power[static_cast<size_t>(b) * K + k];
-    s.power[k] = make_double2(power, 1.0 / power);
+  if (powers) {
+    const double first = 1.0f / static_cast<float>(power);
+    s.power[own_beam] = make_double2(power, fma(fma(-power, first, 1.0), first, first));
   }
   __syncthreads();
   if (tid == 0) a.status[b] = s.bad ? kBadTree : kOk;
