@@ -745,7 +745,7 @@ typedef struct {
 } tv_beam_params;        /* host struct */
 
 /* Bytes of device workspace for these parameters on the current device (0 if they
- * are invalid): of each part of a row (at most 64) its maximum, sum and S best, of
+ * are invalid): of each part of a row (at most 32) its maximum, sum and S best, of
  * each row a factor.
  * Contents need no initialisation; calls that overlap on the GPU need distinct
  * workspaces. */

@@ -15,7 +15,7 @@
 // warps of a CTA, which work on one row, take the least of their c_w-th largest, c_w
 // about S / 8.  Few noted entries pass it (3 to 6 of 512 of a warp; where many do, as
 // with a mask over some warps' parts, the warps tell bounds of their own notes and take
-// the best: 64 x 8 of V = 128256 with the upper half masked 64 us, without 151); their
+// the best: 64 x 8 of V = 128256 with the upper half masked 63 us, without 151); their
 // words are read again, an entry a lane, and ranked into the warp's list.  Within a row
 // the order is exact: it is that of the logits, and of equal ones the lower token.
 //
@@ -37,7 +37,7 @@
 // the 512 CTAs are on an SM, and the merge's 5); for few requests the latency of two
 // dependent kernels.  Measured (device time, the call
 // replayed): 64 requests of 8 beams, V = 128256, bf16, S = 16: 35 us; 32 of 8, V = 32000,
-// fp32: 15.4; 1 of 4: 9.3.  On the way, the first case: a CTA per 8192 entries, entries
+// fp32: 15.4; 1 of 4: 9.2.  On the way, the first case: a CTA per 8192 entries, entries
 // in registers and ranks of the CTA's threads' maxima 153 us; a warp a part with its own
 // bound that rises as it reads 71; bounds shared by a CTA's warps while they read 53;
 // words from shared memory, looked at by all lanes 36, the second 18.8 (a quarter of the
@@ -880,11 +880,13 @@ int smem_of(int turns) { return kWarps * (static_cast<int>(sizeof(List)) + turns
 
 }  // namespace
 
-// Parts of a row, of whole 512 entries: as many whole CTAs a row as leave no more than
-// are resident, 4 an SM, but 32 parts at most, whose lists the merge reads (V = 151936, 1
-// request of 32 beams, S = 64: 22.6 us, of 64 parts 30.8, of 16 24.8; 4 of 16, S = 32:
-// 18.5, 24.7 and 19.6).  A row's CTAs share them evenly: one that is left with few warps
-// has a worse bound.
+// Parts of a row, of whole 512 entries: as many whole CTAs a row as leave no more than 4
+// an SM, but 32 parts at most, whose lists the merge reads (V = 151936, 1 request of 32
+// beams, S = 64: 22.6 us, of 64 parts 30.8, of 16 24.8; 4 of 16, S = 32: 18.5, 24.7 and
+// 19.6).  4 are resident where a part's notes leave them the shared memory: up to 21 turns,
+// with 8 parts 81920 fp32 or 167936 bf16 entries a row.  Beyond, 3 are, and more than 456
+// CTAs take a second, short wave (64 x 8, V = 128256, fp32: 64 us, 38.8 at the copy rate).
+// A row's CTAs share them evenly: one that is left with few warps has a worse bound.
 void plan_beam_parts(BeamArgs& a, int sms) {
   const long long rows = static_cast<long long>(a.batch) * a.beams, fit = 4ll * sms / rows;
   const long long most = min((a.vocab + 511) / 512, kMaxParts), want = (fit > 1 ? fit : 1) * kWarps;

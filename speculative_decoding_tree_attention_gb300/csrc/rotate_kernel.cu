@@ -34,7 +34,10 @@
 // tokens of 32/8 heads 4.2.  Before: with sines by every lane for its own pairs and
 // norm, weights and rotation one after the other 80 us for the first; the kernel of few
 // rows 57, with two or four rows in flight 60 and 57; stretches in batches of 6 rows 4
-// CTAs an SM 50.3, of 2 rows and 8 stages 70.
+// CTAs an SM 50.3, of 2 rows and 8 stages 70.  Other forms of the first: neighbours 49.6,
+// half of each head turned 53.8 (neighbours 51.2), 124 of 128 values, whose halves are not
+// 8 bytes aligned, 72.9.  Held to 64 and 80 registers, ten of the twenty instances spill 4 to
+// 24 bytes (of the kernel of many rows only those by value, 8).
 #include "tv_device.cuh"
 #include "tv_launch.h"
 
